@@ -41,6 +41,32 @@ class TQError(RuntimeError):
         super().__init__(f"{func} failed with status {status}: {detail}")
 
 
+class tq_paged_kv(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("table_len", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32)]
+
+
+class tq_paged_batch(ctypes.Structure):
+    _fields_ = [("cu_q", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("B", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_len", ctypes.c_int32)]
+
+
+class tq_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class tq_rope(ctypes.Structure):
+    _fields_ = [("cos_table", ctypes.c_void_p), ("sin_table", ctypes.c_void_p), ("n_pos", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class tq_diff(ctypes.Structure):
+    _fields_ = [("lambda_w", ctypes.c_void_p), ("lambda_stride", ctypes.c_int64), ("gain", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("out_scale", ctypes.c_float)]
+
+
 class tq_params(ctypes.Structure):
     _fields_ = [("d", ctypes.c_int32), ("format", ctypes.c_int32), ("codebook", ctypes.c_int32),
                 ("rotation", ctypes.c_int32), ("rot_seed", ctypes.c_uint64), ("qjl_seed", ctypes.c_uint64),
@@ -96,6 +122,12 @@ _SIGNATURES = {
     "tq_prefill_prepare_q": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _sz, _vp]),
     "tq_prefill_partial": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _sz, _vp]),
     "tq_prefill_combine": (_i32, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _sz, _vp]),
+    "tq_make_rope_table": (_i32, [_i32, ctypes.c_double, _i64, _vp, _vp]),
+    "tq_paged_append": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "tq_paged_gather": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp]),
+    "tq_paged_workspace_size": (_i32, [_vp, _vp, _vp, _vp, _i32, ctypes.POINTER(_sz)]),
+    "tq_paged_attention": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _f32, _vp, _i32, _vp, _sz, _vp]),
+    "tq_paged_diff_attention": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _f32, _vp, _i32, _vp, _sz, _vp]),
 }
 
 
@@ -500,6 +532,161 @@ def tq_decode_combine(k_ctx, v_ctx, out, workspace, B, Hq, Hkv, L, stream=None):
     _check(lib.tq_decode_combine(k_ctx.handle, v_ctx.handle, B, Hq, Hkv, L, _ptr(out), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _stream(stream)),
            "tq_decode_combine")
+
+
+# --------------------------------------------------------------------------- paged cache
+
+def _tensor(t, dtype, dim, what):
+    """A checked tensor argument: its dtype, its number of dimensions, last dimension packed."""
+    if t.dtype != dtype or t.dim() != dim or (t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what} must be a {dim}-dimensional {dtype} tensor with a packed last dimension")
+    return t
+
+
+class PagedKV:
+    """A turbo4 cache in pages (tq_paged_kv): ``k_pages`` / ``v_pages`` packed uint8 CUDA tensors of
+    [n_pages, Hkv, page_size, 68] bytes (alloc_pages), ``block_table`` an int32 CUDA tensor
+    [B, pages per sequence].  Keeps references to the tensors; a table edited in place is seen
+    by the next call."""
+
+    def __init__(self, k_pages, v_pages, block_table, page_size, Hkv):
+        torch = _torch()[0]
+        _tensor(block_table, torch.int32, 2, "block_table")
+        per = Hkv * page_size * tq_row_bytes("turbo4")
+        for t in (k_pages, v_pages):
+            if t.dtype != torch.uint8 or not t.is_contiguous() or per < 1 or t.numel() % per:
+                raise ValueError("pages must be contiguous uint8 tensors of whole pages")
+        if k_pages.numel() != v_pages.numel():
+            raise ValueError("k_pages and v_pages must have one size")
+        self.k_pages, self.v_pages, self.block_table = k_pages, v_pages, block_table
+        self.page_size, self.Hkv, self.n_pages = page_size, Hkv, k_pages.numel() // per
+        width = block_table.shape[1]
+        stride = max(block_table.stride(0), width) if block_table.shape[0] <= 1 else block_table.stride(0)
+        self.c = tq_paged_kv(_ptr(k_pages), _ptr(v_pages), _ptr(block_table), stride, width, page_size, self.n_pages, Hkv)
+        self.ref = ctypes.byref(self.c)
+
+
+class PagedBatch:
+    """The batch of a paged call (tq_paged_batch): ``seq_lens`` int32 CUDA [B], this call's tokens
+    included; ``cu_q`` int32 CUDA [B + 1] row offsets with ``max_q`` and ``n_tokens``, or None for
+    one row per sequence; ``max_len`` a bound on the lengths (0: what the block table holds)."""
+
+    def __init__(self, seq_lens, cu_q=None, max_q=1, n_tokens=None, max_len=0):
+        torch = _torch()[0]
+        _tensor(seq_lens, torch.int32, 1, "seq_lens")
+        B = seq_lens.shape[0]
+        if cu_q is not None:
+            _tensor(cu_q, torch.int32, 1, "cu_q")
+            if cu_q.shape[0] != B + 1 or n_tokens is None:
+                raise ValueError("cu_q has B + 1 entries and comes with n_tokens")
+        self.seq_lens, self.cu_q, self.B = seq_lens, cu_q, B
+        self.n_tokens = B if n_tokens is None else n_tokens
+        self.c = tq_paged_batch(_ptr(cu_q), _ptr(seq_lens), B, max_q, self.n_tokens, max_len)
+        self.ref = ctypes.byref(self.c)
+
+
+class Rope:
+    """Position rotation (tq_rope): fp32 CUDA tables [n_pos, rot_dim / 2] of cosines and sines."""
+
+    def __init__(self, cos, sin, interleaved=False):
+        torch = _torch()[0]
+        for t in (cos, sin):
+            _tensor(t, torch.float32, 2, "rotation tables")
+            if not t.is_contiguous() or t.shape != cos.shape:
+                raise ValueError("rotation tables must be contiguous and of one shape")
+        self.cos, self.sin = cos, sin
+        self.c = tq_rope(_ptr(cos), _ptr(sin), cos.shape[0], 2 * cos.shape[1], int(bool(interleaved)))
+        self.ref = ctypes.byref(self.c)
+
+
+class DiffMix:
+    """Weights of the differential attention (tq_diff): ``lam`` fp32 CUDA, [Hq / 2] (every row) or
+    [n_tokens, Hq / 2]; ``norm_weight`` fp32 CUDA [128] or None (no norm)."""
+
+    def __init__(self, lam, norm_weight=None, eps=1e-5, out_scale=1.0):
+        torch = _torch()[0]
+        _tensor(lam, torch.float32, lam.dim() if lam.dim() in (1, 2) else 2, "lam")
+        if norm_weight is not None and _tensor(norm_weight, torch.float32, 1, "norm_weight").shape[0] != D:
+            raise ValueError(f"norm_weight must have {D} elements")
+        self.lam, self.norm_weight = lam, norm_weight
+        stride = 0 if lam.dim() == 1 else (lam.stride(0) if lam.shape[0] > 1 else lam.shape[1])
+        self.c = tq_diff(_ptr(lam), stride, _ptr(norm_weight), eps, out_scale)
+        self.ref = ctypes.byref(self.c)
+
+
+def tq_make_rope_table(rot_dim, n_pos, base=10000.0):
+    """Host (cos, sin) tables, float32 [n_pos, rot_dim / 2]."""
+    import numpy as np
+    c, s = np.zeros((n_pos, rot_dim // 2), np.float32), np.zeros((n_pos, rot_dim // 2), np.float32)
+    _check(lib.tq_make_rope_table(rot_dim, base, n_pos, c.ctypes.data, s.ctypes.data), "tq_make_rope_table")
+    return c, s
+
+
+def _rows(t, n_tokens, heads, what):
+    """tq_rows of a [n_tokens, heads, 128] tensor (any strides, elements of a row packed)."""
+    if t.dim() != 3 or t.shape[0] < n_tokens or t.shape[1] != heads or t.shape[2] != D or t.stride(2) != 1:
+        raise ValueError(f"{what} must be [n_tokens, {heads}, {D}] with packed rows")
+    return tq_rows(t.data_ptr(), _dtype_code(t), t.stride(0), t.stride(1))
+
+
+def _dense_out(t, n_tokens, heads, what):
+    if t.dim() != 3 or t.shape[0] < n_tokens or t.shape[1] != heads or t.shape[2] != D or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous [n_tokens, {heads}, {D}] tensor")
+    return t.data_ptr()
+
+
+def tq_paged_append(k_ctx, v_ctx, kv, batch, k, v, rope=None, stream=None):
+    """Quantize the batch's rows k, v ([n_tokens, Hkv, 128]) into their pages, the keys rotated
+    by their positions first (``rope``)."""
+    kr, vr = _rows(k, batch.n_tokens, kv.Hkv, "k"), _rows(v, batch.n_tokens, kv.Hkv, "v")
+    _check(lib.tq_paged_append(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref, ctypes.byref(kr), ctypes.byref(vr),
+                               rope.ref if rope else None, _stream(stream)), "tq_paged_append")
+
+
+def tq_paged_gather(k_ctx, v_ctx, kv, batch, k_out, v_out, unrotate=True, stream=None):
+    """Read the batch's rows back into k_out / v_out ([n_tokens, Hkv, 128], either None)."""
+    outs = [t for t in (k_out, v_out) if t is not None]
+    if not outs or outs[0].dtype != outs[-1].dtype:
+        raise ValueError("one output at least, of one dtype")
+    ptrs = [None if t is None else _dense_out(t, batch.n_tokens, kv.Hkv, "outputs") for t in (k_out, v_out)]
+    _check(lib.tq_paged_gather(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref, int(unrotate), ptrs[0], ptrs[1],
+                               _dtype_code(outs[0]), _stream(stream)), "tq_paged_gather")
+
+
+def tq_paged_workspace_size(k_ctx, v_ctx, kv, batch, Hq):
+    n = _sz(0)
+    _check(lib.tq_paged_workspace_size(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref, Hq, ctypes.byref(n)),
+           "tq_paged_workspace_size")
+    return n.value
+
+
+def tq_paged_attention(k_ctx, v_ctx, kv, batch, q, out, workspace, rope=None, scale=0.0, stream=None):
+    """Causal attention of the batch's rows q ([n_tokens, Hq, 128]) over their sequences' pages."""
+    Hq = q.shape[1]
+    qr = _rows(q, batch.n_tokens, Hq, "q")
+    _check(lib.tq_paged_attention(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref, ctypes.byref(qr), Hq,
+                                  rope.ref if rope else None, scale, _dense_out(out, batch.n_tokens, Hq, "out"),
+                                  _dtype_code(out), _ptr(workspace), _wsb(workspace), _stream(stream)),
+           "tq_paged_attention")
+
+
+def tq_paged_diff_attention(k_ctx, v_ctx, kv, batch, q, diff, out, workspace, rope=None, scale=0.0, stream=None):
+    """Differential attention of the head pairs (2p, 2p + 1) of q; out [n_tokens, Hq / 2, 128]."""
+    Hq = q.shape[1]
+    lam = diff.lam
+    if lam.shape[-1] * 2 != Hq or (lam.dim() == 2 and lam.shape[0] < batch.n_tokens):
+        raise ValueError("lam must be [Hq / 2] or [n_tokens, Hq / 2]")
+    qr = _rows(q, batch.n_tokens, Hq, "q")
+    _check(lib.tq_paged_diff_attention(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref, ctypes.byref(qr), Hq,
+                                       rope.ref if rope else None, diff.ref, scale,
+                                       _dense_out(out, batch.n_tokens, Hq // 2, "out"), _dtype_code(out),
+                                       _ptr(workspace), _wsb(workspace), _stream(stream)), "tq_paged_diff_attention")
+
+
+def alloc_pages(n_pages, Hkv, page_size, device="cuda"):
+    """Zeroed packed pages, uint8 [n_pages, Hkv, page_size, 68]."""
+    import torch
+    return torch.zeros((n_pages, Hkv, page_size, tq_row_bytes("turbo4")), dtype=torch.uint8, device=device)
 
 
 def alloc_workspace(nbytes, device="cuda"):

@@ -16,7 +16,9 @@ constexpr int ACC256 = 8;                 // a d = 256 partial: max, sum, 6 spar
 constexpr int PARTIAL256 = ACC256 + D256;
 
 // Device status codes (see tq_ctx_device_status in tq.h).
-enum DevErr : int32_t { DEVERR_ROW_OOB = 1, DEVERR_SEQLEN = 2, DEVERR_TIMEOUT = 3, DEVERR_LAYOUT = 4 };
+enum DevErr : int32_t {
+  DEVERR_ROW_OOB = 1, DEVERR_SEQLEN = 2, DEVERR_TIMEOUT = 3, DEVERR_LAYOUT = 4, DEVERR_PAGE = 5, DEVERR_ROPE = 6
+};
 
 // Stored codebook: K fp32 centroids and K-1 fp32 decision boundaries.
 struct Codebook {
@@ -260,5 +262,48 @@ cudaError_t launch_prefill(const tq_ctx *k, const tq_ctx *v, const uint8_t *kc, 
                            cudaStream_t st);
 cudaError_t launch_combine_prefill(const tq_ctx *v, const PrefillShape &s, float *out,
                                    const Workspace &ws, cudaStream_t st);
+
+// ---- paged cache (tq_paged_*.cu): the checked arguments of a call, by value ----
+struct PagedView {
+  const int32_t *table;
+  int64_t table_stride;
+  int page_shift;         // page_size = 1 << page_shift
+  int n_pages, Hkv;
+  const int32_t *cu_q;    // null: row b is sequence b's only row
+  const int32_t *seq_lens;
+  int B, max_q, n_tokens, max_len;  // max_len <= table_len * page_size
+  int32_t *status;
+};
+struct RowsView {
+  const uint8_t *data;
+  int dtype;
+  int64_t token_bytes, head_bytes;
+};
+struct RopeView {
+  const float *cos_t, *sin_t;
+  int n_pos, rot_dim, interleaved;  // rot_dim 0: no rotation
+};
+struct DiffView {
+  const float *lambda;  // null: plain attention
+  int64_t lambda_stride;
+  const float *gain;
+  float eps, out_scale;
+};
+struct PagedOut {
+  void *out;
+  int dtype;
+  DiffView diff;
+};
+
+cudaError_t launch_paged_append(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, uint8_t *kp, uint8_t *vp,
+                                const RowsView &kr, const RowsView &vr, const RopeView &rope, cudaStream_t st);
+cudaError_t launch_paged_gather(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,
+                                const uint8_t *vp, int unrotate, void *k_out, void *v_out, int out_dtype,
+                                cudaStream_t st);
+// Scratch of the attention for these sizes; false when they pass 32-bit counts.
+bool paged_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes);
+cudaError_t launch_paged_attention(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,
+                                   const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope, float scale,
+                                   const PagedOut &o, void *ws, cudaStream_t st);
 
 }  // namespace tq

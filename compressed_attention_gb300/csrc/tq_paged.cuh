@@ -1,0 +1,139 @@
+// Device side of the paged cache's calls: where a batch row sits (sequence, position, page),
+// the position rotation of a row held by a warp, and row conversions.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+
+constexpr int PG_ROW = 68;  // bytes of a packed row
+
+// Rows that belong to a sequence.
+static __device__ __forceinline__ int paged_rows(const PagedView &v) {
+  if (!v.cu_q) return v.B;
+  const int n = v.cu_q[v.B];
+  return n < 0 ? 0 : min(n, v.n_tokens);
+}
+
+// Length of sequence b, clamped to [0, max_len] (flagged by the thread with `flag`).
+static __device__ __forceinline__ int paged_len(const PagedView &v, int b, bool flag) {
+  const int n = v.seq_lens[b];
+  if (n >= 0 && n <= v.max_len) return n;
+  if (flag) atomicExch(v.status, (int32_t)DEVERR_SEQLEN);
+  return n < 0 ? 0 : v.max_len;
+}
+
+// The sequence of row i: the largest b with cu_q[b] <= i (in [0, B) whatever cu_q holds).
+static __device__ __forceinline__ int paged_seq(const PagedView &v, int i) {
+  if (!v.cu_q) return i;
+  int lo = 0, hi = v.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (v.cu_q[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Position of row i of sequence b of n tokens; negative: the row has no place.
+static __device__ __forceinline__ int paged_pos(const PagedView &v, int b, int i, int n) {
+  return v.cu_q ? n - (v.cu_q[b + 1] - i) : n - 1;
+}
+
+// Page of position pos (< max_len) of sequence b, or -1 (flagged) for an id out of range.
+static __device__ __forceinline__ int paged_page(const PagedView &v, int b, int pos, bool flag) {
+  const int pg = v.table[(int64_t)b * v.table_stride + (pos >> v.page_shift)];
+  if ((unsigned)pg < (unsigned)v.n_pages) return pg;
+  if (flag) atomicExch(v.status, (int32_t)DEVERR_PAGE);
+  return -1;
+}
+
+// Packed row of (page, KV head, row of the page).
+static __device__ __forceinline__ size_t paged_row(const PagedView &v, int page, int h, int i) {
+  return ((((size_t)page * v.Hkv + h) << v.page_shift) + i) * PG_ROW;
+}
+
+static __device__ __forceinline__ int rope_pos(const RopeView &r, int pos, int32_t *status, bool flag) {
+  if (pos < r.n_pos) return max(pos, 0);
+  if (flag) atomicExch(status, (int32_t)DEVERR_ROPE);
+  return r.n_pos - 1;
+}
+
+// (a, b) -> (a c - b s, a s + b c), every operation rounded once.
+static __device__ __forceinline__ float rot_first(float a, float b, float c, float s) {
+  return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+}
+static __device__ __forceinline__ float rot_second(float a, float b, float c, float s) {
+  return __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
+}
+
+// Elements 4l .. 4l + 3 of a row.
+static __device__ __forceinline__ void load_lane4(const uint8_t *row, int dtype, int lane, float (&x)[4]) {
+  if (dtype == TQ_DTYPE_F32) {
+    const float4 v = reinterpret_cast<const float4 *>(row)[lane];
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+    const uint2 v = reinterpret_cast<const uint2 *>(row)[lane];
+    if (dtype == TQ_DTYPE_BF16) {
+      x[0] = bf16_bits_to_f32(v.x & 0xFFFFu), x[1] = bf16_bits_to_f32(v.x >> 16);
+      x[2] = bf16_bits_to_f32(v.y & 0xFFFFu), x[3] = bf16_bits_to_f32(v.y >> 16);
+    } else {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
+      x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+    }
+  }
+}
+
+// Position rotation of a row held as elements 4l .. 4l + 3 of lane l (the whole warp calls).
+static __device__ __forceinline__ void rope_lane4(float (&x)[4], int lane, const RopeView &r, int pos) {
+  if (!r.rot_dim) return;
+  const int half = r.rot_dim >> 1;
+  const float *ct = r.cos_t + (size_t)pos * half, *st = r.sin_t + (size_t)pos * half;
+  const bool act = 4 * lane < r.rot_dim;
+  if (r.interleaved) {
+    if (act) {
+      const float2 c = reinterpret_cast<const float2 *>(ct)[lane], s = reinterpret_cast<const float2 *>(st)[lane];
+      const float a = x[0], b = x[1], e = x[2], f = x[3];
+      x[0] = rot_first(a, b, c.x, s.x), x[1] = rot_second(a, b, c.x, s.x);
+      x[2] = rot_first(e, f, c.y, s.y), x[3] = rot_second(e, f, c.y, s.y);
+    }
+    return;
+  }
+  const int m = r.rot_dim >> 3;  // lanes of a half
+  float o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = __shfl_xor_sync(FULL_MASK, x[e], m);
+  if (act) {
+    const int at = lane & (m - 1);
+    const float4 c = reinterpret_cast<const float4 *>(ct)[at], s = reinterpret_cast<const float4 *>(st)[at];
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x[e] = (lane & m) ? rot_second(o[e], x[e], cc[e], ss[e]) : rot_first(x[e], o[e], cc[e], ss[e]);
+  }
+}
+
+static __device__ __forceinline__ uint32_t pack_bf162(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Elements 4l .. 4l + 3 of a dense output row of `dtype` starting at element `at`.
+static __device__ __forceinline__ void store_lane4(void *out, int dtype, size_t at, int lane, const float (&x)[4]) {
+  if (dtype == TQ_DTYPE_F32)
+    reinterpret_cast<float4 *>(static_cast<float *>(out) + at)[lane] = make_float4(x[0], x[1], x[2], x[3]);
+  else if (dtype == TQ_DTYPE_BF16)
+    reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at)[lane] =
+        make_uint2(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]));
+  else
+    reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at)[lane] =
+        make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
+}
+
+}  // namespace tq

@@ -15,6 +15,7 @@
 #include "tq_device.cuh"
 #include "tq_internal.h"
 #include "tq_qprep.cuh"
+#include "tq_wht.cuh"
 
 namespace tq {
 
@@ -70,19 +71,6 @@ __device__ __forceinline__ void load4(const void *src, int64_t row, int64_t stri
   }
 }
 
-// x / n rounded to nearest, given r = RN(1/n): q = RN(x r) is within one ulp of x / n,
-// the residual x - q n is exact under a fused multiply-add, and one correction
-// q + (x - q n) r rounded to nearest is RN(x / n) (Markstein's theorem for binary
-// floating point with a correctly rounded reciprocal).  The theorem needs the
-// residual and the quotient away from the subnormal range and 1/n normal; other
-// operands (zeros included) take the IEEE division.
-__device__ __forceinline__ float div_rn(float x, float n, float r) {
-  const float q = __fmul_rn(x, r);
-  if (fabsf(x) >= 0x1p-100f && fabsf(q) >= 0x1p-124f && n <= 0x1p125f)
-    return __fmaf_rn(__fmaf_rn(-q, n, x), r, q);
-  return __fdiv_rn(x, n);
-}
-
 // Canonical fp32 norm and u = x / n (u = 0 when n == 0).
 __device__ __forceinline__ float norm_normalize(float (&x)[4]) {
   float p = __fadd_rn(__fadd_rn(__fmul_rn(x[0], x[0]), __fmul_rn(x[1], x[1])),
@@ -94,16 +82,6 @@ __device__ __forceinline__ float norm_normalize(float (&x)[4]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) x[e] = (n == 0.0f) ? 0.0f : div_rn(x[e], n, r);
   return n;
-}
-
-// Number of boundaries strictly below y (binary search over NB sorted boundaries).
-template <int NB>
-__device__ __forceinline__ uint32_t bucket(float y, const float *sb) {
-  uint32_t pos = 0;
-#pragma unroll
-  for (int step = (NB + 1) / 2; step >= 1; step >>= 1)
-    if (y > sb[pos + step - 1]) pos += step;
-  return pos;
 }
 
 template <int NB>
@@ -157,230 +135,6 @@ __device__ __forceinline__ bool slot_of(const WriteParams &p, int64_t row, int l
 }
 
 // ------------------------------------------------------------------ WHT turbo4/turbo3
-// Four threads per row (a warp takes eight rows).  Thread q holds the four 8-element
-// chunks 32i + 8q .. 32i + 8q + 7 (i = 0..3) in registers, so one load instruction reads
-// 64 contiguous bytes of each row, the butterfly stages 1, 2, 4, 32, 64 and the norm
-// tree's strides 16, 8, 1 run inside the thread, and only butterfly stages 8, 16 and tree
-// strides 4, 2 cross threads (shuffles within the row's four lanes).  The operation order
-// is the canonical one -- four-element partial sums of squares combined over strides
-// 16, 8, 4, 2, 1; butterfly stages of distance 1, 2, ..., 64 with the lower element taking
-// a + b and the upper a - b -- so every value is bit-identical to a sequential fp32
-// implementation of the same order.  Register element 8i + e is row element 32i + 8q + e.
-constexpr int WT_THREADS = 256;
-constexpr int WT_E = 32;     // elements per thread
-constexpr int WT_REP = 16;   // copies of the grid table (one per half-warp lane)
-
-// A thread's four chunks as loaded (bf16 bits or fp32), kept while the previous row is
-// encoded.
-template <int SRC>
-struct Quarter {
-  uint2 w[8];  // chunk i: w[2i], w[2i + 1] (eight bf16)
-};
-template <>
-struct Quarter<TQ_DTYPE_F32> {
-  float4 w[8];  // chunk i: w[2i], w[2i + 1]
-};
-
-// v16: bf16 rows are 16-byte aligned (one 16-byte load per chunk); fp32 rows always are.
-template <int SRC>
-__device__ __forceinline__ void load_quarter(const WriteParams &p, int64_t row, int q, bool v16,
-                                             Quarter<SRC> &raw) {
-  if constexpr (SRC == TQ_DTYPE_F32) {
-    const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p.src) + row * p.stride + 8 * q);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) raw.w[2 * i] = s[8 * i], raw.w[2 * i + 1] = s[8 * i + 1];
-  } else if (v16) {
-    const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.src) + row * p.stride + 8 * q);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 c = s[4 * i];
-      raw.w[2 * i] = make_uint2(c.x, c.y), raw.w[2 * i + 1] = make_uint2(c.z, c.w);
-    }
-  } else {
-    const uint2 *s = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.src) + row * p.stride + 8 * q);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) raw.w[2 * i] = s[8 * i], raw.w[2 * i + 1] = s[8 * i + 1];
-  }
-}
-
-__device__ __forceinline__ void unpack_quarter(const Quarter<TQ_DTYPE_F32> &raw, float (&x)[WT_E]) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    x[4 * k] = raw.w[k].x, x[4 * k + 1] = raw.w[k].y, x[4 * k + 2] = raw.w[k].z, x[4 * k + 3] = raw.w[k].w;
-}
-__device__ __forceinline__ void unpack_quarter(const Quarter<TQ_DTYPE_BF16> &raw, float (&x)[WT_E]) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    x[4 * k] = bf16_bits_to_f32(raw.w[k].x & 0xFFFFu), x[4 * k + 1] = bf16_bits_to_f32(raw.w[k].x >> 16);
-    x[4 * k + 2] = bf16_bits_to_f32(raw.w[k].y & 0xFFFFu), x[4 * k + 3] = bf16_bits_to_f32(raw.w[k].y >> 16);
-  }
-}
-
-// Canonical fp32 norm of the row (the four threads end with the same value), then u = x / n
-// in place (u = 0 when n == 0).  Group g = 8i + 2q + h of the row is register group 2i + h.
-__device__ __forceinline__ float quarter_norm_normalize(float (&x)[WT_E]) {
-  float p[8];  // four-element partial sums of register groups 2i + h
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    p[k] = __fadd_rn(__fadd_rn(__fmul_rn(x[4 * k], x[4 * k]), __fmul_rn(x[4 * k + 1], x[4 * k + 1])),
-                     __fadd_rn(__fmul_rn(x[4 * k + 2], x[4 * k + 2]), __fmul_rn(x[4 * k + 3], x[4 * k + 3])));
-  float s[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    // stride 16 (chunk i + 2) and stride 8 (chunk i + 1), in this thread
-    const float s16a = __fadd_rn(p[h], p[4 + h]), s16b = __fadd_rn(p[2 + h], p[6 + h]);
-    s[h] = __fadd_rn(s16a, s16b);
-  }
-  // stride 4: threads q and q ^ 2; stride 2: q and q ^ 1; stride 1: h = 0 and 1 here
-#pragma unroll
-  for (int h = 0; h < 2; ++h) s[h] = __fadd_rn(s[h], __shfl_xor_sync(FULL_MASK, s[h], 2));
-#pragma unroll
-  for (int h = 0; h < 2; ++h) s[h] = __fadd_rn(s[h], __shfl_xor_sync(FULL_MASK, s[h], 1));
-  const float n = __fsqrt_rn(__fadd_rn(s[0], s[1]));
-  const float r = __frcp_rn(n);
-  // Markstein's correction is exact when every nonzero |x| >= 2^-100 and n <= 2^24 (then
-  // |q| >= 2^-124 and 1/n is normal); zeros come out as zeros.  Otherwise the guarded
-  // per-element division.
-  uint32_t mb = 0xFFFFFFFFu;  // min over elements of |x| bits - 1 (zero -> 0xFFFFFFFF)
-#pragma unroll
-  for (int j = 0; j < WT_E; ++j) mb = min(mb, (__float_as_uint(x[j]) & 0x7FFFFFFFu) - 1u);
-  const bool fast = n <= 0x1p24f && mb >= 0x0D800000u - 1u;  // 0x0D800000: 2^-100
-  if (n == 0.0f) {
-#pragma unroll
-    for (int j = 0; j < WT_E; ++j) x[j] = 0.0f;
-  } else if (fast) {
-#pragma unroll
-    for (int j = 0; j < WT_E; ++j) {
-      const float qq = __fmul_rn(x[j], r);
-      x[j] = __fmaf_rn(__fmaf_rn(-qq, n, x[j]), r, qq);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < WT_E; ++j) x[j] = div_rn(x[j], n, r);
-  }
-  return n;
-}
-
-// Randomized Hadamard of the row: sign flips (bit j % 32 of word j / 32 for row element j;
-// nq[i] = sign word i shifted down by 8q), the butterfly, times RN(1/sqrt(128)).
-__device__ __forceinline__ void wht_quarter(float (&v)[WT_E], const uint32_t (&nq)[4], int q) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[8 * i + e] = __uint_as_float(__float_as_uint(v[8 * i + e]) ^ ((nq[i] << (31 - e)) & 0x80000000u));
-  auto stage = [&](int h, int hr) {  // row distance h = register distance hr, in this thread
-#pragma unroll
-    for (int k = 0; k < WT_E; ++k)
-      if (!(k & hr)) {
-        const float a = v[k], b = v[k + hr];
-        v[k] = __fadd_rn(a, b);
-        v[k + hr] = __fsub_rn(a, b);
-      }
-    (void)h;
-  };
-  stage(1, 1);
-  stage(2, 2);
-  stage(4, 4);
-  // distances 8 and 16: partner thread q ^ 1, then q ^ 2; the lower one keeps v + o, the
-  // upper one o - v, both as one fused o + (+-1) v (the product by +-1 is exact)
-#pragma unroll
-  for (int m = 1; m <= 2; m <<= 1) {
-    const float sgn = (q & m) ? -1.0f : 1.0f;
-#pragma unroll
-    for (int k = 0; k < WT_E; ++k) {
-      const float o = __shfl_xor_sync(FULL_MASK, v[k], m);
-      v[k] = __fmaf_rn(sgn, v[k], o);
-    }
-  }
-  stage(32, 8);
-  stage(64, 16);
-  const float inv_sqrt_d = __int_as_float(0x3DB504F3);  // fp32 nearest 1/sqrt(128)
-#pragma unroll
-  for (int k = 0; k < WT_E; ++k) v[k] = __fmul_rn(v[k], inv_sqrt_d);
-}
-
-// #{k : y > b_k}: the grid (copy l16 of cell t: boundary .x, count .y as integer bits) or,
-// without GRID, binary search over the NB boundaries.
-template <bool GRID, int NB>
-__device__ __forceinline__ uint32_t cell_index(float y, const float2 *ce, int l16, float gs, float go, int gn,
-                                               const float *sb) {
-  if (GRID) {
-    // unsigned round-down conversion: negative, -inf and NaN give 0, +inf saturates
-    const uint32_t t = min(__float2uint_rd(fmaf(y, gs, go)), (uint32_t)(gn - 1));
-    const float2 c = ce[t * WT_REP + l16];
-    return __float_as_uint(c.y) + (y > c.x ? 1u : 0u);
-  }
-  return bucket<NB>(y, sb);
-}
-
-// Nearest-centroid indices of this thread's elements, packed into its part of the row
-// record at row (4-byte aligned).  turbo4 (fp32 norm + 64 nibble bytes): chunk i fills
-// word 1 + 4i + q; thread 0 writes the norm.  turbo3 (four 14-byte blocks {fp16 norm,
-// qs[8] with the low two index bits of block element j at bits 2 (j % 4) of qs[j / 4],
-// signs[4] with the high bit at bit j % 8 of signs[j / 8]}): chunk i is elements
-// 8q .. 8q+7 of block i, i.e. qs[2q], qs[2q + 1] and signs[q].
-template <int FMT, bool GRID>
-__device__ __forceinline__ void pack_quarter(const float (&y)[WT_E], float n, const float2 *ce, int l16,
-                                             float gs, float go, int gn, const float *sb, uint8_t *row,
-                                             int q) {
-  constexpr int NB = (FMT == TQ_FMT_TURBO4) ? 15 : 7;
-  if (FMT == TQ_FMT_TURBO4) {
-    uint32_t *w = reinterpret_cast<uint32_t *>(row);
-    if (q == 0) w[0] = __float_as_uint(n);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t word = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) word |= cell_index<GRID, NB>(y[8 * i + e], ce, l16, gs, go, gn, sb) << (4 * e);
-      w[1 + 4 * i + q] = word;
-    }
-  } else {
-    const __half hn = __float2half_rn(n);
-    const uint16_t nb = *reinterpret_cast<const uint16_t *>(&hn);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t idx[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) idx[e] = cell_index<GRID, NB>(y[8 * i + e], ce, l16, gs, go, gn, sb);
-      uint32_t lo = 0, sg = 0;  // qs[2q] | qs[2q + 1] << 8, signs[q]
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        lo |= (idx[e] & 3u) << (2 * e);
-        sg |= (idx[e] >> 2) << e;
-      }
-      uint8_t *blk = row + 14 * i;  // 2-byte aligned
-      if (q == 0) *reinterpret_cast<uint16_t *>(blk) = nb;
-      *reinterpret_cast<uint16_t *>(blk + 2 + 2 * q) = (uint16_t)lo;
-      blk[10 + q] = (uint8_t)sg;
-    }
-  }
-}
-
-// The WHT write's shared tables: the boundaries, the grid table (cell t, copy c at
-// t * WT_REP + c: boundary .x, count .y as integer bits) and its scale, offset and size.
-struct WhtTables {
-  float sb[16];
-  float2 ce[GRID_CELLS * WT_REP];
-  float2 cell0[GRID_CELLS];  // one copy, read from memory
-  float gs, go;
-  int gn;
-};
-
-// Filled by every thread of the CTA (the caller synchronises again before use).
-template <int FMT>
-__device__ __forceinline__ void wht_tables_fill(const WriteParams &p, WhtTables &tb) {
-  constexpr int NB = (FMT == TQ_FMT_TURBO4) ? 15 : 7;
-  if (threadIdx.x < NB) tb.sb[threadIdx.x] = p.b[threadIdx.x];
-  // each cell read from memory once (one latency for the whole table), then copied with
-  // consecutive threads on consecutive entries
-  for (int t = threadIdx.x; t < GRID_CELLS; t += blockDim.x)
-    tb.cell0[t] = make_float2(p.bt->e[t], __uint_as_float((uint32_t)p.bt->cnt[t]));
-  if (threadIdx.x == 0) tb.gs = p.bt->scale, tb.go = p.bt->offset, tb.gn = p.bt->n;
-  __syncthreads();
-  for (int k = threadIdx.x; k < GRID_CELLS * WT_REP; k += blockDim.x) tb.ce[k] = tb.cell0[k / WT_REP];
-}
-
 // Rows in groups of eight per warp (four threads per row): this warp takes row groups it,
 // it + step, ...  The four threads of a row stay together (whole warps iterate while any
 // row is left); the next group's source chunks and slot are loaded before this one is
@@ -402,7 +156,7 @@ __device__ __forceinline__ void wht_rows(const WriteParams &p, const WhtTables &
   auto fetch = [&](int64_t i) {
     const int64_t row = i * 8 + sub;
     if (i < n_iter && row < p.n_rows) {
-      load_quarter<SRC>(p, row, q, v16, raw);
+      load_quarter<SRC>(static_cast<const char *>(p.src) + row * p.stride * (SRC == TQ_DTYPE_F32 ? 4 : 2), q, v16, raw);
       slot_next = p.row_ids ? p.row_ids[row] : row;
     }
   };
@@ -437,7 +191,7 @@ template <int FMT, int SRC>
 __global__ void __launch_bounds__(WT_THREADS) k_write_wht(const WriteParams p) {
   __shared__ WhtTables tb;
   pdl_trigger();
-  wht_tables_fill<FMT>(p, tb);
+  wht_tables_fill<FMT>(p.b, p.bt, tb);
   __syncthreads();
   pdl_wait();
   wht_rows<FMT, SRC>(p, tb, (int64_t)blockIdx.x * (WT_THREADS / 32) + (threadIdx.x >> 5),
@@ -798,9 +552,9 @@ __global__ void __launch_bounds__(QWARPS * 32) k_step_front_wht(const StepFrontP
     const bool v = c >= rc;
     const int cl = v ? c - rc : c;
     if (v)
-      wht_tables_fill<VF>(sp.wv, tb);
+      wht_tables_fill<VF>(sp.wv.b, sp.wv.bt, tb);
     else
-      wht_tables_fill<KF>(sp.wk, tb);
+      wht_tables_fill<KF>(sp.wk.b, sp.wk.bt, tb);
     __syncthreads();
     pdl_trigger();
     pdl_wait();

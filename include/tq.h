@@ -175,7 +175,8 @@ tq_status tq_ctx_destroy(tq_ctx *ctx);
  * status word: 0 = no device-side error; 1 = row id out of range (write skipped);
  * 2 = sequence length outside [1, L] (clamped); 3 = a bounded wait ran out;
  * 4 = the decode kernel found shared memory laid out unlike the device reported
- * (no output was computed). */
+ * (no output was computed); 5 = a block table's page id outside [0, n_pages); 6 = a
+ * position past the end of the rotation table. */
 tq_status tq_ctx_device_status(const tq_ctx *ctx, int32_t *status, int clear);
 
 /* Write path / SET_ROWS ([turbo4 post-mortem] sections 1, 2): quantize n_rows
@@ -363,6 +364,144 @@ tq_status tq_prefill_partial(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const voi
 tq_status tq_prefill_combine(const tq_ctx *k_ctx, const tq_ctx *v_ctx, int B, int T, int Hq, int Hkv,
                              int L, float *out, void *workspace, size_t workspace_bytes,
                              tq_stream_t stream);
+
+/* ------------------------------------------------------------- paged cache */
+
+/* A TURBO4 cache in pages, for batches of sequences that grow, end and share prefixes: the
+ * packed 68-byte rows of page_size consecutive tokens of every KV head form a page, and a
+ * block table lists each sequence's pages in order.  A row holds the same bytes as in the
+ * contiguous caches, so row (page * Hkv + h) * page_size + i of the pages seen as rows is
+ * token i of the page for KV head h (tq_quantize_set_rows and tq_dequantize take the pages
+ * as they are).  Keys may be appended with their position rotation, and the attention
+ * applies the same rotation to the queries.
+ *   - d = 128, TURBO4 keys and values (either rotation, any codebook); everything else is
+ *     TQ_ERR_UNSUPPORTED.
+ *   - Every structure below is read during the call; the arrays it points to are device
+ *     memory of the caller's, used in stream order.
+ *   - Calls may run at the same time on different streams as long as none of them writes
+ *     what another reads (pages, outputs, workspaces).  A captured call reads the lengths,
+ *     the block table and the rows when it is replayed; the sizes and addresses are those
+ *     of the capture. */
+typedef struct tq_paged_kv {
+  void *k_pages;              /* device [n_pages][Hkv][page_size] packed rows, 16-byte aligned */
+  void *v_pages;              /* the same for the values */
+  const int32_t *block_table; /* device: page i of sequence b is block_table[b * table_stride + i] */
+  int64_t table_stride;       /* >= table_len */
+  int32_t table_len;          /* entries per sequence (those past a sequence's length are not read) */
+  int32_t page_size;          /* 16, 32, 64, 128 or 256 */
+  int32_t n_pages;
+  int32_t Hkv;
+} tq_paged_kv;
+
+/* The batch of one call: sequence b has seq_lens[b] tokens, of which the last
+ * cu_q[b+1] - cu_q[b] are this call's, rows cu_q[b] .. cu_q[b+1] - 1 of its q, k, v and
+ * outputs, in order (token i of them sits at position seq_lens[b] - n_b + i).
+ *   - Rows from cu_q[B] up to n_tokens belong to no sequence (a padded batch): nothing is
+ *     read for them and their outputs are left as they were.
+ *   - A row whose position would be negative (a sequence shorter than its rows; an idle
+ *     slot of length 0) is not appended, and its outputs are zeros.
+ *   - A length outside [0, max_len] is clamped and flagged (device status 2). */
+typedef struct tq_paged_batch {
+  const int32_t *cu_q;      /* device [B + 1], cu_q[0] = 0, not decreasing; NULL: one row per
+                               sequence, row b (n_tokens == B, max_q == 1) */
+  const int32_t *seq_lens;  /* device [B], this call's tokens included */
+  int32_t B;                /* >= 0 (0: nothing is done) */
+  int32_t max_q;            /* >= 1: at least the largest cu_q[b+1] - cu_q[b] (rows of a sequence
+                               past it are left out of the attention, flagged with status 2) */
+  int32_t n_tokens;         /* rows of the buffers; at least cu_q[B] */
+  int32_t max_len;          /* bound on the lengths, 0 = table_len * page_size.  Sizes the split
+                               of the work only: a tight bound is faster */
+} tq_paged_batch;
+
+/* Rows [n_tokens][heads][128] of F32, BF16 or F16: element j of row (i, h) is
+ * data[i * token_stride + h * head_stride + j] (strides in elements), so q, k and v may be
+ * slices of one projection's output.  Every row 16-byte aligned. */
+typedef struct tq_rows {
+  const void *data;
+  int32_t dtype;
+  int64_t token_stride;
+  int64_t head_stride;
+} tq_rows;
+
+/* Position rotation of the first rot_dim elements of a row: with (c, s) = (cos, sin)[p][i]
+ * at position p, pair i becomes (a c - b s, a s + b c), each product and sum rounded once
+ * to fp32, before the row is quantized (or, for q, scored).  Pair i is elements
+ * (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved != 0. */
+typedef struct tq_rope {
+  const float *cos_table;  /* device fp32 [n_pos][rot_dim / 2], 16-byte aligned */
+  const float *sin_table;  /* the same */
+  int32_t n_pos;           /* a position at or past it is clamped and flagged (status 6) */
+  int32_t rot_dim;         /* 32, 64 or 128 */
+  int32_t interleaved;     /* 0 or 1 */
+} tq_rope;
+
+/* Host tables of the usual angles, cos and sin of p * base^(-2i / rot_dim) for p < n_pos,
+ * i < rot_dim / 2, computed in fp64 and rounded once.  No device work. */
+tq_status tq_make_rope_table(int rot_dim, double base, int64_t n_pos, float *cos_table, float *sin_table);
+
+/* Append the batch's rows to the cache (SET_ROWS through the block table): k rotated by its
+ * position (rope; NULL = as it is) and v are quantized as in tq_quantize_set_rows, and the
+ * row at position p of sequence b goes to page block_table[b][p / page_size], row
+ * p % page_size.  Under the WHT rotation the stored bytes are bit-identical to
+ * tq_quantize_set_rows of the rotated fp32 rows; under a dense rotation an index may differ
+ * where the rotated coordinate lies within 1e-5 of a boundary.
+ *   k, v   rows [n_tokens][Hkv][128], one dtype (F32, BF16 or F16).
+ * A row whose page id is out of range is skipped and flagged (status 5).  Two sequences
+ * that share the page of an appended row race.  One launch. */
+tq_status tq_paged_append(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                          const tq_paged_batch *batch, const tq_rows *k, const tq_rows *v,
+                          const tq_rope *rope, tq_stream_t stream);
+
+/* Read the batch's rows back from the cache: k_out / v_out (either may be NULL) receive
+ * [n_tokens][Hkv][128] reconstructions of out_dtype (F32, BF16 or F16, rounded once from
+ * fp32), 16-byte aligned, as tq_dequantize: norm * R^T c[idx], or norm * c[idx] in the
+ * rotated basis with unrotate == 0.  Keys come back with their position rotation.  A whole
+ * sequence is read by a batch whose rows are all its tokens.  A page id out of range reads
+ * page 0 (flagged, status 5). */
+tq_status tq_paged_gather(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                          const tq_paged_batch *batch, int unrotate, void *k_out, void *v_out,
+                          int out_dtype, tq_stream_t stream);
+
+/* Causal attention of the batch's rows over their sequences' pages (which hold the rows'
+ * own keys and values: append first).  For row i of sequence b at position p, q-head h and
+ * KV head kv = floor(h * Hkv / Hq),
+ *   out[i,h] = sum_{t <= p} softmax_t(scale * <q'[i,h], K_hat[b,kv,t]>) V_hat[b,kv,t],
+ * q' = q rotated by its position (rope; NULL = as it is).
+ *   q          rows [n_tokens][Hq][128], F32, BF16 or F16.  Hq a multiple of Hkv, at most
+ *              64 q-heads per KV head.
+ *   scale      0 selects 1/sqrt(128).
+ *   out        device [n_tokens][Hq][128] of out_dtype (F32, BF16 or F16), 16-byte aligned.
+ *   workspace  device scratch of tq_paged_workspace_size() bytes for the same batch sizes,
+ *              256-byte aligned; its contents need no initialisation.
+ * Sums, maxima and outputs are held in fp32; the tensor-core operands are fp16 parts
+ * (header comments of the kernels state which products carry one part and which two).
+ * Accuracy: 2e-3 absolute, 1e-3 relative per row, as tq_decode_attention, before the
+ * rounding to out_dtype. */
+tq_status tq_paged_workspace_size(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                                  const tq_paged_batch *batch, int Hq, size_t *bytes);
+tq_status tq_paged_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                             const tq_paged_batch *batch, const tq_rows *q, int Hq, const tq_rope *rope,
+                             float scale, void *out, int out_dtype, void *workspace, size_t workspace_bytes,
+                             tq_stream_t stream);
+
+/* Differential attention: with a_h the fp32 output of q-head h above, pair p (q-heads 2p and
+ * 2p + 1, which share a KV head: Hq / Hkv even) gives
+ *   d = a_2p - lambda[i][p] a_2p+1,   out[i,p] = out_scale * d * rsqrt(mean(d^2) + eps) * gain
+ * (the norm over the pair's 128 elements; without gain out[i,p] = out_scale * d). */
+typedef struct tq_diff {
+  const float *lambda_w;  /* device fp32: the learned weight of row i, pair p at [i * lambda_stride + p] */
+  int64_t lambda_stride;  /* >= Hq / 2, or 0: one weight per pair for every row */
+  const float *gain;      /* device fp32 [128], or NULL: no norm */
+  float eps;              /* >= 0 */
+  float out_scale;
+} tq_diff;
+
+/* out: device [n_tokens][Hq / 2][128] of out_dtype; the rest as tq_paged_attention (and the
+ * same workspace). */
+tq_status tq_paged_diff_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                                  const tq_paged_batch *batch, const tq_rows *q, int Hq, const tq_rope *rope,
+                                  const tq_diff *diff, float scale, void *out, int out_dtype,
+                                  void *workspace, size_t workspace_bytes, tq_stream_t stream);
 
 /* ---------------------------------------------------------- capture + store */
 

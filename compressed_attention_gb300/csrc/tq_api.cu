@@ -318,6 +318,25 @@ tq_status tq_ctx_create(const tq_params *params, tq_ctx **out) {
       }
       s = to_device(&c->d_pib, rb.data(), rb.size());
     }
+    if (s == TQ_OK && p.format == TQ_FMT_TURBO4 && d == D) {
+      // R and R^T as bf16 hi + lo A fragments of m16n8k16, [matrix][part][m-tile][k-step][lane]:
+      // lane 4g + t holds rows g, g + 8 and columns 2t, 2t + 1 (+ 8) of each 16 x 16 tile
+      std::vector<uint16_t> f(2 * 2 * (size_t)D * D);
+      for (int m = 0; m < 2; ++m)
+        for (int mt = 0; mt < 8; ++mt)
+          for (int ks = 0; ks < 8; ++ks)
+            for (int lane = 0; lane < 32; ++lane)
+              for (int e = 0; e < 8; ++e) {  // register e / 2, half e % 2
+                const int row = 16 * mt + (lane >> 2) + 8 * ((e >> 1) & 1);
+                const int col = 16 * ks + 2 * (lane & 3) + 8 * (e >> 2) + (e & 1);
+                const float x = m ? r[(size_t)col * D + row] : r[(size_t)row * D + col];
+                const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+                const size_t at = ((((size_t)(2 * m) * 8 + mt) * 8 + ks) * 32 + lane) * 8 + e;
+                f[at] = __bfloat16_as_ushort(hi);
+                f[at + (size_t)D * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x - __bfloat162float(hi)));
+              }
+      s = to_device(&c->d_rfrag, reinterpret_cast<const uint4 *>(f.data()), f.size() / 8);
+    }
     if (s == TQ_OK && p.format == TQ_FMT_PROD3) {
       std::vector<float> S((size_t)D * D), St((size_t)D * D);
       tq_make_qjl_matrix(D, p.qjl_seed, S.data());
@@ -348,6 +367,7 @@ tq_status tq_ctx_destroy(tq_ctx *ctx) {
   cudaFree(ctx->d_S);
   cudaFree(ctx->d_St);
   cudaFree(ctx->d_pib);
+  cudaFree(ctx->d_rfrag);
   cudaFree(ctx->d_bt);
   cudaFree(ctx->d_status);
   delete ctx;

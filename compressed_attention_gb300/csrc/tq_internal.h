@@ -73,6 +73,7 @@ struct tq_ctx {
   float *d_S = nullptr;                 // QJL matrix S, fp32 [128][128] row-major
   float *d_St = nullptr;                // S^T, fp32 row-major
   uint16_t *d_pib = nullptr;            // dense R as bf16 hi then lo, [2][128][128] (tensor-core write)
+  uint4 *d_rfrag = nullptr;             // turbo4, d = 128: R then R^T as bf16 hi + lo MMA operands (tq_rotmma.cuh)
   tq::BucketTable bt{};                 // nearest-centroid grid of the codebook (host copy)
   tq::BucketTable *d_bt = nullptr;      // the same on the device
   int32_t *d_status = nullptr;          // device status word
@@ -300,6 +301,11 @@ cudaError_t launch_paged_append(const tq_ctx *k, const tq_ctx *v, const PagedVie
 cudaError_t launch_paged_gather(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,
                                 const uint8_t *vp, int unrotate, void *k_out, void *v_out, int out_dtype,
                                 cudaStream_t st);
+// Single rows (max_q == 1, tq_paged_decode.cu).
+bool paged_decode_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes);
+cudaError_t launch_paged_decode(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,
+                                const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope, float scale,
+                                const PagedOut &o, void *ws, cudaStream_t st);
 // Scratch of the attention for these sizes; false when they pass 32-bit counts.
 bool paged_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes);
 cudaError_t launch_paged_attention(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,

@@ -136,4 +136,28 @@ static __device__ __forceinline__ void store_lane4(void *out, int dtype, size_t 
         make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
 }
 
+// The end of a differential pair: a = out_scale * d [* rsqrt(mean(d^2) + eps) * gain],
+// d = a - lambda b, elements 4l .. 4l + 3 of lane l (the whole warp calls).
+static __device__ __forceinline__ void diff_finish(float (&a)[4], const float (&b)[4], const DiffView &d, int row,
+                                                   int pair, int lane) {
+  const float lam = d.lambda[(int64_t)row * d.lambda_stride + pair];
+  float ss = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    a[e] = fmaf(-lam, b[e], a[e]);
+    ss = fmaf(a[e], a[e], ss);
+  }
+  float f = d.out_scale;
+  float4 g = make_float4(1.f, 1.f, 1.f, 1.f);
+  if (d.gain) {
+#pragma unroll
+    for (int h = 16; h >= 1; h >>= 1) ss += __shfl_xor_sync(FULL_MASK, ss, h);
+    // all zero (a row without keys) stays zero whatever eps is
+    f = ss > 0.f ? f * rsqrtf(fmaf(ss, 1.0f / D, d.eps)) : 0.f;
+    g = reinterpret_cast<const float4 *>(d.gain)[lane];
+    if (isnan(ss)) f = ss;
+  }
+  a[0] *= f * g.x, a[1] *= f * g.y, a[2] *= f * g.z, a[3] *= f * g.w;
+}
+
 }  // namespace tq

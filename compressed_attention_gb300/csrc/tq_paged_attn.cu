@@ -115,14 +115,16 @@ __global__ void __launch_bounds__(AW * 32) k_paged_attention(const AttnParams p)
 
 }  // namespace
 
-bool paged_workspace(const tq_ctx *, const PagedView &, int, size_t *bytes) {
+bool paged_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes) {
+  if (pv.max_q == 1) return paged_decode_workspace(k, pv, Hq, bytes);
   *bytes = 256;
   return true;
 }
 
 cudaError_t launch_paged_attention(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,
                                    const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope, float scale,
-                                   const PagedOut &o, void *, cudaStream_t st) {
+                                   const PagedOut &o, void *ws, cudaStream_t st) {
+  if (pv.max_q == 1) return launch_paged_decode(k, v, pv, kp, vp, q, Hq, rope, scale, o, ws, st);
   AttnParams p{};
   p.pv = pv, p.kp = kp, p.vp = vp, p.q = q, p.rope = rope, p.o = o;
   p.Hq = Hq, p.gq = Hq / pv.Hkv, p.n_hg = (p.gq + AW - 1) / AW;

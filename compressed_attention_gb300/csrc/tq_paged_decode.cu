@@ -1,0 +1,699 @@
+// Single-row attention over the paged cache: split-K decode through a block table, in two
+// launches.
+//
+//   k_paged_partial  persistent, one CTA per SM.  The key tiles (240 keys) of all units
+//                    (sequence, KV head, group of 4 or 8 q-heads) lie end to end in one
+//                    virtual sequence, each unit preceded by a few empty tiles that stand
+//                    for the cost of starting it; CTA c takes the c-th equal share, so
+//                    ragged lengths balance.  The shares come from the lengths on the
+//                    device, so a captured launch follows them.  Per item the consumer
+//                    warps rotate the unit's q by its position (fp32) and by R (bf16 parts
+//                    on the tensor cores, tq_rotmma.cuh) themselves, while the producer
+//                    warp already streams the first tiles: a tile is one bulk copy per
+//                    page it meets (K by lanes 0-15, V by lanes 16-31, the page ids of the
+//                    next tile loaded one tile ahead) on a four-stage ring.  The products
+//                    are those of the contiguous decode: nibble pairs become fp16x2
+//                    centroid pairs through a shared-memory table, scores and PV run as
+//                    m16n8k16 MMAs with q and the probabilities in fp16 hi + lo parts.
+//   k_paged_combine  merges the shares of each unit, R^T o on the tensor cores, the
+//                    differential pair and its norm, rounding to the output type.
+#include <math.h>
+
+#include "tq_decode_common.cuh"
+#include "tq_paged.cuh"
+#include "tq_qprep.cuh"
+#include "tq_rotmma.cuh"
+#include "tq_t4_tile.cuh"
+
+namespace tq {
+
+namespace {
+
+constexpr int CW = 15;               // consumer warps, 16 keys of a tile each
+constexpr int TILE = 16 * CW;        // keys of a pipeline stage
+constexpr int NT = (CW + 1) * 32;    // + the producer warp
+constexpr int NSTAGE = 4;
+constexpr int STAGE = TILE * PG_ROW + 32;  // 16,352 bytes, a multiple of 32
+constexpr int PROW = D + 4;          // floats of a partial: acc[128], max, sum, 2 spare
+constexpr int ITEM_TILES = 4;        // cost of an item ahead of its tiles, in tiles
+
+struct DecodeParams {
+  PagedView pv;
+  const uint8_t *kp, *vp;
+  RowsView q;
+  RopeView rope;
+  int Hq, gq, n_hg, hpc;   // q-heads; per KV head; head groups per KV head; heads of a unit
+  float qmul;              // log2(e) * scale / alpha_K
+  const uint4 *kfrag;      // R of the keys
+  uint32_t kc16[8], vc16[8];
+  uint32_t klo[2], khi[2], vlo[2], vhi[2];
+  float *split;            // [CTA][2][8] partials of units that several CTAs share
+  float *whole;            // [row][Hq] partials of units one CTA finished
+  int32_t *unit;           // per unit: first CTA | CTAs << 16
+};
+
+struct Head {
+  union {
+    float osm[CW][4][D];   // the warps' accumulators of 4 heads, for the merge
+    struct {
+      RotColumns x;        // the item's q
+      float y[8][D + 4];   // R q
+    } prep;
+  };
+  uint64_t full[NSTAGE], empty[NSTAGE];
+  float mw[CW][8], lw[CW][8];
+  int abort_flag;
+  int V, G;                // the V virtual tiles are shared by G CTAs
+};
+struct Tail {
+  uint32_t q[8][D];        // fp16 hi then lo of the item's rotated q
+  float qs[8];             // and its power-of-two scales
+};
+constexpr uint32_t A_OFF = (sizeof(Head) + 15) & ~15u;
+constexpr uint32_t LUT_OFF = LUT_WINDOW - RESERVED_SMEM;
+constexpr uint32_t B_OFF = LUT_OFF + 256 * 64 * 4;
+constexpr int BELOW = 2;   // stage buffers below the table
+constexpr uint32_t TAIL_OFF = B_OFF + (2 * NSTAGE - BELOW) * STAGE;
+constexpr uint32_t SMEM = TAIL_OFF + sizeof(Tail);
+static_assert(A_OFF + BELOW * STAGE <= LUT_OFF, "the head and two stage buffers below the table");
+static_assert(SMEM + RESERVED_SMEM <= 228 * 1024, "shared memory of one SM");
+
+// Stage buffer i: K of stage i (i < 4), V of stage i - 4.
+__device__ __forceinline__ uint8_t *stage_at(uint8_t *sm, int i) {
+  return sm + (i < BELOW ? A_OFF + i * STAGE : B_OFF + (i - BELOW) * STAGE);
+}
+
+__device__ __forceinline__ void consumers_sync() { named_sync1<CW * 32>(); }
+
+// Keys that sequence b's row sees and the row (-1: none).
+__device__ __forceinline__ int seq_keys(const PagedView &v, int b, int *row, bool flag) {
+  const int n = paged_len(v, b, flag);
+  if (!v.cu_q) {
+    *row = b;
+    return n;
+  }
+  const int a = v.cu_q[b], e = v.cu_q[b + 1];
+  if (a < 0 || a >= v.n_tokens || e <= a) {
+    *row = -1;
+    return 0;
+  }
+  if (flag && e - a > 1) atomicExch(v.status, (int32_t)DEVERR_SEQLEN);  // rows past max_q = 1
+  *row = a;
+  return max(n - (e - a) + 1, 0);
+}
+__device__ __forceinline__ int key_tiles(int keys) { return (keys + TILE - 1) / TILE; }
+
+// floor(x * G / V) and the like: 32-bit when the product fits.
+__device__ __forceinline__ int mul_div(uint32_t x, uint32_t m, uint32_t d) {
+  const uint64_t p = (uint64_t)x * m;
+  return (p >> 32) ? (int)(p / d) : (int)((uint32_t)p / d);
+}
+__device__ __forceinline__ int share_start(int c, int V, int G) { return mul_div(c, V, G); }
+// The CTA whose share holds virtual tile v: the largest c with floor(c V / G) <= v.
+__device__ __forceinline__ int share_of(int v, int V, int G) {
+  const uint64_t p = (uint64_t)(uint32_t)(v + 1) * (uint32_t)G - 1;
+  return (p >> 32) ? (int)(p / (uint32_t)V) : (int)((uint32_t)p / (uint32_t)V);
+}
+
+// Walks a CTA's share: per unit met, the tiles [t0, t1) of it.
+struct Walk {
+  int b, u, off, left;  // sequence, unit within it, virtual offset within the unit, tiles left
+  int v;                // virtual position
+  int keys, row, tiles;
+};
+struct Item {
+  int b, u, t0, t1, keys, row, tiles, vstart;
+};
+
+// One warp: the total of virtual tiles (flagging bad lengths), then this CTA's share.
+__device__ __forceinline__ int total_tiles(const DecodeParams &p, int lane, bool flag) {
+  const int upb = p.pv.Hkv * p.n_hg;
+  int sum = 0;
+  for (int b = lane; b < p.pv.B; b += 32) {
+    int row;
+    const int t = key_tiles(seq_keys(p.pv, b, &row, flag));
+    sum += t ? t + ITEM_TILES : 0;
+  }
+#pragma unroll
+  for (int h = 16; h >= 1; h >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, h);
+  return sum * upb;
+}
+// One warp: the sequence that holds virtual tile v and the offset within it.
+__device__ __forceinline__ void seek(const DecodeParams &p, int v, int lane, int *b_out, int *off_out) {
+  const int upb = p.pv.Hkv * p.n_hg;
+  int base = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const int b = b0 + lane;
+    int row, t = 0;
+    if (b < p.pv.B) {
+      t = key_tiles(seq_keys(p.pv, b, &row, false));
+      t = t ? (t + ITEM_TILES) * upb : 0;
+    }
+    int inc = t;
+#pragma unroll
+    for (int h = 1; h < 32; h <<= 1) {
+      const int o = __shfl_up_sync(FULL_MASK, inc, h);
+      if (lane >= h) inc += o;
+    }
+    const uint32_t hit = __ballot_sync(FULL_MASK, base + inc > v);
+    if (hit || b0 + 32 >= p.pv.B) {
+      const int l = hit ? __ffs(hit) - 1 : 31;
+      *b_out = b0 + l;
+      *off_out = v - (base + __shfl_sync(FULL_MASK, inc - t, l));
+      return;
+    }
+    base += __shfl_sync(FULL_MASK, inc, 31);
+  }
+}
+
+__device__ __forceinline__ void walk_load(const DecodeParams &p, Walk &w) {
+  w.keys = w.b < p.pv.B ? seq_keys(p.pv, w.b, &w.row, false) : 0;
+  w.tiles = key_tiles(w.keys);
+}
+// The next item of the share (false: done).
+__device__ __forceinline__ bool next_item(const DecodeParams &p, Walk &w, Item &it) {
+  const int upb = p.pv.Hkv * p.n_hg;
+  while (w.left > 0) {
+    if (w.b >= p.pv.B) return false;
+    if (w.tiles == 0 || w.u >= upb) {
+      ++w.b, w.u = 0, w.off = 0;
+      walk_load(p, w);
+      continue;
+    }
+    const int vt = w.tiles + ITEM_TILES, n = min(vt - w.off, w.left);
+    it.b = w.b, it.u = w.u, it.keys = w.keys, it.row = w.row, it.tiles = w.tiles;
+    it.t0 = max(w.off - ITEM_TILES, 0), it.t1 = w.off + n - ITEM_TILES;
+    it.vstart = w.v - w.off + ITEM_TILES;
+    w.v += n, w.left -= n, w.off += n;
+    if (w.off == vt) ++w.u, w.off = 0;
+    if (it.t1 > it.t0) return true;
+  }
+  return false;
+}
+
+template <int NG, bool FIXED>
+__global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Head &sm = *reinterpret_cast<Head *>(smem_raw);
+  Tail &tl = *reinterpret_cast<Tail *>(smem_raw + TAIL_OFF);
+  uint32_t *lut = reinterpret_cast<uint32_t *>(smem_raw + LUT_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  if (FIXED && smem_addr(smem_raw) != RESERVED_SMEM) {  // layout assumption broken: refuse
+    if (threadIdx.x == 0) atomicExch(p.pv.status, (int32_t)DEVERR_LAYOUT);
+    return;
+  }
+  if (warp == CW) {
+    // ---------------- producer: the CTA's share, then every tile's copies
+    if (lane == 0) {
+      for (int s = 0; s < NSTAGE; ++s) {
+        mbar_init(&sm.full[s], 1);
+        mbar_init(&sm.empty[s], CW);
+      }
+      sm.abort_flag = 0;
+      fence_mbar_init();
+    }
+    pdl_wait();
+    const int V = total_tiles(p, lane, blockIdx.x == 0);
+    const int G = min((int)gridDim.x, V);
+    Walk w{0, 0, 0, 0, 0, 0, 0, 0};
+    if ((int)blockIdx.x < G) {
+      w.v = share_start(blockIdx.x, V, G);
+      w.left = share_start(blockIdx.x + 1, V, G) - w.v;
+      seek(p, w.v, lane, &w.b, &w.off);
+      walk_load(p, w);
+      const int vt = w.tiles + ITEM_TILES;
+      w.u = w.off / vt;
+      w.off -= w.u * vt;
+    }
+    if (lane == 0) {
+      sm.V = V, sm.G = G;
+      tl.q[0][0] = w.b, tl.q[0][1] = w.u, tl.q[0][2] = w.off, tl.q[0][3] = w.left, tl.q[0][4] = w.v;
+    }
+    __syncwarp();
+    named_arrive0<NT>();  // the barriers and the share are set up
+    const int psh = p.pv.page_shift, P = 1 << psh;
+    const bool side = lane >= 16;  // lanes 0-15: K, 16-31: V
+    const int seg = lane & 15;
+    const uint8_t *pages = side ? p.vp : p.kp;
+    int ctr = 0;
+    Item it;
+    bool ok = true;
+    while (ok && next_item(p, w, it)) {
+      const int kvh = it.u / p.n_hg;
+      // the page of this lane's segment of tile j
+      auto page_of = [&](int j) -> int {
+        const int pi = ((j * TILE) >> psh) + seg;
+        if (j >= it.t1 || (pi << psh) >= min((j + 1) * TILE, it.keys)) return -1;
+        return max(paged_page(p.pv, it.b, pi << psh, !side), 0);
+      };
+      int pg = page_of(it.t0);
+      for (int j = it.t0; j < it.t1; ++j) {
+        const int kf = j * TILE, nk = min(TILE, it.keys - kf), s = ctr % NSTAGE;
+        const int pg_next = page_of(j + 1);
+        if (ctr >= NSTAGE && !mbar_wait_bounded(&sm.empty[s], ((ctr / NSTAGE) - 1) & 1, WAIT_LIMIT_NS)) {
+          if (lane == 0) {
+            atomicExch(&sm.abort_flag, 1);
+            atomicExch(p.pv.status, (int32_t)DEVERR_TIMEOUT);
+          }
+          ok = false;
+          break;
+        }
+        // rows of a tile rounded up to four (16-byte copies; they stay inside the page)
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], 2u * ((nk + 3) & ~3) * PG_ROW);
+        __syncwarp();
+        if (pg >= 0) {
+          const int k0 = max((((kf >> psh) + seg) << psh), kf);           // first key of the segment
+          const int k1 = min(((k0 >> psh) + 1) << psh, kf + ((nk + 3) & ~3));
+          bulk_g2s(stage_at(smem_raw, s + (side ? NSTAGE : 0)) + (k0 - kf) * PG_ROW,
+                   pages + paged_row(p.pv, pg, kvh, k0 & (P - 1)), (uint32_t)(k1 - k0) * PG_ROW, &sm.full[s]);
+        }
+        pg = pg_next;
+        ++ctr;
+      }
+    }
+    // Let every issued copy land before the CTA can exit (only matters after a bounded wait
+    // gave up; otherwise the consumers have consumed them all).
+    if (!ok || *reinterpret_cast<volatile int *>(&sm.abort_flag)) {
+      for (int c = (ctr > NSTAGE ? ctr - NSTAGE : 0); c < ctr; ++c)
+        (void)mbar_wait_bounded(&sm.full[c % NSTAGE], (c / NSTAGE) & 1, WAIT_LIMIT_NS);
+    }
+    return;
+  }
+
+  // ---------------- consumers: the table (entry b: centroids of nibbles b & 15, b >> 4)
+  for (int piece = threadIdx.x; piece < 256 * 8; piece += CW * 32) {
+    const int byte = piece >> 3, chunk = piece & 7;  // chunks 0-3: key slots, 4-7: value slots
+    const uint32_t *c16 = (chunk & 4) ? p.vc16 : p.kc16;
+    const uint32_t lo = (c16[(byte & 15) >> 1] >> (16 * (byte & 1))) & 0xFFFFu;
+    const uint32_t hi = (c16[(byte >> 4) >> 1] >> (16 * ((byte >> 4) & 1))) & 0xFFFFu;
+    const uint32_t e = lo | (hi << 16);
+    uint4 *dst = reinterpret_cast<uint4 *>(lut + byte * 64 + chunk * 8);
+    dst[0] = make_uint4(e, e, e, e);
+    dst[1] = make_uint4(e, e, e, e);
+  }
+  pdl_wait();  // the pages, q and the workspace may be written by the previous kernel
+  named_sync0<NT>();
+  Walk w{(int)tl.q[0][0], (int)tl.q[0][1], (int)tl.q[0][2], (int)tl.q[0][3], (int)tl.q[0][4], 0, 0, 0};
+  const int V = sm.V, G = sm.G;
+  if (w.left > 0) walk_load(p, w);
+  consumers_sync();  // tl.q is free
+
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t lut_base = smem_addr(lut);
+  const uint32_t kword = 4u * lane, vword = 128u + 4u * lane;
+  const uint32_t klo[2] = {p.klo[0], p.klo[1]}, khi[2] = {p.khi[0], p.khi[1]};
+  const uint32_t vlo[2] = {p.vlo[0], p.vlo[1]}, vhi[2] = {p.vhi[0], p.vhi[1]};
+  // Tile row of the warp's key k: warps 0-13 pair up on 32-row blocks (rows 16 apart start 16
+  // banks apart), so that the packed words and norms are read without bank conflicts.
+  const bool paired = warp < 2 * (CW / 2);
+  const int r0 = paired ? 32 * (warp >> 1) + 8 * (warp & 1) : 16 * warp;
+  auto row_of = [&](int k) { return paired ? r0 + (k & 7) + 16 * (k >> 3) : r0 + k; };
+  const int pk0 = row_of(key_of_row(g)), pk1 = row_of(key_of_row(g + 8)), pat = row_of((t & 1) | ((t & 2) << 2));
+  const int hs = g >> 1;
+  const int src0 = 4 * t + hs, src1 = 4 * (4 + t) + hs;
+  const float lo_sel = (g & 1) ? 1.f : 0.f;
+
+  int ctr = 0;
+  Item it;
+  bool aborted = false;
+  while (next_item(p, w, it)) {
+    const int kvh = it.u / p.n_hg, hg = it.u - kvh * p.n_hg;
+    const int head0 = kvh * p.gq + hg * p.hpc, GH = min(p.hpc, p.gq - hg * p.hpc);
+
+    // ---- q of the item: position rotation, R q, scale, fp16 hi + lo
+    if (warp < 8) {
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (warp < GH) {
+        load_lane4(p.q.data + it.row * p.q.token_bytes + (head0 + warp) * p.q.head_bytes, p.q.dtype, lane, x);
+        if (p.rope.rot_dim) rope_lane4(x, lane, p.rope, rope_pos(p.rope, it.keys - 1, p.pv.status, lane == 0));
+      }
+      rot_put(sm.prep.x, warp, lane, x);
+    }
+    consumers_sync();
+    if (warp < 8) rot_tile(p.kfrag, 0, warp, lane, sm.prep.x, &sm.prep.y[0][0], D + 4);
+    consumers_sync();
+    if (warp < GH) {
+      const int e = scale_split(sm.prep.y[warp], p.qmul, reinterpret_cast<__half *>(tl.q[warp]), lane);
+      if (lane == 0) tl.qs[warp] = ldexpf(1.0f, e);
+    }
+    consumers_sync();
+    uint32_t qb[NG][8][2];
+    float qs[NG];
+#pragma unroll
+    for (int c = 0; c < NG; ++c) {
+      const int slot = c * 4 + hs;
+      const uint32_t *qw = tl.q[slot] + (g & 1) * 64 + 16 * t;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        qb[c][kk][0] = slot < GH ? qw[2 * kk] : 0u;
+        qb[c][kk][1] = slot < GH ? qw[2 * kk + 1] : 0u;
+      }
+      const int my = c * 4 + t;  // the head whose scores this lane holds
+      qs[c] = my < GH ? tl.qs[my] : 0.f;
+    }
+    float O[NG][8][4];
+    float M[NG], lsum[NG];
+#pragma unroll
+    for (int c = 0; c < NG; ++c) {
+      M[c] = -INFINITY;
+      lsum[c] = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) O[c][mt][0] = O[c][mt][1] = O[c][mt][2] = O[c][mt][3] = 0.f;
+    }
+
+    for (int j = it.t0; j < it.t1; ++j) {
+      const int s = ctr % NSTAGE;
+      if (!mbar_wait_bounded(&sm.full[s], (ctr / NSTAGE) & 1, WAIT_LIMIT_NS)) {
+        if (lane == 0) {
+          atomicExch(p.pv.status, (int32_t)DEVERR_TIMEOUT);
+          atomicExch(&sm.abort_flag, 1);
+        }
+        aborted = true;
+        break;
+      }
+      const int nk = min(TILE, it.keys - j * TILE);
+      const uint8_t *Ks = stage_at(smem_raw, s), *Vs = stage_at(smem_raw, NSTAGE + s);
+      if (r0 < nk) {  // the warp's first row is its lowest: some key is valid
+        // ---- scores S^T[16 keys x 8] = K_hat Q^T, two accumulator chains
+        float sa[NG][4], sb[NG][4];
+#pragma unroll
+        for (int c = 0; c < NG; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sa[c][e] = sb[c][e] = 0.f;
+        const uint8_t *kr0 = Ks + pk0 * PG_ROW + 4 + 16 * t;
+        const uint8_t *kr1 = Ks + pk1 * PG_ROW + 4 + 16 * t;
+#pragma unroll
+        for (int w4 = 0; w4 < 4; ++w4) {
+          uint32_t d0[4], d1[4];
+          const uint32_t x0 = ld_u32(kr0 + 4 * w4), x1 = ld_u32(kr1 + 4 * w4);
+          decode4<false, FIXED>(lut_base, kword, x0, klo, khi, d0);
+          decode4<false, FIXED>(lut_base, kword, x1, klo, khi, d1);
+          const uint32_t a0[4] = {d0[0], d1[0], d0[1], d1[1]};
+          const uint32_t a1[4] = {d0[2], d1[2], d0[3], d1[3]};
+#pragma unroll
+          for (int c = 0; c < NG; ++c) {
+            mma_f16(sa[c], a0, qb[c][2 * w4][0], qb[c][2 * w4][1]);
+            mma_f16(sb[c], a1, qb[c][2 * w4 + 1][0], qb[c][2 * w4 + 1][1]);
+          }
+        }
+        // ---- online softmax over the two keys of this lane, head t of each group; the running
+        // max is of s + log2(value norm), so that the probability operand 2^7 e^s n_v stays in
+        // fp16's range whatever the norms
+        const float nk0 = *reinterpret_cast<const float *>(Ks + pk0 * PG_ROW);
+        const float nk1 = *reinterpret_cast<const float *>(Ks + pk1 * PG_ROW);
+        const float nv0 = *reinterpret_cast<const float *>(Vs + pk0 * PG_ROW);
+        const float nv1 = *reinterpret_cast<const float *>(Vs + pk1 * PG_ROW);
+        const bool ok0 = pk0 < nk, ok1 = pk1 < nk;
+        const float nu0 = ok0 ? fmaxf(log2_approx(nv0), -64.f) : 0.f;
+        const float nu1 = ok1 ? fmaxf(log2_approx(nv1), -64.f) : 0.f;
+        uint32_t pb[NG][2];
+#pragma unroll
+        for (int c = 0; c < NG; ++c) {
+          const float d0 = (sa[c][0] + sa[c][1]) + (sb[c][0] + sb[c][1]);
+          const float d1 = (sa[c][2] + sa[c][3]) + (sb[c][2] + sb[c][3]);
+          const float s0 = ok0 ? d0 * (nk0 * qs[c]) : -INFINITY;
+          const float s1 = ok1 ? d1 * (nk1 * qs[c]) : -INFINITY;
+          const float u0 = s0 + nu0, u1 = s1 + nu1;
+          float bm = fmaxf(u0, u1);
+          bm = fmaxf(bm, __shfl_xor_sync(FULL_MASK, bm, 4));
+          bm = fmaxf(bm, __shfl_xor_sync(FULL_MASK, bm, 8));
+          bm = fmaxf(bm, __shfl_xor_sync(FULL_MASK, bm, 16));
+          if (bm > M[c] + RESCALE_SLACK) {  // also taken while M is -inf
+            const float alpha = exp2_approx(M[c] - bm);
+            M[c] = bm;
+            lsum[c] *= alpha;
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+              O[c][mt][0] *= alpha, O[c][mt][1] *= alpha, O[c][mt][2] *= alpha, O[c][mt][3] *= alpha;
+          }
+          const float Mu = (M[c] == -INFINITY) ? 0.f : M[c];
+          lsum[c] += exp2_approx(s0 - Mu) + exp2_approx(s1 - Mu);
+          p_operand(exp2_approx(u0 - Mu + P_SHIFT), exp2_approx(u1 - Mu + P_SHIFT), src0, src1, lo_sel, pb[c]);
+        }
+        // ---- O^T[dims x cols] += V_hat^T[dims x keys] P^T
+        const uint8_t *va_p = Vs + pat * PG_ROW + 4 + 8 * g;  // key a_t; a_t+2, +4, +6 follow
+#pragma unroll
+        for (int w2 = 0; w2 < 2; ++w2) {
+          const uint32_t xa = ld_u32(va_p + 4 * w2), xb = ld_u32(va_p + 2 * PG_ROW + 4 * w2);
+          const uint32_t xc = ld_u32(va_p + 4 * PG_ROW + 4 * w2), xd = ld_u32(va_p + 6 * PG_ROW + 4 * w2);
+          // byte i of zlo = (low nibble of key a, low nibble of key b) of byte 8g + 4w + i
+          const uint32_t zlo_ab = (xa & 0x0F0F0F0Fu) | ((xb << 4) & 0xF0F0F0F0u);
+          const uint32_t zhi_ab = ((xa >> 4) & 0x0F0F0F0Fu) | (xb & 0xF0F0F0F0u);
+          const uint32_t zlo_cd = (xc & 0x0F0F0F0Fu) | ((xd << 4) & 0xF0F0F0F0u);
+          const uint32_t zhi_cd = ((xc >> 4) & 0x0F0F0F0Fu) | (xd & 0xF0F0F0F0u);
+          uint32_t r0w[4], r1w[4], r2w[4], r3w[4];
+          decode4<false, FIXED>(lut_base, vword, zlo_ab, vlo, vhi, r0w);
+          decode4<false, FIXED>(lut_base, vword, zhi_ab, vlo, vhi, r1w);
+          decode4<false, FIXED>(lut_base, vword, zlo_cd, vlo, vhi, r2w);
+          decode4<false, FIXED>(lut_base, vword, zhi_cd, vlo, vhi, r3w);
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {
+            const uint32_t a[4] = {r0w[jj], r1w[jj], r2w[jj], r3w[jj]};
+#pragma unroll
+            for (int c = 0; c < NG; ++c) mma_f16(O[c][4 * w2 + jj], a, pb[c][0], pb[c][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[s]);
+      ++ctr;
+    }
+    // A warp that gave up waiting has set the flag before any warp can get here past the
+    // same tile, so either every consumer warp enters the merge barriers or none.
+    if (aborted || *reinterpret_cast<volatile int *>(&sm.abort_flag)) return;
+
+    // ---- merge the warps' states and write the item's partial
+#pragma unroll
+    for (int c = 0; c < NG; ++c) {
+      lsum[c] += __shfl_xor_sync(FULL_MASK, lsum[c], 4);
+      lsum[c] += __shfl_xor_sync(FULL_MASK, lsum[c], 8);
+      lsum[c] += __shfl_xor_sync(FULL_MASK, lsum[c], 16);
+    }
+    if (g == 0) {
+#pragma unroll
+      for (int c = 0; c < NG; ++c) {
+        sm.mw[warp][c * 4 + t] = M[c];
+        sm.lw[warp][c * 4 + t] = lsum[c];
+      }
+    }
+    const int first = share_of(it.vstart, V, G), n_split = share_of(it.vstart + it.tiles - 1, V, G) - first + 1;
+    const int cta = blockIdx.x;
+    float *dst0 = n_split == 1 ? p.whole + ((size_t)it.row * p.Hq + head0) * PROW
+                               : p.split + (size_t)(cta * 2 + (cta == first ? 1 : 0)) * 8 * PROW;
+    if (threadIdx.x == 0 && cta == first) p.unit[it.b * p.pv.Hkv * p.n_hg + it.u] = first | (n_split << 16);
+    consumers_sync();
+#pragma unroll
+    for (int c = 0; c < NG; ++c) {
+      const int hh = c * 4 + t;
+      // the head's max and sum over the warps: lane (g, t) takes warps g and g + 8
+      const float m0 = sm.mw[g][hh], l0 = sm.lw[g][hh];
+      const bool has1 = g + 8 < CW;
+      const float m1 = has1 ? sm.mw[g + 8][hh] : -INFINITY, l1 = has1 ? sm.lw[g + 8][hh] : 0.f;
+      float ms = fmaxf(m0, m1);
+      ms = fmaxf(ms, __shfl_xor_sync(FULL_MASK, ms, 4));
+      ms = fmaxf(ms, __shfl_xor_sync(FULL_MASK, ms, 8));
+      ms = fmaxf(ms, __shfl_xor_sync(FULL_MASK, ms, 16));
+      float ls = (m0 == -INFINITY ? 0.f : l0 * exp2_approx(m0 - ms)) + (m1 == -INFINITY ? 0.f : l1 * exp2_approx(m1 - ms));
+      ls += __shfl_xor_sync(FULL_MASK, ls, 4);
+      ls += __shfl_xor_sync(FULL_MASK, ls, 8);
+      ls += __shfl_xor_sync(FULL_MASK, ls, 16);
+      const float fac = (M[c] == -INFINITY) ? 0.f : exp2_approx(M[c] - ms);
+      float *orow = &sm.osm[warp][t][0];  // rows g and g + 8 of m-tile mt: dims 16g + 2mt, + 1
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        orow[16 * g + 2 * mt] = (O[c][mt][0] + O[c][mt][1]) * fac;
+        orow[16 * g + 2 * mt + 1] = (O[c][mt][2] + O[c][mt][3]) * fac;
+      }
+      consumers_sync();
+      const int Gc = min(4, GH - c * 4);
+      for (int idx = threadIdx.x; idx < Gc * D; idx += CW * 32) {
+        const int h4 = idx / D, jd = idx % D;
+        const float ms2 = __shfl_sync(FULL_MASK, ms, h4), ls2 = __shfl_sync(FULL_MASK, ls, h4);
+        float acc = 0.f;
+#pragma unroll
+        for (int ww = 0; ww < CW; ++ww) acc += sm.osm[ww][h4][jd];
+        float *dst = dst0 + (c * 4 + h4) * PROW;
+        dst[jd] = (ms2 == -INFINITY) ? 0.f : acc;
+        if (jd < 2) dst[D + jd] = jd == 0 ? ms2 : ls2;
+      }
+      consumers_sync();
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ combine
+struct CombineParams {
+  PagedView pv;
+  PagedOut o;
+  int Hq, gq, n_hg, hpc, units, grid;
+  float inv_vscale;        // 1 / (2^P_SHIFT * alpha_V)
+  const uint4 *vfrag;      // R and R^T of the values
+  const float *split, *whole;
+  const int32_t *unit;
+};
+
+constexpr int CB_WARPS = 8;
+
+// A unit per CTA and turn: warp h merges head h's partials (m* = max m_s, l* = sum l_s
+// 2^(m_s - m*), o = sum acc_s 2^(m_s - m*) / l*), the eight warps multiply by R^T, then warp h
+// (or pair h) finishes the row.
+__global__ void __launch_bounds__(CB_WARPS * 32) k_paged_combine(const CombineParams p) {
+  __shared__ RotColumns x;
+  __shared__ __align__(16) float y[8][D + 4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  uint4 ahi[8], alo[8];  // this warp's 16 rows of R^T
+  rot_load(ahi, p.vfrag, 1, 0, warp, lane);
+  rot_load(alo, p.vfrag, 1, 1, warp, lane);
+  pdl_wait();
+  const int upb = p.pv.Hkv * p.n_hg;
+  for (int unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
+    const int b = unit / upb, u = unit - b * upb, kvh = u / p.n_hg, hg = u - kvh * p.n_hg;
+    const int head0 = kvh * p.gq + hg * p.hpc, GH = min(p.hpc, p.gq - hg * p.hpc);
+    int row;
+    const int keys = seq_keys(p.pv, b, &row, false);
+    if (row < 0) continue;  // the same for the whole CTA
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    if (warp < GH && keys > 0) {
+      const uint32_t info = (uint32_t)p.unit[unit];
+      const int first = min((int)(info & 0xFFFFu), p.grid - 1), n = min((int)(info >> 16), p.grid - first);
+      float ms = -INFINITY, ls = 0.f;
+      for (int s0 = 0; s0 < n; s0 += 8) {
+        float m8[8], l8[8];
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int s = min(s0 + i, n - 1);
+          const float *src = n == 1 ? p.whole + ((size_t)row * p.Hq + head0 + warp) * PROW
+                                    : p.split + (size_t)(((first + s) * 2 + (s == 0 ? 1 : 0)) * 8 + warp) * PROW;
+          m8[i] = __ldcg(src + D), l8[i] = __ldcg(src + D + 1);
+          v[i] = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
+        }
+        float mc = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (s0 + i < n && l8[i] > 0.f) mc = fmaxf(mc, m8[i]);
+        if (mc > ms) {
+          const float f = (ms == -INFINITY) ? 0.f : exp2f(ms - mc);
+          ls *= f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[e] *= f;
+          ms = mc;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (s0 + i < n && l8[i] > 0.f) {
+            const float f = exp2f(m8[i] - ms);
+            ls = fmaf(f, l8[i], ls);
+            a[0] = fmaf(f, v[i].x, a[0]), a[1] = fmaf(f, v[i].y, a[1]);
+            a[2] = fmaf(f, v[i].z, a[2]), a[3] = fmaf(f, v[i].w, a[3]);
+          }
+        }
+      }
+      const float f = ls > 0.f ? p.inv_vscale / ls : 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] *= f;
+    }
+    rot_put(x, warp, lane, a);
+    __syncthreads();
+    {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
+      rot_mul<true>(acc, ahi, x, lane);
+      rot_mul<false>(acc2, alo, x, lane);
+      float *d = &y[2 * (lane & 3)][16 * warp + (lane >> 2)];
+      d[0] = acc[0] + acc2[0], d[D + 4] = acc[1] + acc2[1];
+      d[8] = acc[2] + acc2[2], d[D + 12] = acc[3] + acc2[3];
+    }
+    __syncthreads();
+    if (!p.o.diff.lambda) {
+      if (warp < GH) {
+        const float4 r = *reinterpret_cast<const float4 *>(&y[warp][4 * lane]);
+        const float v4[4] = {r.x, r.y, r.z, r.w};
+        store_lane4(p.o.out, p.o.dtype, ((size_t)row * p.Hq + head0 + warp) * D, lane, v4);
+      }
+    } else if (2 * warp < GH) {
+      const float4 r = *reinterpret_cast<const float4 *>(&y[2 * warp][4 * lane]);
+      const float4 r2 = *reinterpret_cast<const float4 *>(&y[2 * warp + 1][4 * lane]);
+      float v4[4] = {r.x, r.y, r.z, r.w};
+      const float w4[4] = {r2.x, r2.y, r2.z, r2.w};
+      diff_finish(v4, w4, p.o.diff, row, (head0 >> 1) + warp, lane);
+      store_lane4(p.o.out, p.o.dtype, ((size_t)row * (p.Hq / 2) + (head0 >> 1) + warp) * D, lane, v4);
+    }
+    __syncthreads();  // x and y are free again
+  }
+}
+
+template <int NG>
+cudaError_t launch_partial_ng(const DecodeParams &p, bool fixed, int grid, cudaStream_t st) {
+  auto kern = fixed ? k_paged_partial<NG, true> : k_paged_partial<NG, false>;
+  cudaError_t e = kernel_smem_attr((const void *)kern, (int)SMEM, true);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(grid), dim3(NT), SMEM, st, p);
+}
+
+struct Layout {
+  int hpc, n_hg, grid;
+  size_t split, whole, unit, bytes;
+};
+bool layout(const tq_ctx *k, const PagedView &pv, int Hq, Layout *l) {
+  const int gq = Hq / pv.Hkv;
+  l->hpc = gq > 4 ? 8 : 4;
+  l->n_hg = (gq + l->hpc - 1) / l->hpc;
+  l->grid = k->num_sms;
+  const int64_t units = (int64_t)pv.B * pv.Hkv * l->n_hg;
+  const int64_t tiles = units * ((pv.max_len + TILE - 1) / TILE + ITEM_TILES);
+  if (l->grid > 65535 || tiles > INT32_MAX || (int64_t)pv.n_tokens * Hq > INT32_MAX) return false;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  l->split = 0;
+  l->whole = up((size_t)l->grid * 2 * 8 * PROW * 4);
+  l->unit = l->whole + up((size_t)pv.n_tokens * Hq * PROW * 4);
+  l->bytes = l->unit + up((size_t)units * 4);
+  return true;
+}
+
+}  // namespace
+
+bool paged_decode_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes) {
+  Layout l;
+  if (!layout(k, pv, Hq, &l)) return false;
+  *bytes = l.bytes;
+  return true;
+}
+
+cudaError_t launch_paged_decode(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,
+                                const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope, float scale,
+                                const PagedOut &o, void *ws, cudaStream_t st) {
+  Layout l;
+  if (!layout(k, pv, Hq, &l)) return cudaErrorInvalidValue;
+  uint8_t *base = static_cast<uint8_t *>(ws);
+  DecodeParams p{};
+  p.pv = pv, p.kp = kp, p.vp = vp, p.q = q, p.rope = rope;
+  p.Hq = Hq, p.gq = Hq / pv.Hkv, p.n_hg = l.n_hg, p.hpc = l.hpc;
+  p.qmul = LOG2E * scale / k->f16.alpha;
+  p.kfrag = k->d_rfrag;
+  for (int i = 0; i < 8; ++i) p.kc16[i] = k->f16.c16[i], p.vc16[i] = v->f16.c16[i];
+  for (int i = 0; i < 2; ++i) {
+    p.klo[i] = k->f16.lo[i], p.khi[i] = k->f16.hi[i];
+    p.vlo[i] = v->f16.lo[i], p.vhi[i] = v->f16.hi[i];
+  }
+  p.split = reinterpret_cast<float *>(base + l.split);
+  p.whole = reinterpret_cast<float *>(base + l.whole);
+  p.unit = reinterpret_cast<int32_t *>(base + l.unit);
+  const bool fixed = k->reserved_smem == (int)RESERVED_SMEM;
+  cudaError_t e = l.hpc == 8 ? launch_partial_ng<2>(p, fixed, l.grid, st) : launch_partial_ng<1>(p, fixed, l.grid, st);
+  if (e != cudaSuccess) return e;
+  CombineParams c{};
+  c.pv = pv, c.o = o;
+  c.Hq = Hq, c.gq = p.gq, c.n_hg = l.n_hg, c.hpc = l.hpc, c.grid = l.grid;
+  c.units = pv.B * pv.Hkv * l.n_hg;
+  c.inv_vscale = 1.0f / (exp2f(P_SHIFT) * v->f16.alpha);
+  c.vfrag = v->d_rfrag;
+  c.split = p.split, c.whole = p.whole, c.unit = p.unit;
+  int blocks = 1;
+  if ((e = kernel_occupancy((const void *)k_paged_combine, CB_WARPS * 32, 0, &blocks)) != cudaSuccess) return e;
+  const int most = k->num_sms * blocks;
+  return launch_pdl(k_paged_combine, dim3(c.units < most ? c.units : most), dim3(CB_WARPS * 32), 0, st, c);
+}
+
+}  // namespace tq

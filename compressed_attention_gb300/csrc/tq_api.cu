@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "tq_internal.h"
+#include "tq_tc.cuh"
 
 namespace tq {
 const char *last_error();
@@ -336,6 +337,15 @@ tq_status tq_ctx_create(const tq_params *params, tq_ctx **out) {
                 f[at + (size_t)D * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x - __bfloat162float(hi)));
               }
       s = to_device(&c->d_rfrag, reinterpret_cast<const uint4 *>(f.data()), f.size() / 8);
+      for (int i = 0; i < D; ++i)
+        for (int j = 0; j < D; ++j) {
+          const float x = r[(size_t)i * D + j];
+          const __half hi = __float2half_rn(x);
+          const size_t at = sw128_offset(i, j) / 2;
+          f[at] = __half_as_ushort(hi);
+          f[at + (size_t)D * D] = __half_as_ushort(__float2half_rn(x - __half2float(hi)));
+        }
+      if (s == TQ_OK) s = to_device(&c->d_rtile, f.data(), 2 * (size_t)D * D);
     }
     if (s == TQ_OK && p.format == TQ_FMT_PROD3) {
       std::vector<float> S((size_t)D * D), St((size_t)D * D);
@@ -368,6 +378,7 @@ tq_status tq_ctx_destroy(tq_ctx *ctx) {
   cudaFree(ctx->d_St);
   cudaFree(ctx->d_pib);
   cudaFree(ctx->d_rfrag);
+  cudaFree(ctx->d_rtile);
   cudaFree(ctx->d_bt);
   cudaFree(ctx->d_status);
   delete ctx;

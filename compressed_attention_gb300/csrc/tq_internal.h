@@ -74,6 +74,7 @@ struct tq_ctx {
   float *d_St = nullptr;                // S^T, fp32 row-major
   uint16_t *d_pib = nullptr;            // dense R as bf16 hi then lo, [2][128][128] (tensor-core write)
   uint4 *d_rfrag = nullptr;             // turbo4, d = 128: R then R^T as bf16 hi + lo MMA operands (tq_rotmma.cuh)
+  uint16_t *d_rtile = nullptr;          // the same: R as fp16 hi, lo in the swizzled operand layout (tq_tc.cuh)
   tq::BucketTable bt{};                 // nearest-centroid grid of the codebook (host copy)
   tq::BucketTable *d_bt = nullptr;      // the same on the device
   int32_t *d_status = nullptr;          // device status word
@@ -306,6 +307,11 @@ bool paged_decode_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t
 cudaError_t launch_paged_decode(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,
                                 const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope, float scale,
                                 const PagedOut &o, void *ws, cudaStream_t st);
+// Several rows per sequence (tq_paged_prefill.cu).
+bool paged_prefill_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes);
+cudaError_t launch_paged_prefill(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,
+                                 const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope, float scale,
+                                 const PagedOut &o, void *ws, cudaStream_t st);
 // Scratch of the attention for these sizes; false when they pass 32-bit counts.
 bool paged_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes);
 cudaError_t launch_paged_attention(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,

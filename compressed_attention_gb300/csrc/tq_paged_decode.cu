@@ -103,18 +103,6 @@ __device__ __forceinline__ int seq_keys(const PagedView &v, int b, int *row, boo
 }
 __device__ __forceinline__ int key_tiles(int keys) { return (keys + TILE - 1) / TILE; }
 
-// floor(x * G / V) and the like: 32-bit when the product fits.
-__device__ __forceinline__ int mul_div(uint32_t x, uint32_t m, uint32_t d) {
-  const uint64_t p = (uint64_t)x * m;
-  return (p >> 32) ? (int)(p / d) : (int)((uint32_t)p / d);
-}
-__device__ __forceinline__ int share_start(int c, int V, int G) { return mul_div(c, V, G); }
-// The CTA whose share holds virtual tile v: the largest c with floor(c V / G) <= v.
-__device__ __forceinline__ int share_of(int v, int V, int G) {
-  const uint64_t p = (uint64_t)(uint32_t)(v + 1) * (uint32_t)G - 1;
-  return (p >> 32) ? (int)(p / (uint32_t)V) : (int)((uint32_t)p / (uint32_t)V);
-}
-
 // Walks a CTA's share: per unit met, the tiles [t0, t1) of it.
 struct Walk {
   int b, u, off, left;  // sequence, unit within it, virtual offset within the unit, tiles left

@@ -1,0 +1,1102 @@
+// Chunked attention over the paged cache on the 5th-generation tensor cores: ragged batches
+// of several rows per sequence, causal, in three launches.
+//
+//   k_paged_prep      CTA 0 plans: the key tiles (128 keys) of all units (sequence, tile of
+//                     queries, KV head) laid end to end, each after a few empty tiles for its
+//                     start, cut into one equal share per CTA.  The other CTAs rotate q by
+//                     position (fp32) and by R (bf16 parts, m16n8k16) and round it to fp16
+//                     parts; rows without a key get their zeros.
+//   k_paged_prefill   persistent, one CTA per SM, specialised warps:
+//                       loader     packed tiles, one bulk copy per page, on a ring of three
+//                       decoders   4 warps: nibbles -> fp16 centroids (byte permutes) in
+//                                  128-byte swizzled operand tiles, two stages each of K
+//                                  and V.  Both are written row by row as 16-byte chunks:
+//                                  K is the K-major B operand of S = Q K^T, V the MN-major B
+//                                  operand of O += P V, so V needs no transposition.
+//                       2 issuers  one thread each for S, PV and the un-rotation of one
+//                                  softmax group
+//                       softmax    2 groups of 4 warps, a thread per accumulator row.  S is
+//                                  read from tensor memory once: the exponentials are taken
+//                                  against the running maximum of earlier tiles, the fp16
+//                                  probabilities (value norm folded in) are kept in
+//                                  registers, and only when one passed 2^15 is the maximum
+//                                  raised, O rescaled and the pass repeated; then P takes
+//                                  over S's columns.
+//                     While one group is in its softmax, the other one's products run.
+//                     Groups take two 128-row tiles of one unit (sharing the decoded K and
+//                     V), or, where a unit has at most 128 rows or q and P are carried in
+//                     two parts, alternate key tiles of one 128-row tile.
+//                     At the end of an item O / l goes through the tensor cores once more,
+//                     times R (loaded as if it were a value tile), and a unit that lies in
+//                     one CTA is finished there: differential pairs, norm, rounding.
+//   k_paged_join      units shared by CTAs: the log-sum-exp merge of their partials.
+//
+// Parts: for bf16 outputs q, P and O / l enter as one fp16 each (errors of 2^-12, random over
+// 128 dims or the keys: 3e-4 of the output's norm next to bf16's own 1.7e-3); for fp16 and
+// fp32 outputs as hi + lo, which leaves the fp16 centroid table's 3e-5.
+#include <math.h>
+#include <stddef.h>
+
+#include "tq_decode_common.cuh"
+#include "tq_paged.cuh"
+#include "tq_rotmma.cuh"
+#include "tq_tc.cuh"
+
+namespace tq {
+
+namespace {
+
+constexpr int KT = 128;                // keys per tile
+constexpr int UNIT_TILES = 3;          // cost of an item ahead of its tiles, in tiles
+constexpr int RAW = KT * PG_ROW;       // a packed tile
+constexpr int NRAW = 3;
+constexpr int W_DEC = 8, W_MMA = 12, W_LOAD = 14, N_WARPS = 15;
+constexpr int THREADS = N_WARPS * 32;
+constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // S / P of the groups, O of the groups
+constexpr uint32_t IDESC_PV = IDESC_F16 | (1u << 16);    // B stored MN-major
+
+constexpr uint32_t OFF_Q = 0, OFF_K = 2 * SW_TILE_BYTES, OFF_V = 4 * SW_TILE_BYTES;
+constexpr uint32_t OFF_RAW = 6 * SW_TILE_BYTES, OFF_MISC = OFF_RAW + NRAW * RAW;
+struct Misc {
+  uint64_t raw_full[NRAW], raw_empty[NRAW];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_ready[2], s_done[2], p_ready[2], pv_done[2], drain[2];
+  // Key norms of the last four K tiles (0 past the end): a K stage is free once its product
+  // is done, while the softmax still needs the norms; the decoders reach tile j + 4 only after
+  // every group has finished tile j.  2^7 value norms of the two V stages.
+  alignas(16) float kn[4][KT];
+  alignas(16) float nv[2][KT];
+  float xm[2][128], xl[2][128], xa[2][128];  // alternating groups: max, sum, largest |O| of a row
+  uint32_t tmem;
+  int abort_flag;
+};
+constexpr uint32_t SMEM = OFF_MISC + sizeof(Misc) + 1024;  // + slack to align to 1024
+static_assert(SMEM <= 227 * 1024, "shared memory budget");
+static_assert(OFF_MISC % 16 == 0 && RAW % 16 == 0, "alignment");
+
+struct Start {
+  int b, qt, h, off, left, v, V, G;
+};
+struct JoinInfo {
+  int row, T, base, h, first, n;  // first batch row of the unit, its rows, position of row 0, KV head
+};
+
+struct PrefillParams {
+  PagedView pv;
+  const uint8_t *kp, *vp;
+  PagedOut o;
+  int Hq, gq, qpt, qpu;        // q-heads; per KV head; queries per 128-row tile; per unit
+  const uint16_t *qh;          // prepared q: [row][2 parts][128] fp16
+  const float *qsc;            // [row] power-of-two scales
+  const Start *start;          // per CTA
+  JoinInfo *join;              // per CTA: the unit its first item continues
+  float *split;                // [CTA][2][rows of a unit][SROW] partials
+  uint32_t klo[2], khi[2], vlo[2], vhi[2];
+  float inv_vscale;            // 1 / (2^P_SHIFT * alpha_V)
+  const uint8_t *vr;           // R of the values as fp16 hi, lo tile images
+};
+constexpr int SROW = D + 4;    // floats of a partial row: o[128], max, sum, 2 spare
+
+// ------------------------------------------------------------------------------ schedule
+struct Seq {
+  int row, T, base, n_qt;  // first row, rows taken, position of the first row, query tiles
+};
+__device__ __forceinline__ Seq seq_of(const PagedView &v, int b, int qpu, bool flag) {
+  Seq s{0, 0, 0, 0};
+  if (b >= v.B) return s;
+  const int n = paged_len(v, b, flag);
+  int a = b, e = b + 1;
+  if (v.cu_q) a = v.cu_q[b], e = v.cu_q[b + 1];
+  if (a < 0 || a >= v.n_tokens || e <= a) return s;
+  s.row = a;
+  s.base = n - (e - a);
+  s.T = min(min(e, v.n_tokens) - a, v.max_q);
+  if (flag && e - a > s.T) atomicExch(v.status, (int32_t)DEVERR_SEQLEN);
+  s.n_qt = (s.T + qpu - 1) / qpu;
+  return s;
+}
+// Keys the unit's rows see, and their tiles.
+__device__ __forceinline__ int unit_keys(const Seq &s, int qt, int qpu) {
+  return max(s.base + min(s.T, (qt + 1) * qpu), 0);
+}
+__device__ __forceinline__ int unit_tiles(const Seq &s, int qt, int qpu) {
+  return (unit_keys(s, qt, qpu) + KT - 1) / KT;
+}
+
+struct Item {
+  int b, qt, h, t0, t1, tiles, keys, vstart;
+  Seq s;
+};
+struct Walk {
+  int b, qt, h, off, left, v, tiles;
+  Seq s;
+};
+__device__ __forceinline__ void walk_begin(const PrefillParams &p, Walk &w) {
+  const Start st = p.start[blockIdx.x];
+  w.b = st.b, w.qt = st.qt, w.h = st.h, w.off = st.off, w.left = st.left, w.v = st.v;
+  if (w.left > 0) {
+    w.s = seq_of(p.pv, w.b, p.qpu, false);
+    w.tiles = unit_tiles(w.s, w.qt, p.qpu);
+  }
+}
+__device__ __forceinline__ bool next_item(const PrefillParams &p, Walk &w, Item &it) {
+  while (w.left > 0) {
+    if (w.h >= p.pv.Hkv || w.tiles == 0) {  // next query tile, or sequence
+      w.h = 0, w.off = 0;
+      if (++w.qt >= w.s.n_qt) {
+        if (++w.b >= p.pv.B) return false;
+        w.qt = 0;
+        w.s = seq_of(p.pv, w.b, p.qpu, false);
+      }
+      w.tiles = w.s.n_qt ? unit_tiles(w.s, w.qt, p.qpu) : 0;
+      continue;
+    }
+    const int vt = w.tiles + UNIT_TILES, n = min(vt - w.off, w.left);
+    it.b = w.b, it.qt = w.qt, it.h = w.h, it.s = w.s, it.tiles = w.tiles;
+    it.keys = unit_keys(w.s, w.qt, p.qpu);
+    it.t0 = max(w.off - UNIT_TILES, 0), it.t1 = w.off + n - UNIT_TILES;
+    it.vstart = w.v - w.off + UNIT_TILES;
+    w.v += n, w.left -= n, w.off += n;
+    if (w.off == vt) ++w.h, w.off = 0;
+    if (it.t1 > it.t0) return true;
+  }
+  return false;
+}
+
+// ------------------------------------------------------------------------------ preparation
+struct PrepParams {
+  PagedView pv;
+  RowsView q;
+  RopeView rope;
+  PagedOut o;
+  int Hq, qpu, grid;      // grid: CTAs of the attention
+  float qmul;             // log2(e) * scale / alpha_K
+  const uint4 *kfrag;
+  uint16_t *qh;
+  float *qsc;
+  int32_t *prefix;        // [B + 1] virtual tiles ahead of each sequence
+  Start *start;
+  JoinInfo *join;
+  int lo;                 // also write the lo parts
+};
+
+constexpr int PREP_ROWS = 64;
+constexpr int PREP_PITCH = D + 8;
+
+__device__ __forceinline__ int seq_vtiles(const PagedView &v, int b, int qpu, bool flag) {
+  const Seq s = seq_of(v, b, qpu, flag);
+  int sum = 0;
+  for (int qt = 0; qt < s.n_qt; ++qt) {
+    const int t = unit_tiles(s, qt, qpu);
+    sum += t ? t + UNIT_TILES : 0;
+  }
+  return sum * v.Hkv;
+}
+
+// One CTA of 256 threads: prefix sums over the sequences, then every share's start.
+__device__ void plan(const PrepParams &p) {
+  __shared__ int wsum[8];
+  __shared__ int carry;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) carry = 0;
+  __syncthreads();
+  for (int b0 = 0; b0 < p.pv.B; b0 += 256) {
+    const int b = b0 + tid;
+    const int t = b < p.pv.B ? seq_vtiles(p.pv, b, p.qpu, true) : 0;
+    int inc = t;
+#pragma unroll
+    for (int h = 1; h < 32; h <<= 1) {
+      const int o = __shfl_up_sync(FULL_MASK, inc, h);
+      if (lane >= h) inc += o;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    if (b < p.pv.B) p.prefix[b] = before + inc - t;
+    __syncthreads();
+    if (tid == 255) carry = before + inc;
+    __syncthreads();
+  }
+  const int V = carry, G = min(p.grid, V);
+  __threadfence_block();
+  for (int c = tid; c < p.grid; c += 256) {
+    Start st{0, 0, 0, 0, 0, 0, V, G};
+    p.join[c].n = 0;
+    if (c < G) {
+      st.v = share_start(c, V, G);
+      st.left = share_start(c + 1, V, G) - st.v;
+      int lo = 0, hi = p.pv.B - 1;  // the last sequence whose prefix is <= v (empty ones are passed over)
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.prefix[mid] <= st.v) lo = mid;
+        else hi = mid - 1;
+      }
+      st.b = lo;
+      int o = st.v - p.prefix[lo];
+      const Seq s = seq_of(p.pv, lo, p.qpu, false);
+      for (; st.qt < s.n_qt; ++st.qt) {
+        const int t = unit_tiles(s, st.qt, p.qpu), vt = t ? t + UNIT_TILES : 0;
+        if (o < vt * p.pv.Hkv) {
+          st.h = o / vt;
+          st.off = o - st.h * vt;
+          break;
+        }
+        o -= vt * p.pv.Hkv;
+      }
+    }
+    p.start[c] = st;
+  }
+}
+
+__global__ void __launch_bounds__(256) k_paged_prep(const PrepParams p) {
+  __shared__ __align__(16) uint16_t xs[2][PREP_ROWS][PREP_PITCH];  // bf16 hi, lo
+  float(*y)[D + 4] = reinterpret_cast<float(*)[D + 4]>(&xs[0][0][0]);  // over both, after the products
+  static_assert(sizeof(xs) >= PREP_ROWS * (D + 4) * 4, "y over the parts");
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x == 0) {
+    plan(p);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t n = (int64_t)paged_rows(p.pv) * p.Hq, r0 = (int64_t)(blockIdx.x - 1) * PREP_ROWS;
+  if (r0 >= n) return;
+  // rows 8 per warp: load, position rotation, bf16 parts
+  for (int i = 0; i < PREP_ROWS / 8; ++i) {
+    const int r = warp * (PREP_ROWS / 8) + i;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r0 + r < n) {
+      const int tok = (int)((r0 + r) / p.Hq), h = (int)((r0 + r) - (int64_t)tok * p.Hq);
+      const int b = paged_seq(p.pv, tok), len = paged_len(p.pv, b, false), pos = paged_pos(p.pv, b, tok, len);
+      if (pos >= 0) {
+        load_lane4(p.q.data + tok * p.q.token_bytes + h * p.q.head_bytes, p.q.dtype, lane, x);
+        if (p.rope.rot_dim) rope_lane4(x, lane, p.rope, rope_pos(p.rope, pos, p.pv.status, lane == 0));
+      } else {  // no key: the row's output is zero
+        const float z[4] = {0.f, 0.f, 0.f, 0.f};
+        if (!p.o.diff.lambda) store_lane4(p.o.out, p.o.dtype, (size_t)(r0 + r) * D, lane, z);
+        else if (!(h & 1)) store_lane4(p.o.out, p.o.dtype, ((size_t)tok * (p.Hq / 2) + h / 2) * D, lane, z);
+      }
+    }
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(x[2 * m], x[2 * m + 1]);
+      const float2 f = __bfloat1622float2(a);
+      const __nv_bfloat162 c = __floats2bfloat162_rn(isinf(f.x) ? 0.f : x[2 * m] - f.x, isinf(f.y) ? 0.f : x[2 * m + 1] - f.y);
+      hi[m] = *reinterpret_cast<const uint32_t *>(&a);
+      lo[m] = *reinterpret_cast<const uint32_t *>(&c);
+    }
+    *reinterpret_cast<uint2 *>(&xs[0][r][4 * lane]) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2 *>(&xs[1][r][4 * lane]) = make_uint2(lo[0], lo[1]);
+  }
+  __syncthreads();
+  // warp: rows 16 (w % 4) .. + 15, columns 64 (w / 4) .. + 63 of Y = X R^T; R's A fragments hold
+  // the B fragments of two column tiles each: registers (0, 2) and (1, 3)
+  float acc[8][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+  const int rt = 16 * (warp & 3), mt0 = 4 * (warp >> 2);
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    uint4 a[2];
+    uint32_t *aw = reinterpret_cast<uint32_t *>(a);
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        aw[4 * part + e] = *reinterpret_cast<const uint32_t *>(&xs[part][rt + g + 8 * (e & 1)][16 * s + 2 * t + 8 * (e >> 1)]);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const uint4 rh = __ldg(p.kfrag + ((size_t)(mt0 + m) * 8 + s) * 32 + lane);
+      const uint4 rl = __ldg(p.kfrag + ((size_t)(8 + mt0 + m) * 8 + s) * 32 + lane);
+      mma_bf16(acc[2 * m], a[0], rh.x, rh.z), mma_bf16(acc[2 * m + 1], a[0], rh.y, rh.w);
+      mma_bf16(acc[2 * m], a[1], rh.x, rh.z), mma_bf16(acc[2 * m + 1], a[1], rh.y, rh.w);
+      mma_bf16(acc[2 * m], a[0], rl.x, rl.z), mma_bf16(acc[2 * m + 1], a[0], rl.y, rl.w);
+    }
+  }
+  __syncthreads();  // the parts are read
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int c = 16 * mt0 + 8 * j + 2 * t;
+    *reinterpret_cast<float2 *>(&y[rt + g][c]) = make_float2(acc[j][0], acc[j][1]);
+    *reinterpret_cast<float2 *>(&y[rt + g + 8][c]) = make_float2(acc[j][2], acc[j][3]);
+  }
+  __syncthreads();
+  for (int i = 0; i < PREP_ROWS / 8; ++i) {
+    const int r = warp * (PREP_ROWS / 8) + i;
+    if (r0 + r >= n) break;
+    const float4 v = *reinterpret_cast<const float4 *>(&y[r][4 * lane]);
+    const float x[4] = {v.x * p.qmul, v.y * p.qmul, v.z * p.qmul, v.w * p.qmul};
+    float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+    for (int h = 16; h >= 1; h >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, h));
+    const int e = (amax > 0.f && isfinite(amax)) ? ilogbf(amax) - 13 : 0;
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) split_half2(ldexpf(x[2 * m], -e), ldexpf(x[2 * m + 1], -e), hi[m], lo[m]);
+    uint16_t *dst = p.qh + (size_t)(r0 + r) * 2 * D;
+    reinterpret_cast<uint2 *>(dst)[lane] = make_uint2(hi[0], hi[1]);
+    if (p.lo) reinterpret_cast<uint2 *>(dst + D)[lane] = make_uint2(lo[0], lo[1]);
+    if (lane == 0) p.qsc[r0 + r] = ldexpf(1.0f, e);
+  }
+}
+
+// ------------------------------------------------------------------------------ attention
+__device__ __forceinline__ uint64_t pk2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void upk2(uint64_t r, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Descriptor of a value tile as the MN-major B operand: 64-dim halves SW_HALF_BYTES apart
+// (leading offset), groups of eight keys 1024 bytes apart (stride offset), 128-byte swizzle.
+// K-step s of 16 keys starts 2048 s bytes in.
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((SW_HALF_BYTES >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((1024u >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// Barrier over the 256 softmax threads that ORs a failure flag across them.
+__device__ __forceinline__ bool softmax_sync_or(bool fail) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)fail)
+      : "memory");
+  return r != 0;
+}
+
+// ALT: the groups take alternate key tiles of one 128-row tile.  LO (with ALT): q, P and O / l in
+// two fp16 parts.
+template <bool ALT, bool LO>
+__global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParams p) {
+  static_assert(ALT || !LO, "two parts take both q tiles");
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
+  Misc &ms = *reinterpret_cast<Misc *>(smem + OFF_MISC);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int R_TILES = LO ? 2 : 1;  // R as hi [+ lo] value tiles at an item's end
+  pdl_trigger();
+  if (warp == 0) tmem_alloc(smem_addr(&ms.tmem), TM_COLS);
+  if (tid == 0) {
+    for (int i = 0; i < NRAW; ++i) mbar_init(&ms.raw_full[i], 1), mbar_init(&ms.raw_empty[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.k_full[i], 128), mbar_init(&ms.v_full[i], 128);
+      mbar_init(&ms.k_empty[i], ALT ? 1 : 2), mbar_init(&ms.v_empty[i], ALT ? 1 : 2);
+      mbar_init(&ms.s_done[i], 1), mbar_init(&ms.p_ready[i], 128), mbar_init(&ms.pv_done[i], 1);
+      mbar_init(&ms.drain[i], 1), mbar_init(&ms.q_ready[i], 128);
+    }
+    ms.abort_flag = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  const uint32_t tmem = ms.tmem;
+  // Bounded wait; fails at once when another thread has given up already.
+  auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+    if (*reinterpret_cast<volatile int *>(&ms.abort_flag)) return false;
+    const bool done = mbar_wait_bounded(bar, parity, WAIT_LIMIT_NS);
+    if (!done) {
+      atomicExch(&ms.abort_flag, 1);
+      atomicExch(p.pv.status, (int32_t)DEVERR_TIMEOUT);
+    }
+    return done;
+  };
+  Walk w;
+  Item it;
+  walk_begin(p, w);
+  bool ok = true;
+
+  if (warp == W_LOAD) {
+    // ================ loader: K and V tiles in turn on the ring
+    const int psh = p.pv.page_shift, P = 1 << psh;
+    uint32_t n = 0;  // tiles loaded
+    while (ok && next_item(p, w, it)) {
+      auto page_of = [&](int j) -> int {
+        const int pi = ((j * KT) >> psh) + lane;
+        if (j >= it.t1 || lane >= 8 || (pi << psh) >= min((j + 1) * KT, it.keys)) return -1;
+        return max(paged_page(p.pv, it.b, pi << psh, true), 0);
+      };
+      int pg = page_of(it.t0);
+      for (int j = it.t0; ok && j < it.t1; ++j) {
+        const int kf = j * KT, nk4 = (min(KT, it.keys - kf) + 3) & ~3;
+        const int pg_next = page_of(j + 1);
+        const int k0 = max((((kf >> psh) + lane) << psh), kf), k1 = min(((k0 >> psh) + 1) << psh, kf + nk4);
+        for (int side = 0; side < 2; ++side, ++n) {
+          const int s = n % NRAW;
+          if (n >= NRAW) ok = __all_sync(FULL_MASK, wait(&ms.raw_empty[s], ((n / NRAW) - 1) & 1));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&ms.raw_full[s], nk4 * PG_ROW);
+          __syncwarp();
+          if (pg >= 0)
+            bulk_g2s(smem + OFF_RAW + s * RAW + (k0 - kf) * PG_ROW,
+                     (side ? p.vp : p.kp) + paged_row(p.pv, pg, it.h, k0 & (P - 1)), (uint32_t)(k1 - k0) * PG_ROW,
+                     &ms.raw_full[s]);
+        }
+        pg = pg_next;
+      }
+    }
+    // after a failed wait: let the copies in flight land before the CTA ends
+    if (*reinterpret_cast<volatile int *>(&ms.abort_flag))
+      for (uint32_t c = n > NRAW ? n - NRAW : 0; c < n; ++c)
+        (void)mbar_wait_bounded(&ms.raw_full[c % NRAW], (c / NRAW) & 1, WAIT_LIMIT_NS);
+  } else if (warp >= W_DEC && warp < W_MMA) {
+    // ================ decoders: thread = row of the tile
+    const int row = tid - W_DEC * 32;
+    const uint32_t klo[2] = {p.klo[0], p.klo[1]}, khi[2] = {p.khi[0], p.khi[1]};
+    const uint32_t vlo[2] = {p.vlo[0], p.vlo[1]}, vhi[2] = {p.vhi[0], p.vhi[1]};
+    uint32_t nr = 0, kc = 0, vc = 0;  // raw tiles taken, K and V stages filled
+    uint32_t last_r = 0;              // V stages filled with R by a copy of thread 0: see the drain below
+    while (ok && next_item(p, w, it)) {
+      for (int j = it.t0; ok && j < it.t1; ++j) {
+        const bool live = j * KT + row < it.keys;
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side, ++nr) {
+          uint32_t &c = side ? vc : kc;
+          const int st = c & 1, rs = nr % NRAW;
+          if (c >= 2) ok = wait(side ? &ms.v_empty[st] : &ms.k_empty[st], ((c >> 1) - 1) & 1);
+          if (ok) ok = wait(&ms.raw_full[rs], (nr / NRAW) & 1);
+          ok = __all_sync(FULL_MASK, ok);
+          if (!ok) break;
+          const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + OFF_RAW + rs * RAW + row * PG_ROW);
+          uint8_t *dst = smem + (side ? OFF_V : OFF_K) + st * SW_TILE_BYTES;
+          const float norm = __uint_as_float(src[0]);
+          uint32_t lo2[2], hi2[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) lo2[i] = side ? vlo[i] : klo[i], hi2[i] = side ? vhi[i] : khi[i];
+#pragma unroll
+          for (int ch = 0; ch < 16; ++ch) {
+            uint32_t d[4];
+            decode8<0x5140u, 0x7362u>(src[1 + ch], lo2, hi2, d);
+            *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 8 * ch)) = make_uint4(d[0], d[1], d[2], d[3]);
+          }
+          if (side) ms.nv[st][row] = live ? norm * 128.0f : 0.f;
+          else ms.kn[c & 3][row] = live ? norm : 0.f;
+          fence_async_smem();
+          mbar_arrive(side ? &ms.v_full[st] : &ms.k_full[st]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.raw_empty[rs]);
+          ++c;
+        }
+      }
+      // R of the values as the item's last value tiles
+      for (int r = 0; ok && r < R_TILES; ++r, ++vc) {
+        const int st = vc & 1;
+        if (vc >= 2) ok = __all_sync(FULL_MASK, wait(&ms.v_empty[st], ((vc >> 1) - 1) & 1));
+        if (!ok) break;
+        if (row == 0) {
+          mbar_arrive_expect_tx(&ms.v_full[st], SW_TILE_BYTES);
+          bulk_g2s(smem + OFF_V + st * SW_TILE_BYTES, p.vr + r * SW_TILE_BYTES, SW_TILE_BYTES, &ms.v_full[st]);
+          last_r = vc + 1;
+        } else {
+          mbar_arrive(&ms.v_full[st]);
+        }
+      }
+    }
+    // after a failed wait: the copy of R must land before the CTA ends (every thread of the
+    // warp group arrives for a stage it has passed, so the phase completes with the copy)
+    if (row == 0 && last_r && *reinterpret_cast<volatile int *>(&ms.abort_flag))
+      (void)mbar_wait_bounded(&ms.v_full[(last_r - 1) & 1], ((last_r - 1) >> 1) & 1, WAIT_LIMIT_NS);
+  } else if (warp == W_MMA || warp == W_MMA + 1) {
+    // ================ issuers: one thread per softmax group
+    if (lane == 0) {
+      const int gr = warp - W_MMA;
+      const uint32_t sq = smem_addr(smem + OFF_Q), sk = smem_addr(smem + OFF_K), sv = smem_addr(smem + OFF_V);
+      const uint32_t tS = tmem + TM_S + 128 * gr, tO = tmem + TM_O + 128 * gr;
+      uint32_t kc = 0, vc = 0, nq = 0, np = 0, npv = 0;  // K, V stages passed; items; P tiles; PV products
+      uint32_t np1 = 0;  // ALT, group 0: P tiles of group 1
+      bool issued = false;
+      while (ok && next_item(p, w, it)) {
+        const int n = it.t1 - it.t0;
+        const int q0 = it.qt * p.qpu + (ALT ? 0 : gr * p.qpt);
+        const bool act = q0 < it.s.T;  // (not ALT) the second row tile may be empty
+        if (act) {
+          ok = wait(&ms.q_ready[gr], nq & 1);
+          if (ALT && ok) ok = wait(&ms.q_ready[gr ^ 1], nq & 1);
+          ++nq;
+          if (!ok) break;
+          tc_fence_after();
+        }
+        // S of the group's tile at local index i (K stage kc + i)
+        auto issue_s = [&](int i) -> bool {
+          const uint32_t c = kc + i;
+          if (!wait(&ms.k_full[c & 1], (c >> 1) & 1)) return false;
+          if (act) {
+            tc_fence_after();
+            const uint32_t kb = sk + (c & 1) * SW_TILE_BYTES;
+#pragma unroll
+            for (int part = 0; part < (LO ? 2 : 1); ++part)
+#pragma unroll
+              for (int s = 0; s < 8; ++s)
+                umma<IDESC_F16>(tS, sw128_desc(sq + (LO ? part : (ALT ? 0 : gr)) * SW_TILE_BYTES + sw128_kstep(s)),
+                                sw128_desc(kb + sw128_kstep(s)), (part || s) ? 1u : 0u);
+            issued = true;
+            umma_commit(&ms.s_done[gr]);
+            umma_commit(&ms.k_empty[c & 1]);
+          } else {
+            mbar_arrive(&ms.k_empty[c & 1]);
+          }
+          return true;
+        };
+        const int step = ALT ? 2 : 1;
+        int i = ALT ? gr : 0;
+        if (i < n) ok = issue_s(i);
+        for (bool first = true; ok && i < n; i += step, first = false) {
+          const uint32_t c = vc + i;
+          if (act) ok = wait(&ms.p_ready[gr], np & 1), ++np;
+          if (ok) ok = wait(&ms.v_full[c & 1], (c >> 1) & 1);
+          if (!ok) break;
+          if (act) {
+            tc_fence_after();
+            const uint32_t vb = sv + (c & 1) * SW_TILE_BYTES;
+#pragma unroll
+            for (int part = 0; part < (LO ? 2 : 1); ++part)
+#pragma unroll
+              for (int s = 0; s < 8; ++s)
+                umma_ts<IDESC_PV>(tO, tS + (LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s), v_desc(vb + 2048 * s),
+                                  (!first || part || s) ? 1u : 0u);
+            umma_commit(&ms.pv_done[gr]);
+            umma_commit(&ms.v_empty[c & 1]);
+          } else {
+            mbar_arrive(&ms.v_empty[c & 1]);
+          }
+          if (i + step < n) {
+            // S takes over P's columns: PV must have finished (products on different
+            // accumulators may run out of issue order)
+            if (act) ok = wait(&ms.pv_done[gr], npv & 1);
+            if (ok) ok = issue_s(i + step);
+          }
+          if (act) ++npv;
+        }
+        kc += n, vc += n;
+        // un-rotation: O = (O / l) R with O / l where P was
+        if (ok && (!ALT || gr == 0)) {
+          for (int r = 0; ok && r < R_TILES; ++r) {
+            const uint32_t c = vc + r;
+            if (act && r == 0) {
+              ok = wait(&ms.p_ready[gr], np & 1), ++np;
+              // group 1's last one too (its earlier ones are complete: both groups met before)
+              if (ALT && ok) np1 += n / 2, ok = wait(&ms.p_ready[1], np1 & 1), ++np1;
+            }
+            if (ok) ok = wait(&ms.v_full[c & 1], (c >> 1) & 1);
+            if (!ok) break;
+            if (act) {
+              tc_fence_after();
+              const uint32_t vb = sv + (c & 1) * SW_TILE_BYTES;
+#pragma unroll
+              for (int src = 0; src < (ALT ? 2 : 1); ++src)
+#pragma unroll
+                for (int part = 0; part < (LO && r == 0 ? 2 : 1); ++part)
+#pragma unroll
+                  for (int s = 0; s < 8; ++s)
+                    umma_ts<IDESC_PV>(tO, tS + 128 * src + (LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s),
+                                      v_desc(vb + 2048 * s), (r || src || part || s) ? 1u : 0u);
+              umma_commit(&ms.v_empty[c & 1]);
+            } else {
+              mbar_arrive(&ms.v_empty[c & 1]);
+            }
+          }
+          if (ok && act) {
+            umma_commit(&ms.pv_done[gr]);
+            ++npv;
+          }
+        }
+        if (ALT && gr == 1) ++np;  // its last P is waited for by group 0's issuer
+        vc += R_TILES;
+      }
+      if (issued && *reinterpret_cast<volatile int *>(&ms.abort_flag)) {
+        umma_commit(&ms.drain[gr]);
+        (void)mbar_wait_bounded(&ms.drain[gr], 0, WAIT_LIMIT_NS);
+      }
+    }
+  } else {
+    // ================ softmax: group gr, thread = accumulator row r
+    const int gr = warp >> 2, r = tid & 127;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + TM_S + 128 * gr, tO = tmem + lane_off + TM_O + 128 * gr;
+    const int rq = r / p.gq, rh = r - rq * p.gq;
+    uint32_t kc = 0, vc = 0, ns = 0, npv = 0;  // K, V stages passed; S tiles; completions of pv_done
+    while (ok && next_item(p, w, it)) {
+      const int n = it.t1 - it.t0;
+      const int q0 = it.qt * p.qpu + (ALT ? 0 : gr * p.qpt);
+      if (q0 >= it.s.T) {  // (not ALT) no second row tile
+        kc += n, vc += n + R_TILES;
+        continue;
+      }
+      const int qi = q0 + rq;
+      const bool live = rq < p.qpt && qi < it.s.T;
+      const int64_t brow = (int64_t)it.s.row + qi;                       // batch row
+      const int head = it.h * p.gq + rh;
+      const int64_t qrow = brow * p.Hq + head;
+      const int pos = live ? it.s.base + qi : -1;
+      const float rsc = live ? p.qsc[qrow] : 0.f;
+      const uint64_t rsc2 = pk2(rsc, rsc);
+      if (!ALT || LO || gr == 0) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.qh + (size_t)qrow * 2 * D + (LO ? gr * D : 0));
+        uint8_t *dst = smem + OFF_Q + gr * SW_TILE_BYTES;
+        uint4 v[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) v[c] = live ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4 *>(dst + sw128_offset(r, 8 * c)) = v[c];
+        fence_async_smem();
+      }
+      mbar_arrive(&ms.q_ready[gr]);
+
+      float M = -INFINITY, l = 0.f;
+      int done = 0;
+      for (int i = ALT ? gr : 0; i < n; i += ALT ? 2 : 1) {
+        const int kf = (it.t0 + i) * KT;
+        const uint32_t cv = vc + i;
+        ok = wait(&ms.s_done[gr], ns & 1);
+        ++ns;
+        if (ok) ok = wait(&ms.v_full[cv & 1], (cv >> 1) & 1);
+        ok = __all_sync(FULL_MASK, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const float4 *kn4 = reinterpret_cast<const float4 *>(ms.kn[(kc + i) & 3]);
+        const float4 *nv4 = reinterpret_cast<const float4 *>(ms.nv[cv & 1]);
+        const bool full = kf + KT - 1 <= it.s.base + q0;  // every row sees every key of the tile
+        // the largest s + log2(value norm) of the row
+        auto row_max = [&]() -> float {
+          float bm = -INFINITY;
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            float sv[32];
+            tmem_ld32(tS + 32 * cc, sv);
+#pragma unroll
+            for (int c4 = 0; c4 < 8; ++c4) {
+              const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
+              const float k_[4] = {kn.x, kn.y, kn.z, kn.w}, v_[4] = {nv.x, nv.y, nv.z, nv.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float u = fmaf(sv[4 * c4 + e] * k_[e], rsc, fmaxf(log2_approx(v_[e]) - P_SHIFT, -64.f));
+                if (full || kf + 32 * cc + 4 * c4 + e <= pos) bm = fmaxf(bm, u);
+              }
+            }
+          }
+          return bm;
+        };
+        // raise the running maximum of the rows that need it (the warp together)
+        auto raise_max = [&]() {
+          const float bm = row_max();
+          const bool raise = bm > M + RESCALE_SLACK;  // also from -inf
+          const float alpha = raise ? exp2_approx(M - bm) : 1.f;
+          if (raise) M = bm, l *= alpha;
+          if (done && __any_sync(FULL_MASK, raise)) {
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+              float o[32];
+              tmem_ld32(tO + 32 * cc, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= alpha;
+              tmem_st32(tO + 32 * cc, o);
+            }
+          }
+        };
+        // two columns: exponentials into l2, probabilities as fp32
+        uint64_t l2;
+        auto pair = [&](float s0, float s1, float k0, float k1, float v0, float v1, int c, uint64_t nm2, float &p0, float &p1) {
+          const uint64_t d2 = fma2(mul2(pk2(s0, s1), pk2(k0, k1)), rsc2, nm2);
+          float d0, d1;
+          upk2(d2, d0, d1);
+          float e0 = exp2_approx(d0), e1 = exp2_approx(d1);
+          if (!full) e0 = kf + c <= pos ? e0 : 0.f, e1 = kf + c + 1 <= pos ? e1 : 0.f;
+          const uint64_t e2 = pk2(e0, e1);
+          l2 = add2(l2, e2);
+          upk2(mul2(e2, pk2(v0, v1)), p0, p1);
+          if (!full) p0 = kf + c <= pos ? p0 : 0.f, p1 = kf + c + 1 <= pos ? p1 : 0.f;  // a masked norm may be anything
+        };
+        if constexpr (LO) {
+          raise_max();
+          const float Mu = (M == -INFINITY) ? 0.f : M;
+          const uint64_t nm2 = pk2(-Mu, -Mu);
+          l2 = pk2(0.f, 0.f);
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            float sv[32];
+            tmem_ld32(tS + 32 * cc, sv);
+            uint32_t pw[32];  // the chunk's hi words, then its lo words, over its own columns
+#pragma unroll
+            for (int c4 = 0; c4 < 8; ++c4) {
+              const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
+              float p0, p1;
+              pair(sv[4 * c4], sv[4 * c4 + 1], kn.x, kn.y, nv.x, nv.y, 32 * cc + 4 * c4, nm2, p0, p1);
+              split_half2(p0, p1, pw[2 * c4], pw[16 + 2 * c4]);
+              pair(sv[4 * c4 + 2], sv[4 * c4 + 3], kn.z, kn.w, nv.z, nv.w, 32 * cc + 4 * c4 + 2, nm2, p0, p1);
+              split_half2(p0, p1, pw[2 * c4 + 1], pw[16 + 2 * c4 + 1]);
+            }
+            tmem_st32(tS + 32 * cc, pw);
+          }
+        } else {
+          uint32_t pw[64];
+          bool need = live && M == -INFINITY && kf <= pos;
+          for (int turn = 0;; ++turn) {
+            if (__any_sync(FULL_MASK, need)) raise_max();
+            const float Mu = (M == -INFINITY) ? 0.f : M;
+            const uint64_t nm2 = pk2(-Mu, -Mu);
+            l2 = pk2(0.f, 0.f);
+            __half2 pm = __float2half2_rn(0.f);
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+              float sv[32];
+              tmem_ld32(tS + 32 * cc, sv);
+#pragma unroll
+              for (int c4 = 0; c4 < 8; ++c4) {
+                const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
+                float p0, p1;
+                pair(sv[4 * c4], sv[4 * c4 + 1], kn.x, kn.y, nv.x, nv.y, 32 * cc + 4 * c4, nm2, p0, p1);
+                const __half2 h0 = __floats2half2_rn(p0, p1);
+                pair(sv[4 * c4 + 2], sv[4 * c4 + 3], kn.z, kn.w, nv.z, nv.w, 32 * cc + 4 * c4 + 2, nm2, p0, p1);
+                const __half2 h1 = __floats2half2_rn(p0, p1);
+                pm = __hmax2(pm, __hmax2(h0, h1));
+                pw[16 * cc + 2 * c4] = *reinterpret_cast<const uint32_t *>(&h0);
+                pw[16 * cc + 2 * c4 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+              }
+            }
+            need = live && (__low2float(pm) > 32768.f || __high2float(pm) > 32768.f);
+            if (turn || !__any_sync(FULL_MASK, need)) break;
+          }
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t half[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) half[e] = pw[32 * hf + e];
+            tmem_st32(tS + 32 * hf, half);
+          }
+        }
+        float l0, l1;
+        upk2(l2, l0, l1);
+        l += l0 + l1;
+        tc_fence_before();
+        mbar_arrive(&ms.p_ready[gr]);
+        ++done;
+      }
+      kc += n, vc += n + R_TILES;
+
+      // ---- end of the item: O / l as fp16 with a power-of-two row scale, times R
+      npv += done;
+      if (ok && done) {
+        ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr], (npv - 1) & 1));
+        tc_fence_after();
+      }
+      float amax = 0.f;
+      if (ok && done) {
+#pragma unroll 1
+        for (int cc = 0; cc < 4; ++cc) {
+          float o[32];
+          tmem_ld32(tO + 32 * cc, o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) amax = fmaxf(amax, fabsf(o[e]));
+        }
+      }
+      float fw = 1.f;
+      if (ALT) {  // the two groups' states of a row, merged
+        ms.xm[gr][r] = M, ms.xl[gr][r] = l, ms.xa[gr][r] = amax;
+        if (softmax_sync_or(!ok)) {
+          ok = false;
+          break;
+        }
+        const float M0 = ms.xm[0][r], M1 = ms.xm[1][r], l0 = ms.xl[0][r], l1 = ms.xl[1][r];
+        const float a0 = ms.xa[0][r], a1 = ms.xa[1][r];
+        (void)softmax_sync_or(false);  // read: the next item may write them
+        const float Mx = fmaxf(M0, M1);
+        const float f0 = M0 == -INFINITY ? 0.f : exp2f(M0 - Mx), f1 = M1 == -INFINITY ? 0.f : exp2f(M1 - Mx);
+        fw = gr ? f1 : f0;
+        l = (f0 ? f0 * l0 : 0.f) + (f1 ? f1 * l1 : 0.f);
+        amax = fmaxf(f0 ? f0 * a0 : 0.f, f1 ? f1 * a1 : 0.f);
+        M = Mx;
+      } else if (!ok) {
+        break;
+      }
+      const float fo = l == 0.f ? 0.f : p.inv_vscale / l;
+      const float am = amax * fo;
+      const int ex = (am > 0.f && isfinite(am)) ? ilogbf(am) - 13 : 0;
+      const float mul = ldexpf(fo * fw, -ex), back = ldexpf(1.f, ex);
+      const bool zero = done == 0 || fw == 0.f || fo == 0.f;  // O holds nothing (of the row)
+#pragma unroll 1
+      for (int c2 = 0; c2 < (LO ? 4 : 2); ++c2) {
+        uint32_t pw[32];
+        if constexpr (LO) {
+          float o[32];
+          tmem_ld32(tO + 32 * c2, o);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            split_half2(zero ? 0.f : o[2 * e] * mul, zero ? 0.f : o[2 * e + 1] * mul, pw[e], pw[16 + e]);
+        } else {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float o[32];
+            tmem_ld32(tO + 64 * c2 + 32 * hf, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              pw[16 * hf + e] = pack_half2(zero ? 0.f : o[2 * e] * mul, zero ? 0.f : o[2 * e + 1] * mul);
+          }
+        }
+        tmem_st32(tS + 32 * c2, pw);
+      }
+      tc_fence_before();
+      mbar_arrive(&ms.p_ready[gr]);
+      if (ALT && gr == 1) continue;
+      ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr], npv & 1));
+      ++npv;
+      if (!ok) break;
+      tc_fence_after();
+
+      // ---- the unit's rows, or this CTA's partial of them
+      const Start st = p.start[blockIdx.x];
+      const int first = share_of(it.vstart, st.V, st.G);
+      const int n_split = share_of(it.vstart + it.tiles - 1, st.V, st.G) - first + 1;
+      if (tid == 0 && (int)blockIdx.x != first)
+        p.join[blockIdx.x] = JoinInfo{it.s.row + it.qt * p.qpu, it.s.T - it.qt * p.qpu, 0, it.h, first, n_split};
+      if (n_split > 1) {
+        float *dst = p.split + ((size_t)(blockIdx.x * 2 + ((int)blockIdx.x == first ? 1 : 0)) * (ALT ? 128 : 256) +
+                                gr * 128 + r) * SROW;
+#pragma unroll 1
+        for (int cc = 0; cc < 4; ++cc) {
+          float o[32];
+          tmem_ld32(tO + 32 * cc, o);
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4 *>(dst + 32 * cc + e) = make_float4(o[e] * back, o[e + 1] * back, o[e + 2] * back, o[e + 3] * back);
+          }
+          __syncwarp();
+        }
+        if (live) dst[D] = M, dst[D + 1] = l;
+        continue;
+      }
+      const DiffView &df = p.o.diff;
+      float scale = back, lam = 0.f;
+      int64_t at = qrow * D;
+      bool store = live;
+      if (df.lambda) {  // rows r and r ^ 1 are a pair: the even lane finishes it
+        const int pair_i = head >> 1;
+        at = (brow * (p.Hq / 2) + pair_i) * D;
+        store = live && !(r & 1);
+        if (live) lam = df.lambda[brow * df.lambda_stride + pair_i];
+        scale = df.out_scale;
+        if (df.gain) {
+          float ss = 0.f;
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            float o[32];
+            tmem_ld32(tO + 32 * cc, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float a = o[e] * back, b = __shfl_xor_sync(FULL_MASK, a, 1), d = fmaf(-lam, b, a);
+              ss = fmaf(d, d, ss);
+            }
+          }
+          // all zero (a row without keys) stays zero whatever eps is
+          scale = ss == 0.f ? 0.f : scale * rsqrtf(fmaf(ss, 1.0f / D, df.eps));
+        }
+      }
+#pragma unroll 1
+      for (int cc = 0; cc < 4; ++cc) {
+        float o[32];
+        tmem_ld32(tO + 32 * cc, o);
+        if (df.lambda) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float a = o[e] * back, b = __shfl_xor_sync(FULL_MASK, a, 1);
+            o[e] = fmaf(-lam, b, a) * scale * (df.gain ? df.gain[32 * cc + e] : 1.f);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= scale;
+        }
+        if (store && p.o.dtype == TQ_DTYPE_F32) {
+          float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.o.out) + at + 32 * cc);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else if (store) {
+          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o.out) + at + 32 * cc);
+          const bool bf = p.o.dtype == TQ_DTYPE_BF16;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t x[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              x[m] = bf ? pack_bf162(o[8 * e + 2 * m], o[8 * e + 2 * m + 1]) : pack_half2(o[8 * e + 2 * m], o[8 * e + 2 * m + 1]);
+            dst[e] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, TM_COLS);
+}
+
+// ------------------------------------------------------------------------------ join
+struct JoinParams {
+  PagedOut o;
+  int Hq, gq, qpt, unit_rows, grid;
+  const JoinInfo *join;
+  const float *split;
+};
+constexpr int JOIN_ROWS = 32;
+
+// CTA (c, i): rows 32 i .. + 31 of the unit whose second share is CTA c's; a warp per row (per
+// pair), o = sum w_s o_s / sum w_s with w_s = l_s 2^(m_s - m*).
+__global__ void __launch_bounds__(256) k_paged_join(const JoinParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  pdl_wait();
+  const int c = blockIdx.x;
+  const JoinInfo j = p.join[c];
+  if (j.n < 2 || j.first != c - 1) return;
+  const int ns = min(j.n, p.grid - j.first);
+  const bool diff = p.o.diff.lambda != nullptr;
+  for (int i = warp * (diff ? 2 : 1); i < JOIN_ROWS; i += 8 * (diff ? 2 : 1)) {
+    const int r = blockIdx.y * JOIN_ROWS + i, rr = r & 127, rq = rr / p.gq, qi = (r >> 7) * p.qpt + rq;
+    if (rq >= p.qpt || qi >= j.T) continue;
+    const int head = j.h * p.gq + rr - rq * p.gq;
+    float a[2][4];
+    for (int m = 0; m < (diff ? 2 : 1); ++m) {
+      float ms = -INFINITY, ls = 0.f;
+      a[m][0] = a[m][1] = a[m][2] = a[m][3] = 0.f;
+      for (int s = 0; s < ns; ++s) {
+        const float *src = p.split + ((size_t)((j.first + s) * 2 + (s == 0 ? 1 : 0)) * p.unit_rows + r + m) * SROW;
+        const float mx = __ldcg(src + D), lx = __ldcg(src + D + 1);
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
+        if (lx == 0.f) continue;
+        const float mn = fmaxf(ms, mx), f = exp2f(ms - mn), wx = lx * exp2f(mx - mn);
+        ms = mn;
+        ls = fmaf(ls, f, wx);
+        a[m][0] = fmaf(a[m][0], f, wx * v.x), a[m][1] = fmaf(a[m][1], f, wx * v.y);
+        a[m][2] = fmaf(a[m][2], f, wx * v.z), a[m][3] = fmaf(a[m][3], f, wx * v.w);
+      }
+      const float f = ls == 0.f ? 0.f : 1.f / ls;
+      for (int e = 0; e < 4; ++e) a[m][e] *= f;
+    }
+    const int64_t row = j.row + qi;
+    if (diff) {
+      diff_finish(a[0], a[1], p.o.diff, (int)row, head >> 1, lane);
+      store_lane4(p.o.out, p.o.dtype, (row * (p.Hq / 2) + (head >> 1)) * D, lane, a[0]);
+    } else {
+      store_lane4(p.o.out, p.o.dtype, (row * p.Hq + head) * D, lane, a[0]);
+    }
+  }
+}
+
+struct Layout {
+  int gq, qpt, qpu, grid, unit_rows;
+  bool alt, lo;
+  size_t qsc, prefix, start, join, split, bytes;
+};
+bool layout(const tq_ctx *k, const PagedView &pv, int Hq, int out_dtype, Layout *l) {
+  l->gq = Hq / pv.Hkv;
+  l->qpt = 128 / l->gq;
+  l->lo = out_dtype != TQ_DTYPE_BF16;
+  // one row tile: both groups on it, else half of the softmax would idle
+  l->alt = l->lo || pv.max_q <= l->qpt;
+  l->qpu = l->alt ? l->qpt : 2 * l->qpt;
+  l->unit_rows = l->alt ? 128 : 256;
+  l->grid = k->num_sms;
+  const int64_t units = ((int64_t)pv.n_tokens / l->qpu + pv.B + 1) * pv.Hkv;
+  const int64_t tiles = units * (((int64_t)pv.max_len + KT - 1) / KT + UNIT_TILES);
+  if (tiles > INT32_MAX || (int64_t)pv.n_tokens * Hq > INT32_MAX) return false;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  const size_t rows = (size_t)pv.n_tokens * Hq;
+  l->qsc = up(rows * 2 * D * 2);
+  l->prefix = l->qsc + up(rows * 4);
+  l->start = l->prefix + up((size_t)(pv.B + 1) * 4);
+  l->join = l->start + up((size_t)l->grid * sizeof(Start));
+  l->split = l->join + up((size_t)l->grid * sizeof(JoinInfo));
+  l->bytes = l->split + up((size_t)l->grid * 2 * l->unit_rows * SROW * 4);
+  return true;
+}
+
+template <bool ALT, bool LO>
+cudaError_t launch_main(const PrefillParams &p, int grid, cudaStream_t st) {
+  cudaError_t e = kernel_smem_attr((const void *)k_paged_prefill<ALT, LO>, (int)SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_paged_prefill<ALT, LO>, dim3(grid), dim3(THREADS), SMEM, st, p);
+}
+
+}  // namespace
+
+bool paged_prefill_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes) {
+  Layout a, b;  // the size does not depend on the output's type
+  if (!layout(k, pv, Hq, TQ_DTYPE_BF16, &a) || !layout(k, pv, Hq, TQ_DTYPE_F32, &b)) return false;
+  *bytes = a.bytes > b.bytes ? a.bytes : b.bytes;
+  return true;
+}
+
+cudaError_t launch_paged_prefill(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,
+                                 const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope, float scale,
+                                 const PagedOut &o, void *ws, cudaStream_t st) {
+  Layout l;
+  if (!layout(k, pv, Hq, o.dtype, &l)) return cudaErrorInvalidValue;
+  uint8_t *base = static_cast<uint8_t *>(ws);
+  PrepParams a{};
+  a.pv = pv, a.q = q, a.rope = rope, a.o = o;
+  a.Hq = Hq, a.qpu = l.qpu, a.grid = l.grid;
+  a.qmul = LOG2E * scale / k->f16.alpha;
+  a.kfrag = k->d_rfrag;
+  a.qh = reinterpret_cast<uint16_t *>(base);
+  a.qsc = reinterpret_cast<float *>(base + l.qsc);
+  a.prefix = reinterpret_cast<int32_t *>(base + l.prefix);
+  a.start = reinterpret_cast<Start *>(base + l.start);
+  a.join = reinterpret_cast<JoinInfo *>(base + l.join);
+  a.lo = l.lo;
+  const int64_t rows = (int64_t)pv.n_tokens * Hq;
+  cudaError_t e = launch_pdl(k_paged_prep, dim3(1 + (unsigned)((rows + PREP_ROWS - 1) / PREP_ROWS)), dim3(256), 0, st, a);
+  if (e != cudaSuccess) return e;
+  PrefillParams p{};
+  p.pv = pv, p.kp = kp, p.vp = vp, p.o = o;
+  p.Hq = Hq, p.gq = l.gq, p.qpt = l.qpt, p.qpu = l.qpu;
+  p.qh = a.qh, p.qsc = a.qsc, p.start = a.start, p.join = a.join;
+  p.split = reinterpret_cast<float *>(base + l.split);
+  for (int i = 0; i < 2; ++i) {
+    p.klo[i] = k->f16.lo[i], p.khi[i] = k->f16.hi[i];
+    p.vlo[i] = v->f16.lo[i], p.vhi[i] = v->f16.hi[i];
+  }
+  p.inv_vscale = 1.0f / (exp2f(P_SHIFT) * v->f16.alpha);
+  p.vr = reinterpret_cast<const uint8_t *>(v->d_rtile);
+  e = l.lo ? launch_main<true, true>(p, l.grid, st)
+           : (l.alt ? launch_main<true, false>(p, l.grid, st) : launch_main<false, false>(p, l.grid, st));
+  if (e != cudaSuccess) return e;
+  JoinParams j{};
+  j.o = o;
+  j.Hq = Hq, j.gq = l.gq, j.qpt = l.qpt, j.unit_rows = l.unit_rows, j.grid = l.grid;
+  j.join = p.join, j.split = p.split;
+  return launch_pdl(k_paged_join, dim3(l.grid, l.unit_rows / JOIN_ROWS), dim3(256), 0, st, j);
+}
+
+}  // namespace tq

@@ -473,10 +473,12 @@ tq_status tq_paged_gather(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_pag
  *   out        device [n_tokens][Hq][128] of out_dtype (F32, BF16 or F16), 16-byte aligned.
  *   workspace  device scratch of tq_paged_workspace_size() bytes for the same batch sizes,
  *              256-byte aligned; its contents need no initialisation.
- * Sums, maxima and outputs are held in fp32; the tensor-core operands are fp16 parts
- * (header comments of the kernels state which products carry one part and which two).
- * Accuracy: 2e-3 absolute, 1e-3 relative per row, as tq_decode_attention, before the
- * rounding to out_dtype. */
+ * Sums, maxima and outputs are held in fp32; the tensor-core operands are fp16 parts (the
+ * kernels' header comments state which products carry one part and which two).  With scores
+ * of ordinary size the rows are within 2e-3 absolute and 1e-3 relative of the formula, as
+ * tq_decode_attention's, before the rounding to out_dtype; a score itself is off by at most
+ * about 7e-5 scale |q| |k_hat| (the fp16 centroid table; chunks with a BF16 output add q's
+ * own rounding to fp16), which is what counts where scores reach the hundreds. */
 tq_status tq_paged_workspace_size(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
                                   const tq_paged_batch *batch, int Hq, size_t *bytes);
 tq_status tq_paged_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,

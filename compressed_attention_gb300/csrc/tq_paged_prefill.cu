@@ -53,7 +53,6 @@ constexpr int NRAW = 3;
 constexpr int W_DEC = 8, W_MMA = 12, W_LOAD = 14, N_WARPS = 15;
 constexpr int THREADS = N_WARPS * 32;
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // S / P of the groups, O of the groups
-constexpr uint32_t IDESC_PV = IDESC_F16 | (1u << 16);    // B stored MN-major
 
 constexpr uint32_t OFF_Q = 0, OFF_K = 2 * SW_TILE_BYTES, OFF_V = 4 * SW_TILE_BYTES;
 constexpr uint32_t OFF_RAW = 6 * SW_TILE_BYTES, OFF_MISC = OFF_RAW + NRAW * RAW;
@@ -368,19 +367,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Descriptor of a value tile as the MN-major B operand: 64-dim halves SW_HALF_BYTES apart
-// (leading offset), groups of eight keys 1024 bytes apart (stride offset), 128-byte swizzle.
-// K-step s of 16 keys starts 2048 s bytes in.
-__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((SW_HALF_BYTES >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((1024u >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
 // Barrier over the 256 softmax threads that ORs a failure flag across them.
 __device__ __forceinline__ bool softmax_sync_or(bool fail) {
   uint32_t r;
@@ -582,7 +568,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
             for (int part = 0; part < (LO ? 2 : 1); ++part)
 #pragma unroll
               for (int s = 0; s < 8; ++s)
-                umma_ts<IDESC_PV>(tO, tS + (LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s), v_desc(vb + 2048 * s),
+                umma_ts<IDESC_F16_BMN>(tO, tS + (LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s), sw128_mn_desc(vb + 2048 * s),
                                   (!first || part || s) ? 1u : 0u);
             umma_commit(&ms.pv_done[gr]);
             umma_commit(&ms.v_empty[c & 1]);
@@ -618,8 +604,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
                 for (int part = 0; part < (LO && r == 0 ? 2 : 1); ++part)
 #pragma unroll
                   for (int s = 0; s < 8; ++s)
-                    umma_ts<IDESC_PV>(tO, tS + 128 * src + (LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s),
-                                      v_desc(vb + 2048 * s), (r || src || part || s) ? 1u : 0u);
+                    umma_ts<IDESC_F16_BMN>(tO, tS + 128 * src + (LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s),
+                                      sw128_mn_desc(vb + 2048 * s), (r || src || part || s) ? 1u : 0u);
               umma_commit(&ms.v_empty[c & 1]);
             } else {
               mbar_arrive(&ms.v_empty[c & 1]);

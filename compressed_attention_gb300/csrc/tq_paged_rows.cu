@@ -1,6 +1,6 @@
-// Append to and read back from the paged cache.
+// Append to the paged cache.
 //
-// Append (k_paged_append_wht): SET_ROWS through the block table with the keys' position
+// k_paged_append_wht: SET_ROWS through the block table with the keys' position
 // rotation applied on the way.  The row's encode is the write path's (tq_wht.cuh): four
 // threads per row, eight rows per warp, the canonical order of norm, division and
 // butterfly, so the stored bytes equal those of a plain fp32 sequence.  The rotation's
@@ -211,68 +211,6 @@ __global__ void __launch_bounds__(AD_WARPS * 32) k_paged_append_dense(const Appe
   }
 }
 
-// ------------------------------------------------------------------------------ gather
-struct GatherSide {
-  const uint8_t *pages;
-  void *out;
-  float c[16];
-  const float *r;  // R, fp32 row-major; null: rotated basis
-};
-struct GatherParams {
-  PagedView pv;
-  GatherSide side[2];
-  int dtype;
-  int only;  // 0 or 1: one side; 2: both, alternating CTAs
-};
-
-// A warp per row: lane l holds elements 4l .. 4l + 3; x = norm * R^T c with R staged once.
-constexpr int GA_WARPS = 8;
-constexpr size_t GA_SMEM = (size_t)D * D * 4 + GA_WARPS * D * 4;
-__global__ void __launch_bounds__(GA_WARPS * 32) k_paged_gather(const GatherParams p) {
-  extern __shared__ __align__(16) float gsm[];
-  float *rs = gsm, *cv = gsm + D * D;
-  __shared__ float ct[16];
-  const int side = p.only == 2 ? (blockIdx.x & 1) : p.only, step = p.only == 2 ? 2 : 1;
-  const GatherSide &sd = p.side[side];
-  pdl_trigger();
-  if (sd.r) stage_matrix(rs, sd.r);
-  if (threadIdx.x < 16) ct[threadIdx.x] = sd.c[threadIdx.x];
-  __syncthreads();
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float *c = cv + warp * D;
-  const int64_t n_rows = (int64_t)paged_rows(p.pv) * p.pv.Hkv;
-  const int n_cta = gridDim.x / step;
-  for (int64_t row = (int64_t)(blockIdx.x / step) * GA_WARPS + warp; row < n_rows; row += (int64_t)n_cta * GA_WARPS) {
-    const int tok = (int)(row / p.pv.Hkv), h = (int)(row - (int64_t)tok * p.pv.Hkv);
-    const int b = paged_seq(p.pv, tok), n = paged_len(p.pv, b, lane == 0), pos = paged_pos(p.pv, b, tok, n);
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (pos >= 0 && pos < n) {
-      const int pg = max(paged_page(p.pv, b, pos, lane == 0), 0);
-      const uint8_t *src = sd.pages + paged_row(p.pv, pg, h, pos & ((1 << p.pv.page_shift) - 1));
-      const float norm = *reinterpret_cast<const float *>(src);
-      const uint32_t w = *reinterpret_cast<const uint16_t *>(src + 4 + 2 * lane);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = ct[(w >> (4 * e)) & 15u];
-      if (sd.r) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[4 * lane + e] = x[e], x[e] = 0.f;
-        __syncwarp();
-#pragma unroll 8
-        for (int k = 0; k < D; ++k) {
-          const float4 r4 = *reinterpret_cast<const float4 *>(rs + k * D + 4 * lane);
-          x[0] = fmaf(r4.x, c[k], x[0]), x[1] = fmaf(r4.y, c[k], x[1]);
-          x[2] = fmaf(r4.z, c[k], x[2]), x[3] = fmaf(r4.w, c[k], x[3]);
-        }
-        __syncwarp();
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] *= norm;
-    }
-    store_lane4(sd.out, p.dtype, (size_t)row * D, lane, x);
-  }
-}
-
 template <typename K>
 cudaError_t launch_rows(K kern, const AppendParams &p, int threads, int rows_per_cta, size_t smem, int sms,
                         cudaStream_t st) {
@@ -322,31 +260,6 @@ cudaError_t launch_paged_append(const tq_ctx *k, const tq_ctx *v, const PagedVie
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
-}
-
-cudaError_t launch_paged_gather(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,
-                                const uint8_t *vp, int unrotate, void *k_out, void *v_out, int out_dtype,
-                                cudaStream_t st) {
-  GatherParams p{};
-  p.pv = pv;
-  p.dtype = out_dtype;
-  p.only = k_out && v_out ? 2 : (k_out ? 0 : 1);
-  const tq_ctx *ctx[2] = {k, v};
-  for (int i = 0; i < 2; ++i) {
-    p.side[i].pages = i ? vp : kp;
-    p.side[i].out = i ? v_out : k_out;
-    for (int j = 0; j < 16; ++j) p.side[i].c[j] = ctx[i]->cb.c[j];
-    p.side[i].r = unrotate ? ctx[i]->d_pi : nullptr;
-  }
-  cudaError_t e = kernel_smem_attr((const void *)k_paged_gather, (int)GA_SMEM);
-  int blocks = 1;
-  if (e == cudaSuccess) e = kernel_occupancy((const void *)k_paged_gather, GA_WARPS * 32, GA_SMEM, &blocks);
-  if (e != cudaSuccess) return e;
-  const int sides = p.only == 2 ? 2 : 1;
-  const int64_t want = ((int64_t)pv.n_tokens * pv.Hkv + GA_WARPS - 1) / GA_WARPS;
-  const int64_t most = (int64_t)k->num_sms * blocks / sides;
-  return launch_pdl(k_paged_gather, dim3(sides * (unsigned)(want < most ? want : most)), dim3(GA_WARPS * 32), GA_SMEM,
-                    st, p);
 }
 
 }  // namespace tq

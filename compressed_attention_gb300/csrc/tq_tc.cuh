@@ -38,11 +38,25 @@ __device__ __forceinline__ uint32_t sw128_kstep(int s) {
   return (uint32_t)(s >> 2) * SW_HALF_BYTES + (uint32_t)(s & 3) * 32;
 }
 
+// Descriptor of the same tile read as the MN-major B operand (rows = K, columns = N): 64-column
+// halves SW_HALF_BYTES apart (leading offset), groups of eight rows 1024 bytes apart (stride
+// offset).  K-step s of 16 rows starts 2048 s bytes in.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((SW_HALF_BYTES >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((1024u >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;                         // descriptor version
+  d |= (uint64_t)2 << 61;                         // 128-byte swizzle
+  return d;
+}
+
 // Instruction descriptors of kind::f16, fp32 accumulator, both operands K-major,
 // M = N = 128: bf16 A and B, or fp16 A and B (one MMA never mixes the two).
 constexpr uint32_t IDESC_M128_N128 = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t IDESC_BF16 = IDESC_M128_N128 | (1u << 7) | (1u << 10);
 constexpr uint32_t IDESC_F16 = IDESC_M128_N128;
+constexpr uint32_t IDESC_F16_BMN = IDESC_F16 | (1u << 16);  // B stored MN-major
 
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols));

@@ -192,8 +192,10 @@ __device__ __forceinline__ int seq_vtiles(const PagedView &v, int b, int qpu, bo
   return sum * v.Hkv;
 }
 
-// One CTA of 256 threads: prefix sums over the sequences, then every share's start.
-__device__ void plan(const PrepParams &p) {
+// One CTA of 256 threads: prefix sums over the sequences (in shared memory up to n_sm of
+// them), then every share's start.
+__device__ void plan(const PrepParams &p, int *sm_prefix, int n_sm) {
+  int *prefix = p.pv.B <= n_sm ? sm_prefix : p.prefix;
   __shared__ int wsum[8];
   __shared__ int carry;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -212,13 +214,12 @@ __device__ void plan(const PrepParams &p) {
     __syncthreads();
     int before = carry;
     for (int w = 0; w < warp; ++w) before += wsum[w];
-    if (b < p.pv.B) p.prefix[b] = before + inc - t;
+    if (b < p.pv.B) prefix[b] = before + inc - t;
     __syncthreads();
     if (tid == 255) carry = before + inc;
     __syncthreads();
   }
   const int V = carry, G = min(p.grid, V);
-  __threadfence_block();
   for (int c = tid; c < p.grid; c += 256) {
     Start st{0, 0, 0, 0, 0, 0, V, G};
     p.join[c].n = 0;
@@ -228,11 +229,11 @@ __device__ void plan(const PrepParams &p) {
       int lo = 0, hi = p.pv.B - 1;  // the last sequence whose prefix is <= v (empty ones are passed over)
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.prefix[mid] <= st.v) lo = mid;
+        if (prefix[mid] <= st.v) lo = mid;
         else hi = mid - 1;
       }
       st.b = lo;
-      int o = st.v - p.prefix[lo];
+      int o = st.v - prefix[lo];
       const Seq s = seq_of(p.pv, lo, p.qpu, false);
       for (; st.qt < s.n_qt; ++st.qt) {
         const int t = unit_tiles(s, st.qt, p.qpu), vt = t ? t + UNIT_TILES : 0;
@@ -248,46 +249,100 @@ __device__ void plan(const PrepParams &p) {
   }
 }
 
+// Elements 4l .. 4l + 3 of N rows at once (all loads in flight); a null row gives zeros.
+template <int N>
+__device__ __forceinline__ void load_rows(const uint8_t *const (&row)[N], int dtype, int lane, float (&x)[N][4]) {
+  if (dtype == TQ_DTYPE_F32) {
+    float4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      v[i] = row[i] ? reinterpret_cast<const float4 *>(row[i])[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i][0] = v[i].x, x[i][1] = v[i].y, x[i][2] = v[i].z, x[i][3] = v[i].w;
+    return;
+  }
+  uint2 v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = row[i] ? reinterpret_cast<const uint2 *>(row[i])[lane] : make_uint2(0u, 0u);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (dtype == TQ_DTYPE_BF16) {
+      x[i][0] = bf16_bits_to_f32(v[i].x & 0xFFFFu), x[i][1] = bf16_bits_to_f32(v[i].x >> 16);
+      x[i][2] = bf16_bits_to_f32(v[i].y & 0xFFFFu), x[i][3] = bf16_bits_to_f32(v[i].y >> 16);
+    } else {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v[i].x));
+      const float2 c = __half22float2(*reinterpret_cast<const __half2 *>(&v[i].y));
+      x[i][0] = a.x, x[i][1] = a.y, x[i][2] = c.x, x[i][3] = c.y;
+    }
+  }
+}
+
 __global__ void __launch_bounds__(256) k_paged_prep(const PrepParams p) {
   __shared__ __align__(16) uint16_t xs[2][PREP_ROWS][PREP_PITCH];  // bf16 hi, lo
+  __shared__ int pos_s[PREP_ROWS], tok_s[PREP_ROWS];
   float(*y)[D + 4] = reinterpret_cast<float(*)[D + 4]>(&xs[0][0][0]);  // over both, after the products
   static_assert(sizeof(xs) >= PREP_ROWS * (D + 4) * 4, "y over the parts");
   pdl_trigger();
   pdl_wait();
   if (blockIdx.x == 0) {
-    plan(p);
+    plan(p, reinterpret_cast<int *>(&xs[0][0][0]), (int)(sizeof(xs) / 4));
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int64_t n = (int64_t)paged_rows(p.pv) * p.Hq, r0 = (int64_t)(blockIdx.x - 1) * PREP_ROWS;
   if (r0 >= n) return;
-  // rows 8 per warp: load, position rotation, bf16 parts
-  for (int i = 0; i < PREP_ROWS / 8; ++i) {
-    const int r = warp * (PREP_ROWS / 8) + i;
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r0 + r < n) {
-      const int tok = (int)((r0 + r) / p.Hq), h = (int)((r0 + r) - (int64_t)tok * p.Hq);
-      const int b = paged_seq(p.pv, tok), len = paged_len(p.pv, b, false), pos = paged_pos(p.pv, b, tok, len);
-      if (pos >= 0) {
-        load_lane4(p.q.data + tok * p.q.token_bytes + h * p.q.head_bytes, p.q.dtype, lane, x);
-        if (p.rope.rot_dim) rope_lane4(x, lane, p.rope, rope_pos(p.rope, pos, p.pv.status, lane == 0));
-      } else {  // no key: the row's output is zero
+  // the rows' places: a thread each
+  if (threadIdx.x < PREP_ROWS) {
+    const int64_t r = r0 + threadIdx.x;
+    int tok = -1, pos = -1;
+    if (r < n) {
+      tok = (int)(r / p.Hq);
+      const int b = paged_seq(p.pv, tok);
+      pos = paged_pos(p.pv, b, tok, paged_len(p.pv, b, false));
+    }
+    tok_s[threadIdx.x] = tok, pos_s[threadIdx.x] = pos;
+  }
+  __syncthreads();
+  // eight rows per warp, four at a time: load, position rotation, bf16 parts
+  constexpr int NR = 4;
+#pragma unroll 1
+  for (int i0 = 0; i0 < PREP_ROWS / 8; i0 += NR) {
+    const int rb = warp * (PREP_ROWS / 8) + i0;
+    const uint8_t *src[NR];
+    int pos[NR];
+    float x[NR][4];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int tok = tok_s[rb + i], h = (int)(r0 + rb + i - (int64_t)max(tok, 0) * p.Hq);
+      pos[i] = pos_s[rb + i];
+      src[i] = pos[i] >= 0 ? p.q.data + tok * p.q.token_bytes + h * p.q.head_bytes : nullptr;
+      if (tok >= 0 && pos[i] < 0) {  // no key: the row's output is zero
         const float z[4] = {0.f, 0.f, 0.f, 0.f};
-        if (!p.o.diff.lambda) store_lane4(p.o.out, p.o.dtype, (size_t)(r0 + r) * D, lane, z);
+        if (!p.o.diff.lambda) store_lane4(p.o.out, p.o.dtype, (size_t)(r0 + rb + i) * D, lane, z);
         else if (!(h & 1)) store_lane4(p.o.out, p.o.dtype, ((size_t)tok * (p.Hq / 2) + h / 2) * D, lane, z);
       }
+      if (p.rope.rot_dim) pos[i] = rope_pos(p.rope, pos[i], p.pv.status, lane == 0);
     }
-    uint32_t hi[2], lo[2];
+    load_rows(src, p.q.dtype, lane, x);
+    if (p.rope.rot_dim) {
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(x[2 * m], x[2 * m + 1]);
-      const float2 f = __bfloat1622float2(a);
-      const __nv_bfloat162 c = __floats2bfloat162_rn(isinf(f.x) ? 0.f : x[2 * m] - f.x, isinf(f.y) ? 0.f : x[2 * m + 1] - f.y);
-      hi[m] = *reinterpret_cast<const uint32_t *>(&a);
-      lo[m] = *reinterpret_cast<const uint32_t *>(&c);
+      for (int i = 0; i < NR; ++i) rope_lane4(x[i], lane, p.rope, pos[i]);
     }
-    *reinterpret_cast<uint2 *>(&xs[0][r][4 * lane]) = make_uint2(hi[0], hi[1]);
-    *reinterpret_cast<uint2 *>(&xs[1][r][4 * lane]) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(x[i][2 * m], x[i][2 * m + 1]);
+        const float2 f = __bfloat1622float2(a);
+        const __nv_bfloat162 c = __floats2bfloat162_rn(isinf(f.x) ? 0.f : x[i][2 * m] - f.x,
+                                                       isinf(f.y) ? 0.f : x[i][2 * m + 1] - f.y);
+        hi[m] = *reinterpret_cast<const uint32_t *>(&a);
+        lo[m] = *reinterpret_cast<const uint32_t *>(&c);
+      }
+      *reinterpret_cast<uint2 *>(&xs[0][rb + i][4 * lane]) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2 *>(&xs[1][rb + i][4 * lane]) = make_uint2(lo[0], lo[1]);
+    }
   }
   __syncthreads();
   // warp: rows 16 (w % 4) .. + 15, columns 64 (w / 4) .. + 63 of Y = X R^T; R's A fragments hold
@@ -955,11 +1010,11 @@ struct JoinParams {
   const JoinInfo *join;
   const float *split;
 };
-constexpr int JOIN_ROWS = 32;
+constexpr int JOIN_WARPS = 8;
 
-// CTA (c, i): rows 32 i .. + 31 of the unit whose second share is CTA c's; a warp per row (per
-// pair), o = sum w_s o_s / sum w_s with w_s = l_s 2^(m_s - m*).
-__global__ void __launch_bounds__(256) k_paged_join(const JoinParams p) {
+// CTA (c, i): rows of the unit whose second share is CTA c's, a warp per row (per pair):
+// o = sum w_s o_s / sum w_s with w_s = l_s 2^(m_s - m*), four partials in flight.
+__global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const JoinParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();
@@ -968,35 +1023,46 @@ __global__ void __launch_bounds__(256) k_paged_join(const JoinParams p) {
   if (j.n < 2 || j.first != c - 1) return;
   const int ns = min(j.n, p.grid - j.first);
   const bool diff = p.o.diff.lambda != nullptr;
-  for (int i = warp * (diff ? 2 : 1); i < JOIN_ROWS; i += 8 * (diff ? 2 : 1)) {
-    const int r = blockIdx.y * JOIN_ROWS + i, rr = r & 127, rq = rr / p.gq, qi = (r >> 7) * p.qpt + rq;
-    if (rq >= p.qpt || qi >= j.T) continue;
-    const int head = j.h * p.gq + rr - rq * p.gq;
-    float a[2][4];
-    for (int m = 0; m < (diff ? 2 : 1); ++m) {
-      float ms = -INFINITY, ls = 0.f;
-      a[m][0] = a[m][1] = a[m][2] = a[m][3] = 0.f;
-      for (int s = 0; s < ns; ++s) {
+  const int r = (blockIdx.y * JOIN_WARPS + warp) * (diff ? 2 : 1), rr = r & 127, rq = rr / p.gq;
+  const int qi = (r >> 7) * p.qpt + rq;
+  if (rq >= p.qpt || qi >= j.T) return;
+  const int head = j.h * p.gq + rr - rq * p.gq;
+  float a[2][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    float ms = -INFINITY, ls = 0.f;
+    a[m][0] = a[m][1] = a[m][2] = a[m][3] = 0.f;
+    if (m && !diff) break;
+    for (int s0 = 0; s0 < ns; s0 += 4) {
+      float mx[4], lx[4];
+      float4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int s = min(s0 + i, ns - 1);
         const float *src = p.split + ((size_t)((j.first + s) * 2 + (s == 0 ? 1 : 0)) * p.unit_rows + r + m) * SROW;
-        const float mx = __ldcg(src + D), lx = __ldcg(src + D + 1);
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
-        if (lx == 0.f) continue;
-        const float mn = fmaxf(ms, mx), f = exp2f(ms - mn), wx = lx * exp2f(mx - mn);
+        mx[i] = __ldcg(src + D), lx[i] = __ldcg(src + D + 1);
+        v[i] = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (s0 + i >= ns || lx[i] == 0.f) continue;
+        const float mn = fmaxf(ms, mx[i]), f = exp2f(ms - mn), wx = lx[i] * exp2f(mx[i] - mn);
         ms = mn;
         ls = fmaf(ls, f, wx);
-        a[m][0] = fmaf(a[m][0], f, wx * v.x), a[m][1] = fmaf(a[m][1], f, wx * v.y);
-        a[m][2] = fmaf(a[m][2], f, wx * v.z), a[m][3] = fmaf(a[m][3], f, wx * v.w);
+        a[m][0] = fmaf(a[m][0], f, wx * v[i].x), a[m][1] = fmaf(a[m][1], f, wx * v[i].y);
+        a[m][2] = fmaf(a[m][2], f, wx * v[i].z), a[m][3] = fmaf(a[m][3], f, wx * v[i].w);
       }
-      const float f = ls == 0.f ? 0.f : 1.f / ls;
-      for (int e = 0; e < 4; ++e) a[m][e] *= f;
     }
-    const int64_t row = j.row + qi;
-    if (diff) {
-      diff_finish(a[0], a[1], p.o.diff, (int)row, head >> 1, lane);
-      store_lane4(p.o.out, p.o.dtype, (row * (p.Hq / 2) + (head >> 1)) * D, lane, a[0]);
-    } else {
-      store_lane4(p.o.out, p.o.dtype, (row * p.Hq + head) * D, lane, a[0]);
-    }
+    const float f = ls == 0.f ? 0.f : 1.f / ls;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[m][e] *= f;
+  }
+  const int64_t row = j.row + qi;
+  if (diff) {
+    diff_finish(a[0], a[1], p.o.diff, (int)row, head >> 1, lane);
+    store_lane4(p.o.out, p.o.dtype, (row * (p.Hq / 2) + (head >> 1)) * D, lane, a[0]);
+  } else {
+    store_lane4(p.o.out, p.o.dtype, (row * p.Hq + head) * D, lane, a[0]);
   }
 }
 
@@ -1082,7 +1148,8 @@ cudaError_t launch_paged_prefill(const tq_ctx *k, const tq_ctx *v, const PagedVi
   j.o = o;
   j.Hq = Hq, j.gq = l.gq, j.qpt = l.qpt, j.unit_rows = l.unit_rows, j.grid = l.grid;
   j.join = p.join, j.split = p.split;
-  return launch_pdl(k_paged_join, dim3(l.grid, l.unit_rows / JOIN_ROWS), dim3(256), 0, st, j);
+  return launch_pdl(k_paged_join, dim3(l.grid, l.unit_rows / (JOIN_WARPS * (o.diff.lambda ? 2 : 1))),
+                    dim3(JOIN_WARPS * 32), 0, st, j);
 }
 
 }  // namespace tq

@@ -37,6 +37,8 @@
 #include <math.h>
 #include <stddef.h>
 
+#include <type_traits>
+
 #include "tq_decode_common.cuh"
 #include "tq_paged.cuh"
 #include "tq_rotmma.cuh"
@@ -386,7 +388,11 @@ __global__ void __launch_bounds__(256) k_paged_prep(const PrepParams p) {
     float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
     for (int h = 16; h >= 1; h >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, h));
-    const int e = (amax > 0.f && isfinite(amax)) ? ilogbf(amax) - 13 : 0;
+    // The power of two that brings the largest element to [2^13, 2^14).  One part leaves rows alone
+    // whose largest element already lies in [2^-10, 2^14) (what fp16 drops there is below 2^-14 of
+    // it): their scores then need no scaling in the softmax.
+    const bool as_is = !p.lo && amax >= 0x1p-10f && amax < 0x1p14f;
+    const int e = (amax > 0.f && isfinite(amax) && !as_is) ? ilogbf(amax) - 13 : 0;
     uint32_t hi[2], lo[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) split_half2(ldexpf(x[2 * m], -e), ldexpf(x[2 * m + 1], -e), hi[m], lo[m]);
@@ -701,6 +707,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       const int pos = live ? it.s.base + qi : -1;
       const float rsc = live ? p.qsc[qrow] : 0.f;
       const uint64_t rsc2 = pk2(rsc, rsc);
+      const bool scaled = __any_sync(FULL_MASK, live && rsc != 1.f);
       if (!ALT || LO || gr == 0) {
         const uint4 *src = reinterpret_cast<const uint4 *>(p.qh + (size_t)qrow * 2 * D + (LO ? gr * D : 0));
         uint8_t *dst = smem + OFF_Q + gr * SW_TILE_BYTES;
@@ -764,40 +771,47 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
             }
           }
         };
-        // two columns: exponentials into l2, probabilities as fp32
+        // two columns: exponentials into l2, probabilities as fp32.  Tiles that every row sees whole,
+        // with rows that carry no scale, take the short version.
         uint64_t l2;
-        auto pair = [&](float s0, float s1, float k0, float k1, float v0, float v1, int c, uint64_t nm2, float &p0, float &p1) {
-          const uint64_t d2 = fma2(mul2(pk2(s0, s1), pk2(k0, k1)), rsc2, nm2);
+        auto pair = [&](auto whole, float s0, float s1, float k0, float k1, float v0, float v1, int c, uint64_t nm2,
+                        float &p0, float &p1) {
+          const uint64_t sk2 = LO || !decltype(whole)::value ? mul2(pk2(s0, s1), rsc2) : pk2(s0, s1);
           float d0, d1;
-          upk2(d2, d0, d1);
+          upk2(fma2(sk2, pk2(k0, k1), nm2), d0, d1);
           float e0 = exp2_approx(d0), e1 = exp2_approx(d1);
-          if (!full) e0 = kf + c <= pos ? e0 : 0.f, e1 = kf + c + 1 <= pos ? e1 : 0.f;
+          if constexpr (!decltype(whole)::value) e0 = kf + c <= pos ? e0 : 0.f, e1 = kf + c + 1 <= pos ? e1 : 0.f;
           const uint64_t e2 = pk2(e0, e1);
           l2 = add2(l2, e2);
           upk2(mul2(e2, pk2(v0, v1)), p0, p1);
-          if (!full) p0 = kf + c <= pos ? p0 : 0.f, p1 = kf + c + 1 <= pos ? p1 : 0.f;  // a masked norm may be anything
+          // a masked value norm may be anything
+          if constexpr (!decltype(whole)::value) p0 = kf + c <= pos ? p0 : 0.f, p1 = kf + c + 1 <= pos ? p1 : 0.f;
         };
         if constexpr (LO) {
           raise_max();
           const float Mu = (M == -INFINITY) ? 0.f : M;
           const uint64_t nm2 = pk2(-Mu, -Mu);
           l2 = pk2(0.f, 0.f);
+          auto two_parts = [&](auto whole) {
 #pragma unroll 1
-          for (int cc = 0; cc < 4; ++cc) {
-            float sv[32];
-            tmem_ld32(tS + 32 * cc, sv);
-            uint32_t pw[32];  // the chunk's hi words, then its lo words, over its own columns
+            for (int cc = 0; cc < 4; ++cc) {
+              float sv[32];
+              tmem_ld32(tS + 32 * cc, sv);
+              uint32_t pw[32];  // the chunk's hi words, then its lo words, over its own columns
 #pragma unroll
-            for (int c4 = 0; c4 < 8; ++c4) {
-              const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
-              float p0, p1;
-              pair(sv[4 * c4], sv[4 * c4 + 1], kn.x, kn.y, nv.x, nv.y, 32 * cc + 4 * c4, nm2, p0, p1);
-              split_half2(p0, p1, pw[2 * c4], pw[16 + 2 * c4]);
-              pair(sv[4 * c4 + 2], sv[4 * c4 + 3], kn.z, kn.w, nv.z, nv.w, 32 * cc + 4 * c4 + 2, nm2, p0, p1);
-              split_half2(p0, p1, pw[2 * c4 + 1], pw[16 + 2 * c4 + 1]);
+              for (int c4 = 0; c4 < 8; ++c4) {
+                const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
+                float p0, p1;
+                pair(whole, sv[4 * c4], sv[4 * c4 + 1], kn.x, kn.y, nv.x, nv.y, 32 * cc + 4 * c4, nm2, p0, p1);
+                split_half2(p0, p1, pw[2 * c4], pw[16 + 2 * c4]);
+                pair(whole, sv[4 * c4 + 2], sv[4 * c4 + 3], kn.z, kn.w, nv.z, nv.w, 32 * cc + 4 * c4 + 2, nm2, p0, p1);
+                split_half2(p0, p1, pw[2 * c4 + 1], pw[16 + 2 * c4 + 1]);
+              }
+              tmem_st32(tS + 32 * cc, pw);
             }
-            tmem_st32(tS + 32 * cc, pw);
-          }
+          };
+          if (full) two_parts(std::true_type());
+          else two_parts(std::false_type());
         } else {
           uint32_t pw[64];
           bool need = live && M == -INFINITY && kf <= pos;
@@ -807,23 +821,27 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
             const uint64_t nm2 = pk2(-Mu, -Mu);
             l2 = pk2(0.f, 0.f);
             __half2 pm = __float2half2_rn(0.f);
+            auto one_part = [&](auto whole) {
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-              float sv[32];
-              tmem_ld32(tS + 32 * cc, sv);
+              for (int cc = 0; cc < 4; ++cc) {
+                float sv[32];
+                tmem_ld32(tS + 32 * cc, sv);
 #pragma unroll
-              for (int c4 = 0; c4 < 8; ++c4) {
-                const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
-                float p0, p1;
-                pair(sv[4 * c4], sv[4 * c4 + 1], kn.x, kn.y, nv.x, nv.y, 32 * cc + 4 * c4, nm2, p0, p1);
-                const __half2 h0 = __floats2half2_rn(p0, p1);
-                pair(sv[4 * c4 + 2], sv[4 * c4 + 3], kn.z, kn.w, nv.z, nv.w, 32 * cc + 4 * c4 + 2, nm2, p0, p1);
-                const __half2 h1 = __floats2half2_rn(p0, p1);
-                pm = __hmax2(pm, __hmax2(h0, h1));
-                pw[16 * cc + 2 * c4] = *reinterpret_cast<const uint32_t *>(&h0);
-                pw[16 * cc + 2 * c4 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+                for (int c4 = 0; c4 < 8; ++c4) {
+                  const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
+                  float p0, p1;
+                  pair(whole, sv[4 * c4], sv[4 * c4 + 1], kn.x, kn.y, nv.x, nv.y, 32 * cc + 4 * c4, nm2, p0, p1);
+                  const __half2 h0 = __floats2half2_rn(p0, p1);
+                  pair(whole, sv[4 * c4 + 2], sv[4 * c4 + 3], kn.z, kn.w, nv.z, nv.w, 32 * cc + 4 * c4 + 2, nm2, p0, p1);
+                  const __half2 h1 = __floats2half2_rn(p0, p1);
+                  pm = __hmax2(pm, __hmax2(h0, h1));
+                  pw[16 * cc + 2 * c4] = *reinterpret_cast<const uint32_t *>(&h0);
+                  pw[16 * cc + 2 * c4 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+                }
               }
-            }
+            };
+            if (full && !scaled) one_part(std::true_type());
+            else one_part(std::false_type());
             need = live && (__low2float(pm) > 32768.f || __high2float(pm) > 32768.f);
             if (turn || !__any_sync(FULL_MASK, need)) break;
           }

@@ -54,6 +54,7 @@ constexpr int RAW = KT * PG_ROW;       // a packed tile
 constexpr int NRAW = 3;
 constexpr int W_DEC = 8, W_MMA = 12, W_LOAD = 14, N_WARPS = 15;
 constexpr int THREADS = N_WARPS * 32;
+constexpr uint32_t IDESC_S = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);  // fp16, M = 128, N = 64
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // S / P of the groups, O of the groups
 
 constexpr uint32_t OFF_Q = 0, OFF_K = 2 * SW_TILE_BYTES, OFF_V = 4 * SW_TILE_BYTES;
@@ -61,7 +62,7 @@ constexpr uint32_t OFF_RAW = 6 * SW_TILE_BYTES, OFF_MISC = OFF_RAW + NRAW * RAW;
 struct Misc {
   uint64_t raw_full[NRAW], raw_empty[NRAW];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_ready[2], s_done[2], p_ready[2], pv_done[2], drain[2];
+  uint64_t q_ready[2], s_done[2][2], p_ready[2][2], pv_done[2], drain[2];  // [group][half]
   // Key norms of the last four K tiles (0 past the end): a K stage is free once its product
   // is done, while the softmax still needs the norms; the decoders reach tile j + 4 only after
   // every group has finished tile j.  2^7 value norms of the two V stages.
@@ -457,7 +458,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms.k_full[i], 128), mbar_init(&ms.v_full[i], 128);
       mbar_init(&ms.k_empty[i], ALT ? 1 : 2), mbar_init(&ms.v_empty[i], ALT ? 1 : 2);
-      mbar_init(&ms.s_done[i], 1), mbar_init(&ms.p_ready[i], 128), mbar_init(&ms.pv_done[i], 1);
+      for (int h = 0; h < 2; ++h) mbar_init(&ms.s_done[i][h], 1), mbar_init(&ms.p_ready[i][h], 128);
+      mbar_init(&ms.pv_done[i], 1);
       mbar_init(&ms.drain[i], 1), mbar_init(&ms.q_ready[i], 128);
     }
     ms.abort_flag = 0;
@@ -579,70 +581,66 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       const int gr = warp - W_MMA;
       const uint32_t sq = smem_addr(smem + OFF_Q), sk = smem_addr(smem + OFF_K), sv = smem_addr(smem + OFF_V);
       const uint32_t tS = tmem + TM_S + 128 * gr, tO = tmem + TM_O + 128 * gr;
-      uint32_t kc = 0, vc = 0, nq = 0, np = 0, npv = 0;  // K, V stages passed; items; P tiles; PV products
-      uint32_t np1 = 0;  // ALT, group 0: P tiles of group 1
+      uint32_t kc = 0, vc = 0, nq = 0, nt = 0, npv = 0;  // K, V stages passed; items; tiles; PV products
+      uint32_t nf = 0, nt1 = 0;  // final P tiles (on half 0's barrier); ALT, group 0: group 1's tiles
       bool issued = false;
       while (ok && next_item(p, w, it)) {
         const int n = it.t1 - it.t0;
         const int q0 = it.qt * p.qpu + (ALT ? 0 : gr * p.qpt);
         const bool act = q0 < it.s.T;  // (not ALT) the second row tile may be empty
-        if (act) {
+        const int step = ALT ? 2 : 1, i0 = ALT ? gr : 0, tiles = n > i0 ? (n - i0 + step - 1) / step : 0;
+        if (!act) {  // pass the stages on
+          for (int i = 0; ok && i < n; ++i) {
+            ok = wait(&ms.k_full[(kc + i) & 1], ((kc + i) >> 1) & 1);
+            if (ok) mbar_arrive(&ms.k_empty[(kc + i) & 1]), ok = wait(&ms.v_full[(vc + i) & 1], ((vc + i) >> 1) & 1);
+            if (ok) mbar_arrive(&ms.v_empty[(vc + i) & 1]);
+          }
+        } else {
           ok = wait(&ms.q_ready[gr], nq & 1);
           if (ALT && ok) ok = wait(&ms.q_ready[gr ^ 1], nq & 1);
           ++nq;
           if (!ok) break;
           tc_fence_after();
-        }
-        // S of the group's tile at local index i (K stage kc + i)
-        auto issue_s = [&](int i) -> bool {
-          const uint32_t c = kc + i;
-          if (!wait(&ms.k_full[c & 1], (c >> 1) & 1)) return false;
-          if (act) {
+          // S of half m & 1 (64 keys) of the group's tile m / 2
+          auto issue_s = [&](int m) -> bool {
+            const uint32_t c = kc + i0 + step * (m >> 1), h = m & 1;
+            if (!h && !wait(&ms.k_full[c & 1], (c >> 1) & 1)) return false;
             tc_fence_after();
-            const uint32_t kb = sk + (c & 1) * SW_TILE_BYTES;
+            const uint32_t kb = sk + (c & 1) * SW_TILE_BYTES + h * 64 * 128;
 #pragma unroll
             for (int part = 0; part < (LO ? 2 : 1); ++part)
 #pragma unroll
               for (int s = 0; s < 8; ++s)
-                umma<IDESC_F16>(tS, sw128_desc(sq + (LO ? part : (ALT ? 0 : gr)) * SW_TILE_BYTES + sw128_kstep(s)),
-                                sw128_desc(kb + sw128_kstep(s)), (part || s) ? 1u : 0u);
+                umma<IDESC_S>(tS + 64 * h, sw128_desc(sq + (LO ? part : (ALT ? 0 : gr)) * SW_TILE_BYTES + sw128_kstep(s)),
+                              sw128_desc(kb + sw128_kstep(s)), (part || s) ? 1u : 0u);
             issued = true;
-            umma_commit(&ms.s_done[gr]);
-            umma_commit(&ms.k_empty[c & 1]);
-          } else {
-            mbar_arrive(&ms.k_empty[c & 1]);
-          }
-          return true;
-        };
-        const int step = ALT ? 2 : 1;
-        int i = ALT ? gr : 0;
-        if (i < n) ok = issue_s(i);
-        for (bool first = true; ok && i < n; i += step, first = false) {
-          const uint32_t c = vc + i;
-          if (act) ok = wait(&ms.p_ready[gr], np & 1), ++np;
-          if (ok) ok = wait(&ms.v_full[c & 1], (c >> 1) & 1);
-          if (!ok) break;
-          if (act) {
+            umma_commit(&ms.s_done[gr][h]);
+            if (h) umma_commit(&ms.k_empty[c & 1]);
+            return true;
+          };
+          for (int m = 0; ok && m < 2 && m < 2 * tiles; ++m) ok = issue_s(m);
+          for (int m = 0; ok && m < 2 * tiles; ++m) {
+            const uint32_t c = vc + i0 + step * (m >> 1), h = m & 1;
+            ok = wait(&ms.p_ready[gr][h], (h ? nt + (m >> 1) : nt + nf + (m >> 1)) & 1);
+            if (ok && !h) ok = wait(&ms.v_full[c & 1], (c >> 1) & 1);
+            if (!ok) break;
             tc_fence_after();
-            const uint32_t vb = sv + (c & 1) * SW_TILE_BYTES;
+            const uint32_t vb = sv + (c & 1) * SW_TILE_BYTES + 2048 * 4 * h;
 #pragma unroll
             for (int part = 0; part < (LO ? 2 : 1); ++part)
 #pragma unroll
-              for (int s = 0; s < 8; ++s)
-                umma_ts<IDESC_F16_BMN>(tO, tS + (LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s), sw128_mn_desc(vb + 2048 * s),
-                                  (!first || part || s) ? 1u : 0u);
+              for (int s = 0; s < 4; ++s)
+                umma_ts<IDESC_F16_BMN>(tO, tS + 64 * h + (LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s),
+                                       sw128_mn_desc(vb + 2048 * s), (m || part || s) ? 1u : 0u);
             umma_commit(&ms.pv_done[gr]);
-            umma_commit(&ms.v_empty[c & 1]);
-          } else {
-            mbar_arrive(&ms.v_empty[c & 1]);
+            if (h) umma_commit(&ms.v_empty[c & 1]);
+            // the half's next S takes over P's columns: PV must have finished (products on
+            // different accumulators may run out of issue order); the softmax is on the other half
+            ok = wait(&ms.pv_done[gr], npv & 1);
+            ++npv;
+            if (ok && m + 2 < 2 * tiles) ok = issue_s(m + 2);
           }
-          if (i + step < n) {
-            // S takes over P's columns: PV must have finished (products on different
-            // accumulators may run out of issue order)
-            if (act) ok = wait(&ms.pv_done[gr], npv & 1);
-            if (ok) ok = issue_s(i + step);
-          }
-          if (act) ++npv;
+          nt += tiles;
         }
         kc += n, vc += n;
         // un-rotation: O = (O / l) R with O / l where P was
@@ -650,9 +648,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           for (int r = 0; ok && r < R_TILES; ++r) {
             const uint32_t c = vc + r;
             if (act && r == 0) {
-              ok = wait(&ms.p_ready[gr], np & 1), ++np;
+              ok = wait(&ms.p_ready[gr][0], (nt + nf) & 1);
               // group 1's last one too (its earlier ones are complete: both groups met before)
-              if (ALT && ok) np1 += n / 2, ok = wait(&ms.p_ready[1], np1 & 1), ++np1;
+              if (ALT && ok) nt1 += n / 2, ok = wait(&ms.p_ready[1][0], (nt1 + nf) & 1);
             }
             if (ok) ok = wait(&ms.v_full[c & 1], (c >> 1) & 1);
             if (!ok) break;
@@ -677,7 +675,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
             ++npv;
           }
         }
-        if (ALT && gr == 1) ++np;  // its last P is waited for by group 0's issuer
+        if (act) ++nf;  // (ALT: group 1's last P is waited for by group 0's issuer)
         vc += R_TILES;
       }
       if (issued && *reinterpret_cast<volatile int *>(&ms.abort_flag)) {
@@ -721,26 +719,29 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       mbar_arrive(&ms.q_ready[gr]);
 
       float M = -INFINITY, l = 0.f;
-      int done = 0;
-      for (int i = ALT ? gr : 0; i < n; i += ALT ? 2 : 1) {
-        const int kf = (it.t0 + i) * KT;
-        const uint32_t cv = vc + i;
-        ok = wait(&ms.s_done[gr], ns & 1);
-        ++ns;
-        if (ok) ok = wait(&ms.v_full[cv & 1], (cv >> 1) & 1);
+      int done = 0;  // halves
+      // halves of 64 keys: S of half m + 1 is done while this one is in its softmax
+      const int tiles = ALT ? (n > gr ? (n - gr + 1) / 2 : 0) : n;
+      for (int m = 0; m < 2 * tiles; ++m, ++done) {
+        const int i = ALT ? gr + 2 * (m >> 1) : (m >> 1), h = m & 1;
+        const int kf = (it.t0 + i) * KT + 64 * h;
+        const uint32_t cv = vc + i, tH = tS + 64 * h;
+        ok = wait(&ms.s_done[gr][h], ns & 1);
+        ns += h;
+        if (ok && !h) ok = wait(&ms.v_full[cv & 1], (cv >> 1) & 1);
         ok = __all_sync(FULL_MASK, ok);
         if (!ok) break;
         tc_fence_after();
-        const float4 *kn4 = reinterpret_cast<const float4 *>(ms.kn[(kc + i) & 3]);
-        const float4 *nv4 = reinterpret_cast<const float4 *>(ms.nv[cv & 1]);
-        const bool full = kf + KT - 1 <= it.s.base + q0;  // every row sees every key of the tile
+        const float4 *kn4 = reinterpret_cast<const float4 *>(ms.kn[(kc + i) & 3]) + 16 * h;
+        const float4 *nv4 = reinterpret_cast<const float4 *>(ms.nv[cv & 1]) + 16 * h;
+        const bool full = kf + 63 <= it.s.base + q0;  // every row sees every key of the half
         // the largest s + log2(value norm) of the row
         auto row_max = [&]() -> float {
           float bm = -INFINITY;
 #pragma unroll 1
-          for (int cc = 0; cc < 4; ++cc) {
+          for (int cc = 0; cc < 2; ++cc) {
             float sv[32];
-            tmem_ld32(tS + 32 * cc, sv);
+            tmem_ld32(tH + 32 * cc, sv);
 #pragma unroll
             for (int c4 = 0; c4 < 8; ++c4) {
               const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
@@ -761,6 +762,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           const float alpha = raise ? exp2_approx(M - bm) : 1.f;
           if (raise) M = bm, l *= alpha;
           if (done && __any_sync(FULL_MASK, raise)) {
+            // O is whole once the previous half's PV has finished
+            ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr], (npv + done - 1) & 1));
+            if (!ok) return;
+            tc_fence_after();
 #pragma unroll 1
             for (int cc = 0; cc < 4; ++cc) {
               float o[32];
@@ -794,9 +799,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           l2 = pk2(0.f, 0.f);
           auto two_parts = [&](auto whole) {
 #pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc) {
+            for (int cc = 0; cc < 2; ++cc) {
               float sv[32];
-              tmem_ld32(tS + 32 * cc, sv);
+              tmem_ld32(tH + 32 * cc, sv);
               uint32_t pw[32];  // the chunk's hi words, then its lo words, over its own columns
 #pragma unroll
               for (int c4 = 0; c4 < 8; ++c4) {
@@ -807,13 +812,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
                 pair(whole, sv[4 * c4 + 2], sv[4 * c4 + 3], kn.z, kn.w, nv.z, nv.w, 32 * cc + 4 * c4 + 2, nm2, p0, p1);
                 split_half2(p0, p1, pw[2 * c4 + 1], pw[16 + 2 * c4 + 1]);
               }
-              tmem_st32(tS + 32 * cc, pw);
+              tmem_st32(tH + 32 * cc, pw);
             }
           };
           if (full) two_parts(std::true_type());
           else two_parts(std::false_type());
         } else {
-          uint32_t pw[64];
+          uint32_t pw[32];
           bool need = live && M == -INFINITY && kf <= pos;
           for (int turn = 0;; ++turn) {
             if (__any_sync(FULL_MASK, need)) raise_max();
@@ -823,9 +828,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
             __half2 pm = __float2half2_rn(0.f);
             auto one_part = [&](auto whole) {
 #pragma unroll
-              for (int cc = 0; cc < 4; ++cc) {
+              for (int cc = 0; cc < 2; ++cc) {
                 float sv[32];
-                tmem_ld32(tS + 32 * cc, sv);
+                tmem_ld32(tH + 32 * cc, sv);
 #pragma unroll
                 for (int c4 = 0; c4 < 8; ++c4) {
                   const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
@@ -845,27 +850,23 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
             need = live && (__low2float(pm) > 32768.f || __high2float(pm) > 32768.f);
             if (turn || !__any_sync(FULL_MASK, need)) break;
           }
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t half[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) half[e] = pw[32 * hf + e];
-            tmem_st32(tS + 32 * hf, half);
-          }
+          tmem_st32(tH, pw);
         }
         float l0, l1;
         upk2(l2, l0, l1);
         l += l0 + l1;
         tc_fence_before();
-        mbar_arrive(&ms.p_ready[gr]);
-        ++done;
+        if (!ok) break;  // (a failed wait while raising the maximum)
+        mbar_arrive(&ms.p_ready[gr][h]);
       }
       kc += n, vc += n + R_TILES;
 
       // ---- end of the item: O / l as fp16 with a power-of-two row scale, times R
       npv += done;
-      if (ok && done) {
-        ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr], (npv - 1) & 1));
+      if (ok && done) {  // the last two PVs, in order
+        ok = wait(&ms.pv_done[gr], (npv - 2) & 1);
+        if (ok) ok = wait(&ms.pv_done[gr], (npv - 1) & 1);
+        ok = __all_sync(FULL_MASK, ok);
         tc_fence_after();
       }
       float amax = 0.f;
@@ -924,7 +925,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
         tmem_st32(tS + 32 * c2, pw);
       }
       tc_fence_before();
-      mbar_arrive(&ms.p_ready[gr]);
+      mbar_arrive(&ms.p_ready[gr][0]);
       if (ALT && gr == 1) continue;
       ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr], npv & 1));
       ++npv;

@@ -54,7 +54,6 @@ constexpr int RAW = KT * PG_ROW;       // a packed tile
 constexpr int NRAW = 3;
 constexpr int W_DEC = 8, W_MMA = 12, W_LOAD = 14, N_WARPS = 15;
 constexpr int THREADS = N_WARPS * 32;
-constexpr uint32_t IDESC_S = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);  // fp16, M = 128, N = 64
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // S / P of the groups, O of the groups
 
 constexpr uint32_t OFF_Q = 0, OFF_K = 2 * SW_TILE_BYTES, OFF_V = 4 * SW_TILE_BYTES;
@@ -62,7 +61,10 @@ constexpr uint32_t OFF_RAW = 6 * SW_TILE_BYTES, OFF_MISC = OFF_RAW + NRAW * RAW;
 struct Misc {
   uint64_t raw_full[NRAW], raw_empty[NRAW];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_ready[2], s_done[2][2], p_ready[2][2], pv_done[2], drain[2];  // [group][half]
+  uint64_t q_ready[2], s_done[2], drain[2];   // [group]
+  // [group][half of the key tile]: a thread that waits for a phase of one of these is at most one
+  // phase behind, so that the parity tells; the items' final P and un-rotation use half 0 and 1
+  uint64_t p_ready[2][2], pv_done[2][2];
   // Key norms of the last four K tiles (0 past the end): a K stage is free once its product
   // is done, while the softmax still needs the norms; the decoders reach tile j + 4 only after
   // every group has finished tile j.  2^7 value norms of the two V stages.
@@ -458,8 +460,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms.k_full[i], 128), mbar_init(&ms.v_full[i], 128);
       mbar_init(&ms.k_empty[i], ALT ? 1 : 2), mbar_init(&ms.v_empty[i], ALT ? 1 : 2);
-      for (int h = 0; h < 2; ++h) mbar_init(&ms.s_done[i][h], 1), mbar_init(&ms.p_ready[i][h], 128);
-      mbar_init(&ms.pv_done[i], 1);
+      mbar_init(&ms.s_done[i], 1), mbar_init(&ms.p_ready[i][0], 128), mbar_init(&ms.p_ready[i][1], 128);
+      mbar_init(&ms.pv_done[i][0], 1), mbar_init(&ms.pv_done[i][1], 1);
       mbar_init(&ms.drain[i], 1), mbar_init(&ms.q_ready[i], 128);
     }
     ms.abort_flag = 0;
@@ -581,8 +583,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       const int gr = warp - W_MMA;
       const uint32_t sq = smem_addr(smem + OFF_Q), sk = smem_addr(smem + OFF_K), sv = smem_addr(smem + OFF_V);
       const uint32_t tS = tmem + TM_S + 128 * gr, tO = tmem + TM_O + 128 * gr;
-      uint32_t kc = 0, vc = 0, nq = 0, nt = 0, npv = 0;  // K, V stages passed; items; tiles; PV products
-      uint32_t nf = 0, nt1 = 0;  // final P tiles (on half 0's barrier); ALT, group 0: group 1's tiles
+      uint32_t kc = 0, vc = 0, nq = 0, nt = 0;  // K, V stages passed; items begun; tiles
+      uint32_t nf = 0, nt1 = 0;  // items finished; ALT, group 0: group 1's tiles
       bool issued = false;
       while (ok && next_item(p, w, it)) {
         const int n = it.t1 - it.t0;
@@ -601,25 +603,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           ++nq;
           if (!ok) break;
           tc_fence_after();
-          // S of half m & 1 (64 keys) of the group's tile m / 2
-          auto issue_s = [&](int m) -> bool {
-            const uint32_t c = kc + i0 + step * (m >> 1), h = m & 1;
-            if (!h && !wait(&ms.k_full[c & 1], (c >> 1) & 1)) return false;
+          auto issue_s = [&](int m) -> bool {  // S of the group's tile m
+            const uint32_t c = kc + i0 + step * m;
+            if (!wait(&ms.k_full[c & 1], (c >> 1) & 1)) return false;
             tc_fence_after();
-            const uint32_t kb = sk + (c & 1) * SW_TILE_BYTES + h * 64 * 128;
+            const uint32_t kb = sk + (c & 1) * SW_TILE_BYTES;
 #pragma unroll
             for (int part = 0; part < (LO ? 2 : 1); ++part)
 #pragma unroll
               for (int s = 0; s < 8; ++s)
-                umma<IDESC_S>(tS + 64 * h, sw128_desc(sq + (LO ? part : (ALT ? 0 : gr)) * SW_TILE_BYTES + sw128_kstep(s)),
-                              sw128_desc(kb + sw128_kstep(s)), (part || s) ? 1u : 0u);
+                umma<IDESC_F16>(tS, sw128_desc(sq + (LO ? part : (ALT ? 0 : gr)) * SW_TILE_BYTES + sw128_kstep(s)),
+                                sw128_desc(kb + sw128_kstep(s)), (part || s) ? 1u : 0u);
             issued = true;
-            umma_commit(&ms.s_done[gr][h]);
-            if (h) umma_commit(&ms.k_empty[c & 1]);
+            umma_commit(&ms.s_done[gr]);
+            umma_commit(&ms.k_empty[c & 1]);
             return true;
           };
-          for (int m = 0; ok && m < 2 && m < 2 * tiles; ++m) ok = issue_s(m);
-          for (int m = 0; ok && m < 2 * tiles; ++m) {
+          if (tiles) ok = issue_s(0);
+          for (int m = 0; ok && m < 2 * tiles; ++m) {  // halves of 64 keys
             const uint32_t c = vc + i0 + step * (m >> 1), h = m & 1;
             ok = wait(&ms.p_ready[gr][h], (h ? nt + (m >> 1) : nt + nf + (m >> 1)) & 1);
             if (ok && !h) ok = wait(&ms.v_full[c & 1], (c >> 1) & 1);
@@ -632,13 +633,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
               for (int s = 0; s < 4; ++s)
                 umma_ts<IDESC_F16_BMN>(tO, tS + 64 * h + (LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s),
                                        sw128_mn_desc(vb + 2048 * s), (m || part || s) ? 1u : 0u);
-            umma_commit(&ms.pv_done[gr]);
+            umma_commit(&ms.pv_done[gr][h]);
             if (h) umma_commit(&ms.v_empty[c & 1]);
-            // the half's next S takes over P's columns: PV must have finished (products on
-            // different accumulators may run out of issue order); the softmax is on the other half
-            ok = wait(&ms.pv_done[gr], npv & 1);
-            ++npv;
-            if (ok && m + 2 < 2 * tiles) ok = issue_s(m + 2);
+            // (ALT: group 1 has no un-rotation of its own)
+            ok = wait(&ms.pv_done[gr][h], (nt + (h && !(ALT && gr) ? nf : 0) + (m >> 1)) & 1);
+            // the next S takes over P's columns: PV must have finished (products on different
+            // accumulators may run out of issue order)
+            if (ok && h && m + 1 < 2 * tiles) ok = issue_s((m + 1) >> 1);
           }
           nt += tiles;
         }
@@ -670,10 +671,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
               mbar_arrive(&ms.v_empty[c & 1]);
             }
           }
-          if (ok && act) {
-            umma_commit(&ms.pv_done[gr]);
-            ++npv;
-          }
+          if (ok && act) umma_commit(&ms.pv_done[gr][1]);
         }
         if (act) ++nf;  // (ALT: group 1's last P is waited for by group 0's issuer)
         vc += R_TILES;
@@ -689,7 +687,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + TM_S + 128 * gr, tO = tmem + lane_off + TM_O + 128 * gr;
     const int rq = r / p.gq, rh = r - rq * p.gq;
-    uint32_t kc = 0, vc = 0, ns = 0, npv = 0;  // K, V stages passed; S tiles; completions of pv_done
+    uint32_t kc = 0, vc = 0, ns = 0, nf = 0;  // K, V stages passed; S tiles; items finished
     while (ok && next_item(p, w, it)) {
       const int n = it.t1 - it.t0;
       const int q0 = it.qt * p.qpu + (ALT ? 0 : gr * p.qpt);
@@ -720,18 +718,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
 
       float M = -INFINITY, l = 0.f;
       int done = 0;  // halves
-      // halves of 64 keys: S of half m + 1 is done while this one is in its softmax
+      // halves of 64 keys: the first half's PV runs under the second one's softmax
       const int tiles = ALT ? (n > gr ? (n - gr + 1) / 2 : 0) : n;
       for (int m = 0; m < 2 * tiles; ++m, ++done) {
         const int i = ALT ? gr + 2 * (m >> 1) : (m >> 1), h = m & 1;
         const int kf = (it.t0 + i) * KT + 64 * h;
         const uint32_t cv = vc + i, tH = tS + 64 * h;
-        ok = wait(&ms.s_done[gr][h], ns & 1);
-        ns += h;
-        if (ok && !h) ok = wait(&ms.v_full[cv & 1], (cv >> 1) & 1);
-        ok = __all_sync(FULL_MASK, ok);
-        if (!ok) break;
-        tc_fence_after();
+        if (!h) {
+          ok = wait(&ms.s_done[gr], ns & 1);
+          ++ns;
+          if (ok) ok = wait(&ms.v_full[cv & 1], (cv >> 1) & 1);
+          ok = __all_sync(FULL_MASK, ok);
+          if (!ok) break;
+          tc_fence_after();
+        }
         const float4 *kn4 = reinterpret_cast<const float4 *>(ms.kn[(kc + i) & 3]) + 16 * h;
         const float4 *nv4 = reinterpret_cast<const float4 *>(ms.nv[cv & 1]) + 16 * h;
         const bool full = kf + 63 <= it.s.base + q0;  // every row sees every key of the half
@@ -762,10 +762,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           const float alpha = raise ? exp2_approx(M - bm) : 1.f;
           if (raise) M = bm, l *= alpha;
           if (done && __any_sync(FULL_MASK, raise)) {
-            // O is whole once the previous half's PV has finished
-            ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr], (npv + done - 1) & 1));
-            if (!ok) return;
-            tc_fence_after();
+            // O is whole once the first half's PV has finished (earlier tiles' have: S was issued
+            // after them); ns counts this tile already
+            if (h) {
+              ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr][0], (ns - 1) & 1));
+              if (!ok) return;
+              tc_fence_after();
+            }
 #pragma unroll 1
             for (int cc = 0; cc < 4; ++cc) {
               float o[32];
@@ -827,22 +830,19 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
             l2 = pk2(0.f, 0.f);
             __half2 pm = __float2half2_rn(0.f);
             auto one_part = [&](auto whole) {
+              float sv[64];
+              tmem_ld64(tH, sv);
 #pragma unroll
-              for (int cc = 0; cc < 2; ++cc) {
-                float sv[32];
-                tmem_ld32(tH + 32 * cc, sv);
-#pragma unroll
-                for (int c4 = 0; c4 < 8; ++c4) {
-                  const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
-                  float p0, p1;
-                  pair(whole, sv[4 * c4], sv[4 * c4 + 1], kn.x, kn.y, nv.x, nv.y, 32 * cc + 4 * c4, nm2, p0, p1);
-                  const __half2 h0 = __floats2half2_rn(p0, p1);
-                  pair(whole, sv[4 * c4 + 2], sv[4 * c4 + 3], kn.z, kn.w, nv.z, nv.w, 32 * cc + 4 * c4 + 2, nm2, p0, p1);
-                  const __half2 h1 = __floats2half2_rn(p0, p1);
-                  pm = __hmax2(pm, __hmax2(h0, h1));
-                  pw[16 * cc + 2 * c4] = *reinterpret_cast<const uint32_t *>(&h0);
-                  pw[16 * cc + 2 * c4 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
-                }
+              for (int c4 = 0; c4 < 16; ++c4) {
+                const float4 kn = kn4[c4], nv = nv4[c4];
+                float p0, p1;
+                pair(whole, sv[4 * c4], sv[4 * c4 + 1], kn.x, kn.y, nv.x, nv.y, 4 * c4, nm2, p0, p1);
+                const __half2 h0 = __floats2half2_rn(p0, p1);
+                pair(whole, sv[4 * c4 + 2], sv[4 * c4 + 3], kn.z, kn.w, nv.z, nv.w, 4 * c4 + 2, nm2, p0, p1);
+                const __half2 h1 = __floats2half2_rn(p0, p1);
+                pm = __hmax2(pm, __hmax2(h0, h1));
+                pw[2 * c4] = *reinterpret_cast<const uint32_t *>(&h0);
+                pw[2 * c4 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
               }
             };
             if (full && !scaled) one_part(std::true_type());
@@ -862,11 +862,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       kc += n, vc += n + R_TILES;
 
       // ---- end of the item: O / l as fp16 with a power-of-two row scale, times R
-      npv += done;
-      if (ok && done) {  // the last two PVs, in order
-        ok = wait(&ms.pv_done[gr], (npv - 2) & 1);
-        if (ok) ok = wait(&ms.pv_done[gr], (npv - 1) & 1);
-        ok = __all_sync(FULL_MASK, ok);
+      if (ok && done) {
+        // ALT: group 1's un-rotation is group 0's, so its own barrier counts its tiles alone
+        ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr][1], (ns - 1 + (ALT && gr ? 0 : nf)) & 1));
         tc_fence_after();
       }
       float amax = 0.f;
@@ -927,8 +925,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       tc_fence_before();
       mbar_arrive(&ms.p_ready[gr][0]);
       if (ALT && gr == 1) continue;
-      ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr], npv & 1));
-      ++npv;
+      ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr][1], (ns + nf) & 1));
+      ++nf;
       if (!ok) break;
       tc_fence_after();
 

@@ -144,19 +144,21 @@ __global__ void __launch_bounds__(GatherCfg<PARTS>::GROUPS * 128) k_paged_gather
     fence_async_smem();
     tc_fence_before();
     group_sync();
-    if (r == 0) {
+    if ((warp & 3) == 0) {
       tc_fence_after();
       if (!r_ok) ok = mbar_wait_bounded(r_full, 0, 2000000000ull), r_ok = true;
-      if (ok) {
-        const uint32_t sa = smem_addr(at), sr = smem_addr(smem);
+      ok = __all_sync(FULL_MASK, ok);
+      const uint64_t da = sw128_desc(smem_addr(at)), dr = sw128_mn_desc(smem_addr(smem));
+      if (ok && elect_lane()) {
 #pragma unroll
         for (int part = 0; part < PARTS; ++part)  // C R_hi, C R_lo, C_lo R_hi
 #pragma unroll
           for (int s = 0; s < 8; ++s)
-            umma<IDESC_F16_BMN>(tm, sw128_desc(sa + (part == 2 ? SW_TILE_BYTES : 0) + sw128_kstep(s)),
-                                sw128_mn_desc(sr + (part == 1 ? SW_TILE_BYTES : 0) + 2048 * s), (part || s) ? 1u : 0u);
+            umma<IDESC_F16_BMN>(tm, desc_step(da, (part == 2 ? SW_TILE_BYTES : 0) + sw128_kstep(s)),
+                                desc_step(dr, (part == 1 ? SW_TILE_BYTES : 0) + 2048 * s), (part || s) ? 1u : 0u);
         umma_commit(&done[grp]);
       }
+      __syncwarp();
     }
     bool up = mbar_wait_bounded(&done[grp], phase & 1, 4000000000ull);
     ++phase;

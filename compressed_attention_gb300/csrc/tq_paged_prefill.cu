@@ -52,8 +52,14 @@ constexpr int KT = 128;                // keys per tile
 constexpr int UNIT_TILES = 3;          // cost of an item ahead of its tiles, in tiles
 constexpr int RAW = KT * PG_ROW;       // a packed tile
 constexpr int NRAW = 3;
-constexpr int W_DEC = 8, W_MMA = 12, W_LOAD = 14, N_WARPS = 15;
+constexpr int W_DEC = 8, W_MMA = 12, W_LOAD = 14, N_WARPS = 16;  // the last warp only fills its group
 constexpr int THREADS = N_WARPS * 32;
+// Registers: 512 threads x 128 at launch; the softmax groups take 160 (64 scores, 32 packed
+// probabilities and the norms of several columns in flight), the other two groups give theirs up
+// to 96: 256 * 160 + 256 * 96 = 65,536.
+constexpr int REGS_SOFTMAX = 160, REGS_OTHER = 96;
+static_assert(2 * 128 * REGS_SOFTMAX + 2 * 128 * REGS_OTHER <= THREADS * 128, "the launch's registers");
+constexpr uint32_t IDESC_S = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);  // fp16, M = 128, N = 64
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // S / P of the groups, O of the groups
 
 constexpr uint32_t OFF_Q = 0, OFF_K = 2 * SW_TILE_BYTES, OFF_V = 4 * SW_TILE_BYTES;
@@ -61,10 +67,10 @@ constexpr uint32_t OFF_RAW = 6 * SW_TILE_BYTES, OFF_MISC = OFF_RAW + NRAW * RAW;
 struct Misc {
   uint64_t raw_full[NRAW], raw_empty[NRAW];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_ready[2], s_done[2], drain[2];   // [group]
+  uint64_t q_ready[2], drain[2];   // [group]
   // [group][half of the key tile]: a thread that waits for a phase of one of these is at most one
   // phase behind, so that the parity tells; the items' final P and un-rotation use half 0 and 1
-  uint64_t p_ready[2][2], pv_done[2][2];
+  uint64_t s_done[2][2], p_ready[2][2], pv_done[2][2];
   // Key norms of the last four K tiles (0 past the end): a K stage is free once its product
   // is done, while the softmax still needs the norms; the decoders reach tile j + 4 only after
   // every group has finished tile j.  2^7 value norms of the two V stages.
@@ -458,11 +464,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
   if (tid == 0) {
     for (int i = 0; i < NRAW; ++i) mbar_init(&ms.raw_full[i], 1), mbar_init(&ms.raw_empty[i], 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ms.k_full[i], 128), mbar_init(&ms.v_full[i], 128);
+      mbar_init(&ms.k_full[i], 4), mbar_init(&ms.v_full[i], 4);
       mbar_init(&ms.k_empty[i], ALT ? 1 : 2), mbar_init(&ms.v_empty[i], ALT ? 1 : 2);
-      mbar_init(&ms.s_done[i], 1), mbar_init(&ms.p_ready[i][0], 128), mbar_init(&ms.p_ready[i][1], 128);
-      mbar_init(&ms.pv_done[i][0], 1), mbar_init(&ms.pv_done[i][1], 1);
-      mbar_init(&ms.drain[i], 1), mbar_init(&ms.q_ready[i], 128);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&ms.s_done[i][h], 1), mbar_init(&ms.p_ready[i][h], 4);
+        mbar_init(&ms.pv_done[i][h], 1);
+      }
+      mbar_init(&ms.drain[i], 1), mbar_init(&ms.q_ready[i], 4);
     }
     ms.abort_flag = 0;
     fence_mbar_init();
@@ -487,6 +495,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
   walk_begin(p, w);
   bool ok = true;
 
+  if (warp >= W_DEC) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
   if (warp == W_LOAD) {
     // ================ loader: K and V tiles in turn on the ring
     const int psh = p.pv.page_shift, P = 1 << psh;
@@ -520,7 +530,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
     if (*reinterpret_cast<volatile int *>(&ms.abort_flag))
       for (uint32_t c = n > NRAW ? n - NRAW : 0; c < n; ++c)
         (void)mbar_wait_bounded(&ms.raw_full[c % NRAW], (c / NRAW) & 1, WAIT_LIMIT_NS);
-  } else if (warp >= W_DEC && warp < W_MMA) {
+  } else if (warp < W_MMA) {
     // ================ decoders: thread = row of the tile
     const int row = tid - W_DEC * 32;
     const uint32_t klo[2] = {p.klo[0], p.klo[1]}, khi[2] = {p.khi[0], p.khi[1]};
@@ -553,9 +563,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           if (side) ms.nv[st][row] = live ? norm * 128.0f : 0.f;
           else ms.kn[c & 3][row] = live ? norm : 0.f;
           fence_async_smem();
-          mbar_arrive(side ? &ms.v_full[st] : &ms.k_full[st]);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ms.raw_empty[rs]);
+          if (lane == 0) mbar_arrive(side ? &ms.v_full[st] : &ms.k_full[st]), mbar_arrive(&ms.raw_empty[rs]);
           ++c;
         }
       }
@@ -568,7 +577,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           mbar_arrive_expect_tx(&ms.v_full[st], SW_TILE_BYTES);
           bulk_g2s(smem + OFF_V + st * SW_TILE_BYTES, p.vr + r * SW_TILE_BYTES, SW_TILE_BYTES, &ms.v_full[st]);
           last_r = vc + 1;
-        } else {
+        } else if (lane == 0) {
           mbar_arrive(&ms.v_full[st]);
         }
       }
@@ -578,110 +587,127 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
     if (row == 0 && last_r && *reinterpret_cast<volatile int *>(&ms.abort_flag))
       (void)mbar_wait_bounded(&ms.v_full[(last_r - 1) & 1], ((last_r - 1) >> 1) & 1, WAIT_LIMIT_NS);
   } else if (warp == W_MMA || warp == W_MMA + 1) {
-    // ================ issuers: one thread per softmax group
-    if (lane == 0) {
-      const int gr = warp - W_MMA;
-      const uint32_t sq = smem_addr(smem + OFF_Q), sk = smem_addr(smem + OFF_K), sv = smem_addr(smem + OFF_V);
-      const uint32_t tS = tmem + TM_S + 128 * gr, tO = tmem + TM_O + 128 * gr;
-      uint32_t kc = 0, vc = 0, nq = 0, nt = 0;  // K, V stages passed; items begun; tiles
-      uint32_t nf = 0, nt1 = 0;  // items finished; ALT, group 0: group 1's tiles
-      bool issued = false;
-      while (ok && next_item(p, w, it)) {
-        const int n = it.t1 - it.t0;
-        const int q0 = it.qt * p.qpu + (ALT ? 0 : gr * p.qpt);
-        const bool act = q0 < it.s.T;  // (not ALT) the second row tile may be empty
-        const int step = ALT ? 2 : 1, i0 = ALT ? gr : 0, tiles = n > i0 ? (n - i0 + step - 1) / step : 0;
-        if (!act) {  // pass the stages on
-          for (int i = 0; ok && i < n; ++i) {
-            ok = wait(&ms.k_full[(kc + i) & 1], ((kc + i) >> 1) & 1);
-            if (ok) mbar_arrive(&ms.k_empty[(kc + i) & 1]), ok = wait(&ms.v_full[(vc + i) & 1], ((vc + i) >> 1) & 1);
-            if (ok) mbar_arrive(&ms.v_empty[(vc + i) & 1]);
-          }
-        } else {
-          ok = wait(&ms.q_ready[gr], nq & 1);
-          if (ALT && ok) ok = wait(&ms.q_ready[gr ^ 1], nq & 1);
-          ++nq;
-          if (!ok) break;
+    // ================ issuers: a warp per softmax group, its elected lane issues
+    const int gr = __shfl_sync(FULL_MASK, warp - W_MMA, 0);
+    const bool lead = elect_lane();
+    const uint32_t tS = __shfl_sync(FULL_MASK, tmem, 0) + TM_S + 128 * gr, tO = tS + TM_O - TM_S;
+    const uint64_t dq = sw128_desc(smem_addr(smem + OFF_Q) + (ALT ? 0 : gr) * SW_TILE_BYTES);
+    const uint64_t dk = sw128_desc(smem_addr(smem + OFF_K)), dv = sw128_mn_desc(smem_addr(smem + OFF_V));
+    uint32_t kc = 0, vc = 0, nq = 0, nt = 0;  // K, V stages passed; items begun; tiles
+    uint32_t nf = 0, nt1 = 0;  // items finished; ALT, group 0: group 1's tiles
+    bool issued = false;
+    // where P's K-step s (of a half, or of a whole row for the un-rotation) lies
+    auto p_col = [](int part, int s) { return LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s; };
+    while (ok && next_item(p, w, it)) {
+      const int n = it.t1 - it.t0;
+      const int q0 = it.qt * p.qpu + (ALT ? 0 : gr * p.qpt);
+      const bool act = q0 < it.s.T;  // (not ALT) the second row tile may be empty
+      const int step = ALT ? 2 : 1, i0 = ALT ? gr : 0, tiles = n > i0 ? (n - i0 + step - 1) / step : 0;
+      if (!act) {  // pass the stages on
+        for (int i = 0; ok && i < n; ++i) {
+          ok = wait(&ms.k_full[(kc + i) & 1], ((kc + i) >> 1) & 1);
+          if (ok && lead) mbar_arrive(&ms.k_empty[(kc + i) & 1]);
+          if (ok) ok = wait(&ms.v_full[(vc + i) & 1], ((vc + i) >> 1) & 1);
+          if (ok && lead) mbar_arrive(&ms.v_empty[(vc + i) & 1]);
+          ok = __all_sync(FULL_MASK, ok);
+        }
+      } else {
+        ok = wait(&ms.q_ready[gr], nq & 1);
+        if (ALT && ok) ok = wait(&ms.q_ready[gr ^ 1], nq & 1);
+        ++nq;
+        if (!(ok = __all_sync(FULL_MASK, ok))) break;
+        tc_fence_after();
+        // S of half m & 1 (64 keys) of the group's tile m / 2
+        auto issue_s = [&](int m) -> bool {
+          const uint32_t c = kc + i0 + step * (m >> 1), h = m & 1;
+          if (!h && !__all_sync(FULL_MASK, wait(&ms.k_full[c & 1], (c >> 1) & 1))) return false;
           tc_fence_after();
-          auto issue_s = [&](int m) -> bool {  // S of the group's tile m
-            const uint32_t c = kc + i0 + step * m;
-            if (!wait(&ms.k_full[c & 1], (c >> 1) & 1)) return false;
-            tc_fence_after();
-            const uint32_t kb = sk + (c & 1) * SW_TILE_BYTES;
+          const uint64_t kb = desc_step(dk, (c & 1) * SW_TILE_BYTES + h * 64 * 128);
+          if (lead) {
 #pragma unroll
             for (int part = 0; part < (LO ? 2 : 1); ++part)
 #pragma unroll
               for (int s = 0; s < 8; ++s)
-                umma<IDESC_F16>(tS, sw128_desc(sq + (LO ? part : (ALT ? 0 : gr)) * SW_TILE_BYTES + sw128_kstep(s)),
-                                sw128_desc(kb + sw128_kstep(s)), (part || s) ? 1u : 0u);
-            issued = true;
-            umma_commit(&ms.s_done[gr]);
-            umma_commit(&ms.k_empty[c & 1]);
-            return true;
-          };
-          if (tiles) ok = issue_s(0);
-          for (int m = 0; ok && m < 2 * tiles; ++m) {  // halves of 64 keys
-            const uint32_t c = vc + i0 + step * (m >> 1), h = m & 1;
-            ok = wait(&ms.p_ready[gr][h], (h ? nt + (m >> 1) : nt + nf + (m >> 1)) & 1);
-            if (ok && !h) ok = wait(&ms.v_full[c & 1], (c >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t vb = sv + (c & 1) * SW_TILE_BYTES + 2048 * 4 * h;
+                umma<IDESC_S>(tS + 64 * h, desc_step(dq, part * SW_TILE_BYTES + sw128_kstep(s)),
+                              desc_step(kb, sw128_kstep(s)), (part || s) ? 1u : 0u);
+            umma_commit(&ms.s_done[gr][h]);
+            if (h) umma_commit(&ms.k_empty[c & 1]);
+          }
+          __syncwarp();
+          issued = true;
+          return true;
+        };
+        for (int m = 0; ok && m < 2 && m < 2 * tiles; ++m) ok = issue_s(m);
+        for (int m = 0; ok && m < 2 * tiles; ++m) {
+          const uint32_t c = vc + i0 + step * (m >> 1), h = m & 1;
+          ok = wait(&ms.p_ready[gr][h], (h ? nt + (m >> 1) : nt + nf + (m >> 1)) & 1);
+          if (ok && !h) ok = wait(&ms.v_full[c & 1], (c >> 1) & 1);
+          if (!(ok = __all_sync(FULL_MASK, ok))) break;
+          tc_fence_after();
+          const uint64_t vb = desc_step(dv, (c & 1) * SW_TILE_BYTES + 2048 * 4 * h);
+          if (lead) {
 #pragma unroll
             for (int part = 0; part < (LO ? 2 : 1); ++part)
 #pragma unroll
               for (int s = 0; s < 4; ++s)
-                umma_ts<IDESC_F16_BMN>(tO, tS + 64 * h + (LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s),
-                                       sw128_mn_desc(vb + 2048 * s), (m || part || s) ? 1u : 0u);
+                umma_ts<IDESC_F16_BMN>(tO, tS + 64 * h + p_col(part, s), desc_step(vb, 2048 * s), (m || part || s) ? 1u : 0u);
             umma_commit(&ms.pv_done[gr][h]);
             if (h) umma_commit(&ms.v_empty[c & 1]);
-            // (ALT: group 1 has no un-rotation of its own)
-            ok = wait(&ms.pv_done[gr][h], (nt + (h && !(ALT && gr) ? nf : 0) + (m >> 1)) & 1);
-            // the next S takes over P's columns: PV must have finished (products on different
-            // accumulators may run out of issue order)
-            if (ok && h && m + 1 < 2 * tiles) ok = issue_s((m + 1) >> 1);
           }
-          nt += tiles;
+          __syncwarp();
+          // the half's next S takes over P's columns: PV must have finished (products on
+          // different accumulators may run out of issue order); the softmax is on the other half
+          // (ALT: group 1 has no un-rotation of its own)
+          ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr][h], (nt + (h && !(ALT && gr) ? nf : 0) + (m >> 1)) & 1));
+          if (ok && m + 2 < 2 * tiles) ok = issue_s(m + 2);
         }
-        kc += n, vc += n;
-        // un-rotation: O = (O / l) R with O / l where P was
-        if (ok && (!ALT || gr == 0)) {
-          for (int r = 0; ok && r < R_TILES; ++r) {
-            const uint32_t c = vc + r;
-            if (act && r == 0) {
-              ok = wait(&ms.p_ready[gr][0], (nt + nf) & 1);
-              // group 1's last one too (its earlier ones are complete: both groups met before)
-              if (ALT && ok) nt1 += n / 2, ok = wait(&ms.p_ready[1][0], (nt1 + nf) & 1);
-            }
-            if (ok) ok = wait(&ms.v_full[c & 1], (c >> 1) & 1);
-            if (!ok) break;
+        nt += tiles;
+      }
+      kc += n, vc += n;
+      // un-rotation: O = (O / l) R with O / l where P was
+      if (ok && (!ALT || gr == 0)) {
+        for (int r = 0; ok && r < R_TILES; ++r) {
+          const uint32_t c = vc + r;
+          if (act && r == 0) {
+            ok = wait(&ms.p_ready[gr][0], (nt + nf) & 1);
+            // group 1's last one too (its earlier ones are complete: both groups met before)
+            if (ALT && ok) nt1 += n / 2, ok = wait(&ms.p_ready[1][0], (nt1 + nf) & 1);
+          }
+          if (ok) ok = wait(&ms.v_full[c & 1], (c >> 1) & 1);
+          if (!(ok = __all_sync(FULL_MASK, ok))) break;
+          tc_fence_after();
+          if (lead) {
             if (act) {
-              tc_fence_after();
-              const uint32_t vb = sv + (c & 1) * SW_TILE_BYTES;
+              const uint64_t vb = desc_step(dv, (c & 1) * SW_TILE_BYTES);
 #pragma unroll
               for (int src = 0; src < (ALT ? 2 : 1); ++src)
 #pragma unroll
-                for (int part = 0; part < (LO && r == 0 ? 2 : 1); ++part)
+                for (int part = 0; part < (LO ? 2 : 1); ++part)
+                  if (part == 0 || r == 0) {
 #pragma unroll
-                  for (int s = 0; s < 8; ++s)
-                    umma_ts<IDESC_F16_BMN>(tO, tS + 128 * src + (LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s),
-                                      sw128_mn_desc(vb + 2048 * s), (r || src || part || s) ? 1u : 0u);
+                    for (int s = 0; s < 8; ++s)
+                      umma_ts<IDESC_F16_BMN>(tO, tS + 128 * src + p_col(part, s), desc_step(vb, 2048 * s),
+                                             (r || src || part || s) ? 1u : 0u);
+                  }
               umma_commit(&ms.v_empty[c & 1]);
             } else {
               mbar_arrive(&ms.v_empty[c & 1]);
             }
           }
-          if (ok && act) umma_commit(&ms.pv_done[gr][1]);
+          __syncwarp();
         }
-        if (act) ++nf;  // (ALT: group 1's last P is waited for by group 0's issuer)
-        vc += R_TILES;
+        if (ok && act && lead) umma_commit(&ms.pv_done[gr][1]);
       }
-      if (issued && *reinterpret_cast<volatile int *>(&ms.abort_flag)) {
-        umma_commit(&ms.drain[gr]);
-        (void)mbar_wait_bounded(&ms.drain[gr], 0, WAIT_LIMIT_NS);
-      }
+      if (act) ++nf;  // (ALT: group 1's last P is waited for by group 0's issuer)
+      vc += R_TILES;
     }
+    if (issued && lead && *reinterpret_cast<volatile int *>(&ms.abort_flag)) {
+      umma_commit(&ms.drain[gr]);
+      (void)mbar_wait_bounded(&ms.drain[gr], 0, WAIT_LIMIT_NS);
+    }
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     // ================ softmax: group gr, thread = accumulator row r
     const int gr = warp >> 2, r = tid & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -714,24 +740,22 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
         for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4 *>(dst + sw128_offset(r, 8 * c)) = v[c];
         fence_async_smem();
       }
-      mbar_arrive(&ms.q_ready[gr]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.q_ready[gr]);
 
       float M = -INFINITY, l = 0.f;
       int done = 0;  // halves
-      // halves of 64 keys: the first half's PV runs under the second one's softmax
+      // halves of 64 keys: the other half's PV and next S run under this one's softmax
       const int tiles = ALT ? (n > gr ? (n - gr + 1) / 2 : 0) : n;
       for (int m = 0; m < 2 * tiles; ++m, ++done) {
         const int i = ALT ? gr + 2 * (m >> 1) : (m >> 1), h = m & 1;
         const int kf = (it.t0 + i) * KT + 64 * h;
         const uint32_t cv = vc + i, tH = tS + 64 * h;
-        if (!h) {
-          ok = wait(&ms.s_done[gr], ns & 1);
-          ++ns;
-          if (ok) ok = wait(&ms.v_full[cv & 1], (cv >> 1) & 1);
-          ok = __all_sync(FULL_MASK, ok);
-          if (!ok) break;
-          tc_fence_after();
-        }
+        ok = wait(&ms.s_done[gr][h], ns & 1);
+        if (ok && !h) ok = wait(&ms.v_full[cv & 1], (cv >> 1) & 1);
+        ok = __all_sync(FULL_MASK, ok);
+        if (!ok) break;
+        tc_fence_after();
         const float4 *kn4 = reinterpret_cast<const float4 *>(ms.kn[(kc + i) & 3]) + 16 * h;
         const float4 *nv4 = reinterpret_cast<const float4 *>(ms.nv[cv & 1]) + 16 * h;
         const bool full = kf + 63 <= it.s.base + q0;  // every row sees every key of the half
@@ -762,13 +786,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           const float alpha = raise ? exp2_approx(M - bm) : 1.f;
           if (raise) M = bm, l *= alpha;
           if (done && __any_sync(FULL_MASK, raise)) {
-            // O is whole once the first half's PV has finished (earlier tiles' have: S was issued
-            // after them); ns counts this tile already
-            if (h) {
-              ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr][0], (ns - 1) & 1));
-              if (!ok) return;
-              tc_fence_after();
-            }
+            // O is whole once the previous half's PV has finished (this half's S was issued after
+            // the one before that): half 0 of this tile, or half 1 of the tile before, which
+            // shares its barrier with the items' un-rotations
+            const uint32_t ph = h ? ns : ns - 1 + (ALT && gr ? 0 : nf);
+            ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr][h ^ 1], ph & 1));
+            if (!ok) return;
+            tc_fence_after();
 #pragma unroll 1
             for (int cc = 0; cc < 4; ++cc) {
               float o[32];
@@ -857,7 +881,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
         l += l0 + l1;
         tc_fence_before();
         if (!ok) break;  // (a failed wait while raising the maximum)
-        mbar_arrive(&ms.p_ready[gr][h]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.p_ready[gr][h]);
+        ns += h;
       }
       kc += n, vc += n + R_TILES;
 
@@ -923,7 +949,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
         tmem_st32(tS + 32 * c2, pw);
       }
       tc_fence_before();
-      mbar_arrive(&ms.p_ready[gr][0]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.p_ready[gr][0]);
       if (ALT && gr == 1) continue;
       ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr][1], (ns + nf) & 1));
       ++nf;

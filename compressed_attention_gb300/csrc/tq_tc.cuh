@@ -51,6 +51,18 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
   return d;
 }
 
+// True in one lane of a converged warp.  A loop of products issues at the tensor core's rate (a
+// 128 x 128 x 16 product each 64 cycles) when the block that one elected lane enters holds
+// whole runs of them with descriptors made beforehand (base + constant steps): building each
+// descriptor on the way took 176 cycles a product.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+// A descriptor moved on by `bytes` (a multiple of 16, inside shared memory).
+__device__ __forceinline__ uint64_t desc_step(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
 // Instruction descriptors of kind::f16, fp32 accumulator, both operands K-major,
 // M = N = 128: bf16 A and B, or fp16 A and B (one MMA never mixes the two).
 constexpr uint32_t IDESC_M128_N128 = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);

@@ -19,7 +19,7 @@
 //                                  read from tensor memory once: the exponentials are taken
 //                                  against the running maximum of earlier tiles, the fp16
 //                                  probabilities (value norm folded in) are kept in
-//                                  registers, and only when one passed 2^15 is the maximum
+//                                  registers, and only when their sum passed 2^15 is the maximum
 //                                  raised, O rescaled and the pass repeated; then P takes
 //                                  over S's columns.
 //                     While one group is in its softmax, the other one's products run.
@@ -52,13 +52,13 @@ constexpr int KT = 128;                // keys per tile
 constexpr int UNIT_TILES = 3;          // cost of an item ahead of its tiles, in tiles
 constexpr int RAW = KT * PG_ROW;       // a packed tile
 constexpr int NRAW = 3;
-constexpr int W_DEC = 8, W_MMA = 12, W_LOAD = 14, N_WARPS = 16;  // the last warp only fills its group
+constexpr int W_DEC = 8, W_MMA = 16, W_LOAD = 18, N_WARPS = 20;  // the last warp only fills its group
 constexpr int THREADS = N_WARPS * 32;
-// Registers: 512 threads x 128 at launch; the softmax groups take 160 (64 scores, 32 packed
-// probabilities and the norms of several columns in flight), the other two groups give theirs up
-// to 96: 256 * 160 + 256 * 96 = 65,536.
-constexpr int REGS_SOFTMAX = 160, REGS_OTHER = 96;
-static_assert(2 * 128 * REGS_SOFTMAX + 2 * 128 * REGS_OTHER <= THREADS * 128, "the launch's registers");
+// Registers: 640 threads x 96 at launch; the softmax groups take 144 (64 scores, 32 packed
+// probabilities and the norms of several columns in flight), the other three groups give theirs
+// up to 64: 256 * 144 + 384 * 64 = 640 * 96.
+constexpr int REGS_LAUNCH = 96, REGS_SOFTMAX = 144, REGS_OTHER = 64;
+static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "the launch's registers");
 constexpr uint32_t IDESC_S = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);  // fp16, M = 128, N = 64
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // S / P of the groups, O of the groups
 
@@ -531,52 +531,49 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       for (uint32_t c = n > NRAW ? n - NRAW : 0; c < n; ++c)
         (void)mbar_wait_bounded(&ms.raw_full[c % NRAW], (c / NRAW) & 1, WAIT_LIMIT_NS);
   } else if (warp < W_MMA) {
-    // ================ decoders: thread = row of the tile
-    const int row = tid - W_DEC * 32;
-    const uint32_t klo[2] = {p.klo[0], p.klo[1]}, khi[2] = {p.khi[0], p.khi[1]};
-    const uint32_t vlo[2] = {p.vlo[0], p.vlo[1]}, vhi[2] = {p.vhi[0], p.vhi[1]};
-    uint32_t nr = 0, kc = 0, vc = 0;  // raw tiles taken, K and V stages filled
-    uint32_t last_r = 0;              // V stages filled with R by a copy of thread 0: see the drain below
+    // ================ decoders: a group for the keys, one for the values, thread = row of the tile
+    const int row = tid & 127;
+    const bool side = warp >= W_DEC + 4;
+    uint32_t lo2[2], hi2[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) lo2[i] = side ? p.vlo[i] : p.klo[i], hi2[i] = side ? p.vhi[i] : p.khi[i];
+    uint64_t *full = side ? ms.v_full : ms.k_full, *empty = side ? ms.v_empty : ms.k_empty;
+    uint8_t *stages = smem + (side ? OFF_V : OFF_K);
+    uint32_t nr = side ? 1 : 0, c = 0;  // raw tiles of both sides passed; stages filled
+    uint32_t last_r = 0;                // stages filled with R by a copy of thread 0: see the drain below
     while (ok && next_item(p, w, it)) {
-      for (int j = it.t0; ok && j < it.t1; ++j) {
+      for (int j = it.t0; ok && j < it.t1; ++j, nr += 2, ++c) {
         const bool live = j * KT + row < it.keys;
-#pragma unroll 1
-        for (int side = 0; side < 2; ++side, ++nr) {
-          uint32_t &c = side ? vc : kc;
-          const int st = c & 1, rs = nr % NRAW;
-          if (c >= 2) ok = wait(side ? &ms.v_empty[st] : &ms.k_empty[st], ((c >> 1) - 1) & 1);
-          if (ok) ok = wait(&ms.raw_full[rs], (nr / NRAW) & 1);
-          ok = __all_sync(FULL_MASK, ok);
-          if (!ok) break;
-          const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + OFF_RAW + rs * RAW + row * PG_ROW);
-          uint8_t *dst = smem + (side ? OFF_V : OFF_K) + st * SW_TILE_BYTES;
-          const float norm = __uint_as_float(src[0]);
-          uint32_t lo2[2], hi2[2];
+        const int st = c & 1, rs = nr % NRAW;
+        if (c >= 2) ok = wait(&empty[st], ((c >> 1) - 1) & 1);
+        if (ok) ok = wait(&ms.raw_full[rs], (nr / NRAW) & 1);
+        ok = __all_sync(FULL_MASK, ok);
+        if (!ok) break;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + OFF_RAW + rs * RAW + row * PG_ROW);
+        uint8_t *dst = stages + st * SW_TILE_BYTES;
+        const float norm = __uint_as_float(src[0]);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) lo2[i] = side ? vlo[i] : klo[i], hi2[i] = side ? vhi[i] : khi[i];
-#pragma unroll
-          for (int ch = 0; ch < 16; ++ch) {
-            uint32_t d[4];
-            decode8<0x5140u, 0x7362u>(src[1 + ch], lo2, hi2, d);
-            *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 8 * ch)) = make_uint4(d[0], d[1], d[2], d[3]);
-          }
-          if (side) ms.nv[st][row] = live ? norm * 128.0f : 0.f;
-          else ms.kn[c & 3][row] = live ? norm : 0.f;
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(side ? &ms.v_full[st] : &ms.k_full[st]), mbar_arrive(&ms.raw_empty[rs]);
-          ++c;
+        for (int ch = 0; ch < 16; ++ch) {
+          uint32_t d[4];
+          decode8<0x5140u, 0x7362u>(src[1 + ch], lo2, hi2, d);
+          *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 8 * ch)) = make_uint4(d[0], d[1], d[2], d[3]);
         }
+        if (side) ms.nv[st][row] = live ? norm * 128.0f : 0.f;
+        else ms.kn[c & 3][row] = live ? norm : 0.f;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]), mbar_arrive(&ms.raw_empty[rs]);
       }
+      if (!side) continue;
       // R of the values as the item's last value tiles
-      for (int r = 0; ok && r < R_TILES; ++r, ++vc) {
-        const int st = vc & 1;
-        if (vc >= 2) ok = __all_sync(FULL_MASK, wait(&ms.v_empty[st], ((vc >> 1) - 1) & 1));
+      for (int r = 0; ok && r < R_TILES; ++r, ++c) {
+        const int st = c & 1;
+        if (c >= 2) ok = __all_sync(FULL_MASK, wait(&ms.v_empty[st], ((c >> 1) - 1) & 1));
         if (!ok) break;
         if (row == 0) {
           mbar_arrive_expect_tx(&ms.v_full[st], SW_TILE_BYTES);
           bulk_g2s(smem + OFF_V + st * SW_TILE_BYTES, p.vr + r * SW_TILE_BYTES, SW_TILE_BYTES, &ms.v_full[st]);
-          last_r = vc + 1;
+          last_r = c + 1;
         } else if (lane == 0) {
           mbar_arrive(&ms.v_full[st]);
         }
@@ -584,7 +581,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
     }
     // after a failed wait: the copy of R must land before the CTA ends (every thread of the
     // warp group arrives for a stage it has passed, so the phase completes with the copy)
-    if (row == 0 && last_r && *reinterpret_cast<volatile int *>(&ms.abort_flag))
+    if (side && row == 0 && last_r && *reinterpret_cast<volatile int *>(&ms.abort_flag))
       (void)mbar_wait_bounded(&ms.v_full[(last_r - 1) & 1], ((last_r - 1) >> 1) & 1, WAIT_LIMIT_NS);
   } else if (warp == W_MMA || warp == W_MMA + 1) {
     // ================ issuers: a warp per softmax group, its elected lane issues
@@ -780,9 +777,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           return bm;
         };
         // raise the running maximum of the rows that need it (the warp together)
-        auto raise_max = [&]() {
+        auto raise_max = [&](bool now) {
           const float bm = row_max();
-          const bool raise = bm > M + RESCALE_SLACK;  // also from -inf
+          const bool raise = bm > M + (now ? 0.f : RESCALE_SLACK);  // also from -inf
           const float alpha = raise ? exp2_approx(M - bm) : 1.f;
           if (raise) M = bm, l *= alpha;
           if (done && __any_sync(FULL_MASK, raise)) {
@@ -820,7 +817,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           if constexpr (!decltype(whole)::value) p0 = kf + c <= pos ? p0 : 0.f, p1 = kf + c + 1 <= pos ? p1 : 0.f;
         };
         if constexpr (LO) {
-          raise_max();
+          raise_max(false);
           const float Mu = (M == -INFINITY) ? 0.f : M;
           const uint64_t nm2 = pk2(-Mu, -Mu);
           l2 = pk2(0.f, 0.f);
@@ -848,30 +845,38 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           uint32_t pw[32];
           bool need = live && M == -INFINITY && kf <= pos;
           for (int turn = 0;; ++turn) {
-            if (__any_sync(FULL_MASK, need)) raise_max();
+            if (__any_sync(FULL_MASK, need)) raise_max(need);
             const float Mu = (M == -INFINITY) ? 0.f : M;
             const uint64_t nm2 = pk2(-Mu, -Mu);
             l2 = pk2(0.f, 0.f);
-            __half2 pm = __float2half2_rn(0.f);
+            uint64_t ps2 = pk2(0.f, 0.f);
             auto one_part = [&](auto whole) {
-              float sv[64];
-              tmem_ld64(tH, sv);
 #pragma unroll
-              for (int c4 = 0; c4 < 16; ++c4) {
-                const float4 kn = kn4[c4], nv = nv4[c4];
-                float p0, p1;
-                pair(whole, sv[4 * c4], sv[4 * c4 + 1], kn.x, kn.y, nv.x, nv.y, 4 * c4, nm2, p0, p1);
-                const __half2 h0 = __floats2half2_rn(p0, p1);
-                pair(whole, sv[4 * c4 + 2], sv[4 * c4 + 3], kn.z, kn.w, nv.z, nv.w, 4 * c4 + 2, nm2, p0, p1);
-                const __half2 h1 = __floats2half2_rn(p0, p1);
-                pm = __hmax2(pm, __hmax2(h0, h1));
-                pw[2 * c4] = *reinterpret_cast<const uint32_t *>(&h0);
-                pw[2 * c4 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+              for (int cc = 0; cc < 2; ++cc) {
+                float sv[32];
+                tmem_ld32(tH + 32 * cc, sv);
+#pragma unroll
+                for (int c4 = 0; c4 < 8; ++c4) {
+                  const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
+                  const int c = 32 * cc + 4 * c4;
+                  float p0, p1;
+                  pair(whole, sv[4 * c4], sv[4 * c4 + 1], kn.x, kn.y, nv.x, nv.y, c, nm2, p0, p1);
+                  pw[c / 2] = pack_half2(p0, p1);
+                  ps2 = add2(ps2, pk2(p0, p1));
+                  pair(whole, sv[4 * c4 + 2], sv[4 * c4 + 3], kn.z, kn.w, nv.z, nv.w, c + 2, nm2, p0, p1);
+                  pw[c / 2 + 1] = pack_half2(p0, p1);
+                  ps2 = add2(ps2, pk2(p0, p1));
+                }
               }
             };
             if (full && !scaled) one_part(std::true_type());
             else one_part(std::false_type());
-            need = live && (__low2float(pm) > 32768.f || __high2float(pm) > 32768.f);
+            // A probability past 2^15 shows in their sum (at most 2^13 under the current maximum):
+            // one packed add a pair, where a maximum would take the slower ALU.  The redo then takes
+            // the tile's own maximum.
+            float ps0, ps1;
+            upk2(ps2, ps0, ps1);
+            need = live && !(ps0 + ps1 <= 32768.f);
             if (turn || !__any_sync(FULL_MASK, need)) break;
           }
           tmem_st32(tH, pw);

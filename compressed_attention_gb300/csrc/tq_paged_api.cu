@@ -51,6 +51,7 @@ tq_status check_paged(const tq_ctx *k, const tq_ctx *v, const tq_paged_kv *kv, c
   if (!aligned(kv->k_pages, 16) || !aligned(kv->v_pages, 16)) return fail(TQ_ERR_ALIGNMENT, "pages must be 16-byte aligned");
   if (!aligned(kv->block_table, 4) || !aligned(bt->seq_lens, 4) || !aligned(bt->cu_q, 4))
     return fail(TQ_ERR_ALIGNMENT, "block table, lengths and cu_q must be 4-byte aligned");
+  if ((int64_t)bt->n_tokens * kv->Hkv > INT32_MAX / 2) return fail(TQ_ERR_INVALID_ARG, "n_tokens * Hkv passes 2^30");
   *pv = PagedView{};
   pv->table = kv->block_table, pv->table_stride = kv->table_stride;
   for (pv->page_shift = 4; (1 << pv->page_shift) < kv->page_size;) ++pv->page_shift;

@@ -5,8 +5,8 @@
 // threads per row, eight rows per warp, the canonical order of norm, division and
 // butterfly, so the stored bytes equal those of a plain fp32 sequence.  The rotation's
 // pairs (j, j + 64) and (j, j + 32) and adjacent pairs lie inside one thread's chunks;
-// pairs (j, j + 16) cross to the thread two over.  Even CTAs take the keys, odd ones the
-// values, so a CTA keeps one codebook grid.
+// pairs (j, j + 16) cross to the thread two over.  A CTA takes keys or values, so it keeps one
+// codebook grid.
 #include "tq_paged.cuh"
 #include "tq_qprep.cuh"
 #include "tq_wht.cuh"
@@ -27,7 +27,8 @@ struct AppendParams {
   PagedView pv;
   RopeView rope;
   AppendSide side[2];  // keys, values
-  int only;            // 0 or 1: that side; 2: both (even CTAs keys, odd ones values)
+  int only;            // 0 or 1: that side; 2: both
+  int k_ctas;          // the first CTAs take the keys, the others the values
 };
 
 // Position rotation of a row in quarter layout (register element 8i + e = row element
@@ -60,11 +61,16 @@ __device__ __forceinline__ void rope_quarter(float (&x)[WT_E], int q, const Rope
       const float4 s4 = *reinterpret_cast<const float4 *>(st + at + 4 * h);
       const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
+      for (int m = 0; m < 4; m += 2) {
         const int e = 4 * h + m;
-        const float a = x[8 * ga + e], b = x[8 * gb + e];
-        x[8 * ga + e] = rot_first(a, b, c[m], s[m]);
-        x[8 * gb + e] = rot_second(a, b, c[m], s[m]);
+        const F2 a = f2(x[8 * ga + e], x[8 * ga + e + 1]), b = f2(x[8 * gb + e], x[8 * gb + e + 1]);
+        const F2 cc = f2(c[m], c[m + 1]), ss = f2(s[m], s[m + 1]);
+        // packed products, scalar sums: a packed product feeding a packed sum may be contracted
+        float ac0, ac1, bs0, bs1, as0, as1, bc0, bc1;
+        f2_split(f2_mul(a, cc), ac0, ac1), f2_split(f2_mul(b, ss), bs0, bs1);
+        f2_split(f2_mul(a, ss), as0, as1), f2_split(f2_mul(b, cc), bc0, bc1);
+        x[8 * ga + e] = __fsub_rn(ac0, bs0), x[8 * ga + e + 1] = __fsub_rn(ac1, bs1);
+        x[8 * gb + e] = __fadd_rn(as0, bc0), x[8 * gb + e + 1] = __fadd_rn(as1, bc1);
       }
     }
   };
@@ -103,7 +109,7 @@ __device__ __forceinline__ Place place_row(const PagedView &v, int tok, int h, b
 template <int SRC>
 __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendParams p) {
   __shared__ WhtTables tb;
-  const int side = p.only == 2 ? (blockIdx.x & 1) : p.only, n_side = p.only == 2 ? 2 : 1;
+  const int side = (int)blockIdx.x < p.k_ctas ? 0 : 1;
   const AppendSide &sd = p.side[side];
   pdl_trigger();
   wht_tables_fill<TQ_FMT_TURBO4>(sd.b, sd.bt, tb);
@@ -115,21 +121,40 @@ __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendPar
   uint32_t nq[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) nq[i] = sd.wht_neg[i] >> (8 * q);
-  const int64_t n_rows = (int64_t)paged_rows(p.pv) * p.pv.Hkv;
-  const int64_t n_iter = (n_rows + 7) / 8, step = (int64_t)(gridDim.x / n_side) * (WT_THREADS / 32);
+  // Rows in groups of eight per warp: this thread's row moves on by 8 * step rows a turn, kept as
+  // (token, head) with the sequence and its length beside it (tokens only grow, so the sequence
+  // is found by stepping on from the last one).
+  const int Hkv = p.pv.Hkv, n_rows = paged_rows(p.pv) * Hkv;
+  const int cta = side ? blockIdx.x - p.k_ctas : blockIdx.x, n_cta = side ? gridDim.x - p.k_ctas : p.k_ctas;
+  const int step = n_cta * (WT_THREADS / 32), n_iter = (n_rows + 7) / 8;
+  const int d_tok = 8 * step / Hkv, d_head = 8 * step - d_tok * Hkv;
+  int it = cta * (WT_THREADS / 32) + (threadIdx.x >> 5);
+  int tok = (it * 8 + sub) / Hkv, head = it * 8 + sub - tok * Hkv;
+  int b = -1, b_end = 0, len = 0;  // the row's sequence, the row after its last, its length
   const bool turn = side == 0 && p.rope.rot_dim != 0;
   Quarter<SRC> raw;
   Place pl{-1, 0};
-  auto fetch = [&](int64_t i) {
-    const int64_t row = i * 8 + sub;
+  auto fetch = [&](int i) {
     pl.at = -1;
-    if (i < n_iter && row < n_rows) {
-      const int tok = (int)(row / p.pv.Hkv), h = (int)(row - (int64_t)tok * p.pv.Hkv);
-      load_quarter<SRC>(sd.src.data + tok * sd.src.token_bytes + h * sd.src.head_bytes, q, true, raw);
-      pl = place_row(p.pv, tok, h, q == 0);
+    if (i < n_iter && i * 8 + sub < n_rows) {
+      load_quarter<SRC>(sd.src.data + tok * sd.src.token_bytes + head * sd.src.head_bytes, q, true, raw);
+      if (b < 0 || tok >= b_end) {
+        if (b < 0 || !p.pv.cu_q) b = paged_seq(p.pv, tok);
+        else
+          do ++b;
+          while (b + 1 < p.pv.B && p.pv.cu_q[b + 1] <= tok);
+        b_end = p.pv.cu_q ? p.pv.cu_q[b + 1] : tok + 1;
+        len = paged_len(p.pv, b, q == 0);
+      }
+      pl.pos = len - (b_end - tok);
+      if (pl.pos >= 0 && pl.pos < len) {
+        const int pg = paged_page(p.pv, b, pl.pos, q == 0);
+        if (pg >= 0) pl.at = (int64_t)paged_row(p.pv, pg, head, pl.pos & ((1 << p.pv.page_shift) - 1));
+      }
+      tok += d_tok, head += d_head;
+      if (head >= Hkv) head -= Hkv, ++tok;
     }
   };
-  int64_t it = (int64_t)(blockIdx.x / n_side) * (WT_THREADS / 32) + (threadIdx.x >> 5);
   fetch(it);
   for (; it < n_iter; it += step) {
     const Place at = pl;
@@ -154,13 +179,14 @@ __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendPar
   }
 }
 
-// Dense rotation: a warp per row, R^T staged once per CTA (even CTAs: keys, odd: values).
+// Dense rotation: a warp per row, R^T staged once per CTA.
 constexpr int AD_WARPS = 8;
 constexpr size_t AD_SMEM = (size_t)D * D * 4 + AD_WARPS * D * 4;
 __global__ void __launch_bounds__(AD_WARPS * 32) k_paged_append_dense(const AppendParams p) {
   extern __shared__ __align__(16) float asm_f[];
   float *rt = asm_f, *uv = asm_f + D * D;
-  const int side = p.only == 2 ? (blockIdx.x & 1) : p.only, n_side = p.only == 2 ? 2 : 1;
+  const int side = (int)blockIdx.x < p.k_ctas ? 0 : 1;
+  const int cta = side ? blockIdx.x - p.k_ctas : blockIdx.x, n_cta = side ? gridDim.x - p.k_ctas : p.k_ctas;
   const AppendSide &sd = p.side[side];
   __shared__ float sb[16];
   __shared__ __align__(16) uint8_t ib[AD_WARPS][D];
@@ -172,8 +198,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32) k_paged_append_dense(const Appe
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float *u = uv + warp * D;
   const int64_t n_rows = (int64_t)paged_rows(p.pv) * p.pv.Hkv;
-  for (int64_t row = (int64_t)(blockIdx.x / n_side) * AD_WARPS + warp; row < n_rows;
-       row += (int64_t)(gridDim.x / n_side) * AD_WARPS) {
+  for (int64_t row = (int64_t)cta * AD_WARPS + warp; row < n_rows; row += (int64_t)n_cta * AD_WARPS) {
     const int tok = (int)(row / p.pv.Hkv), h = (int)(row - (int64_t)tok * p.pv.Hkv);
     const Place at = place_row(p.pv, tok, h, lane == 0);
     if (at.at < 0) continue;
@@ -211,17 +236,21 @@ __global__ void __launch_bounds__(AD_WARPS * 32) k_paged_append_dense(const Appe
   }
 }
 
+// A key row with its rotation takes about 5/4 of a value row's instructions: the CTAs are shared
+// out in that proportion.
 template <typename K>
-cudaError_t launch_rows(K kern, const AppendParams &p, int threads, int rows_per_cta, size_t smem, int sms,
-                        cudaStream_t st) {
+cudaError_t launch_rows(K kern, AppendParams p, int threads, int rows_per_cta, size_t smem, int sms, cudaStream_t st) {
   cudaError_t e = smem ? kernel_smem_attr((const void *)kern, (int)smem) : cudaSuccess;
   int blocks = 1;
   if (e == cudaSuccess) e = kernel_occupancy((const void *)kern, threads, smem, &blocks);
   if (e != cudaSuccess) return e;
   const int sides = p.only == 2 ? 2 : 1;
   const int64_t want = ((int64_t)p.pv.n_tokens * p.pv.Hkv + rows_per_cta - 1) / rows_per_cta;
-  const int64_t most = (int64_t)sms * blocks / sides;
-  return launch_pdl(kern, dim3(sides * (unsigned)(want < most ? want : most)), dim3(threads), smem, st, p);
+  const int64_t most = (int64_t)sms * blocks;
+  const int grid = (int)(want * sides < most ? want * sides : most);
+  p.k_ctas = p.only == 0 ? grid : (p.only == 1 ? 0 : grid / 2);
+  if (p.only == 2 && grid == most && p.rope.rot_dim) p.k_ctas = grid * 5 / 9;
+  return launch_pdl(kern, dim3(grid), dim3(threads), smem, st, p);
 }
 
 cudaError_t launch_append(const AppendParams &p, bool dense, int dtype, int sms, cudaStream_t st) {

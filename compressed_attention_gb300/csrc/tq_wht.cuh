@@ -11,6 +11,40 @@
 
 namespace tq {
 
+// Two fp32 values in a register pair: one instruction does both, each rounded exactly as the
+// scalar operation, so that the canonical order keeps its bits at half the issue slots.
+struct F2 {
+  uint64_t v;
+};
+static __device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+static __device__ __forceinline__ void f2_split(F2 x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+static __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+static __device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+static __device__ __forceinline__ F2 f2_sub(F2 a, F2 b) {
+  F2 r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+static __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 // x / n rounded to nearest, given r = RN(1/n): q = RN(x r) is within one ulp of x / n,
 // the residual x - q n is exact under a fused multiply-add, and one correction
 // q + (x - q n) r rounded to nearest is RN(x / n) (Markstein's theorem for binary
@@ -106,9 +140,13 @@ static __device__ __forceinline__ void unpack_quarter(const Quarter<TQ_DTYPE_BF1
 static __device__ __forceinline__ float quarter_norm_normalize(float (&x)[WT_E]) {
   float p[8];  // four-element partial sums of register groups 2i + h
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    p[k] = __fadd_rn(__fadd_rn(__fmul_rn(x[4 * k], x[4 * k]), __fmul_rn(x[4 * k + 1], x[4 * k + 1])),
-                     __fadd_rn(__fmul_rn(x[4 * k + 2], x[4 * k + 2]), __fmul_rn(x[4 * k + 3], x[4 * k + 3])));
+  for (int k = 0; k < 8; ++k) {
+    const F2 a = f2(x[4 * k], x[4 * k + 1]), b = f2(x[4 * k + 2], x[4 * k + 3]);
+    float a0, a1, b0, b1;
+    f2_split(f2_mul(a, a), a0, a1);
+    f2_split(f2_mul(b, b), b0, b1);
+    p[k] = __fadd_rn(__fadd_rn(a0, a1), __fadd_rn(b0, b1));
+  }
   float s[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -124,20 +162,26 @@ static __device__ __forceinline__ float quarter_norm_normalize(float (&x)[WT_E])
   const float n = __fsqrt_rn(__fadd_rn(s[0], s[1]));
   const float r = __frcp_rn(n);
   // Markstein's correction is exact when every nonzero |x| >= 2^-100 and n <= 2^24 (then
-  // |q| >= 2^-124 and 1/n is normal); zeros come out as zeros.  Otherwise the guarded
-  // per-element division.
-  uint32_t mb = 0xFFFFFFFFu;  // min over elements of |x| bits - 1 (zero -> 0xFFFFFFFF)
+  // |q| >= 2^-124 and 1/n is normal); zeros come out as zeros.  Otherwise (a row with a zero
+  // among its elements asks again, element by element) the guarded per-element division.
+  float mn = fabsf(x[0]);
 #pragma unroll
-  for (int j = 0; j < WT_E; ++j) mb = min(mb, (__float_as_uint(x[j]) & 0x7FFFFFFFu) - 1u);
-  const bool fast = n <= 0x1p24f && mb >= 0x0D800000u - 1u;  // 0x0D800000: 2^-100
+  for (int j = 1; j < WT_E; ++j) mn = fminf(mn, fabsf(x[j]));
+  bool fast = n <= 0x1p24f && mn >= 0x1p-100f;
+  if (n <= 0x1p24f && !fast) {
+    uint32_t mb = 0xFFFFFFFFu;  // min over elements of |x| bits - 1 (zero -> 0xFFFFFFFF)
+#pragma unroll
+    for (int j = 0; j < WT_E; ++j) mb = min(mb, (__float_as_uint(x[j]) & 0x7FFFFFFFu) - 1u);
+    fast = mb >= 0x0D800000u - 1u;  // 0x0D800000: 2^-100
+  }
   if (n == 0.0f) {
 #pragma unroll
     for (int j = 0; j < WT_E; ++j) x[j] = 0.0f;
   } else if (fast) {
 #pragma unroll
-    for (int j = 0; j < WT_E; ++j) {
-      const float qq = __fmul_rn(x[j], r);
-      x[j] = __fmaf_rn(__fmaf_rn(-qq, n, x[j]), r, qq);
+    for (int j = 0; j < WT_E; j += 2) {  // q + (x - q n) r; fma(q, -n, x) is fma(-q, n, x)
+      const F2 xx = f2(x[j], x[j + 1]), rr = f2(r, r), qq = f2_mul(xx, rr);
+      f2_split(f2_fma(f2_fma(qq, f2(-n, -n), xx), rr, qq), x[j], x[j + 1]);
     }
   } else {
 #pragma unroll
@@ -157,10 +201,14 @@ static __device__ __forceinline__ void wht_quarter(float (&v)[WT_E], const uint3
   auto stage = [&](int h, int hr) {  // row distance h = register distance hr, in this thread
 #pragma unroll
     for (int k = 0; k < WT_E; ++k)
-      if (!(k & hr)) {
+      if (!(k & hr) && hr == 1) {
         const float a = v[k], b = v[k + hr];
         v[k] = __fadd_rn(a, b);
         v[k + hr] = __fsub_rn(a, b);
+      } else if (!(k & hr) && !(k & 1)) {
+        const F2 a = f2(v[k], v[k + 1]), b = f2(v[k + hr], v[k + hr + 1]);
+        f2_split(f2_add(a, b), v[k], v[k + 1]);
+        f2_split(f2_sub(a, b), v[k + hr], v[k + hr + 1]);
       }
     (void)h;
   };
@@ -173,16 +221,17 @@ static __device__ __forceinline__ void wht_quarter(float (&v)[WT_E], const uint3
   for (int m = 1; m <= 2; m <<= 1) {
     const float sgn = (q & m) ? -1.0f : 1.0f;
 #pragma unroll
-    for (int k = 0; k < WT_E; ++k) {
-      const float o = __shfl_xor_sync(FULL_MASK, v[k], m);
-      v[k] = __fmaf_rn(sgn, v[k], o);
+    for (int k = 0; k < WT_E; k += 2) {
+      const float o0 = __shfl_xor_sync(FULL_MASK, v[k], m), o1 = __shfl_xor_sync(FULL_MASK, v[k + 1], m);
+      f2_split(f2_fma(f2(sgn, sgn), f2(v[k], v[k + 1]), f2(o0, o1)), v[k], v[k + 1]);
     }
   }
   stage(32, 8);
   stage(64, 16);
   const float inv_sqrt_d = __int_as_float(0x3DB504F3);  // fp32 nearest 1/sqrt(128)
 #pragma unroll
-  for (int k = 0; k < WT_E; ++k) v[k] = __fmul_rn(v[k], inv_sqrt_d);
+  for (int k = 0; k < WT_E; k += 2)
+    f2_split(f2_mul(f2(v[k], v[k + 1]), f2(inv_sqrt_d, inv_sqrt_d)), v[k], v[k + 1]);
 }
 
 // #{k : y > b_k}: the grid (copy l16 of cell t: boundary .x, count .y as integer bits) or,

@@ -624,13 +624,15 @@ def tq_make_rope_table(rot_dim, n_pos, base=10000.0):
 
 def _rows(t, n_tokens, heads, what):
     """tq_rows of a [n_tokens, heads, 128] tensor (any strides, elements of a row packed)."""
-    if t.dim() != 3 or t.shape[0] < n_tokens or t.shape[1] != heads or t.shape[2] != D or t.stride(2) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] < n_tokens or shape[1] != heads or shape[2] != D or stride[2] != 1:
         raise ValueError(f"{what} must be [n_tokens, {heads}, {D}] with packed rows")
-    return tq_rows(t.data_ptr(), _dtype_code(t), t.stride(0), t.stride(1))
+    return tq_rows(t.data_ptr(), _dtype_code(t), stride[0], stride[1])
 
 
 def _dense_out(t, n_tokens, heads, what):
-    if t.dim() != 3 or t.shape[0] < n_tokens or t.shape[1] != heads or t.shape[2] != D or not t.is_contiguous():
+    shape = t.shape
+    if len(shape) != 3 or shape[0] < n_tokens or shape[1] != heads or shape[2] != D or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous [n_tokens, {heads}, {D}] tensor")
     return t.data_ptr()
 

@@ -72,13 +72,16 @@ static __device__ __forceinline__ float rot_second(float a, float b, float c, fl
   return __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
 }
 
-// Elements 4l .. 4l + 3 of a row.
-static __device__ __forceinline__ void load_lane4(const uint8_t *row, int dtype, int lane, float (&x)[4]) {
+// Elements 4l .. 4l + 3 of a row: as loaded, and as fp32.
+static __device__ __forceinline__ uint4 load_lane4_raw(const uint8_t *row, int dtype, int lane) {
+  if (dtype == TQ_DTYPE_F32) return reinterpret_cast<const uint4 *>(row)[lane];
+  const uint2 v = reinterpret_cast<const uint2 *>(row)[lane];
+  return make_uint4(v.x, v.y, 0u, 0u);
+}
+static __device__ __forceinline__ void lane4_floats(const uint4 &v, int dtype, float (&x)[4]) {
   if (dtype == TQ_DTYPE_F32) {
-    const float4 v = reinterpret_cast<const float4 *>(row)[lane];
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   } else {
-    const uint2 v = reinterpret_cast<const uint2 *>(row)[lane];
     if (dtype == TQ_DTYPE_BF16) {
       x[0] = bf16_bits_to_f32(v.x & 0xFFFFu), x[1] = bf16_bits_to_f32(v.x >> 16);
       x[2] = bf16_bits_to_f32(v.y & 0xFFFFu), x[3] = bf16_bits_to_f32(v.y >> 16);
@@ -89,19 +92,38 @@ static __device__ __forceinline__ void load_lane4(const uint8_t *row, int dtype,
     }
   }
 }
+static __device__ __forceinline__ void load_lane4(const uint8_t *row, int dtype, int lane, float (&x)[4]) {
+  lane4_floats(load_lane4_raw(row, dtype, lane), dtype, x);
+}
 
-// Position rotation of a row held as elements 4l .. 4l + 3 of lane l (the whole warp calls).
-static __device__ __forceinline__ void rope_lane4(float (&x)[4], int lane, const RopeView &r, int pos) {
-  if (!r.rot_dim) return;
+// Angles of a row's elements 4l .. 4l + 3 (lane l), loaded ahead of the row they turn.
+struct LaneAngles {
+  float4 c, s;  // interleaved: two pairs, in .x and .y
+};
+static __device__ __forceinline__ LaneAngles rope_angles(int lane, const RopeView &r, int pos) {
+  LaneAngles a;
+  a.c = make_float4(1.f, 1.f, 1.f, 1.f), a.s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (4 * lane >= r.rot_dim) return a;
   const int half = r.rot_dim >> 1;
   const float *ct = r.cos_t + (size_t)pos * half, *st = r.sin_t + (size_t)pos * half;
+  if (r.interleaved) {
+    const float2 c = reinterpret_cast<const float2 *>(ct)[lane], z = reinterpret_cast<const float2 *>(st)[lane];
+    a.c.x = c.x, a.c.y = c.y, a.s.x = z.x, a.s.y = z.y;
+  } else {
+    const int at = lane & ((r.rot_dim >> 3) - 1);
+    a.c = reinterpret_cast<const float4 *>(ct)[at], a.s = reinterpret_cast<const float4 *>(st)[at];
+  }
+  return a;
+}
+
+// Position rotation of a row held as elements 4l .. 4l + 3 of lane l (the whole warp calls).
+static __device__ __forceinline__ void rope_turn(float (&x)[4], int lane, const RopeView &r, const LaneAngles &an) {
   const bool act = 4 * lane < r.rot_dim;
   if (r.interleaved) {
     if (act) {
-      const float2 c = reinterpret_cast<const float2 *>(ct)[lane], s = reinterpret_cast<const float2 *>(st)[lane];
       const float a = x[0], b = x[1], e = x[2], f = x[3];
-      x[0] = rot_first(a, b, c.x, s.x), x[1] = rot_second(a, b, c.x, s.x);
-      x[2] = rot_first(e, f, c.y, s.y), x[3] = rot_second(e, f, c.y, s.y);
+      x[0] = rot_first(a, b, an.c.x, an.s.x), x[1] = rot_second(a, b, an.c.x, an.s.x);
+      x[2] = rot_first(e, f, an.c.y, an.s.y), x[3] = rot_second(e, f, an.c.y, an.s.y);
     }
     return;
   }
@@ -110,13 +132,14 @@ static __device__ __forceinline__ void rope_lane4(float (&x)[4], int lane, const
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] = __shfl_xor_sync(FULL_MASK, x[e], m);
   if (act) {
-    const int at = lane & (m - 1);
-    const float4 c = reinterpret_cast<const float4 *>(ct)[at], s = reinterpret_cast<const float4 *>(st)[at];
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    const float cc[4] = {an.c.x, an.c.y, an.c.z, an.c.w}, ss[4] = {an.s.x, an.s.y, an.s.z, an.s.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       x[e] = (lane & m) ? rot_second(o[e], x[e], cc[e], ss[e]) : rot_first(x[e], o[e], cc[e], ss[e]);
   }
+}
+static __device__ __forceinline__ void rope_lane4(float (&x)[4], int lane, const RopeView &r, int pos) {
+  if (r.rot_dim) rope_turn(x, lane, r, rope_angles(lane, r, pos));
 }
 
 static __device__ __forceinline__ uint32_t pack_bf162(float a, float b) {

@@ -21,7 +21,6 @@
 
 #include "tq_decode_common.cuh"
 #include "tq_paged.cuh"
-#include "tq_qprep.cuh"
 #include "tq_rotmma.cuh"
 #include "tq_t4_tile.cuh"
 
@@ -84,6 +83,38 @@ __device__ __forceinline__ uint8_t *stage_at(uint8_t *sm, int i) {
 }
 
 __device__ __forceinline__ void consumers_sync() { named_sync1<CW * 32>(); }
+// Barrier over the first N threads, apart from that of all the consumers.
+template <int N>
+__device__ __forceinline__ void named_sync2() {
+  asm volatile("bar.sync 2, %0;" ::"n"(N) : "memory");
+}
+
+// A head's R q times mul, scaled by a power of two 2^-e so that the largest element lies in
+// [2^13, 2^14), as fp16 hi and lo: word w of a part (elements 2w, 2w + 1) at
+// 16 (w / 16) + ((w % 16) ^ x), x of the part and block, so that the consumers' lanes, which read
+// word w % 16 of 16 (part, block) pairs of a bank each, hit 32 banks.
+__device__ __forceinline__ void split_q(const float *y, float mul, Tail &tl, int slot, int lane) {
+  float2 v[2];
+  float amax = 0.f;
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    v[m] = *reinterpret_cast<const float2 *>(y + 2 * (lane + 32 * m));
+    v[m].x *= mul, v[m].y *= mul;
+    amax = fmaxf(amax, fmaxf(fabsf(v[m].x), fabsf(v[m].y)));
+  }
+#pragma unroll
+  for (int h = 16; h >= 1; h >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, h));
+  const int e = (amax > 0.f && isfinite(amax)) ? ilogbf(amax) - 13 : 0;
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    uint32_t hi, lo;
+    split_half2(ldexpf(v[m].x, -e), ldexpf(v[m].y, -e), hi, lo);
+    const int w = lane + 32 * m, t = w >> 4, at = 16 * t + (w & 15), x = 4 * (slot & 3) + (t >> 1);
+    tl.q[slot][at ^ x] = hi;             // part 0: 2 g + t / 2 with g = 2 (slot % 4)
+    tl.q[slot][64 + (at ^ (x + 2))] = lo;  // part 1: g + 1
+  }
+  if (lane == 0) tl.qs[slot] = ldexpf(1.0f, e);
+}
 
 // Keys that sequence b's row sees and the row (-1: none).
 __device__ __forceinline__ int seq_keys(const PagedView &v, int b, int *row, bool flag) {
@@ -216,7 +247,7 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     }
     if (lane == 0) {
       sm.V = V, sm.G = G;
-      tl.q[0][0] = w.b, tl.q[0][1] = w.u, tl.q[0][2] = w.off, tl.q[0][3] = w.left, tl.q[0][4] = w.v;
+      *reinterpret_cast<Walk *>(tl.q[0]) = w;
     }
     __syncwarp();
     named_arrive0<NT>();  // the barriers and the share are set up
@@ -282,10 +313,8 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
   }
   pdl_wait();  // the pages, q and the workspace may be written by the previous kernel
   named_sync0<NT>();
-  Walk w{(int)tl.q[0][0], (int)tl.q[0][1], (int)tl.q[0][2], (int)tl.q[0][3], (int)tl.q[0][4], 0, 0, 0};
+  Walk w = *reinterpret_cast<const Walk *>(tl.q[0]);
   const int V = sm.V, G = sm.G;
-  if (w.left > 0) walk_load(p, w);
-  consumers_sync();  // tl.q is free
 
   const int g = lane >> 2, t = lane & 3;
   const uint32_t lut_base = smem_addr(lut);
@@ -303,39 +332,56 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
   const float lo_sel = (g & 1) ? 1.f : 0.f;
 
   int ctr = 0;
-  Item it;
+  Item it, nx;
   bool aborted = false;
-  while (next_item(p, w, it)) {
-    const int kvh = it.u / p.n_hg, hg = it.u - kvh * p.n_hg;
-    const int head0 = kvh * p.gq + hg * p.hpc, GH = min(p.hpc, p.gq - hg * p.hpc);
+  // an item's first q-head and heads; warp h < heads loads head h's row and its angles
+  auto heads_of = [&](const Item &i, int &head0, int &GH) {
+    const int kvh = i.u / p.n_hg, hg = i.u - kvh * p.n_hg;
+    head0 = kvh * p.gq + hg * p.hpc, GH = min(p.hpc, p.gq - hg * p.hpc);
+  };
+  uint4 q_raw = make_uint4(0u, 0u, 0u, 0u);
+  LaneAngles q_ang;
+  auto fetch_q = [&](const Item &i) {
+    int head0, GH;
+    heads_of(i, head0, GH);
+    if (warp >= GH) return;
+    q_raw = load_lane4_raw(p.q.data + i.row * p.q.token_bytes + (head0 + warp) * p.q.head_bytes, p.q.dtype, lane);
+    if (p.rope.rot_dim) q_ang = rope_angles(lane, p.rope, rope_pos(p.rope, i.keys - 1, p.pv.status, lane == 0));
+  };
+  bool have = next_item(p, w, it);
+  if (have) fetch_q(it);
+  consumers_sync();  // tl.q (the share) has been read
+  while (have) {
+    int head0, GH;
+    heads_of(it, head0, GH);
 
     // ---- q of the item: position rotation, R q, scale, fp16 hi + lo
     if (warp < 8) {
+      uint4 rh[8], rl[8];  // this warp's 16 rows of R, under the wait for q
+      rot_load(rh, p.kfrag, 0, 0, warp, lane);
+      rot_load(rl, p.kfrag, 0, 1, warp, lane);
       float x[4] = {0.f, 0.f, 0.f, 0.f};
       if (warp < GH) {
-        load_lane4(p.q.data + it.row * p.q.token_bytes + (head0 + warp) * p.q.head_bytes, p.q.dtype, lane, x);
-        if (p.rope.rot_dim) rope_lane4(x, lane, p.rope, rope_pos(p.rope, it.keys - 1, p.pv.status, lane == 0));
+        lane4_floats(q_raw, p.q.dtype, x);
+        if (p.rope.rot_dim) rope_turn(x, lane, p.rope, q_ang);
       }
       rot_put(sm.prep.x, warp, lane, x);
-    }
-    consumers_sync();
-    if (warp < 8) rot_tile(p.kfrag, 0, warp, lane, sm.prep.x, &sm.prep.y[0][0], D + 4);
-    consumers_sync();
-    if (warp < GH) {
-      const int e = scale_split(sm.prep.y[warp], p.qmul, reinterpret_cast<__half *>(tl.q[warp]), lane);
-      if (lane == 0) tl.qs[warp] = ldexpf(1.0f, e);
+      named_sync2<8 * 32>();
+      rot_tile(rh, rl, warp, lane, sm.prep.x, &sm.prep.y[0][0], D + 4);
+      named_sync2<8 * 32>();
+      if (warp < GH) split_q(sm.prep.y[warp], p.qmul, tl, warp, lane);
     }
     consumers_sync();
     uint32_t qb[NG][8][2];
     float qs[NG];
 #pragma unroll
     for (int c = 0; c < NG; ++c) {
-      const int slot = c * 4 + hs;
+      const int slot = c * 4 + hs, sw = 2 * g + (t >> 1);
       const uint32_t *qw = tl.q[slot] + (g & 1) * 64 + 16 * t;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        qb[c][kk][0] = slot < GH ? qw[2 * kk] : 0u;
-        qb[c][kk][1] = slot < GH ? qw[2 * kk + 1] : 0u;
+        qb[c][kk][0] = slot < GH ? qw[(2 * kk) ^ sw] : 0u;
+        qb[c][kk][1] = slot < GH ? qw[(2 * kk + 1) ^ sw] : 0u;
       }
       const int my = c * 4 + t;  // the head whose scores this lane holds
       qs[c] = my < GH ? tl.qs[my] : 0.f;
@@ -451,6 +497,9 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     // same tile, so either every consumer warp enters the merge barriers or none.
     if (aborted || *reinterpret_cast<volatile int *>(&sm.abort_flag)) return;
 
+    have = next_item(p, w, nx);
+    if (have) fetch_q(nx);  // under the merge
+
     // ---- merge the warps' states and write the item's partial
 #pragma unroll
     for (int c = 0; c < NG; ++c) {
@@ -487,11 +536,14 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
       ls += __shfl_xor_sync(FULL_MASK, ls, 8);
       ls += __shfl_xor_sync(FULL_MASK, ls, 16);
       const float fac = (M[c] == -INFINITY) ? 0.f : exp2_approx(M[c] - ms);
-      float *orow = &sm.osm[warp][t][0];  // rows g and g + 8 of m-tile mt: dims 16g + 2mt, + 1
+      // rows g and g + 8 of m-tile mt: dims 16g + 2mt, + 1, in blocks of 16 permuted so that the
+      // warp's lanes hit 32 banks
+      float *orow = &sm.osm[warp][t][16 * g];
+      const int sw = 4 * (g >> 1) + t;
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) {
-        orow[16 * g + 2 * mt] = (O[c][mt][0] + O[c][mt][1]) * fac;
-        orow[16 * g + 2 * mt + 1] = (O[c][mt][2] + O[c][mt][3]) * fac;
+        orow[(2 * mt) ^ sw] = (O[c][mt][0] + O[c][mt][1]) * fac;
+        orow[(2 * mt + 1) ^ sw] = (O[c][mt][2] + O[c][mt][3]) * fac;
       }
       consumers_sync();
       const int Gc = min(4, GH - c * 4);
@@ -500,13 +552,14 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
         const float ms2 = __shfl_sync(FULL_MASK, ms, h4), ls2 = __shfl_sync(FULL_MASK, ls, h4);
         float acc = 0.f;
 #pragma unroll
-        for (int ww = 0; ww < CW; ++ww) acc += sm.osm[ww][h4][jd];
+        for (int ww = 0; ww < CW; ++ww) acc += sm.osm[ww][h4][jd ^ (4 * (jd >> 5) + h4)];
         float *dst = dst0 + (c * 4 + h4) * PROW;
         dst[jd] = (ms2 == -INFINITY) ? 0.f : acc;
         if (jd < 2) dst[D + jd] = jd == 0 ? ms2 : ls2;
       }
       consumers_sync();
     }
+    it = nx;
   }
 }
 

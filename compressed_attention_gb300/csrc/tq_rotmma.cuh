@@ -69,15 +69,12 @@ static __device__ __forceinline__ void rot_mul(float (&acc)[4], const uint4 (&a)
   }
 }
 
-// Row-tile mt of Y = M X into y[column][16 mt ..] (rows of `pitch` floats) by one warp.
-static __device__ __forceinline__ void rot_tile(const uint4 *frag, int m, int mt, int lane, const RotColumns &x,
-                                                float *y, int pitch) {
-  uint4 a[8];
+// Row-tile mt of Y = M X, from its loaded parts, into y[column][16 mt ..] (rows of `pitch` floats).
+static __device__ __forceinline__ void rot_tile(const uint4 (&hi)[8], const uint4 (&lo)[8], int mt, int lane,
+                                                const RotColumns &x, float *y, int pitch) {
   float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
-  rot_load(a, frag, m, 0, mt, lane);
-  rot_mul<true>(acc, a, x, lane);
-  rot_load(a, frag, m, 1, mt, lane);
-  rot_mul<false>(acc2, a, x, lane);
+  rot_mul<true>(acc, hi, x, lane);
+  rot_mul<false>(acc2, lo, x, lane);
   const int g = lane >> 2, t = lane & 3;
   float *d = y + 2 * t * pitch + 16 * mt + g;
   d[0] = acc[0] + acc2[0], d[pitch] = acc[1] + acc2[1];

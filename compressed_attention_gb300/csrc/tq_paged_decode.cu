@@ -7,8 +7,9 @@
 //                    for the cost of starting it; CTA c takes the c-th equal share, so
 //                    ragged lengths balance.  The shares come from the lengths on the
 //                    device, so a captured launch follows them.  Per item the consumer
-//                    warps rotate the unit's q by its position (fp32) and by R (bf16 parts
-//                    on the tensor cores, tq_rotmma.cuh) themselves, while the producer
+//                    warps rotate the unit's q by its position (fp32) and by R (a WHT in the
+//                    warp, a dense R as bf16 parts on the tensor cores,
+//                    tq_rotmma.cuh) themselves, while the producer
 //                    warp already streams the first tiles: a tile is one bulk copy per
 //                    page it meets (K by lanes 0-15, V by lanes 16-31, the page ids of the
 //                    next tile loaded one tile ahead) on a four-stage ring.  The products
@@ -43,7 +44,8 @@ struct DecodeParams {
   RopeView rope;
   int Hq, gq, n_hg, hpc;   // q-heads; per KV head; head groups per KV head; heads of a unit
   float qmul;              // log2(e) * scale / alpha_K
-  const uint4 *kfrag;      // R of the keys
+  const uint4 *kfrag;      // dense R of the keys (null: WHT, signs in wht_neg)
+  uint32_t wht_neg[4];
   uint32_t kc16[8], vc16[8];
   uint32_t klo[2], khi[2], vlo[2], vhi[2];
   float *split;            // [CTA][2][8] partials of units that several CTAs share
@@ -89,31 +91,41 @@ __device__ __forceinline__ void named_sync2() {
   asm volatile("bar.sync 2, %0;" ::"n"(N) : "memory");
 }
 
-// A head's R q times mul, scaled by a power of two 2^-e so that the largest element lies in
-// [2^13, 2^14), as fp16 hi and lo: word w of a part (elements 2w, 2w + 1) at
-// 16 (w / 16) + ((w % 16) ^ x), x of the part and block, so that the consumers' lanes, which read
-// word w % 16 of 16 (part, block) pairs of a bank each, hit 32 banks.
-__device__ __forceinline__ void split_q(const float *y, float mul, Tail &tl, int slot, int lane) {
-  float2 v[2];
+// A head's R q (elements 4l .. 4l + 3 of lane l) times mul, scaled by a power of two 2^-e so that
+// the largest element lies in [2^13, 2^14), as fp16 hi and lo: word w of a part (elements 2w,
+// 2w + 1) at 16 (w / 16) + ((w % 16) ^ x), x of the part and block, so that the consumers' lanes,
+// which read word w % 16 of 16 (part, block) pairs of a bank each, hit 32 banks.
+__device__ __forceinline__ void split_q(float (&v)[4], float mul, Tail &tl, int slot, int lane) {
   float amax = 0.f;
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    v[m] = *reinterpret_cast<const float2 *>(y + 2 * (lane + 32 * m));
-    v[m].x *= mul, v[m].y *= mul;
-    amax = fmaxf(amax, fmaxf(fabsf(v[m].x), fabsf(v[m].y)));
-  }
+  for (int m = 0; m < 4; ++m) v[m] *= mul, amax = fmaxf(amax, fabsf(v[m]));
 #pragma unroll
   for (int h = 16; h >= 1; h >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, h));
   const int e = (amax > 0.f && isfinite(amax)) ? ilogbf(amax) - 13 : 0;
+  const int t = lane >> 3, at = 16 * t + 2 * (lane & 7), x = 4 * (slot & 3) + (t >> 1);
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     uint32_t hi, lo;
-    split_half2(ldexpf(v[m].x, -e), ldexpf(v[m].y, -e), hi, lo);
-    const int w = lane + 32 * m, t = w >> 4, at = 16 * t + (w & 15), x = 4 * (slot & 3) + (t >> 1);
-    tl.q[slot][at ^ x] = hi;             // part 0: 2 g + t / 2 with g = 2 (slot % 4)
-    tl.q[slot][64 + (at ^ (x + 2))] = lo;  // part 1: g + 1
+    split_half2(ldexpf(v[2 * m], -e), ldexpf(v[2 * m + 1], -e), hi, lo);
+    tl.q[slot][(at + m) ^ x] = hi;               // part 0: 2 g + t / 2 with g = 2 (slot % 4)
+    tl.q[slot][64 + ((at + m) ^ (x + 2))] = lo;  // part 1: g + 1
   }
   if (lane == 0) tl.qs[slot] = ldexpf(1.0f, e);
+}
+
+// H D x of a row held as elements 4l .. 4l + 3 of lane l (without the 1 / sqrt(128)).
+__device__ __forceinline__ void wht_lane4(float (&x)[4], const uint32_t (&neg)[4], int lane) {
+  const uint32_t n = neg[lane >> 3] >> (4 * (lane & 7));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = (n >> e) & 1u ? -x[e] : x[e];
+  const float a = x[0] + x[1], b = x[0] - x[1], c = x[2] + x[3], d = x[2] - x[3];
+  x[0] = a + c, x[1] = b + d, x[2] = a - c, x[3] = b - d;
+#pragma unroll
+  for (int h = 1; h <= 16; h <<= 1) {
+    const float sg = (lane & h) ? -1.f : 1.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = fmaf(sg, x[e], __shfl_xor_sync(FULL_MASK, x[e], h));
+  }
 }
 
 // Keys that sequence b's row sees and the row (-1: none).
@@ -355,21 +367,31 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     int head0, GH;
     heads_of(it, head0, GH);
 
-    // ---- q of the item: position rotation, R q, scale, fp16 hi + lo
-    if (warp < 8) {
-      uint4 rh[8], rl[8];  // this warp's 16 rows of R, under the wait for q
+    // ---- q of the item: position rotation, R q, scale, fp16 hi + lo.  The WHT runs in a warp per
+    // head; a dense R takes its 64 KB from L2 and two barriers more (1.4 us).
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (warp < GH) {
+      lane4_floats(q_raw, p.q.dtype, x);
+      if (p.rope.rot_dim) rope_turn(x, lane, p.rope, q_ang);
+    }
+    if (!p.kfrag) {
+      if (warp < GH) {
+        wht_lane4(x, p.wht_neg, lane);
+        split_q(x, p.qmul * 0.08838834764831845f, tl, warp, lane);
+      }
+    } else if (warp < 8) {
+      uint4 rh[8], rl[8];  // this warp's 16 rows of R
       rot_load(rh, p.kfrag, 0, 0, warp, lane);
       rot_load(rl, p.kfrag, 0, 1, warp, lane);
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      if (warp < GH) {
-        lane4_floats(q_raw, p.q.dtype, x);
-        if (p.rope.rot_dim) rope_turn(x, lane, p.rope, q_ang);
-      }
       rot_put(sm.prep.x, warp, lane, x);
       named_sync2<8 * 32>();
       rot_tile(rh, rl, warp, lane, sm.prep.x, &sm.prep.y[0][0], D + 4);
       named_sync2<8 * 32>();
-      if (warp < GH) split_q(sm.prep.y[warp], p.qmul, tl, warp, lane);
+      if (warp < GH) {
+        const float4 v = *reinterpret_cast<const float4 *>(&sm.prep.y[warp][4 * lane]);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        split_q(x, p.qmul, tl, warp, lane);
+      }
     }
     consumers_sync();
     uint32_t qb[NG][8][2];
@@ -712,7 +734,8 @@ cudaError_t launch_paged_decode(const tq_ctx *k, const tq_ctx *v, const PagedVie
   p.pv = pv, p.kp = kp, p.vp = vp, p.q = q, p.rope = rope;
   p.Hq = Hq, p.gq = Hq / pv.Hkv, p.n_hg = l.n_hg, p.hpc = l.hpc;
   p.qmul = LOG2E * scale / k->f16.alpha;
-  p.kfrag = k->d_rfrag;
+  p.kfrag = k->p.rotation == TQ_ROT_DENSE ? k->d_rfrag : nullptr;
+  for (int i = 0; i < 4; ++i) p.wht_neg[i] = k->wht_neg[i];
   for (int i = 0; i < 8; ++i) p.kc16[i] = k->f16.c16[i], p.vc16[i] = v->f16.c16[i];
   for (int i = 0; i < 2; ++i) {
     p.klo[i] = k->f16.lo[i], p.khi[i] = k->f16.hi[i];

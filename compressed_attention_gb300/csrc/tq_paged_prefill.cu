@@ -711,7 +711,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
     const uint32_t tS = tmem + lane_off + TM_S + 128 * gr, tO = tmem + lane_off + TM_O + 128 * gr;
     const int rq = r / p.gq, rh = r - rq * p.gq;
     uint32_t kc = 0, vc = 0, ns = 0, nf = 0;  // K, V stages passed; S tiles; items finished
-    while (ok && next_item(p, w, it)) {
+    // After a failed wait a warp goes on to the next barrier of all softmax warps (ALT), where they
+    // leave together; without one (not ALT) it leaves by itself.
+    bool alive = true;
+    while (alive && next_item(p, w, it)) {
       const int n = it.t1 - it.t0;
       const int q0 = it.qt * p.qpu + (ALT ? 0 : gr * p.qpt);
       if (q0 >= it.s.T) {  // (not ALT) no second row tile
@@ -912,7 +915,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       if (ALT) {  // the two groups' states of a row, merged
         ms.xm[gr][r] = M, ms.xl[gr][r] = l, ms.xa[gr][r] = amax;
         if (softmax_sync_or(!ok)) {
-          ok = false;
+          alive = false;
           break;
         }
         const float M0 = ms.xm[0][r], M1 = ms.xm[1][r], l0 = ms.xl[0][r], l1 = ms.xl[1][r];
@@ -959,7 +962,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       if (ALT && gr == 1) continue;
       ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr][1], (ns + nf) & 1));
       ++nf;
-      if (!ok) break;
+      if (!ok) {
+        if (ALT) continue;
+        break;
+      }
       tc_fence_after();
 
       // ---- the unit's rows, or this CTA's partial of them

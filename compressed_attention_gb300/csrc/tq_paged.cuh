@@ -142,6 +142,15 @@ static __device__ __forceinline__ void rope_lane4(float (&x)[4], int lane, const
   if (r.rot_dim) rope_turn(x, lane, r, rope_angles(lane, r, pos));
 }
 
+// The exponent whose power of two brings amax down (or up) to [2^13, 2^14), fp16's upper end with a
+// bit to spare; 0 for a row of zeros, infinity or NaN.  In [-126, 114]: a row below 2^-113 is
+// brought up by 2^126 only, so that the power and its inverse are normal numbers.
+static __device__ __forceinline__ int scale_exp(float amax) {
+  const int eb = __float_as_int(amax) >> 23;
+  return amax > 0.f && eb < 255 ? max(eb - 127, -113) - 13 : 0;
+}
+static __device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }  // |e| <= 126
+
 static __device__ __forceinline__ uint32_t pack_bf162(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);

@@ -99,18 +99,18 @@ __device__ __forceinline__ void split_q(float (&v)[4], float mul, Tail &tl, int 
   float amax = 0.f;
 #pragma unroll
   for (int m = 0; m < 4; ++m) v[m] *= mul, amax = fmaxf(amax, fabsf(v[m]));
-#pragma unroll
-  for (int h = 16; h >= 1; h >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, h));
-  const int e = (amax > 0.f && isfinite(amax)) ? ilogbf(amax) - 13 : 0;
+  amax = __uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(amax)));  // ordered like the floats
+  const int e = scale_exp(amax);
+  const float down = pow2i(-e);
   const int t = lane >> 3, at = 16 * t + 2 * (lane & 7), x = 4 * (slot & 3) + (t >> 1);
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     uint32_t hi, lo;
-    split_half2(ldexpf(v[2 * m], -e), ldexpf(v[2 * m + 1], -e), hi, lo);
+    split_half2(v[2 * m] * down, v[2 * m + 1] * down, hi, lo);
     tl.q[slot][(at + m) ^ x] = hi;               // part 0: 2 g + t / 2 with g = 2 (slot % 4)
     tl.q[slot][64 + ((at + m) ^ (x + 2))] = lo;  // part 1: g + 1
   }
-  if (lane == 0) tl.qs[slot] = ldexpf(1.0f, e);
+  if (lane == 0) tl.qs[slot] = pow2i(e);
 }
 
 // H D x of a row held as elements 4l .. 4l + 3 of lane l (without the 1 / sqrt(128)).

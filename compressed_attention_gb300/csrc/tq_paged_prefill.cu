@@ -174,6 +174,7 @@ __device__ __forceinline__ bool next_item(const PrefillParams &p, Walk &w, Item 
 }
 
 // ------------------------------------------------------------------------------ preparation
+constexpr int PREP_WARPS = 16;
 struct PrepParams {
   PagedView pv;
   RowsView q;
@@ -190,50 +191,66 @@ struct PrepParams {
   int lo;                 // also write the lo parts
 };
 
-constexpr int PREP_ROWS = 64;
 constexpr int PREP_PITCH = D + 8;
 
-__device__ __forceinline__ int seq_vtiles(const PagedView &v, int b, int qpu, bool flag) {
-  const Seq s = seq_of(v, b, qpu, flag);
-  int sum = 0;
-  for (int qt = 0; qt < s.n_qt; ++qt) {
-    const int t = unit_tiles(s, qt, qpu);
-    sum += t ? t + UNIT_TILES : 0;
+// Virtual tiles of query tile qt of s (0 past its end), one head.
+__device__ __forceinline__ int unit_vtiles(const Seq &s, int qt, int qpu) {
+  const int t = qt < s.n_qt ? unit_tiles(s, qt, qpu) : 0;
+  return t ? t + UNIT_TILES : 0;
+}
+__device__ __forceinline__ Seq seq_from_lane(const Seq &s, int src) {
+  return Seq{__shfl_sync(FULL_MASK, s.row, src), __shfl_sync(FULL_MASK, s.T, src), __shfl_sync(FULL_MASK, s.base, src),
+             __shfl_sync(FULL_MASK, s.n_qt, src)};
+}
+__device__ __forceinline__ int warp_scan(int x, int lane) {
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1) {
+    const int o = __shfl_up_sync(FULL_MASK, x, h);
+    if (lane >= h) x += o;
   }
-  return sum * v.Hkv;
+  return x;
 }
 
-// One CTA of 256 threads: prefix sums over the sequences (in shared memory up to n_sm of
-// them), then every share's start.
+// One CTA of PREP_WARPS warps: prefix sums over the sequences (in shared memory up to n_sm of them), then
+// every share's start.  A thread per sequence, then per share; query tiles are walked 32 at a time
+// by the whole warp, one sequence or share after the other (a thread walking 64 tiles by itself,
+// twice, took 30 us: longer than all of q's preparation beside it).
 __device__ void plan(const PrepParams &p, int *sm_prefix, int n_sm) {
   int *prefix = p.pv.B <= n_sm ? sm_prefix : p.prefix;
-  __shared__ int wsum[8];
+  __shared__ int wsum[PREP_WARPS];
   __shared__ int carry;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, Hkv = p.pv.Hkv;
   if (tid == 0) carry = 0;
   __syncthreads();
-  for (int b0 = 0; b0 < p.pv.B; b0 += 256) {
+  for (int b0 = 0; b0 < p.pv.B; b0 += PREP_WARPS * 32) {
     const int b = b0 + tid;
-    const int t = b < p.pv.B ? seq_vtiles(p.pv, b, p.qpu, true) : 0;
-    int inc = t;
-#pragma unroll
-    for (int h = 1; h < 32; h <<= 1) {
-      const int o = __shfl_up_sync(FULL_MASK, inc, h);
-      if (lane >= h) inc += o;
+    const Seq s = seq_of(p.pv, b, p.qpu, true);
+    int t = unit_vtiles(s, 0, p.qpu);
+    for (uint32_t m = __ballot_sync(FULL_MASK, s.n_qt > 1); m; m &= m - 1) {
+      const int src = __ffs(m) - 1;
+      const Seq w = seq_from_lane(s, src);
+      int sum = 0;
+      for (int qt = lane; qt < w.n_qt; qt += 32) sum += unit_vtiles(w, qt, p.qpu);
+      sum = __reduce_add_sync(FULL_MASK, sum);
+      if (lane == src) t = sum;
     }
+    t *= Hkv;
+    const int inc = warp_scan(t, lane);
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
     int before = carry;
     for (int w = 0; w < warp; ++w) before += wsum[w];
     if (b < p.pv.B) prefix[b] = before + inc - t;
     __syncthreads();
-    if (tid == 255) carry = before + inc;
+    if (tid == PREP_WARPS * 32 - 1) carry = before + inc;
     __syncthreads();
   }
   const int V = carry, G = min(p.grid, V);
-  for (int c = tid; c < p.grid; c += 256) {
+  for (int c0 = 0; c0 < p.grid; c0 += PREP_WARPS * 32) {
+    const int c = c0 + lane * PREP_WARPS + warp;  // neighbours in different warps: all of them have work
     Start st{0, 0, 0, 0, 0, 0, V, G};
-    p.join[c].n = 0;
+    Seq s{0, 0, 0, 0};
+    int o = 0;
     if (c < G) {
       st.v = share_start(c, V, G);
       st.left = share_start(c + 1, V, G) - st.v;
@@ -244,19 +261,34 @@ __device__ void plan(const PrepParams &p, int *sm_prefix, int n_sm) {
         else hi = mid - 1;
       }
       st.b = lo;
-      int o = st.v - prefix[lo];
-      const Seq s = seq_of(p.pv, lo, p.qpu, false);
-      for (; st.qt < s.n_qt; ++st.qt) {
-        const int t = unit_tiles(s, st.qt, p.qpu), vt = t ? t + UNIT_TILES : 0;
-        if (o < vt * p.pv.Hkv) {
-          st.h = o / vt;
-          st.off = o - st.h * vt;
+      o = st.v - prefix[lo];
+      s = seq_of(p.pv, lo, p.qpu, false);
+    }
+    // the query tile that holds o: the first whose inclusive sum passes it
+    for (uint32_t m = __ballot_sync(FULL_MASK, s.n_qt > 0); m; m &= m - 1) {
+      const int src = __ffs(m) - 1;
+      const Seq w = seq_from_lane(s, src);
+      int wo = __shfl_sync(FULL_MASK, o, src);
+      for (int q0 = 0; q0 < w.n_qt; q0 += 32) {
+        const int vt = unit_vtiles(w, q0 + lane, p.qpu), inc = warp_scan(vt * Hkv, lane);
+        const uint32_t past = __ballot_sync(FULL_MASK, inc > wo);
+        if (past) {
+          const int f = __ffs(past) - 1, fvt = __shfl_sync(FULL_MASK, vt, f);
+          const int ahead = __shfl_sync(FULL_MASK, inc, f) - fvt * Hkv;
+          if (lane == src) {
+            st.qt = q0 + f;
+            st.h = (wo - ahead) / fvt;
+            st.off = wo - ahead - st.h * fvt;
+          }
           break;
         }
-        o -= vt * p.pv.Hkv;
+        wo -= __shfl_sync(FULL_MASK, inc, 31);
       }
     }
-    p.start[c] = st;
+    if (c < p.grid) {
+      p.join[c].n = 0;
+      p.start[c] = st;
+    }
   }
 }
 
@@ -288,128 +320,164 @@ __device__ __forceinline__ void load_rows(const uint8_t *const (&row)[N], int dt
   }
 }
 
-__global__ void __launch_bounds__(256) k_paged_prep(const PrepParams p) {
-  __shared__ __align__(16) uint16_t xs[2][PREP_ROWS][PREP_PITCH];  // bf16 hi, lo
-  __shared__ int pos_s[PREP_ROWS], tok_s[PREP_ROWS];
-  float(*y)[D + 4] = reinterpret_cast<float(*)[D + 4]>(&xs[0][0][0]);  // over both, after the products
-  static_assert(sizeof(xs) >= PREP_ROWS * (D + 4) * 4, "y over the parts");
+__device__ __forceinline__ uint4 ldmatrix_x4(const void *row) {
+  uint4 r;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"((uint32_t)__cvta_generic_to_shared(row))
+               : "memory");
+  return r;
+}
+
+// CTA 0 plans; in the others each warp takes tiles of 16 q rows by itself: loaded in rows, turned
+// by position, split into bf16 parts in the warp's own shared memory, multiplied by R (three
+// products of parts) and stored from the product's fragments.  R's fragments (64 KB) lie in shared
+// memory once per SM, from one bulk copy ahead of the wait.  16 warps of their own pace hide each
+// other's latencies; blocks of 64 rows that eight warps shared, with barriers between the steps,
+// took 36 us for 47488 rows.
+struct PrepSmem {
+  uint4 r[2][8][8][32];  // R, bf16 hi and lo
+  alignas(16) uint16_t xs[PREP_WARPS][2][16][PREP_PITCH];  // a warp's rows, bf16 hi and lo
+  uint64_t full;
+};
+
+__global__ void __launch_bounds__(PREP_WARPS * 32) k_paged_prep(const PrepParams p) {
+  extern __shared__ __align__(128) uint8_t smem_prep[];
+  PrepSmem &sm = *reinterpret_cast<PrepSmem *>(smem_prep);
   pdl_trigger();
-  pdl_wait();
   if (blockIdx.x == 0) {
-    plan(p, reinterpret_cast<int *>(&xs[0][0][0]), (int)(sizeof(xs) / 4));
+    pdl_wait();
+    plan(p, reinterpret_cast<int *>(&sm.xs[0][0][0][0]), (int)(sizeof(sm.xs) / 4));
     return;
   }
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.full, 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(&sm.full, sizeof(sm.r));
+    bulk_g2s(&sm.r[0][0][0][0], p.kfrag, sizeof(sm.r), &sm.full);
+  }
+  __syncthreads();
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t n = (int64_t)paged_rows(p.pv) * p.Hq, r0 = (int64_t)(blockIdx.x - 1) * PREP_ROWS;
-  if (r0 >= n) return;
-  // the rows' places: a thread each
-  if (threadIdx.x < PREP_ROWS) {
-    const int64_t r = r0 + threadIdx.x;
-    int tok = -1, pos = -1;
-    if (r < n) {
-      tok = (int)(r / p.Hq);
-      const int b = paged_seq(p.pv, tok);
-      pos = paged_pos(p.pv, b, tok, paged_len(p.pv, b, false));
+  auto &xs = sm.xs[warp];
+  const int64_t n = (int64_t)paged_rows(p.pv) * p.Hq;
+  const int ctas = gridDim.x - 1;
+  bool have_r = false;
+  // tiles over the CTAs first: a few rows use as many SMs as they can
+  for (int64_t tile = (int64_t)warp * ctas + blockIdx.x - 1; tile * 16 < n; tile += (int64_t)PREP_WARPS * ctas) {
+    const int64_t r0 = tile * 16;
+    int my_tok = -1, my_pos = -1;  // of row r0 + lane
+    if (lane < 16 && r0 + lane < n) {
+      my_tok = (int)((uint32_t)(r0 + lane) / (uint32_t)p.Hq);
+      const int b = paged_seq(p.pv, my_tok);
+      my_pos = paged_pos(p.pv, b, my_tok, paged_len(p.pv, b, false));
     }
-    tok_s[threadIdx.x] = tok, pos_s[threadIdx.x] = pos;
-  }
-  __syncthreads();
-  // eight rows per warp, four at a time: load, position rotation, bf16 parts
-  constexpr int NR = 4;
+    __syncwarp();  // the last tile's fragments are read
+    constexpr int NR = 8;
 #pragma unroll 1
-  for (int i0 = 0; i0 < PREP_ROWS / 8; i0 += NR) {
-    const int rb = warp * (PREP_ROWS / 8) + i0;
-    const uint8_t *src[NR];
-    int pos[NR];
-    float x[NR][4];
+    for (int rb = 0; rb < 16; rb += NR) {  // eight rows' loads in flight
+      const uint8_t *src[NR];
+      int pos[NR];
+      float x[NR][4];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const int tok = tok_s[rb + i], h = (int)(r0 + rb + i - (int64_t)max(tok, 0) * p.Hq);
-      pos[i] = pos_s[rb + i];
-      src[i] = pos[i] >= 0 ? p.q.data + tok * p.q.token_bytes + h * p.q.head_bytes : nullptr;
-      if (tok >= 0 && pos[i] < 0) {  // no key: the row's output is zero
-        const float z[4] = {0.f, 0.f, 0.f, 0.f};
-        if (!p.o.diff.lambda) store_lane4(p.o.out, p.o.dtype, (size_t)(r0 + rb + i) * D, lane, z);
-        else if (!(h & 1)) store_lane4(p.o.out, p.o.dtype, ((size_t)tok * (p.Hq / 2) + h / 2) * D, lane, z);
+      for (int i = 0; i < NR; ++i) {
+        const int tok = __shfl_sync(FULL_MASK, my_tok, rb + i), h = (int)(r0 + rb + i - (int64_t)max(tok, 0) * p.Hq);
+        pos[i] = __shfl_sync(FULL_MASK, my_pos, rb + i);
+        src[i] = pos[i] >= 0 ? p.q.data + tok * p.q.token_bytes + h * p.q.head_bytes : nullptr;
+        if (tok >= 0 && pos[i] < 0) {  // no key: the row's output is zero
+          const float z[4] = {0.f, 0.f, 0.f, 0.f};
+          if (!p.o.diff.lambda) store_lane4(p.o.out, p.o.dtype, (size_t)(r0 + rb + i) * D, lane, z);
+          else if (!(h & 1)) store_lane4(p.o.out, p.o.dtype, ((size_t)tok * (p.Hq / 2) + h / 2) * D, lane, z);
+        }
       }
-      if (p.rope.rot_dim) pos[i] = rope_pos(p.rope, pos[i], p.pv.status, lane == 0);
-    }
-    load_rows(src, p.q.dtype, lane, x);
-    if (p.rope.rot_dim) {
+      load_rows(src, p.q.dtype, lane, x);
+      if (p.rope.rot_dim) {
+        LaneAngles an;
 #pragma unroll
-      for (int i = 0; i < NR; ++i) rope_lane4(x[i], lane, p.rope, pos[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(x[i][2 * m], x[i][2 * m + 1]);
-        const float2 f = __bfloat1622float2(a);
-        const __nv_bfloat162 c = __floats2bfloat162_rn(isinf(f.x) ? 0.f : x[i][2 * m] - f.x,
-                                                       isinf(f.y) ? 0.f : x[i][2 * m + 1] - f.y);
-        hi[m] = *reinterpret_cast<const uint32_t *>(&a);
-        lo[m] = *reinterpret_cast<const uint32_t *>(&c);
+        for (int i = 0; i < NR; ++i) {
+          if (i == 0 || pos[i] != pos[i - 1])  // the heads of a token share its angles
+            an = rope_angles(lane, p.rope, rope_pos(p.rope, pos[i], p.pv.status, lane == 0));
+          rope_turn(x[i], lane, p.rope, an);
+        }
       }
-      *reinterpret_cast<uint2 *>(&xs[0][rb + i][4 * lane]) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2 *>(&xs[1][rb + i][4 * lane]) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const __nv_bfloat162 a = __floats2bfloat162_rn(x[i][2 * m], x[i][2 * m + 1]);
+          const float2 f = __bfloat1622float2(a);
+          const __nv_bfloat162 c = __floats2bfloat162_rn(isinf(f.x) ? 0.f : x[i][2 * m] - f.x,
+                                                         isinf(f.y) ? 0.f : x[i][2 * m + 1] - f.y);
+          hi[m] = *reinterpret_cast<const uint32_t *>(&a);
+          lo[m] = *reinterpret_cast<const uint32_t *>(&c);
+        }
+        *reinterpret_cast<uint2 *>(&xs[0][rb + i][4 * lane]) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2 *>(&xs[1][rb + i][4 * lane]) = make_uint2(lo[0], lo[1]);
+      }
+    }
+    __syncwarp();
+    if (!have_r) {
+      if (!mbar_wait_bounded(&sm.full, 0, WAIT_LIMIT_NS)) {
+        if (lane == 0) atomicExch(p.pv.status, (int32_t)DEVERR_TIMEOUT);
+        return;
+      }
+      have_r = true;
+    }
+    // Y = X R^T; R's A fragments hold the B fragments of two column tiles each: registers (0, 2)
+    // and (1, 3)
+    float acc[16][4];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll 2
+    for (int s = 0; s < 8; ++s) {
+      uint4 a[2];
+#pragma unroll
+      for (int part = 0; part < 2; ++part) a[part] = ldmatrix_x4(&xs[part][lane & 15][16 * s + 8 * (lane >> 4)]);
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const uint4 rh = sm.r[0][m][s][lane], rl = sm.r[1][m][s][lane];
+        mma_bf16(acc[2 * m], a[0], rh.x, rh.z), mma_bf16(acc[2 * m + 1], a[0], rh.y, rh.w);
+        mma_bf16(acc[2 * m], a[1], rh.x, rh.z), mma_bf16(acc[2 * m + 1], a[1], rh.y, rh.w);
+        mma_bf16(acc[2 * m], a[0], rl.x, rl.z), mma_bf16(acc[2 * m + 1], a[0], rl.y, rl.w);
+      }
+    }
+    // rows g and g + 8, columns 8 j + 2 t and the next
+    float amax[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[j][e] *= p.qmul;
+        amax[e >> 1] = fmaxf(amax[e >> 1], fabsf(acc[j][e]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t r = r0 + g + 8 * i;
+      float m = amax[i];
+      m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, 2));
+      if (r >= n) continue;
+      // The power of two that brings the largest element to [2^13, 2^14).  One part leaves rows alone
+      // whose largest element already lies in [2^-10, 2^14) (what fp16 drops there is below 2^-14 of
+      // it): their scores then need no scaling in the softmax.
+      const bool as_is = !p.lo && m >= 0x1p-10f && m < 0x1p14f;
+      const int e = as_is ? 0 : scale_exp(m);
+      const float down = pow2i(-e);
+      uint16_t *dst = p.qh + (size_t)r * 2 * D;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        uint32_t hi, lo;
+        split_half2(acc[j][2 * i] * down, acc[j][2 * i + 1] * down, hi, lo);
+        *reinterpret_cast<uint32_t *>(dst + 8 * j + 2 * t) = hi;
+        if (p.lo) *reinterpret_cast<uint32_t *>(dst + D + 8 * j + 2 * t) = lo;
+      }
+      if (t == 0) p.qsc[r] = pow2i(e);
     }
   }
-  __syncthreads();
-  // warp: rows 16 (w % 4) .. + 15, columns 64 (w / 4) .. + 63 of Y = X R^T; R's A fragments hold
-  // the B fragments of two column tiles each: registers (0, 2) and (1, 3)
-  float acc[8][4];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-  const int rt = 16 * (warp & 3), mt0 = 4 * (warp >> 2);
-#pragma unroll
-  for (int s = 0; s < 8; ++s) {
-    uint4 a[2];
-    uint32_t *aw = reinterpret_cast<uint32_t *>(a);
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        aw[4 * part + e] = *reinterpret_cast<const uint32_t *>(&xs[part][rt + g + 8 * (e & 1)][16 * s + 2 * t + 8 * (e >> 1)]);
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const uint4 rh = __ldg(p.kfrag + ((size_t)(mt0 + m) * 8 + s) * 32 + lane);
-      const uint4 rl = __ldg(p.kfrag + ((size_t)(8 + mt0 + m) * 8 + s) * 32 + lane);
-      mma_bf16(acc[2 * m], a[0], rh.x, rh.z), mma_bf16(acc[2 * m + 1], a[0], rh.y, rh.w);
-      mma_bf16(acc[2 * m], a[1], rh.x, rh.z), mma_bf16(acc[2 * m + 1], a[1], rh.y, rh.w);
-      mma_bf16(acc[2 * m], a[0], rl.x, rl.z), mma_bf16(acc[2 * m + 1], a[0], rl.y, rl.w);
-    }
-  }
-  __syncthreads();  // the parts are read
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int c = 16 * mt0 + 8 * j + 2 * t;
-    *reinterpret_cast<float2 *>(&y[rt + g][c]) = make_float2(acc[j][0], acc[j][1]);
-    *reinterpret_cast<float2 *>(&y[rt + g + 8][c]) = make_float2(acc[j][2], acc[j][3]);
-  }
-  __syncthreads();
-  for (int i = 0; i < PREP_ROWS / 8; ++i) {
-    const int r = warp * (PREP_ROWS / 8) + i;
-    if (r0 + r >= n) break;
-    const float4 v = *reinterpret_cast<const float4 *>(&y[r][4 * lane]);
-    const float x[4] = {v.x * p.qmul, v.y * p.qmul, v.z * p.qmul, v.w * p.qmul};
-    float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-    for (int h = 16; h >= 1; h >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, h));
-    // The power of two that brings the largest element to [2^13, 2^14).  One part leaves rows alone
-    // whose largest element already lies in [2^-10, 2^14) (what fp16 drops there is below 2^-14 of
-    // it): their scores then need no scaling in the softmax.
-    const bool as_is = !p.lo && amax >= 0x1p-10f && amax < 0x1p14f;
-    const int e = (amax > 0.f && isfinite(amax) && !as_is) ? ilogbf(amax) - 13 : 0;
-    uint32_t hi[2], lo[2];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) split_half2(ldexpf(x[2 * m], -e), ldexpf(x[2 * m + 1], -e), hi[m], lo[m]);
-    uint16_t *dst = p.qh + (size_t)(r0 + r) * 2 * D;
-    reinterpret_cast<uint2 *>(dst)[lane] = make_uint2(hi[0], hi[1]);
-    if (p.lo) reinterpret_cast<uint2 *>(dst + D)[lane] = make_uint2(lo[0], lo[1]);
-    if (lane == 0) p.qsc[r0 + r] = ldexpf(1.0f, e);
-  }
+  // (a CTA without rows: R's copy must land before it ends)
+  if (!have_r && threadIdx.x == 0) (void)mbar_wait_bounded(&sm.full, 0, WAIT_LIMIT_NS);
 }
 
 // ------------------------------------------------------------------------------ attention
@@ -932,8 +1000,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       }
       const float fo = l == 0.f ? 0.f : p.inv_vscale / l;
       const float am = amax * fo;
-      const int ex = (am > 0.f && isfinite(am)) ? ilogbf(am) - 13 : 0;
-      const float mul = ldexpf(fo * fw, -ex), back = ldexpf(1.f, ex);
+      const int ex = scale_exp(am);
+      const float mul = fo * fw * pow2i(-ex), back = pow2i(ex);
       const bool zero = done == 0 || fw == 0.f || fo == 0.f;  // O holds nothing (of the row)
 #pragma unroll 1
       for (int c2 = 0; c2 < (LO ? 4 : 2); ++c2) {
@@ -1066,9 +1134,10 @@ struct JoinParams {
   const float *split;
 };
 constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_FLY = 4;  // parts in flight per warp
 
 // CTA (c, i): rows of the unit whose second share is CTA c's, a warp per row (per pair):
-// o = sum w_s o_s / sum w_s with w_s = l_s 2^(m_s - m*), four partials in flight.
+// o = sum w_s o_s / sum w_s with w_s = l_s 2^(m_s - m*), JOIN_FLY partials in flight.
 __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const JoinParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
@@ -1088,19 +1157,22 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const JoinParams
     float ms = -INFINITY, ls = 0.f;
     a[m][0] = a[m][1] = a[m][2] = a[m][3] = 0.f;
     if (m && !diff) break;
-    for (int s0 = 0; s0 < ns; s0 += 4) {
-      float mx[4], lx[4];
-      float4 v[4];
+    for (int s0 = 0; s0 < ns; s0 += JOIN_FLY) {
+      float mx[JOIN_FLY], lx[JOIN_FLY];
+      float4 v[JOIN_FLY];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int s = min(s0 + i, ns - 1);
-        const float *src = p.split + ((size_t)((j.first + s) * 2 + (s == 0 ? 1 : 0)) * p.unit_rows + r + m) * SROW;
-        mx[i] = __ldcg(src + D), lx[i] = __ldcg(src + D + 1);
-        v[i] = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
+      for (int i = 0; i < JOIN_FLY; ++i) {
+        const int s = s0 + i;
+        mx[i] = lx[i] = 0.f, v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s < ns) {
+          const float *src = p.split + ((size_t)((j.first + s) * 2 + (s == 0 ? 1 : 0)) * p.unit_rows + r + m) * SROW;
+          mx[i] = __ldcg(src + D), lx[i] = __ldcg(src + D + 1);
+          v[i] = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (s0 + i >= ns || lx[i] == 0.f) continue;
+      for (int i = 0; i < JOIN_FLY; ++i) {
+        if (lx[i] == 0.f) continue;
         const float mn = fmaxf(ms, mx[i]), f = exp2f(ms - mn), wx = lx[i] * exp2f(mx[i] - mn);
         ms = mn;
         ls = fmaf(ls, f, wx);
@@ -1183,7 +1255,11 @@ cudaError_t launch_paged_prefill(const tq_ctx *k, const tq_ctx *v, const PagedVi
   a.join = reinterpret_cast<JoinInfo *>(base + l.join);
   a.lo = l.lo;
   const int64_t rows = (int64_t)pv.n_tokens * Hq;
-  cudaError_t e = launch_pdl(k_paged_prep, dim3(1 + (unsigned)((rows + PREP_ROWS - 1) / PREP_ROWS)), dim3(256), 0, st, a);
+  cudaError_t e = kernel_smem_attr((const void *)k_paged_prep, (int)sizeof(PrepSmem));
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (rows + 15) / 16, most = k->num_sms - 1;
+  e = launch_pdl(k_paged_prep, dim3(1 + (unsigned)(tiles < most ? tiles : most)), dim3(PREP_WARPS * 32), sizeof(PrepSmem),
+                 st, a);
   if (e != cudaSuccess) return e;
   PrefillParams p{};
   p.pv = pv, p.kp = kp, p.vp = vp, p.o = o;

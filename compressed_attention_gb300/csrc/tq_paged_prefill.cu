@@ -174,7 +174,7 @@ __device__ __forceinline__ bool next_item(const PrefillParams &p, Walk &w, Item 
 }
 
 // ------------------------------------------------------------------------------ preparation
-constexpr int PREP_WARPS = 16;
+constexpr int PREP_WARPS = 20;
 struct PrepParams {
   PagedView pv;
   RowsView q;
@@ -191,7 +191,6 @@ struct PrepParams {
   int lo;                 // also write the lo parts
 };
 
-constexpr int PREP_PITCH = D + 8;
 
 // Virtual tiles of query tile qt of s (0 past its end), one head.
 __device__ __forceinline__ int unit_vtiles(const Seq &s, int qt, int qpu) {
@@ -332,12 +331,12 @@ __device__ __forceinline__ uint4 ldmatrix_x4(const void *row) {
 // CTA 0 plans; in the others each warp takes tiles of 16 q rows by itself: loaded in rows, turned
 // by position, split into bf16 parts in the warp's own shared memory, multiplied by R (three
 // products of parts) and stored from the product's fragments.  R's fragments (64 KB) lie in shared
-// memory once per SM, from one bulk copy ahead of the wait.  16 warps of their own pace hide each
+// memory once per SM, from one bulk copy ahead of the wait.  20 warps of their own pace hide each
 // other's latencies; blocks of 64 rows that eight warps shared, with barriers between the steps,
 // took 36 us for 47488 rows.
 struct PrepSmem {
   uint4 r[2][8][8][32];  // R, bf16 hi and lo
-  alignas(16) uint16_t xs[PREP_WARPS][2][16][PREP_PITCH];  // a warp's rows, bf16 hi and lo
+  uint16_t xs[PREP_WARPS][2][16][D];  // a warp's rows, bf16 hi and lo; 16-byte chunk c of row r at c ^ (r % 8)
   uint64_t full;
 };
 
@@ -366,54 +365,68 @@ __global__ void __launch_bounds__(PREP_WARPS * 32) k_paged_prep(const PrepParams
   // tiles over the CTAs first: a few rows use as many SMs as they can
   for (int64_t tile = (int64_t)warp * ctas + blockIdx.x - 1; tile * 16 < n; tile += (int64_t)PREP_WARPS * ctas) {
     const int64_t r0 = tile * 16;
-    int my_tok = -1, my_pos = -1;  // of row r0 + lane
+    int my_tok = -1, my_pos = -1;  // of row r0 + lane, and its address (0: no key)
+    uint64_t my_src = 0;
     if (lane < 16 && r0 + lane < n) {
       my_tok = (int)((uint32_t)(r0 + lane) / (uint32_t)p.Hq);
       const int b = paged_seq(p.pv, my_tok);
       my_pos = paged_pos(p.pv, b, my_tok, paged_len(p.pv, b, false));
+      const int h = (int)(r0 + lane - (int64_t)my_tok * p.Hq);
+      if (my_pos >= 0) my_src = (uint64_t)(uintptr_t)(p.q.data + my_tok * p.q.token_bytes + h * p.q.head_bytes);
     }
+    for (uint32_t m = __ballot_sync(FULL_MASK, my_tok >= 0 && my_pos < 0); m; m &= m - 1) {  // no key: the row's output is zero
+      const int64_t r = r0 + __ffs(m) - 1;
+      const float z[4] = {0.f, 0.f, 0.f, 0.f};
+      if (!p.o.diff.lambda) store_lane4(p.o.out, p.o.dtype, (size_t)r * D, lane, z);
+      else if (!(r & 1)) store_lane4(p.o.out, p.o.dtype, (size_t)(r >> 1) * D, lane, z);  // Hq is even
+    }
+    int my_turn = 0;
+    if (p.rope.rot_dim) my_turn = rope_pos(p.rope, my_pos, p.pv.status, true);
     __syncwarp();  // the last tile's fragments are read
     constexpr int NR = 8;
 #pragma unroll 1
     for (int rb = 0; rb < 16; rb += NR) {  // eight rows' loads in flight
       const uint8_t *src[NR];
-      int pos[NR];
       float x[NR][4];
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const int tok = __shfl_sync(FULL_MASK, my_tok, rb + i), h = (int)(r0 + rb + i - (int64_t)max(tok, 0) * p.Hq);
-        pos[i] = __shfl_sync(FULL_MASK, my_pos, rb + i);
-        src[i] = pos[i] >= 0 ? p.q.data + tok * p.q.token_bytes + h * p.q.head_bytes : nullptr;
-        if (tok >= 0 && pos[i] < 0) {  // no key: the row's output is zero
-          const float z[4] = {0.f, 0.f, 0.f, 0.f};
-          if (!p.o.diff.lambda) store_lane4(p.o.out, p.o.dtype, (size_t)(r0 + rb + i) * D, lane, z);
-          else if (!(h & 1)) store_lane4(p.o.out, p.o.dtype, ((size_t)tok * (p.Hq / 2) + h / 2) * D, lane, z);
-        }
-      }
-      load_rows(src, p.q.dtype, lane, x);
+      for (int i = 0; i < NR; ++i)
+        src[i] = reinterpret_cast<const uint8_t *>((uintptr_t)__shfl_sync(FULL_MASK, my_src, rb + i));
       if (p.rope.rot_dim) {
-        LaneAngles an;
+        const int turn = __shfl_sync(FULL_MASK, my_turn, rb);
+        // the heads of a token share its angles
+        if (__all_sync(FULL_MASK, my_turn == turn || (lane & 8) != rb || lane >= 16)) {
+          const LaneAngles an = rope_angles(lane, p.rope, turn);
+          load_rows(src, p.q.dtype, lane, x);
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          if (i == 0 || pos[i] != pos[i - 1])  // the heads of a token share its angles
-            an = rope_angles(lane, p.rope, rope_pos(p.rope, pos[i], p.pv.status, lane == 0));
-          rope_turn(x[i], lane, p.rope, an);
+          for (int i = 0; i < NR; ++i) rope_turn(x[i], lane, p.rope, an);
+        } else {
+          load_rows(src, p.q.dtype, lane, x);
+#pragma unroll
+          for (int i = 0; i < NR; ++i)
+            rope_turn(x[i], lane, p.rope, rope_angles(lane, p.rope, __shfl_sync(FULL_MASK, my_turn, rb + i)));
         }
+      } else {
+        load_rows(src, p.q.dtype, lane, x);
       }
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         uint32_t hi[2], lo[2];
+        float f[4];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          const __nv_bfloat162 a = __floats2bfloat162_rn(x[i][2 * m], x[i][2 * m + 1]);
-          const float2 f = __bfloat1622float2(a);
-          const __nv_bfloat162 c = __floats2bfloat162_rn(isinf(f.x) ? 0.f : x[i][2 * m] - f.x,
-                                                         isinf(f.y) ? 0.f : x[i][2 * m + 1] - f.y);
-          hi[m] = *reinterpret_cast<const uint32_t *>(&a);
-          lo[m] = *reinterpret_cast<const uint32_t *>(&c);
+          hi[m] = pack_bf162(x[i][2 * m], x[i][2 * m + 1]);
+          f[2 * m] = __uint_as_float(hi[m] << 16), f[2 * m + 1] = __uint_as_float(hi[m] & 0xFFFF0000u);
         }
-        *reinterpret_cast<uint2 *>(&xs[0][rb + i][4 * lane]) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2 *>(&xs[1][rb + i][4 * lane]) = make_uint2(lo[0], lo[1]);
+        const float big = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+        if (big == INFINITY) {  // an infinite part has no rest
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][e] = isinf(f[e]) ? f[e] = 0.f : x[i][e];
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) lo[m] = pack_bf162(x[i][2 * m] - f[2 * m], x[i][2 * m + 1] - f[2 * m + 1]);
+        const int at = 8 * ((lane >> 1) ^ i) + 4 * (lane & 1);  // NR rows: i is the row modulo 8
+        *reinterpret_cast<uint2 *>(&xs[0][rb + i][at]) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2 *>(&xs[1][rb + i][at]) = make_uint2(lo[0], lo[1]);
       }
     }
     __syncwarp();
@@ -433,7 +446,7 @@ __global__ void __launch_bounds__(PREP_WARPS * 32) k_paged_prep(const PrepParams
     for (int s = 0; s < 8; ++s) {
       uint4 a[2];
 #pragma unroll
-      for (int part = 0; part < 2; ++part) a[part] = ldmatrix_x4(&xs[part][lane & 15][16 * s + 8 * (lane >> 4)]);
+      for (int part = 0; part < 2; ++part) a[part] = ldmatrix_x4(&xs[part][lane & 15][8 * ((2 * s + (lane >> 4)) ^ (lane & 7))]);
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
         const uint4 rh = sm.r[0][m][s][lane], rl = sm.r[1][m][s][lane];
@@ -466,12 +479,18 @@ __global__ void __launch_bounds__(PREP_WARPS * 32) k_paged_prep(const PrepParams
       const int e = as_is ? 0 : scale_exp(m);
       const float down = pow2i(-e);
       uint16_t *dst = p.qh + (size_t)r * 2 * D;
+      if (p.lo) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        uint32_t hi, lo;
-        split_half2(acc[j][2 * i] * down, acc[j][2 * i + 1] * down, hi, lo);
-        *reinterpret_cast<uint32_t *>(dst + 8 * j + 2 * t) = hi;
-        if (p.lo) *reinterpret_cast<uint32_t *>(dst + D + 8 * j + 2 * t) = lo;
+        for (int j = 0; j < 16; ++j) {
+          uint32_t hi, lo;
+          split_half2(acc[j][2 * i] * down, acc[j][2 * i + 1] * down, hi, lo);
+          *reinterpret_cast<uint32_t *>(dst + 8 * j + 2 * t) = hi;
+          *reinterpret_cast<uint32_t *>(dst + D + 8 * j + 2 * t) = lo;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          *reinterpret_cast<uint32_t *>(dst + 8 * j + 2 * t) = pack_half2(acc[j][2 * i] * down, acc[j][2 * i + 1] * down);
       }
       if (t == 0) p.qsc[r] = pow2i(e);
     }

@@ -76,6 +76,11 @@ struct Misc {
   // every group has finished tile j.  2^7 value norms of the two V stages.
   alignas(16) float kn[4][KT];
   alignas(16) float nv[2][KT];
+  // One part: the norms are in the operands, and these hold for 32 rows of a K tile its power of two, and
+  // for 32 of a V tile log2 of its power (+ P_SHIFT), 2^- of that, and the rows whose norm is not finite.
+  float ks[4][KT / 32];
+  float ve[2][KT / 32], vi[2][KT / 32];
+  uint32_t vbad[2][KT / 32];
   float xm[2][128], xl[2][128], xa[2][128];  // alternating groups: max, sum, largest |O| of a row
   uint32_t tmem;
   int abort_flag;
@@ -105,6 +110,8 @@ struct PrefillParams {
   float inv_vscale;            // 1 / (2^P_SHIFT * alpha_V)
   const uint8_t *vr;           // R of the values as fp16 hi, lo tile images
 };
+// Norms in the operands: up to 2^13 times a scaled centroid (below 4) stays below 2^15.
+constexpr int NORM_EXP = 12;
 constexpr int SROW = D + 4;    // floats of a partial row: o[128], max, sum, 2 spare
 
 // ------------------------------------------------------------------------------ schedule
@@ -638,15 +645,48 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
         if (!ok) break;
         const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + OFF_RAW + rs * RAW + row * PG_ROW);
         uint8_t *dst = stages + st * SW_TILE_BYTES;
-        const float norm = __uint_as_float(src[0]);
+        const float norm = live ? __uint_as_float(src[0]) : 0.f;
+        if constexpr (LO) {
 #pragma unroll
-        for (int ch = 0; ch < 16; ++ch) {
-          uint32_t d[4];
-          decode8<0x5140u, 0x7362u>(src[1 + ch], lo2, hi2, d);
-          *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 8 * ch)) = make_uint4(d[0], d[1], d[2], d[3]);
+          for (int ch = 0; ch < 16; ++ch) {
+            uint32_t d[4];
+            decode8<0x5140u, 0x7362u>(src[1 + ch], lo2, hi2, d);
+            *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 8 * ch)) = make_uint4(d[0], d[1], d[2], d[3]);
+          }
+          if (side) ms.nv[st][row] = norm * 128.0f;
+          else ms.kn[c & 3][row] = norm;
+        } else {
+          // The norm goes into the operand: x (nh + nl), the norm as two fp16 parts after the power of
+          // two that brings the largest of the warp's 32 rows to [2^NORM_EXP, 2^(NORM_EXP + 1)).  One
+          // rounding an element, like q's and P's; a norm 2^20 times smaller than the largest keeps
+          // its precision.
+          const float an = fabsf(norm);
+          const bool bad = !(an < INFINITY);
+          const uint32_t most = __reduce_max_sync(FULL_MASK, bad ? 0u : __float_as_uint(an));
+          const int em = max((int)(most >> 23) - 127, side ? -64 : -114);
+          const float sn = side && bad ? 0.f : norm * pow2i(NORM_EXP - em);
+          const __half nh = __float2half_rn(sn), nl = __float2half_rn(sn - __half2float(nh));
+          const __half2 nh2 = __half2half2(nh), nl2 = __half2half2(nl);
+#pragma unroll 4
+          for (int ch = 0; ch < 16; ++ch) {
+            uint32_t d[4];
+            decode8<0x5140u, 0x7362u>(src[1 + ch], lo2, hi2, d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 x = *reinterpret_cast<const __half2 *>(&d[e]), y = __hfma2(x, nh2, __hmul2(x, nl2));
+              d[e] = *reinterpret_cast<const uint32_t *>(&y);
+            }
+            *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 8 * ch)) = make_uint4(d[0], d[1], d[2], d[3]);
+          }
+          const uint32_t bads = __ballot_sync(FULL_MASK, bad);
+          const int blk = warp & 3;
+          if (lane == 0) {
+            // a value of no finite norm: zeros here, so that rows that do not see it stay clean; the
+            // softmax makes the others NaN
+            if (side) ms.ve[st][blk] = (float)em + P_SHIFT, ms.vi[st][blk] = pow2i(-em) * exp2f(-P_SHIFT), ms.vbad[st][blk] = bads;
+            else ms.ks[c & 3][blk] = pow2i(em - NORM_EXP);
+          }
         }
-        if (side) ms.nv[st][row] = live ? norm * 128.0f : 0.f;
-        else ms.kn[c & 3][row] = live ? norm : 0.f;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]), mbar_arrive(&ms.raw_empty[rs]);
@@ -815,8 +855,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       const int64_t qrow = brow * p.Hq + head;
       const int pos = live ? it.s.base + qi : -1;
       const float rsc = live ? p.qsc[qrow] : 0.f;
-      const uint64_t rsc2 = pk2(rsc, rsc);
-      const bool scaled = __any_sync(FULL_MASK, live && rsc != 1.f);
+      [[maybe_unused]] const uint64_t rsc2 = pk2(rsc, rsc);
       if (!ALT || LO || gr == 0) {
         const uint4 *src = reinterpret_cast<const uint4 *>(p.qh + (size_t)qrow * 2 * D + (LO ? gr * D : 0));
         uint8_t *dst = smem + OFF_Q + gr * SW_TILE_BYTES;
@@ -843,24 +882,39 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
         ok = __all_sync(FULL_MASK, ok);
         if (!ok) break;
         tc_fence_after();
-        const float4 *kn4 = reinterpret_cast<const float4 *>(ms.kn[(kc + i) & 3]) + 16 * h;
-        const float4 *nv4 = reinterpret_cast<const float4 *>(ms.nv[cv & 1]) + 16 * h;
+        [[maybe_unused]] const float4 *kn4 = reinterpret_cast<const float4 *>(ms.kn[(kc + i) & 3]) + 16 * h;
+        [[maybe_unused]] const float4 *nv4 = reinterpret_cast<const float4 *>(ms.nv[cv & 1]) + 16 * h;
         const bool full = kf + 63 <= it.s.base + q0;  // every row sees every key of the half
-        // the largest s + log2(value norm) of the row
+        // the largest s + log2(value norm, or the power of two in its operand) of the row
         auto row_max = [&]() -> float {
           float bm = -INFINITY;
+          if constexpr (!LO) {
 #pragma unroll 1
-          for (int cc = 0; cc < 2; ++cc) {
-            float sv[32];
-            tmem_ld32(tH + 32 * cc, sv);
+            for (int cc = 0; cc < 2; ++cc) {
+              float sv[32];
+              tmem_ld32(tH + 32 * cc, sv);
+              const float k = ms.ks[(kc + i) & 3][2 * h + cc] * rsc, v = ms.ve[cv & 1][2 * h + cc] - P_SHIFT;
+              const int seen = full ? 32 : pos - (kf + 32 * cc) + 1;
 #pragma unroll
-            for (int c4 = 0; c4 < 8; ++c4) {
-              const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
-              const float k_[4] = {kn.x, kn.y, kn.z, kn.w}, v_[4] = {nv.x, nv.y, nv.z, nv.w};
+              for (int e = 0; e < 32; ++e) {
+                const float u = fmaf(sv[e], k, v);
+                if (e < seen) bm = fmaxf(bm, u);
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int cc = 0; cc < 2; ++cc) {
+              float sv[32];
+              tmem_ld32(tH + 32 * cc, sv);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float u = fmaf(sv[4 * c4 + e] * k_[e], rsc, fmaxf(log2_approx(v_[e]) - P_SHIFT, -64.f));
-                if (full || kf + 32 * cc + 4 * c4 + e <= pos) bm = fmaxf(bm, u);
+              for (int c4 = 0; c4 < 8; ++c4) {
+                const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
+                const float k_[4] = {kn.x, kn.y, kn.z, kn.w}, v_[4] = {nv.x, nv.y, nv.z, nv.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float u = fmaf(sv[4 * c4 + e] * k_[e], rsc, fmaxf(log2_approx(v_[e]) - P_SHIFT, -64.f));
+                  if (full || kf + 32 * cc + 4 * c4 + e <= pos) bm = fmaxf(bm, u);
+                }
               }
             }
           }
@@ -890,27 +944,26 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
             }
           }
         };
-        // two columns: exponentials into l2, probabilities as fp32.  Tiles that every row sees whole,
-        // with rows that carry no scale, take the short version.
-        uint64_t l2;
-        auto pair = [&](auto whole, float s0, float s1, float k0, float k1, float v0, float v1, int c, uint64_t nm2,
-                        float &p0, float &p1) {
-          const uint64_t sk2 = LO || !decltype(whole)::value ? mul2(pk2(s0, s1), rsc2) : pk2(s0, s1);
-          float d0, d1;
-          upk2(fma2(sk2, pk2(k0, k1), nm2), d0, d1);
-          float e0 = exp2_approx(d0), e1 = exp2_approx(d1);
-          if constexpr (!decltype(whole)::value) e0 = kf + c <= pos ? e0 : 0.f, e1 = kf + c + 1 <= pos ? e1 : 0.f;
-          const uint64_t e2 = pk2(e0, e1);
-          l2 = add2(l2, e2);
-          upk2(mul2(e2, pk2(v0, v1)), p0, p1);
-          // a masked value norm may be anything
-          if constexpr (!decltype(whole)::value) p0 = kf + c <= pos ? p0 : 0.f, p1 = kf + c + 1 <= pos ? p1 : 0.f;
-        };
+        float lsum;
         if constexpr (LO) {
           raise_max(false);
           const float Mu = (M == -INFINITY) ? 0.f : M;
           const uint64_t nm2 = pk2(-Mu, -Mu);
-          l2 = pk2(0.f, 0.f);
+          uint64_t l2 = pk2(0.f, 0.f);
+          // two columns: exponentials into l2, probabilities as fp32; short where every row sees all
+          auto pair = [&](auto whole, float s0, float s1, float k0, float k1, float v0, float v1, int c, uint64_t nm2,
+                          float &p0, float &p1) {
+            const uint64_t sk2 = mul2(pk2(s0, s1), rsc2);
+            float d0, d1;
+            upk2(fma2(sk2, pk2(k0, k1), nm2), d0, d1);
+            float e0 = exp2_approx(d0), e1 = exp2_approx(d1);
+            if constexpr (!decltype(whole)::value) e0 = kf + c <= pos ? e0 : 0.f, e1 = kf + c + 1 <= pos ? e1 : 0.f;
+            const uint64_t e2 = pk2(e0, e1);
+            l2 = add2(l2, e2);
+            upk2(mul2(e2, pk2(v0, v1)), p0, p1);
+            // a masked value norm may be anything
+            if constexpr (!decltype(whole)::value) p0 = kf + c <= pos ? p0 : 0.f, p1 = kf + c + 1 <= pos ? p1 : 0.f;
+          };
           auto two_parts = [&](auto whole) {
 #pragma unroll 1
             for (int cc = 0; cc < 2; ++cc) {
@@ -931,49 +984,58 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           };
           if (full) two_parts(std::true_type());
           else two_parts(std::false_type());
+          float l0, l1;
+          upk2(l2, l0, l1);
+          lsum = l0 + l1;
         } else {
           uint32_t pw[32];
           bool need = live && M == -INFINITY && kf <= pos;
           for (int turn = 0;; ++turn) {
             if (__any_sync(FULL_MASK, need)) raise_max(need);
             const float Mu = (M == -INFINITY) ? 0.f : M;
-            const uint64_t nm2 = pk2(-Mu, -Mu);
-            l2 = pk2(0.f, 0.f);
-            uint64_t ps2 = pk2(0.f, 0.f);
+            float ps = 0.f;
+            lsum = 0.f;
             auto one_part = [&](auto whole) {
 #pragma unroll
               for (int cc = 0; cc < 2; ++cc) {
                 float sv[32];
                 tmem_ld32(tH + 32 * cc, sv);
+                const float k = ms.ks[(kc + i) & 3][2 * h + cc] * rsc, mv = ms.ve[cv & 1][2 * h + cc] - Mu;
+                const uint64_t k2 = pk2(k, k), mv2 = pk2(mv, mv);
+                const int seen = pos - (kf + 32 * cc) + 1;  // keys of the 32 that the row sees
+                uint64_t ps2[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
 #pragma unroll
-                for (int c4 = 0; c4 < 8; ++c4) {
-                  const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
-                  const int c = 32 * cc + 4 * c4;
-                  float p0, p1;
-                  pair(whole, sv[4 * c4], sv[4 * c4 + 1], kn.x, kn.y, nv.x, nv.y, c, nm2, p0, p1);
-                  pw[c / 2] = pack_half2(p0, p1);
-                  ps2 = add2(ps2, pk2(p0, p1));
-                  pair(whole, sv[4 * c4 + 2], sv[4 * c4 + 3], kn.z, kn.w, nv.z, nv.w, c + 2, nm2, p0, p1);
-                  pw[c / 2 + 1] = pack_half2(p0, p1);
-                  ps2 = add2(ps2, pk2(p0, p1));
+                for (int c = 0; c < 32; c += 2) {
+                  float d0, d1;
+                  upk2(fma2(pk2(sv[c], sv[c + 1]), k2, mv2), d0, d1);
+                  float p0 = exp2_approx(d0), p1 = exp2_approx(d1);
+                  if constexpr (!decltype(whole)::value) p0 = c < seen ? p0 : 0.f, p1 = c + 1 < seen ? p1 : 0.f;
+                  pw[16 * cc + c / 2] = pack_half2(p0, p1);
+                  ps2[(c >> 1) & 1] = add2(ps2[(c >> 1) & 1], pk2(p0, p1));
                 }
+                float p0, p1;
+                upk2(add2(ps2[0], ps2[1]), p0, p1);
+                p0 += p1;
+                ps += p0;
+                lsum = fmaf(p0, ms.vi[cv & 1][2 * h + cc], lsum);
               }
             };
-            if (full && !scaled) one_part(std::true_type());
+            if (full) one_part(std::true_type());
             else one_part(std::false_type());
-            // A probability past 2^15 shows in their sum (at most 2^13 under the current maximum):
-            // one packed add a pair, where a maximum would take the slower ALU.  The redo then takes
-            // the tile's own maximum.
-            float ps0, ps1;
-            upk2(ps2, ps0, ps1);
-            need = live && !(ps0 + ps1 <= 32768.f);
+            // A probability past 2^15 shows in their sum (at most 2^13 under the current maximum): a
+            // maximum would take the slower ALU.  The redo then takes the tile's own maximum.
+            need = live && !(ps <= 32768.f);
             if (turn || !__any_sync(FULL_MASK, need)) break;
+          }
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            const uint32_t bad = ms.vbad[cv & 1][2 * h + cc];
+            const int seen = pos - (kf + 32 * cc) + 1;
+            if (bad && seen > 0 && (bad & (0xFFFFFFFFu >> (32 - min(seen, 32))))) lsum = NAN;
           }
           tmem_st32(tH, pw);
         }
-        float l0, l1;
-        upk2(l2, l0, l1);
-        l += l0 + l1;
+        l += lsum;
         tc_fence_before();
         if (!ok) break;  // (a failed wait while raising the maximum)
         __syncwarp();
@@ -1289,7 +1351,7 @@ cudaError_t launch_paged_prefill(const tq_ctx *k, const tq_ctx *v, const PagedVi
     p.klo[i] = k->f16.lo[i], p.khi[i] = k->f16.hi[i];
     p.vlo[i] = v->f16.lo[i], p.vhi[i] = v->f16.hi[i];
   }
-  p.inv_vscale = 1.0f / (exp2f(P_SHIFT) * v->f16.alpha);
+  p.inv_vscale = 1.0f / (exp2f(P_SHIFT + (l.lo ? 0 : NORM_EXP)) * v->f16.alpha);
   p.vr = reinterpret_cast<const uint8_t *>(v->d_rtile);
   e = l.lo ? launch_main<true, true>(p, l.grid, st)
            : (l.alt ? launch_main<true, false>(p, l.grid, st) : launch_main<false, false>(p, l.grid, st));

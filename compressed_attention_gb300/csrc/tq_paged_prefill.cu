@@ -54,10 +54,10 @@ constexpr int RAW = KT * PG_ROW;       // a packed tile
 constexpr int NRAW = 3;
 constexpr int W_DEC = 8, W_MMA = 16, W_LOAD = 18, N_WARPS = 20;  // the last warp only fills its group
 constexpr int THREADS = N_WARPS * 32;
-// Registers: 640 threads x 96 at launch; the softmax groups take 144 (64 scores, 32 packed
-// probabilities and the norms of several columns in flight), the other three groups give theirs
-// up to 64: 256 * 144 + 384 * 64 = 640 * 96.
-constexpr int REGS_LAUNCH = 96, REGS_SOFTMAX = 144, REGS_OTHER = 64;
+// Registers: 640 threads x 96 at launch; the softmax groups take 128 (64 scores, 32 packed
+// probabilities), the other three groups give theirs up to 72 (the decoders' 17 words of a row
+// and norm parts): 256 * 128 + 384 * 72 <= 640 * 96.  144 and 64 spilled in the issuers.
+constexpr int REGS_LAUNCH = 96, REGS_SOFTMAX = 128, REGS_OTHER = 72;
 static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "the launch's registers");
 constexpr uint32_t IDESC_S = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);  // fp16, M = 128, N = 64
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // S / P of the groups, O of the groups
@@ -77,9 +77,9 @@ struct Misc {
   alignas(16) float kn[4][KT];
   alignas(16) float nv[2][KT];
   // One part: the norms are in the operands, and these hold for 32 rows of a K tile its power of two, and
-  // for 32 of a V tile log2 of its power (+ P_SHIFT), 2^- of that, and the rows whose norm is not finite.
-  float ks[4][KT / 32];
-  float ve[2][KT / 32], vi[2][KT / 32];
+  // for 32 of a V tile log2 of its power (+ P_SHIFT), 2^- of that (negative: some norms are not finite), and the rows of those.
+  alignas(8) float ks[4][KT / 32];
+  alignas(8) float ve[2][KT / 32], vi[2][KT / 32];
   uint32_t vbad[2][KT / 32];
   float xm[2][128], xl[2][128], xa[2][128];  // alternating groups: max, sum, largest |O| of a row
   uint32_t tmem;
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           const float sn = side && bad ? 0.f : norm * pow2i(NORM_EXP - em);
           const __half nh = __float2half_rn(sn), nl = __float2half_rn(sn - __half2float(nh));
           const __half2 nh2 = __half2half2(nh), nl2 = __half2half2(nl);
-#pragma unroll 4
+#pragma unroll
           for (int ch = 0; ch < 16; ++ch) {
             uint32_t d[4];
             decode8<0x5140u, 0x7362u>(src[1 + ch], lo2, hi2, d);
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           if (lane == 0) {
             // a value of no finite norm: zeros here, so that rows that do not see it stay clean; the
             // softmax makes the others NaN
-            if (side) ms.ve[st][blk] = (float)em + P_SHIFT, ms.vi[st][blk] = pow2i(-em) * exp2f(-P_SHIFT), ms.vbad[st][blk] = bads;
+            if (side) ms.ve[st][blk] = (float)em + P_SHIFT, ms.vi[st][blk] = (bads ? -1.f : 1.f) * pow2i(-em) * exp2f(-P_SHIFT), ms.vbad[st][blk] = bads;
             else ms.ks[c & 3][blk] = pow2i(em - NORM_EXP);
           }
         }
@@ -989,6 +989,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           lsum = l0 + l1;
         } else {
           uint32_t pw[32];
+          const float2 vi2 = *reinterpret_cast<const float2 *>(&ms.vi[cv & 1][2 * h]);
+          const float vi[2] = {vi2.x, vi2.y};
+          const float2 ve2 = *reinterpret_cast<const float2 *>(&ms.ve[cv & 1][2 * h]);
+          const float2 ks2 = *reinterpret_cast<const float2 *>(&ms.ks[(kc + i) & 3][2 * h]);
+          const float ve[2] = {ve2.x, ve2.y}, ks[2] = {ks2.x, ks2.y};
           bool need = live && M == -INFINITY && kf <= pos;
           for (int turn = 0;; ++turn) {
             if (__any_sync(FULL_MASK, need)) raise_max(need);
@@ -996,18 +1001,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
             float ps = 0.f;
             lsum = 0.f;
             auto one_part = [&](auto whole) {
+              uint32_t sw[2][32];
 #pragma unroll
               for (int cc = 0; cc < 2; ++cc) {
-                float sv[32];
-                tmem_ld32(tH + 32 * cc, sv);
-                const float k = ms.ks[(kc + i) & 3][2 * h + cc] * rsc, mv = ms.ve[cv & 1][2 * h + cc] - Mu;
+                if (!cc) {
+                  tmem_ld32_start(tH, sw[0]);
+                  tmem_ld32_wait(sw[0]);
+                  tmem_ld32_start(tH + 32, sw[1]);
+                } else {
+                  tmem_ld32_wait(sw[1]);
+                }
+                const float k = ks[cc] * rsc, mv = ve[cc] - Mu;
                 const uint64_t k2 = pk2(k, k), mv2 = pk2(mv, mv);
                 const int seen = pos - (kf + 32 * cc) + 1;  // keys of the 32 that the row sees
                 uint64_t ps2[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
                   float d0, d1;
-                  upk2(fma2(pk2(sv[c], sv[c + 1]), k2, mv2), d0, d1);
+                  upk2(fma2(pk2(__uint_as_float(sw[cc][c]), __uint_as_float(sw[cc][c + 1])), k2, mv2), d0, d1);
                   float p0 = exp2_approx(d0), p1 = exp2_approx(d1);
                   if constexpr (!decltype(whole)::value) p0 = c < seen ? p0 : 0.f, p1 = c + 1 < seen ? p1 : 0.f;
                   pw[16 * cc + c / 2] = pack_half2(p0, p1);
@@ -1017,7 +1028,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
                 upk2(add2(ps2[0], ps2[1]), p0, p1);
                 p0 += p1;
                 ps += p0;
-                lsum = fmaf(p0, ms.vi[cv & 1][2 * h + cc], lsum);
+                lsum = fmaf(p0, fabsf(vi[cc]), lsum);
               }
             };
             if (full) one_part(std::true_type());
@@ -1029,9 +1040,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           }
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
+            if (vi[cc] > 0.f) continue;  // values without a finite norm among the 32
             const uint32_t bad = ms.vbad[cv & 1][2 * h + cc];
             const int seen = pos - (kf + 32 * cc) + 1;
-            if (bad && seen > 0 && (bad & (0xFFFFFFFFu >> (32 - min(seen, 32))))) lsum = NAN;
+            if (seen > 0 && (bad & (0xFFFFFFFFu >> (32 - min(seen, 32))))) lsum = NAN;
           }
           tmem_st32(tH, pw);
         }

@@ -326,15 +326,6 @@ __device__ __forceinline__ void load_rows(const uint8_t *const (&row)[N], int dt
   }
 }
 
-__device__ __forceinline__ uint4 ldmatrix_x4(const void *row) {
-  uint4 r;
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "r"((uint32_t)__cvta_generic_to_shared(row))
-               : "memory");
-  return r;
-}
-
 // CTA 0 plans; in the others each warp takes tiles of 16 q rows by itself: loaded in rows, turned
 // by position, split into bf16 parts in the warp's own shared memory, multiplied by R (three
 // products of parts) and stored from the product's fragments.  R's fragments (64 KB) lie in shared

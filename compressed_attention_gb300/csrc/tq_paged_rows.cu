@@ -7,8 +7,10 @@
 // pairs (j, j + 64) and (j, j + 32) and adjacent pairs lie inside one thread's chunks;
 // pairs (j, j + 16) cross to the thread two over.  A CTA takes keys or values, so it keeps one
 // codebook grid.
+#include "tq_decode_common.cuh"
 #include "tq_paged.cuh"
 #include "tq_qprep.cuh"
+#include "tq_rotmma.cuh"
 #include "tq_wht.cuh"
 
 namespace tq {
@@ -21,7 +23,8 @@ struct AppendSide {
   uint32_t wht_neg[4];
   float b[15];
   const BucketTable *bt;
-  const float *pit;  // dense: R^T, fp32
+  const uint4 *rfrag;  // dense: R as bf16 hi + lo fragments
+  const float *pit;    // dense: R^T, fp32
 };
 struct AppendParams {
   PagedView pv;
@@ -179,17 +182,206 @@ __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendPar
   }
 }
 
-// Dense rotation: a warp per row, R^T staged once per CTA.
-constexpr int AD_WARPS = 8;
-constexpr size_t AD_SMEM = (size_t)D * D * 4 + AD_WARPS * D * 4;
+// Dense rotation on the tensor cores: each warp takes tiles of 16 rows by itself.  Rows are loaded
+// and turned by position as in q's preparation, normalised, split into bf16 parts in the warp's
+// shared memory and multiplied by R (fragments of its parts, 64 KB per CTA from one bulk copy).
+// y = R u, |u| = 1, in four products of parts: what the parts drop of u and of R is at most 2^-18
+// of |u| |row of R| each, 7.6e-6 together with the sums' rounding below the 1e-5 within which an
+// index may differ; three products (without lo lo) could reach 1.2e-5.  Lane (g, t) holds columns
+// 8 j + 2 t and the next of rows g and g + 8, one byte of nibbles of word j: the four lanes of a row
+// transpose their bytes and store words.  13.8K tokens of 8 KV heads, keys and values: 134 us, the
+// legacy matrix pipe 40% busy; a warp per row on the CUDA cores took 560 us.
+constexpr int AD_WARPS = 16;
+struct DenseSmem {
+  uint4 r[2][8][8][32];            // R, bf16 hi and lo
+  uint16_t xs[AD_WARPS][2][16][D]; // a warp's rows, bf16 hi and lo; 16-byte chunk c of row r at c ^ (r % 8)
+  WhtTables tb;
+  uint64_t full;
+};
+
+static_assert(sizeof(DenseSmem) <= 227 * 1024, "shared memory budget");
+
+// Four lanes' words of bytes transposed: byte u of lane t's result is byte t of lane u's word.
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t v, int t) {
+  const uint32_t o = __shfl_xor_sync(FULL_MASK, v, 2);
+  v = prmt(v, o, (t & 2) ? 0x3276u : 0x5410u);
+  const uint32_t w = __shfl_xor_sync(FULL_MASK, v, 1);
+  return prmt(v, w, (t & 1) ? 0x3715u : 0x6240u);
+}
+
+template <int DT>
 __global__ void __launch_bounds__(AD_WARPS * 32) k_paged_append_dense(const AppendParams p) {
+  extern __shared__ __align__(128) uint8_t smem_dense[];
+  DenseSmem &sm = *reinterpret_cast<DenseSmem *>(smem_dense);
+  const int side = (int)blockIdx.x < p.k_ctas ? 0 : 1;
+  const int cta = side ? blockIdx.x - p.k_ctas : blockIdx.x, n_cta = side ? gridDim.x - p.k_ctas : p.k_ctas;
+  const AppendSide &sd = p.side[side];
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.full, 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(&sm.full, sizeof(sm.r));
+    bulk_g2s(&sm.r[0][0][0][0], sd.rfrag, sizeof(sm.r), &sm.full);
+  }
+  WhtTables &tb = sm.tb;
+  wht_tables_fill<TQ_FMT_TURBO4>(sd.b, sd.bt, tb);
+  __syncthreads();
+  const bool ok = mbar_wait_bounded(&sm.full, 0, WAIT_LIMIT_NS);
+  pdl_wait();
+  if (!ok) {
+    if (threadIdx.x == 0) atomicExch(p.pv.status, (int32_t)DEVERR_TIMEOUT);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, l16 = lane & 15;
+  const float gs = tb.gs, go = tb.go;
+  const int gn = tb.gn, Hkv = p.pv.Hkv;
+  const bool turn = side == 0 && p.rope.rot_dim;
+  auto &xs = sm.xs[warp];
+  const int64_t n_rows = (int64_t)paged_rows(p.pv) * Hkv;
+  // lane i < 16: the place and source of row i of a tile
+  struct Spot {
+    int64_t at;
+    uint64_t src;
+    int pos;
+  };
+  auto find = [&](int64_t tile) -> Spot {
+    Spot sp{-1, 0, 0};
+    const int64_t r = tile * 16 + lane;
+    if (lane < 16 && r < n_rows) {
+      const int tok = (int)((uint32_t)r / (uint32_t)Hkv), h = (int)(r - (int64_t)tok * Hkv);
+      const Place pl = place_row(p.pv, tok, h, true);
+      sp.at = pl.at, sp.pos = pl.pos;
+      if (pl.at >= 0) sp.src = (uint64_t)(uintptr_t)(sd.src.data + tok * sd.src.token_bytes + h * sd.src.head_bytes);
+    }
+    return sp;
+  };
+  // tiles over the CTAs first: a few rows use as many SMs as they can
+  const int64_t step = (int64_t)AD_WARPS * n_cta;
+  int64_t tile = (int64_t)warp * n_cta + cta;
+  Spot spot = find(tile);
+  for (; tile * 16 < n_rows; tile += step) {
+    const Spot at = spot;
+    const int ang = turn ? rope_pos(p.rope, at.at >= 0 ? at.pos : 0, p.pv.status, true) : 0;
+    __syncwarp();  // the last tile's fragments are read
+    constexpr int NR = 8;
+#pragma unroll 1
+    for (int rb = 0; rb < 16; rb += NR) {  // eight rows' loads in flight
+      float x[NR][4];
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const uint8_t *src = reinterpret_cast<const uint8_t *>((uintptr_t)__shfl_sync(FULL_MASK, at.src, rb + i));
+        if (src) load_lane4(src, DT, lane, x[i]);
+        else x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+      }
+      if (turn) {
+        const int a0 = __shfl_sync(FULL_MASK, ang, rb);
+        if (__all_sync(FULL_MASK, ang == a0 || (lane & 8) != rb || lane >= 16)) {  // one token's heads
+          const LaneAngles an = rope_angles(lane, p.rope, a0);
+#pragma unroll
+          for (int i = 0; i < NR; ++i) rope_turn(x[i], lane, p.rope, an);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NR; ++i)
+            rope_turn(x[i], lane, p.rope, rope_angles(lane, p.rope, __shfl_sync(FULL_MASK, ang, rb + i)));
+        }
+      }
+      // norms in the canonical order of the plain fp32 sequence, a row per four lanes in the end
+      float s[NR];
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+        s[i] = __fadd_rn(__fadd_rn(__fmul_rn(x[i][0], x[i][0]), __fmul_rn(x[i][1], x[i][1])),
+                         __fadd_rn(__fmul_rn(x[i][2], x[i][2]), __fmul_rn(x[i][3], x[i][3])));
+#pragma unroll
+      for (int m = 16, k = 4; m >= 4; m >>= 1, k >>= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+          const float keep = up ? s[i + k] : s[i], give = up ? s[i] : s[i + k];
+          s[i] = __fadd_rn(keep, __shfl_xor_sync(FULL_MASK, give, m));
+        }
+      }
+      s[0] = __fadd_rn(s[0], __shfl_xor_sync(FULL_MASK, s[0], 2));
+      s[0] = __fadd_rn(s[0], __shfl_xor_sync(FULL_MASK, s[0], 1));
+      const float n = __fsqrt_rn(s[0]);  // of row rb + lane / 4
+      const bool tiny = n < 0x1p-100f && n > 0.f;
+      float inv = n >= 0x1p-100f ? __fdiv_rn(1.0f, n) : 0.0f;
+      if (__any_sync(FULL_MASK, tiny)) {  // 1 / n might not be finite: both by 2^64 first
+        if (tiny) inv = __fdiv_rn(1.0f, n * 0x1p64f);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const float f = __shfl_sync(FULL_MASK, tiny ? 0x1p64f : 1.f, 4 * i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][e] *= f;
+        }
+      }
+      const int64_t to = __shfl_sync(FULL_MASK, at.at, rb + (lane >> 2));
+      if (t == 0 && to >= 0) *reinterpret_cast<float *>(sd.pages + to) = n;
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const float r = __shfl_sync(FULL_MASK, inv, 4 * i);
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float u0 = x[i][2 * m] * r, u1 = x[i][2 * m + 1] * r;
+          hi[m] = pack_bf162(u0, u1);
+          lo[m] = pack_bf162(u0 - __uint_as_float(hi[m] << 16), u1 - __uint_as_float(hi[m] & 0xFFFF0000u));
+        }
+        const int c = 8 * ((lane >> 1) ^ i) + 4 * (lane & 1);  // i is the row modulo 8
+        *reinterpret_cast<uint2 *>(&xs[0][rb + i][c]) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2 *>(&xs[1][rb + i][c]) = make_uint2(lo[0], lo[1]);
+      }
+    }
+    __syncwarp();
+    spot = find(tile + step);  // its loads run under the products
+    float acc[16][4];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < 8; ++k) {
+      uint4 a[2];
+#pragma unroll
+      for (int part = 0; part < 2; ++part) a[part] = ldmatrix_x4(&xs[part][lane & 15][8 * ((2 * k + (lane >> 4)) ^ (lane & 7))]);
+      // R's A fragments hold the B fragments of two column tiles each: registers (0, 2) and (1, 3)
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const uint4 rh = sm.r[0][m][k][lane], rl = sm.r[1][m][k][lane];
+        mma_bf16(acc[2 * m], a[1], rl.x, rl.z), mma_bf16(acc[2 * m + 1], a[1], rl.y, rl.w);
+        mma_bf16(acc[2 * m], a[1], rh.x, rh.z), mma_bf16(acc[2 * m + 1], a[1], rh.y, rh.w);
+        mma_bf16(acc[2 * m], a[0], rl.x, rl.z), mma_bf16(acc[2 * m + 1], a[0], rl.y, rl.w);
+        mma_bf16(acc[2 * m], a[0], rh.x, rh.z), mma_bf16(acc[2 * m + 1], a[0], rh.y, rh.w);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t dst = __shfl_sync(FULL_MASK, at.at, g + 8 * i);
+#pragma unroll
+      for (int j4 = 0; j4 < 4; ++j4) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float y0 = acc[4 * j4 + j][2 * i], y1 = acc[4 * j4 + j][2 * i + 1];
+          const uint32_t c0 = gn ? cell_index<true, 15>(y0, tb.ce, l16, gs, go, gn, tb.sb) : bucket<15>(y0, tb.sb);
+          const uint32_t c1 = gn ? cell_index<true, 15>(y1, tb.ce, l16, gs, go, gn, tb.sb) : bucket<15>(y1, tb.sb);
+          v |= (c0 | (c1 << 4)) << (8 * j);
+        }
+        v = transpose_bytes(v, t);
+        if (dst >= 0) reinterpret_cast<uint32_t *>(sd.pages + dst)[1 + 4 * j4 + t] = v;
+      }
+    }
+  }
+}
+
+// Dense rotation, few rows: a warp per row on the CUDA cores, R^T staged once per CTA.
+constexpr int AF_WARPS = 8;
+constexpr size_t AF_SMEM = (size_t)D * D * 4 + AF_WARPS * D * 4;
+__global__ void __launch_bounds__(AF_WARPS * 32) k_paged_append_dense_few(const AppendParams p) {
   extern __shared__ __align__(16) float asm_f[];
   float *rt = asm_f, *uv = asm_f + D * D;
   const int side = (int)blockIdx.x < p.k_ctas ? 0 : 1;
   const int cta = side ? blockIdx.x - p.k_ctas : blockIdx.x, n_cta = side ? gridDim.x - p.k_ctas : p.k_ctas;
   const AppendSide &sd = p.side[side];
   __shared__ float sb[16];
-  __shared__ __align__(16) uint8_t ib[AD_WARPS][D];
+  __shared__ __align__(16) uint8_t ib[AF_WARPS][D];
   pdl_trigger();
   stage_matrix(rt, sd.pit);
   if (threadIdx.x < 15) sb[threadIdx.x] = sd.b[threadIdx.x];
@@ -198,7 +390,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32) k_paged_append_dense(const Appe
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float *u = uv + warp * D;
   const int64_t n_rows = (int64_t)paged_rows(p.pv) * p.pv.Hkv;
-  for (int64_t row = (int64_t)cta * AD_WARPS + warp; row < n_rows; row += (int64_t)n_cta * AD_WARPS) {
+  for (int64_t row = (int64_t)cta * AF_WARPS + warp; row < n_rows; row += (int64_t)n_cta * AF_WARPS) {
     const int tok = (int)(row / p.pv.Hkv), h = (int)(row - (int64_t)tok * p.pv.Hkv);
     const Place at = place_row(p.pv, tok, h, lane == 0);
     if (at.at < 0) continue;
@@ -254,7 +446,17 @@ cudaError_t launch_rows(K kern, AppendParams p, int threads, int rows_per_cta, s
 }
 
 cudaError_t launch_append(const AppendParams &p, bool dense, int dtype, int sms, cudaStream_t st) {
-  if (dense) return launch_rows(k_paged_append_dense, p, AD_WARPS * 32, AD_WARPS, AD_SMEM, sms, st);
+  if (dense) {
+    // Up to a 16-row tile per SM the tensor cores have too few rows to hide a tile's latency: 64 rows
+    // of each side take 10.3 us a warp per row and 14.0 us in tiles, 1500 rows about the same.
+    if ((int64_t)p.pv.n_tokens * p.pv.Hkv <= 16 * sms)
+      return launch_rows(k_paged_append_dense_few, p, AF_WARPS * 32, AF_WARPS, AF_SMEM, sms, st);
+    if (dtype == TQ_DTYPE_F32)
+      return launch_rows(k_paged_append_dense<TQ_DTYPE_F32>, p, AD_WARPS * 32, 16, sizeof(DenseSmem), sms, st);
+    if (dtype == TQ_DTYPE_BF16)
+      return launch_rows(k_paged_append_dense<TQ_DTYPE_BF16>, p, AD_WARPS * 32, 16, sizeof(DenseSmem), sms, st);
+    return launch_rows(k_paged_append_dense<TQ_DTYPE_F16>, p, AD_WARPS * 32, 16, sizeof(DenseSmem), sms, st);
+  }
   constexpr int per = 8 * (WT_THREADS / 32);
   if (dtype == TQ_DTYPE_F32) return launch_rows(k_paged_append_wht<TQ_DTYPE_F32>, p, WT_THREADS, per, 0, sms, st);
   if (dtype == TQ_DTYPE_BF16) return launch_rows(k_paged_append_wht<TQ_DTYPE_BF16>, p, WT_THREADS, per, 0, sms, st);
@@ -277,6 +479,7 @@ cudaError_t launch_paged_append(const tq_ctx *k, const tq_ctx *v, const PagedVie
     for (int j = 0; j < 4; ++j) s.wht_neg[j] = ctx[i]->wht_neg[j];
     for (int j = 0; j < 15; ++j) s.b[j] = ctx[i]->cb.b[j];
     s.bt = ctx[i]->d_bt;
+    s.rfrag = ctx[i]->d_rfrag;
     s.pit = ctx[i]->d_pit;
   }
   const bool dk = k->p.rotation == TQ_ROT_DENSE, dv = v->p.rotation == TQ_ROT_DENSE;

@@ -54,6 +54,16 @@ static __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint4 &a, u
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
+// The A operand of 16 rows by 16 elements; lane l gives the address of row l % 16, half l / 16.
+static __device__ __forceinline__ uint4 ldmatrix_x4(const void *row) {
+  uint4 r;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"((uint32_t)__cvta_generic_to_shared(row))
+               : "memory");
+  return r;
+}
+
 // acc += A (X_hi [+ X_lo]): rows g, g + 8 of the tile, columns 2t, 2t + 1 (lane 4g + t).
 template <bool LO>
 static __device__ __forceinline__ void rot_mul(float (&acc)[4], const uint4 (&a)[8], const RotColumns &x, int lane) {

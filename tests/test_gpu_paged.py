@@ -190,6 +190,46 @@ def test_append_writes_the_oracles_records(case, rot):
         assert ok, n_diff
 
 
+APPEND_MANY = [  # dense rotations in 16-row tiles: above 16 rows per SM
+    ([900, 0, 333], [900, 0, 20], 4, 64, "bf16", 128, False, 3, True),
+    ([611, 77, 64], [600, 50, 64], 5, 16, "f16", 64, True, 0, False),
+    ([2600], [2590], 1, 32, "f32", 32, False, 11, False),
+    ([130, 170, 90, 1, 300], [130, 170, 90, 1, 300], 8, 128, "f32", 0, False, 0, True),
+]
+
+
+@pytest.mark.parametrize("case", APPEND_MANY, ids=lambda c: f"{c[4]}-p{c[3]}-r{c[5]}{'i' if c[6] else ''}-h{c[2]}")
+@pytest.mark.parametrize("rot", [("dense", "dense"), ("dense", "wht")], ids="/".join)
+def test_append_of_many_dense_rows(case, rot):
+    test_append_writes_the_oracles_records(case, rot)
+
+
+def test_append_of_many_dense_rows_at_the_ends_of_the_range():
+    """Norms down to fp32's smallest, rows of zeros, and non-finite rows, in the tiles of other rows."""
+    tq = lib()
+    s = Setup(tq, [400], [400], 8, 16, 5, ("dense", "dense"), fill=False)
+    x = s.rng.standard_normal((400, 8, 128))
+    x[5:90] *= 2.0 ** -s.rng.integers(90, 130, (85, 8, 1))
+    x[100] = 0
+    x[110, 3, 1:] = 0
+    x[110, 3, 0] = 2.0 ** -149
+    k, k32 = device_rows(x, "f32")
+    bad = np.zeros((400, 8), bool)
+    for i, h, value in ((200, 0, np.nan), (201, 7, np.inf), (202, 3, -np.inf)):
+        k[i, h, 9], bad[i, h] = float(value), True
+    tq.tq_paged_append(*s.ctx, s.kv, s.batch, k, k)
+    assert s.status() == 0
+    for i in range(2):
+        rec, info = s.codec[i].encode(np.ascontiguousarray(k32.reshape(-1, 128), np.float32))
+        got = s.pages[i].cpu().numpy()[s.table[0, :25]].transpose(0, 2, 1, 3).reshape(-1, 68)
+        n1, idx1 = unpack_turbo4(got)
+        n0, idx0 = unpack_turbo4(rec)
+        ok = ~bad.reshape(-1)
+        assert np.array_equal(n1[ok], n0[ok])
+        fine, n_diff = band_ok(idx1[ok], idx0[ok], info["y"].reshape(-1, 128)[ok], s.codec[i].b32, BAND)
+        assert fine, n_diff
+
+
 def test_append_equals_set_rows_through_slots():
     """Without a rotation the call is tq_quantize_set_rows at the pages' row slots."""
     import torch

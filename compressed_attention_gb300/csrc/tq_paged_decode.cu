@@ -1,7 +1,8 @@
 // Single-row attention over the paged cache: split-K decode through a block table, in two
 // launches.
 //
-//   k_paged_partial  persistent, one CTA per SM.  The key tiles (240 keys) of all units
+//   k_paged_partial  persistent, one CTA per SM.  The key tiles (240 keys; 224 where a unit has
+//                    more than four heads) of all units
 //                    (sequence, KV head, group of 4 or 8 q-heads) lie end to end in one
 //                    virtual sequence, each unit preceded by a few empty tiles that stand
 //                    for the cost of starting it; CTA c takes the c-th equal share, so
@@ -29,11 +30,15 @@ namespace tq {
 
 namespace {
 
-constexpr int CW = 15;               // consumer warps, 16 keys of a tile each
-constexpr int TILE = 16 * CW;        // keys of a pipeline stage
-constexpr int NT = (CW + 1) * 32;    // + the producer warp
+// Consumer warps, keys of a pipeline stage and threads (with the producer warp).  GROUPS = 1: units of
+// up to four heads, a warp per 16 keys.  GROUPS = 2: up to eight, two warps per 32 keys.
+template <int GROUPS>
+struct Shape {
+  static constexpr int CW = GROUPS == 1 ? 15 : 14, TILE = 16 * CW, NT = (CW + 1) * 32;
+};
+constexpr int MAX_CW = Shape<1>::CW, MAX_TILE = Shape<1>::TILE;
 constexpr int NSTAGE = 4;
-constexpr int STAGE = TILE * PG_ROW + 32;  // 16,352 bytes, a multiple of 32
+constexpr int STAGE = MAX_TILE * PG_ROW + 32;  // 16,352 bytes, a multiple of 32
 constexpr int PROW = D + 4;          // floats of a partial: acc[128], max, sum, 2 spare
 constexpr int ITEM_TILES = 4;        // cost of an item ahead of its tiles, in tiles
 
@@ -55,14 +60,15 @@ struct DecodeParams {
 
 struct Head {
   union {
-    float osm[CW][4][D];   // the warps' accumulators of 4 heads, for the merge
+    float osm[MAX_CW][4][D];   // the warps' accumulators of 4 heads, for the merge
     struct {
       RotColumns x;        // the item's q
       float y[8][D + 4];   // R q
     } prep;
   };
   uint64_t full[NSTAGE], empty[NSTAGE];
-  float mw[CW][8], lw[CW][8];
+  float mw[MAX_CW][4], lw[MAX_CW][4];
+  float mh[8], lh[8];      // the item's maxima and sums
   int abort_flag;
   int V, G;                // the V virtual tiles are shared by G CTAs
 };
@@ -84,7 +90,6 @@ __device__ __forceinline__ uint8_t *stage_at(uint8_t *sm, int i) {
   return sm + (i < BELOW ? A_OFF + i * STAGE : B_OFF + (i - BELOW) * STAGE);
 }
 
-__device__ __forceinline__ void consumers_sync() { named_sync1<CW * 32>(); }
 // Barrier over the first N threads, apart from that of all the consumers.
 template <int N>
 __device__ __forceinline__ void named_sync2() {
@@ -144,6 +149,7 @@ __device__ __forceinline__ int seq_keys(const PagedView &v, int b, int *row, boo
   *row = a;
   return max(n - (e - a) + 1, 0);
 }
+template <int TILE>
 __device__ __forceinline__ int key_tiles(int keys) { return (keys + TILE - 1) / TILE; }
 
 // Walks a CTA's share: per unit met, the tiles [t0, t1) of it.
@@ -157,12 +163,13 @@ struct Item {
 };
 
 // One warp: the total of virtual tiles (flagging bad lengths), then this CTA's share.
+template <int TILE>
 __device__ __forceinline__ int total_tiles(const DecodeParams &p, int lane, bool flag) {
   const int upb = p.pv.Hkv * p.n_hg;
   int sum = 0;
   for (int b = lane; b < p.pv.B; b += 32) {
     int row;
-    const int t = key_tiles(seq_keys(p.pv, b, &row, flag));
+    const int t = key_tiles<TILE>(seq_keys(p.pv, b, &row, flag));
     sum += t ? t + ITEM_TILES : 0;
   }
 #pragma unroll
@@ -170,6 +177,7 @@ __device__ __forceinline__ int total_tiles(const DecodeParams &p, int lane, bool
   return sum * upb;
 }
 // One warp: the sequence that holds virtual tile v and the offset within it.
+template <int TILE>
 __device__ __forceinline__ void seek(const DecodeParams &p, int v, int lane, int *b_out, int *off_out) {
   const int upb = p.pv.Hkv * p.n_hg;
   int base = 0;
@@ -177,7 +185,7 @@ __device__ __forceinline__ void seek(const DecodeParams &p, int v, int lane, int
     const int b = b0 + lane;
     int row, t = 0;
     if (b < p.pv.B) {
-      t = key_tiles(seq_keys(p.pv, b, &row, false));
+      t = key_tiles<TILE>(seq_keys(p.pv, b, &row, false));
       t = t ? (t + ITEM_TILES) * upb : 0;
     }
     int inc = t;
@@ -197,18 +205,20 @@ __device__ __forceinline__ void seek(const DecodeParams &p, int v, int lane, int
   }
 }
 
+template <int TILE>
 __device__ __forceinline__ void walk_load(const DecodeParams &p, Walk &w) {
   w.keys = w.b < p.pv.B ? seq_keys(p.pv, w.b, &w.row, false) : 0;
-  w.tiles = key_tiles(w.keys);
+  w.tiles = key_tiles<TILE>(w.keys);
 }
 // The next item of the share (false: done).
+template <int TILE>
 __device__ __forceinline__ bool next_item(const DecodeParams &p, Walk &w, Item &it) {
   const int upb = p.pv.Hkv * p.n_hg;
   while (w.left > 0) {
     if (w.b >= p.pv.B) return false;
     if (w.tiles == 0 || w.u >= upb) {
       ++w.b, w.u = 0, w.off = 0;
-      walk_load(p, w);
+      walk_load<TILE>(p, w);
       continue;
     }
     const int vt = w.tiles + ITEM_TILES, n = min(vt - w.off, w.left);
@@ -222,8 +232,14 @@ __device__ __forceinline__ bool next_item(const DecodeParams &p, Walk &w, Item &
   return false;
 }
 
-template <int NG, bool FIXED>
+// GROUPS = 1: at most four heads; warps 2i and 2i + 1 take 16 keys of the i-th 32 each.  GROUPS = 2: five to
+// eight heads in two halves; warp i of either half takes all of the i-th 32 keys.  Both halves decode
+// every key, but a warp holds the state of four heads only: one that held eight decoded once, spilled, and
+// took 2.2 us a tile against 1.9 (64 ragged sequences, 6 heads per KV head: 37 us).
+template <int GROUPS, bool FIXED>
 __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
+  constexpr int CW = Shape<GROUPS>::CW, TILE = Shape<GROUPS>::TILE, NT = Shape<GROUPS>::NT;
+  auto consumers_sync = [] { named_sync1<CW * 32>(); };
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Head &sm = *reinterpret_cast<Head *>(smem_raw);
   Tail &tl = *reinterpret_cast<Tail *>(smem_raw + TAIL_OFF);
@@ -245,14 +261,14 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
       fence_mbar_init();
     }
     pdl_wait();
-    const int V = total_tiles(p, lane, blockIdx.x == 0);
+    const int V = total_tiles<TILE>(p, lane, blockIdx.x == 0);
     const int G = min((int)gridDim.x, V);
     Walk w{0, 0, 0, 0, 0, 0, 0, 0};
     if ((int)blockIdx.x < G) {
       w.v = share_start(blockIdx.x, V, G);
       w.left = share_start(blockIdx.x + 1, V, G) - w.v;
-      seek(p, w.v, lane, &w.b, &w.off);
-      walk_load(p, w);
+      seek<TILE>(p, w.v, lane, &w.b, &w.off);
+      walk_load<TILE>(p, w);
       const int vt = w.tiles + ITEM_TILES;
       w.u = w.off / vt;
       w.off -= w.u * vt;
@@ -270,7 +286,7 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     int ctr = 0;
     Item it;
     bool ok = true;
-    while (ok && next_item(p, w, it)) {
+    while (ok && next_item<TILE>(p, w, it)) {
       const int kvh = it.u / p.n_hg;
       // the page of this lane's segment of tile j
       auto page_of = [&](int j) -> int {
@@ -333,10 +349,11 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
   const uint32_t kword = 4u * lane, vword = 128u + 4u * lane;
   const uint32_t klo[2] = {p.klo[0], p.klo[1]}, khi[2] = {p.khi[0], p.khi[1]};
   const uint32_t vlo[2] = {p.vlo[0], p.vlo[1]}, vhi[2] = {p.vhi[0], p.vhi[1]};
-  // Tile row of the warp's key k: warps 0-13 pair up on 32-row blocks (rows 16 apart start 16
-  // banks apart), so that the packed words and norms are read without bank conflicts.
-  const bool paired = warp < 2 * (CW / 2);
-  const int r0 = paired ? 32 * (warp >> 1) + 8 * (warp & 1) : 16 * warp;
+  const int grp = GROUPS == 2 && warp >= CW / 2 ? 1 : 0, wi = warp - grp * (CW / 2);
+  // Tile row of key k of the warp's 16 (the first of two such blocks, eight rows apart, in a half):
+  // rows 16 apart start 16 banks apart, so that the packed words and norms are read without bank conflicts.
+  const bool paired = GROUPS == 2 || warp < 2 * (CW / 2);  // (the 15th warp's rows lie together)
+  const int r0 = GROUPS == 2 ? 32 * wi : (paired ? 32 * (warp >> 1) + 8 * (warp & 1) : 16 * warp);
   auto row_of = [&](int k) { return paired ? r0 + (k & 7) + 16 * (k >> 3) : r0 + k; };
   const int pk0 = row_of(key_of_row(g)), pk1 = row_of(key_of_row(g + 8)), pat = row_of((t & 1) | ((t & 2) << 2));
   const int hs = g >> 1;
@@ -360,7 +377,7 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     q_raw = load_lane4_raw(p.q.data + i.row * p.q.token_bytes + (head0 + warp) * p.q.head_bytes, p.q.dtype, lane);
     if (p.rope.rot_dim) q_ang = rope_angles(lane, p.rope, rope_pos(p.rope, i.keys - 1, p.pv.status, lane == 0));
   };
-  bool have = next_item(p, w, it);
+  bool have = next_item<TILE>(p, w, it);
   if (have) fetch_q(it);
   consumers_sync();  // tl.q (the share) has been read
   while (have) {
@@ -394,29 +411,23 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
       }
     }
     consumers_sync();
-    uint32_t qb[NG][8][2];
-    float qs[NG];
-#pragma unroll
-    for (int c = 0; c < NG; ++c) {
-      const int slot = c * 4 + hs, sw = 2 * g + (t >> 1);
+    uint32_t qb[8][2];
+    float qs;
+    {
+      const int slot = grp * 4 + hs, sw = 2 * g + (t >> 1);
       const uint32_t *qw = tl.q[slot] + (g & 1) * 64 + 16 * t;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        qb[c][kk][0] = slot < GH ? qw[(2 * kk) ^ sw] : 0u;
-        qb[c][kk][1] = slot < GH ? qw[(2 * kk + 1) ^ sw] : 0u;
+        qb[kk][0] = slot < GH ? qw[(2 * kk) ^ sw] : 0u;
+        qb[kk][1] = slot < GH ? qw[(2 * kk + 1) ^ sw] : 0u;
       }
-      const int my = c * 4 + t;  // the head whose scores this lane holds
-      qs[c] = my < GH ? tl.qs[my] : 0.f;
+      const int my = grp * 4 + t;  // the head whose scores this lane holds
+      qs = my < GH ? tl.qs[my] : 0.f;
     }
-    float O[NG][8][4];
-    float M[NG], lsum[NG];
+    float O[8][4];
+    float M = -INFINITY, lsum = 0.f;
 #pragma unroll
-    for (int c = 0; c < NG; ++c) {
-      M[c] = -INFINITY;
-      lsum[c] = 0.f;
-#pragma unroll
-      for (int mt = 0; mt < 8; ++mt) O[c][mt][0] = O[c][mt][1] = O[c][mt][2] = O[c][mt][3] = 0.f;
-    }
+    for (int mt = 0; mt < 8; ++mt) O[mt][0] = O[mt][1] = O[mt][2] = O[mt][3] = 0.f;
 
     for (int j = it.t0; j < it.t1; ++j) {
       const int s = ctr % NSTAGE;
@@ -430,15 +441,14 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
       }
       const int nk = min(TILE, it.keys - j * TILE);
       const uint8_t *Ks = stage_at(smem_raw, s), *Vs = stage_at(smem_raw, NSTAGE + s);
-      if (r0 < nk) {  // the warp's first row is its lowest: some key is valid
+#pragma unroll 1
+      for (int b8 = 0; b8 < 8 * GROUPS; b8 += 8) {
+        if (r0 + b8 >= nk) break;  // the block's first row is its lowest: no valid key
         // ---- scores S^T[16 keys x 8] = K_hat Q^T, two accumulator chains
-        float sa[NG][4], sb[NG][4];
-#pragma unroll
-        for (int c = 0; c < NG; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sa[c][e] = sb[c][e] = 0.f;
-        const uint8_t *kr0 = Ks + pk0 * PG_ROW + 4 + 16 * t;
-        const uint8_t *kr1 = Ks + pk1 * PG_ROW + 4 + 16 * t;
+        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+        const int k0 = pk0 + b8, k1 = pk1 + b8;
+        const uint8_t *kr0 = Ks + k0 * PG_ROW + 4 + 16 * t;
+        const uint8_t *kr1 = Ks + k1 * PG_ROW + 4 + 16 * t;
 #pragma unroll
         for (int w4 = 0; w4 < 4; ++w4) {
           uint32_t d0[4], d1[4];
@@ -447,48 +457,48 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
           decode4<false, FIXED>(lut_base, kword, x1, klo, khi, d1);
           const uint32_t a0[4] = {d0[0], d1[0], d0[1], d1[1]};
           const uint32_t a1[4] = {d0[2], d1[2], d0[3], d1[3]};
-#pragma unroll
-          for (int c = 0; c < NG; ++c) {
-            mma_f16(sa[c], a0, qb[c][2 * w4][0], qb[c][2 * w4][1]);
-            mma_f16(sb[c], a1, qb[c][2 * w4 + 1][0], qb[c][2 * w4 + 1][1]);
-          }
+          mma_f16(sa, a0, qb[2 * w4][0], qb[2 * w4][1]);
+          mma_f16(sb, a1, qb[2 * w4 + 1][0], qb[2 * w4 + 1][1]);
         }
         // ---- online softmax over the two keys of this lane, head t of each group; the running
         // max is of s + log2(value norm), so that the probability operand 2^7 e^s n_v stays in
         // fp16's range whatever the norms
-        const float nk0 = *reinterpret_cast<const float *>(Ks + pk0 * PG_ROW);
-        const float nk1 = *reinterpret_cast<const float *>(Ks + pk1 * PG_ROW);
-        const float nv0 = *reinterpret_cast<const float *>(Vs + pk0 * PG_ROW);
-        const float nv1 = *reinterpret_cast<const float *>(Vs + pk1 * PG_ROW);
-        const bool ok0 = pk0 < nk, ok1 = pk1 < nk;
-        const float nu0 = ok0 ? fmaxf(log2_approx(nv0), -64.f) : 0.f;
-        const float nu1 = ok1 ? fmaxf(log2_approx(nv1), -64.f) : 0.f;
-        uint32_t pb[NG][2];
-#pragma unroll
-        for (int c = 0; c < NG; ++c) {
-          const float d0 = (sa[c][0] + sa[c][1]) + (sb[c][0] + sb[c][1]);
-          const float d1 = (sa[c][2] + sa[c][3]) + (sb[c][2] + sb[c][3]);
-          const float s0 = ok0 ? d0 * (nk0 * qs[c]) : -INFINITY;
-          const float s1 = ok1 ? d1 * (nk1 * qs[c]) : -INFINITY;
-          const float u0 = s0 + nu0, u1 = s1 + nu1;
+        const float nk0 = *reinterpret_cast<const float *>(Ks + k0 * PG_ROW);
+        const float nk1 = *reinterpret_cast<const float *>(Ks + k1 * PG_ROW);
+        const float nv0 = *reinterpret_cast<const float *>(Vs + k0 * PG_ROW);
+        const float nv1 = *reinterpret_cast<const float *>(Vs + k1 * PG_ROW);
+        const bool ok0 = k0 < nk, ok1 = k1 < nk;
+        const float pv0 = ok0 ? nv0 * 128.f : 0.f, pv1 = ok1 ? nv1 * 128.f : 0.f;  // 2^P_SHIFT
+        uint32_t pb[2];
+        const float d0 = (sa[0] + sa[1]) + (sb[0] + sb[1]);
+        const float d1 = (sa[2] + sa[3]) + (sb[2] + sb[3]);
+        const float s0 = ok0 ? d0 * (nk0 * qs) : -INFINITY;
+        const float s1 = ok1 ? d1 * (nk1 * qs) : -INFINITY;
+        float e0 = exp2_approx(s0 - M), e1 = exp2_approx(s1 - M);
+        // An operand past 2^15, or no maximum yet (e then infinite or NaN): the maximum is raised.  One
+        // vote a tile, where the maximum itself takes three exchanges.
+        if (__any_sync(FULL_MASK, !(fmaxf(e0 * pv0, e1 * pv1) <= 32768.f) || M == -INFINITY)) {
+          const float u0 = s0 + (ok0 ? fmaxf(log2_approx(nv0), -64.f) : 0.f);
+          const float u1 = s1 + (ok1 ? fmaxf(log2_approx(nv1), -64.f) : 0.f);
           float bm = fmaxf(u0, u1);
           bm = fmaxf(bm, __shfl_xor_sync(FULL_MASK, bm, 4));
           bm = fmaxf(bm, __shfl_xor_sync(FULL_MASK, bm, 8));
           bm = fmaxf(bm, __shfl_xor_sync(FULL_MASK, bm, 16));
-          if (bm > M[c] + RESCALE_SLACK) {  // also taken while M is -inf
-            const float alpha = exp2_approx(M[c] - bm);
-            M[c] = bm;
-            lsum[c] *= alpha;
+          if (bm > M + RESCALE_SLACK) {  // also taken while M is -inf
+            const float alpha = exp2_approx(M - bm);
+            M = bm;
+            lsum *= alpha;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt)
-              O[c][mt][0] *= alpha, O[c][mt][1] *= alpha, O[c][mt][2] *= alpha, O[c][mt][3] *= alpha;
+              O[mt][0] *= alpha, O[mt][1] *= alpha, O[mt][2] *= alpha, O[mt][3] *= alpha;
           }
-          const float Mu = (M[c] == -INFINITY) ? 0.f : M[c];
-          lsum[c] += exp2_approx(s0 - Mu) + exp2_approx(s1 - Mu);
-          p_operand(exp2_approx(u0 - Mu + P_SHIFT), exp2_approx(u1 - Mu + P_SHIFT), src0, src1, lo_sel, pb[c]);
+          const float Mu = (M == -INFINITY) ? 0.f : M;
+          e0 = exp2_approx(s0 - Mu), e1 = exp2_approx(s1 - Mu);
         }
+        lsum += e0 + e1;
+        p_operand(e0 * pv0, e1 * pv1, src0, src1, lo_sel, pb);
         // ---- O^T[dims x cols] += V_hat^T[dims x keys] P^T
-        const uint8_t *va_p = Vs + pat * PG_ROW + 4 + 8 * g;  // key a_t; a_t+2, +4, +6 follow
+        const uint8_t *va_p = Vs + (pat + b8) * PG_ROW + 4 + 8 * g;  // key a_t; a_t+2, +4, +6 follow
 #pragma unroll
         for (int w2 = 0; w2 < 2; ++w2) {
           const uint32_t xa = ld_u32(va_p + 4 * w2), xb = ld_u32(va_p + 2 * PG_ROW + 4 * w2);
@@ -506,8 +516,7 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
 #pragma unroll
           for (int jj = 0; jj < 4; ++jj) {
             const uint32_t a[4] = {r0w[jj], r1w[jj], r2w[jj], r3w[jj]};
-#pragma unroll
-            for (int c = 0; c < NG; ++c) mma_f16(O[c][4 * w2 + jj], a, pb[c][0], pb[c][1]);
+            mma_f16(O[4 * w2 + jj], a, pb[0], pb[1]);
           }
         }
       }
@@ -519,36 +528,27 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     // same tile, so either every consumer warp enters the merge barriers or none.
     if (aborted || *reinterpret_cast<volatile int *>(&sm.abort_flag)) return;
 
-    have = next_item(p, w, nx);
+    have = next_item<TILE>(p, w, nx);
     if (have) fetch_q(nx);  // under the merge
 
     // ---- merge the warps' states and write the item's partial
-#pragma unroll
-    for (int c = 0; c < NG; ++c) {
-      lsum[c] += __shfl_xor_sync(FULL_MASK, lsum[c], 4);
-      lsum[c] += __shfl_xor_sync(FULL_MASK, lsum[c], 8);
-      lsum[c] += __shfl_xor_sync(FULL_MASK, lsum[c], 16);
-    }
-    if (g == 0) {
-#pragma unroll
-      for (int c = 0; c < NG; ++c) {
-        sm.mw[warp][c * 4 + t] = M[c];
-        sm.lw[warp][c * 4 + t] = lsum[c];
-      }
-    }
+    lsum += __shfl_xor_sync(FULL_MASK, lsum, 4);
+    lsum += __shfl_xor_sync(FULL_MASK, lsum, 8);
+    lsum += __shfl_xor_sync(FULL_MASK, lsum, 16);
+    if (g == 0) sm.mw[warp][t] = M, sm.lw[warp][t] = lsum;
     const int first = share_of(it.vstart, V, G), n_split = share_of(it.vstart + it.tiles - 1, V, G) - first + 1;
     const int cta = blockIdx.x;
     float *dst0 = n_split == 1 ? p.whole + ((size_t)it.row * p.Hq + head0) * PROW
                                : p.split + (size_t)(cta * 2 + (cta == first ? 1 : 0)) * 8 * PROW;
     if (threadIdx.x == 0 && cta == first) p.unit[it.b * p.pv.Hkv * p.n_hg + it.u] = first | (n_split << 16);
     consumers_sync();
-#pragma unroll
-    for (int c = 0; c < NG; ++c) {
-      const int hh = c * 4 + t;
-      // the head's max and sum over the warps: lane (g, t) takes warps g and g + 8
-      const float m0 = sm.mw[g][hh], l0 = sm.lw[g][hh];
-      const bool has1 = g + 8 < CW;
-      const float m1 = has1 ? sm.mw[g + 8][hh] : -INFINITY, l1 = has1 ? sm.lw[g + 8][hh] : 0.f;
+    {
+      // the head's max and sum over its warps: lane (g, t) takes warps g and g + 8 of them
+      constexpr int WPG = CW / GROUPS;
+      const int wb = grp * WPG;
+      const bool has0 = g < WPG, has1 = g + 8 < WPG;
+      const float m0 = has0 ? sm.mw[wb + g][t] : -INFINITY, l0 = has0 ? sm.lw[wb + g][t] : 0.f;
+      const float m1 = has1 ? sm.mw[wb + g + 8][t] : -INFINITY, l1 = has1 ? sm.lw[wb + g + 8][t] : 0.f;
       float ms = fmaxf(m0, m1);
       ms = fmaxf(ms, __shfl_xor_sync(FULL_MASK, ms, 4));
       ms = fmaxf(ms, __shfl_xor_sync(FULL_MASK, ms, 8));
@@ -557,25 +557,25 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
       ls += __shfl_xor_sync(FULL_MASK, ls, 4);
       ls += __shfl_xor_sync(FULL_MASK, ls, 8);
       ls += __shfl_xor_sync(FULL_MASK, ls, 16);
-      const float fac = (M[c] == -INFINITY) ? 0.f : exp2_approx(M[c] - ms);
+      if (wi == 0 && g == 0) sm.mh[grp * 4 + t] = ms, sm.lh[grp * 4 + t] = ls;
+      const float fac = (M == -INFINITY) ? 0.f : exp2_approx(M - ms);
       // rows g and g + 8 of m-tile mt: dims 16g + 2mt, + 1, in blocks of 16 permuted so that the
       // warp's lanes hit 32 banks
       float *orow = &sm.osm[warp][t][16 * g];
       const int sw = 4 * (g >> 1) + t;
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) {
-        orow[(2 * mt) ^ sw] = (O[c][mt][0] + O[c][mt][1]) * fac;
-        orow[(2 * mt + 1) ^ sw] = (O[c][mt][2] + O[c][mt][3]) * fac;
+        orow[(2 * mt) ^ sw] = (O[mt][0] + O[mt][1]) * fac;
+        orow[(2 * mt + 1) ^ sw] = (O[mt][2] + O[mt][3]) * fac;
       }
       consumers_sync();
-      const int Gc = min(4, GH - c * 4);
-      for (int idx = threadIdx.x; idx < Gc * D; idx += CW * 32) {
-        const int h4 = idx / D, jd = idx % D;
-        const float ms2 = __shfl_sync(FULL_MASK, ms, h4), ls2 = __shfl_sync(FULL_MASK, ls, h4);
+      for (int idx = threadIdx.x; idx < GH * D; idx += CW * 32) {
+        const int h = idx / D, jd = idx % D, h4 = h & 3, w0 = GROUPS == 2 ? (h >> 2) * WPG : 0;
+        const float ms2 = sm.mh[h], ls2 = sm.lh[h];
         float acc = 0.f;
 #pragma unroll
-        for (int ww = 0; ww < CW; ++ww) acc += sm.osm[ww][h4][jd ^ (4 * (jd >> 5) + h4)];
-        float *dst = dst0 + (c * 4 + h4) * PROW;
+        for (int ww = 0; ww < WPG; ++ww) acc += sm.osm[w0 + ww][h4][jd ^ (4 * (jd >> 5) + h4)];
+        float *dst = dst0 + h * PROW;
         dst[jd] = (ms2 == -INFINITY) ? 0.f : acc;
         if (jd < 2) dst[D + jd] = jd == 0 ? ms2 : ls2;
       }
@@ -687,12 +687,12 @@ __global__ void __launch_bounds__(CB_WARPS * 32) k_paged_combine(const CombinePa
   }
 }
 
-template <int NG>
+template <int GROUPS>
 cudaError_t launch_partial_ng(const DecodeParams &p, bool fixed, int grid, cudaStream_t st) {
-  auto kern = fixed ? k_paged_partial<NG, true> : k_paged_partial<NG, false>;
+  auto kern = fixed ? k_paged_partial<GROUPS, true> : k_paged_partial<GROUPS, false>;
   cudaError_t e = kernel_smem_attr((const void *)kern, (int)SMEM, true);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(grid), dim3(NT), SMEM, st, p);
+  return launch_pdl(kern, dim3(grid), dim3(Shape<GROUPS>::NT), SMEM, st, p);
 }
 
 struct Layout {
@@ -705,7 +705,8 @@ bool layout(const tq_ctx *k, const PagedView &pv, int Hq, Layout *l) {
   l->n_hg = (gq + l->hpc - 1) / l->hpc;
   l->grid = k->num_sms;
   const int64_t units = (int64_t)pv.B * pv.Hkv * l->n_hg;
-  const int64_t tiles = units * ((pv.max_len + TILE - 1) / TILE + ITEM_TILES);
+  const int tile = l->hpc == 8 ? Shape<2>::TILE : Shape<1>::TILE;
+  const int64_t tiles = units * ((pv.max_len + tile - 1) / tile + ITEM_TILES);
   if (l->grid > 65535 || tiles > INT32_MAX || (int64_t)pv.n_tokens * Hq > INT32_MAX) return false;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   l->split = 0;

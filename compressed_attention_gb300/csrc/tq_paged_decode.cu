@@ -35,12 +35,14 @@ namespace {
 template <int GROUPS>
 struct Shape {
   static constexpr int CW = GROUPS == 1 ? 15 : 14, TILE = 16 * CW, NT = (CW + 1) * 32;
+  // Cost of an item ahead of its tiles, in tiles, as measured: 4 of 1 us, 2 of 1.9 us (64 ragged sequences
+  // of 6 heads: 32.9 us with 4, 31.3 with 3, 29.7 with 2; differential decode of 16: 30.0 with 4, 31.1 with 3).
+  static constexpr int ITEM_TILES = GROUPS == 1 ? 4 : 2;
 };
 constexpr int MAX_CW = Shape<1>::CW, MAX_TILE = Shape<1>::TILE;
 constexpr int NSTAGE = 4;
 constexpr int STAGE = MAX_TILE * PG_ROW + 32;  // 16,352 bytes, a multiple of 32
 constexpr int PROW = D + 4;          // floats of a partial: acc[128], max, sum, 2 spare
-constexpr int ITEM_TILES = 4;        // cost of an item ahead of its tiles, in tiles
 
 struct DecodeParams {
   PagedView pv;
@@ -149,8 +151,10 @@ __device__ __forceinline__ int seq_keys(const PagedView &v, int b, int *row, boo
   *row = a;
   return max(n - (e - a) + 1, 0);
 }
-template <int TILE>
-__device__ __forceinline__ int key_tiles(int keys) { return (keys + TILE - 1) / TILE; }
+template <int GROUPS>
+__device__ __forceinline__ int key_tiles(int keys) {
+  return (keys + Shape<GROUPS>::TILE - 1) / Shape<GROUPS>::TILE;
+}
 
 // Walks a CTA's share: per unit met, the tiles [t0, t1) of it.
 struct Walk {
@@ -163,21 +167,21 @@ struct Item {
 };
 
 // One warp: the total of virtual tiles (flagging bad lengths), then this CTA's share.
-template <int TILE>
+template <int GROUPS>
 __device__ __forceinline__ int total_tiles(const DecodeParams &p, int lane, bool flag) {
   const int upb = p.pv.Hkv * p.n_hg;
   int sum = 0;
   for (int b = lane; b < p.pv.B; b += 32) {
     int row;
-    const int t = key_tiles<TILE>(seq_keys(p.pv, b, &row, flag));
-    sum += t ? t + ITEM_TILES : 0;
+    const int t = key_tiles<GROUPS>(seq_keys(p.pv, b, &row, flag));
+    sum += t ? t + Shape<GROUPS>::ITEM_TILES : 0;
   }
 #pragma unroll
   for (int h = 16; h >= 1; h >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, h);
   return sum * upb;
 }
 // One warp: the sequence that holds virtual tile v and the offset within it.
-template <int TILE>
+template <int GROUPS>
 __device__ __forceinline__ void seek(const DecodeParams &p, int v, int lane, int *b_out, int *off_out) {
   const int upb = p.pv.Hkv * p.n_hg;
   int base = 0;
@@ -185,8 +189,8 @@ __device__ __forceinline__ void seek(const DecodeParams &p, int v, int lane, int
     const int b = b0 + lane;
     int row, t = 0;
     if (b < p.pv.B) {
-      t = key_tiles<TILE>(seq_keys(p.pv, b, &row, false));
-      t = t ? (t + ITEM_TILES) * upb : 0;
+      t = key_tiles<GROUPS>(seq_keys(p.pv, b, &row, false));
+      t = t ? (t + Shape<GROUPS>::ITEM_TILES) * upb : 0;
     }
     int inc = t;
 #pragma unroll
@@ -205,26 +209,26 @@ __device__ __forceinline__ void seek(const DecodeParams &p, int v, int lane, int
   }
 }
 
-template <int TILE>
+template <int GROUPS>
 __device__ __forceinline__ void walk_load(const DecodeParams &p, Walk &w) {
   w.keys = w.b < p.pv.B ? seq_keys(p.pv, w.b, &w.row, false) : 0;
-  w.tiles = key_tiles<TILE>(w.keys);
+  w.tiles = key_tiles<GROUPS>(w.keys);
 }
 // The next item of the share (false: done).
-template <int TILE>
+template <int GROUPS>
 __device__ __forceinline__ bool next_item(const DecodeParams &p, Walk &w, Item &it) {
   const int upb = p.pv.Hkv * p.n_hg;
   while (w.left > 0) {
     if (w.b >= p.pv.B) return false;
     if (w.tiles == 0 || w.u >= upb) {
       ++w.b, w.u = 0, w.off = 0;
-      walk_load<TILE>(p, w);
+      walk_load<GROUPS>(p, w);
       continue;
     }
-    const int vt = w.tiles + ITEM_TILES, n = min(vt - w.off, w.left);
+    const int vt = w.tiles + Shape<GROUPS>::ITEM_TILES, n = min(vt - w.off, w.left);
     it.b = w.b, it.u = w.u, it.keys = w.keys, it.row = w.row, it.tiles = w.tiles;
-    it.t0 = max(w.off - ITEM_TILES, 0), it.t1 = w.off + n - ITEM_TILES;
-    it.vstart = w.v - w.off + ITEM_TILES;
+    it.t0 = max(w.off - Shape<GROUPS>::ITEM_TILES, 0), it.t1 = w.off + n - Shape<GROUPS>::ITEM_TILES;
+    it.vstart = w.v - w.off + Shape<GROUPS>::ITEM_TILES;
     w.v += n, w.left -= n, w.off += n;
     if (w.off == vt) ++w.u, w.off = 0;
     if (it.t1 > it.t0) return true;
@@ -239,6 +243,7 @@ __device__ __forceinline__ bool next_item(const DecodeParams &p, Walk &w, Item &
 template <int GROUPS, bool FIXED>
 __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
   constexpr int CW = Shape<GROUPS>::CW, TILE = Shape<GROUPS>::TILE, NT = Shape<GROUPS>::NT;
+  constexpr int ITEM_TILES = Shape<GROUPS>::ITEM_TILES;
   auto consumers_sync = [] { named_sync1<CW * 32>(); };
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Head &sm = *reinterpret_cast<Head *>(smem_raw);
@@ -261,14 +266,14 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
       fence_mbar_init();
     }
     pdl_wait();
-    const int V = total_tiles<TILE>(p, lane, blockIdx.x == 0);
+    const int V = total_tiles<GROUPS>(p, lane, blockIdx.x == 0);
     const int G = min((int)gridDim.x, V);
     Walk w{0, 0, 0, 0, 0, 0, 0, 0};
     if ((int)blockIdx.x < G) {
       w.v = share_start(blockIdx.x, V, G);
       w.left = share_start(blockIdx.x + 1, V, G) - w.v;
-      seek<TILE>(p, w.v, lane, &w.b, &w.off);
-      walk_load<TILE>(p, w);
+      seek<GROUPS>(p, w.v, lane, &w.b, &w.off);
+      walk_load<GROUPS>(p, w);
       const int vt = w.tiles + ITEM_TILES;
       w.u = w.off / vt;
       w.off -= w.u * vt;
@@ -286,7 +291,7 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     int ctr = 0;
     Item it;
     bool ok = true;
-    while (ok && next_item<TILE>(p, w, it)) {
+    while (ok && next_item<GROUPS>(p, w, it)) {
       const int kvh = it.u / p.n_hg;
       // the page of this lane's segment of tile j
       auto page_of = [&](int j) -> int {
@@ -377,7 +382,7 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     q_raw = load_lane4_raw(p.q.data + i.row * p.q.token_bytes + (head0 + warp) * p.q.head_bytes, p.q.dtype, lane);
     if (p.rope.rot_dim) q_ang = rope_angles(lane, p.rope, rope_pos(p.rope, i.keys - 1, p.pv.status, lane == 0));
   };
-  bool have = next_item<TILE>(p, w, it);
+  bool have = next_item<GROUPS>(p, w, it);
   if (have) fetch_q(it);
   consumers_sync();  // tl.q (the share) has been read
   while (have) {
@@ -528,7 +533,7 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     // same tile, so either every consumer warp enters the merge barriers or none.
     if (aborted || *reinterpret_cast<volatile int *>(&sm.abort_flag)) return;
 
-    have = next_item<TILE>(p, w, nx);
+    have = next_item<GROUPS>(p, w, nx);
     if (have) fetch_q(nx);  // under the merge
 
     // ---- merge the warps' states and write the item's partial
@@ -553,7 +558,8 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
       ms = fmaxf(ms, __shfl_xor_sync(FULL_MASK, ms, 4));
       ms = fmaxf(ms, __shfl_xor_sync(FULL_MASK, ms, 8));
       ms = fmaxf(ms, __shfl_xor_sync(FULL_MASK, ms, 16));
-      float ls = (m0 == -INFINITY ? 0.f : l0 * exp2_approx(m0 - ms)) + (m1 == -INFINITY ? 0.f : l1 * exp2_approx(m1 - ms));
+      // (without a maximum a warp's sum is 0, or NaN where its scores are)
+      float ls = (m0 == -INFINITY ? l0 : l0 * exp2_approx(m0 - ms)) + (m1 == -INFINITY ? l1 : l1 * exp2_approx(m1 - ms));
       ls += __shfl_xor_sync(FULL_MASK, ls, 4);
       ls += __shfl_xor_sync(FULL_MASK, ls, 8);
       ls += __shfl_xor_sync(FULL_MASK, ls, 16);
@@ -636,7 +642,7 @@ __global__ void __launch_bounds__(CB_WARPS * 32) k_paged_combine(const CombinePa
         float mc = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (s0 + i < n && l8[i] > 0.f) mc = fmaxf(mc, m8[i]);
+          if (s0 + i < n && l8[i] != 0.f) mc = fmaxf(mc, m8[i]);
         if (mc > ms) {
           const float f = (ms == -INFINITY) ? 0.f : exp2f(ms - mc);
           ls *= f;
@@ -646,7 +652,7 @@ __global__ void __launch_bounds__(CB_WARPS * 32) k_paged_combine(const CombinePa
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (s0 + i < n && l8[i] > 0.f) {
+          if (s0 + i < n && l8[i] != 0.f) {
             const float f = exp2f(m8[i] - ms);
             ls = fmaf(f, l8[i], ls);
             a[0] = fmaf(f, v[i].x, a[0]), a[1] = fmaf(f, v[i].y, a[1]);
@@ -654,7 +660,7 @@ __global__ void __launch_bounds__(CB_WARPS * 32) k_paged_combine(const CombinePa
           }
         }
       }
-      const float f = ls > 0.f ? p.inv_vscale / ls : 0.f;
+      const float f = ls == 0.f ? 0.f : p.inv_vscale / ls;  // (NaN stays)
 #pragma unroll
       for (int e = 0; e < 4; ++e) a[e] *= f;
     }
@@ -705,8 +711,9 @@ bool layout(const tq_ctx *k, const PagedView &pv, int Hq, Layout *l) {
   l->n_hg = (gq + l->hpc - 1) / l->hpc;
   l->grid = k->num_sms;
   const int64_t units = (int64_t)pv.B * pv.Hkv * l->n_hg;
-  const int tile = l->hpc == 8 ? Shape<2>::TILE : Shape<1>::TILE;
-  const int64_t tiles = units * ((pv.max_len + tile - 1) / tile + ITEM_TILES);
+  const bool two = l->hpc == 8;
+  const int tile = two ? Shape<2>::TILE : Shape<1>::TILE, item = two ? Shape<2>::ITEM_TILES : Shape<1>::ITEM_TILES;
+  const int64_t tiles = units * ((pv.max_len + tile - 1) / tile + item);
   if (l->grid > 65535 || tiles > INT32_MAX || (int64_t)pv.n_tokens * Hq > INT32_MAX) return false;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   l->split = 0;

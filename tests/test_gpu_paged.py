@@ -390,6 +390,86 @@ def test_chunks_sharp_softmax():
         check_sharp(s, got, ref, s.q32, scale, f"scale {scale}")
 
 
+def set_norms(s, side, norms):
+    """norms: {(sequence, head, position): norm}, into the records of one side."""
+    import torch
+    for (b, h, pos), n in norms.items():
+        s.host[side][s.table[b, pos // s.P], h, pos % s.P, :4] = np.frombuffer(np.float32(n).tobytes(), np.uint8)
+    s.pages[side].copy_(torch.from_numpy(s.host[side]))
+
+
+NORMS = [  # lens, new, Hq, Hkv, P, output type
+    ([70, 40], [70, 3], 8, 2, 16, "bf16"),
+    ([300, 40], [2, 40], 8, 2, 32, "bf16"),
+    ([70, 40], [70, 3], 8, 2, 16, "f16"),
+    ([70, 40], [1, 1], 8, 2, 64, "bf16"),
+    ([520, 40], [1, 1], 12, 2, 64, "f16"),
+]
+
+
+@pytest.mark.parametrize("case", NORMS, ids=lambda c: f"{c[5]}-t{max(c[1])}-n{max(c[0])}-g{c[2] // c[3]}")
+def test_norms_without_a_value_reach_the_rows_that_see_them(case):
+    """NaN and infinite norms of keys and values: the rows that see one are not finite, the others are as if
+    it were not there."""
+    tq = lib()
+    lens, new, Hq, Hkv, P, out_dtype = case
+    s = Setup(tq, lens, new, Hkv, P, 43, ("wht", "dense"), ragged=max(new) > 1)
+    spots = [(0, 0, 1, 33, np.nan), (1, 0, 0, 50, np.inf), (1, 1, 1, 38, np.nan), (1, 0, 1, 52, np.nan)]
+    for side, b, h, pos, n in spots:
+        set_norms(s, side, {(b, h, pos): n})
+    got, ref = run_attention(s, Hq, "bf16", out_dtype)
+    bad = np.zeros((s.n_rows, Hq), bool)
+    for b in range(2):
+        for i in range(s.cu[b], s.cu[b + 1]):
+            at = lens[b] - (s.cu[b + 1] - i)
+            for _, b2, h, pos, _ in spots:
+                if b2 == b and at >= pos:
+                    bad[i, h * (Hq // Hkv):(h + 1) * (Hq // Hkv)] = True
+    got32 = got.float().cpu().numpy()
+    assert not np.isfinite(got32[bad]).any() and bad.any()
+    import torch
+    ref[bad] = 0
+    check_attention(torch.from_numpy(np.where(bad[..., None], 0, got32)).cuda(), ref, out_dtype)
+
+
+@pytest.mark.parametrize("keys", [8.0, 1.0])
+@pytest.mark.parametrize("case", [([90, 64], [90, 40], 8, 2, 16, "bf16"), ([90, 64], [90, 40], 2, 2, 16, "f16"),
+                                  ([200], [1], 8, 2, 32, "f32"), ([200], [1], 6, 1, 32, "f32")],
+                         ids=lambda c: f"{c[5]}-t{max(c[1])}-g{c[2] // c[3]}")
+def test_norms_of_a_wide_range(case, keys):
+    """Value norms 2^-16 .. 2^15 within 32 keys, rising with the position, so that early rows see the small
+    ones alone; key norms `keys` times 2^-3 .. 2^2.  The usual relative bound holds for each row.  On top:
+    bf16 outputs of several rows carry values as fp16 with the largest of 32 norms at 2^12 .. 2^13, so
+    an element is off by up to 2^-25 2^(15 - 12) where that is more than its relative half step (a mean of
+    values: times sqrt(128) for a row); fp16 outputs have steps of 2^-24 below 2^-14.  keys = 8: scores up
+    to 32 |q| / sqrt(128): off by d <= (2^-11 + 2^-11) |q| max|k| / sqrt(128) with one part (the centroids'
+    error e else), which moves the mean by (exp(2d) - 1) (max|v| + |out|) over the values the row sees."""
+    tq = lib()
+    lens, new, Hq, Hkv, P, out_dtype = case
+    s = Setup(tq, lens, new, Hkv, P, 47, ("dense", "wht"), ragged=max(new) > 1)
+    for b, n in enumerate(lens):
+        for h in range(Hkv):
+            set_norms(s, 1, {(b, h, t): 2.0 ** (t % 32 - 16) for t in range(n)})
+            set_norms(s, 0, {(b, h, t): keys * 2.0 ** ((5 * t) % 6 - 3) for t in range(n)})
+    got, ref = run_attention(s, Hq, "bf16", out_dtype)
+    got = got.float().cpu().numpy().astype(np.float64)
+    num = np.linalg.norm(got[:s.n] - ref[:s.n], axis=-1)
+    den = np.linalg.norm(ref[:s.n], axis=-1)
+    tol = (RTOL + HALF[out_dtype]) * den
+    if out_dtype == "bf16":
+        tol += 2.0 ** -25 * 2.0 ** (15 - 12) * np.sqrt(128)
+    if out_dtype == "f16":
+        tol += 2.0 ** -24 * np.sqrt(128)
+    if keys > 1:
+        e = 2.0 ** -10 if out_dtype == "bf16" else centroid_error(s.codec[0]) + 2.0 ** -20
+        d = e * np.linalg.norm(s.q32[:s.n], axis=-1) * keys * 4 / np.sqrt(128)
+        for b, n in enumerate(lens):
+            for i in range(s.cu[b], s.cu[b + 1]):
+                last = n - (s.cu[b + 1] - i)
+                tol[i] += np.expm1(2 * d[i]) * (2.0 ** (min(last, 31) - 16) + den[i])
+    assert np.all(num <= tol)
+
+
 # ------------------------------------------------------------------------------ differential
 
 DIFF = [

@@ -105,14 +105,16 @@ struct PrefillParams {
   const float *qsc;            // [row] power-of-two scales
   const Start *start;          // per CTA
   JoinInfo *join;              // per CTA: the unit its first item continues
-  float *split;                // [CTA][2][rows of a unit][SROW] partials
+  float *split;                // [CTA][2][128-row tiles of a unit][PART] partials
   uint32_t klo[2], khi[2], vlo[2], vhi[2];
   float inv_vscale;            // 1 / (2^P_SHIFT * alpha_V)
   const uint8_t *vr;           // R of the values as fp16 hi, lo tile images
 };
 // Norms in the operands: up to 2^13 times a scaled centroid (below 4) stays below 2^15.
 constexpr int NORM_EXP = 12;
-constexpr int SROW = D + 4;    // floats of a partial row: o[128], max, sum, 2 spare
+// Floats of a 128-row partial: float4 e of row r at e * 128 + r, so that the threads of a warp, a row
+// each, write 512 bytes in a row (a row at a time they took 5 us an item); then maxima, sums.
+constexpr int PART = 128 * D + 256;
 
 // ------------------------------------------------------------------------------ schedule
 struct Seq {
@@ -1127,20 +1129,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       if (tid == 0 && (int)blockIdx.x != first)
         p.join[blockIdx.x] = JoinInfo{it.s.row + it.qt * p.qpu, it.s.T - it.qt * p.qpu, 0, it.h, first, n_split};
       if (n_split > 1) {
-        float *dst = p.split + ((size_t)(blockIdx.x * 2 + ((int)blockIdx.x == first ? 1 : 0)) * (ALT ? 128 : 256) +
-                                gr * 128 + r) * SROW;
+        float *part = p.split + ((size_t)(blockIdx.x * 2 + ((int)blockIdx.x == first ? 1 : 0)) * (ALT ? 1 : 2) + gr) * PART;
 #pragma unroll 1
         for (int cc = 0; cc < 4; ++cc) {
           float o[32];
           tmem_ld32(tO + 32 * cc, o);
           if (live) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4 *>(dst + 32 * cc + e) = make_float4(o[e] * back, o[e + 1] * back, o[e + 2] * back, o[e + 3] * back);
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<float4 *>(part)[(8 * cc + e) * 128 + r] =
+                  make_float4(o[4 * e] * back, o[4 * e + 1] * back, o[4 * e + 2] * back, o[4 * e + 3] * back);
           }
           __syncwarp();
         }
-        if (live) dst[D] = M, dst[D + 1] = l;
+        if (live) part[128 * D + r] = M, part[128 * D + 128 + r] = l;
         continue;
       }
       const DiffView &df = p.o.diff;
@@ -1217,12 +1219,13 @@ struct JoinParams {
   const JoinInfo *join;
   const float *split;
 };
-constexpr int JOIN_WARPS = 8;
-constexpr int JOIN_FLY = 4;  // parts in flight per warp
+constexpr int JOIN_WARPS = 8, JOIN_ROWS = 16;
 
-// CTA (c, i): rows of the unit whose second share is CTA c's, a warp per row (per pair):
-// o = sum w_s o_s / sum w_s with w_s = l_s 2^(m_s - m*), JOIN_FLY partials in flight.
+// CTA (c, y): 16 rows of the unit whose second share is CTA c's: o = sum w_s o_s / sum w_s with
+// w_s = l_s 2^(m_s - m*).  Lane (e, r) of a warp takes row r of eight and two float4 of the 32, so that loads
+// follow the partials' layout; four warps make up the rows, four parts of each are in flight.
 __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const JoinParams p) {
+  __shared__ float sums[JOIN_WARPS][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();
@@ -1231,49 +1234,80 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const JoinParams
   if (j.n < 2 || j.first != c - 1) return;
   const int ns = min(j.n, p.grid - j.first);
   const bool diff = p.o.diff.lambda != nullptr;
-  const int r = (blockIdx.y * JOIN_WARPS + warp) * (diff ? 2 : 1), rr = r & 127, rq = rr / p.gq;
-  const int qi = (r >> 7) * p.qpt + rq;
-  if (rq >= p.qpt || qi >= j.T) return;
-  const int head = j.h * p.gq + rr - rq * p.gq;
-  float a[2][4];
+  const int r = JOIN_ROWS * blockIdx.y + 8 * (warp >> 2) + (lane & 7), rr = r & 127, rq = rr / p.gq;
+  const int qi = (r >> 7) * p.qpt + rq, head = j.h * p.gq + rr - rq * p.gq, e0 = 8 * (warp & 3) + (lane >> 3);
+  const bool live = rq < p.qpt && qi < j.T;
+  auto part_of = [&](int s) {
+    return p.split + ((size_t)((j.first + s) * 2 + (s == 0 ? 1 : 0)) * (p.unit_rows / 128) + (r >> 7)) * PART;
+  };
+  constexpr int FLY = 4;
+  float a[2][4] = {}, top = -INFINITY, sum = 0.f;
+  for (int s0 = 0; s0 < ns; s0 += FLY) {
+    float mx[FLY], lx[FLY];
+    float4 v[FLY][2];
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    float ms = -INFINITY, ls = 0.f;
-    a[m][0] = a[m][1] = a[m][2] = a[m][3] = 0.f;
-    if (m && !diff) break;
-    for (int s0 = 0; s0 < ns; s0 += JOIN_FLY) {
-      float mx[JOIN_FLY], lx[JOIN_FLY];
-      float4 v[JOIN_FLY];
+    for (int i = 0; i < FLY; ++i) {
+      mx[i] = lx[i] = 0.f, v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (live && s0 + i < ns) {
+        const float *part = part_of(s0 + i);
+        mx[i] = __ldcg(part + 128 * D + rr), lx[i] = __ldcg(part + 128 * D + 128 + rr);
 #pragma unroll
-      for (int i = 0; i < JOIN_FLY; ++i) {
-        const int s = s0 + i;
-        mx[i] = lx[i] = 0.f, v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (s < ns) {
-          const float *src = p.split + ((size_t)((j.first + s) * 2 + (s == 0 ? 1 : 0)) * p.unit_rows + r + m) * SROW;
-          mx[i] = __ldcg(src + D), lx[i] = __ldcg(src + D + 1);
-          v[i] = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < JOIN_FLY; ++i) {
-        if (lx[i] == 0.f) continue;
-        const float mn = fmaxf(ms, mx[i]), f = exp2f(ms - mn), wx = lx[i] * exp2f(mx[i] - mn);
-        ms = mn;
-        ls = fmaf(ls, f, wx);
-        a[m][0] = fmaf(a[m][0], f, wx * v[i].x), a[m][1] = fmaf(a[m][1], f, wx * v[i].y);
-        a[m][2] = fmaf(a[m][2], f, wx * v[i].z), a[m][3] = fmaf(a[m][3], f, wx * v[i].w);
+        for (int h = 0; h < 2; ++h) v[i][h] = __ldcg(reinterpret_cast<const float4 *>(part) + (e0 + 4 * h) * 128 + rr);
       }
     }
-    const float f = ls == 0.f ? 0.f : 1.f / ls;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a[m][e] *= f;
+    for (int i = 0; i < FLY; ++i) {
+      if (lx[i] == 0.f) continue;
+      const float mn = fmaxf(top, mx[i]), f = exp2f(top - mn), wx = lx[i] * exp2f(mx[i] - mn);
+      top = mn;
+      sum = fmaf(sum, f, wx);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        a[h][0] = fmaf(a[h][0], f, wx * v[i][h].x), a[h][1] = fmaf(a[h][1], f, wx * v[i][h].y);
+        a[h][2] = fmaf(a[h][2], f, wx * v[i][h].z), a[h][3] = fmaf(a[h][3], f, wx * v[i][h].w);
+      }
+    }
   }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[h][e] *= inv;
   const int64_t row = j.row + qi;
-  if (diff) {
-    diff_finish(a[0], a[1], p.o.diff, (int)row, head >> 1, lane);
-    store_lane4(p.o.out, p.o.dtype, (row * (p.Hq / 2) + (head >> 1)) * D, lane, a[0]);
-  } else {
-    store_lane4(p.o.out, p.o.dtype, (row * p.Hq + head) * D, lane, a[0]);
+  if (!diff) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (live) store_lane4(p.o.out, p.o.dtype, (row * p.Hq + head) * D, e0 + 4 * h, a[h]);
+    return;
+  }
+  // rows r and r ^ 1 are a pair, finished by the even one
+  const DiffView &d = p.o.diff;
+  const float lam = live ? d.lambda[row * d.lambda_stride + (head >> 1)] : 0.f;
+  float ss = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a[h][e] = fmaf(-lam, __shfl_xor_sync(FULL_MASK, a[h][e], 1), a[h][e]);
+      ss = fmaf(a[h][e], a[h][e], ss);
+    }
+  float f = d.out_scale;
+  if (d.gain) {
+    ss += __shfl_xor_sync(FULL_MASK, ss, 8);
+    ss += __shfl_xor_sync(FULL_MASK, ss, 16);
+    if (lane < 8) sums[warp][lane] = ss;
+    __syncthreads();
+    const int w0 = warp & ~3, q = lane & 7;
+    ss = (sums[w0][q] + sums[w0 + 1][q]) + (sums[w0 + 2][q] + sums[w0 + 3][q]);
+    // all zero (a row without keys) stays zero whatever eps is; NaN stays
+    f = ss == 0.f ? 0.f : f * rsqrtf(fmaf(ss, 1.0f / D, d.eps));
+  }
+  if (!live || (r & 1)) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float4 g = d.gain ? reinterpret_cast<const float4 *>(d.gain)[e0 + 4 * h] : make_float4(1.f, 1.f, 1.f, 1.f);
+    a[h][0] *= f * g.x, a[h][1] *= f * g.y, a[h][2] *= f * g.z, a[h][3] *= f * g.w;
+    store_lane4(p.o.out, p.o.dtype, (row * (p.Hq / 2) + (head >> 1)) * D, e0 + 4 * h, a[h]);
   }
 }
 
@@ -1301,7 +1335,7 @@ bool layout(const tq_ctx *k, const PagedView &pv, int Hq, int out_dtype, Layout 
   l->start = l->prefix + up((size_t)(pv.B + 1) * 4);
   l->join = l->start + up((size_t)l->grid * sizeof(Start));
   l->split = l->join + up((size_t)l->grid * sizeof(JoinInfo));
-  l->bytes = l->split + up((size_t)l->grid * 2 * l->unit_rows * SROW * 4);
+  l->bytes = l->split + up((size_t)l->grid * 2 * (l->unit_rows / 128) * PART * 4);
   return true;
 }
 
@@ -1363,8 +1397,7 @@ cudaError_t launch_paged_prefill(const tq_ctx *k, const tq_ctx *v, const PagedVi
   j.o = o;
   j.Hq = Hq, j.gq = l.gq, j.qpt = l.qpt, j.unit_rows = l.unit_rows, j.grid = l.grid;
   j.join = p.join, j.split = p.split;
-  return launch_pdl(k_paged_join, dim3(l.grid, l.unit_rows / (JOIN_WARPS * (o.diff.lambda ? 2 : 1))),
-                    dim3(JOIN_WARPS * 32), 0, st, j);
+  return launch_pdl(k_paged_join, dim3(l.grid, l.unit_rows / JOIN_ROWS), dim3(JOIN_WARPS * 32), 0, st, j);
 }
 
 }  // namespace tq

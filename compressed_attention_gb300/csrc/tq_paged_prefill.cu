@@ -52,7 +52,7 @@ constexpr int KT = 128;                // keys per tile
 constexpr int UNIT_TILES = 3;          // cost of an item ahead of its tiles, in tiles
 constexpr int RAW = KT * PG_ROW;       // a packed tile
 constexpr int NRAW = 3;
-constexpr int W_DEC = 8, W_MMA = 16, W_LOAD = 18, N_WARPS = 20;  // the last warp only fills its group
+constexpr int W_DEC = 8, W_MMA = 16, W_LOAD = 18, W_Q = 19, N_WARPS = 20;
 constexpr int THREADS = N_WARPS * 32;
 // Registers: 640 threads x 96 at launch; the softmax groups take 128 (64 scores, 32 packed
 // probabilities), the other three groups give theirs up to 72 (the decoders' 17 words of a row
@@ -67,7 +67,8 @@ constexpr uint32_t OFF_RAW = 6 * SW_TILE_BYTES, OFF_MISC = OFF_RAW + NRAW * RAW;
 struct Misc {
   uint64_t raw_full[NRAW], raw_empty[NRAW];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_ready[2], drain[2];   // [group]
+  uint64_t q_full[2], q_empty[2];  // q's tiles (ALT: the first, for both groups and parts)
+  uint64_t s_free[2], drain[2];    // [group] the un-rotation has read the columns of S (ALT: the first)
   // [group][half of the key tile]: a thread that waits for a phase of one of these is at most one
   // phase behind, so that the parity tells; the items' final P and un-rotation use half 0 and 1
   uint64_t s_done[2][2], p_ready[2][2], pv_done[2][2];
@@ -96,13 +97,30 @@ struct JoinInfo {
   int row, T, base, h, first, n;  // first batch row of the unit, its rows, position of row 0, KV head
 };
 
+// Prepared q as images of the operand tiles: for each KV head, part and half of the dims the rows
+// (64 dims, 128 bytes, 16-byte chunk c of row r at c ^ (r % 8)) of all 128-row tiles one after the
+// other, so that a tile is loaded by a bulk copy per part and half.  A sequence's tiles start at a
+// multiple of eight rows and take tr = 8 ceil(qpt gq / 8) each.  With phi(x) = tr floor(x / qpt) + gq (x mod qpt),
+// which is superadditive, 8 ceil(phi(a) / 8) + 8 b is past the rows of all sequences before
+// sequence b of first row a, whatever their lengths: no sums over sequences.
+struct QImage {
+  int gq, qpt, tr, rows;  // rows: of a plane
+  __host__ __device__ static int phi(int x, int gq, int qpt, int tr) { return x / qpt * tr + x % qpt * gq; }
+  __device__ __forceinline__ int first(int a, int b) const { return ((phi(a, gq, qpt, tr) + 7) & ~7) + 8 * b; }
+  // element offset of image row r in the plane of (KV head, part, half)
+  __device__ __forceinline__ size_t at(int h, int parts, int part, int half, int r) const {
+    return (((size_t)(h * parts + part) * 2 + half) * rows + r) * 64;
+  }
+};
+
 struct PrefillParams {
   PagedView pv;
   const uint8_t *kp, *vp;
   PagedOut o;
   int Hq, gq, qpt, qpu;        // q-heads; per KV head; queries per 128-row tile; per unit
-  const uint16_t *qh;          // prepared q: [row][2 parts][128] fp16
-  const float *qsc;            // [row] power-of-two scales
+  const uint16_t *qh;          // prepared q: see QImage
+  const float *qsc;            // [KV head][image row] power-of-two scales
+  QImage qi;
   const Start *start;          // per CTA
   JoinInfo *join;              // per CTA: the unit its first item continues
   float *split;                // [CTA][2][128-row tiles of a unit][PART] partials
@@ -194,6 +212,7 @@ struct PrepParams {
   const uint4 *kfrag;
   uint16_t *qh;
   float *qsc;
+  QImage qi;
   int32_t *prefix;        // [B + 1] virtual tiles ahead of each sequence
   Start *start;
   JoinInfo *join;
@@ -365,13 +384,17 @@ __global__ void __launch_bounds__(PREP_WARPS * 32) k_paged_prep(const PrepParams
   // tiles over the CTAs first: a few rows use as many SMs as they can
   for (int64_t tile = (int64_t)warp * ctas + blockIdx.x - 1; tile * 16 < n; tile += (int64_t)PREP_WARPS * ctas) {
     const int64_t r0 = tile * 16;
-    int my_tok = -1, my_pos = -1;  // of row r0 + lane, and its address (0: no key)
+    int my_tok = -1, my_pos = -1;  // of row r0 + lane, its address (0: no key), and its place in q's image
     uint64_t my_src = 0;
+    int my_row = -1, my_kvh = 0;
     if (lane < 16 && r0 + lane < n) {
       my_tok = (int)((uint32_t)(r0 + lane) / (uint32_t)p.Hq);
       const int b = paged_seq(p.pv, my_tok);
       my_pos = paged_pos(p.pv, b, my_tok, paged_len(p.pv, b, false));
-      const int h = (int)(r0 + lane - (int64_t)my_tok * p.Hq);
+      const int h = (int)(r0 + lane - (int64_t)my_tok * p.Hq), a = p.pv.cu_q ? p.pv.cu_q[b] : b, li = my_tok - a;
+      my_kvh = h / p.qi.gq;
+      if (a >= 0 && li >= 0)
+        my_row = p.qi.first(a, b) + QImage::phi(li, p.qi.gq, p.qi.qpt, p.qi.tr) + h - my_kvh * p.qi.gq;
       if (my_pos >= 0) my_src = (uint64_t)(uintptr_t)(p.q.data + my_tok * p.q.token_bytes + h * p.q.head_bytes);
     }
     for (uint32_t m = __ballot_sync(FULL_MASK, my_tok >= 0 && my_pos < 0); m; m &= m - 1) {  // no key: the row's output is zero
@@ -467,32 +490,36 @@ __global__ void __launch_bounds__(PREP_WARPS * 32) k_paged_prep(const PrepParams
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t r = r0 + g + 8 * i;
+      const int row = __shfl_sync(FULL_MASK, my_row, g + 8 * i), kvh = __shfl_sync(FULL_MASK, my_kvh, g + 8 * i);
       float m = amax[i];
       m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, 1));
       m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, 2));
-      if (r >= n) continue;
+      if (row < 0) continue;
       // The power of two that brings the largest element to [2^13, 2^14).  One part leaves rows alone
       // whose largest element already lies in [2^-10, 2^14) (what fp16 drops there is below 2^-14 of
-      // it): their scores then need no scaling in the softmax.
+      // it).
       const bool as_is = !p.lo && m >= 0x1p-10f && m < 0x1p14f;
       const int e = as_is ? 0 : scale_exp(m);
       const float down = pow2i(-e);
-      uint16_t *dst = p.qh + (size_t)r * 2 * D;
-      if (p.lo) {
+      const int parts = p.lo ? 2 : 1;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          uint32_t hi, lo;
-          split_half2(acc[j][2 * i] * down, acc[j][2 * i + 1] * down, hi, lo);
-          *reinterpret_cast<uint32_t *>(dst + 8 * j + 2 * t) = hi;
-          *reinterpret_cast<uint32_t *>(dst + D + 8 * j + 2 * t) = lo;
+      for (int half = 0; half < 2; ++half) {
+        uint16_t *hi_p = p.qh + p.qi.at(kvh, parts, 0, half, row) + 2 * t;
+        uint16_t *lo_p = p.qh + p.qi.at(kvh, parts, parts - 1, half, row) + 2 * t;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int j = 8 * half + c, to = 8 * (c ^ (row & 7));
+          if (p.lo) {
+            uint32_t hi, lo;
+            split_half2(acc[j][2 * i] * down, acc[j][2 * i + 1] * down, hi, lo);
+            *reinterpret_cast<uint32_t *>(hi_p + to) = hi;
+            *reinterpret_cast<uint32_t *>(lo_p + to) = lo;
+          } else {
+            *reinterpret_cast<uint32_t *>(hi_p + to) = pack_half2(acc[j][2 * i] * down, acc[j][2 * i + 1] * down);
+          }
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          *reinterpret_cast<uint32_t *>(dst + 8 * j + 2 * t) = pack_half2(acc[j][2 * i] * down, acc[j][2 * i + 1] * down);
       }
-      if (t == 0) p.qsc[r] = pow2i(e);
+      if (t == 0) p.qsc[(size_t)kvh * p.qi.rows + row] = pow2i(e);
     }
   }
   // (a CTA without rows: R's copy must land before it ends)
@@ -557,7 +584,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
         mbar_init(&ms.s_done[i][h], 1), mbar_init(&ms.p_ready[i][h], 4);
         mbar_init(&ms.pv_done[i][h], 1);
       }
-      mbar_init(&ms.drain[i], 1), mbar_init(&ms.q_ready[i], 4);
+      mbar_init(&ms.drain[i], 1), mbar_init(&ms.s_free[i], 1);
+      mbar_init(&ms.q_full[i], 1), mbar_init(&ms.q_empty[i], ALT ? 2 : 1);
     }
     ms.abort_flag = 0;
     fence_mbar_init();
@@ -617,6 +645,33 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
     if (*reinterpret_cast<volatile int *>(&ms.abort_flag))
       for (uint32_t c = n > NRAW ? n - NRAW : 0; c < n; ++c)
         (void)mbar_wait_bounded(&ms.raw_full[c % NRAW], (c / NRAW) & 1, WAIT_LIMIT_NS);
+  } else if (warp == W_Q) {
+    // ================ q's tiles, each as soon as the last item's scores are done
+    uint32_t nl[2] = {0, 0};
+    while (ok && next_item(p, w, it)) {
+#pragma unroll
+      for (int gr = 0; gr < (ALT ? 1 : 2); ++gr) {
+        const int q0 = it.qt * p.qpu + gr * p.qpt;
+        if (!ok || q0 >= it.s.T) continue;
+        if (nl[gr]) ok = __all_sync(FULL_MASK, wait(&ms.q_empty[gr], (nl[gr] - 1) & 1));
+        if (!ok) continue;
+        const int row = p.qi.first(it.s.row, it.b) + q0 / p.qpt * p.qi.tr;
+        const uint32_t bytes = min(p.qi.tr, ((it.s.T - q0) * p.gq + 7) & ~7) * 128;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ms.q_full[gr], bytes * (LO ? 4 : 2));
+#pragma unroll
+          for (int x = 0; x < (LO ? 4 : 2); ++x)  // part, half
+            bulk_g2s(smem + OFF_Q + (gr + (x >> 1)) * SW_TILE_BYTES + (x & 1) * SW_HALF_BYTES,
+                     p.qh + p.qi.at(it.h, LO ? 2 : 1, x >> 1, x & 1, row), bytes, &ms.q_full[gr]);
+        }
+        __syncwarp();
+        ++nl[gr];
+      }
+    }
+    // after a failed wait: let the copies in flight land before the CTA ends
+    if (*reinterpret_cast<volatile int *>(&ms.abort_flag))
+      for (int gr = 0; gr < 2; ++gr)
+        if (nl[gr]) (void)mbar_wait_bounded(&ms.q_full[gr], (nl[gr] - 1) & 1, WAIT_LIMIT_NS);
   } else if (warp < W_MMA) {
     // ================ decoders: a group for the keys, one for the values, thread = row of the tile
     const int row = tid & 127;
@@ -710,8 +765,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
     const uint32_t tS = __shfl_sync(FULL_MASK, tmem, 0) + TM_S + 128 * gr, tO = tS + TM_O - TM_S;
     const uint64_t dq = sw128_desc(smem_addr(smem + OFF_Q) + (ALT ? 0 : gr) * SW_TILE_BYTES);
     const uint64_t dk = sw128_desc(smem_addr(smem + OFF_K)), dv = sw128_mn_desc(smem_addr(smem + OFF_V));
-    uint32_t kc = 0, vc = 0, nq = 0, nt = 0;  // K, V stages passed; items begun; tiles
-    uint32_t nf = 0, nt1 = 0;  // items finished; ALT, group 0: group 1's tiles
+    uint32_t kc = 0, vc = 0, nt = 0;  // K, V stages passed; tiles
+    uint32_t nf = 0, nt1 = 0;         // items finished; ALT, group 0: group 1's tiles
     bool issued = false;
     // where P's K-step s (of a half, or of a whole row for the un-rotation) lies
     auto p_col = [](int part, int s) { return LO ? 32 * (s >> 1) + 16 * part + 8 * (s & 1) : 8 * s; };
@@ -729,9 +784,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           ok = __all_sync(FULL_MASK, ok);
         }
       } else {
-        ok = wait(&ms.q_ready[gr], nq & 1);
-        if (ALT && ok) ok = wait(&ms.q_ready[gr ^ 1], nq & 1);
-        ++nq;
+        // q, and the columns of S: the last item's un-rotation has read them
+        ok = wait(&ms.q_full[ALT ? 0 : gr], nf & 1);
+        if (ok && nf) ok = wait(&ms.s_free[ALT ? 0 : gr], (nf - 1) & 1);
         if (!(ok = __all_sync(FULL_MASK, ok))) break;
         tc_fence_after();
         // S of half m & 1 (64 keys) of the group's tile m / 2
@@ -749,11 +804,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
                               desc_step(kb, sw128_kstep(s)), (part || s) ? 1u : 0u);
             umma_commit(&ms.s_done[gr][h]);
             if (h) umma_commit(&ms.k_empty[c & 1]);
+            if (m == 2 * tiles - 1) umma_commit(&ms.q_empty[ALT ? 0 : gr]);
           }
           __syncwarp();
           issued = true;
           return true;
         };
+        if (ALT && tiles == 0 && lead) mbar_arrive(&ms.q_empty[0]);
         for (int m = 0; ok && m < 2 && m < 2 * tiles; ++m) ok = issue_s(m);
         for (int m = 0; ok && m < 2 * tiles; ++m) {
           const uint32_t c = vc + i0 + step * (m >> 1), h = m & 1;
@@ -813,7 +870,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           }
           __syncwarp();
         }
-        if (ok && act && lead) umma_commit(&ms.pv_done[gr][1]);
+        if (ok && act && lead) umma_commit(&ms.pv_done[gr][1]), umma_commit(&ms.s_free[gr]);
       }
       if (act) ++nf;  // (ALT: group 1's last P is waited for by group 0's issuer)
       vc += R_TILES;
@@ -847,21 +904,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       const int head = it.h * p.gq + rh;
       const int64_t qrow = brow * p.Hq + head;
       const int pos = live ? it.s.base + qi : -1;
-      const float rsc = live ? p.qsc[qrow] : 0.f;
+      const float rsc = live ? p.qsc[(size_t)it.h * p.qi.rows + p.qi.first(it.s.row, it.b) + q0 / p.qpt * p.qi.tr + r] : 0.f;
       [[maybe_unused]] const uint64_t rsc2 = pk2(rsc, rsc);
-      if (!ALT || LO || gr == 0) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.qh + (size_t)qrow * 2 * D + (LO ? gr * D : 0));
-        uint8_t *dst = smem + OFF_Q + gr * SW_TILE_BYTES;
-        uint4 v[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) v[c] = live ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4 *>(dst + sw128_offset(r, 8 * c)) = v[c];
-        fence_async_smem();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms.q_ready[gr]);
-
       float M = -INFINITY, l = 0.f;
       int done = 0;  // halves
       // halves of 64 keys: the other half's PV and next S run under this one's softmax
@@ -1313,6 +1357,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const JoinParams
 
 struct Layout {
   int gq, qpt, qpu, grid, unit_rows;
+  QImage qi;
   bool alt, lo;
   size_t qsc, prefix, start, join, split, bytes;
 };
@@ -1329,9 +1374,12 @@ bool layout(const tq_ctx *k, const PagedView &pv, int Hq, int out_dtype, Layout 
   const int64_t tiles = units * (((int64_t)pv.max_len + KT - 1) / KT + UNIT_TILES);
   if (tiles > INT32_MAX || (int64_t)pv.n_tokens * Hq > INT32_MAX) return false;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  const size_t rows = (size_t)pv.n_tokens * Hq;
-  l->qsc = up(rows * 2 * D * 2);
-  l->prefix = l->qsc + up(rows * 4);
+  const int tr = (l->qpt * l->gq + 7) & ~7;
+  const int64_t plane = (int64_t)pv.n_tokens / l->qpt * tr + (int64_t)(pv.n_tokens % l->qpt) * l->gq + 8 + 8 * ((int64_t)pv.B + 1);
+  if (plane * pv.Hkv > INT32_MAX) return false;
+  l->qi = QImage{l->gq, l->qpt, tr, (int)plane};
+  l->qsc = up((size_t)pv.Hkv * (l->lo ? 2 : 1) * plane * D * 2);
+  l->prefix = l->qsc + up((size_t)pv.Hkv * plane * 4);
   l->start = l->prefix + up((size_t)(pv.B + 1) * 4);
   l->join = l->start + up((size_t)l->grid * sizeof(Start));
   l->split = l->join + up((size_t)l->grid * sizeof(JoinInfo));
@@ -1363,7 +1411,7 @@ cudaError_t launch_paged_prefill(const tq_ctx *k, const tq_ctx *v, const PagedVi
   uint8_t *base = static_cast<uint8_t *>(ws);
   PrepParams a{};
   a.pv = pv, a.q = q, a.rope = rope, a.o = o;
-  a.Hq = Hq, a.qpu = l.qpu, a.grid = l.grid;
+  a.Hq = Hq, a.qpu = l.qpu, a.grid = l.grid, a.qi = l.qi;
   a.qmul = LOG2E * scale / k->f16.alpha;
   a.kfrag = k->d_rfrag;
   a.qh = reinterpret_cast<uint16_t *>(base);
@@ -1382,7 +1430,7 @@ cudaError_t launch_paged_prefill(const tq_ctx *k, const tq_ctx *v, const PagedVi
   PrefillParams p{};
   p.pv = pv, p.kp = kp, p.vp = vp, p.o = o;
   p.Hq = Hq, p.gq = l.gq, p.qpt = l.qpt, p.qpu = l.qpu;
-  p.qh = a.qh, p.qsc = a.qsc, p.start = a.start, p.join = a.join;
+  p.qh = a.qh, p.qsc = a.qsc, p.qi = l.qi, p.start = a.start, p.join = a.join;
   p.split = reinterpret_cast<float *>(base + l.split);
   for (int i = 0; i < 2; ++i) {
     p.klo[i] = k->f16.lo[i], p.khi[i] = k->f16.hi[i];

@@ -3,26 +3,29 @@
 //
 //   k_paged_prep      CTA 0 plans: the key tiles (128 keys) of all units (sequence, tile of
 //                     queries, KV head) laid end to end, each after a few empty tiles for its
-//                     start, cut into one equal share per CTA.  The other CTAs rotate q by
-//                     position (fp32) and by R (bf16 parts, m16n8k16) and round it to fp16
-//                     parts; rows without a key get their zeros.
+//                     start, cut into one equal share per CTA.  In the other CTAs each warp
+//                     turns 16 rows of q by position (fp32), by R (bf16 parts, m16n8k16) and
+//                     rounds them to fp16 parts, stored as images of the operand tiles; rows
+//                     without a key get their zeros.
 //   k_paged_prefill   persistent, one CTA per SM, specialised warps:
-//                       loader     packed tiles, one bulk copy per page, on a ring of three
-//                       decoders   4 warps: nibbles -> fp16 centroids (byte permutes) in
-//                                  128-byte swizzled operand tiles, two stages each of K
-//                                  and V.  Both are written row by row as 16-byte chunks:
-//                                  K is the K-major B operand of S = Q K^T, V the MN-major B
-//                                  operand of O += P V, so V needs no transposition.
+//                       loaders    packed tiles, one bulk copy per page, on a ring of three;
+//                                  q's tiles, one copy per part and half of the dims
+//                       decoders   4 warps each for K and V: nibbles -> fp16 centroids (byte
+//                                  permutes) in 128-byte swizzled operand tiles, two stages
+//                                  each.  Both are written row by row as 16-byte chunks: K
+//                                  is the K-major B operand of S = Q K^T, V the MN-major B
+//                                  operand of O += P V, so V needs no transposition.  In one part
+//                                  the rows' norms go into the operands: the softmax then reads
+//                                  no norms (two 16-byte reads of shared memory per four scores
+//                                  of every row, a quarter of its traffic).
 //                       2 issuers  one thread each for S, PV and the un-rotation of one
 //                                  softmax group
-//                       softmax    2 groups of 4 warps, a thread per accumulator row.  S is
-//                                  read from tensor memory once: the exponentials are taken
-//                                  against the running maximum of earlier tiles, the fp16
-//                                  probabilities (value norm folded in) are kept in
-//                                  registers, and only when their sum passed 2^15 is the maximum
-//                                  raised, O rescaled and the pass repeated; then P takes
-//                                  over S's columns.
-//                     While one group is in its softmax, the other one's products run.
+//                       softmax    2 groups of 4 warps, a thread per accumulator row, 64 keys at a
+//                                  time while the other 64 columns' products run.  The
+//                                  exponentials are taken against the running maximum of
+//                                  earlier tiles, and only when the probabilities' sum passed
+//                                  2^15 is the maximum raised, O rescaled and the pass repeated;
+//                                  then P takes over S's columns.
 //                     Groups take two 128-row tiles of one unit (sharing the decoded K and
 //                     V), or, where a unit has at most 128 rows or q and P are carried in
 //                     two parts, alternate key tiles of one 128-row tile.
@@ -31,9 +34,20 @@
 //                     one CTA is finished there: differential pairs, norm, rounding.
 //   k_paged_join      units shared by CTAs: the log-sum-exp merge of their partials.
 //
-// Parts: for bf16 outputs q, P and O / l enter as one fp16 each (errors of 2^-12, random over
-// 128 dims or the keys: 3e-4 of the output's norm next to bf16's own 1.7e-3); for fp16 and
-// fp32 outputs as hi + lo, which leaves the fp16 centroid table's 3e-5.
+// Parts: for bf16 outputs q, K, V, P and O / l enter as one fp16 each (errors of 2^-12, random
+// over 128 dims or the keys: 4e-4 of the output's norm next to bf16's own 1.7e-3); for fp16
+// and fp32 outputs q, P and O / l as hi + lo and K, V as centroids with fp32 norms outside the
+// products, which leaves the fp16 centroid table's 3e-5.
+//
+// Measured (GB300): 4 chunks of 200 .. 512 tokens on 4K .. 16K keys, 32 q-heads on 8, bf16: 240 us
+// for 199 GFLOP (prep 20, join 13, the rest the attention), 43% of the cuBLAS bf16 rate; prompts of
+// 129 .. 2047 tokens, 8 heads on 8, fp16 in two parts: 75 us.  A step of 64 keys takes 1.2 us
+// for 2 x 128 rows: 0.9 us from S to P (64 exponentials a thread, beside the decoders' issue slots) and
+// 0.3 us of barriers between the roles.  Shared memory carries 37% operands and 39% loads and
+// stores of its bandwidth, the issue slots are half used, the tensor pipe 39%: no one unit is
+// full, the chain S -> P -> PV -> S of a group is.  Tried and slower: two threads a row
+// (28 warps, 375 us when this form took 312), scores in registers ahead of the next product
+// (spills at the registers 640 threads leave: 298 us to 240), 152 and 56 registers.
 #include <math.h>
 #include <stddef.h>
 
@@ -709,7 +723,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           // rounding an element, like q's and P's; a norm 2^20 times smaller than the largest keeps
           // its precision.
           const float an = fabsf(norm);
-          const bool bad = !(an < INFINITY);
+          const bool bad = !(an < (side ? 0x1p120f : INFINITY));  // (past 2^120 a sum of weights would underflow)
           const uint32_t most = __reduce_max_sync(FULL_MASK, bad ? 0u : __float_as_uint(an));
           const int em = max((int)(most >> 23) - 127, side ? -64 : -114);
           const float sn = side && bad ? 0.f : norm * pow2i(NORM_EXP - em);

@@ -408,7 +408,7 @@ typedef struct tq_paged_batch {
   int32_t B;                /* >= 0 (0: nothing is done) */
   int32_t max_q;            /* >= 1: at least the largest cu_q[b+1] - cu_q[b] (rows of a sequence
                                past it are left out of the attention, flagged with status 2) */
-  int32_t n_tokens;         /* rows of the buffers; at least cu_q[B] */
+  int32_t n_tokens;         /* rows of the buffers; at least cu_q[B]; n_tokens * Hkv <= 2^30 */
   int32_t max_len;          /* bound on the lengths, 0 = table_len * page_size.  Sizes the split
                                of the work only: a tight bound is faster */
 } tq_paged_batch;
@@ -447,7 +447,8 @@ tq_status tq_make_rope_table(int rot_dim, double base, int64_t n_pos, float *cos
  * where the rotated coordinate lies within 1e-5 of a boundary.
  *   k, v   rows [n_tokens][Hkv][128], one dtype (F32, BF16 or F16).
  * A row whose page id is out of range is skipped and flagged (status 5).  Two sequences
- * that share the page of an appended row race.  One launch. */
+ * that share the page of an appended row race.  One launch (two where keys and values have
+ * different rotation kinds). */
 tq_status tq_paged_append(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
                           const tq_paged_batch *batch, const tq_rows *k, const tq_rows *v,
                           const tq_rope *rope, tq_stream_t stream);
@@ -478,7 +479,11 @@ tq_status tq_paged_gather(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_pag
  * of ordinary size the rows are within 2e-3 absolute and 1e-3 relative of the formula, as
  * tq_decode_attention's, before the rounding to out_dtype; a score itself is off by at most
  * about 7e-5 scale |q| |k_hat| (the fp16 centroid table; chunks with a BF16 output add q's
- * own rounding to fp16), which is what counts where scores reach the hundreds. */
+ * and the keys' own rounding to fp16), which is what counts where scores reach the hundreds.
+ * Chunks with a BF16 output also carry the values in fp16, the largest norm of 32 neighbours
+ * at 2^12 to 2^13: a row that sees only values 2^20 times smaller than a neighbour's is
+ * off by up to 1e-10 of that neighbour's norm.  A key with a NaN norm, or a value whose norm is
+ * not finite (there: not below 2^120), makes the rows that see it not finite, and no others. */
 tq_status tq_paged_workspace_size(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
                                   const tq_paged_batch *batch, int Hq, size_t *bytes);
 tq_status tq_paged_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,

@@ -382,6 +382,39 @@ def test_chunks(case):
     check_attention(got, ref, out_dtype)
 
 
+@pytest.mark.parametrize("out_dtype", ["bf16", "f16"])
+def test_chunks_of_many_short_sequences(out_dtype):
+    """More sequences than the plan's threads take at once, most of them below a tile's rows, some empty."""
+    tq = lib()
+    rng = np.random.default_rng(61)
+    new = rng.integers(0, 7, 700)
+    new[5], new[300] = 90, 41
+    lens = new + rng.integers(0, 30, 700) * rng.integers(0, 2, 700)
+    s = Setup(tq, lens.tolist(), new.tolist(), 1, 16, 61, ("dense", "wht"), pad=3)
+    got, ref = run_attention(s, 3, "bf16", out_dtype, 64)
+    check_attention(got, ref, out_dtype)
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+def test_chunks_of_many_query_tiles(out_dtype):
+    """A sequence of more query tiles than a warp has lanes, between short ones."""
+    tq = lib()
+    s = Setup(tq, [40, 1230, 9], [3, 1200, 9], 1, 32, 62, ("wht", "dense"))
+    got, ref = run_attention(s, 16, "bf16", out_dtype, 128)
+    check_attention(got, ref, out_dtype)
+
+
+def test_single_rows_of_many_sequences():
+    tq = lib()
+    rng = np.random.default_rng(63)
+    lens = rng.integers(0, 60, 500)
+    lens[77], lens[401] = 3000, 700
+    for Hq in (3, 7):  # one group of heads, two
+        s = Setup(tq, lens.tolist(), [1] * 500, 1, 16, 63, ("wht", "dense"), ragged=False)
+        got, ref = run_attention(s, Hq, "bf16", "f32", 32)
+        check_attention(got, ref, "f32")
+
+
 def test_chunks_sharp_softmax():
     tq = lib()
     s = Setup(tq, [500, 250], [100, 250], 1, 16, 13)

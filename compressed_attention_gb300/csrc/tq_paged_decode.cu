@@ -73,6 +73,7 @@ struct Head {
   float mh[8], lh[8];      // the item's maxima and sums
   int abort_flag;
   int V, G;                // the V virtual tiles are shared by G CTAs
+  int first, n_split;      // the CTAs that share the item's unit
 };
 struct Tail {
   uint32_t q[8][D];        // fp16 hi then lo of the item's rotated q
@@ -370,7 +371,7 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
   bool aborted = false;
   // an item's first q-head and heads; warp h < heads loads head h's row and its angles
   auto heads_of = [&](const Item &i, int &head0, int &GH) {
-    const int kvh = i.u / p.n_hg, hg = i.u - kvh * p.n_hg;
+    const int kvh = p.n_hg == 1 ? i.u : i.u / p.n_hg, hg = i.u - kvh * p.n_hg;
     head0 = kvh * p.gq + hg * p.hpc, GH = min(p.hpc, p.gq - hg * p.hpc);
   };
   uint4 q_raw = make_uint4(0u, 0u, 0u, 0u);
@@ -389,6 +390,10 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     int head0, GH;
     heads_of(it, head0, GH);
 
+    if (warp == CW - 1) {  // (it prepares no q)
+      const int f = share_of(it.vstart, V, G), n = share_of(it.vstart + it.tiles - 1, V, G) - f + 1;
+      if (lane == 0) sm.first = f, sm.n_split = n;
+    }
     // ---- q of the item: position rotation, R q, scale, fp16 hi + lo.  The WHT runs in a warp per
     // head; a dense R takes its 64 KB from L2 and two barriers more (1.4 us).
     float x[4] = {0.f, 0.f, 0.f, 0.f};
@@ -420,12 +425,9 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     float qs;
     {
       const int slot = grp * 4 + hs, sw = 2 * g + (t >> 1);
-      const uint32_t *qw = tl.q[slot] + (g & 1) * 64 + 16 * t;
+      const uint32_t *qw = tl.q[slot] + (g & 1) * 64 + 16 * t, held = slot < GH ? ~0u : 0u;
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        qb[kk][0] = slot < GH ? qw[(2 * kk) ^ sw] : 0u;
-        qb[kk][1] = slot < GH ? qw[(2 * kk + 1) ^ sw] : 0u;
-      }
+      for (int kk = 0; kk < 8; ++kk) qb[kk][0] = qw[(2 * kk) ^ sw] & held, qb[kk][1] = qw[(2 * kk + 1) ^ sw] & held;
       const int my = grp * 4 + t;  // the head whose scores this lane holds
       qs = my < GH ? tl.qs[my] : 0.f;
     }
@@ -434,6 +436,7 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) O[mt][0] = O[mt][1] = O[mt][2] = O[mt][3] = 0.f;
 
+    const bool more = next_item<GROUPS>(p, w, nx);  // its lengths are loaded under the tiles
     for (int j = it.t0; j < it.t1; ++j) {
       const int s = ctr % NSTAGE;
       if (!mbar_wait_bounded(&sm.full[s], (ctr / NSTAGE) & 1, WAIT_LIMIT_NS)) {
@@ -533,7 +536,7 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     // same tile, so either every consumer warp enters the merge barriers or none.
     if (aborted || *reinterpret_cast<volatile int *>(&sm.abort_flag)) return;
 
-    have = next_item<GROUPS>(p, w, nx);
+    have = more;
     if (have) fetch_q(nx);  // under the merge
 
     // ---- merge the warps' states and write the item's partial
@@ -541,7 +544,7 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
     lsum += __shfl_xor_sync(FULL_MASK, lsum, 8);
     lsum += __shfl_xor_sync(FULL_MASK, lsum, 16);
     if (g == 0) sm.mw[warp][t] = M, sm.lw[warp][t] = lsum;
-    const int first = share_of(it.vstart, V, G), n_split = share_of(it.vstart + it.tiles - 1, V, G) - first + 1;
+    const int first = sm.first, n_split = sm.n_split;
     const int cta = blockIdx.x;
     float *dst0 = n_split == 1 ? p.whole + ((size_t)it.row * p.Hq + head0) * PROW
                                : p.split + (size_t)(cta * 2 + (cta == first ? 1 : 0)) * 8 * PROW;

@@ -35,9 +35,10 @@ namespace {
 template <int GROUPS>
 struct Shape {
   static constexpr int CW = GROUPS == 1 ? 15 : 14, TILE = 16 * CW, NT = (CW + 1) * 32;
-  // Cost of an item ahead of its tiles, in tiles, as measured: 4 of 1 us, 2 of 1.9 us (64 ragged sequences
-  // of 6 heads: 32.9 us with 4, 31.3 with 3, 29.7 with 2; differential decode of 16: 30.0 with 4, 31.1 with 3).
-  static constexpr int ITEM_TILES = GROUPS == 1 ? 4 : 2;
+  // Cost of an item ahead of its tiles, in tiles, as measured: 3 of 1 us (differential decode of 16: 29.5 us
+  // with 3, 29.9 with 4, 30.4 with 5), 1 of 1.9 us (64 ragged sequences of 6 heads: 28.6 us with 1, 29.2
+  // with 2, 30.8 with 3).
+  static constexpr int ITEM_TILES = GROUPS == 1 ? 3 : 1;
 };
 constexpr int MAX_CW = Shape<1>::CW, MAX_TILE = Shape<1>::TILE;
 constexpr int NSTAGE = 4;
@@ -240,7 +241,7 @@ __device__ __forceinline__ bool next_item(const DecodeParams &p, Walk &w, Item &
 // GROUPS = 1: at most four heads; warps 2i and 2i + 1 take 16 keys of the i-th 32 each.  GROUPS = 2: five to
 // eight heads in two halves; warp i of either half takes all of the i-th 32 keys.  Both halves decode
 // every key, but a warp holds the state of four heads only: one that held eight decoded once, spilled, and
-// took 2.2 us a tile against 1.9 (64 ragged sequences, 6 heads per KV head: 37 us).
+// took 2.2 us a tile against 1.9.
 template <int GROUPS, bool FIXED>
 __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
   constexpr int CW = Shape<GROUPS>::CW, TILE = Shape<GROUPS>::TILE, NT = Shape<GROUPS>::NT;

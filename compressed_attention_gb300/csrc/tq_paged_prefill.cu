@@ -90,7 +90,7 @@ struct Misc {
   // is done, while the softmax still needs the norms; the decoders reach tile j + 4 only after
   // every group has finished tile j.  2^7 value norms of the two V stages.
   alignas(16) float kn[4][KT];
-  alignas(16) float nv[2][KT];
+  alignas(16) float nv[2][KT], nu[2][KT];  // and log2 of the norms
   // One part: the norms are in the operands, and these hold for 32 rows of a K tile its power of two, and
   // for 32 of a V tile log2 of its power (+ P_SHIFT), 2^- of that (negative: some norms are not finite), and the rows of those.
   alignas(8) float ks[4][KT / 32];
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
             decode8<0x5140u, 0x7362u>(src[1 + ch], lo2, hi2, d);
             *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 8 * ch)) = make_uint4(d[0], d[1], d[2], d[3]);
           }
-          if (side) ms.nv[st][row] = norm * 128.0f;
+          if (side) ms.nv[st][row] = norm * 128.0f, ms.nu[st][row] = fmaxf(log2_approx(norm), -64.f);
           else ms.kn[c & 3][row] = norm;
         } else {
           // The norm goes into the operand: x (nh + nl), the norm as two fp16 parts after the power of
@@ -935,6 +935,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
         tc_fence_after();
         [[maybe_unused]] const float4 *kn4 = reinterpret_cast<const float4 *>(ms.kn[(kc + i) & 3]) + 16 * h;
         [[maybe_unused]] const float4 *nv4 = reinterpret_cast<const float4 *>(ms.nv[cv & 1]) + 16 * h;
+        [[maybe_unused]] const float4 *nu4 = reinterpret_cast<const float4 *>(ms.nu[cv & 1]) + 16 * h;
         const bool full = kf + 63 <= it.s.base + q0;  // every row sees every key of the half
         // the largest s + log2(value norm, or the power of two in its operand) of the row
         auto row_max = [&]() -> float {
@@ -959,11 +960,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
               tmem_ld32(tH + 32 * cc, sv);
 #pragma unroll
               for (int c4 = 0; c4 < 8; ++c4) {
-                const float4 kn = kn4[8 * cc + c4], nv = nv4[8 * cc + c4];
-                const float k_[4] = {kn.x, kn.y, kn.z, kn.w}, v_[4] = {nv.x, nv.y, nv.z, nv.w};
+                const float4 kn = kn4[8 * cc + c4], nu = nu4[8 * cc + c4];
+                const float k_[4] = {kn.x, kn.y, kn.z, kn.w}, u_[4] = {nu.x, nu.y, nu.z, nu.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const float u = fmaf(sv[4 * c4 + e] * k_[e], rsc, fmaxf(log2_approx(v_[e]) - P_SHIFT, -64.f));
+                  const float u = fmaf(sv[4 * c4 + e] * k_[e], rsc, u_[e]);
                   if (full || kf + 32 * cc + 4 * c4 + e <= pos) bm = fmaxf(bm, u);
                 }
               }

@@ -35,12 +35,22 @@ struct GatherParams {
   int only;  // 0 or 1: one side; 2: both, alternating CTAs
 };
 
+// The sequence of a thread's last row, [lo, hi) its rows: the next row is mostly of the same one, and
+// then costs one load (its page), not the search's chain of them.
+struct SeqOf {
+  int b = 0, lo = 0, hi = 0, n = 0;
+};
 // The packed row of output row `row` (token-major), -1 without one.
-__device__ __forceinline__ int64_t source_row(const PagedView &v, int64_t row, bool flag) {
-  const int tok = (int)(row / v.Hkv), h = (int)(row - (int64_t)tok * v.Hkv);
-  const int b = paged_seq(v, tok), n = paged_len(v, b, flag), pos = paged_pos(v, b, tok, n);
-  if (pos < 0) return -1;
-  return (int64_t)paged_row(v, max(paged_page(v, b, pos, flag), 0), h, pos & ((1 << v.page_shift) - 1));
+__device__ __forceinline__ int64_t source_row(const PagedView &v, SeqOf &s, int64_t row, bool flag) {
+  const int tok = (int)((uint32_t)row / (uint32_t)v.Hkv), h = (int)(row - (int64_t)tok * v.Hkv);
+  if (tok < s.lo || tok >= s.hi) {
+    s.b = paged_seq(v, tok);
+    s.lo = v.cu_q ? v.cu_q[s.b] : tok, s.hi = v.cu_q ? v.cu_q[s.b + 1] : tok + 1;
+    s.n = paged_len(v, s.b, flag);
+  }
+  const int pos = s.n - (s.hi - tok);
+  if (pos < 0 || pos >= s.n) return -1;
+  return (int64_t)paged_row(v, max(paged_page(v, s.b, pos, flag), 0), h, pos & ((1 << v.page_shift) - 1));
 }
 
 constexpr int RAW = 128 * PG_ROW;
@@ -95,9 +105,10 @@ __global__ void __launch_bounds__(GatherCfg<PARTS>::GROUPS * 128) k_paged_gather
   const int n_cta = gridDim.x / n_side;
   // this warp's 32 packed rows of tile t: lane l copies words l, l + 32, ... of the 32 x 17
   int64_t src = -1;
+  SeqOf seq;
   auto fetch = [&](int64_t t) {
     const int64_t row = t * 128 + r;
-    src = t < n_tiles && row < n_rows ? source_row(p.pv, row, true) : -1;
+    src = t < n_tiles && row < n_rows ? source_row(p.pv, seq, row, true) : -1;
     uint32_t *dst = raw + (warp & 3) * 32 * 17;
 #pragma unroll
     for (int k = 0; k < 17; ++k) {
@@ -235,8 +246,9 @@ __global__ void __launch_bounds__(GA_WARPS * 32) k_paged_gather(const GatherPara
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t n_rows = (int64_t)paged_rows(p.pv) * p.pv.Hkv;
   const int n_cta = gridDim.x / step;
+  SeqOf seq;
   for (int64_t row = (int64_t)(blockIdx.x / step) * GA_WARPS + warp; row < n_rows; row += (int64_t)n_cta * GA_WARPS) {
-    const int64_t at = source_row(p.pv, row, lane == 0);
+    const int64_t at = source_row(p.pv, seq, row, lane == 0);
     float x[4] = {0.f, 0.f, 0.f, 0.f};
     if (at >= 0) {
       const float norm = *reinterpret_cast<const float *>(sd.pages + at);

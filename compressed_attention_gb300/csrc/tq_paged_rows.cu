@@ -136,9 +136,10 @@ __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendPar
   int b = -1, b_end = 0, len = 0;  // the row's sequence, the row after its last, its length
   const bool turn = side == 0 && p.rope.rot_dim != 0;
   Quarter<SRC> raw;
-  Place pl{-1, 0};
+  // the next row: its page as in the table (loaded, and looked at when its turn comes), head and position
+  int nx_page = -1, nx_head = 0, nx_pos = -1;
   auto fetch = [&](int i) {
-    pl.at = -1;
+    nx_pos = -1;
     if (i < n_iter && i * 8 + sub < n_rows) {
       load_quarter<SRC>(sd.src.data + tok * sd.src.token_bytes + head * sd.src.head_bytes, q, true, raw);
       if (b < 0 || tok >= b_end) {
@@ -149,10 +150,10 @@ __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendPar
         b_end = p.pv.cu_q ? p.pv.cu_q[b + 1] : tok + 1;
         len = paged_len(p.pv, b, q == 0);
       }
-      pl.pos = len - (b_end - tok);
-      if (pl.pos >= 0 && pl.pos < len) {
-        const int pg = paged_page(p.pv, b, pl.pos, q == 0);
-        if (pg >= 0) pl.at = (int64_t)paged_row(p.pv, pg, head, pl.pos & ((1 << p.pv.page_shift) - 1));
+      const int pos = len - (b_end - tok);
+      if (pos >= 0 && pos < len) {
+        nx_page = p.pv.table[(int64_t)b * p.pv.table_stride + (pos >> p.pv.page_shift)];
+        nx_pos = pos, nx_head = head;
       }
       tok += d_tok, head += d_head;
       if (head >= Hkv) head -= Hkv, ++tok;
@@ -160,7 +161,12 @@ __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendPar
   };
   fetch(it);
   for (; it < n_iter; it += step) {
-    const Place at = pl;
+    Place at{-1, nx_pos};
+    if (nx_pos >= 0) {
+      if ((unsigned)nx_page < (unsigned)p.pv.n_pages)
+        at.at = (int64_t)paged_row(p.pv, nx_page, nx_head, nx_pos & ((1 << p.pv.page_shift) - 1));
+      else if (q == 0) atomicExch(p.pv.status, (int32_t)DEVERR_PAGE);
+    }
     float v[WT_E];
     if (at.at >= 0) {
       unpack_quarter(raw, v);

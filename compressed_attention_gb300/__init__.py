@@ -560,6 +560,8 @@ class PagedKV:
             raise ValueError("k_pages and v_pages must have one size")
         self.k_pages, self.v_pages, self.block_table = k_pages, v_pages, block_table
         self.page_size, self.Hkv, self.n_pages = page_size, Hkv, k_pages.numel() // per
+        self.n_seqs = block_table.shape[0]
+        self.on_gpu = k_pages.is_cuda and v_pages.is_cuda and block_table.is_cuda
         width = block_table.shape[1]
         stride = max(block_table.stride(0), width) if block_table.shape[0] <= 1 else block_table.stride(0)
         self.c = tq_paged_kv(_ptr(k_pages), _ptr(v_pages), _ptr(block_table), stride, width, page_size, self.n_pages, Hkv)
@@ -580,6 +582,7 @@ class PagedBatch:
             if cu_q.shape[0] != B + 1 or n_tokens is None:
                 raise ValueError("cu_q has B + 1 entries and comes with n_tokens")
         self.seq_lens, self.cu_q, self.B = seq_lens, cu_q, B
+        self.on_gpu = seq_lens.is_cuda and (cu_q is None or cu_q.is_cuda)
         self.n_tokens = B if n_tokens is None else n_tokens
         self.c = tq_paged_batch(_ptr(cu_q), _ptr(seq_lens), B, max_q, self.n_tokens, max_len)
         self.ref = ctypes.byref(self.c)
@@ -595,6 +598,7 @@ class Rope:
             if not t.is_contiguous() or t.shape != cos.shape:
                 raise ValueError("rotation tables must be contiguous and of one shape")
         self.cos, self.sin = cos, sin
+        self.on_gpu = cos.is_cuda and sin.is_cuda
         self.c = tq_rope(_ptr(cos), _ptr(sin), cos.shape[0], 2 * cos.shape[1], int(bool(interleaved)))
         self.ref = ctypes.byref(self.c)
 
@@ -609,6 +613,7 @@ class DiffMix:
         if norm_weight is not None and _tensor(norm_weight, torch.float32, 1, "norm_weight").shape[0] != D:
             raise ValueError(f"norm_weight must have {D} elements")
         self.lam, self.norm_weight = lam, norm_weight
+        self.on_gpu = lam.is_cuda and (norm_weight is None or norm_weight.is_cuda)
         stride = 0 if lam.dim() == 1 else (lam.stride(0) if lam.shape[0] > 1 else lam.shape[1])
         self.c = tq_diff(_ptr(lam), stride, _ptr(norm_weight), eps, out_scale)
         self.ref = ctypes.byref(self.c)
@@ -625,21 +630,30 @@ def tq_make_rope_table(rot_dim, n_pos, base=10000.0):
 def _rows(t, n_tokens, heads, what):
     """tq_rows of a [n_tokens, heads, 128] tensor (any strides, elements of a row packed)."""
     shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] < n_tokens or shape[1] != heads or shape[2] != D or stride[2] != 1:
-        raise ValueError(f"{what} must be [n_tokens, {heads}, {D}] with packed rows")
+    if len(shape) != 3 or shape[0] < n_tokens or shape[1] != heads or shape[2] != D or stride[2] != 1 or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor [n_tokens, {heads}, {D}] with packed rows")
     return tq_rows(t.data_ptr(), _dtype_code(t), stride[0], stride[1])
 
 
 def _dense_out(t, n_tokens, heads, what):
     shape = t.shape
-    if len(shape) != 3 or shape[0] < n_tokens or shape[1] != heads or shape[2] != D or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous [n_tokens, {heads}, {D}] tensor")
+    if len(shape) != 3 or shape[0] < n_tokens or shape[1] != heads or shape[2] != D or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what} must be a contiguous CUDA tensor [n_tokens, {heads}, {D}]")
     return t.data_ptr()
+
+
+def _check_call(kv, batch, rope=None, diff=None):
+    """What the library cannot see: where tensors live, the block table's rows."""
+    if not (kv.on_gpu and batch.on_gpu and (rope is None or rope.on_gpu) and (diff is None or diff.on_gpu)):
+        raise ValueError("the cache, the batch, the rotation's tables and the mix must be CUDA tensors")
+    if batch.B > kv.n_seqs:
+        raise ValueError(f"{batch.B} sequences, but the block table has {kv.n_seqs} rows")
 
 
 def tq_paged_append(k_ctx, v_ctx, kv, batch, k, v, rope=None, stream=None):
     """Quantize the batch's rows k, v ([n_tokens, Hkv, 128]) into their pages, the keys rotated
     by their positions first (``rope``)."""
+    _check_call(kv, batch, rope)
     kr, vr = _rows(k, batch.n_tokens, kv.Hkv, "k"), _rows(v, batch.n_tokens, kv.Hkv, "v")
     _check(lib.tq_paged_append(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref, ctypes.byref(kr), ctypes.byref(vr),
                                rope.ref if rope else None, _stream(stream)), "tq_paged_append")
@@ -647,6 +661,7 @@ def tq_paged_append(k_ctx, v_ctx, kv, batch, k, v, rope=None, stream=None):
 
 def tq_paged_gather(k_ctx, v_ctx, kv, batch, k_out, v_out, unrotate=True, stream=None):
     """Read the batch's rows back into k_out / v_out ([n_tokens, Hkv, 128], either None)."""
+    _check_call(kv, batch)
     outs = [t for t in (k_out, v_out) if t is not None]
     if not outs or outs[0].dtype != outs[-1].dtype:
         raise ValueError("one output at least, of one dtype")
@@ -664,6 +679,7 @@ def tq_paged_workspace_size(k_ctx, v_ctx, kv, batch, Hq):
 
 def tq_paged_attention(k_ctx, v_ctx, kv, batch, q, out, workspace, rope=None, scale=0.0, stream=None):
     """Causal attention of the batch's rows q ([n_tokens, Hq, 128]) over their sequences' pages."""
+    _check_call(kv, batch, rope)
     Hq = q.shape[1]
     qr = _rows(q, batch.n_tokens, Hq, "q")
     _check(lib.tq_paged_attention(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref, ctypes.byref(qr), Hq,
@@ -674,6 +690,7 @@ def tq_paged_attention(k_ctx, v_ctx, kv, batch, q, out, workspace, rope=None, sc
 
 def tq_paged_diff_attention(k_ctx, v_ctx, kv, batch, q, diff, out, workspace, rope=None, scale=0.0, stream=None):
     """Differential attention of the head pairs (2p, 2p + 1) of q; out [n_tokens, Hq / 2, 128]."""
+    _check_call(kv, batch, rope, diff)
     Hq = q.shape[1]
     lam = diff.lam
     if lam.shape[-1] * 2 != Hq or (lam.dim() == 2 and lam.shape[0] < batch.n_tokens):

@@ -814,3 +814,32 @@ def test_refusals():
     assert L.tq_paged_gather(*H, a, b, 1, out.data_ptr(), None, 9, None) == INV
     torch.cuda.synchronize()
     assert torch.all(out == 7.0) and s.status() == 0
+
+
+def test_python_refusals():
+    """What the binding can see and the library cannot: tensors off the GPU, a block table of fewer rows than
+    sequences, workspaces and outputs that are too small."""
+    import torch
+    tq = lib()
+    s = Setup(tq, [40, 30], [1, 1], 2, 16, 54, ragged=False)
+    q = torch.randn((2, 4, 128), device="cuda")
+    kv = torch.randn((2, 2, 128), device="cuda")
+    out, ws = torch.full_like(q, 7.0), s.workspace(4)
+    one = tq.PagedKV(s.pages[0], s.pages[1], s.kv.block_table[:1], 16, 2)
+    bad = [lambda: tq.tq_paged_attention(*s.ctx, one, s.batch, q, out, ws),
+           lambda: tq.tq_paged_append(*s.ctx, one, s.batch, kv, kv),
+           lambda: tq.tq_paged_gather(*s.ctx, one, s.batch, kv, None),
+           lambda: tq.tq_paged_attention(*s.ctx, s.kv, s.batch, q.cpu(), out, ws),
+           lambda: tq.tq_paged_attention(*s.ctx, s.kv, s.batch, q, out.cpu(), ws),
+           lambda: tq.tq_paged_attention(*s.ctx, s.kv, s.batch, q, out[:1], ws),
+           lambda: tq.tq_paged_append(*s.ctx, s.kv, s.batch, kv, kv.cpu()),
+           lambda: tq.tq_paged_attention(*s.ctx, tq.PagedKV(s.pages[0].cpu(), s.pages[1], s.kv.block_table, 16, 2), s.batch, q, out, ws),
+           lambda: tq.tq_paged_attention(*s.ctx, tq.PagedKV(s.pages[0], s.pages[1], s.kv.block_table.cpu(), 16, 2), s.batch, q, out, ws),
+           lambda: tq.tq_paged_attention(*s.ctx, s.kv, tq.PagedBatch(s.d_lens.cpu()), q, out, ws),
+           lambda: tq.tq_paged_attention(*s.ctx, s.kv, s.batch, q, out, ws, rope=tq.Rope(torch.ones(4, 64), torch.ones(4, 64))),
+           lambda: tq.tq_paged_diff_attention(*s.ctx, s.kv, s.batch, q, tq.DiffMix(torch.ones(2)), out[:, :2].contiguous(), ws)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    torch.cuda.synchronize()
+    assert s.status() == 0 and torch.all(out == 7.0)

@@ -41,10 +41,10 @@
 //
 // Measured (GB300): 4 chunks of 200 .. 512 tokens on 4K .. 16K keys, 32 q-heads on 8, bf16: 240 us
 // for 199 GFLOP (prep 20, join 13, the rest the attention), 43% of the cuBLAS bf16 rate; prompts of
-// 129 .. 2047 tokens, 8 heads on 8, fp16 in two parts: 75 us.  A step of 64 keys takes 1.2 us
+// 129 .. 2047 tokens, 8 heads on 8, fp16 in two parts: 73 us.  A step of 64 keys takes 1.2 us
 // for 2 x 128 rows: 0.9 us from S to P (64 exponentials a thread, beside the decoders' issue slots) and
-// 0.3 us of barriers between the roles.  Shared memory carries 37% operands and 39% loads and
-// stores of its bandwidth, the issue slots are half used, the tensor pipe 39%: no one unit is
+// 0.3 us of barriers between the roles.  Shared memory carries 41% operands and 23% loads and
+// stores of its bandwidth, the issue slots are 60% used, the tensor pipe 44%: no one unit is
 // full, the chain S -> P -> PV -> S of a group is.  Tried and slower: two threads a row
 // (28 warps, 375 us when this form took 312), scores in registers ahead of the next product
 // (spills at the registers 640 threads leave: 298 us to 240), 152 and 56 registers.
@@ -63,7 +63,9 @@ namespace tq {
 namespace {
 
 constexpr int KT = 128;                // keys per tile
-constexpr int UNIT_TILES = 3;          // cost of an item ahead of its tiles, in tiles
+// Cost of an item ahead of its tiles, in tiles, as measured (differential chunks, prompts: 45.5 and 81 us
+// with 1, 43.1 and 72.9 with 2, 41.2 and 72.6 with 3, 42.5 and 75.5 with 5).
+constexpr int UNIT_TILES = 3;
 constexpr int RAW = KT * PG_ROW;       // a packed tile
 constexpr int NRAW = 3;
 constexpr int W_DEC = 8, W_MMA = 16, W_LOAD = 18, W_Q = 19, N_WARPS = 20;

@@ -6,7 +6,9 @@
 // butterfly, so the stored bytes equal those of a plain fp32 sequence.  The rotation's
 // pairs (j, j + 64) and (j, j + 32) and adjacent pairs lie inside one thread's chunks;
 // pairs (j, j + 16) cross to the thread two over.  A CTA takes keys or values, so it keeps one
-// codebook grid.
+// codebook grid.  The next row's elements and page id are in flight under a row's encode.  13.8K
+// tokens of 8 KV heads (bf16, keys turned): 43 us for 76 MB, 129 warp instructions a row; issue and
+// latency at 16 warps an SM bind it (128 registers; 24 warps at 80 spilled and were slower).
 #include "tq_decode_common.cuh"
 #include "tq_paged.cuh"
 #include "tq_qprep.cuh"

@@ -474,6 +474,8 @@ tq_status tq_paged_gather(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_pag
  *   out        device [n_tokens][Hq][128] of out_dtype (F32, BF16 or F16), 16-byte aligned.
  *   workspace  device scratch of tq_paged_workspace_size() bytes for the same batch sizes,
  *              256-byte aligned; its contents need no initialisation.
+ * TQ_ERR_UNSUPPORTED where n_tokens * Hq, or the tiles of keys that the sizes and max_len allow
+ * for (give a tight max_len), pass 2^31.
  * Sums, maxima and outputs are held in fp32; the tensor-core operands are fp16 parts (the
  * kernels' header comments state which products carry one part and which two).  With scores
  * of ordinary size the rows are within 2e-3 absolute and 1e-3 relative of the formula, as

@@ -652,6 +652,57 @@ def test_two_streams_and_repeated_calls_agree():
             assert torch.equal(o, first)
 
 
+@pytest.mark.parametrize("rot", [("wht", "wht"), ("dense", "dense")], ids="/".join)
+def test_captured_chunks_follow_the_batch(rot):
+    """Append, read back, chunk attention and the differential one captured together; replayed after the
+    rows, the offsets and the lengths changed in place they give an eager run's bits."""
+    import torch
+    tq = lib()
+    s = Setup(tq, [700, 520, 90], [400, 300, 60], 4, 32, 71, rot, pad=40)
+    cu = torch.from_numpy(s.cu).cuda()
+    batch = tq.PagedBatch(s.d_lens, cu, 420, s.n_rows)
+    rope, _ = s.rope(128, False)
+    k, v = (torch.randn((s.n_rows, 4, 128), device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn((s.n_rows, 16, 128), device="cuda").bfloat16()
+    mix = tq.DiffMix(torch.rand(8, device="cuda"), torch.ones(128, device="cuda"))
+    ws = torch.empty(max(tq.tq_paged_workspace_size(*s.ctx, s.kv, batch, 16), 256), dtype=torch.uint8, device="cuda")
+
+    def outputs():
+        return [torch.full((s.n_rows, h, 128), 7.0, dtype=d, device="cuda")
+                for h, d in ((16, torch.bfloat16), (16, torch.float16), (8, torch.bfloat16), (4, torch.float16))]
+
+    def run(o):
+        tq.tq_paged_append(*s.ctx, s.kv, batch, k, v, rope=rope)
+        tq.tq_paged_attention(*s.ctx, s.kv, batch, q, o[0], ws, rope=rope)
+        tq.tq_paged_attention(*s.ctx, s.kv, batch, q, o[1], ws, rope=rope)
+        tq.tq_paged_diff_attention(*s.ctx, s.kv, batch, q, mix, o[2], ws, rope=rope)
+        tq.tq_paged_gather(*s.ctx, s.kv, batch, o[3], None)
+
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    held = outputs()
+    with torch.cuda.stream(stream):
+        run(held)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        run(held)
+    for lens, new in (([700, 520, 90], [400, 300, 60]), ([610, 333, 70], [20, 333, 1]), ([5, 0, 96], [0, 0, 96])):
+        s.d_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        cu.copy_(torch.from_numpy(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)))
+        for t in (k, v, q):
+            t.normal_()
+        for o in held:
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        pages = [p.clone() for p in s.pages]
+        eager = outputs()
+        run(eager)
+        assert s.status() == 0
+        for a, b in zip(held + pages, eager + list(s.pages)):
+            assert torch.equal(a, b)
+
+
 def test_offsets_past_32_bits():
     """Pages of more than 2^32 bytes; the sequence's pages lie at the end."""
     import torch

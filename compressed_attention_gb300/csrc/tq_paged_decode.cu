@@ -221,15 +221,32 @@ __device__ __forceinline__ void walk_load(const DecodeParams &p, Walk &w) {
   w.keys = w.b < p.pv.B ? seq_keys(p.pv, w.b, &w.row, false) : 0;
   w.tiles = key_tiles<GROUPS>(w.keys);
 }
-// The next item of the share (false: done).
+// The next sequence with keys, looked for 32 at a time by the whole warp (idle slots may be many).
+template <int GROUPS>
+__device__ __forceinline__ bool walk_next(const DecodeParams &p, Walk &w) {
+  for (int b0 = w.b + 1; b0 < p.pv.B; b0 += 32) {
+    const int b = b0 + (int)(threadIdx.x & 31);
+    int row = -1;
+    const int keys = b < p.pv.B ? seq_keys(p.pv, b, &row, false) : 0;
+    const uint32_t m = __ballot_sync(FULL_MASK, keys > 0);
+    if (m) {
+      const int src = __ffs(m) - 1;
+      w.b = b0 + src, w.keys = __shfl_sync(FULL_MASK, keys, src), w.row = __shfl_sync(FULL_MASK, row, src);
+      w.tiles = key_tiles<GROUPS>(w.keys);
+      return true;
+    }
+  }
+  return false;
+}
+// The next item of the share (false: done).  The whole warp calls.
 template <int GROUPS>
 __device__ __forceinline__ bool next_item(const DecodeParams &p, Walk &w, Item &it) {
   const int upb = p.pv.Hkv * p.n_hg;
   while (w.left > 0) {
     if (w.b >= p.pv.B) return false;
     if (w.tiles == 0 || w.u >= upb) {
-      ++w.b, w.u = 0, w.off = 0;
-      walk_load<GROUPS>(p, w);
+      w.u = 0, w.off = 0;
+      if (!walk_next<GROUPS>(p, w)) return false;
       continue;
     }
     const int vt = w.tiles + Shape<GROUPS>::ITEM_TILES, n = min(vt - w.off, w.left);
@@ -310,7 +327,8 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
       for (int j = it.t0; j < it.t1; ++j) {
         const int kf = j * TILE, nk = min(TILE, it.keys - kf), s = ctr % NSTAGE;
         const int pg_next = page_of(j + 1);
-        if (ctr >= NSTAGE && !mbar_wait_bounded(&sm.empty[s], ((ctr / NSTAGE) - 1) & 1, WAIT_LIMIT_NS)) {
+        const bool up = ctr < NSTAGE || mbar_wait_bounded(&sm.empty[s], ((ctr / NSTAGE) - 1) & 1, WAIT_LIMIT_NS);
+        if (!__all_sync(FULL_MASK, up)) {  // (the warp together: the walk takes all its lanes)
           if (lane == 0) {
             atomicExch(&sm.abort_flag, 1);
             atomicExch(p.pv.status, (int32_t)DEVERR_TIMEOUT);

@@ -192,16 +192,33 @@ __device__ __forceinline__ void walk_begin(const PrefillParams &p, Walk &w) {
     w.tiles = unit_tiles(w.s, w.qt, p.qpu);
   }
 }
+__device__ __forceinline__ Seq seq_from_lane(const Seq &s, int src) {
+  return Seq{__shfl_sync(FULL_MASK, s.row, src), __shfl_sync(FULL_MASK, s.T, src), __shfl_sync(FULL_MASK, s.base, src),
+             __shfl_sync(FULL_MASK, s.n_qt, src)};
+}
+// The next sequence with rows, looked for 32 at a time by the whole warp (idle slots may be many).
+__device__ __forceinline__ bool next_seq(const PrefillParams &p, Walk &w) {
+  for (int b0 = w.b + 1; b0 < p.pv.B; b0 += 32) {
+    const Seq s = seq_of(p.pv, b0 + (int)(threadIdx.x & 31), p.qpu, false);
+    const uint32_t m = __ballot_sync(FULL_MASK, s.n_qt > 0);
+    if (m) {
+      w.b = b0 + __ffs(m) - 1;
+      w.s = seq_from_lane(s, __ffs(m) - 1);
+      return true;
+    }
+  }
+  return false;
+}
+// (the whole warp calls)
 __device__ __forceinline__ bool next_item(const PrefillParams &p, Walk &w, Item &it) {
   while (w.left > 0) {
     if (w.h >= p.pv.Hkv || w.tiles == 0) {  // next query tile, or sequence
       w.h = 0, w.off = 0;
       if (++w.qt >= w.s.n_qt) {
-        if (++w.b >= p.pv.B) return false;
         w.qt = 0;
-        w.s = seq_of(p.pv, w.b, p.qpu, false);
+        if (!next_seq(p, w)) return false;
       }
-      w.tiles = w.s.n_qt ? unit_tiles(w.s, w.qt, p.qpu) : 0;
+      w.tiles = unit_tiles(w.s, w.qt, p.qpu);
       continue;
     }
     const int vt = w.tiles + UNIT_TILES, n = min(vt - w.off, w.left);
@@ -240,10 +257,6 @@ struct PrepParams {
 __device__ __forceinline__ int unit_vtiles(const Seq &s, int qt, int qpu) {
   const int t = qt < s.n_qt ? unit_tiles(s, qt, qpu) : 0;
   return t ? t + UNIT_TILES : 0;
-}
-__device__ __forceinline__ Seq seq_from_lane(const Seq &s, int src) {
-  return Seq{__shfl_sync(FULL_MASK, s.row, src), __shfl_sync(FULL_MASK, s.T, src), __shfl_sync(FULL_MASK, s.base, src),
-             __shfl_sync(FULL_MASK, s.n_qt, src)};
 }
 __device__ __forceinline__ int warp_scan(int x, int lane) {
 #pragma unroll

@@ -395,6 +395,20 @@ def test_chunks_of_many_short_sequences(out_dtype):
     check_attention(got, ref, out_dtype)
 
 
+@pytest.mark.parametrize("most", [5, 1])
+def test_a_batch_of_mostly_idle_slots(most):
+    """45,000 slots, 60 of them in use (the plan's prefix sums then lie in the workspace)."""
+    tq = lib()
+    rng = np.random.default_rng(67)
+    new, lens = np.zeros(45000, int), np.zeros(45000, int)
+    used = np.concatenate([rng.choice(44999, 59, replace=False), [44999]])
+    new[used] = rng.integers(1, most + 1, 60)
+    lens[used] = new[used] + rng.integers(0, 40, 60)
+    s = Setup(tq, lens.tolist(), new.tolist(), 1, 16, 67, ("dense", "wht"), pad=2)
+    got, ref = run_attention(s, 2, "bf16", "bf16", 32)
+    check_attention(got, ref, "bf16")
+
+
 @pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
 def test_chunks_of_many_query_tiles(out_dtype):
     """A sequence of more query tiles than a warp has lanes, between short ones."""

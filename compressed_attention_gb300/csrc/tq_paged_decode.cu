@@ -644,79 +644,84 @@ __global__ void __launch_bounds__(CB_WARPS * 32) k_paged_combine(const CombinePa
   rot_load(alo, p.vfrag, 1, 1, warp, lane);
   pdl_wait();
   const int upb = p.pv.Hkv * p.n_hg;
-  for (int unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
-    const int b = unit / upb, u = unit - b * upb, kvh = u / p.n_hg, hg = u - kvh * p.n_hg;
-    const int head0 = kvh * p.gq + hg * p.hpc, GH = min(p.hpc, p.gq - hg * p.hpc);
-    int row;
-    const int keys = seq_keys(p.pv, b, &row, false);
-    if (row < 0) continue;  // the same for the whole CTA
-    float a[4] = {0.f, 0.f, 0.f, 0.f};
-    if (warp < GH && keys > 0) {
-      const uint32_t info = (uint32_t)p.unit[unit];
-      const int first = min((int)(info & 0xFFFFu), p.grid - 1), n = min((int)(info >> 16), p.grid - first);
-      float ms = -INFINITY, ls = 0.f;
-      for (int s0 = 0; s0 < n; s0 += 8) {
-        float m8[8], l8[8];
-        float4 v[8];
+  // The CTA's units 32 at a time: a lane finds one's row (idle slots have none, and cost nothing more).
+  for (int u0 = blockIdx.x; u0 < p.units; u0 += 32 * gridDim.x) {
+    const int of_lane = u0 + lane * gridDim.x;
+    int lane_row = -1;
+    const int lane_keys = of_lane < p.units ? seq_keys(p.pv, of_lane / upb, &lane_row, false) : 0;
+    for (uint32_t todo = __ballot_sync(FULL_MASK, lane_row >= 0); todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1, unit = u0 + src * gridDim.x;
+      const int row = __shfl_sync(FULL_MASK, lane_row, src), keys = __shfl_sync(FULL_MASK, lane_keys, src);
+      const int b = unit / upb, u = unit - b * upb, kvh = u / p.n_hg, hg = u - kvh * p.n_hg;
+      const int head0 = kvh * p.gq + hg * p.hpc, GH = min(p.hpc, p.gq - hg * p.hpc);
+      float a[4] = {0.f, 0.f, 0.f, 0.f};
+      if (warp < GH && keys > 0) {
+        const uint32_t info = (uint32_t)p.unit[unit];
+        const int first = min((int)(info & 0xFFFFu), p.grid - 1), n = min((int)(info >> 16), p.grid - first);
+        float ms = -INFINITY, ls = 0.f;
+        for (int s0 = 0; s0 < n; s0 += 8) {
+          float m8[8], l8[8];
+          float4 v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int s = min(s0 + i, n - 1);
-          const float *src = n == 1 ? p.whole + ((size_t)row * p.Hq + head0 + warp) * PROW
-                                    : p.split + (size_t)(((first + s) * 2 + (s == 0 ? 1 : 0)) * 8 + warp) * PROW;
-          m8[i] = __ldcg(src + D), l8[i] = __ldcg(src + D + 1);
-          v[i] = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
-        }
-        float mc = -INFINITY;
+          for (int i = 0; i < 8; ++i) {
+            const int s = min(s0 + i, n - 1);
+            const float *src = n == 1 ? p.whole + ((size_t)row * p.Hq + head0 + warp) * PROW
+                                      : p.split + (size_t)(((first + s) * 2 + (s == 0 ? 1 : 0)) * 8 + warp) * PROW;
+            m8[i] = __ldcg(src + D), l8[i] = __ldcg(src + D + 1);
+            v[i] = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
+          }
+          float mc = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (s0 + i < n && l8[i] != 0.f) mc = fmaxf(mc, m8[i]);
-        if (mc > ms) {
-          const float f = (ms == -INFINITY) ? 0.f : exp2f(ms - mc);
-          ls *= f;
+          for (int i = 0; i < 8; ++i)
+            if (s0 + i < n && l8[i] != 0.f) mc = fmaxf(mc, m8[i]);
+          if (mc > ms) {
+            const float f = (ms == -INFINITY) ? 0.f : exp2f(ms - mc);
+            ls *= f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) a[e] *= f;
-          ms = mc;
-        }
+            for (int e = 0; e < 4; ++e) a[e] *= f;
+            ms = mc;
+          }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (s0 + i < n && l8[i] != 0.f) {
-            const float f = exp2f(m8[i] - ms);
-            ls = fmaf(f, l8[i], ls);
-            a[0] = fmaf(f, v[i].x, a[0]), a[1] = fmaf(f, v[i].y, a[1]);
-            a[2] = fmaf(f, v[i].z, a[2]), a[3] = fmaf(f, v[i].w, a[3]);
+          for (int i = 0; i < 8; ++i) {
+            if (s0 + i < n && l8[i] != 0.f) {
+              const float f = exp2f(m8[i] - ms);
+              ls = fmaf(f, l8[i], ls);
+              a[0] = fmaf(f, v[i].x, a[0]), a[1] = fmaf(f, v[i].y, a[1]);
+              a[2] = fmaf(f, v[i].z, a[2]), a[3] = fmaf(f, v[i].w, a[3]);
+            }
           }
         }
-      }
-      const float f = ls == 0.f ? 0.f : p.inv_vscale / ls;  // (NaN stays)
+        const float f = ls == 0.f ? 0.f : p.inv_vscale / ls;  // (NaN stays)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) a[e] *= f;
-    }
-    rot_put(x, warp, lane, a);
-    __syncthreads();
-    {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
-      rot_mul<true>(acc, ahi, x, lane);
-      rot_mul<false>(acc2, alo, x, lane);
-      float *d = &y[2 * (lane & 3)][16 * warp + (lane >> 2)];
-      d[0] = acc[0] + acc2[0], d[D + 4] = acc[1] + acc2[1];
-      d[8] = acc[2] + acc2[2], d[D + 12] = acc[3] + acc2[3];
-    }
-    __syncthreads();
-    if (!p.o.diff.lambda) {
-      if (warp < GH) {
-        const float4 r = *reinterpret_cast<const float4 *>(&y[warp][4 * lane]);
-        const float v4[4] = {r.x, r.y, r.z, r.w};
-        store_lane4(p.o.out, p.o.dtype, ((size_t)row * p.Hq + head0 + warp) * D, lane, v4);
+        for (int e = 0; e < 4; ++e) a[e] *= f;
       }
-    } else if (2 * warp < GH) {
-      const float4 r = *reinterpret_cast<const float4 *>(&y[2 * warp][4 * lane]);
-      const float4 r2 = *reinterpret_cast<const float4 *>(&y[2 * warp + 1][4 * lane]);
-      float v4[4] = {r.x, r.y, r.z, r.w};
-      const float w4[4] = {r2.x, r2.y, r2.z, r2.w};
-      diff_finish(v4, w4, p.o.diff, row, (head0 >> 1) + warp, lane);
-      store_lane4(p.o.out, p.o.dtype, ((size_t)row * (p.Hq / 2) + (head0 >> 1) + warp) * D, lane, v4);
+      rot_put(x, warp, lane, a);
+      __syncthreads();
+      {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
+        rot_mul<true>(acc, ahi, x, lane);
+        rot_mul<false>(acc2, alo, x, lane);
+        float *d = &y[2 * (lane & 3)][16 * warp + (lane >> 2)];
+        d[0] = acc[0] + acc2[0], d[D + 4] = acc[1] + acc2[1];
+        d[8] = acc[2] + acc2[2], d[D + 12] = acc[3] + acc2[3];
+      }
+      __syncthreads();
+      if (!p.o.diff.lambda) {
+        if (warp < GH) {
+          const float4 r = *reinterpret_cast<const float4 *>(&y[warp][4 * lane]);
+          const float v4[4] = {r.x, r.y, r.z, r.w};
+          store_lane4(p.o.out, p.o.dtype, ((size_t)row * p.Hq + head0 + warp) * D, lane, v4);
+        }
+      } else if (2 * warp < GH) {
+        const float4 r = *reinterpret_cast<const float4 *>(&y[2 * warp][4 * lane]);
+        const float4 r2 = *reinterpret_cast<const float4 *>(&y[2 * warp + 1][4 * lane]);
+        float v4[4] = {r.x, r.y, r.z, r.w};
+        const float w4[4] = {r2.x, r2.y, r2.z, r2.w};
+        diff_finish(v4, w4, p.o.diff, row, (head0 >> 1) + warp, lane);
+        store_lane4(p.o.out, p.o.dtype, ((size_t)row * (p.Hq / 2) + (head0 >> 1) + warp) * D, lane, v4);
+      }
+      __syncthreads();  // x and y are free again
     }
-    __syncthreads();  // x and y are free again
   }
 }
 

@@ -20,8 +20,8 @@
 //   k_paged_combine  merges the shares of each unit, R^T o on the tensor cores, the
 //                    differential pair and its norm, rounding to the output type.
 //
-// Measured (GB300): 8 sequences of 24K .. 32K tokens, 32 q-heads on 8: 57 us for 238 MB; 64 ragged
-// sequences up to 16K, 12 on 2: 28.8 us; one of 733 tokens: 9.4 us.  A tile takes 1 us (1.9 us of five
+// Measured (GB300): 8 sequences of 24K .. 32K tokens, 32 q-heads on 8: 58 us for 238 MB; 64 ragged
+// sequences up to 16K, 12 on 2: 28.9 us; one of 733 tokens: 9.6 us.  A tile takes 1 us (1.9 us of five
 // to eight heads), bound by 64 table lookups a warp and 16 keys on the shared-memory path (63%) and by issue
 // (61%); an item's start and merge take 2.5 us, the launch's start 3.5 us.
 #include <math.h>

@@ -507,9 +507,12 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
         const float s0 = ok0 ? d0 * (nk0 * qs) : -INFINITY;
         const float s1 = ok1 ? d1 * (nk1 * qs) : -INFINITY;
         float e0 = exp2_approx(s0 - M), e1 = exp2_approx(s1 - M);
-        // An operand past 2^15, or no maximum yet (e then infinite or NaN): the maximum is raised.  One
-        // vote a tile, where the maximum itself takes three exchanges.
-        if (__any_sync(FULL_MASK, !(fmaxf(e0 * pv0, e1 * pv1) <= 32768.f) || M == -INFINITY)) {
+        // An operand past 2^15, a weight past 2^72 (what a norm of 2^-64 then has, the least that counts
+        // below: a value of no norm has operand 0, or NaN of an infinite weight, which fmaxf drops), or
+        // no maximum yet (e then infinite or NaN): the maximum is raised.  One vote a tile, where the
+        // maximum itself takes three exchanges.
+        if (__any_sync(FULL_MASK, !(fmaxf(e0 * pv0, e1 * pv1) <= 32768.f) || !(fmaxf(e0, e1) <= 0x1p72f) ||
+                                      M == -INFINITY)) {
           const float u0 = s0 + (ok0 ? fmaxf(log2_approx(nv0), -64.f) : 0.f);
           const float u1 = s1 + (ok1 ? fmaxf(log2_approx(nv1), -64.f) : 0.f);
           float bm = fmaxf(u0, u1);

@@ -1,0 +1,63 @@
+"""Paged calls at the ends of their contract: keys and values of extreme norms."""
+
+import numpy as np
+import pytest
+
+from gpu_util import lib
+from oracle import paged
+from test_gpu_paged import Setup, check_attention, run_attention, set_norms
+
+pytestmark = pytest.mark.gpu
+
+# lens, new, Hq, Hkv, P, output type; the position whose value has (almost) no norm: behind the first key
+# block of its warp, and behind its CTA's first tile of keys
+DOMINANT = [
+    ([32] * 6, [1] * 6, 6, 1, 16, "f32", 8),
+    ([500] * 170, [1] * 170, 4, 1, 32, "bf16", 300),
+    ([500] * 170, [1] * 170, 3, 1, 64, "f16", 247),
+    ([32] * 6, [2] * 6, 6, 1, 16, "bf16", 8),
+    ([500] * 40, [2] * 40, 16, 1, 32, "bf16", 300),
+    ([500] * 40, [20] * 40, 8, 1, 32, "bf16", 300),
+    ([500] * 40, [2] * 40, 4, 1, 32, "f16", 300),
+]
+
+
+@pytest.mark.parametrize("norm", [0.0, 2.0 ** -80])
+@pytest.mark.parametrize("case", DOMINANT, ids=lambda c: f"{c[5]}-t{max(c[1])}-g{c[2] // c[3]}-n{max(c[0])}")
+def test_a_value_of_no_norm_that_takes_all_the_weight(case, norm):
+    """One key of norm 4000 moves its score by some 350 z nats (z normal); its value is (almost) zero.  A row
+    where it leads by 60 nats is at most n exp(-60) of the largest value, one where it trails by 60 does
+    not feel it, and a score's own error is 7e-5 (one part: 1e-3) of |q| |k| / sqrt(128) ~ 4000, below 8 nats."""
+    lens, new, Hq, Hkv, P, out_dtype, at = case
+    tq = lib()
+    s = Setup(tq, lens, new, Hkv, P, 83, ("dense", "wht"), ragged=max(new) > 1)
+    some = range(0, len(lens), max(1, len(lens) // 12))
+    for b in some:
+        set_norms(s, 0, {(b, 0, at): 4000.0})
+        set_norms(s, 1, {(b, 0, at): norm})
+    got, ref = run_attention(s, Hq, "f32", out_dtype)
+    got32 = got.float().cpu().numpy().astype(np.float64)
+    assert np.all(np.isfinite(got32[:s.n]))
+    led, trailed = [], []
+    for b in some:
+        K = paged.dequantize(s.codec[0], paged.sequence_rows(s.host[0], s.table, b, lens[b]))[:, 0]
+        for i in range(s.cu[b], s.cu[b + 1]):
+            n = lens[b] - (s.cu[b + 1] - i) + 1
+            x = s.q32[i].astype(np.float64) @ K[:n].T / np.sqrt(128)
+            lead = x[:, at] - np.delete(x, at, axis=1).max(axis=1)
+            led += [(i, h) for h in np.nonzero(lead >= 60)[0]]
+            trailed += [(i, h) for h in np.nonzero(lead <= -60)[0]]
+    assert len(led) >= 10 and len(trailed) >= 10
+    V = [paged.dequantize(s.codec[1], paged.sequence_rows(s.host[1], s.table, b, lens[b])) for b in some]
+    big = max(np.abs(v).max() for v in V)
+    for i, h in led:
+        assert np.abs(got32[i, h]).max() <= max(lens) * np.exp(-52) * big
+    keep = np.zeros(got32.shape[:2], bool)
+    for i, h in trailed:
+        keep[i, h] = True
+    for b in range(len(lens)):
+        if b not in some:
+            keep[s.cu[b]:s.cu[b + 1]] = True
+    import torch
+    ref[~keep] = 0
+    check_attention(torch.from_numpy(np.where(keep[..., None], got32, 0)), ref, out_dtype)

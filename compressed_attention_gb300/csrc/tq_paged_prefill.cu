@@ -1152,7 +1152,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
         const float Mx = fmaxf(M0, M1);
         const float f0 = M0 == -INFINITY ? 0.f : exp2f(M0 - Mx), f1 = M1 == -INFINITY ? 0.f : exp2f(M1 - Mx);
         fw = gr ? f1 : f0;
-        l = (f0 ? f0 * l0 : 0.f) + (f1 ? f1 * l1 : 0.f);
+        // (without a maximum a group's sum is 0, or NaN where its scores are)
+        l = (M0 == -INFINITY ? l0 : f0 * l0) + (M1 == -INFINITY ? l1 : f1 * l1);
         amax = fmaxf(f0 ? f0 * a0 : 0.f, f1 ? f1 * a1 : 0.f);
         M = Mx;
       } else if (!ok) {
@@ -1161,7 +1162,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
       const float fo = l == 0.f ? 0.f : p.inv_vscale / l;
       const float am = amax * fo;
       const int ex = scale_exp(am);
-      const float mul = fo * fw * pow2i(-ex), back = pow2i(ex);
+      // (a row without a maximum holds zeros here: a NaN sum reaches it through the scale)
+      const float mul = fo * fw * pow2i(-ex), back = isnan(l) ? l : pow2i(ex);
       const bool zero = done == 0 || fw == 0.f || fo == 0.f;  // O holds nothing (of the row)
 #pragma unroll 1
       for (int c2 = 0; c2 < (LO ? 4 : 2); ++c2) {

@@ -1,11 +1,12 @@
-"""Paged calls at the ends of their contract: keys and values of extreme norms."""
+"""Paged calls at the ends of their contract: keys and values of extreme norms, scores without a
+maximum."""
 
 import numpy as np
 import pytest
 
 from gpu_util import lib
 from oracle import paged
-from test_gpu_paged import Setup, check_attention, run_attention, set_norms
+from test_gpu_paged import Setup, check_attention, device_rows, dt, run_attention, set_norms
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,40 @@ def test_a_value_of_no_norm_that_takes_all_the_weight(case, norm):
     import torch
     ref[~keep] = 0
     check_attention(torch.from_numpy(np.where(keep[..., None], got32, 0)), ref, out_dtype)
+
+
+NO_MAXIMUM = [  # lens, new, Hq, Hkv, P, output type
+    ([130, 40], [2, 2], 8, 2, 16, "bf16"),
+    ([130, 40], [2, 2], 8, 2, 16, "f16"),
+    ([130, 70], [2, 70], 8, 1, 16, "bf16"),
+    ([130, 40], [1, 1], 8, 2, 16, "bf16"),
+    ([260, 40], [1, 1], 12, 2, 64, "f32"),
+]
+
+
+@pytest.mark.parametrize("case", NO_MAXIMUM, ids=lambda c: f"{c[5]}-t{max(c[1])}-g{c[2] // c[3]}")
+def test_scores_that_are_all_nan_reach_the_row(case):
+    """A last tile of keys whose norms are all NaN, and a row of q that is NaN: the rows that see them are not
+    finite, the others are as if they were not there."""
+    import torch
+    lens, new, Hq, Hkv, P, out_dtype = case
+    tq = lib()
+    s = Setup(tq, lens, new, Hkv, P, 89, ("wht", "dense"), ragged=max(new) > 1)
+    first = lens[0] - 2 if max(new) > 1 else lens[0] - 1  # NaN from here on, for the last KV head
+    set_norms(s, 0, {(0, Hkv - 1, t): np.nan for t in range(first, lens[0])})
+    q, q32 = device_rows(s.rng.standard_normal((s.n_rows, Hq, 128)), "f32")
+    last = s.n - 1
+    q[last, 1, 5] = float("nan")
+    out = torch.full((s.n_rows, Hq, 128), 7.0, dtype=dt(out_dtype), device="cuda")
+    tq.tq_paged_attention(*s.ctx, s.kv, s.batch, q, out, s.workspace(Hq))
+    assert s.status() == 0
+    ref = s.oracle(q32)
+    bad = np.zeros((s.n_rows, Hq), bool)
+    for i in range(s.cu[0], s.cu[1]):
+        if lens[0] - (s.cu[1] - i) >= first:
+            bad[i, Hq - Hq // Hkv:] = True
+    bad[last, 1] = True
+    got = out.float().cpu().numpy()
+    assert bad.sum() > 1 and not np.isfinite(got[bad]).any()
+    ref[bad] = 0
+    check_attention(torch.from_numpy(np.where(bad[..., None], 0, got)), ref, out_dtype)

@@ -13,6 +13,14 @@ namespace tq {
 
 constexpr int PG_ROW = 68;  // bytes of a packed row
 
+// The attention's weights are 2^W_SHIFT exp2(score - m), m the running maximum of score + log2(value
+// norm) (norms below 2^-64 count as 2^-64), up to RESCALE_SLACK past it: from 2^-127 at the largest finite norm
+// to 2^72 at none ahead of the shift, which leaves 23 octaves of smaller weights above exp2's flush
+// at 2^-126, and 2^31 keys below 2^127.
+constexpr int W_SHIFT = 24;
+constexpr float W_MOST = 0x1p96f;         // 2^(64 + RESCALE_SLACK + W_SHIFT)
+constexpr float NORM_FACTOR = 0x1p-17f;   // of a value norm, for a probability operand at 2^P_SHIFT: 2^(P_SHIFT - W_SHIFT)
+
 // Rows that belong to a sequence.
 static __device__ __forceinline__ int paged_rows(const PagedView &v) {
   if (!v.cu_q) return v.B;

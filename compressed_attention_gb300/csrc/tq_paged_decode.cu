@@ -48,7 +48,7 @@ struct Shape {
 constexpr int MAX_CW = Shape<1>::CW, MAX_TILE = Shape<1>::TILE;
 constexpr int NSTAGE = 4;
 constexpr int STAGE = MAX_TILE * PG_ROW + 32;  // 16,352 bytes, a multiple of 32
-constexpr int PROW = D + 4;          // floats of a partial: acc[128], max, sum, 2 spare
+constexpr int PROW = D + 4;          // floats of a partial: acc[128], max (less W_SHIFT), sum, 2 spare
 
 struct DecodeParams {
   PagedView pv;
@@ -500,25 +500,24 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
         const float nv0 = *reinterpret_cast<const float *>(Vs + k0 * PG_ROW);
         const float nv1 = *reinterpret_cast<const float *>(Vs + k1 * PG_ROW);
         const bool ok0 = k0 < nk, ok1 = k1 < nk;
-        const float pv0 = ok0 ? nv0 * 128.f : 0.f, pv1 = ok1 ? nv1 * 128.f : 0.f;  // 2^P_SHIFT
+        const float pv0 = ok0 ? nv0 * NORM_FACTOR : 0.f, pv1 = ok1 ? nv1 * NORM_FACTOR : 0.f;
         uint32_t pb[2];
         const float d0 = (sa[0] + sa[1]) + (sb[0] + sb[1]);
         const float d1 = (sa[2] + sa[3]) + (sb[2] + sb[3]);
         const float s0 = ok0 ? d0 * (nk0 * qs) : -INFINITY;
         const float s1 = ok1 ? d1 * (nk1 * qs) : -INFINITY;
         float e0 = exp2_approx(s0 - M), e1 = exp2_approx(s1 - M);
-        // An operand past 2^15, a weight past 2^72 (what a norm of 2^-64 then has, the least that counts
-        // below: a value of no norm has operand 0, or NaN of an infinite weight, which fmaxf drops), or
-        // no maximum yet (e then infinite or NaN): the maximum is raised.  One vote a tile, where the
-        // maximum itself takes three exchanges.
-        if (__any_sync(FULL_MASK, !(fmaxf(e0 * pv0, e1 * pv1) <= 32768.f) || !(fmaxf(e0, e1) <= 0x1p72f) ||
+        // An operand past 2^15, a weight past W_MOST (a value of no norm has operand 0, or NaN of an
+        // infinite weight, which fmaxf drops), or no maximum yet (e then infinite or NaN): the maximum is
+        // raised.  One vote a tile, where the maximum itself takes three exchanges.
+        if (__any_sync(FULL_MASK, !(fmaxf(e0 * pv0, e1 * pv1) <= 32768.f) || !(fmaxf(e0, e1) <= W_MOST) ||
                                       M == -INFINITY)) {
           const float u0 = s0 + (ok0 ? fmaxf(log2_approx(nv0), -64.f) : 0.f);
           const float u1 = s1 + (ok1 ? fmaxf(log2_approx(nv1), -64.f) : 0.f);
           float bm = fmaxf(u0, u1);
           bm = fmaxf(bm, __shfl_xor_sync(FULL_MASK, bm, 4));
           bm = fmaxf(bm, __shfl_xor_sync(FULL_MASK, bm, 8));
-          bm = fmaxf(bm, __shfl_xor_sync(FULL_MASK, bm, 16));
+          bm = fmaxf(bm, __shfl_xor_sync(FULL_MASK, bm, 16)) - W_SHIFT;  // M is the maximum less W_SHIFT
           if (bm > M + RESCALE_SLACK) {  // also taken while M is -inf
             const float alpha = exp2_approx(M - bm);
             M = bm;
@@ -626,7 +625,7 @@ struct CombineParams {
   PagedView pv;
   PagedOut o;
   int Hq, gq, n_hg, hpc, units, grid;
-  float inv_vscale;        // 1 / (2^P_SHIFT * alpha_V)
+  float inv_vscale;        // 2^W_SHIFT / (2^P_SHIFT * alpha_V)
   const uint4 *vfrag;      // R and R^T of the values
   const float *split, *whole;
   const int32_t *unit;
@@ -794,7 +793,7 @@ cudaError_t launch_paged_decode(const tq_ctx *k, const tq_ctx *v, const PagedVie
   c.pv = pv, c.o = o;
   c.Hq = Hq, c.gq = p.gq, c.n_hg = l.n_hg, c.hpc = l.hpc, c.grid = l.grid;
   c.units = pv.B * pv.Hkv * l.n_hg;
-  c.inv_vscale = 1.0f / (exp2f(P_SHIFT) * v->f16.alpha);
+  c.inv_vscale = 1.0f / (exp2f(P_SHIFT - W_SHIFT) * v->f16.alpha);
   c.vfrag = v->d_rfrag;
   c.split = p.split, c.whole = p.whole, c.unit = p.unit;
   int blocks = 1;

@@ -90,7 +90,7 @@ struct Misc {
   uint64_t s_done[2][2], p_ready[2][2], pv_done[2][2];
   // Key norms of the last four K tiles (0 past the end): a K stage is free once its product
   // is done, while the softmax still needs the norms; the decoders reach tile j + 4 only after
-  // every group has finished tile j.  2^7 value norms of the two V stages.
+  // every group has finished tile j.  The value norms of the two V stages times NORM_FACTOR.
   alignas(16) float kn[4][KT];
   alignas(16) float nv[2][KT], nu[2][KT];  // and log2 of the norms
   // One part: the norms are in the operands, and these hold for 32 rows of a K tile its power of two, and
@@ -141,7 +141,7 @@ struct PrefillParams {
   JoinInfo *join;              // per CTA: the unit its first item continues
   float *split;                // [CTA][2][128-row tiles of a unit][PART] partials
   uint32_t klo[2], khi[2], vlo[2], vhi[2];
-  float inv_vscale;            // 1 / (2^P_SHIFT * alpha_V)
+  float inv_vscale;            // 1 / (2^P_SHIFT * alpha_V) times 2^-NORM_EXP (one part) or 2^W_SHIFT (two)
   const uint8_t *vr;           // R of the values as fp16 hi, lo tile images
 };
 // Norms in the operands: up to 2^13 times a scaled centroid (below 4) stays below 2^15.
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
             decode8<0x5140u, 0x7362u>(src[1 + ch], lo2, hi2, d);
             *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 8 * ch)) = make_uint4(d[0], d[1], d[2], d[3]);
           }
-          if (side) ms.nv[st][row] = norm * 128.0f, ms.nu[st][row] = fmaxf(log2_approx(norm), -64.f);
+          if (side) ms.nv[st][row] = norm * NORM_FACTOR, ms.nu[st][row] = fmaxf(log2_approx(norm), -64.f);
           else ms.kn[c & 3][row] = norm;
         } else {
           // The norm goes into the operand: x (nh + nl), the norm as two fp16 parts after the power of
@@ -987,9 +987,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           }
           return bm;
         };
-        // raise the running maximum of the rows that need it (the warp together)
+        // raise the running maximum of the rows that need it (the warp together); with two parts M is the
+        // maximum less W_SHIFT
         auto raise_max = [&](bool now) {
-          const float bm = row_max();
+          const float bm = row_max() - (LO ? W_SHIFT : 0);
           const bool raise = bm > M + (now ? 0.f : RESCALE_SLACK);  // also from -inf
           const float alpha = raise ? exp2_approx(M - bm) : 1.f;
           if (raise) M = bm, l *= alpha;
@@ -1468,7 +1469,7 @@ cudaError_t launch_paged_prefill(const tq_ctx *k, const tq_ctx *v, const PagedVi
     p.klo[i] = k->f16.lo[i], p.khi[i] = k->f16.hi[i];
     p.vlo[i] = v->f16.lo[i], p.vhi[i] = v->f16.hi[i];
   }
-  p.inv_vscale = 1.0f / (exp2f(P_SHIFT + (l.lo ? 0 : NORM_EXP)) * v->f16.alpha);
+  p.inv_vscale = 1.0f / (exp2f(P_SHIFT + (l.lo ? -W_SHIFT : NORM_EXP)) * v->f16.alpha);
   p.vr = reinterpret_cast<const uint8_t *>(v->d_rtile);
   e = l.lo ? launch_main<true, true>(p, l.grid, st)
            : (l.alt ? launch_main<true, false>(p, l.grid, st) : launch_main<false, false>(p, l.grid, st));

@@ -99,3 +99,41 @@ def test_scores_that_are_all_nan_reach_the_row(case):
     assert bad.sum() > 1 and not np.isfinite(got[bad]).any()
     ref[bad] = 0
     check_attention(torch.from_numpy(np.where(bad[..., None], 0, got)), ref, out_dtype)
+
+
+BIG = [  # lens, new, Hq, Hkv, P, output type
+    ([600, 40], [1, 1], 4, 2, 16, "f32"),
+    ([600, 40], [1, 1], 12, 2, 64, "f32"),
+    ([600, 40], [3, 40], 4, 2, 16, "f32"),
+    ([600, 40], [3, 3], 32, 2, 32, "bf16"),
+    ([600, 300], [20, 200], 16, 2, 32, "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", BIG, ids=lambda c: f"{c[5]}-t{max(c[1])}-g{c[2] // c[3]}")
+def test_value_norms_up_to_the_limit(case):
+    """Values of norms 2^126 and 2^127 everywhere (bf16 chunks: 2^118 and 2^119): the usual relative bound.  A norm
+    that is not finite (there: 2^120) makes the rows that see it not finite, and no others."""
+    import torch
+    lens, new, Hq, Hkv, P, out_dtype = case
+    tq = lib()
+    s = Setup(tq, lens, new, Hkv, P, 97, ("dense", "wht"), ragged=max(new) > 1)
+    top = 119 if out_dtype == "bf16" else 127
+    set_norms(s, 1, {(b, h, t): 2.0 ** (top - t % 2) for b, n in enumerate(lens) for h in range(Hkv) for t in range(n)})
+    got, ref = run_attention(s, Hq, "bf16", out_dtype)
+    small = 2.0 ** (1 - top)
+    got = got.float().cpu().numpy().astype(np.float64) * small
+    check_attention(torch.from_numpy(got), ref * small, out_dtype)
+    spots = [(0, 1, 577), (1, 0, 38)]
+    set_norms(s, 1, {x: 2.0 ** 120 if out_dtype == "bf16" else np.inf for x in spots})
+    got, ref = run_attention(s, Hq, "bf16", out_dtype)
+    got = got.float().cpu().numpy().astype(np.float64)
+    bad = np.zeros((s.n_rows, Hq), bool)
+    g = Hq // Hkv
+    for b, h, pos in spots:
+        for i in range(s.cu[b], s.cu[b + 1]):
+            if lens[b] - (s.cu[b + 1] - i) >= pos:
+                bad[i, h * g:(h + 1) * g] = True
+    assert bad.any() and not np.isfinite(got[bad]).any()
+    ref[bad] = 0
+    check_attention(torch.from_numpy(np.where(bad[..., None], 0, got * small)), ref * small, out_dtype)

@@ -21,6 +21,11 @@ constexpr int W_SHIFT = 24;
 constexpr float W_MOST = 0x1p96f;         // 2^(64 + RESCALE_SLACK + W_SHIFT)
 constexpr float NORM_FACTOR = 0x1p-17f;   // of a value norm, for a probability operand at 2^P_SHIFT: 2^(P_SHIFT - W_SHIFT)
 
+// x 2^d, d <= 0, of a sum of weights when its maximum is raised: in two halves, since 2^d alone may be
+// flushed (weights beside values of no norm, merged with values of norm 2^60) where the product is not.
+static __device__ __forceinline__ float lower(float x, float half_factor) { return x * half_factor * half_factor; }
+static __device__ __forceinline__ float lower_by(float x, float d) { return lower(x, exp2f(0.5f * d)); }
+
 // Rows that belong to a sequence.
 static __device__ __forceinline__ int paged_rows(const PagedView &v) {
   if (!v.cu_q) return v.B;

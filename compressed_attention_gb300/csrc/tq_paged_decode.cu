@@ -519,9 +519,9 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
           bm = fmaxf(bm, __shfl_xor_sync(FULL_MASK, bm, 8));
           bm = fmaxf(bm, __shfl_xor_sync(FULL_MASK, bm, 16)) - W_SHIFT;  // M is the maximum less W_SHIFT
           if (bm > M + RESCALE_SLACK) {  // also taken while M is -inf
-            const float alpha = exp2_approx(M - bm);
+            const float half = exp2_approx(0.5f * (M - bm)), alpha = half * half;
             M = bm;
-            lsum *= alpha;
+            lsum = lower(lsum, half);
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt)
               O[mt][0] *= alpha, O[mt][1] *= alpha, O[mt][2] *= alpha, O[mt][3] *= alpha;
@@ -588,7 +588,8 @@ __global__ void __maxnreg__(128) k_paged_partial(const DecodeParams p) {
       ms = fmaxf(ms, __shfl_xor_sync(FULL_MASK, ms, 8));
       ms = fmaxf(ms, __shfl_xor_sync(FULL_MASK, ms, 16));
       // (without a maximum a warp's sum is 0, or NaN where its scores are)
-      float ls = (m0 == -INFINITY ? l0 : l0 * exp2_approx(m0 - ms)) + (m1 == -INFINITY ? l1 : l1 * exp2_approx(m1 - ms));
+      float ls = (m0 == -INFINITY ? l0 : lower(l0, exp2_approx(0.5f * (m0 - ms)))) +
+                 (m1 == -INFINITY ? l1 : lower(l1, exp2_approx(0.5f * (m1 - ms))));
       ls += __shfl_xor_sync(FULL_MASK, ls, 4);
       ls += __shfl_xor_sync(FULL_MASK, ls, 8);
       ls += __shfl_xor_sync(FULL_MASK, ls, 16);
@@ -677,8 +678,8 @@ __global__ void __launch_bounds__(CB_WARPS * 32) k_paged_combine(const CombinePa
           for (int i = 0; i < 8; ++i)
             if (s0 + i < n && l8[i] != 0.f) mc = fmaxf(mc, m8[i]);
           if (mc > ms) {
-            const float f = (ms == -INFINITY) ? 0.f : exp2f(ms - mc);
-            ls *= f;
+            const float h = (ms == -INFINITY) ? 0.f : exp2f(0.5f * (ms - mc)), f = h * h;
+            ls = lower(ls, h);
 #pragma unroll
             for (int e = 0; e < 4; ++e) a[e] *= f;
             ms = mc;
@@ -686,8 +687,8 @@ __global__ void __launch_bounds__(CB_WARPS * 32) k_paged_combine(const CombinePa
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (s0 + i < n && l8[i] != 0.f) {
-              const float f = exp2f(m8[i] - ms);
-              ls = fmaf(f, l8[i], ls);
+              const float h = exp2f(0.5f * (m8[i] - ms)), f = h * h;
+              ls += lower(l8[i], h);
               a[0] = fmaf(f, v[i].x, a[0]), a[1] = fmaf(f, v[i].y, a[1]);
               a[2] = fmaf(f, v[i].z, a[2]), a[3] = fmaf(f, v[i].w, a[3]);
             }

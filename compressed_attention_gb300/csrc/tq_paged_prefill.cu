@@ -146,6 +146,10 @@ struct PrefillParams {
 };
 // Norms in the operands: up to 2^13 times a scaled centroid (below 4) stays below 2^15.
 constexpr int NORM_EXP = 12;
+// The least power of two of 32 value norms.  A weight beside values of no norm is 2^(7 + V_EXP_LEAST - e) when the
+// row's maximum has norms of 2^e: at 2^64, the largest that the encode writes, 21 octaves above exp2's flush.
+// Smaller norms use the operand's own range: 2^-67 keeps its precision.
+constexpr int V_EXP_LEAST = -48;
 // Floats of a 128-row partial: float4 e of row r at e * 128 + r, so that the threads of a warp, a row
 // each, write 512 bytes in a row (a row at a time they took 5 us an item); then maxima, sums.
 constexpr int PART = 128 * D + 256;
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
           const float an = fabsf(norm);
           const bool bad = !(an < (side ? 0x1p120f : INFINITY));  // (past 2^120 a sum of weights would underflow)
           const uint32_t most = __reduce_max_sync(FULL_MASK, bad ? 0u : __float_as_uint(an));
-          const int em = max((int)(most >> 23) - 127, side ? -64 : -114);
+          const int em = max((int)(most >> 23) - 127, side ? V_EXP_LEAST : -114);
           const float sn = side && bad ? 0.f : norm * pow2i(NORM_EXP - em);
           const __half nh = __float2half_rn(sn), nl = __float2half_rn(sn - __half2float(nh));
           const __half2 nh2 = __half2half2(nh), nl2 = __half2half2(nl);
@@ -992,8 +996,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
         auto raise_max = [&](bool now) {
           const float bm = row_max() - (LO ? W_SHIFT : 0);
           const bool raise = bm > M + (now ? 0.f : RESCALE_SLACK);  // also from -inf
-          const float alpha = raise ? exp2_approx(M - bm) : 1.f;
-          if (raise) M = bm, l *= alpha;
+          const float half = raise ? exp2_approx(0.5f * (M - bm)) : 1.f, alpha = half * half;
+          if (raise) M = bm, l = lower(l, half);
           if (done && __any_sync(FULL_MASK, raise)) {
             // O is whole once the previous half's PV has finished (this half's S was issued after
             // the one before that): half 0 of this tile, or half 1 of the tile before, which
@@ -1154,7 +1158,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
         const float f0 = M0 == -INFINITY ? 0.f : exp2f(M0 - Mx), f1 = M1 == -INFINITY ? 0.f : exp2f(M1 - Mx);
         fw = gr ? f1 : f0;
         // (without a maximum a group's sum is 0, or NaN where its scores are)
-        l = (M0 == -INFINITY ? l0 : f0 * l0) + (M1 == -INFINITY ? l1 : f1 * l1);
+        l = (M0 == -INFINITY ? l0 : lower_by(l0, M0 - Mx)) + (M1 == -INFINITY ? l1 : lower_by(l1, M1 - Mx));
         amax = fmaxf(f0 ? f0 * a0 : 0.f, f1 ? f1 * a1 : 0.f);
         M = Mx;
       } else if (!ok) {
@@ -1335,9 +1339,9 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const JoinParams
 #pragma unroll
     for (int i = 0; i < FLY; ++i) {
       if (lx[i] == 0.f) continue;
-      const float mn = fmaxf(top, mx[i]), f = exp2f(top - mn), wx = lx[i] * exp2f(mx[i] - mn);
+      const float mn = fmaxf(top, mx[i]), fh = exp2f(0.5f * (top - mn)), f = fh * fh, wx = lower_by(lx[i], mx[i] - mn);
       top = mn;
-      sum = fmaf(sum, f, wx);
+      sum = lower(sum, fh) + wx;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         a[h][0] = fmaf(a[h][0], f, wx * v[i][h].x), a[h][1] = fmaf(a[h][1], f, wx * v[i][h].y);

@@ -483,10 +483,10 @@ tq_status tq_paged_gather(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_pag
  * about 7e-5 scale |q| |k_hat| (the fp16 centroid table; chunks with a BF16 output add q's
  * and the keys' own rounding to fp16), which is what counts where scores reach the hundreds.
  * Chunks with a BF16 output also carry the values in fp16, the largest norm of 32 neighbours
- * at 2^12 to 2^13: a row that sees only values 2^20 times smaller than a neighbour's is
- * off by up to 1e-10 of that neighbour's norm.  A key with a NaN norm, or a value whose norm is
- * not finite (in chunks with a BF16 output: not below 2^120), makes the rows that see it not
- * finite, and no others. */
+ * at 2^12 to 2^13 (norms below 2^-48 lower, below 2^-67 with fewer bits): a row that sees only
+ * values 2^20 times smaller than a neighbour's is off by up to 1e-10 of that neighbour's norm.
+ * A key with a NaN norm, or a value whose norm is not finite (in chunks with a BF16 output: not
+ * below 2^120), makes the rows that see it not finite, and no others. */
 tq_status tq_paged_workspace_size(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
                                   const tq_paged_batch *batch, int Hq, size_t *bytes);
 tq_status tq_paged_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,

@@ -137,3 +137,23 @@ def test_value_norms_up_to_the_limit(case):
     assert bad.any() and not np.isfinite(got[bad]).any()
     ref[bad] = 0
     check_attention(torch.from_numpy(np.where(bad[..., None], 0, got * small)), ref * small, out_dtype)
+
+
+@pytest.mark.parametrize("case", [([700], [1], 4, 1, 16, "f32"), ([700], [1], 8, 1, 16, "f32"),
+                                  ([700, 90], [3, 3], 4, 1, 16, "f32"), ([700, 90], [3, 3], 16, 1, 16, "bf16"),
+                                  ([700, 90], [40, 60], 8, 1, 16, "bf16")],
+                         ids=lambda c: f"{c[5]}-t{max(c[1])}-g{c[2] // c[3]}")
+def test_weights_beside_values_of_the_largest_norm(case):
+    """A few values of norm 2^64 (the largest that the encode writes), the others zero: every key still counts in
+    the weights.  The large ones lie in three blocks of 32 keys, so that some warps, halves and tiles hold
+    zeros alone.  Outputs are a share of the large values; the usual relative bound."""
+    import torch
+    lens, new, Hq, Hkv, P, out_dtype = case
+    tq = lib()
+    s = Setup(tq, lens, new, Hkv, P, 101, ("wht", "wht"), ragged=max(new) > 1)
+    set_norms(s, 1, {(b, 0, t): 1.8e19 if t // 32 % 7 == 3 and t % 3 == 0 else 0.0
+                     for b, n in enumerate(lens) for t in range(n)})
+    got, ref = run_attention(s, Hq, "bf16", out_dtype)
+    scale = 2.0 ** -64
+    back = torch.from_numpy(got.float().cpu().numpy().astype(np.float64) * scale)
+    check_attention(back, ref * scale, out_dtype)

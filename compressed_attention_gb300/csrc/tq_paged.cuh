@@ -181,6 +181,14 @@ static __device__ __forceinline__ void store_lane4(void *out, int dtype, size_t 
         make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
 }
 
+// out_scale * rsqrt(mean(d^2) + eps) of a pair's ss = sum d^2.  All zero (a row without keys) stays zero
+// whatever eps is, NaN stays, and a mean below fp32's normal numbers counts as the least of them: the
+// factor, and with it the row, stays finite.
+static __device__ __forceinline__ float diff_factor(float ss, const DiffView &d) {
+  const float m = fmaf(ss, 1.0f / D, d.eps);
+  return ss == 0.f ? 0.f : d.out_scale * rsqrtf(m < 0x1p-126f ? 0x1p-126f : m);
+}
+
 // The end of a differential pair: a = out_scale * d [* rsqrt(mean(d^2) + eps) * gain],
 // d = a - lambda b, elements 4l .. 4l + 3 of lane l (the whole warp calls).
 static __device__ __forceinline__ void diff_finish(float (&a)[4], const float (&b)[4], const DiffView &d, int row,
@@ -197,10 +205,8 @@ static __device__ __forceinline__ void diff_finish(float (&a)[4], const float (&
   if (d.gain) {
 #pragma unroll
     for (int h = 16; h >= 1; h >>= 1) ss += __shfl_xor_sync(FULL_MASK, ss, h);
-    // all zero (a row without keys) stays zero whatever eps is
-    f = ss > 0.f ? f * rsqrtf(fmaf(ss, 1.0f / D, d.eps)) : 0.f;
+    f = diff_factor(ss, d);
     g = reinterpret_cast<const float4 *>(d.gain)[lane];
-    if (isnan(ss)) f = ss;
   }
   a[0] *= f * g.x, a[1] *= f * g.y, a[2] *= f * g.z, a[3] *= f * g.w;
 }

@@ -1248,8 +1248,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_paged_prefill(const PrefillParam
               ss = fmaf(d, d, ss);
             }
           }
-          // all zero (a row without keys) stays zero whatever eps is
-          scale = ss == 0.f ? 0.f : scale * rsqrtf(fmaf(ss, 1.0f / D, df.eps));
+          scale = diff_factor(ss, df);
         }
       }
 #pragma unroll 1
@@ -1380,8 +1379,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const JoinParams
     __syncthreads();
     const int w0 = warp & ~3, q = lane & 7;
     ss = (sums[w0][q] + sums[w0 + 1][q]) + (sums[w0 + 2][q] + sums[w0 + 3][q]);
-    // all zero (a row without keys) stays zero whatever eps is; NaN stays
-    f = ss == 0.f ? 0.f : f * rsqrtf(fmaf(ss, 1.0f / D, d.eps));
+    f = diff_factor(ss, d);
   }
   if (!live || (r & 1)) return;
 #pragma unroll

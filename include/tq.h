@@ -497,7 +497,11 @@ tq_status tq_paged_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_
 /* Differential attention: with a_h the fp32 output of q-head h above, pair p (q-heads 2p and
  * 2p + 1, which share a KV head: Hq / Hkv even) gives
  *   d = a_2p - lambda[i][p] a_2p+1,   out[i,p] = out_scale * d * rsqrt(mean(d^2) + eps) * gain
- * (the norm over the pair's 128 elements; without gain out[i,p] = out_scale * d). */
+ * (the norm over the pair's 128 elements; without gain out[i,p] = out_scale * d).  Both maps of a
+ * pair score against the same keys and weigh the same values of 128 elements: the form with
+ * grouped heads, not the one with keys of their own per map and values of two heads' width.
+ * The mean is held in fp32: with eps = 0 a pair with |d| below 2^-60 comes out smaller than the
+ * formula's, and past |d| = 2^63 the norm has no value. */
 typedef struct tq_diff {
   const float *lambda_w;  /* device fp32: the learned weight of row i, pair p at [i * lambda_stride + p] */
   int64_t lambda_stride;  /* >= Hq / 2, or 0: one weight per pair for every row */

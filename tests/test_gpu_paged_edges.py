@@ -1,10 +1,10 @@
 """Paged calls at the ends of their contract: keys and values of extreme norms, scores without a
-maximum."""
+maximum, pairs of small differences."""
 
 import numpy as np
 import pytest
 
-from gpu_util import lib
+from gpu_util import RTOL, lib
 from oracle import paged
 from test_gpu_paged import Setup, check_attention, device_rows, dt, run_attention, set_norms
 
@@ -157,3 +157,29 @@ def test_weights_beside_values_of_the_largest_norm(case):
     scale = 2.0 ** -64
     back = torch.from_numpy(got.float().cpu().numpy().astype(np.float64) * scale)
     check_attention(back, ref * scale, out_dtype)
+
+
+@pytest.mark.parametrize("case", [([40, 9], [1, 1], 4), ([40, 9], [2, 9], 4), ([2000], [1], 4), ([2000], [3], 4)],
+                         ids=lambda c: f"t{max(c[1])}-n{max(c[0])}")
+def test_differential_norm_of_small_pairs(case):
+    """eps = 0 and lambda = 0: the row over its rms, 1.5 in rms whatever the values' norms while their squares are
+    fp32's (2^-45), and finite, no larger, where they are not (2^-70, 2^-72, where the mean's square root
+    would be that of zero).  The relative bound of a row counts twice: for the row and for its norm."""
+    import torch
+    lens, new, Hq = case
+    tq = lib()
+    s = Setup(tq, lens, new, 1, 16, 103, ("wht", "dense"), ragged=max(new) > 1)
+    mix = tq.DiffMix(torch.zeros(Hq // 2, device="cuda"), torch.ones(128, device="cuda"), eps=0.0, out_scale=1.5)
+    q, q32 = device_rows(s.rng.standard_normal((s.n_rows, Hq, 128)), "f32")
+    for e in (-45, -70, -72):
+        set_norms(s, 1, {(b, 0, t): 2.0 ** e for b, n in enumerate(lens) for t in range(n)})
+        out = torch.full((s.n_rows, Hq // 2, 128), 7.0, device="cuda")
+        tq.tq_paged_diff_attention(*s.ctx, s.kv, s.batch, q, mix, out, s.workspace(Hq))
+        assert s.status() == 0
+        got = out.cpu().numpy().astype(np.float64)
+        assert np.all(np.isfinite(got))
+        ref = paged.differential(s.oracle(q32), np.zeros(Hq // 2), np.ones(128), 0.0, 1.5)
+        err, size = np.linalg.norm(got - ref, axis=-1), np.linalg.norm(ref, axis=-1)
+        if e == -45:
+            assert np.all(err <= 2 * RTOL * size)
+        assert np.all(np.linalg.norm(got, axis=-1) <= (1 + 2 * RTOL) * size)

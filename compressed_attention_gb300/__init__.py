@@ -570,10 +570,12 @@ class PagedKV:
 
 class PagedBatch:
     """The batch of a paged call (tq_paged_batch): ``seq_lens`` int32 CUDA [B], this call's tokens
-    included; ``cu_q`` int32 CUDA [B + 1] row offsets with ``max_q`` and ``n_tokens``, or None for
-    one row per sequence; ``max_len`` a bound on the lengths (0: what the block table holds)."""
+    included; ``cu_q`` int32 CUDA [B + 1] row offsets with ``n_tokens``, or None for one row per
+    sequence; ``max_q`` at least the most rows of a sequence (left out: n_tokens, which holds for any
+    offsets; single rows are faster with 1); ``max_len`` a bound on the lengths (0: what the block
+    table holds)."""
 
-    def __init__(self, seq_lens, cu_q=None, max_q=1, n_tokens=None, max_len=0):
+    def __init__(self, seq_lens, cu_q=None, max_q=None, n_tokens=None, max_len=0):
         torch = _torch()[0]
         _tensor(seq_lens, torch.int32, 1, "seq_lens")
         B = seq_lens.shape[0]
@@ -584,6 +586,8 @@ class PagedBatch:
         self.seq_lens, self.cu_q, self.B = seq_lens, cu_q, B
         self.on_gpu = seq_lens.is_cuda and (cu_q is None or cu_q.is_cuda)
         self.n_tokens = B if n_tokens is None else n_tokens
+        if max_q is None:
+            max_q = 1 if cu_q is None else max(self.n_tokens, 1)
         self.c = tq_paged_batch(_ptr(cu_q), _ptr(seq_lens), B, max_q, self.n_tokens, max_len)
         self.ref = ctypes.byref(self.c)
 

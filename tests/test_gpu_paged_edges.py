@@ -1,5 +1,5 @@
 """Paged calls at the ends of their contract: keys and values of extreme norms, scores without a
-maximum, pairs of small differences."""
+maximum, pairs of small differences, a batch without max_q."""
 
 import numpy as np
 import pytest
@@ -183,3 +183,12 @@ def test_differential_norm_of_small_pairs(case):
         if e == -45:
             assert np.all(err <= 2 * RTOL * size)
         assert np.all(np.linalg.norm(got, axis=-1) <= (1 + 2 * RTOL) * size)
+
+
+def test_offsets_without_the_most_rows():
+    """max_q left out: every row of a ragged batch is computed."""
+    tq = lib()
+    s = Setup(tq, [70, 9, 30], [5, 9, 1], 2, 16, 107)
+    s.batch = tq.PagedBatch(s.d_lens, s.batch.cu_q, n_tokens=s.n_rows)
+    got, ref = run_attention(s, 8, "bf16", "f32")
+    check_attention(got, ref, "f32")

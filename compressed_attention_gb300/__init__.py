@@ -552,14 +552,14 @@ class PagedKV:
     def __init__(self, k_pages, v_pages, block_table, page_size, Hkv):
         torch = _torch()[0]
         _tensor(block_table, torch.int32, 2, "block_table")
-        per = Hkv * page_size * tq_row_bytes("turbo4")
+        page = (Hkv, page_size, tq_row_bytes("turbo4"))
         for t in (k_pages, v_pages):
-            if t.dtype != torch.uint8 or not t.is_contiguous() or per < 1 or t.numel() % per:
-                raise ValueError("pages must be contiguous uint8 tensors of whole pages")
-        if k_pages.numel() != v_pages.numel():
+            if t.dtype != torch.uint8 or not t.is_contiguous() or t.shape[1:] != page or not t.shape[0]:
+                raise ValueError(f"pages must be contiguous uint8 tensors [n_pages, {', '.join(map(str, page))}]")
+        if k_pages.shape != v_pages.shape:
             raise ValueError("k_pages and v_pages must have one size")
         self.k_pages, self.v_pages, self.block_table = k_pages, v_pages, block_table
-        self.page_size, self.Hkv, self.n_pages = page_size, Hkv, k_pages.numel() // per
+        self.page_size, self.Hkv, self.n_pages = page_size, Hkv, k_pages.shape[0]
         self.n_seqs = block_table.shape[0]
         self.on_gpu = k_pages.is_cuda and v_pages.is_cuda and block_table.is_cuda
         width = block_table.shape[1]

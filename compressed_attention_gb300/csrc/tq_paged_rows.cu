@@ -311,17 +311,8 @@ __global__ void __launch_bounds__(AD_WARPS * 32) k_paged_append_dense(const Appe
       s[0] = __fadd_rn(s[0], __shfl_xor_sync(FULL_MASK, s[0], 2));
       s[0] = __fadd_rn(s[0], __shfl_xor_sync(FULL_MASK, s[0], 1));
       const float n = __fsqrt_rn(s[0]);  // of row rb + lane / 4
-      const bool tiny = n < 0x1p-100f && n > 0.f;
-      float inv = n >= 0x1p-100f ? __fdiv_rn(1.0f, n) : 0.0f;
-      if (__any_sync(FULL_MASK, tiny)) {  // 1 / n might not be finite: both by 2^64 first
-        if (tiny) inv = __fdiv_rn(1.0f, n * 0x1p64f);
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const float f = __shfl_sync(FULL_MASK, tiny ? 0x1p64f : 1.f, 4 * i);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][e] *= f;
-        }
-      }
+      // a norm that is not zero is at least 2^-74.5, the root of the smallest fp32: 1 / n is finite
+      const float inv = n > 0.f ? __fdiv_rn(1.0f, n) : 0.0f;
       const int64_t to = __shfl_sync(FULL_MASK, at.at, rb + (lane >> 2));
       if (t == 0 && to >= 0) *reinterpret_cast<float *>(sd.pages + to) = n;
 #pragma unroll

@@ -73,15 +73,84 @@ tq_status build_rotation(int kind, int d, uint64_t seed, std::vector<float> &r, 
   return TQ_OK;
 }
 
-template <typename T>
-tq_status to_device(T **dst, const T *src, size_t n) {
-  cudaError_t e = cudaMalloc((void **)dst, n * sizeof(T));
-  if (e != cudaSuccess) return fail(TQ_ERR_ALLOC, "cudaMalloc failed");
-  e = cudaMemcpy(*dst, src, n * sizeof(T), cudaMemcpyHostToDevice);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy");
-  return TQ_OK;
+// What follows from R (and the QJL matrix S), element by element.
+struct TableParams {
+  int d;
+  const float *r;    // [d][d]
+  float *rt;         // R^T
+  uint16_t *pib;     // dense, d = 128: R as bf16 hi, lo
+  uint16_t *frag;    // turbo4, d = 128: R and R^T as bf16 hi + lo A fragments of m16n8k16
+  uint16_t *tile;    // the same: R as fp16 hi, lo in the swizzled operand layout
+  const float *S;    // prod3: [128][128]
+  float *St;
+};
+__global__ void k_ctx_tables(const TableParams p) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < p.d * p.d) p.rt[(i % p.d) * p.d + i / p.d] = p.r[i];
+  if (i < D * D) {
+    if (p.St) p.St[(i % D) * D + i / D] = p.S[i];
+    if (p.pib) {  // hi = RN(r), lo = RN(r - hi)
+      const __nv_bfloat16 hi = __float2bfloat16_rn(p.r[i]);
+      p.pib[i] = __bfloat16_as_ushort(hi);
+      p.pib[D * D + i] = __bfloat16_as_ushort(__float2bfloat16_rn(p.r[i] - __bfloat162float(hi)));
+    }
+    if (p.tile) {
+      const __half hi = __float2half_rn(p.r[i]);
+      const uint32_t at = sw128_offset(i / D, i % D) / 2;
+      p.tile[at] = __half_as_ushort(hi);
+      p.tile[D * D + at] = __half_as_ushort(__float2half_rn(p.r[i] - __half2float(hi)));
+    }
+  }
+  if (p.frag && i < 2 * D * D) {
+    // [matrix][part][m-tile][k-step][lane][8]: lane 4g + t holds rows g, g + 8 and columns 2t, 2t + 1
+    // (+ 8) of each 16 x 16 tile, register e / 2, half e % 2
+    const int m = i / (D * D), e = i & 7, lane = (i >> 3) & 31, ks = (i >> 8) & 7, mt = (i >> 11) & 7;
+    const int row = 16 * mt + (lane >> 2) + 8 * ((e >> 1) & 1), col = 16 * ks + 2 * (lane & 3) + 8 * (e >> 2) + (e & 1);
+    const float x = m ? p.r[col * D + row] : p.r[row * D + col];
+    const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+    uint16_t *f = p.frag + 2 * m * D * D + (i & (D * D - 1));
+    f[0] = __bfloat16_as_ushort(hi);
+    f[D * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x - __bfloat162float(hi)));
+  }
 }
 
+// The context's device tables, in one allocation: R, S, the bucket table and the status word come from the host
+// in one copy, the rest from R on the device (bf16 and fp16 parts of 65,536 elements took the host as long as
+// everything else).
+tq_status device_tables(tq_ctx *c, const std::vector<float> &r, const std::vector<float> &S) {
+  size_t bytes = 0;
+  auto take = [&](size_t n) {
+    const size_t at = bytes;
+    bytes = (bytes + n + 255) & ~(size_t)255;
+    return at;
+  };
+  const size_t dd = (size_t)D * D;
+  const bool parts = c->fmt == TQ_FMT_TURBO4 && c->d == D, dense = c->p.rotation == TQ_ROT_DENSE && c->d == D && !r.empty();
+  const size_t status = take(sizeof(int32_t)), bt = take(r.empty() ? 0 : sizeof(BucketTable));
+  const size_t pi = take(r.size() * 4), s = take(S.size() * 4), host = bytes;
+  const size_t pit = take(r.size() * 4), st = take(S.size() * 4), pib = take(dense ? 2 * dd * 2 : 0);
+  const size_t frag = take(parts ? 4 * dd * 2 : 0), tile = take(parts ? 2 * dd * 2 : 0);
+  cudaError_t e = cudaMalloc(&c->d_tables, bytes);
+  if (e != cudaSuccess) return fail(TQ_ERR_ALLOC, "cudaMalloc failed");
+  uint8_t *base = static_cast<uint8_t *>(c->d_tables);
+  std::vector<uint8_t> up(host, 0);
+  if (!r.empty()) std::memcpy(up.data() + bt, &c->bt, sizeof(c->bt)), std::memcpy(up.data() + pi, r.data(), r.size() * 4);
+  if (!S.empty()) std::memcpy(up.data() + s, S.data(), S.size() * 4);
+  if ((e = cudaMemcpy(base, up.data(), host, cudaMemcpyHostToDevice)) != cudaSuccess) return cuda_fail(e, "cudaMemcpy");
+  c->d_status = reinterpret_cast<int32_t *>(base + status);
+  if (r.empty()) return TQ_OK;
+  c->d_bt = reinterpret_cast<BucketTable *>(base + bt);
+  c->d_pi = reinterpret_cast<float *>(base + pi), c->d_pit = reinterpret_cast<float *>(base + pit);
+  if (!S.empty()) c->d_S = reinterpret_cast<float *>(base + s), c->d_St = reinterpret_cast<float *>(base + st);
+  if (dense) c->d_pib = reinterpret_cast<uint16_t *>(base + pib);
+  if (parts) c->d_rfrag = reinterpret_cast<uint4 *>(base + frag), c->d_rtile = reinterpret_cast<uint16_t *>(base + tile);
+  const TableParams p{c->d, c->d_pi, c->d_pit, c->d_pib, reinterpret_cast<uint16_t *>(c->d_rfrag), c->d_rtile, c->d_S, c->d_St};
+  k_ctx_tables<<<256, 256>>>(p);  // 65,536 threads: the elements of a d = 256 matrix
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "k_ctx_tables");
+  // the tables are whole before any stream may use them
+  if ((e = cudaStreamSynchronize(nullptr)) != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
+  return TQ_OK;
+}
 
 tq_status check_decode_common(const tq_ctx *k, const tq_ctx *v, int B, int Hq, int Hkv, int L,
                               DecodeShape *shape) {
@@ -288,6 +357,7 @@ tq_status tq_ctx_create(const tq_params *params, tq_ctx **out) {
     return cuda_fail(e, "cudaGetDevice");
   }
   tq_status s = TQ_OK;
+  std::vector<float> r, S;
   if (rotated) {
     const int bits = code_bits(p.format);
     int kind = p.codebook;
@@ -299,69 +369,13 @@ tq_status tq_ctx_create(const tq_params *params, tq_ctx **out) {
     store_codebook(c64, c->cb.K, c->cb.c, c->cb.b);
     c->f16 = make_f16_table(c->cb.c, c->cb.K);
     c->bt = make_bucket_table(c->cb.b, c->cb.K - 1);
-    std::vector<float> r;
     s = build_rotation(p.rotation, d, p.rot_seed, r, c->wht_neg);
-    if (s == TQ_OK) s = to_device(&c->d_pi, r.data(), r.size());
-    if (s == TQ_OK) {
-      std::vector<float> rt((size_t)d * d);
-      for (int i = 0; i < d; ++i)
-        for (int j = 0; j < d; ++j) rt[(size_t)j * d + i] = r[(size_t)i * d + j];
-      s = to_device(&c->d_pit, rt.data(), rt.size());
-    }
-    if (s == TQ_OK && p.rotation == TQ_ROT_DENSE && d == D) {
-      // bf16 hi + lo parts of R for the tensor-core write: hi = RN(r), lo = RN(r - hi)
-      std::vector<uint16_t> rb(2 * (size_t)D * D);
-      for (size_t i = 0; i < (size_t)D * D; ++i) {
-        const __nv_bfloat16 hi = __float2bfloat16_rn(r[i]);
-        const __nv_bfloat16 lo = __float2bfloat16_rn(r[i] - __bfloat162float(hi));
-        rb[i] = __bfloat16_as_ushort(hi);
-        rb[(size_t)D * D + i] = __bfloat16_as_ushort(lo);
-      }
-      s = to_device(&c->d_pib, rb.data(), rb.size());
-    }
-    if (s == TQ_OK && p.format == TQ_FMT_TURBO4 && d == D) {
-      // R and R^T as bf16 hi + lo A fragments of m16n8k16, [matrix][part][m-tile][k-step][lane]:
-      // lane 4g + t holds rows g, g + 8 and columns 2t, 2t + 1 (+ 8) of each 16 x 16 tile
-      std::vector<uint16_t> f(2 * 2 * (size_t)D * D);
-      for (int m = 0; m < 2; ++m)
-        for (int mt = 0; mt < 8; ++mt)
-          for (int ks = 0; ks < 8; ++ks)
-            for (int lane = 0; lane < 32; ++lane)
-              for (int e = 0; e < 8; ++e) {  // register e / 2, half e % 2
-                const int row = 16 * mt + (lane >> 2) + 8 * ((e >> 1) & 1);
-                const int col = 16 * ks + 2 * (lane & 3) + 8 * (e >> 2) + (e & 1);
-                const float x = m ? r[(size_t)col * D + row] : r[(size_t)row * D + col];
-                const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-                const size_t at = ((((size_t)(2 * m) * 8 + mt) * 8 + ks) * 32 + lane) * 8 + e;
-                f[at] = __bfloat16_as_ushort(hi);
-                f[at + (size_t)D * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x - __bfloat162float(hi)));
-              }
-      s = to_device(&c->d_rfrag, reinterpret_cast<const uint4 *>(f.data()), f.size() / 8);
-      for (int i = 0; i < D; ++i)
-        for (int j = 0; j < D; ++j) {
-          const float x = r[(size_t)i * D + j];
-          const __half hi = __float2half_rn(x);
-          const size_t at = sw128_offset(i, j) / 2;
-          f[at] = __half_as_ushort(hi);
-          f[at + (size_t)D * D] = __half_as_ushort(__float2half_rn(x - __half2float(hi)));
-        }
-      if (s == TQ_OK) s = to_device(&c->d_rtile, f.data(), 2 * (size_t)D * D);
-    }
     if (s == TQ_OK && p.format == TQ_FMT_PROD3) {
-      std::vector<float> S((size_t)D * D), St((size_t)D * D);
+      S.resize((size_t)D * D);
       tq_make_qjl_matrix(D, p.qjl_seed, S.data());
-      for (int i = 0; i < D; ++i)
-        for (int j = 0; j < D; ++j) St[(size_t)j * D + i] = S[(size_t)i * D + j];
-      s = to_device(&c->d_S, S.data(), S.size());
-      if (s == TQ_OK) s = to_device(&c->d_St, St.data(), St.size());
     }
   }
-  if (s == TQ_OK && rotated) s = to_device(&c->d_bt, &c->bt, 1);
-  if (s == TQ_OK) {
-    e = cudaMalloc((void **)&c->d_status, sizeof(int32_t));
-    if (e != cudaSuccess) s = fail(TQ_ERR_ALLOC, "cudaMalloc failed");
-    else if ((e = cudaMemset(c->d_status, 0, sizeof(int32_t))) != cudaSuccess) s = cuda_fail(e, "cudaMemset");
-  }
+  if (s == TQ_OK) s = device_tables(c, r, S);
   if (s != TQ_OK) {
     tq_ctx_destroy(c);
     return s;
@@ -372,15 +386,7 @@ tq_status tq_ctx_create(const tq_params *params, tq_ctx **out) {
 
 tq_status tq_ctx_destroy(tq_ctx *ctx) {
   if (!ctx) return TQ_OK;
-  cudaFree(ctx->d_pi);
-  cudaFree(ctx->d_pit);
-  cudaFree(ctx->d_S);
-  cudaFree(ctx->d_St);
-  cudaFree(ctx->d_pib);
-  cudaFree(ctx->d_rfrag);
-  cudaFree(ctx->d_rtile);
-  cudaFree(ctx->d_bt);
-  cudaFree(ctx->d_status);
+  cudaFree(ctx->d_tables);
   delete ctx;
   return TQ_OK;
 }

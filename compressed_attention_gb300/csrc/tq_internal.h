@@ -68,6 +68,7 @@ struct tq_ctx {
   tq::F16Table f16{};
   int d = 128;                         // head dimension: 128, or 256 (turbo4)
   uint32_t wht_neg[8] = {};             // bit j set: WHT sign j is -1
+  void *d_tables = nullptr;             // the one allocation that holds the tables below
   float *d_pi = nullptr;                // rotation R (dense Pi or the WHT matrix), fp32 row-major
   float *d_pit = nullptr;               // R^T, fp32 row-major
   float *d_S = nullptr;                 // QJL matrix S, fp32 [128][128] row-major

@@ -34,10 +34,12 @@
 //                     one CTA is finished there: differential pairs, norm, rounding.
 //   k_paged_join      units shared by CTAs: the log-sum-exp merge of their partials.
 //
-// Parts: for bf16 outputs q, K, V, P and O / l enter as one fp16 each (errors of 2^-12, random
-// over 128 dims or the keys: 4e-4 of the output's norm next to bf16's own 1.7e-3); for fp16
-// and fp32 outputs q, P and O / l as hi + lo and K, V as centroids with fp32 norms outside the
-// products, which leaves the fp16 centroid table's 3e-5.
+// Parts: for bf16 outputs q, K, V, P, O / l and R enter as one fp16 each (errors of 2^-12, random over
+// 128 dims or the keys).  Together 6e-4 of the output's norm in rms at 300 keys and 8e-4 at 16,000
+// (1 to 4% of the rows beyond 1e-3, one in a thousand beyond 2e-3) next to bf16's own 1.7e-3; the largest
+// share is that of the scores, where a key's 16 values round alike.  For fp16 and fp32 outputs q, P
+// and O / l enter as hi + lo and K, V as centroids with fp32 norms outside the products, which leaves
+// the fp16 centroid table's 6e-5.
 //
 // Measured (GB300): 4 chunks of 200 .. 512 tokens on 4K .. 16K keys, 32 q-heads on 8, bf16: 240 us
 // for 199 GFLOP (prep 20, join 13, the rest the attention), 43% of the cuBLAS bf16 rate; prompts of

@@ -456,9 +456,11 @@ tq_status tq_paged_append(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_pag
 /* Read the batch's rows back from the cache: k_out / v_out (either may be NULL) receive
  * [n_tokens][Hkv][128] reconstructions of out_dtype (F32, BF16 or F16, rounded once from
  * fp32), 16-byte aligned, as tq_dequantize: norm * R^T c[idx], or norm * c[idx] in the
- * rotated basis with unrotate == 0.  Keys come back with their position rotation.  A whole
- * sequence is read by a batch whose rows are all its tokens.  A page id out of range reads
- * page 0 (flagged, status 5). */
+ * rotated basis with unrotate == 0.  Un-rotated BF16 and F16 outputs take the centroids from the
+ * fp16 table (within 6e-5 of the row's norm), BF16 ones R as one fp16 too (2e-4 of the norm in
+ * rms, next to the 1.7e-3 of their own rounding).  Keys come back with their position rotation.
+ * A whole sequence is read by a batch whose rows are all its tokens.  A page id out of range
+ * reads page 0 (flagged, status 5). */
 tq_status tq_paged_gather(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
                           const tq_paged_batch *batch, int unrotate, void *k_out, void *v_out,
                           int out_dtype, tq_stream_t stream);
@@ -478,13 +480,17 @@ tq_status tq_paged_gather(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_pag
  * for (give a tight max_len), pass 2^31.
  * Sums, maxima and outputs are held in fp32; the tensor-core operands are fp16 parts (the
  * kernels' header comments state which products carry one part and which two).  With scores
- * of ordinary size the rows are within 2e-3 absolute and 1e-3 relative of the formula, as
- * tq_decode_attention's, before the rounding to out_dtype; a score itself is off by at most
- * about 7e-5 scale |q| |k_hat| (the fp16 centroid table; chunks with a BF16 output add q's
- * and the keys' own rounding to fp16), which is what counts where scores reach the hundreds.
- * Chunks with a BF16 output also carry the values in fp16, the largest norm of 32 neighbours
- * at 2^12 to 2^13 (norms below 2^-48 lower, below 2^-67 with fewer bits): a row that sees only
- * values 2^20 times smaller than a neighbour's is off by up to 1e-10 of that neighbour's norm.
+ * of ordinary size single rows, and chunks with an F32 or F16 output, are within 2e-3 absolute
+ * and 1e-3 relative of the formula, as tq_decode_attention's, before the rounding to out_dtype;
+ * a score itself is off by at most about 7e-5 scale |q| |k_hat| (the fp16 centroid table), which
+ * is what counts where scores reach the hundreds.
+ * Chunks with a BF16 output carry q, the keys and the values with their norms, the probabilities,
+ * the quotient and the un-rotation as one fp16 each: a row is off by 6e-4 (300 keys) to 8e-4
+ * (16,000 keys) of its norm in rms, by 2.5e-3 at most in 99.9% of the rows, and a score by up
+ * to 2^-10 scale |q| |k_hat|, beside bf16's own rounding (1.7e-3 in rms; measured with rows and q
+ * of unit variance).  The largest norm of 32 neighbouring values is held at 2^12 to 2^13
+ * (norms below 2^-48 lower, below 2^-67 with fewer bits): a row that sees only values 2^20 times
+ * smaller than a neighbour's is off by up to 1e-10 of that neighbour's norm.
  * A key with a NaN norm, or a value whose norm is not finite (in chunks with a BF16 output: not
  * below 2^120), makes the rows that see it not finite, and no others. */
 tq_status tq_paged_workspace_size(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,

@@ -6,6 +6,7 @@ import pytest
 
 from gpu_util import RTOL, lib
 from oracle import paged
+from oracle.formats import unpack_turbo4
 from test_gpu_paged import Setup, check_attention, device_rows, dt, run_attention, set_norms
 
 pytestmark = pytest.mark.gpu
@@ -192,3 +193,62 @@ def test_offsets_without_the_most_rows():
     s.batch = tq.PagedBatch(s.d_lens, s.batch.cu_q, n_tokens=s.n_rows)
     got, ref = run_attention(s, 8, "bf16", "f32")
     check_attention(got, ref, "f32")
+
+
+def one_part(s, b, q32, Hq):
+    """Sequence b's rows in fp64: by the formula, and with q, the keys, the probabilities, the values, the
+    quotient and R each rounded once to fp16, in the kernel's units (the centroids times the alpha that
+    makes their fp16 table's error smallest, q times log2(e) / (sqrt(128) alpha))."""
+    f16 = lambda x: x.astype(np.float16).astype(np.float64)  # noqa: E731
+    n, lo, hi = s.lens[b], int(s.cu[b]), int(s.cu[b + 1])
+    g, pos = Hq // s.Hkv, n - (hi - lo) + np.arange(hi - lo)
+    table, alpha, norms = [], [], []
+    for c, h in zip(s.codec, s.host):
+        mag = np.abs(c.c32[:8]).astype(np.float64)
+        a = 1 + np.arange(65536) / 65536
+        v = a[:, None] * mag
+        alpha.append(a[(np.abs(v.astype(np.float32).astype(np.float16) - v) / v).max(1).argmin()])
+        norm, idx = unpack_turbo4(paged.sequence_rows(h, s.table, b, n).reshape(-1, 68))
+        table.append(c.c32.astype(np.float64)[idx].reshape(n, s.Hkv, 128))
+        norms.append(norm.astype(np.float64).reshape(n, s.Hkv, 1))
+    ref, em = np.empty((2, hi - lo, Hq, 128))
+    seen = np.arange(n) <= pos[:, None]
+    for h in range(Hq):
+        q = q32[lo:hi, h].astype(np.float64) @ s.codec[0].rot.R.T
+        K, V = (norms[i][:, h // g] * table[i][:, h // g] for i in range(2))
+        x = np.where(seen, q @ K.T / np.sqrt(128), -np.inf)
+        w = np.exp(x - x.max(1, keepdims=True))
+        ref[:, h] = w @ V / w.sum(1, keepdims=True) @ s.codec[1].rot.R
+        K1, V1 = (f16(norms[i][:, h // g] * 2.0 ** 8 * f16(alpha[i] * table[i][:, h // g])) * 2.0 ** -8 for i in range(2))
+        x = np.where(seen, f16(q * (1 / np.log(2) / np.sqrt(128) / alpha[0])) @ K1.T, -np.inf)
+        p = 2.0 ** (x - x.max(1, keepdims=True) + 7)
+        o = f16(p) @ V1 / p.sum(1, keepdims=True) / alpha[1]
+        up = 2.0 ** (13 - np.floor(np.log2(np.abs(o).max(1, keepdims=True))))
+        em[:, h] = f16(o * up) / up @ f16(s.codec[1].rot.R)
+    return ref, em
+
+
+@pytest.mark.parametrize("rot", ["wht", "dense"])
+@pytest.mark.parametrize("n", [300, 6000])
+def test_bf16_chunks_add_what_their_operands_round(rot, n):
+    """What a bf16 chunk is off beyond the rounding of its output, in rms over all elements: the rounding of the
+    formula's own values is independent of the rest, so the squares subtract.  The rest is that of the six
+    operands' roundings (two of them, of other draws than the emulation's, and 1.5% of noise in the
+    difference: 10%), and below 1e-3 of the rows' norm."""
+    tq = lib()
+    s = Setup(tq, [n, 150], [128, 100], 2, 64, 109, (rot, rot))
+    import torch
+    q, q32 = device_rows(s.rng.standard_normal((s.n_rows, 8, 128)), "bf16")
+    out = torch.zeros((s.n_rows, 8, 128), dtype=torch.bfloat16, device="cuda")
+    tq.tq_paged_attention(*s.ctx, s.kv, s.batch, q, out, s.workspace(8))
+    assert s.status() == 0
+    ref, em = (np.concatenate(x) for x in zip(*(one_part(s, b, q32, 8) for b in range(2))))
+    nearest = torch.from_numpy(ref).to(torch.bfloat16).double().numpy()
+    got = out.float().cpu().numpy().astype(np.float64)
+    square = lambda x: float((x * x).sum())  # noqa: E731
+    for rows in (slice(0, 128), slice(128, 228)):
+        size = square(ref[rows])
+        rest = np.sqrt(max(square((got - ref)[rows]) - square((nearest - ref)[rows]), 0) / size)
+        emulated = np.sqrt(square((em - ref)[rows]) / size)
+        print(f"{rot} {n}: {rest:.3e}, emulated {emulated:.3e}")
+        assert rest <= 1.1 * emulated and rest <= 1e-3

@@ -7,9 +7,13 @@
 
 #include <cmath>
 #include <cstring>
+#include <list>
+#include <map>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <string>
+#include <tuple>
 #include <vector>
 
 #include "tq_internal.h"
@@ -45,15 +49,65 @@ int code_bits(int fmt) {
   }
 }
 
+// The tables that a format's codebook gives: constants of (bits, d, kind), made once in a process.
+struct CodeTables {
+  Codebook cb;
+  F16Table f16;
+  BucketTable bt;
+};
+const CodeTables &code_tables(int bits, int d, int kind) {
+  static std::mutex mu;
+  static std::map<std::tuple<int, int, int>, CodeTables> made;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_tuple(bits, d, kind);
+  const auto it = made.find(key);
+  if (it != made.end()) return it->second;
+  CodeTables t;
+  double c64[16];
+  make_codebook_f64(bits, d, kind, c64);
+  t.cb.bits = bits;
+  t.cb.K = 1 << bits;
+  store_codebook(c64, t.cb.K, t.cb.c, t.cb.b);
+  t.f16 = make_f16_table(t.cb.c, t.cb.K);
+  t.bt = make_bucket_table(t.cb.b, t.cb.K - 1);
+  return made.emplace(key, t).first->second;
+}
+
+// The dense rotation of a seed, fp32.  A model's layers make their contexts of one or two seeds: the last
+// eight matrices (64 KB each at d = 128) are held, since a factorisation takes as long as ten contexts
+// without one.  Null: a rank-deficient Gaussian.
+std::shared_ptr<const std::vector<float>> dense_rotation(uint64_t seed, int d) {
+  using Matrix = std::shared_ptr<const std::vector<float>>;
+  struct Held {
+    uint64_t seed;
+    int d;
+    Matrix m;
+  };
+  static std::mutex mu;
+  static std::list<Held> held;  // the last used first
+  std::lock_guard<std::mutex> lock(mu);
+  for (auto it = held.begin(); it != held.end(); ++it)
+    if (it->seed == seed && it->d == d) {
+      held.splice(held.begin(), held, it);
+      return it->m;
+    }
+  std::vector<double> pi((size_t)d * d);
+  if (!dense_rotation_f64(seed, d, pi.data())) return nullptr;
+  Matrix m = std::make_shared<const std::vector<float>>(pi.begin(), pi.end());
+  held.push_front(Held{seed, d, m});
+  if (held.size() > 8) held.pop_back();
+  return m;
+}
+
 // The d x d rotation R (row-major fp32) and, for the WHT, its sign bits (d / 32 words).
 tq_status build_rotation(int kind, int d, uint64_t seed, std::vector<float> &r, uint32_t *neg) {
-  r.assign((size_t)d * d, 0.f);
   if (kind == TQ_ROT_DENSE) {
-    std::vector<double> pi((size_t)d * d);
-    if (!dense_rotation_f64(seed, d, pi.data())) return fail(TQ_ERR_INVALID_ARG, "rank-deficient Gaussian");
-    for (size_t i = 0; i < pi.size(); ++i) r[i] = (float)pi[i];
+    const auto m = dense_rotation(seed, d);
+    if (!m) return fail(TQ_ERR_INVALID_ARG, "rank-deficient Gaussian");
+    r = *m;
     return TQ_OK;
   }
+  r.assign((size_t)d * d, 0.f);
   std::vector<uint64_t> out(d);
   splitmix64_fill(seed, out.data(), d);
   for (int i = 0; i < d / 32; ++i) neg[i] = 0;
@@ -150,6 +204,35 @@ tq_status device_tables(tq_ctx *c, const std::vector<float> &r, const std::vecto
   // the tables are whole before any stream may use them
   if ((e = cudaStreamSynchronize(nullptr)) != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
   return TQ_OK;
+}
+
+// What a new context holds, from its checked parameters.
+tq_status fill_context(tq_ctx *c, const tq_params &p, bool rotated) {
+  c->p = p;
+  c->fmt = p.format;
+  c->d = p.d;
+  const int d = p.d;
+  c->qjl_factor = (p.format == TQ_FMT_PROD3 && p.qjl_shrink) ? (float)(2.0 / 3.14159265358979323846) : 1.0f;
+  cudaError_t e = cudaGetDevice(&c->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(&c->reserved_smem, cudaDevAttrReservedSharedMemoryPerBlock, c->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  tq_status s = TQ_OK;
+  std::vector<float> r, S;
+  if (rotated) {
+    const int bits = code_bits(p.format);
+    int kind = p.codebook;
+    if (kind == TQ_CB_DEFAULT) kind = (p.format == TQ_FMT_TURBO4) ? TQ_CB_QUANTILE : TQ_CB_LLOYD;
+    const CodeTables &t = code_tables(bits, d, kind);
+    c->cb = t.cb, c->f16 = t.f16, c->bt = t.bt;
+    s = build_rotation(p.rotation, d, p.rot_seed, r, c->wht_neg);
+    if (s == TQ_OK && p.format == TQ_FMT_PROD3) {
+      S.resize((size_t)D * D);
+      tq_make_qjl_matrix(D, p.qjl_seed, S.data());
+    }
+  }
+  return s == TQ_OK ? device_tables(c, r, S) : s;
 }
 
 tq_status check_decode_common(const tq_ctx *k, const tq_ctx *v, int B, int Hq, int Hkv, int L,
@@ -343,39 +426,12 @@ tq_status tq_ctx_create(const tq_params *params, tq_ctx **out) {
 
   tq_ctx *c = new (std::nothrow) tq_ctx();
   if (!c) return fail(TQ_ERR_ALLOC, "host allocation failed");
-  c->p = p;
-  c->fmt = p.format;
-  c->d = p.d;
-  const int d = p.d;
-  c->qjl_factor = (p.format == TQ_FMT_PROD3 && p.qjl_shrink) ? (float)(2.0 / 3.14159265358979323846) : 1.0f;
-  cudaError_t e = cudaGetDevice(&c->device);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device);
-  if (e == cudaSuccess)
-    e = cudaDeviceGetAttribute(&c->reserved_smem, cudaDevAttrReservedSharedMemoryPerBlock, c->device);
-  if (e != cudaSuccess) {
-    delete c;
-    return cuda_fail(e, "cudaGetDevice");
+  tq_status s = TQ_ERR_ALLOC;
+  try {
+    s = fill_context(c, p, rotated);
+  } catch (...) {  // a host allocation of the tables
+    fail(s, "host allocation failed");
   }
-  tq_status s = TQ_OK;
-  std::vector<float> r, S;
-  if (rotated) {
-    const int bits = code_bits(p.format);
-    int kind = p.codebook;
-    if (kind == TQ_CB_DEFAULT) kind = (p.format == TQ_FMT_TURBO4) ? TQ_CB_QUANTILE : TQ_CB_LLOYD;
-    double c64[16];
-    make_codebook_f64(bits, d, kind, c64);
-    c->cb.bits = bits;
-    c->cb.K = 1 << bits;
-    store_codebook(c64, c->cb.K, c->cb.c, c->cb.b);
-    c->f16 = make_f16_table(c->cb.c, c->cb.K);
-    c->bt = make_bucket_table(c->cb.b, c->cb.K - 1);
-    s = build_rotation(p.rotation, d, p.rot_seed, r, c->wht_neg);
-    if (s == TQ_OK && p.format == TQ_FMT_PROD3) {
-      S.resize((size_t)D * D);
-      tq_make_qjl_matrix(D, p.qjl_seed, S.data());
-    }
-  }
-  if (s == TQ_OK) s = device_tables(c, r, S);
   if (s != TQ_OK) {
     tq_ctx_destroy(c);
     return s;

@@ -211,12 +211,12 @@ static __device__ __forceinline__ void diff_finish(float (&a)[4], const float (&
   a[0] *= f * g.x, a[1] *= f * g.y, a[2] *= f * g.z, a[3] *= f * g.w;
 }
 
-// Equal shares of V virtual tiles over G CTAs: CTA c takes [floor(c V / G), floor((c + 1) V / G)).
-// floor(x * G / V) and the like: 32-bit when the product fits.
+// floor(x m / d), in 32 bits where the product fits.
 static __device__ __forceinline__ int mul_div(uint32_t x, uint32_t m, uint32_t d) {
   const uint64_t p = (uint64_t)x * m;
   return (p >> 32) ? (int)(p / d) : (int)((uint32_t)p / d);
 }
+// Equal shares of V virtual tiles over G CTAs: CTA c takes [floor(c V / G), floor((c + 1) V / G)).
 static __device__ __forceinline__ int share_start(int c, int V, int G) { return mul_div(c, V, G); }
 // The CTA whose share holds virtual tile v: the largest c with floor(c V / G) <= v.
 static __device__ __forceinline__ int share_of(int v, int V, int G) {

@@ -34,7 +34,7 @@
 //                     one CTA is finished there: differential pairs, norm, rounding.
 //   k_paged_join      units shared by CTAs: the log-sum-exp merge of their partials.
 //
-// Parts: for bf16 outputs q, K, V, P, O / l and R enter as one fp16 each (errors of 2^-12, random over
+// Parts: for bf16 outputs q, K, V, P, O / l and R enter as one fp16 each (off by 2^-11 at most, random over
 // 128 dims or the keys).  Together 6e-4 of the output's norm in rms at 300 keys and 8e-4 at 16,000
 // (1 to 4% of the rows beyond 1e-3, one in a thousand beyond 2e-3) next to bf16's own 1.7e-3; the largest
 // share is that of the scores, where a key's 16 values round alike.  For fp16 and fp32 outputs q, P

@@ -7,7 +7,7 @@
 // pairs (j, j + 64) and (j, j + 32) and adjacent pairs lie inside one thread's chunks;
 // pairs (j, j + 16) cross to the thread two over.  A CTA takes keys or values, so it keeps one
 // codebook grid.  The next row's elements and page id are in flight under a row's encode.  13.8K
-// tokens of 8 KV heads (bf16, keys turned): 43 us for 76 MB, 129 warp instructions a row; issue and
+// tokens of 8 KV heads (bf16, keys turned): 40 us for 79 MB, 129 warp instructions a row; issue and
 // latency at 16 warps an SM bind it (128 registers; 24 warps at 80 spilled and were slower).
 #include "tq_decode_common.cuh"
 #include "tq_paged.cuh"
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendPar
 // of |u| |row of R| each, 7.6e-6 together with the sums' rounding below the 1e-5 within which an
 // index may differ; three products (without lo lo) could reach 1.2e-5.  Lane (g, t) holds columns
 // 8 j + 2 t and the next of rows g and g + 8, one byte of nibbles of word j: the four lanes of a row
-// transpose their bytes and store words.  13.8K tokens of 8 KV heads, keys and values: 134 us, the
-// legacy matrix pipe 40% busy; a warp per row on the CUDA cores took 560 us.
+// transpose their bytes and store words.  13.8K tokens of 8 KV heads, keys and values: 112 us; a
+// warp per row on the CUDA cores took 560 us.
 constexpr int AD_WARPS = 16;
 struct DenseSmem {
   uint4 r[2][8][8][32];            // R, bf16 hi and lo
@@ -446,8 +446,9 @@ cudaError_t launch_rows(K kern, AppendParams p, int threads, int rows_per_cta, s
 
 cudaError_t launch_append(const AppendParams &p, bool dense, int dtype, int sms, cudaStream_t st) {
   if (dense) {
-    // Up to a 16-row tile per SM the tensor cores have too few rows to hide a tile's latency: 64 rows
-    // of each side take 10.3 us a warp per row and 14.0 us in tiles, 1500 rows about the same.
+    // Up to a 16-row tile per SM a warp takes a row.  Back to back, 64 rows of each side take 5.1 us so and
+    // 8.1 us in tiles, whose latency so few rows do not hide; 512 rows 8.8 and 8.4, 1,200 rows 10.4 and 9.2,
+    // 2,400 rows 13.3 and 9.5.
     if ((int64_t)p.pv.n_tokens * p.pv.Hkv <= 16 * sms)
       return launch_rows(k_paged_append_dense_few, p, AF_WARPS * 32, AF_WARPS, AF_SMEM, sms, st);
     if (dtype == TQ_DTYPE_F32)

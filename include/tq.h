@@ -378,6 +378,7 @@ tq_status tq_prefill_combine(const tq_ctx *k_ctx, const tq_ctx *v_ctx, int B, in
  *     TQ_ERR_UNSUPPORTED.
  *   - Every structure below is read during the call; the arrays it points to are device
  *     memory of the caller's, used in stream order.
+ *   - Device-side conditions of both sides are flagged in k_ctx's status word.
  *   - Calls may run at the same time on different streams as long as none of them writes
  *     what another reads (pages, outputs, workspaces).  A captured call reads the lengths,
  *     the block table and the rows when it is replayed; the sizes and addresses are those
@@ -492,7 +493,7 @@ tq_status tq_paged_gather(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_pag
  * (norms below 2^-48 lower, below 2^-67 with fewer bits): a row that sees only values 2^20 times
  * smaller than a neighbour's is off by up to 1e-10 of that neighbour's norm.
  * A key with a NaN norm, or a value whose norm is not finite (in chunks with a BF16 output: not
- * below 2^120), makes the rows that see it not finite, and no others. */
+ * below 2^120), makes the rows that see it not finite, and no others (an infinite key norm may). */
 tq_status tq_paged_workspace_size(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
                                   const tq_paged_batch *batch, int Hq, size_t *bytes);
 tq_status tq_paged_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,

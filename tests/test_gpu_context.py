@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("rot,step,most_ms", [("wht", 1, 1.2), ("dense", 1, 3.0), ("dense", 0, 1.2)])
 def test_a_context_is_made_in_about_a_millisecond(rot, step, most_ms):
-    """The fastest of 20: 0.2 ms under the WHT and with the dense matrix of a seed that was used before, 1.0 with a
+    """The fastest of 20: 0.05 ms under the WHT and with the dense matrix of a seed that was used before, 0.9 with a
     new one's factorisation; several times that is a step of their construction that went back to single
     elements on the host (2.4 and 6.5 ms)."""
     tq = lib()

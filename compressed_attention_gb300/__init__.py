@@ -67,6 +67,11 @@ class tq_diff(ctypes.Structure):
                 ("eps", ctypes.c_float), ("out_scale", ctypes.c_float)]
 
 
+class tq_probs(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("row_stride", ctypes.c_int64)]
+
+
 class tq_params(ctypes.Structure):
     _fields_ = [("d", ctypes.c_int32), ("format", ctypes.c_int32), ("codebook", ctypes.c_int32),
                 ("rotation", ctypes.c_int32), ("rot_seed", ctypes.c_uint64), ("qjl_seed", ctypes.c_uint64),
@@ -127,6 +132,11 @@ _SIGNATURES = {
     "tq_paged_gather": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp]),
     "tq_paged_workspace_size": (_i32, [_vp, _vp, _vp, _vp, _i32, ctypes.POINTER(_sz)]),
     "tq_paged_attention": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _f32, _vp, _i32, _vp, _sz, _vp]),
+    "tq_paged_tree_append": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "tq_paged_tree_workspace_size": (_i32, [_vp, _vp, _vp, _vp, _i32, ctypes.POINTER(_sz)]),
+    "tq_paged_tree_attention": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _f32, _vp, _i32, _vp, _sz, _vp]),
+    "tq_paged_tree_keep": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
+    "tq_tree_verify": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
     "tq_paged_diff_attention": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _f32, _vp, _i32, _vp, _sz, _vp]),
 }
 
@@ -704,6 +714,93 @@ def tq_paged_diff_attention(k_ctx, v_ctx, kv, batch, q, diff, out, workspace, ro
                                        rope.ref if rope else None, diff.ref, scale,
                                        _dense_out(out, batch.n_tokens, Hq // 2, "out"), _dtype_code(out),
                                        _ptr(workspace), _wsb(workspace), _stream(stream)), "tq_paged_diff_attention")
+
+
+# --------------------------------------------------------------------------- drafted trees
+
+def _words(t, n, what):
+    """Address of a packed int32 CUDA tensor of at least n elements."""
+    if t.dtype != _torch()[0].int32 or t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1) or not t.is_cuda:
+        raise ValueError(f"{what} must be a packed int32 CUDA tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _randoms(t, n, what):
+    if t.dtype != _torch()[0].float32 or t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1) or not t.is_cuda:
+        raise ValueError(f"{what} must be a packed float32 CUDA tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _path(t, batch):
+    """Address and row stride of a path tensor, int32 [B, max_q] at least."""
+    if t.dtype != _torch()[0].int32 or t.dim() != 2 or t.shape[0] < batch.B or t.shape[1] < batch.c.max_q \
+            or (t.shape[1] > 1 and t.stride(1) != 1) or not t.is_cuda:
+        raise ValueError(f"path must be an int32 CUDA tensor [{batch.B}, {batch.c.max_q}] with packed rows")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def _probs(t, n_tokens, what):
+    if t.dim() != 2 or t.shape[0] < n_tokens or (t.shape[1] > 1 and t.stride(1) != 1) or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor [n_tokens, vocab] with packed rows")
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return tq_probs(t.data_ptr(), _dtype_code(t), t.shape[1], stride)
+
+
+def tq_paged_tree_append(k_ctx, v_ctx, kv, batch, parents, k, v, rope=None, stream=None):
+    """tq_paged_append of the nodes of drafted trees (``parents`` int32 CUDA [n_tokens], -1 or an earlier
+    node of the row's sequence), the keys rotated by context + depth (``rope``)."""
+    _check_call(kv, batch, rope)
+    kr, vr = _rows(k, batch.n_tokens, kv.Hkv, "k"), _rows(v, batch.n_tokens, kv.Hkv, "v")
+    _check(lib.tq_paged_tree_append(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref,
+                                    _words(parents, batch.n_tokens, "parents"), ctypes.byref(kr), ctypes.byref(vr),
+                                    rope.ref if rope else None, _stream(stream)), "tq_paged_tree_append")
+
+
+def tq_paged_tree_workspace_size(k_ctx, v_ctx, kv, batch, Hq):
+    n = _sz(0)
+    _check(lib.tq_paged_tree_workspace_size(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref, Hq, ctypes.byref(n)),
+           "tq_paged_tree_workspace_size")
+    return n.value
+
+
+def tq_paged_tree_attention(k_ctx, v_ctx, kv, batch, parents, q, out, workspace, rope=None, scale=0.0, stream=None):
+    """Attention of the nodes q ([n_tokens, Hq, 128]) to their context, their ancestors and themselves."""
+    _check_call(kv, batch, rope)
+    Hq = q.shape[1]
+    qr = _rows(q, batch.n_tokens, Hq, "q")
+    _check(lib.tq_paged_tree_attention(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref,
+                                       _words(parents, batch.n_tokens, "parents"), ctypes.byref(qr), Hq,
+                                       rope.ref if rope else None, scale, _dense_out(out, batch.n_tokens, Hq, "out"),
+                                       _dtype_code(out), _ptr(workspace), _wsb(workspace), _stream(stream)),
+           "tq_paged_tree_attention")
+
+
+def tq_tree_verify(ctx, batch, parents, tokens, target, u_accept, u_next, path, n_path, next_token, draft=None,
+                   stream=None):
+    """Walk each sequence's tree by the random numbers u_accept [n_tokens] and u_next [B] against the rows
+    ``target`` [n_tokens, vocab] of probabilities, and ``draft`` (the rows that the children were drawn
+    from) or None; fills path [B, max_q] (nodes, then -1), n_path [B] and next_token [B]."""
+    if not batch.on_gpu:
+        raise ValueError("the batch must be CUDA tensors")
+    n, B = batch.n_tokens, batch.B
+    tp = _probs(target, n, "target")
+    dp = None if draft is None else _probs(draft, n, "draft")
+    pp, stride = _path(path, batch)
+    _check(lib.tq_tree_verify(ctx.handle, batch.ref, _words(parents, n, "parents"), _words(tokens, n, "tokens"),
+                              ctypes.byref(tp), None if dp is None else ctypes.byref(dp),
+                              _randoms(u_accept, n, "u_accept"), _randoms(u_next, B, "u_next"), pp, stride,
+                              _words(n_path, B, "n_path"), _words(next_token, B, "next_token"), _stream(stream)),
+           "tq_tree_verify")
+
+
+def tq_paged_tree_keep(k_ctx, v_ctx, kv, batch, path, n_path, new_lens, stream=None):
+    """Move the records of each sequence's path to the front of its nodes' slots, and set new_lens [B] (the
+    batch's own lengths may be given) to context + n_path."""
+    _check_call(kv, batch)
+    pp, stride = _path(path, batch)
+    _check(lib.tq_paged_tree_keep(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref, pp, stride,
+                                  _words(n_path, batch.B, "n_path"), _words(new_lens, batch.B, "new_lens"),
+                                  _stream(stream)), "tq_paged_tree_keep")
 
 
 def alloc_pages(n_pages, Hkv, page_size, device="cuda"):

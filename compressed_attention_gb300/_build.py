@@ -23,7 +23,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "lib", "libtq.so")
 
 SOURCES = ["tq_host.cu", "tq_api.cu", "tq_write.cu", "tq_decode.cu", "tq_dequant.cu", "tq_static_ws.cu", "tq_decode_pv.cu", "tq_write_tc.cu", "tq_prefill.cu", "tq_store.cu", "tq_d256.cu",
-           "tq_paged_api.cu", "tq_paged_rows.cu", "tq_paged_gather.cu", "tq_paged_attn.cu", "tq_paged_decode.cu", "tq_paged_prefill.cu"]
+           "tq_paged_api.cu", "tq_paged_rows.cu", "tq_paged_gather.cu", "tq_paged_attn.cu", "tq_paged_decode.cu", "tq_paged_prefill.cu",
+           "tq_paged_tree.cu", "tq_paged_keep.cu", "tq_tree_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

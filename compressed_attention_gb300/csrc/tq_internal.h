@@ -17,7 +17,8 @@ constexpr int PARTIAL256 = ACC256 + D256;
 
 // Device status codes (see tq_ctx_device_status in tq.h).
 enum DevErr : int32_t {
-  DEVERR_ROW_OOB = 1, DEVERR_SEQLEN = 2, DEVERR_TIMEOUT = 3, DEVERR_LAYOUT = 4, DEVERR_PAGE = 5, DEVERR_ROPE = 6
+  DEVERR_ROW_OOB = 1, DEVERR_SEQLEN = 2, DEVERR_TIMEOUT = 3, DEVERR_LAYOUT = 4, DEVERR_PAGE = 5, DEVERR_ROPE = 6,
+  DEVERR_TREE = 7
 };
 
 // Stored codebook: K fp32 centroids and K-1 fp32 decision boundaries.
@@ -299,7 +300,8 @@ struct PagedOut {
 };
 
 cudaError_t launch_paged_append(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, uint8_t *kp, uint8_t *vp,
-                                const RowsView &kr, const RowsView &vr, const RopeView &rope, cudaStream_t st);
+                                const RowsView &kr, const RowsView &vr, const RopeView &rope, const int32_t *parents,
+                                cudaStream_t st);  // parents: null, or the rows are nodes of trees
 cudaError_t launch_paged_gather(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,
                                 const uint8_t *vp, int unrotate, void *k_out, void *v_out, int out_dtype,
                                 cudaStream_t st);
@@ -318,5 +320,27 @@ bool paged_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes
 cudaError_t launch_paged_attention(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const uint8_t *kp,
                                    const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope, float scale,
                                    const PagedOut &o, void *ws, cudaStream_t st);
+
+// ---- drafted trees (tq_paged_tree.cu, tq_tree_verify.cu) ----
+constexpr int TREE_MAX = 128;  // nodes of a sequence
+bool paged_tree_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes);
+cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const int32_t *parents,
+                              const uint8_t *kp, const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope,
+                              float scale, const PagedOut &o, void *ws, cudaStream_t st);
+cudaError_t launch_paged_keep(const PagedView &pv, uint8_t *kp, uint8_t *vp, const int32_t *path, int64_t path_stride,
+                              const int32_t *n_path, int32_t *new_lens, cudaStream_t st);
+struct VerifyArgs {
+  const int32_t *cu_q;  // null: one row per sequence
+  int B, max_q, n_tokens;
+  const int32_t *parents, *tokens;
+  const void *target, *draft;  // draft: null without one
+  int dtype, vocab;
+  int64_t target_stride, draft_stride;
+  const float *u_accept, *u_next;
+  int32_t *path;
+  int64_t path_stride;
+  int32_t *n_path, *next_token, *status;
+};
+cudaError_t launch_tree_verify(const VerifyArgs &a, int num_sms, cudaStream_t st);
 
 }  // namespace tq

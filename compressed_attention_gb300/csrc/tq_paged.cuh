@@ -66,6 +66,23 @@ static __device__ __forceinline__ int paged_page(const PagedView &v, int b, int 
   return -1;
 }
 
+// The node that node i of a tree follows (row lo + i of `parents`), or -1; what is neither counts as -1.
+static __device__ __forceinline__ int tree_parent(const int32_t *parents, int lo, int i, int32_t *status, bool flag) {
+  const int p = parents[lo + i];
+  if (p >= -1 && p < i) return p;
+  if (flag) atomicExch(status, (int32_t)DEVERR_TREE);
+  return -1;
+}
+// Position of row tok of sequence b, a node of a tree, in slot `slot`: the context's length plus the
+// node's depth (a walk of at most as many steps as nodes lie before it).
+static __device__ __forceinline__ int tree_pos(const PagedView &v, const int32_t *parents, int b, int tok, int slot, bool flag) {
+  const int lo = v.cu_q ? v.cu_q[b] : b, i = tok - lo;
+  if (lo < 0 || i < 0) return slot;
+  int d = 0;
+  for (int n = i; (n = tree_parent(parents, lo, n, v.status, flag)) >= 0;) ++d;
+  return slot - i + d;
+}
+
 // Packed row of (page, KV head, row of the page).
 static __device__ __forceinline__ size_t paged_row(const PagedView &v, int page, int h, int i) {
   return ((((size_t)page * v.Hkv + h) << v.page_shift) + i) * PG_ROW;

@@ -95,13 +95,22 @@ tq_status check_heads(const tq_paged_kv *kv, int Hq) {
   return TQ_OK;
 }
 
+tq_status check_tree(const tq_paged_batch *bt, const int32_t *parents, bool empty) {
+  if (bt->max_q > TREE_MAX) return fail(TQ_ERR_UNSUPPORTED, "at most 128 nodes per sequence");
+  if (!parents && !empty) return fail(TQ_ERR_INVALID_ARG, "null parents");
+  if (!aligned(parents, 4)) return fail(TQ_ERR_ALIGNMENT, "parents must be 4-byte aligned");
+  return TQ_OK;
+}
+
 tq_status attention(const tq_ctx *k, const tq_ctx *v, const tq_paged_kv *kv, const tq_paged_batch *bt,
                     const tq_rows *q, int Hq, const tq_rope *rope, const DiffView &diff, float scale, void *out,
-                    int out_dtype, void *ws, size_t ws_bytes, tq_stream_t stream, const char *who) {
+                    int out_dtype, void *ws, size_t ws_bytes, tq_stream_t stream, const char *who,
+                    bool tree = false, const int32_t *parents = nullptr) {
   PagedView pv;
   bool empty;
   tq_status st = check_paged(k, v, kv, bt, who, &pv, &empty);
   if (st != TQ_OK || (st = check_heads(kv, Hq)) != TQ_OK) return st;
+  if (tree && (st = check_tree(bt, parents, empty)) != TQ_OK) return st;
   if (diff.lambda && (Hq / kv->Hkv) % 2) return fail(TQ_ERR_INVALID_ARG, "a head pair shares a KV head: Hq / Hkv must be even");
   if (!dtype_ok(out_dtype)) return fail(TQ_ERR_INVALID_ARG, "the output must be F32, BF16 or F16");
   if (!std::isfinite(scale)) return fail(TQ_ERR_INVALID_ARG, "scale must be finite");
@@ -112,7 +121,8 @@ tq_status attention(const tq_ctx *k, const tq_ctx *v, const tq_paged_kv *kv, con
   if (!out) return fail(TQ_ERR_INVALID_ARG, "null output");
   if (!aligned(out, 16)) return fail(TQ_ERR_ALIGNMENT, "the output must be 16-byte aligned");
   size_t need = 0;
-  if (!paged_workspace(k, pv, Hq, &need)) return fail(TQ_ERR_UNSUPPORTED, "the batch passes 32-bit work counts");
+  if (!(tree ? paged_tree_workspace(k, pv, Hq, &need) : paged_workspace(k, pv, Hq, &need)))
+    return fail(TQ_ERR_UNSUPPORTED, "the batch passes 32-bit work counts");
   if (!ws || ws_bytes < need) {
     set_error("workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
     return TQ_ERR_WORKSPACE;
@@ -120,9 +130,37 @@ tq_status attention(const tq_ctx *k, const tq_ctx *v, const tq_paged_kv *kv, con
   if (!aligned(ws, 256)) return fail(TQ_ERR_ALIGNMENT, "the workspace must be 256-byte aligned");
   if (scale == 0.f) scale = 1.0f / std::sqrt((float)D);
   const PagedOut o{out, out_dtype, diff};
-  cudaError_t e = launch_paged_attention(k, v, pv, (const uint8_t *)kv->k_pages, (const uint8_t *)kv->v_pages, qv, Hq,
-                                         rv, scale, o, ws, (cudaStream_t)stream);
+  const uint8_t *kp = (const uint8_t *)kv->k_pages, *vp = (const uint8_t *)kv->v_pages;
+  const cudaError_t e =
+      tree ? launch_paged_tree(k, v, pv, parents, kp, vp, qv, Hq, rv, scale, o, ws, (cudaStream_t)stream)
+           : launch_paged_attention(k, v, pv, kp, vp, qv, Hq, rv, scale, o, ws, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, who);
+  return TQ_OK;
+}
+
+tq_status append(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv, const tq_paged_batch *batch,
+                 const tq_rows *k, const tq_rows *v, const tq_rope *rope, tq_stream_t stream, const char *who,
+                 bool tree = false, const int32_t *parents = nullptr) {
+  PagedView pv;
+  bool empty;
+  tq_status st = check_paged(k_ctx, v_ctx, kv, batch, who, &pv, &empty);
+  if (st != TQ_OK || (tree && (st = check_tree(batch, parents, empty)) != TQ_OK)) return st;
+  RopeView rv;
+  if ((st = check_rope(rope, &rv)) != TQ_OK || empty) return st;
+  RowsView kr, vr;
+  if ((st = check_rows(k, kv->Hkv, &kr)) != TQ_OK || (st = check_rows(v, kv->Hkv, &vr)) != TQ_OK) return st;
+  if (kr.dtype != vr.dtype) return fail(TQ_ERR_INVALID_ARG, "k and v must have one dtype");
+  const cudaError_t e = launch_paged_append(k_ctx, v_ctx, pv, (uint8_t *)kv->k_pages, (uint8_t *)kv->v_pages, kr, vr,
+                                            rv, parents, (cudaStream_t)stream);
+  return e == cudaSuccess ? TQ_OK : cuda_fail(e, who);
+}
+
+tq_status check_probs(const tq_probs *p) {
+  if (!p || !p->data) return fail(TQ_ERR_INVALID_ARG, "null probabilities");
+  if (!dtype_ok(p->dtype)) return fail(TQ_ERR_INVALID_ARG, "probabilities must be F32, BF16 or F16");
+  if (p->vocab < 1) return fail(TQ_ERR_INVALID_ARG, "vocab must be >= 1");
+  if (p->row_stride < p->vocab || p->row_stride > INT64_MAX / 8 / INT32_MAX) return fail(TQ_ERR_INVALID_ARG, "bad row stride of the probabilities");
+  if (!aligned(p->data, p->dtype == TQ_DTYPE_F32 ? 4 : 2)) return fail(TQ_ERR_ALIGNMENT, "probabilities must be aligned to their elements");
   return TQ_OK;
 }
 
@@ -158,19 +196,7 @@ tq_status tq_make_rope_table(int rot_dim, double base, int64_t n_pos, float *cos
 tq_status tq_paged_append(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
                           const tq_paged_batch *batch, const tq_rows *k, const tq_rows *v,
                           const tq_rope *rope, tq_stream_t stream) {
-  return guarded([&] {
-    PagedView pv;
-    bool empty;
-    tq_status st = check_paged(k_ctx, v_ctx, kv, batch, "tq_paged_append", &pv, &empty);
-    RopeView rv;
-    if (st != TQ_OK || (st = check_rope(rope, &rv)) != TQ_OK || empty) return st;
-    RowsView kr, vr;
-    if ((st = check_rows(k, kv->Hkv, &kr)) != TQ_OK || (st = check_rows(v, kv->Hkv, &vr)) != TQ_OK) return st;
-    if (kr.dtype != vr.dtype) return fail(TQ_ERR_INVALID_ARG, "k and v must have one dtype");
-    const cudaError_t e = launch_paged_append(k_ctx, v_ctx, pv, (uint8_t *)kv->k_pages, (uint8_t *)kv->v_pages, kr, vr,
-                                              rv, (cudaStream_t)stream);
-    return e == cudaSuccess ? TQ_OK : cuda_fail(e, "tq_paged_append");
-  });
+  return guarded([&] { return append(k_ctx, v_ctx, kv, batch, k, v, rope, stream, "tq_paged_append"); });
 }
 
 tq_status tq_paged_gather(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
@@ -230,6 +256,95 @@ tq_status tq_paged_diff_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, cons
     const DiffView dv{diff->lambda_w, diff->lambda_stride, diff->gain, diff->eps, diff->out_scale};
     return attention(k_ctx, v_ctx, kv, batch, q, Hq, rope, dv, scale, out, out_dtype, workspace, workspace_bytes,
                      stream, "tq_paged_diff_attention");
+  });
+}
+
+tq_status tq_paged_tree_append(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                               const tq_paged_batch *batch, const int32_t *parents, const tq_rows *k,
+                               const tq_rows *v, const tq_rope *rope, tq_stream_t stream) {
+  return guarded([&] { return append(k_ctx, v_ctx, kv, batch, k, v, rope, stream, "tq_paged_tree_append", true, parents); });
+}
+
+tq_status tq_paged_tree_workspace_size(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                                       const tq_paged_batch *batch, int Hq, size_t *bytes) {
+  if (!bytes) return fail(TQ_ERR_INVALID_ARG, "null output");
+  return guarded([&] {
+    PagedView pv;
+    bool empty;
+    tq_status st = check_paged(k_ctx, v_ctx, kv, batch, "tq_paged_tree_workspace_size", &pv, &empty);
+    if (st != TQ_OK || (st = check_heads(kv, Hq)) != TQ_OK) return st;
+    if (batch->max_q > TREE_MAX) return fail(TQ_ERR_UNSUPPORTED, "at most 128 nodes per sequence");
+    size_t n = 256;
+    if (!empty && !paged_tree_workspace(k_ctx, pv, Hq, &n)) return fail(TQ_ERR_UNSUPPORTED, "the batch passes 32-bit work counts");
+    *bytes = n;
+    return TQ_OK;
+  });
+}
+
+tq_status tq_paged_tree_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                                  const tq_paged_batch *batch, const int32_t *parents, const tq_rows *q, int Hq,
+                                  const tq_rope *rope, float scale, void *out, int out_dtype, void *workspace,
+                                  size_t workspace_bytes, tq_stream_t stream) {
+  return guarded([&] {
+    return attention(k_ctx, v_ctx, kv, batch, q, Hq, rope, DiffView{}, scale, out, out_dtype, workspace,
+                     workspace_bytes, stream, "tq_paged_tree_attention", true, parents);
+  });
+}
+
+tq_status tq_tree_verify(const tq_ctx *ctx, const tq_paged_batch *batch, const int32_t *parents,
+                         const int32_t *tokens, const tq_probs *target, const tq_probs *draft,
+                         const float *u_accept, const float *u_next, int32_t *path, int64_t path_stride,
+                         int32_t *n_path, int32_t *next_token, tq_stream_t stream) {
+  return guarded([&] {
+    if (!ctx) return fail(TQ_ERR_INVALID_ARG, "null context");
+    if (!batch) return fail(TQ_ERR_INVALID_ARG, "null batch");
+    tq_status st = check_current_device(ctx->device, "tq_tree_verify");
+    if (st != TQ_OK) return st;
+    if (batch->B < 0 || batch->n_tokens < 0) return fail(TQ_ERR_INVALID_ARG, "B and n_tokens must be >= 0");
+    if (batch->max_q < 1) return fail(TQ_ERR_INVALID_ARG, "max_q must be >= 1");
+    if (batch->max_q > TREE_MAX) return fail(TQ_ERR_UNSUPPORTED, "at most 128 nodes per sequence");
+    if (!batch->cu_q && (batch->n_tokens != batch->B || batch->max_q != 1))
+      return fail(TQ_ERR_INVALID_ARG, "without cu_q every sequence has one row: n_tokens == B and max_q == 1");
+    if (path_stride < batch->max_q || path_stride > INT64_MAX / 8 / INT32_MAX) return fail(TQ_ERR_INVALID_ARG, "path_stride below max_q");
+    if (batch->B > INT32_MAX / 64) return fail(TQ_ERR_UNSUPPORTED, "too many sequences");
+    if ((st = check_probs(target)) != TQ_OK || (draft && (st = check_probs(draft)) != TQ_OK)) return st;
+    if (draft && (draft->dtype != target->dtype || draft->vocab != target->vocab))
+      return fail(TQ_ERR_INVALID_ARG, "the draft's rows must have the target's dtype and vocab");
+    if (batch->B == 0) return TQ_OK;
+    if (!parents || !tokens || !u_accept || !u_next) return fail(TQ_ERR_INVALID_ARG, "null parents, tokens or random numbers");
+    if (!path || !n_path || !next_token) return fail(TQ_ERR_INVALID_ARG, "null output");
+    if (!aligned(parents, 4) || !aligned(tokens, 4) || !aligned(u_accept, 4) || !aligned(u_next, 4) || !aligned(path, 4) ||
+        !aligned(n_path, 4) || !aligned(next_token, 4) || !aligned(batch->cu_q, 4))
+      return fail(TQ_ERR_ALIGNMENT, "arrays must be 4-byte aligned");
+    VerifyArgs a{};
+    a.cu_q = batch->cu_q, a.B = batch->B, a.max_q = batch->max_q, a.n_tokens = batch->n_tokens;
+    a.parents = parents, a.tokens = tokens;
+    a.target = target->data, a.target_stride = target->row_stride, a.dtype = target->dtype, a.vocab = target->vocab;
+    if (draft) a.draft = draft->data, a.draft_stride = draft->row_stride;
+    a.u_accept = u_accept, a.u_next = u_next;
+    a.path = path, a.path_stride = path_stride, a.n_path = n_path, a.next_token = next_token, a.status = ctx->d_status;
+    const cudaError_t e = launch_tree_verify(a, ctx->num_sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e, "tq_tree_verify");
+  });
+}
+
+tq_status tq_paged_tree_keep(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                             const tq_paged_batch *batch, const int32_t *path, int64_t path_stride,
+                             const int32_t *n_path, int32_t *new_lens, tq_stream_t stream) {
+  return guarded([&] {
+    PagedView pv;
+    bool empty;
+    tq_status st = check_paged(k_ctx, v_ctx, kv, batch, "tq_paged_tree_keep", &pv, &empty);
+    if (st != TQ_OK) return st;
+    if (batch->max_q > TREE_MAX) return fail(TQ_ERR_UNSUPPORTED, "at most 128 nodes per sequence");
+    if (path_stride < 1 || path_stride > INT64_MAX / 8 / INT32_MAX) return fail(TQ_ERR_INVALID_ARG, "path_stride must be >= 1");
+    if (batch->B == 0) return TQ_OK;
+    if (empty) return fail(TQ_ERR_INVALID_ARG, "a batch without rows has no path to keep");
+    if (!path || !n_path || !new_lens) return fail(TQ_ERR_INVALID_ARG, "null path, counts or new lengths");
+    if (!aligned(path, 4) || !aligned(n_path, 4) || !aligned(new_lens, 4)) return fail(TQ_ERR_ALIGNMENT, "path, counts and new lengths must be 4-byte aligned");
+    const cudaError_t e = launch_paged_keep(pv, (uint8_t *)kv->k_pages, (uint8_t *)kv->v_pages, path, path_stride, n_path,
+                                            new_lens, (cudaStream_t)stream);
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e, "tq_paged_tree_keep");
   });
 }
 

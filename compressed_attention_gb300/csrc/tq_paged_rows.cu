@@ -31,6 +31,7 @@ struct AppendSide {
 struct AppendParams {
   PagedView pv;
   RopeView rope;
+  const int32_t *parents;  // TREE: the rows are nodes of trees
   AppendSide side[2];  // keys, values
   int only;            // 0 or 1: that side; 2: both
   int k_ctas;          // the first CTAs take the keys, the others the values
@@ -95,23 +96,26 @@ __device__ __forceinline__ void rope_quarter(float (&x)[WT_E], int q, const Rope
   }
 }
 
-// Where a batch row goes; row < 0: nowhere.
+// Where a batch row goes.
 struct Place {
   int64_t at;  // byte of the packed row, or -1
-  int pos;
+  int pos;     // the position it is turned by
 };
-__device__ __forceinline__ Place place_row(const PagedView &v, int tok, int h, bool flag) {
+template <bool TREE>
+__device__ __forceinline__ Place place_row(const PagedView &v, const int32_t *parents, int tok, int h, bool flag) {
   const int b = paged_seq(v, tok);
   const int n = paged_len(v, b, flag);
   Place pl{-1, paged_pos(v, b, tok, n)};
   if (pl.pos >= 0 && pl.pos < n) {
     const int pg = paged_page(v, b, pl.pos, flag);
     if (pg >= 0) pl.at = (int64_t)paged_row(v, pg, h, pl.pos & ((1 << v.page_shift) - 1));
+    if (TREE) pl.pos = tree_pos(v, parents, b, tok, pl.pos, flag);
   }
   return pl;
 }
 
-template <int SRC>
+// TREE: a row's rotation is by its node's position, not by its slot's.
+template <int SRC, bool TREE>
 __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendParams p) {
   __shared__ WhtTables tb;
   const int side = (int)blockIdx.x < p.k_ctas ? 0 : 1;
@@ -139,7 +143,7 @@ __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendPar
   const bool turn = side == 0 && p.rope.rot_dim != 0;
   Quarter<SRC> raw;
   // the next row: its page as in the table (loaded, and looked at when its turn comes), head and position
-  int nx_page = -1, nx_head = 0, nx_pos = -1;
+  int nx_page = -1, nx_head = 0, nx_pos = -1, nx_turn = 0;
   auto fetch = [&](int i) {
     nx_pos = -1;
     if (i < n_iter && i * 8 + sub < n_rows) {
@@ -156,6 +160,7 @@ __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendPar
       if (pos >= 0 && pos < len) {
         nx_page = p.pv.table[(int64_t)b * p.pv.table_stride + (pos >> p.pv.page_shift)];
         nx_pos = pos, nx_head = head;
+        if (TREE && turn) nx_turn = tree_pos(p.pv, p.parents, b, tok, pos, q == 0);
       }
       tok += d_tok, head += d_head;
       if (head >= Hkv) head -= Hkv, ++tok;
@@ -163,7 +168,7 @@ __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendPar
   };
   fetch(it);
   for (; it < n_iter; it += step) {
-    Place at{-1, nx_pos};
+    Place at{-1, TREE ? nx_turn : nx_pos};
     if (nx_pos >= 0) {
       if ((unsigned)nx_page < (unsigned)p.pv.n_pages)
         at.at = (int64_t)paged_row(p.pv, nx_page, nx_head, nx_pos & ((1 << p.pv.page_shift) - 1));
@@ -217,7 +222,7 @@ __device__ __forceinline__ uint32_t transpose_bytes(uint32_t v, int t) {
   return prmt(v, w, (t & 1) ? 0x3715u : 0x6240u);
 }
 
-template <int DT>
+template <int DT, bool TREE>
 __global__ void __launch_bounds__(AD_WARPS * 32) k_paged_append_dense(const AppendParams p) {
   extern __shared__ __align__(128) uint8_t smem_dense[];
   DenseSmem &sm = *reinterpret_cast<DenseSmem *>(smem_dense);
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32) k_paged_append_dense(const Appe
     const int64_t r = tile * 16 + lane;
     if (lane < 16 && r < n_rows) {
       const int tok = (int)((uint32_t)r / (uint32_t)Hkv), h = (int)(r - (int64_t)tok * Hkv);
-      const Place pl = place_row(p.pv, tok, h, true);
+      const Place pl = place_row<TREE>(p.pv, p.parents, tok, h, true);
       sp.at = pl.at, sp.pos = pl.pos;
       if (pl.at >= 0) sp.src = (uint64_t)(uintptr_t)(sd.src.data + tok * sd.src.token_bytes + h * sd.src.head_bytes);
     }
@@ -373,6 +378,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32) k_paged_append_dense(const Appe
 // Dense rotation, few rows: a warp per row on the CUDA cores, R^T staged once per CTA.
 constexpr int AF_WARPS = 8;
 constexpr size_t AF_SMEM = (size_t)D * D * 4 + AF_WARPS * D * 4;
+template <bool TREE>
 __global__ void __launch_bounds__(AF_WARPS * 32) k_paged_append_dense_few(const AppendParams p) {
   extern __shared__ __align__(16) float asm_f[];
   float *rt = asm_f, *uv = asm_f + D * D;
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(AF_WARPS * 32) k_paged_append_dense_few(const 
   const int64_t n_rows = (int64_t)paged_rows(p.pv) * p.pv.Hkv;
   for (int64_t row = (int64_t)cta * AF_WARPS + warp; row < n_rows; row += (int64_t)n_cta * AF_WARPS) {
     const int tok = (int)(row / p.pv.Hkv), h = (int)(row - (int64_t)tok * p.pv.Hkv);
-    const Place at = place_row(p.pv, tok, h, lane == 0);
+    const Place at = place_row<TREE>(p.pv, p.parents, tok, h, lane == 0);
     if (at.at < 0) continue;
     float x[4];
     load_lane4(sd.src.data + tok * sd.src.token_bytes + h * sd.src.head_bytes, sd.src.dtype, lane, x);
@@ -444,32 +450,35 @@ cudaError_t launch_rows(K kern, AppendParams p, int threads, int rows_per_cta, s
   return launch_pdl(kern, dim3(grid), dim3(threads), smem, st, p);
 }
 
+template <bool TREE>
 cudaError_t launch_append(const AppendParams &p, bool dense, int dtype, int sms, cudaStream_t st) {
   if (dense) {
     // Up to a 16-row tile per SM a warp takes a row.  Back to back, 64 rows of each side take 5.1 us so and
     // 8.1 us in tiles, whose latency so few rows do not hide; 512 rows 8.8 and 8.4, 1,200 rows 10.4 and 9.2,
     // 2,400 rows 13.3 and 9.5.
     if ((int64_t)p.pv.n_tokens * p.pv.Hkv <= 16 * sms)
-      return launch_rows(k_paged_append_dense_few, p, AF_WARPS * 32, AF_WARPS, AF_SMEM, sms, st);
+      return launch_rows(k_paged_append_dense_few<TREE>, p, AF_WARPS * 32, AF_WARPS, AF_SMEM, sms, st);
     if (dtype == TQ_DTYPE_F32)
-      return launch_rows(k_paged_append_dense<TQ_DTYPE_F32>, p, AD_WARPS * 32, 16, sizeof(DenseSmem), sms, st);
+      return launch_rows(k_paged_append_dense<TQ_DTYPE_F32, TREE>, p, AD_WARPS * 32, 16, sizeof(DenseSmem), sms, st);
     if (dtype == TQ_DTYPE_BF16)
-      return launch_rows(k_paged_append_dense<TQ_DTYPE_BF16>, p, AD_WARPS * 32, 16, sizeof(DenseSmem), sms, st);
-    return launch_rows(k_paged_append_dense<TQ_DTYPE_F16>, p, AD_WARPS * 32, 16, sizeof(DenseSmem), sms, st);
+      return launch_rows(k_paged_append_dense<TQ_DTYPE_BF16, TREE>, p, AD_WARPS * 32, 16, sizeof(DenseSmem), sms, st);
+    return launch_rows(k_paged_append_dense<TQ_DTYPE_F16, TREE>, p, AD_WARPS * 32, 16, sizeof(DenseSmem), sms, st);
   }
   constexpr int per = 8 * (WT_THREADS / 32);
-  if (dtype == TQ_DTYPE_F32) return launch_rows(k_paged_append_wht<TQ_DTYPE_F32>, p, WT_THREADS, per, 0, sms, st);
-  if (dtype == TQ_DTYPE_BF16) return launch_rows(k_paged_append_wht<TQ_DTYPE_BF16>, p, WT_THREADS, per, 0, sms, st);
-  return launch_rows(k_paged_append_wht<TQ_DTYPE_F16>, p, WT_THREADS, per, 0, sms, st);
+  if (dtype == TQ_DTYPE_F32) return launch_rows(k_paged_append_wht<TQ_DTYPE_F32, TREE>, p, WT_THREADS, per, 0, sms, st);
+  if (dtype == TQ_DTYPE_BF16) return launch_rows(k_paged_append_wht<TQ_DTYPE_BF16, TREE>, p, WT_THREADS, per, 0, sms, st);
+  return launch_rows(k_paged_append_wht<TQ_DTYPE_F16, TREE>, p, WT_THREADS, per, 0, sms, st);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, uint8_t *kp, uint8_t *vp,
-                                const RowsView &kr, const RowsView &vr, const RopeView &rope, cudaStream_t st) {
+                                const RowsView &kr, const RowsView &vr, const RopeView &rope, const int32_t *parents,
+                                cudaStream_t st) {
   AppendParams p{};
   p.pv = pv;
   p.rope = rope;
+  p.parents = parents;
   const tq_ctx *ctx[2] = {k, v};
   const RowsView *rows[2] = {&kr, &vr};
   for (int i = 0; i < 2; ++i) {
@@ -482,13 +491,14 @@ cudaError_t launch_paged_append(const tq_ctx *k, const tq_ctx *v, const PagedVie
     s.rfrag = ctx[i]->d_rfrag;
     s.pit = ctx[i]->d_pit;
   }
+  const auto launch = parents && rope.rot_dim ? launch_append<true> : launch_append<false>;
   const bool dk = k->p.rotation == TQ_ROT_DENSE, dv = v->p.rotation == TQ_ROT_DENSE;
   if (dk == dv) {
     p.only = 2;
-    return launch_append(p, dk, kr.dtype, k->num_sms, st);
+    return launch(p, dk, kr.dtype, k->num_sms, st);
   }
   for (p.only = 0; p.only < 2; ++p.only) {  // one rotation kind each: one launch per side
-    const cudaError_t e = launch_append(p, p.only ? dv : dk, kr.dtype, k->num_sms, st);
+    const cudaError_t e = launch(p, p.only ? dv : dk, kr.dtype, k->num_sms, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -176,7 +176,8 @@ tq_status tq_ctx_destroy(tq_ctx *ctx);
  * 2 = sequence length outside [1, L] (clamped); 3 = a bounded wait ran out;
  * 4 = the decode kernel found shared memory laid out unlike the device reported
  * (no output was computed); 5 = a block table's page id outside [0, n_pages); 6 = a
- * position past the end of the rotation table. */
+ * position past the end of the rotation table; 7 = a drafted tree's parent, token or path out
+ * of order. */
 tq_status tq_ctx_device_status(const tq_ctx *ctx, int32_t *status, int clear);
 
 /* Write path / SET_ROWS ([turbo4 post-mortem] sections 1, 2): quantize n_rows
@@ -523,6 +524,90 @@ tq_status tq_paged_diff_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, cons
                                   const tq_paged_batch *batch, const tq_rows *q, int Hq, const tq_rope *rope,
                                   const tq_diff *diff, float scale, void *out, int out_dtype,
                                   void *workspace, size_t workspace_bytes, tq_stream_t stream);
+
+/* ------------------------------------------------------------- drafted trees */
+
+/* Speculative decoding over the paged cache.  A step drafts a tree of tokens per sequence, runs the
+ * model on all of them at once, keeps the path that the target's probabilities accept and goes on
+ * from the token drawn behind it: tq_paged_tree_append and tq_paged_tree_attention in every layer,
+ * then tq_tree_verify, then tq_paged_tree_keep in every layer.
+ *   The batch's rows are the nodes: sequence b's rows cu_q[b] .. cu_q[b+1] - 1 are its nodes 0, 1, ... T - 1
+ * (T <= 128: max_q above it is TQ_ERR_UNSUPPORTED), and lie in the cache's slots c .. c + T - 1 behind the
+ * context of c = seq_lens[b] - T tokens.  parents[i] of row i is the node that node i follows, an
+ * earlier node of the same sequence, or -1: the node follows the context.  Node i's position is
+ * c + depth(i), the number of its ancestors above the context (siblings share a position, not a slot).
+ *   A parent that is neither -1 nor an earlier node counts as -1 (flagged, status 7).  The calls
+ * follow the paged calls' rules on padded batches, idle slots, lengths, pages, streams and capture. */
+
+/* tq_paged_append with k rotated by the nodes' positions: row i goes to slot c + i. */
+tq_status tq_paged_tree_append(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                               const tq_paged_batch *batch, const int32_t *parents, const tq_rows *k,
+                               const tq_rows *v, const tq_rope *rope, tq_stream_t stream);
+
+/* Attention of the nodes over their sequences' pages (which hold the nodes' own keys and values):
+ * node i sees the c keys of the context, its ancestors and itself,
+ *   out[i,h] = sum_{t in C(i)} softmax_t(scale * <q'[i,h], K_hat[b,kv,t]>) V_hat[b,kv,t],
+ * q' = q rotated by the node's position.  Arguments as tq_paged_attention, parents device
+ * int32 [n_tokens]; the workspace of tq_paged_tree_workspace_size() bytes for the same batch sizes.
+ * A node that has no slot (a sequence shorter than its nodes) gets zeros and is seen by none.
+ * Accuracy, and NaN or infinite norms: as tq_paged_attention's (F16 and F32 outputs: q and the
+ * probabilities as two fp16 parts; BF16 outputs: as one). */
+tq_status tq_paged_tree_workspace_size(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                                       const tq_paged_batch *batch, int Hq, size_t *bytes);
+tq_status tq_paged_tree_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                                  const tq_paged_batch *batch, const int32_t *parents, const tq_rows *q, int Hq,
+                                  const tq_rope *rope, float scale, void *out, int out_dtype, void *workspace,
+                                  size_t workspace_bytes, tq_stream_t stream);
+
+/* Rows of probabilities over the vocabulary, one per row of a batch: element w of row i is
+ * data[i * row_stride + w], F32, BF16 or F16, in [0, 1] (what is not counts as 0 or 1, NaN as 0). */
+typedef struct tq_probs {
+  const void *data;    /* device, aligned to its element */
+  int32_t dtype;
+  int32_t vocab;       /* >= 1 */
+  int64_t row_stride;  /* >= vocab */
+} tq_probs;
+
+/* Verification of drafted tokens from given random numbers.  Sequence b's walk starts on its node
+ * 0 (the token chosen last, taken as it is).  On node v, with p and q the target's and the draft's row of
+ * v (what follows v), weights r = p and Z = 1, the children c of v in order, x = tokens[c]:
+ *   with a draft     c is taken when u_accept[c] q(x) Z < r(x); else r <- max(r - Z q, 0), Z <- sum r
+ *                    (left as they were when that sum is 0).  The children drawn independently from q.
+ *   without one      c is taken when u_accept[c] Z < r(x); else Z <- Z - r(x), r(x) <- 0.  Any
+ *                    children, the draft's likeliest tokens say: a token twice is taken once.
+ * The walk goes on from the child taken; where none is, next_token[b] is the smallest w with
+ * r(0) + ... + r(w) > u_next[b] (r(0) + ... + r(vocab - 1)), and -1 where r has no weight.  So the
+ * tokens of the path and next_token are distributed as the target's (rows that sum to 1).
+ *   Weights and sums are whole multiples of 2^-62, so the outcome depends neither on the order of the
+ * sums nor on the launch; rows that sum to 2 or more have no stated outcome (a token of the vocabulary, or -1).
+ *   ctx         gives the device and the status word (any context).
+ *   batch       cu_q, B, max_q and n_tokens; the lengths are not read and may be NULL.
+ *   tokens      device int32 [n_tokens]; node 0's is not read.  One outside the vocabulary is never
+ *               taken (flagged, status 7).
+ *   draft       NULL, or rows of the target's dtype and vocab.
+ *   u_accept    device fp32 [n_tokens] in [0, 1) (node 0's is not read), u_next device fp32 [B]; what lies
+ *               outside counts as 0 or as the largest number below 1, NaN as 0.
+ *   path        device int32, the nodes of sequence b's path at path[b * path_stride], ascending, -1
+ *               behind them up to max_q; path_stride >= max_q.
+ *   n_path      device int32 [B]: nodes of the path, node 0 included; 0 (and next_token -1) for a
+ *               sequence without rows.  Nodes past max_q are left out (flagged, status 2). */
+tq_status tq_tree_verify(const tq_ctx *ctx, const tq_paged_batch *batch, const int32_t *parents,
+                         const int32_t *tokens, const tq_probs *target, const tq_probs *draft,
+                         const float *u_accept, const float *u_next, int32_t *path, int64_t path_stride,
+                         int32_t *n_path, int32_t *next_token, tq_stream_t stream);
+
+/* Keep a path of the nodes in the cache: slot c + j takes the record of slot c + path[j], keys and values
+ * of every KV head, for j < n_path[b], and new_lens[b] = c + n_path[b] (0 at least; the length itself for a
+ * sequence without rows).  Slots behind the path keep their bytes.
+ *   path, path_stride, n_path   as tq_tree_verify writes them: ascending nodes.  A path that is not, or
+ *               that names a node past the sequence's, is not taken (flagged, status 7): nothing is
+ *               moved and new_lens[b] = c.
+ *   new_lens    device int32 [B]; may be batch->seq_lens itself.
+ * The batch has a row at least (or B = 0: nothing is done).  A row whose page id is out of range is
+ * not moved (status 5).  Sequences must not share the pages of their nodes. */
+tq_status tq_paged_tree_keep(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                             const tq_paged_batch *batch, const int32_t *path, int64_t path_stride,
+                             const int32_t *n_path, int32_t *new_lens, tq_stream_t stream);
 
 /* ---------------------------------------------------------- capture + store */
 

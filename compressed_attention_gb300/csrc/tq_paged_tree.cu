@@ -1,101 +1,1004 @@
-// Attention of drafted trees over the paged cache.
+// Attention of drafted trees over the paged cache on the 5th-generation tensor cores, in three
+// launches.
 //
-// A CTA per (node, KV head): the node's heads one after the other over the keys that it sees, 128 at a
-// time: a thread per key for the scores, a thread per dimension for the values.
+// A unit is a sequence's KV head with as many of its nodes as fit R columns (a column is a node's q-head).
+// Few columns against long contexts: so the products are laid with the keys in the rows,
+//   S^T [128 keys x R] = K_hat Q^T,   O^T [128 dims x N] += V_hat^T P^T,
+// and the time of a tile goes with its 128 keys and its columns, where rows of 128 queries (the chunk kernel's
+// form) would compute 128 exponentials a key whatever the tree holds.  A softmax thread is a key: its norms are two
+// scalars, and the sums of weights stay in its registers until the item's end.
+//
+//   k_tree_prep     each warp turns 16 columns of q by their nodes' positions (fp32), by R (bf16 parts,
+//                   m16n8k16), and rounds them to fp16 parts in images of the units' operand tiles; other
+//                   warps write which columns see each of the nodes' keys.
+//   k_tree_partial  persistent, one CTA per SM; the key tiles of all units lie end to end (each unit after a few
+//                   empty tiles that stand for its start) and are shared out evenly, as in the paged decode.
+//                   Specialised warps:
+//                     loader      packed tiles, one bulk copy per page and side, on rings; q's images
+//                     K decoders  nibbles -> fp16 centroids (byte permutes) in tensor memory, a key per lane:
+//                                 the A operand of S^T, without a trip through shared memory
+//                     V decoders  the same into 128-byte swizzled tiles, the MN-major A operand of O^T
+//                     issuer      one thread
+//                     softmax     two groups of four warps, each half of the columns: S^T from tensor
+//                                 memory, weights against the columns' running maxima, P as the MN-major
+//                                 B operand in shared memory.  A maximum is raised (and O rescaled)
+//                                 only when a weight would leave the operand's range: one vote a tile.
+//   k_tree_combine  the log-sum-exp merge of a column's shares, R^T o on the tensor cores, rounding.
+//
+// Parts: for bf16 outputs q and P enter as one fp16 each; for fp16 and fp32 outputs as hi + lo, the lo parts as
+// more columns.  K and V are centroids of the fp16 table with fp32 norms outside the products.
 #include <math.h>
 
 #include "tq_decode_common.cuh"
 #include "tq_paged.cuh"
+#include "tq_rotmma.cuh"
+#include "tq_tc.cuh"
 
 namespace tq {
 
 namespace {
 
-struct SimpleParams {
+constexpr int KT = 128;          // keys per tile
+constexpr int ITEM_TILES = 3;    // cost of an item ahead of its tiles, in tiles
+constexpr int RAW = KT * PG_ROW; // a packed tile
+constexpr int PROW = D + 4;      // floats of a partial: acc[128], max (less W_SHIFT), sum, 2 spare
+constexpr int W_KDEC = 8, W_VDEC = 12, W_MMA = 16, W_LOAD = 17, W_Q = 18, THREADS = 640;
+constexpr int REGS_LAUNCH = 96;
+
+// R columns of a unit, PARTS fp16 parts of q and P.
+template <int R_, int PARTS_>
+struct Cfg {
+  static constexpr int R = R_, PARTS = PARTS_;
+  static constexpr int N = R * PARTS < 64 ? 64 : R * PARTS;  // columns of P and O (whole 128-byte rows)
+  static constexpr int C = R / 2;                            // columns of a softmax group
+  static constexpr int CH = C < 32 ? C : 32;                 // at a time
+  static constexpr int NRAW = R * PARTS == 128 ? 3 : 4;
+  static constexpr uint32_t TM_S = 0, TM_O = 2 * R, TM_K = TM_O + N;
+  static_assert(TM_K + 2 * 64 <= 512, "tensor memory");
+  static constexpr uint32_t Q_HALF = R * PARTS * 128, Q_BYTES = 2 * Q_HALF, P_BYTES = (N / 64) * SW_HALF_BYTES;
+  static constexpr uint32_t OFF_V = 0, OFF_P = 2 * SW_TILE_BYTES, OFF_Q = OFF_P + 2 * P_BYTES;
+  static constexpr uint32_t OFF_RAW = OFF_Q + Q_BYTES, OFF_MISC = OFF_RAW + 2 * NRAW * RAW;
+  static constexpr uint32_t IDESC_S = (1u << 4) | (uint32_t(R >> 3) << 17) | ((128u >> 4) << 24);
+  static constexpr uint32_t IDESC_PV = (1u << 4) | (1u << 15) | (1u << 16) | (uint32_t(N >> 3) << 17) | ((128u >> 4) << 24);
+  // Registers: the softmax groups hold a sum per column and 32 scores.
+  static constexpr int REGS_SOFTMAX = R == 128 ? 144 : 128, REGS_OTHER = R == 128 ? 64 : 72;
+  static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "the launch's registers");
+};
+
+struct TreeView {
   PagedView pv;
   const int32_t *parents;
-  const uint8_t *kp, *vp;
+  int npu, n_qt, gq;  // nodes of a unit, units of a sequence and KV head (for max_q nodes), q-heads per KV head
+};
+
+// A sequence's nodes and keys.
+struct Seq {
+  int row, T, base, len;  // first row, nodes taken, slot of node 0 (negative: some have none), keys
+};
+__device__ __forceinline__ Seq seq_of(const TreeView &v, int b, bool flag) {
+  Seq s{0, 0, 0, 0};
+  if (b >= v.pv.B) return s;
+  const int n = paged_len(v.pv, b, flag);
+  int a = b, e = b + 1;
+  if (v.pv.cu_q) a = v.pv.cu_q[b], e = v.pv.cu_q[b + 1];
+  if (a < 0 || a >= v.pv.n_tokens || e <= a) return s;
+  s.row = a, s.base = n - (e - a), s.len = n;
+  s.T = min(min(e, v.pv.n_tokens) - a, v.pv.max_q);
+  if (flag && e - a > s.T) atomicExch(v.pv.status, (int32_t)DEVERR_SEQLEN);
+  return s;
+}
+__device__ __forceinline__ int seq_tiles(const Seq &s) { return s.T ? (s.len + KT - 1) / KT : 0; }
+__device__ __forceinline__ int seq_qt(const TreeView &v, const Seq &s) { return (s.T + v.npu - 1) / v.npu; }
+// Virtual tiles of the sequence.
+__device__ __forceinline__ int seq_vtiles(const TreeView &v, const Seq &s) {
+  const int t = seq_tiles(s);
+  return t ? seq_qt(v, s) * v.pv.Hkv * (t + ITEM_TILES) : 0;
+}
+// Units of a sequence lie KV head by KV head, the tiles of nodes of one next to each other.
+__device__ __forceinline__ int unit_index(const TreeView &v, int b, int h, int qt) { return (b * v.pv.Hkv + h) * v.n_qt + qt; }
+
+struct Walk {
+  int b, u, off, left, v, tiles, units;  // sequence, unit within it, virtual offset within the unit, tiles left, position
+  Seq s;
+};
+struct Item {
+  int b, h, qt, t0, t1, tiles, vstart;
+  Seq s;
+};
+__device__ __forceinline__ void walk_load(const TreeView &v, Walk &w) {
+  w.s = seq_of(v, w.b, false);
+  w.tiles = seq_tiles(w.s);
+  w.units = seq_qt(v, w.s) * v.pv.Hkv;
+}
+// The next sequence with keys, looked for 32 at a time by the whole warp (idle slots may be many).
+__device__ __forceinline__ bool walk_next(const TreeView &v, Walk &w) {
+  for (int b0 = w.b + 1; b0 < v.pv.B; b0 += 32) {
+    const uint32_t m = __ballot_sync(FULL_MASK, seq_tiles(seq_of(v, b0 + (int)(threadIdx.x & 31), false)) > 0);
+    if (m) {
+      w.b = b0 + __ffs(m) - 1;
+      walk_load(v, w);
+      return true;
+    }
+  }
+  return false;
+}
+// The next item of the share (false: done).  The whole warp calls.
+__device__ __forceinline__ bool next_item(const TreeView &v, Walk &w, Item &it) {
+  while (w.left > 0) {
+    if (w.b >= v.pv.B) return false;
+    if (w.tiles == 0 || w.u >= w.units) {
+      w.u = 0, w.off = 0;
+      if (!walk_next(v, w)) return false;
+      continue;
+    }
+    const int vt = w.tiles + ITEM_TILES, n = min(vt - w.off, w.left), nq = seq_qt(v, w.s);
+    it.b = w.b, it.h = w.u / nq, it.qt = w.u - it.h * nq, it.s = w.s, it.tiles = w.tiles;
+    it.t0 = max(w.off - ITEM_TILES, 0), it.t1 = w.off + n - ITEM_TILES;
+    it.vstart = w.v - w.off + ITEM_TILES;
+    w.v += n, w.left -= n, w.off += n;
+    if (w.off == vt) ++w.u, w.off = 0;
+    if (it.t1 > it.t0) return true;
+  }
+  return false;
+}
+// One warp: all virtual tiles (flagging bad lengths), then where this CTA's share starts.
+__device__ void find_share(const TreeView &v, int lane, Walk &w, int &V, int &G) {
+  int sum = 0;
+  for (int b = lane; b < v.pv.B; b += 32) sum += seq_vtiles(v, seq_of(v, b, blockIdx.x == 0));
+  V = __reduce_add_sync(FULL_MASK, sum);
+  G = min((int)gridDim.x, V);
+  w = Walk{};
+  if ((int)blockIdx.x >= G) return;
+  w.v = share_start(blockIdx.x, V, G);
+  w.left = share_start(blockIdx.x + 1, V, G) - w.v;
+  int base = 0;
+  for (int b0 = 0; b0 < v.pv.B; b0 += 32) {
+    const int t = seq_vtiles(v, seq_of(v, b0 + lane, false));
+    int inc = t;
+#pragma unroll
+    for (int h = 1; h < 32; h <<= 1) {
+      const int o = __shfl_up_sync(FULL_MASK, inc, h);
+      if (lane >= h) inc += o;
+    }
+    const uint32_t hit = __ballot_sync(FULL_MASK, base + inc > w.v);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      w.b = b0 + l;
+      w.off = w.v - (base + __shfl_sync(FULL_MASK, inc - t, l));
+      break;
+    }
+    base += __shfl_sync(FULL_MASK, inc, 31);
+  }
+  walk_load(v, w);
+  const int vt = w.tiles + ITEM_TILES;
+  w.u = w.off / vt;
+  w.off -= w.u * vt;
+}
+
+// ------------------------------------------------------------------------------ preparation
+constexpr int PREP_WARPS = 16;
+struct PrepParams {
+  TreeView v;
   RowsView q;
   RopeView rope;
   PagedOut o;
-  int Hq, gq;
-  float scale;
-  const float *kr, *vr;
-  float kc[16], vc[16];
+  int Hq, R, parts;
+  float qmul;          // log2(e) * scale / alpha_K
+  const uint4 *kfrag;  // R of the keys
+  uint8_t *qh;         // [unit] operand images: two halves of 64 dims, rows of 128 bytes (columns' hi parts, then lo)
+  float *qsc;          // [unit][R] power-of-two scales, 0 for a column without a node
+  uint4 *sees;         // [sequence][tile of nodes][node's key]: the columns that see it
+};
+struct PrepSmem {
+  uint4 r[2][8][8][32];               // R, bf16 hi and lo
+  uint16_t xs[PREP_WARPS][2][16][D];  // a warp's rows, bf16 hi and lo; 16-byte chunk c of row r at c ^ (r % 8)
+  uint64_t full;
 };
 
-__global__ void __launch_bounds__(128) k_tree_simple(const SimpleParams p) {
-  __shared__ float x[D], y[D], s[128], w[128];
-  __shared__ uint32_t anc[TREE_MAX / 32];
-  const int tok = blockIdx.x, kvh = blockIdx.y, tid = threadIdx.x;
-  pdl_trigger();
-  pdl_wait();
-  if (tok >= paged_rows(p.pv)) return;
-  const int b = paged_seq(p.pv, tok), n = paged_len(p.pv, b, true);
-  const int lo = p.pv.cu_q ? p.pv.cu_q[b] : b, T = p.pv.cu_q ? p.pv.cu_q[b + 1] - lo : 1, i = tok - lo;
-  const int base = n - T, slot = base + i;
-  if (tid < TREE_MAX / 32) anc[tid] = 0;
-  __syncthreads();
-  const bool none = slot < 0 || i >= p.pv.max_q;
-  if (i >= p.pv.max_q && tid == 0) atomicExch(p.pv.status, (int32_t)DEVERR_SEQLEN);
-  if (tid == 0 && !none)
-    for (int m = i; m >= 0; m = tree_parent(p.parents, lo, m, p.pv.status, true)) anc[m >> 5] |= 1u << (m & 31);
-  __syncthreads();
-  for (int h = kvh * p.gq; h < (kvh + 1) * p.gq; ++h) {
-    float acc = 0.f, l = 0.f, M = -INFINITY;
-    if (!none) {
-      if (tid < 32) {
-        float v[4];
-        load_lane4(p.q.data + tok * p.q.token_bytes + h * p.q.head_bytes, p.q.dtype, tid, v);
-        if (p.rope.rot_dim) rope_lane4(v, tid, p.rope, rope_pos(p.rope, tree_pos(p.pv, p.parents, b, tok, slot, false), p.pv.status, true));
-        for (int e = 0; e < 4; ++e) x[4 * tid + e] = v[e];
-      }
-      __syncthreads();
-      float a = 0.f;
-      for (int k = 0; k < D; ++k) a = fmaf(p.kr[tid * D + k], x[k], a);
-      y[tid] = a * p.scale * LOG2E;
-      __syncthreads();
-      for (int k0 = 0; k0 < n; k0 += 128) {
-        const int t = k0 + tid, j = t - base;
-        const bool see = t < n && (j < 0 || (j < TREE_MAX && ((anc[j >> 5] >> (j & 31)) & 1u)));
-        float sc = -INFINITY;
-        if (see) {
-          const uint8_t *r = p.kp + paged_row(p.pv, max(paged_page(p.pv, b, t, true), 0), kvh, t & ((1 << p.pv.page_shift) - 1));
-          float d = 0.f;
-          for (int e = 0; e < 64; ++e) d += p.kc[r[4 + e] & 15] * y[2 * e] + p.kc[r[4 + e] >> 4] * y[2 * e + 1];
-          sc = d * *reinterpret_cast<const float *>(r);
-        }
-        s[tid] = sc;
-        __syncthreads();
-        float bm = -INFINITY;
-        for (int e = 0; e < 128; ++e) bm = fmaxf(bm, s[e]);
-        const float mn = fmaxf(M, bm), mu = mn == -INFINITY ? 0.f : mn, f = exp2f(M - mu);
-        w[tid] = see ? exp2f(sc - mu) : 0.f;
-        __syncthreads();
-        M = mn, l *= f, acc *= f;
-        for (int e = 0; e < 128 && k0 + e < n; ++e) {
-          if (w[e] == 0.f) continue;
-          const int te = k0 + e;
-          const uint8_t *r = p.vp + paged_row(p.pv, max(paged_page(p.pv, b, te, false), 0), kvh, te & ((1 << p.pv.page_shift) - 1));
-          const int idx = (r[4 + tid / 2] >> (4 * (tid & 1))) & 15;
-          l += w[e];
-          acc += w[e] * *reinterpret_cast<const float *>(r) * p.vc[idx];
-        }
-        __syncthreads();
-      }
-    }
-    x[tid] = l == 0.f ? 0.f : acc / l;
-    __syncthreads();
-    float o = 0.f;
-    for (int k = 0; k < D; ++k) o = fmaf(p.vr[k * D + tid], x[k], o);
-    y[tid] = o;
-    __syncthreads();
-    if (tid < 32) {
-      const float v[4] = {y[4 * tid], y[4 * tid + 1], y[4 * tid + 2], y[4 * tid + 3]};
-      if (i < p.pv.max_q) store_lane4(p.o.out, p.o.dtype, ((size_t)tok * p.Hq + h) * D, tid, v);
-    }
-    __syncthreads();
+// Which columns of tile qt see key 32 jw + lane of sequence b's nodes.
+__device__ __forceinline__ void see_bits(const PrepParams &p, int b, int qt, int jw, int lane) {
+  const Seq s = seq_of(p.v, b, false);
+  const int n0 = qt * p.v.npu;
+  if (n0 >= s.T) return;
+  uint32_t word[TREE_MAX / 32];  // lane l: ancestors 32 jw .. of nodes n0 + l, n0 + l + 32, ...
+#pragma unroll
+  for (int i = 0; i < TREE_MAX / 32; ++i) {
+    word[i] = 0;
+    const int local = 32 * i + lane;
+    if (local >= p.v.npu || n0 + local >= s.T || s.base + n0 + local < 0) continue;
+    for (int m = n0 + local; m >= 0; m = tree_parent(p.v.parents, s.row, m, p.v.pv.status, jw == 0))
+      if ((m >> 5) == jw) word[i] |= 1u << (m & 31);
   }
+  uint32_t out[4] = {0, 0, 0, 0};
+  int node = 0, h = 0;
+#pragma unroll
+  for (int o = 0; o < 4; ++o) {
+    for (int bit = 0; bit < 32 && 32 * o + bit < p.R; ++bit) {
+      const uint32_t w0 = node < 64 ? (node < 32 ? word[0] : word[1]) : (node < 96 ? word[2] : word[3]);
+      const uint32_t w = __shfl_sync(FULL_MASK, w0, node & 31);  // (node is the same in every lane)
+      if (node < p.v.npu) out[o] |= ((w >> lane) & 1u) << bit;
+      if (++h == p.v.gq) h = 0, ++node;
+    }
+  }
+  p.sees[((size_t)b * p.v.n_qt + qt) * TREE_MAX + 32 * jw + lane] = make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// R's fragments (64 KB) lie in shared memory once per CTA, from one bulk copy ahead of the wait; each warp takes tasks
+// by itself: 16 columns of a unit (loaded in rows, turned by position, split into bf16 parts in the warp's own
+// shared memory, multiplied by R in three products of parts, stored from the product's fragments), or the
+// bits of 32 keys.
+__global__ void __launch_bounds__(PREP_WARPS * 32) k_tree_prep(const PrepParams p) {
+  extern __shared__ __align__(128) uint8_t smem_prep[];
+  PrepSmem &sm = *reinterpret_cast<PrepSmem *>(smem_prep);
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.full, 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(&sm.full, sizeof(sm.r));
+    bulk_g2s(&sm.r[0][0][0][0], p.kfrag, sizeof(sm.r), &sm.full);
+  }
+  __syncthreads();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  auto &xs = sm.xs[warp];
+  const TreeView &v = p.v;
+  const int blocks = p.R / 16;
+  const int64_t q_tasks = (int64_t)v.pv.B * v.pv.Hkv * v.n_qt * blocks, tasks = q_tasks + (int64_t)v.pv.B * v.n_qt * 4;
+  bool have_r = false;
+  // tasks over the CTAs first: a few use as many SMs as they can
+  for (int64_t task = (int64_t)warp * gridDim.x + blockIdx.x; task < tasks; task += (int64_t)PREP_WARPS * gridDim.x) {
+    if (task >= q_tasks) {
+      const int x = (int)(task - q_tasks), bq = x >> 2;
+      see_bits(p, bq / v.n_qt, bq % v.n_qt, x & 3, lane);
+      continue;
+    }
+    const int unit = (int)(task / blocks), c0 = 16 * (int)(task - (int64_t)unit * blocks);
+    const int qt = unit % v.n_qt, bh = unit / v.n_qt, b = bh / v.pv.Hkv, h = bh - b * v.pv.Hkv;
+    const Seq s = seq_of(v, b, false);
+    if (qt * v.npu >= s.T) continue;
+    // lane i < 16: column c0 + i
+    int my_turn = 0;
+    uint64_t my_src = 0;
+    if (lane < 16) {
+      const int c = c0 + lane, local = c / v.gq, node = qt * v.npu + local, head = h * v.gq + c - local * v.gq;
+      if (local < v.npu && node < s.T) {
+        const int tok = s.row + node;
+        if (s.base + node >= 0) {
+          my_src = (uint64_t)(uintptr_t)(p.q.data + tok * p.q.token_bytes + head * p.q.head_bytes);
+          if (p.rope.rot_dim)
+            my_turn = rope_pos(p.rope, tree_pos(v.pv, v.parents, b, tok, s.base + node, true), v.pv.status, true);
+        }
+      }
+    }
+    __syncwarp();  // the last task's fragments are read
+    constexpr int NR = 8;
+#pragma unroll 1
+    for (int rb = 0; rb < 16; rb += NR) {  // eight rows' loads in flight
+      float x[NR][4];
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const uint8_t *src = reinterpret_cast<const uint8_t *>((uintptr_t)__shfl_sync(FULL_MASK, my_src, rb + i));
+        if (src) load_lane4(src, p.q.dtype, lane, x[i]);
+        else x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+      }
+      if (p.rope.rot_dim) {
+        const int turn = __shfl_sync(FULL_MASK, my_turn, rb);
+        if (__all_sync(FULL_MASK, my_turn == turn || (lane & 8) != rb || lane >= 16)) {  // one node's heads
+          const LaneAngles an = rope_angles(lane, p.rope, turn);
+#pragma unroll
+          for (int i = 0; i < NR; ++i) rope_turn(x[i], lane, p.rope, an);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NR; ++i)
+            rope_turn(x[i], lane, p.rope, rope_angles(lane, p.rope, __shfl_sync(FULL_MASK, my_turn, rb + i)));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        uint32_t hi[2], lo[2];
+        float f[4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          hi[m] = pack_bf162(x[i][2 * m], x[i][2 * m + 1]);
+          f[2 * m] = __uint_as_float(hi[m] << 16), f[2 * m + 1] = __uint_as_float(hi[m] & 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = isinf(f[e]) ? x[i][e] = 0.f : f[e];  // an infinite part has no rest
+#pragma unroll
+        for (int m = 0; m < 2; ++m) lo[m] = pack_bf162(x[i][2 * m] - f[2 * m], x[i][2 * m + 1] - f[2 * m + 1]);
+        const int at = 8 * ((lane >> 1) ^ i) + 4 * (lane & 1);  // NR rows: i is the row modulo 8
+        *reinterpret_cast<uint2 *>(&xs[0][rb + i][at]) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2 *>(&xs[1][rb + i][at]) = make_uint2(lo[0], lo[1]);
+      }
+    }
+    __syncwarp();
+    if (!have_r) {
+      if (!mbar_wait_bounded(&sm.full, 0, WAIT_LIMIT_NS)) {
+        if (lane == 0) atomicExch(v.pv.status, (int32_t)DEVERR_TIMEOUT);
+        return;
+      }
+      have_r = true;
+    }
+    // Y = X R^T; R's A fragments hold the B fragments of two column tiles each: registers (0, 2)
+    // and (1, 3)
+    float acc[16][4];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < 8; ++k) {
+      uint4 a[2];
+#pragma unroll
+      for (int part = 0; part < 2; ++part) a[part] = ldmatrix_x4(&xs[part][lane & 15][8 * ((2 * k + (lane >> 4)) ^ (lane & 7))]);
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const uint4 rh = sm.r[0][m][k][lane], rl = sm.r[1][m][k][lane];
+        mma_bf16(acc[2 * m], a[0], rh.x, rh.z), mma_bf16(acc[2 * m + 1], a[0], rh.y, rh.w);
+        mma_bf16(acc[2 * m], a[1], rh.x, rh.z), mma_bf16(acc[2 * m + 1], a[1], rh.y, rh.w);
+        mma_bf16(acc[2 * m], a[0], rl.x, rl.z), mma_bf16(acc[2 * m + 1], a[0], rl.y, rl.w);
+      }
+    }
+    // columns g and g + 8 of the task, dims 8 j + 2 t and the next
+    uint8_t *image = p.qh + (size_t)unit * p.R * p.parts * 256;
+    const uint32_t half_bytes = p.R * p.parts * 128;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool live = __shfl_sync(FULL_MASK, my_src, g + 8 * i) != 0;
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        acc[j][2 * i] *= p.qmul, acc[j][2 * i + 1] *= p.qmul;
+        m = fmaxf(m, fmaxf(fabsf(acc[j][2 * i]), fabsf(acc[j][2 * i + 1])));
+      }
+      m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, 2));
+      // the power of two that brings the largest element to [2^13, 2^14)
+      const int e = scale_exp(m), row = c0 + g + 8 * i;
+      const float down = pow2i(-e);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        uint32_t hi, lo;
+        split_half2(acc[j][2 * i] * down, acc[j][2 * i + 1] * down, hi, lo);
+        uint8_t *dst = image + (j >> 3) * half_bytes + row * 128 + (((j & 7) ^ (row & 7)) << 4) + 4 * t;
+        *reinterpret_cast<uint32_t *>(dst) = hi;
+        if (p.parts == 2) *reinterpret_cast<uint32_t *>(dst + p.R * 128) = lo;
+      }
+      if (t == 0) p.qsc[(size_t)unit * p.R + row] = live ? pow2i(e) : 0.f;
+    }
+  }
+  // (a CTA without columns: R's copy must land before it ends)
+  if (!have_r && threadIdx.x == 0) (void)mbar_wait_bounded(&sm.full, 0, WAIT_LIMIT_NS);
+}
+
+// ------------------------------------------------------------------------------ attention
+struct PartialParams {
+  TreeView v;
+  const uint8_t *kp, *vp;
+  int Hq;
+  const uint8_t *qh;
+  const float *qsc;
+  const uint4 *sees;
+  uint32_t klo[2], khi[2], vlo[2], vhi[2];
+  float *split;   // [CTA][2][R] partials of units that several CTAs share
+  float *whole;   // [row][Hq] partials of units one CTA finished
+  int32_t *unit;  // per unit: first CTA | CTAs << 16
+};
+
+struct Misc {
+  uint64_t raw_full[2][4], raw_empty[2][4];  // [side][stage]
+  uint64_t k_full[2], k_empty[2], v_full[2];
+  uint64_t s_done[2], p_ready[2], pv_done[2];  // a P buffer and a V stage are free once their product is done
+  uint64_t q_full, q_empty, o_free, drain;
+  // Key norms of the last four K tiles: a K stage is free once its product is done, while the softmax still
+  // needs the norms; the decoders reach tile j + 4 only after every group has finished tile j.
+  float kn[4][KT], nv[2][KT];
+  float4 qm[64];          // columns 2i, 2i + 1: scales of q, minus the running maxima (less W_SHIFT; none yet: 0)
+  float4 move[64];        // and, where maxima are raised: what the scores fall by, the square root of O's factor
+  float mx[128];          // the running maxima, -infinity without one
+  float red[2][4][64];    // [group][warp][column of the group]
+  uint32_t tmem;
+  int abort_flag;
+  Walk walk;
+  int V, G;
+};
+
+__device__ __forceinline__ uint64_t pk2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void upk2(uint64_t r, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Barrier of softmax group gr (128 threads) that ORs a flag across them.
+__device__ __forceinline__ bool group_or(int gr, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " bar.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(1 + gr)
+      : "memory");
+  return r != 0;
+}
+
+// CH consecutive columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&x)[32]) { tmem_ld32(taddr, x); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&x)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&x)[32]) { tmem_st32(taddr, x); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&x)[16]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(x[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+template <int R, int PARTS>
+__global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams p) {
+  using F = Cfg<R, PARTS>;
+  constexpr int C = F::C, CH = F::CH, NRAW = F::NRAW;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
+  Misc &ms = *reinterpret_cast<Misc *>(smem + F::OFF_MISC);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  if (warp == 0) tmem_alloc(smem_addr(&ms.tmem), 512);
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      for (int i = 0; i < NRAW; ++i) mbar_init(&ms.raw_full[s][i], 1), mbar_init(&ms.raw_empty[s][i], 4);
+      mbar_init(&ms.k_full[s], 4), mbar_init(&ms.v_full[s], 4);
+      mbar_init(&ms.k_empty[s], 1), mbar_init(&ms.s_done[s], 1), mbar_init(&ms.pv_done[s], 1);
+      mbar_init(&ms.p_ready[s], 8);
+    }
+    mbar_init(&ms.q_full, 1), mbar_init(&ms.q_empty, 1), mbar_init(&ms.o_free, 8), mbar_init(&ms.drain, 1);
+    ms.abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  if (warp == W_LOAD) {
+    Walk w;
+    int V, G;
+    find_share(p.v, lane, w, V, G);
+    if (lane == 0) ms.walk = w, ms.V = V, ms.G = G;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem;
+  // Bounded wait; fails at once when another thread has given up already.
+  auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+    if (*reinterpret_cast<volatile int *>(&ms.abort_flag)) return false;
+    const bool done = mbar_wait_bounded(bar, parity, WAIT_LIMIT_NS);
+    if (!done) {
+      atomicExch(&ms.abort_flag, 1);
+      atomicExch(p.v.pv.status, (int32_t)DEVERR_TIMEOUT);
+    }
+    return done;
+  };
+  Walk w = ms.walk;
+  Item it;
+  bool ok = true;
+
+  if (warp >= W_KDEC) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F::REGS_OTHER));
+    if (warp == W_LOAD) {
+      // ================ loader: lanes 0-7 the keys' pages, 16-23 the values'
+      const int psh = p.v.pv.page_shift, P = 1 << psh, side = lane >> 4, seg = lane & 15;
+      const uint8_t *pages = side ? p.vp : p.kp;
+      uint32_t n = 0;  // tiles loaded
+      while (ok && next_item(p.v, w, it)) {
+        auto page_of = [&](int j) -> int {
+          const int pi = ((j * KT) >> psh) + seg;
+          if (j >= it.t1 || seg >= 8 || (pi << psh) >= min((j + 1) * KT, it.s.len)) return -1;
+          return max(paged_page(p.v.pv, it.b, pi << psh, !side), 0);
+        };
+        int pg = page_of(it.t0);
+        for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
+          const int kf = j * KT, nk4 = (min(KT, it.s.len - kf) + 3) & ~3, s = n % NRAW;
+          const int pg_next = page_of(j + 1);
+          if (n >= NRAW) {
+            ok = wait(&ms.raw_empty[0][s], ((n / NRAW) - 1) & 1) && wait(&ms.raw_empty[1][s], ((n / NRAW) - 1) & 1);
+            if (!(ok = __all_sync(FULL_MASK, ok))) break;
+          }
+          // rows of a tile rounded up to four (16-byte copies; they stay inside the page)
+          if (seg == 0) mbar_arrive_expect_tx(&ms.raw_full[side][s], nk4 * PG_ROW);
+          __syncwarp();
+          if (pg >= 0) {
+            const int k0 = max((((kf >> psh) + seg) << psh), kf), k1 = min(((k0 >> psh) + 1) << psh, kf + nk4);
+            bulk_g2s(smem + F::OFF_RAW + (2 * s + side) * RAW + (k0 - kf) * PG_ROW,
+                     pages + paged_row(p.v.pv, pg, it.h, k0 & (P - 1)), (uint32_t)(k1 - k0) * PG_ROW, &ms.raw_full[side][s]);
+          }
+          pg = pg_next;
+        }
+      }
+      // after a failed wait: let the copies in flight land before the CTA ends
+      if (*reinterpret_cast<volatile int *>(&ms.abort_flag))
+        for (uint32_t c = n > NRAW ? n - NRAW : 0; c < n; ++c)
+          for (int s = 0; s < 2; ++s) (void)mbar_wait_bounded(&ms.raw_full[s][c % NRAW], (c / NRAW) & 1, WAIT_LIMIT_NS);
+    } else if (warp == W_Q) {
+      // ================ q's image, as soon as the last item's scores are done
+      uint32_t n = 0;
+      while (ok && next_item(p.v, w, it)) {
+        if (n) ok = __all_sync(FULL_MASK, wait(&ms.q_empty, (n - 1) & 1));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ms.q_full, F::Q_BYTES);
+          bulk_g2s(smem + F::OFF_Q, p.qh + (size_t)unit_index(p.v, it.b, it.h, it.qt) * F::Q_BYTES, F::Q_BYTES, &ms.q_full);
+        }
+        __syncwarp();
+        ++n;
+      }
+      if (n && *reinterpret_cast<volatile int *>(&ms.abort_flag)) (void)mbar_wait_bounded(&ms.q_full, (n - 1) & 1, WAIT_LIMIT_NS);
+    } else if (warp < W_MMA) {
+      // ================ decoders: a warp group for the keys, one for the values, thread = key of the tile
+      const int row = tid & 127;
+      const bool side = warp >= W_VDEC;
+      uint32_t lo2[2], hi2[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) lo2[i] = side ? p.vlo[i] : p.klo[i], hi2[i] = side ? p.vhi[i] : p.khi[i];
+      const uint32_t tK = tmem + ((uint32_t)((warp & 3) * 32) << 16) + F::TM_K;
+      uint32_t n = 0;
+      while (ok && next_item(p.v, w, it)) {
+        for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
+          const int st = n & 1, rs = n % NRAW;
+          if (n >= 2) ok = wait(side ? &ms.pv_done[st] : &ms.k_empty[st], ((n >> 1) - 1) & 1);
+          if (ok) ok = wait(&ms.raw_full[side][rs], (n / NRAW) & 1);
+          if (!(ok = __all_sync(FULL_MASK, ok))) break;
+          const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + F::OFF_RAW + (2 * rs + side) * RAW + row * PG_ROW);
+          const float norm = j * KT + row < it.s.len ? __uint_as_float(src[0]) : 0.f;
+          if (side) {
+            uint8_t *dst = smem + F::OFF_V + st * SW_TILE_BYTES;
+#pragma unroll
+            for (int ch = 0; ch < 16; ++ch) {
+              uint32_t d[4];
+              decode8<0x5140u, 0x7362u>(src[1 + ch], lo2, hi2, d);
+              *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 8 * ch)) = make_uint4(d[0], d[1], d[2], d[3]);
+            }
+            ms.nv[st][row] = norm;
+            fence_async_smem();
+          } else {
+            tc_fence_after();  // the product that read the stage
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t d[32];
+#pragma unroll
+              for (int ch = 0; ch < 8; ++ch) {
+                uint32_t x[4];
+                decode8<0x5140u, 0x7362u>(src[1 + 8 * half + ch], lo2, hi2, x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[4 * ch + e] = x[e];
+              }
+              tmem_st32(tK + 64 * st + 32 * half, d);
+            }
+            ms.kn[n & 3][row] = norm;
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(side ? &ms.v_full[st] : &ms.k_full[st]), mbar_arrive(&ms.raw_empty[side][rs]);
+        }
+      }
+    } else if (warp == W_MMA) {
+      // ================ issuer
+      const bool lead = elect_lane();
+      const uint32_t tb = __shfl_sync(FULL_MASK, tmem, 0), tS = tb + F::TM_S, tO = tb + F::TM_O, tK = tb + F::TM_K;
+      const uint64_t dq = sw128_desc(smem_addr(smem + F::OFF_Q));
+      const uint64_t dv = sw128_mn_desc(smem_addr(smem + F::OFF_V)), dp = sw128_mn_desc(smem_addr(smem + F::OFF_P));
+      uint32_t n = 0, items = 0;  // tiles and items before this one
+      bool issued = false;
+      while (ok && next_item(p.v, w, it)) {
+        const uint32_t tiles = it.t1 - it.t0;
+        if (!(ok = __all_sync(FULL_MASK, wait(&ms.q_full, items & 1)))) break;
+        // S^T of the item's tile m: its buffer was read before the P of two tiles ago was ready
+        auto issue_s = [&](uint32_t m) -> bool {
+          const uint32_t c = n + m, st = c & 1;
+          if (!__all_sync(FULL_MASK, wait(&ms.k_full[st], (c >> 1) & 1))) return false;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+              for (int s = 0; s < 8; ++s)
+                umma_ts<F::IDESC_S>(tS + R * st, tK + 64 * st + 8 * s,
+                                    desc_step(dq, (s >> 2) * F::Q_HALF + part * R * 128 + (s & 3) * 32), (part || s) ? 1u : 0u);
+            umma_commit(&ms.s_done[st]);
+            umma_commit(&ms.k_empty[st]);
+            if (m == tiles - 1) umma_commit(&ms.q_empty);
+          }
+          __syncwarp();
+          issued = true;
+          return true;
+        };
+        for (uint32_t m = 0; ok && m < 2 && m < tiles; ++m) ok = issue_s(m);
+        for (uint32_t m = 0; ok && m < tiles; ++m) {
+          const uint32_t c = n + m, st = c & 1;
+          ok = wait(&ms.p_ready[st], (c >> 1) & 1);
+          if (ok) ok = wait(&ms.v_full[st], (c >> 1) & 1);
+          if (ok && m == 0 && items) ok = wait(&ms.o_free, (items - 1) & 1);
+          if (!(ok = __all_sync(FULL_MASK, ok))) break;
+          tc_fence_after();
+          if (lead) {
+            const uint64_t a = desc_step(dv, st * SW_TILE_BYTES), b = desc_step(dp, st * F::P_BYTES);
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              umma<F::IDESC_PV>(tO, desc_step(a, 2048 * s), desc_step(b, 2048 * s), (m || s) ? 1u : 0u);
+            umma_commit(&ms.pv_done[st]);
+          }
+          __syncwarp();
+          if (m + 2 < tiles) ok = issue_s(m + 2);
+        }
+        n += tiles, ++items;
+      }
+      if (issued && lead && *reinterpret_cast<volatile int *>(&ms.abort_flag)) {
+        umma_commit(&ms.drain);
+        (void)mbar_wait_bounded(&ms.drain, 0, WAIT_LIMIT_NS);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F::REGS_SOFTMAX));
+    // ================ softmax: group gr takes columns gr C .. + C, thread = key
+    const int gr = warp >> 2, key = tid & 127, wq = warp & 3, col0 = gr * C;
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_off + F::TM_S + col0, tO = tmem + lane_off + F::TM_O + col0;
+    uint32_t n = 0;
+    while (next_item(p.v, w, it)) {
+      const int unit = unit_index(p.v, it.b, it.h, it.qt), n0 = it.qt * p.v.npu;
+      const int cols = min(it.s.T - n0, p.v.npu) * p.v.gq;  // columns with a node
+      // the group's columns: no maximum yet; those without a node keep 0
+      if (key < C) {
+        const int c = col0 + key;
+        const float sc = p.qsc[(size_t)unit * R + c];
+        float *qm = reinterpret_cast<float *>(&ms.qm[c >> 1]);
+        qm[c & 1] = sc, qm[2 + (c & 1)] = 0.f;
+        ms.mx[c] = sc == 0.f ? 0.f : -INFINITY;
+      }
+      bool fresh = true;  // some column has no maximum yet
+      uint64_t l2[C / 2];
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i) l2[i] = 0;
+      (void)group_or(gr, false);
+      const int tiles = it.t1 - it.t0;
+      for (int m = 0; m < tiles; ++m, ++n) {
+        const int st = n & 1, t = (it.t0 + m) * KT + key, j = t - it.s.base;
+        ok = wait(&ms.s_done[st], (n >> 1) & 1);
+        if (ok) ok = wait(&ms.v_full[st], (n >> 1) & 1);
+        if (ok && n >= 2) ok = wait(&ms.pv_done[st], ((n >> 1) - 1) & 1);  // the P buffer is free
+        ok = __all_sync(FULL_MASK, ok);
+        tc_fence_after();
+        const float kn = ms.kn[n & 3][key], nv = ms.nv[st][key];
+        const uint64_t kn2 = pk2(kn, kn);
+        const float lv = fmaxf(log2_approx(nv), -64.f), nvf = nv * NORM_FACTOR;
+        // a score past this leaves the operand's range (2^15), or a weight passes W_MOST
+        const float most = fminf(15.f - log2_approx(nvf), 96.f);
+        const bool whole = (it.t0 + m + 1) * KT <= it.s.base;  // every column sees every key of the tile
+        uint4 see = make_uint4(~0u, ~0u, ~0u, ~0u);
+        if (!whole && j >= 0) {
+          see = make_uint4(0u, 0u, 0u, 0u);
+          if (t < it.s.len && j < TREE_MAX) see = p.sees[((size_t)it.b * p.v.n_qt + it.qt) * TREE_MAX + j];
+        }
+        bool stop = false, some = false;
+#pragma unroll
+        for (int cc = 0; cc < C; cc += CH) {
+          float d[CH];
+          tmem_ld(tS + R * st + cc, d);
+          const uint32_t bits = (R == 32 ? see.x >> (16 * gr)
+                                         : (R == 64 ? (gr ? see.y : see.x) : (gr ? (cc ? see.w : see.z) : (cc ? see.y : see.x))));
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < CH; c += 2) {
+            const float4 qm = ms.qm[(col0 + cc + c) >> 1];
+            upk2(fma2(mul2(pk2(d[c], d[c + 1]), kn2), pk2(qm.x, qm.y), pk2(qm.z, qm.w)), d[c], d[c + 1]);
+          }
+          if (!whole) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) d[c] = (bits >> c) & 1u ? d[c] : -INFINITY;
+          }
+#pragma unroll
+          for (int c = 0; c < CH; ++c) top = fmaxf(top, d[c]);
+          const bool need = fresh || top > most || !ok;
+          if (group_or(gr, need)) {
+            // ---- maxima of the chunk's columns over the tile's keys; raise those that need it
+            if (group_or(gr, !ok)) {
+              stop = true;
+              break;
+            }
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              float u = d[c] + lv;
+#pragma unroll
+              for (int h = 16; h >= 1; h >>= 1) u = fmaxf(u, __shfl_xor_sync(FULL_MASK, u, h));
+              if (lane == (c & 31)) ms.red[gr][wq][cc + c] = u;
+            }
+            (void)group_or(gr, false);
+            bool none = false, raised = false;
+            if (key < CH) {
+              const int c = col0 + cc + key;
+              const float bm = fmaxf(fmaxf(ms.red[gr][0][cc + key], ms.red[gr][1][cc + key]),
+                                     fmaxf(ms.red[gr][2][cc + key], ms.red[gr][3][cc + key])) - W_SHIFT;
+              const float old = ms.mx[c];
+              float by = 0.f, root = 1.f;  // the maximum rises by `by` (from 0 without one)
+              if (bm > (old == -INFINITY ? -INFINITY : RESCALE_SLACK)) {
+                by = bm;
+                ms.mx[c] = old == -INFINITY ? bm : old + bm;
+                reinterpret_cast<float *>(&ms.qm[c >> 1])[2 + (c & 1)] = -ms.mx[c];
+                raised = old != -INFINITY;
+                if (raised) root = exp2_approx(-0.5f * by);
+              } else {
+                none = old == -INFINITY;
+              }
+              float *move = reinterpret_cast<float *>(&ms.move[c >> 1]);
+              move[c & 1] = by, move[2 + (c & 1)] = root;
+            }
+            if (group_or(gr, none)) some = true;
+            if (group_or(gr, raised) && m) {  // O is whole once the last tile's product has finished
+              ok = __all_sync(FULL_MASK, wait(&ms.pv_done[st ^ 1], ((n - 1) >> 1) & 1));
+              if (group_or(gr, !ok)) {
+                stop = true;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int part = 0; part < PARTS; ++part) {
+                float o[CH];
+                tmem_ld(tO + part * R + cc, o);
+#pragma unroll
+                for (int c = 0; c < CH; c += 2) {
+                  const float4 move = ms.move[(col0 + cc + c) >> 1];
+                  o[c] *= move.z * move.z, o[c + 1] *= move.w * move.w;
+                }
+                tmem_st(tO + part * R + cc, o);
+              }
+              tc_fence_before();
+            }
+#pragma unroll
+            for (int c = 0; c < CH; c += 2) {
+              const float4 move = ms.move[(col0 + cc + c) >> 1];
+              d[c] -= move.x, d[c + 1] -= move.y;
+              float l0, l1;
+              upk2(l2[(cc + c) / 2], l0, l1);
+              l2[(cc + c) / 2] = pk2(lower(l0, move.z), lower(l1, move.w));
+            }
+          }
+          // ---- weights, their sums and the operand P
+          uint32_t hi[CH / 2], lo[CH / 2];
+          const uint64_t nvf2 = pk2(nvf, nvf);
+#pragma unroll
+          for (int c = 0; c < CH; c += 2) {
+            const uint64_t e2 = pk2(exp2_approx(d[c]), exp2_approx(d[c + 1]));
+            uint64_t &l = l2[(cc + c) / 2];
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(l) : "l"(e2));
+            float p0, p1;
+            upk2(mul2(e2, nvf2), p0, p1);
+            // a key that is not seen: its norm may be anything
+            if (!whole) p0 = (bits >> c) & 1u ? p0 : 0.f, p1 = (bits >> (c + 1)) & 1u ? p1 : 0.f;
+            if (PARTS == 2) split_half2(p0, p1, hi[c / 2], lo[c / 2]);
+            else hi[c / 2] = pack_half2(p0, p1);
+          }
+          uint8_t *pb = smem + F::OFF_P + st * F::P_BYTES;
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) {
+            const uint32_t *x = part ? lo : hi;
+#pragma unroll
+            for (int c = 0; c < CH; c += 8)
+              *reinterpret_cast<uint4 *>(pb + sw128_offset(key, part * R + col0 + cc + c)) =
+                  make_uint4(x[c / 2], x[c / 2 + 1], x[c / 2 + 2], x[c / 2 + 3]);
+          }
+        }
+        if (stop) {
+          ok = false;
+          break;
+        }
+        fresh = some;
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.p_ready[st]);
+      }
+      if (!ok) break;
+
+      // ---- end of the item: O^T (thread = dim) and the sums of weights
+      ok = __all_sync(FULL_MASK, wait(&ms.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1));
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < C; c += 2) {
+        float l0, l1;
+        upk2(l2[c / 2], l0, l1);
+#pragma unroll
+        for (int h = 16; h >= 1; h >>= 1) l0 += __shfl_xor_sync(FULL_MASK, l0, h), l1 += __shfl_xor_sync(FULL_MASK, l1, h);
+        if (lane == 0) ms.red[gr][wq][c] = l0, ms.red[gr][wq][c + 1] = l1;
+      }
+      if (group_or(gr, !ok)) break;
+      const int first = share_of(it.vstart, ms.V, ms.G);
+      const int n_split = share_of(it.vstart + it.tiles - 1, ms.V, ms.G) - first + 1, cta = blockIdx.x;
+      if (tid == 0 && cta == first) p.unit[unit] = first | (n_split << 16);
+      const int head0 = it.h * p.v.gq;
+      auto row_of = [&](int c) -> float * {
+        if (n_split > 1) return p.split + ((size_t)(cta * 2 + (cta == first ? 1 : 0)) * R + c) * PROW;
+        const int local = c / p.v.gq;
+        return p.whole + ((size_t)(it.s.row + n0 + local) * p.Hq + head0 + c - local * p.v.gq) * PROW;
+      };
+      if (key < C && col0 + key < cols) {
+        float *dst = row_of(col0 + key) + D;
+        const float l = (ms.red[gr][0][key] + ms.red[gr][1][key]) + (ms.red[gr][2][key] + ms.red[gr][3][key]);
+        dst[0] = ms.mx[col0 + key], dst[1] = l;
+      }
+#pragma unroll 1
+      for (int cc = 0; cc < C; cc += CH) {
+        float o[CH];
+        tmem_ld(tO + cc, o);
+        if (PARTS == 2) {
+          float x[CH];
+          tmem_ld(tO + R + cc, x);
+#pragma unroll
+          for (int c = 0; c < CH; ++c) o[c] += x[c];
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+          if (col0 + cc + c < cols) row_of(col0 + cc + c)[32 * wq + lane] = o[c];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.o_free);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------------------ combine
+struct CombineParams {
+  TreeView v;
+  PagedOut o;
+  int Hq, R, grid;
+  float inv_vscale;    // 2^W_SHIFT / (2^P_SHIFT * alpha_V)
+  const uint4 *vfrag;  // R and R^T of the values
+  const float *split, *whole;
+  const int32_t *unit;
+};
+constexpr int CB_WARPS = 8;
+
+// Eight columns (a node's q-head each) per CTA and turn: warp w merges column w's partials (m* = max m_s, l* = sum
+// l_s 2^(m_s - m*), o = sum acc_s 2^(m_s - m*) / l*), the eight warps multiply by R^T, then warp w rounds the row.
+__global__ void __launch_bounds__(CB_WARPS * 32) k_tree_combine(const CombineParams p) {
+  __shared__ RotColumns x;
+  __shared__ __align__(16) float y[8][D + 4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  uint4 ahi[8], alo[8];  // this warp's 16 rows of R^T
+  rot_load(ahi, p.vfrag, 1, 0, warp, lane);
+  rot_load(alo, p.vfrag, 1, 1, warp, lane);
+  pdl_wait();
+  const TreeView &v = p.v;
+  const int64_t n = (int64_t)paged_rows(v.pv) * p.Hq;
+  for (int64_t r0 = (int64_t)blockIdx.x * 8; r0 < n; r0 += (int64_t)gridDim.x * 8) {
+    const int64_t r = r0 + warp;
+    const int tok = (int)(min(r, n - 1) / p.Hq), head = (int)(min(r, n - 1) - (int64_t)tok * p.Hq);
+    const int b = paged_seq(v.pv, tok);
+    const Seq s = seq_of(v, b, false);
+    const int node = tok - s.row;
+    const bool taken = r < n && node >= 0 && node < s.T;  // (rows past max_q are left as they were)
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    if (taken && s.base + node >= 0) {
+      const int qt = node / v.npu, h = head / v.gq, c = (node - qt * v.npu) * v.gq + head - h * v.gq;
+      const uint32_t info = (uint32_t)p.unit[unit_index(v, b, h, qt)];
+      const int first = min((int)(info & 0xFFFFu), p.grid - 1), ns = min((int)(info >> 16), p.grid - first);
+      float ms = -INFINITY, ls = 0.f;
+      for (int s0 = 0; s0 < ns; s0 += 8) {
+        float m8[8], l8[8];
+        float4 v8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = min(s0 + i, ns - 1);
+          const float *src = ns == 1 ? p.whole + ((size_t)tok * p.Hq + head) * PROW
+                                     : p.split + ((size_t)((first + k) * 2 + (k == 0 ? 1 : 0)) * p.R + c) * PROW;
+          m8[i] = __ldcg(src + D), l8[i] = __ldcg(src + D + 1);
+          v8[i] = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
+        }
+        float mc = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (s0 + i < ns && l8[i] != 0.f) mc = fmaxf(mc, m8[i]);
+        if (mc > ms) {
+          const float hf = (ms == -INFINITY) ? 0.f : exp2f(0.5f * (ms - mc)), f = hf * hf;
+          ls = lower(ls, hf);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[e] *= f;
+          ms = mc;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (s0 + i < ns && l8[i] != 0.f) {
+            const float hf = exp2f(0.5f * (m8[i] - ms)), f = hf * hf;
+            ls += lower(l8[i], hf);
+            a[0] = fmaf(f, v8[i].x, a[0]), a[1] = fmaf(f, v8[i].y, a[1]);
+            a[2] = fmaf(f, v8[i].z, a[2]), a[3] = fmaf(f, v8[i].w, a[3]);
+          }
+        }
+      }
+      const float f = ls == 0.f ? 0.f : p.inv_vscale / ls;  // (NaN stays)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] *= f;
+    }
+    rot_put(x, warp, lane, a);
+    __syncthreads();
+    {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
+      rot_mul<true>(acc, ahi, x, lane);
+      rot_mul<false>(acc2, alo, x, lane);
+      float *d = &y[2 * (lane & 3)][16 * warp + (lane >> 2)];
+      d[0] = acc[0] + acc2[0], d[D + 4] = acc[1] + acc2[1];
+      d[8] = acc[2] + acc2[2], d[D + 12] = acc[3] + acc2[3];
+    }
+    __syncthreads();
+    if (taken) {
+      const float4 z = *reinterpret_cast<const float4 *>(&y[warp][4 * lane]);
+      const float v4[4] = {z.x, z.y, z.z, z.w};
+      store_lane4(p.o.out, p.o.dtype, (size_t)r * D, lane, v4);
+    }
+    __syncthreads();  // x and y are free again
+  }
+}
+
+struct Layout {
+  int R, parts, npu, n_qt, gq, grid;
+  int64_t units;
+  size_t qsc, sees, unit, split, whole, bytes;
+};
+bool layout(const tq_ctx *k, const PagedView &pv, int Hq, int out_dtype, Layout *l) {
+  l->gq = Hq / pv.Hkv;
+  l->parts = out_dtype == TQ_DTYPE_BF16 ? 1 : 2;
+  const int rows = pv.max_q * l->gq;
+  l->R = rows <= 32 ? 32 : (rows <= 64 || l->parts == 2 ? 64 : 128);
+  l->npu = l->R / l->gq;  // at least one: 64 heads per KV head at most
+  l->n_qt = (pv.max_q + l->npu - 1) / l->npu;
+  l->grid = k->num_sms;
+  l->units = (int64_t)pv.B * pv.Hkv * l->n_qt;
+  const int64_t tiles = l->units * (((int64_t)pv.max_len + KT - 1) / KT + ITEM_TILES);
+  if (l->grid > 65535 || tiles > INT32_MAX || (int64_t)pv.n_tokens * Hq > INT32_MAX || l->units > INT32_MAX / 8) return false;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  l->qsc = up((size_t)l->units * l->R * l->parts * 256);
+  l->sees = l->qsc + up((size_t)l->units * l->R * 4);
+  l->unit = l->sees + up((size_t)pv.B * l->n_qt * TREE_MAX * 16);
+  l->split = l->unit + up((size_t)l->units * 4);
+  l->whole = l->split + up((size_t)l->grid * 2 * l->R * PROW * 4);
+  l->bytes = l->whole + up((size_t)pv.n_tokens * Hq * PROW * 4);
+  return true;
+}
+
+template <int R, int PARTS>
+cudaError_t launch_partial(const PartialParams &p, int grid, cudaStream_t st) {
+  constexpr uint32_t smem = Cfg<R, PARTS>::OFF_MISC + sizeof(Misc) + 1024;  // + slack to align to 1024
+  static_assert(smem <= 227 * 1024, "shared memory budget");
+  const cudaError_t e = kernel_smem_attr((const void *)k_tree_partial<R, PARTS>, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_tree_partial<R, PARTS>, dim3(grid), dim3(THREADS), smem, st, p);
 }
 
 }  // namespace
@@ -105,7 +1008,9 @@ static bool is_decode(const PagedView &pv, int Hq) { return pv.max_q == 1 && Hq 
 
 bool paged_tree_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes) {
   if (is_decode(pv, Hq)) return paged_decode_workspace(k, pv, Hq, bytes);
-  *bytes = 256;
+  Layout a, b;  // the size does not depend on the output's type
+  if (!layout(k, pv, Hq, TQ_DTYPE_BF16, &a) || !layout(k, pv, Hq, TQ_DTYPE_F32, &b)) return false;
+  *bytes = a.bytes > b.bytes ? a.bytes : b.bytes;
   return true;
 }
 
@@ -113,11 +1018,49 @@ cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView 
                               const uint8_t *kp, const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope,
                               float scale, const PagedOut &o, void *ws, cudaStream_t st) {
   if (is_decode(pv, Hq)) return launch_paged_decode(k, v, pv, kp, vp, q, Hq, rope, scale, o, ws, st);
-  SimpleParams p{};
-  p.pv = pv, p.parents = parents, p.kp = kp, p.vp = vp, p.q = q, p.rope = rope, p.o = o;
-  p.Hq = Hq, p.gq = Hq / pv.Hkv, p.scale = scale, p.kr = k->d_pi, p.vr = v->d_pi;
-  for (int i = 0; i < 16; ++i) p.kc[i] = k->cb.c[i], p.vc[i] = v->cb.c[i];
-  return launch_pdl(k_tree_simple, dim3(pv.n_tokens, pv.Hkv), dim3(128), 0, st, p);
+  Layout l;
+  if (!layout(k, pv, Hq, o.dtype, &l)) return cudaErrorInvalidValue;
+  uint8_t *base = static_cast<uint8_t *>(ws);
+  const TreeView tv{pv, parents, l.npu, l.n_qt, l.gq};
+  PrepParams a{};
+  a.v = tv, a.q = q, a.rope = rope, a.o = o;
+  a.Hq = Hq, a.R = l.R, a.parts = l.parts;
+  a.qmul = LOG2E * scale / k->f16.alpha;
+  a.kfrag = k->d_rfrag;
+  a.qh = base;
+  a.qsc = reinterpret_cast<float *>(base + l.qsc);
+  a.sees = reinterpret_cast<uint4 *>(base + l.sees);
+  cudaError_t e = kernel_smem_attr((const void *)k_tree_prep, (int)sizeof(PrepSmem));
+  if (e != cudaSuccess) return e;
+  const int64_t tasks = l.units * (l.R / 16) + (int64_t)pv.B * l.n_qt * 4;
+  e = launch_pdl(k_tree_prep, dim3((unsigned)(tasks < k->num_sms ? tasks : k->num_sms)), dim3(PREP_WARPS * 32),
+                 sizeof(PrepSmem), st, a);
+  if (e != cudaSuccess) return e;
+  PartialParams p{};
+  p.v = tv, p.kp = kp, p.vp = vp, p.Hq = Hq;
+  p.qh = a.qh, p.qsc = a.qsc, p.sees = a.sees;
+  for (int i = 0; i < 2; ++i) {
+    p.klo[i] = k->f16.lo[i], p.khi[i] = k->f16.hi[i];
+    p.vlo[i] = v->f16.lo[i], p.vhi[i] = v->f16.hi[i];
+  }
+  p.split = reinterpret_cast<float *>(base + l.split);
+  p.whole = reinterpret_cast<float *>(base + l.whole);
+  p.unit = reinterpret_cast<int32_t *>(base + l.unit);
+  if (l.parts == 1)
+    e = l.R == 32 ? launch_partial<32, 1>(p, l.grid, st)
+                  : (l.R == 64 ? launch_partial<64, 1>(p, l.grid, st) : launch_partial<128, 1>(p, l.grid, st));
+  else
+    e = l.R == 32 ? launch_partial<32, 2>(p, l.grid, st) : launch_partial<64, 2>(p, l.grid, st);
+  if (e != cudaSuccess) return e;
+  CombineParams c{};
+  c.v = tv, c.o = o, c.Hq = Hq, c.R = l.R, c.grid = l.grid;
+  c.inv_vscale = 1.0f / (exp2f(P_SHIFT - W_SHIFT) * v->f16.alpha);
+  c.vfrag = v->d_rfrag;
+  c.split = p.split, c.whole = p.whole, c.unit = p.unit;
+  int blocks = 1;
+  if ((e = kernel_occupancy((const void *)k_tree_combine, CB_WARPS * 32, 0, &blocks)) != cudaSuccess) return e;
+  const int64_t want = ((int64_t)pv.n_tokens * Hq + 7) / 8, most = (int64_t)k->num_sms * blocks;
+  return launch_pdl(k_tree_combine, dim3((unsigned)(want < most ? want : most)), dim3(CB_WARPS * 32), 0, st, c);
 }
 
 }  // namespace tq

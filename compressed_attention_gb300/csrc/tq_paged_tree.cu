@@ -15,14 +15,17 @@
 //                   empty tiles that stand for its start) and are shared out evenly, as in the paged decode.
 //                   Specialised warps:
 //                     loader      packed tiles, one bulk copy per page and side, on rings; q's images
-//                     K decoders  nibbles -> fp16 centroids (byte permutes) in tensor memory, a key per lane:
-//                                 the A operand of S^T, without a trip through shared memory
-//                     V decoders  the same into 128-byte swizzled tiles, the MN-major A operand of O^T
+//                     K decoders  nibble pairs -> fp16 centroid pairs through a table in shared memory (a column of
+//                                 it per lane: no bank conflicts) into tensor memory, a key per lane: the A
+//                                 operand of S^T
+//                     V decoders  nibbles -> fp16 centroids (byte permutes) into 128-byte swizzled tiles, the
+//                                 MN-major A operand of O^T.  (Tables for both would fill the shared-memory
+//                                 path, permutes for both the ALU, which takes one every other cycle.)
 //                     issuer      one thread
-//                     softmax     two groups of four warps, each half of the columns: S^T from tensor
-//                                 memory, weights against the columns' running maxima, P as the MN-major
-//                                 B operand in shared memory.  A maximum is raised (and O rescaled)
-//                                 only when a weight would leave the operand's range: one vote a tile.
+//                     softmax     two groups of four warps on alternate key tiles, each with its own O^T: S^T from
+//                                 tensor memory, weights against the columns' running maxima, P as the
+//                                 MN-major B operand in shared memory.  A maximum is raised (and O
+//                                 rescaled) only when a weight would leave the operand's range: one vote a tile.
 //   k_tree_combine  the log-sum-exp merge of a column's shares, R^T o on the tensor cores, rounding.
 //
 // Parts: for bf16 outputs q and P enter as one fp16 each; for fp16 and fp32 outputs as hi + lo, the lo parts as
@@ -42,27 +45,29 @@ constexpr int KT = 128;          // keys per tile
 constexpr int ITEM_TILES = 3;    // cost of an item ahead of its tiles, in tiles
 constexpr int RAW = KT * PG_ROW; // a packed tile
 constexpr int PROW = D + 4;      // floats of a partial: acc[128], max (less W_SHIFT), sum, 2 spare
-constexpr int W_KDEC = 8, W_VDEC = 12, W_MMA = 16, W_LOAD = 17, W_Q = 18, THREADS = 640;
-constexpr int REGS_LAUNCH = 96;
+constexpr int W_KDEC = 8, W_VDEC = 16, W_PV = 24, W_LOAD = 25, W_S = 27, THREADS = 896;  // (W_LOAD: keys, then values)
+constexpr int NITEM = 4;         // items known ahead
+constexpr int REGS_LAUNCH = 72, REGS_SOFTMAX = 128, REGS_OTHER = 48;
+static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "the launch's registers");
 
 // R columns of a unit, PARTS fp16 parts of q and P.
 template <int R_, int PARTS_>
 struct Cfg {
   static constexpr int R = R_, PARTS = PARTS_;
   static constexpr int N = R * PARTS < 64 ? 64 : R * PARTS;  // columns of P and O (whole 128-byte rows)
-  static constexpr int C = R / 2;                            // columns of a softmax group
-  static constexpr int CH = C < 32 ? C : 32;                 // at a time
-  static constexpr int NRAW = R * PARTS == 128 ? 3 : 4;
-  static constexpr uint32_t TM_S = 0, TM_O = 2 * R, TM_K = TM_O + N;
+  static constexpr int CH = 32;                              // columns a thread takes at a time
+  static constexpr bool LUT = R * PARTS <= 64;               // K by table (32 KB), where shared memory holds it
+  static constexpr int NRAW = 3;
+  static constexpr int NS = R * PARTS == 128 ? 2 : 4;        // buffers of S
+  static constexpr uint32_t TM_S = 0, TM_O = NS * R, TM_K = TM_O + 2 * N;
   static_assert(TM_K + 2 * 64 <= 512, "tensor memory");
+  static constexpr int NKN = NS + 4;                         // tiles whose norms are kept (at least NS + 2)
   static constexpr uint32_t Q_HALF = R * PARTS * 128, Q_BYTES = 2 * Q_HALF, P_BYTES = (N / 64) * SW_HALF_BYTES;
   static constexpr uint32_t OFF_V = 0, OFF_P = 2 * SW_TILE_BYTES, OFF_Q = OFF_P + 2 * P_BYTES;
-  static constexpr uint32_t OFF_RAW = OFF_Q + Q_BYTES, OFF_MISC = OFF_RAW + 2 * NRAW * RAW;
+  static constexpr uint32_t OFF_LUT = OFF_Q + Q_BYTES, OFF_RAW = OFF_LUT + (LUT ? 256 * 128 : 0);
+  static constexpr uint32_t OFF_MISC = OFF_RAW + 2 * NRAW * RAW;
   static constexpr uint32_t IDESC_S = (1u << 4) | (uint32_t(R >> 3) << 17) | ((128u >> 4) << 24);
   static constexpr uint32_t IDESC_PV = (1u << 4) | (1u << 15) | (1u << 16) | (uint32_t(N >> 3) << 17) | ((128u >> 4) << 24);
-  // Registers: the softmax groups hold a sum per column and 32 scores.
-  static constexpr int REGS_SOFTMAX = R == 128 ? 144 : 128, REGS_OTHER = R == 128 ? 64 : 72;
-  static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "the launch's registers");
 };
 
 struct TreeView {
@@ -213,6 +218,7 @@ __device__ __forceinline__ void see_bits(const PrepParams &p, int b, int qt, int
   int node = 0, h = 0;
 #pragma unroll
   for (int o = 0; o < 4; ++o) {
+#pragma unroll 1
     for (int bit = 0; bit < 32 && 32 * o + bit < p.R; ++bit) {
       const uint32_t w0 = node < 64 ? (node < 32 ? word[0] : word[1]) : (node < 96 ? word[2] : word[3]);
       const uint32_t w = __shfl_sync(FULL_MASK, w0, node & 31);  // (node is the same in every lane)
@@ -275,22 +281,25 @@ __global__ void __launch_bounds__(PREP_WARPS * 32) k_tree_prep(const PrepParams 
 #pragma unroll 1
     for (int rb = 0; rb < 16; rb += NR) {  // eight rows' loads in flight
       float x[NR][4];
+      {
+        uint4 raw[NR];
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const uint8_t *src = reinterpret_cast<const uint8_t *>((uintptr_t)__shfl_sync(FULL_MASK, my_src, rb + i));
-        if (src) load_lane4(src, p.q.dtype, lane, x[i]);
-        else x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+        for (int i = 0; i < NR; ++i) {
+          const uint8_t *src = reinterpret_cast<const uint8_t *>((uintptr_t)__shfl_sync(FULL_MASK, my_src, rb + i));
+          raw[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (src) raw[i] = load_lane4_raw(src, p.q.dtype, lane);
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) lane4_floats(raw[i], p.q.dtype, x[i]);
       }
       if (p.rope.rot_dim) {
-        const int turn = __shfl_sync(FULL_MASK, my_turn, rb);
-        if (__all_sync(FULL_MASK, my_turn == turn || (lane & 8) != rb || lane >= 16)) {  // one node's heads
-          const LaneAngles an = rope_angles(lane, p.rope, turn);
+        int turn = -1;
+        LaneAngles an;
 #pragma unroll
-          for (int i = 0; i < NR; ++i) rope_turn(x[i], lane, p.rope, an);
-        } else {
-#pragma unroll
-          for (int i = 0; i < NR; ++i)
-            rope_turn(x[i], lane, p.rope, rope_angles(lane, p.rope, __shfl_sync(FULL_MASK, my_turn, rb + i)));
+        for (int i = 0; i < NR; ++i) {
+          const int mine = __shfl_sync(FULL_MASK, my_turn, rb + i);
+          if (mine != turn) an = rope_angles(lane, p.rope, turn = mine);  // (a node's heads share theirs)
+          rope_turn(x[i], lane, p.rope, an);
         }
       }
 #pragma unroll
@@ -351,8 +360,10 @@ __global__ void __launch_bounds__(PREP_WARPS * 32) k_tree_prep(const PrepParams 
       }
       m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, 1));
       m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, 2));
-      // the power of two that brings the largest element to [2^13, 2^14)
-      const int e = scale_exp(m), row = c0 + g + 8 * i;
+      // The power of two that brings the largest element to [2^13, 2^14); none for rows of ordinary size, of
+      // which fp16 drops what is below 2^-14 of the largest element, and two parts what is below 2^-20 of it.
+      const bool as_is = m >= (p.parts == 2 ? 0x1p-4f : 0x1p-10f) && m < 0x1p14f;
+      const int e = as_is ? 0 : scale_exp(m), row = c0 + g + 8 * i;
       const float down = pow2i(-e);
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
@@ -377,27 +388,32 @@ struct PartialParams {
   const uint8_t *qh;
   const float *qsc;
   const uint4 *sees;
+  uint32_t kc16[8];  // the keys' fp16 centroids
   uint32_t klo[2], khi[2], vlo[2], vhi[2];
   float *split;   // [CTA][2][R] partials of units that several CTAs share
   float *whole;   // [row][Hq] partials of units one CTA finished
   int32_t *unit;  // per unit: first CTA | CTAs << 16
 };
 
+template <int NKN>
 struct Misc {
-  uint64_t raw_full[2][4], raw_empty[2][4];  // [side][stage]
+  uint64_t raw_full[2][3], raw_empty[2][3];  // [side][stage]
   uint64_t k_full[2], k_empty[2], v_full[2];
-  uint64_t s_done[2], p_ready[2], pv_done[2];  // a P buffer and a V stage are free once their product is done
-  uint64_t q_full, q_empty, o_free, drain;
-  // Key norms of the last four K tiles: a K stage is free once its product is done, while the softmax still
-  // needs the norms; the decoders reach tile j + 4 only after every group has finished tile j.
-  float kn[4][KT], nv[2][KT];
-  float4 qm[64];          // columns 2i, 2i + 1: scales of q, minus the running maxima (less W_SHIFT; none yet: 0)
-  float4 move[64];        // and, where maxima are raised: what the scores fall by, the square root of O's factor
-  float mx[128];          // the running maxima, -infinity without one
-  float red[2][4][64];    // [group][warp][column of the group]
+  uint64_t s_done[4], s_free[4];      // [buffer]
+  uint64_t p_ready[2], pv_done[2];    // [group]: a P buffer and a V stage are free once their product is done
+  uint64_t q_full, q_empty, o_free, drain[2];
+  // Norms of the last tiles, both written by the K decoders, so that the softmax waits for no values: a K stage is
+  // free once its product is done, while the softmax still X
+  float kn[NKN][KT], nv[NKN][KT];
+  alignas(16) float nm[2][64], qs[2][64];  // [group] minus the running maxima (less W_SHIFT; none yet: 0), scales of q
+  float4 move[2][32];     // and, where maxima are raised: what the scores fall by, the square root of O's factor
+  float mx[2][64];        // the running maxima, -infinity without one
+  float red[2][4][64];    // [group][warp][column]
+  float4 end[64];         // per column at the item's end: factors of the groups' O^T, place of the partial (two words)
   uint32_t tmem;
   int abort_flag;
-  Walk walk;
+  uint64_t item_full[NITEM], item_empty[NITEM];
+  Item item[NITEM];       // found by the keys' loader, one without tiles at the end
   int V, G;
 };
 
@@ -432,9 +448,19 @@ __device__ __forceinline__ bool group_or(int gr, bool x) {
   return r != 0;
 }
 
-// CH consecutive columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&x)[32]) { tmem_ld32(taddr, x); }
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&x)[16]) {
+// Barrier of both softmax groups that ORs a flag across them.
+__device__ __forceinline__ bool both_or(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " bar.red.or.pred q, 3, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+// 16 consecutive columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&x)[16]) {
   uint32_t r[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -445,91 +471,138 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&x)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&x)[32]) { tmem_st32(taddr, x); }
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&x)[16]) {
-  uint32_t r[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(x[i]);
+__device__ __forceinline__ void tmem_st16_start(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&x)[16]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(x[i]);
+  tmem_st16_start(taddr, r);
+  tmem_st_wait();
+}
+// The larger of three, and of a warp's (NaN counts as none).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void acc2(uint64_t &a, uint64_t b) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b)); }
 
 template <int R, int PARTS>
 __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams p) {
   using F = Cfg<R, PARTS>;
-  constexpr int C = F::C, CH = F::CH, NRAW = F::NRAW;
+  constexpr int CH = F::CH, NRAW = F::NRAW, NS = F::NS, NKN = F::NKN;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
-  Misc &ms = *reinterpret_cast<Misc *>(smem + F::OFF_MISC);
+  Misc<NKN> &ms = *reinterpret_cast<Misc<NKN> *>(smem + F::OFF_MISC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   if (warp == 0) tmem_alloc(smem_addr(&ms.tmem), 512);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      for (int i = 0; i < NRAW; ++i) mbar_init(&ms.raw_full[s][i], 1), mbar_init(&ms.raw_empty[s][i], 4);
+      for (int i = 0; i < NRAW; ++i) mbar_init(&ms.raw_full[s][i], 1), mbar_init(&ms.raw_empty[s][i], s ? 8 : 4);
       mbar_init(&ms.k_full[s], 4), mbar_init(&ms.v_full[s], 4);
-      mbar_init(&ms.k_empty[s], 1), mbar_init(&ms.s_done[s], 1), mbar_init(&ms.pv_done[s], 1);
-      mbar_init(&ms.p_ready[s], 8);
+      mbar_init(&ms.k_empty[s], 1), mbar_init(&ms.pv_done[s], 1);
+      mbar_init(&ms.p_ready[s], 4);
     }
-    mbar_init(&ms.q_full, 1), mbar_init(&ms.q_empty, 1), mbar_init(&ms.o_free, 8), mbar_init(&ms.drain, 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&ms.s_done[i], 1), mbar_init(&ms.s_free[i], 4);
+    mbar_init(&ms.q_full, 1), mbar_init(&ms.q_empty, 1), mbar_init(&ms.o_free, 8);
+    mbar_init(&ms.drain[0], 1), mbar_init(&ms.drain[1], 1);
+    for (int i = 0; i < NITEM; ++i) mbar_init(&ms.item_full[i], 1), mbar_init(&ms.item_empty[i], THREADS / 32 - 1);
     ms.abort_flag = 0;
     fence_mbar_init();
   }
-  pdl_wait();
-  if (warp == W_LOAD) {
-    Walk w;
-    int V, G;
-    find_share(p.v, lane, w, V, G);
-    if (lane == 0) ms.walk = w, ms.V = V, ms.G = G;
+  if (F::LUT) {  // entry b: the centroids of nibbles b & 15, b >> 4, once per lane
+    for (int i = tid; i < 256 * 8; i += THREADS) {
+      const int b = i >> 3;
+      const uint32_t lo = (p.kc16[(b & 15) >> 1] >> (16 * (b & 1))) & 0xFFFFu;
+      const uint32_t hi = (p.kc16[b >> 5] >> (16 * ((b >> 4) & 1))) & 0xFFFFu, e = lo | (hi << 16);
+      reinterpret_cast<uint4 *>(smem + F::OFF_LUT)[i] = make_uint4(e, e, e, e);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
   const uint32_t tmem = ms.tmem;
-  // Bounded wait; fails at once when another thread has given up already.
+  // Bounded wait, in few instructions (they are on every role's path); fails when another thread has given up.
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-    if (*reinterpret_cast<volatile int *>(&ms.abort_flag)) return false;
-    const bool done = mbar_wait_bounded(bar, parity, WAIT_LIMIT_NS);
-    if (!done) {
-      atomicExch(&ms.abort_flag, 1);
-      atomicExch(p.v.pv.status, (int32_t)DEVERR_TIMEOUT);
+    uint64_t t0 = 0;
+    while (!mbar_try_wait(bar, parity)) {
+      const uint64_t t = global_timer_ns();
+      if (!t0) t0 = t;
+      if (t - t0 > WAIT_LIMIT_NS) {
+        atomicExch(&ms.abort_flag, 1);
+        atomicExch(p.v.pv.status, (int32_t)DEVERR_TIMEOUT);
+      }
+      if (*reinterpret_cast<volatile int *>(&ms.abort_flag)) return false;
     }
-    return done;
+    return true;
   };
-  Walk w = ms.walk;
   Item it;
   bool ok = true;
-
+  uint32_t n_items = 0;
+  auto next = [&]() -> bool {  // the next item, as the keys' loader found it
+    const uint32_t i = n_items % NITEM;
+    if (!__all_sync(FULL_MASK, wait(&ms.item_full[i], (n_items / NITEM) & 1))) return ok = false;
+    it = ms.item[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ms.item_empty[i]);
+    ++n_items;
+    return it.t1 > it.t0;
+  };
   if (warp >= W_KDEC) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F::REGS_OTHER));
-    if (warp == W_LOAD) {
-      // ================ loader: lanes 0-7 the keys' pages, 16-23 the values'
-      const int psh = p.v.pv.page_shift, P = 1 << psh, side = lane >> 4, seg = lane & 15;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+    if (warp == W_LOAD || warp == W_LOAD + 1) {
+      // ================ loaders: a warp for the keys, one for the values; a lane per page of a tile
+      const int psh = p.v.pv.page_shift, P = 1 << psh, side = warp - W_LOAD;
       const uint8_t *pages = side ? p.vp : p.kp;
+      Walk w;
+      if (!side) {
+        int V, G;
+        find_share(p.v, lane, w, V, G);
+        if (lane == 0) ms.V = V, ms.G = G;
+      }
+      auto publish = [&]() -> bool {  // the keys' loader walks its share for all
+        const uint32_t i = n_items % NITEM;
+        if (!next_item(p.v, w, it)) it.t0 = it.t1 = 0;
+        if (n_items >= NITEM && !__all_sync(FULL_MASK, wait(&ms.item_empty[i], ((n_items / NITEM) - 1) & 1))) return ok = false;
+        if (lane == 0) {
+          ms.item[i] = it;
+          mbar_arrive(&ms.item_full[i]);
+        }
+        __syncwarp();
+        ++n_items;
+        return it.t1 > it.t0;
+      };
       uint32_t n = 0;  // tiles loaded
-      while (ok && next_item(p.v, w, it)) {
+      while (ok && (side ? next() : publish())) {
         auto page_of = [&](int j) -> int {
-          const int pi = ((j * KT) >> psh) + seg;
-          if (j >= it.t1 || seg >= 8 || (pi << psh) >= min((j + 1) * KT, it.s.len)) return -1;
+          const int pi = ((j * KT) >> psh) + lane;
+          if (j >= it.t1 || lane >= 8 || (pi << psh) >= min((j + 1) * KT, it.s.len)) return -1;
           return max(paged_page(p.v.pv, it.b, pi << psh, !side), 0);
         };
         int pg = page_of(it.t0);
         for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
           const int kf = j * KT, nk4 = (min(KT, it.s.len - kf) + 3) & ~3, s = n % NRAW;
           const int pg_next = page_of(j + 1);
-          if (n >= NRAW) {
-            ok = wait(&ms.raw_empty[0][s], ((n / NRAW) - 1) & 1) && wait(&ms.raw_empty[1][s], ((n / NRAW) - 1) & 1);
-            if (!(ok = __all_sync(FULL_MASK, ok))) break;
-          }
+          if (n >= NRAW && !(ok = __all_sync(FULL_MASK, wait(&ms.raw_empty[side][s], ((n / NRAW) - 1) & 1)))) break;
           // rows of a tile rounded up to four (16-byte copies; they stay inside the page)
-          if (seg == 0) mbar_arrive_expect_tx(&ms.raw_full[side][s], nk4 * PG_ROW);
+          if (lane == 0) mbar_arrive_expect_tx(&ms.raw_full[side][s], nk4 * PG_ROW);
           __syncwarp();
           if (pg >= 0) {
-            const int k0 = max((((kf >> psh) + seg) << psh), kf), k1 = min(((k0 >> psh) + 1) << psh, kf + nk4);
+            const int k0 = max((((kf >> psh) + lane) << psh), kf), k1 = min(((k0 >> psh) + 1) << psh, kf + nk4);
             bulk_g2s(smem + F::OFF_RAW + (2 * s + side) * RAW + (k0 - kf) * PG_ROW,
                      pages + paged_row(p.v.pv, pg, it.h, k0 & (P - 1)), (uint32_t)(k1 - k0) * PG_ROW, &ms.raw_full[side][s]);
           }
@@ -539,330 +612,407 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
       // after a failed wait: let the copies in flight land before the CTA ends
       if (*reinterpret_cast<volatile int *>(&ms.abort_flag))
         for (uint32_t c = n > NRAW ? n - NRAW : 0; c < n; ++c)
-          for (int s = 0; s < 2; ++s) (void)mbar_wait_bounded(&ms.raw_full[s][c % NRAW], (c / NRAW) & 1, WAIT_LIMIT_NS);
-    } else if (warp == W_Q) {
-      // ================ q's image, as soon as the last item's scores are done
+          (void)mbar_wait_bounded(&ms.raw_full[side][c % NRAW], (c / NRAW) & 1, WAIT_LIMIT_NS);
+    } else if (warp < W_PV) {
+      // ================ decoders: two groups of four warps for the keys, two for the values, on alternate tiles;
+      // thread = key of the tile
+      const int row = tid & 127;
+      const bool side = warp >= W_VDEC;
+      const int st = (warp >> 2) & 1;  // the group, and its stage
+      uint32_t lo2[2], hi2[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) lo2[i] = side ? p.vlo[i] : p.klo[i], hi2[i] = side ? p.vhi[i] : p.khi[i];
+      const uint32_t tK = tmem + ((uint32_t)((warp & 3) * 32) << 16) + F::TM_K;
+      const uint32_t to_v = smem_addr(smem + F::OFF_V) + row * 128 + 16 * (row & 7);  // chunk 0 of the row
       uint32_t n = 0;
-      while (ok && next_item(p.v, w, it)) {
-        if (n) ok = __all_sync(FULL_MASK, wait(&ms.q_empty, (n - 1) & 1));
+      while (ok && next()) {
+        for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
+          if ((n & 1) != (uint32_t)st) continue;
+          const int rs = n % NRAW;
+          if (n >= 2) ok = wait(side ? &ms.pv_done[st] : &ms.k_empty[st], ((n >> 1) - 1) & 1);
+          if (ok) ok = wait(&ms.raw_full[side][rs], (n / NRAW) & 1);
+          if (!(ok = __all_sync(FULL_MASK, ok))) break;
+          const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + F::OFF_RAW + (2 * rs + side) * RAW + row * PG_ROW);
+          // Short loops (the warps of an SM run six different ones), the next words loaded ahead of the stores of these.
+          if (side) {
+            const uint32_t to = to_v + st * SW_TILE_BYTES;
+            uint32_t word[4], next[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) word[i] = src[1 + i];
+#pragma unroll 1
+            for (int q4 = 0; q4 < 4; ++q4) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) next[i] = src[1 + 4 * min(q4 + 1, 3) + i];
+              // chunk 4 (q4 % 2) + i of half q4 / 2, at its place ^ (row % 8)
+              const uint32_t at = (to + (q4 >> 1) * SW_HALF_BYTES) ^ (64u * (q4 & 1));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t d[4];
+                decode8<0x5140u, 0x7362u>(word[i], lo2, hi2, d);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (16u * i)), "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]) : "memory");
+                word[i] = next[i];
+              }
+            }
+            fence_async_smem();
+          } else {
+            tc_fence_after();  // the product that read the stage
+            const uint32_t lut = smem_addr(smem + F::OFF_LUT) + 4 * lane;
+#pragma unroll 1
+            for (int q2 = 0; q2 < 4; ++q2) {
+              uint32_t d[16];
+#pragma unroll
+              for (int ch = 0; ch < 4; ++ch) {
+                uint32_t x[4];
+                const uint32_t word = src[1 + 4 * q2 + ch];
+                if constexpr (F::LUT) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[e]) : "r"(lut + 128u * prmt(word, 0u, 0x4440u + e)));
+                } else {
+                  decode8<0x5140u, 0x7362u>(word, lo2, hi2, x);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[4 * ch + e] = x[e];
+              }
+              tmem_st16_start(tK + 64 * st + 16 * q2, d);
+            }
+            tmem_st_wait();
+            const bool live = j * KT + row < it.s.len;
+            ms.kn[n % NKN][row] = live ? __uint_as_float(src[0]) : 0.f;
+            ok = __all_sync(FULL_MASK, wait(&ms.raw_full[1][rs], (n / NRAW) & 1));
+            if (!ok) break;
+            ms.nv[n % NKN][row] = live ? __uint_as_float(src[RAW / 4]) : 0.f;  // (the values' tile lies behind the keys')
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(side ? &ms.v_full[st] : &ms.k_full[st]), mbar_arrive(&ms.raw_empty[side][rs]);
+            if (!side) mbar_arrive(&ms.raw_empty[1][rs]);
+          }
+        }
+      }
+    } else if (warp == W_S) {
+      // ================ issuer of the scores, as far ahead as their buffers go; q's image once the last item's are done
+      const bool lead = elect_lane();
+      const uint32_t tb = __shfl_sync(FULL_MASK, tmem, 0), tS = tb + F::TM_S, tK = tb + F::TM_K;
+      const uint64_t dq = sw128_desc(smem_addr(smem + F::OFF_Q));
+      uint32_t n = 0, items = 0;
+      bool issued = false, q_ok = true;
+      while (ok && next()) {
+        if (items) ok = __all_sync(FULL_MASK, wait(&ms.q_empty, (items - 1) & 1));
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&ms.q_full, F::Q_BYTES);
           bulk_g2s(smem + F::OFF_Q, p.qh + (size_t)unit_index(p.v, it.b, it.h, it.qt) * F::Q_BYTES, F::Q_BYTES, &ms.q_full);
         }
         __syncwarp();
-        ++n;
-      }
-      if (n && *reinterpret_cast<volatile int *>(&ms.abort_flag)) (void)mbar_wait_bounded(&ms.q_full, (n - 1) & 1, WAIT_LIMIT_NS);
-    } else if (warp < W_MMA) {
-      // ================ decoders: a warp group for the keys, one for the values, thread = key of the tile
-      const int row = tid & 127;
-      const bool side = warp >= W_VDEC;
-      uint32_t lo2[2], hi2[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) lo2[i] = side ? p.vlo[i] : p.klo[i], hi2[i] = side ? p.vhi[i] : p.khi[i];
-      const uint32_t tK = tmem + ((uint32_t)((warp & 3) * 32) << 16) + F::TM_K;
-      uint32_t n = 0;
-      while (ok && next_item(p.v, w, it)) {
+        q_ok = ok = __all_sync(FULL_MASK, wait(&ms.q_full, items & 1));
         for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
-          const int st = n & 1, rs = n % NRAW;
-          if (n >= 2) ok = wait(side ? &ms.pv_done[st] : &ms.k_empty[st], ((n >> 1) - 1) & 1);
-          if (ok) ok = wait(&ms.raw_full[side][rs], (n / NRAW) & 1);
+          const uint32_t st = n & 1, sb = n % NS;
+          if (n >= NS) ok = wait(&ms.s_free[sb], ((n / NS) - 1) & 1);
+          if (ok) ok = wait(&ms.k_full[st], (n >> 1) & 1);
           if (!(ok = __all_sync(FULL_MASK, ok))) break;
-          const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + F::OFF_RAW + (2 * rs + side) * RAW + row * PG_ROW);
-          const float norm = j * KT + row < it.s.len ? __uint_as_float(src[0]) : 0.f;
-          if (side) {
-            uint8_t *dst = smem + F::OFF_V + st * SW_TILE_BYTES;
-#pragma unroll
-            for (int ch = 0; ch < 16; ++ch) {
-              uint32_t d[4];
-              decode8<0x5140u, 0x7362u>(src[1 + ch], lo2, hi2, d);
-              *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 8 * ch)) = make_uint4(d[0], d[1], d[2], d[3]);
-            }
-            ms.nv[st][row] = norm;
-            fence_async_smem();
-          } else {
-            tc_fence_after();  // the product that read the stage
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t d[32];
-#pragma unroll
-              for (int ch = 0; ch < 8; ++ch) {
-                uint32_t x[4];
-                decode8<0x5140u, 0x7362u>(src[1 + 8 * half + ch], lo2, hi2, x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) d[4 * ch + e] = x[e];
-              }
-              tmem_st32(tK + 64 * st + 32 * half, d);
-            }
-            ms.kn[n & 3][row] = norm;
-            tc_fence_before();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(side ? &ms.v_full[st] : &ms.k_full[st]), mbar_arrive(&ms.raw_empty[side][rs]);
-        }
-      }
-    } else if (warp == W_MMA) {
-      // ================ issuer
-      const bool lead = elect_lane();
-      const uint32_t tb = __shfl_sync(FULL_MASK, tmem, 0), tS = tb + F::TM_S, tO = tb + F::TM_O, tK = tb + F::TM_K;
-      const uint64_t dq = sw128_desc(smem_addr(smem + F::OFF_Q));
-      const uint64_t dv = sw128_mn_desc(smem_addr(smem + F::OFF_V)), dp = sw128_mn_desc(smem_addr(smem + F::OFF_P));
-      uint32_t n = 0, items = 0;  // tiles and items before this one
-      bool issued = false;
-      while (ok && next_item(p.v, w, it)) {
-        const uint32_t tiles = it.t1 - it.t0;
-        if (!(ok = __all_sync(FULL_MASK, wait(&ms.q_full, items & 1)))) break;
-        // S^T of the item's tile m: its buffer was read before the P of two tiles ago was ready
-        auto issue_s = [&](uint32_t m) -> bool {
-          const uint32_t c = n + m, st = c & 1;
-          if (!__all_sync(FULL_MASK, wait(&ms.k_full[st], (c >> 1) & 1))) return false;
           tc_fence_after();
           if (lead) {
 #pragma unroll
             for (int part = 0; part < PARTS; ++part)
 #pragma unroll
               for (int s = 0; s < 8; ++s)
-                umma_ts<F::IDESC_S>(tS + R * st, tK + 64 * st + 8 * s,
+                umma_ts<F::IDESC_S>(tS + R * sb, tK + 64 * st + 8 * s,
                                     desc_step(dq, (s >> 2) * F::Q_HALF + part * R * 128 + (s & 3) * 32), (part || s) ? 1u : 0u);
-            umma_commit(&ms.s_done[st]);
+            umma_commit(&ms.s_done[sb]);
             umma_commit(&ms.k_empty[st]);
-            if (m == tiles - 1) umma_commit(&ms.q_empty);
+            if (j == it.t1 - 1) umma_commit(&ms.q_empty);
           }
           __syncwarp();
           issued = true;
-          return true;
-        };
-        for (uint32_t m = 0; ok && m < 2 && m < tiles; ++m) ok = issue_s(m);
-        for (uint32_t m = 0; ok && m < tiles; ++m) {
-          const uint32_t c = n + m, st = c & 1;
-          ok = wait(&ms.p_ready[st], (c >> 1) & 1);
-          if (ok) ok = wait(&ms.v_full[st], (c >> 1) & 1);
-          if (ok && m == 0 && items) ok = wait(&ms.o_free, (items - 1) & 1);
+        }
+        ++items;
+      }
+      // after a failed wait: the copy of q and the products in flight end before the CTA does
+      if (*reinterpret_cast<volatile int *>(&ms.abort_flag)) {
+        if (!q_ok) (void)mbar_wait_bounded(&ms.q_full, items & 1, WAIT_LIMIT_NS);
+        if (issued && lead) umma_commit(&ms.drain[0]), (void)mbar_wait_bounded(&ms.drain[0], 0, WAIT_LIMIT_NS);
+      }
+    } else if (warp == W_PV) {
+      // ================ issuer of O^T
+      const bool lead = elect_lane();
+      const uint32_t tO = __shfl_sync(FULL_MASK, tmem, 0) + F::TM_O;
+      const uint64_t dv = sw128_mn_desc(smem_addr(smem + F::OFF_V)), dp = sw128_mn_desc(smem_addr(smem + F::OFF_P));
+      uint32_t n = 0, items = 0;
+      bool issued = false;
+      while (ok && next()) {
+        for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
+          const uint32_t st = n & 1;
+          ok = wait(&ms.p_ready[st], (n >> 1) & 1);
+          if (ok) ok = wait(&ms.v_full[st], (n >> 1) & 1);
+          if (ok && j == it.t0 && items) ok = wait(&ms.o_free, (items - 1) & 1);
           if (!(ok = __all_sync(FULL_MASK, ok))) break;
           tc_fence_after();
           if (lead) {
             const uint64_t a = desc_step(dv, st * SW_TILE_BYTES), b = desc_step(dp, st * F::P_BYTES);
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-              umma<F::IDESC_PV>(tO, desc_step(a, 2048 * s), desc_step(b, 2048 * s), (m || s) ? 1u : 0u);
+            for (int s = 0; s < 8; ++s)  // (each group's first tile of the item starts its accumulator)
+              umma<F::IDESC_PV>(tO + F::N * st, desc_step(a, 2048 * s), desc_step(b, 2048 * s), (j >= it.t0 + 2 || s) ? 1u : 0u);
             umma_commit(&ms.pv_done[st]);
           }
           __syncwarp();
-          if (m + 2 < tiles) ok = issue_s(m + 2);
+          issued = true;
         }
-        n += tiles, ++items;
+        ++items;
       }
-      if (issued && lead && *reinterpret_cast<volatile int *>(&ms.abort_flag)) {
-        umma_commit(&ms.drain);
-        (void)mbar_wait_bounded(&ms.drain, 0, WAIT_LIMIT_NS);
-      }
+      if (issued && lead && *reinterpret_cast<volatile int *>(&ms.abort_flag))
+        umma_commit(&ms.drain[1]), (void)mbar_wait_bounded(&ms.drain[1], 0, WAIT_LIMIT_NS);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F::REGS_SOFTMAX));
-    // ================ softmax: group gr takes columns gr C .. + C, thread = key
-    const int gr = warp >> 2, key = tid & 127, wq = warp & 3, col0 = gr * C;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+    // ================ softmax: group gr takes the tiles n with n % 2 == gr, thread = key
+    const int gr = warp >> 2, key = tid & 127, wq = warp & 3;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS = tmem + lane_off + F::TM_S + col0, tO = tmem + lane_off + F::TM_O + col0;
-    uint32_t n = 0;
-    while (next_item(p.v, w, it)) {
+    const uint32_t tS = tmem + lane_off + F::TM_S, tO = tmem + lane_off + F::TM_O + F::N * gr;
+    float *const nm = ms.nm[gr];
+    float4 *const mv = ms.move[gr];
+    uint32_t n = 0;  // tiles before the item
+    while (next()) {
       const int unit = unit_index(p.v, it.b, it.h, it.qt), n0 = it.qt * p.v.npu;
       const int cols = min(it.s.T - n0, p.v.npu) * p.v.gq;  // columns with a node
-      // the group's columns: no maximum yet; those without a node keep 0
-      if (key < C) {
-        const int c = col0 + key;
-        const float sc = p.qsc[(size_t)unit * R + c];
-        float *qm = reinterpret_cast<float *>(&ms.qm[c >> 1]);
-        qm[c & 1] = sc, qm[2 + (c & 1)] = 0.f;
-        ms.mx[c] = sc == 0.f ? 0.f : -INFINITY;
+      // no column has a maximum yet; those without a node keep 0
+      bool scale = false;
+      if (key < R) {
+        const float sc = p.qsc[(size_t)unit * R + key];
+        ms.qs[gr][key] = sc, nm[key] = 0.f;
+        ms.mx[gr][key] = sc == 0.f ? 0.f : -INFINITY;
+        scale = sc != 0.f && sc != 1.f;
       }
       bool fresh = true;  // some column has no maximum yet
-      uint64_t l2[C / 2];
+      uint64_t l2[R / 2];
 #pragma unroll
-      for (int i = 0; i < C / 2; ++i) l2[i] = 0;
-      (void)group_or(gr, false);
+      for (int i = 0; i < R / 2; ++i) l2[i] = 0;
+      const bool scaled = group_or(gr, scale);  // some column's q is held times a power of two
       const int tiles = it.t1 - it.t0;
-      for (int m = 0; m < tiles; ++m, ++n) {
-        const int st = n & 1, t = (it.t0 + m) * KT + key, j = t - it.s.base;
-        ok = wait(&ms.s_done[st], (n >> 1) & 1);
-        if (ok) ok = wait(&ms.v_full[st], (n >> 1) & 1);
-        if (ok && n >= 2) ok = wait(&ms.pv_done[st], ((n >> 1) - 1) & 1);  // the P buffer is free
+      const int first_m = (n & 1) == (uint32_t)gr ? 0 : 1;
+      bool held = false;  // O^T holds something of the item
+      for (int m = first_m; m < tiles; m += 2) {
+        const uint32_t c = n + m, sb = c % NS;
+        const int t = (it.t0 + m) * KT + key, j = t - it.s.base;
+        ok = wait(&ms.s_done[sb], (c / NS) & 1);
+        if (ok && c >= 2) ok = wait(&ms.pv_done[gr], ((c >> 1) - 1) & 1);  // the P buffer is free, O^T whole
         ok = __all_sync(FULL_MASK, ok);
         tc_fence_after();
-        const float kn = ms.kn[n & 3][key], nv = ms.nv[st][key];
-        const uint64_t kn2 = pk2(kn, kn);
-        const float lv = fmaxf(log2_approx(nv), -64.f), nvf = nv * NORM_FACTOR;
-        // a score past this leaves the operand's range (2^15), or a weight passes W_MOST
+        const float kn = ms.kn[c % NKN][key], nv = ms.nv[c % NKN][key], nvf = nv * NORM_FACTOR;
+        const uint64_t kn2 = pk2(kn, kn), nvf2 = pk2(nvf, nvf);
+        // a score past this leaves the operand's range (2^15), or its weight passes W_MOST
         const float most = fminf(15.f - log2_approx(nvf), 96.f);
         const bool whole = (it.t0 + m + 1) * KT <= it.s.base;  // every column sees every key of the tile
-        uint4 see = make_uint4(~0u, ~0u, ~0u, ~0u);
+        uint32_t see[R / 32];
+#pragma unroll
+        for (int i = 0; i < R / 32; ++i) see[i] = ~0u;
         if (!whole && j >= 0) {
-          see = make_uint4(0u, 0u, 0u, 0u);
-          if (t < it.s.len && j < TREE_MAX) see = p.sees[((size_t)it.b * p.v.n_qt + it.qt) * TREE_MAX + j];
+          const uint32_t *src = reinterpret_cast<const uint32_t *>(p.sees + ((size_t)it.b * p.v.n_qt + it.qt) * TREE_MAX + j);
+#pragma unroll
+          for (int i = 0; i < R / 32; ++i) see[i] = t < it.s.len && j < TREE_MAX ? src[i] : 0u;
         }
-        bool stop = false, some = false;
+        bool some = false;
+        uint8_t *const pb = smem + F::OFF_P + gr * F::P_BYTES;
 #pragma unroll
-        for (int cc = 0; cc < C; cc += CH) {
-          float d[CH];
-          tmem_ld(tS + R * st + cc, d);
-          const uint32_t bits = (R == 32 ? see.x >> (16 * gr)
-                                         : (R == 64 ? (gr ? see.y : see.x) : (gr ? (cc ? see.w : see.z) : (cc ? see.y : see.x))));
-          float top = -INFINITY;
+        for (int cc = 0; cc < R; cc += CH) {
+          const uint32_t bits = see[cc / 32];
+          // scores less the running maxima, and the largest
+          float d[CH], top = -INFINITY;
+          tmem_ld32(tS + R * sb + cc, d);
+          if (cc + CH == R) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.s_free[sb]);
+          }
+          if (scaled) {
 #pragma unroll
-          for (int c = 0; c < CH; c += 2) {
-            const float4 qm = ms.qm[(col0 + cc + c) >> 1];
-            upk2(fma2(mul2(pk2(d[c], d[c + 1]), kn2), pk2(qm.x, qm.y), pk2(qm.z, qm.w)), d[c], d[c + 1]);
+            for (int e = 0; e < CH; ++e) d[e] *= ms.qs[gr][cc + e];
+          }
+#pragma unroll
+          for (int e = 0; e < CH; e += 2) {
+            const float2 x = *reinterpret_cast<const float2 *>(&nm[cc + e]);
+            upk2(fma2(pk2(d[e], d[e + 1]), kn2, pk2(x.x, x.y)), d[e], d[e + 1]);
           }
           if (!whole) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c) d[c] = (bits >> c) & 1u ? d[c] : -INFINITY;
+            for (int e = 0; e < CH; ++e) d[e] = (bits >> e) & 1u ? d[e] : -INFINITY;
           }
 #pragma unroll
-          for (int c = 0; c < CH; ++c) top = fmaxf(top, d[c]);
-          const bool need = fresh || top > most || !ok;
-          if (group_or(gr, need)) {
-            // ---- maxima of the chunk's columns over the tile's keys; raise those that need it
+          for (int e = 0; e < CH; e += 2) top = max3(top, d[e], d[e + 1]);
+          if (group_or(gr, fresh || top > most || !ok)) {
+            // ---- the columns' maxima over the tile's keys of score + log2(value norm); raise those that need it
             if (group_or(gr, !ok)) {
-              stop = true;
+              ok = false;
               break;
             }
+            const float lv = fmaxf(log2_approx(nv), -64.f);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-              float u = d[c] + lv;
-#pragma unroll
-              for (int h = 16; h >= 1; h >>= 1) u = fmaxf(u, __shfl_xor_sync(FULL_MASK, u, h));
-              if (lane == (c & 31)) ms.red[gr][wq][cc + c] = u;
+            for (int e = 0; e < CH; ++e) {
+              const float u = warp_max(d[e] + lv);
+              if (lane == e) ms.red[gr][wq][e] = u;
             }
             (void)group_or(gr, false);
             bool none = false, raised = false;
             if (key < CH) {
-              const int c = col0 + cc + key;
-              const float bm = fmaxf(fmaxf(ms.red[gr][0][cc + key], ms.red[gr][1][cc + key]),
-                                     fmaxf(ms.red[gr][2][cc + key], ms.red[gr][3][cc + key])) - W_SHIFT;
-              const float old = ms.mx[c];
+              const int col = cc + key;
+              const float bm = fmaxf(fmaxf(ms.red[gr][0][key], ms.red[gr][1][key]),
+                                     fmaxf(ms.red[gr][2][key], ms.red[gr][3][key])) - W_SHIFT;
+              const float old = ms.mx[gr][col];
               float by = 0.f, root = 1.f;  // the maximum rises by `by` (from 0 without one)
               if (bm > (old == -INFINITY ? -INFINITY : RESCALE_SLACK)) {
                 by = bm;
-                ms.mx[c] = old == -INFINITY ? bm : old + bm;
-                reinterpret_cast<float *>(&ms.qm[c >> 1])[2 + (c & 1)] = -ms.mx[c];
+                ms.mx[gr][col] = old == -INFINITY ? bm : old + bm;
+                nm[col] = -ms.mx[gr][col];
                 raised = old != -INFINITY;
                 if (raised) root = exp2_approx(-0.5f * by);
               } else {
                 none = old == -INFINITY;
               }
-              float *move = reinterpret_cast<float *>(&ms.move[c >> 1]);
-              move[c & 1] = by, move[2 + (c & 1)] = root;
+              float *x = reinterpret_cast<float *>(&mv[col >> 1]);
+              x[col & 1] = by, x[2 + (col & 1)] = root;
             }
             if (group_or(gr, none)) some = true;
-            if (group_or(gr, raised) && m) {  // O is whole once the last tile's product has finished
-              ok = __all_sync(FULL_MASK, wait(&ms.pv_done[st ^ 1], ((n - 1) >> 1) & 1));
-              if (group_or(gr, !ok)) {
-                stop = true;
-                break;
-              }
-              tc_fence_after();
 #pragma unroll
-              for (int part = 0; part < PARTS; ++part) {
-                float o[CH];
-                tmem_ld(tO + part * R + cc, o);
-#pragma unroll
-                for (int c = 0; c < CH; c += 2) {
-                  const float4 move = ms.move[(col0 + cc + c) >> 1];
-                  o[c] *= move.z * move.z, o[c + 1] *= move.w * move.w;
-                }
-                tmem_st(tO + part * R + cc, o);
-              }
-              tc_fence_before();
+            for (int e = 0; e < CH; e += 2) {
+              const float4 x = mv[(cc + e) >> 1];
+              d[e] -= x.x, d[e + 1] -= x.y;
             }
+            if (group_or(gr, raised)) {
 #pragma unroll
-            for (int c = 0; c < CH; c += 2) {
-              const float4 move = ms.move[(col0 + cc + c) >> 1];
-              d[c] -= move.x, d[c + 1] -= move.y;
-              float l0, l1;
-              upk2(l2[(cc + c) / 2], l0, l1);
-              l2[(cc + c) / 2] = pk2(lower(l0, move.z), lower(l1, move.w));
+              for (int e = 0; e < CH; e += 2) {
+                const float4 x = mv[(cc + e) >> 1];
+                const uint64_t f2 = pk2(x.z, x.w);
+                l2[(cc + e) / 2] = mul2(mul2(l2[(cc + e) / 2], f2), f2);
+              }
+              if (held) {
+#pragma unroll
+                for (int at = 0; at < PARTS * CH; at += 16) {
+                  float o[16];
+                  const int col = cc + at % CH;
+                  tmem_ld16(tO + at / CH * R + col, o);
+#pragma unroll
+                  for (int e = 0; e < 16; e += 2) {
+                    const float4 x = mv[(col + e) >> 1];
+                    o[e] *= x.z * x.z, o[e + 1] *= x.w * x.w;
+                  }
+                  tmem_st16(tO + at / CH * R + col, o);
+                }
+              }
             }
           }
           // ---- weights, their sums and the operand P
-          uint32_t hi[CH / 2], lo[CH / 2];
-          const uint64_t nvf2 = pk2(nvf, nvf);
 #pragma unroll
-          for (int c = 0; c < CH; c += 2) {
-            const uint64_t e2 = pk2(exp2_approx(d[c]), exp2_approx(d[c + 1]));
-            uint64_t &l = l2[(cc + c) / 2];
-            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(l) : "l"(e2));
-            float p0, p1;
-            upk2(mul2(e2, nvf2), p0, p1);
-            // a key that is not seen: its norm may be anything
-            if (!whole) p0 = (bits >> c) & 1u ? p0 : 0.f, p1 = (bits >> (c + 1)) & 1u ? p1 : 0.f;
-            if (PARTS == 2) split_half2(p0, p1, hi[c / 2], lo[c / 2]);
-            else hi[c / 2] = pack_half2(p0, p1);
-          }
-          uint8_t *pb = smem + F::OFF_P + st * F::P_BYTES;
+          for (int e = 0; e < CH; e += 8) {
+            uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int part = 0; part < PARTS; ++part) {
-            const uint32_t *x = part ? lo : hi;
-#pragma unroll
-            for (int c = 0; c < CH; c += 8)
-              *reinterpret_cast<uint4 *>(pb + sw128_offset(key, part * R + col0 + cc + c)) =
-                  make_uint4(x[c / 2], x[c / 2 + 1], x[c / 2 + 2], x[c / 2 + 3]);
+            for (int i = 0; i < 8; i += 2) {
+              const uint64_t e2 = pk2(exp2_approx(d[e + i]), exp2_approx(d[e + i + 1]));
+              acc2(l2[(cc + e + i) / 2], e2);
+              float p0, p1;
+              upk2(mul2(e2, nvf2), p0, p1);
+              if (PARTS == 2) split_half2(p0, p1, hi[i / 2], lo[i / 2]);
+              else hi[i / 2] = pack_half2(p0, p1);
+            }
+            *reinterpret_cast<uint4 *>(pb + sw128_offset(key, cc + e)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (PARTS == 2) *reinterpret_cast<uint4 *>(pb + sw128_offset(key, R + cc + e)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
-        if (stop) {
-          ok = false;
-          break;
+        if (!ok) break;
+        // A norm that is not finite makes NaN of a weight of 0 too: not for the columns that do not see the key.
+        if (!whole && !(fabsf(nvf) < INFINITY)) {
+#pragma unroll 1
+          for (int c2 = 0; c2 < R * PARTS; ++c2) {
+            const int col = c2 % R;
+            if (!(((R == 64 && col >= 32 ? see[R / 32 - 1] : see[0]) >> (col & 31)) & 1u))
+              *reinterpret_cast<uint16_t *>(pb + sw128_offset(key, c2)) = 0;
+          }
         }
         fresh = some;
+        held = true;
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.p_ready[st]);
+        if (lane == 0) mbar_arrive(&ms.p_ready[gr]);
       }
-      if (!ok) break;
+      n += tiles;
 
-      // ---- end of the item: O^T (thread = dim) and the sums of weights
-      ok = __all_sync(FULL_MASK, wait(&ms.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1));
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < C; c += 2) {
-        float l0, l1;
-        upk2(l2[c / 2], l0, l1);
-#pragma unroll
-        for (int h = 16; h >= 1; h >>= 1) l0 += __shfl_xor_sync(FULL_MASK, l0, h), l1 += __shfl_xor_sync(FULL_MASK, l1, h);
-        if (lane == 0) ms.red[gr][wq][c] = l0, ms.red[gr][wq][c + 1] = l1;
+      // ---- end of the item: the groups' states merged; O^T: thread = dim
+      if (ok && held) {  // the group's last tile
+        const uint32_t c = n - 1 - (((n - 1) ^ gr) & 1);
+        ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr], (c >> 1) & 1));
       }
-      if (group_or(gr, !ok)) break;
+#pragma unroll
+      for (int cc = 0; cc < R; cc += 32) {  // sums over the warp's keys: column cc + l to lane l
+        float x[32];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) upk2(l2[(cc + e) / 2], x[e], x[e + 1]);
+#pragma unroll
+        for (int h = 16; h >= 1; h >>= 1) {
+          const bool up = lane & h;
+#pragma unroll
+          for (int e = 0; e < h; ++e) {
+            const float mine = up ? x[e + h] : x[e], other = up ? x[e] : x[e + h];
+            x[e] = mine + __shfl_xor_sync(FULL_MASK, other, h);
+          }
+        }
+        ms.red[gr][wq][cc + lane] = x[0];
+      }
+      tc_fence_before();
+      if (both_or(!ok)) break;
+      tc_fence_after();
       const int first = share_of(it.vstart, ms.V, ms.G);
       const int n_split = share_of(it.vstart + it.tiles - 1, ms.V, ms.G) - first + 1, cta = blockIdx.x;
       if (tid == 0 && cta == first) p.unit[unit] = first | (n_split << 16);
-      const int head0 = it.h * p.v.gq;
-      auto row_of = [&](int c) -> float * {
-        if (n_split > 1) return p.split + ((size_t)(cta * 2 + (cta == first ? 1 : 0)) * R + c) * PROW;
-        const int local = c / p.v.gq;
-        return p.whole + ((size_t)(it.s.row + n0 + local) * p.Hq + head0 + c - local * p.v.gq) * PROW;
-      };
-      if (key < C && col0 + key < cols) {
-        float *dst = row_of(col0 + key) + D;
-        const float l = (ms.red[gr][0][key] + ms.red[gr][1][key]) + (ms.red[gr][2][key] + ms.red[gr][3][key]);
-        dst[0] = ms.mx[col0 + key], dst[1] = l;
+      if (tid < cols) {
+        auto sum = [&](int g2) {
+          return (ms.red[g2][0][tid] + ms.red[g2][1][tid]) + (ms.red[g2][2][tid] + ms.red[g2][3][tid]);
+        };
+        const float m0 = ms.mx[0][tid], m1 = ms.mx[1][tid], mx = fmaxf(m0, m1), l0 = sum(0), l1 = sum(1);
+        const float f0 = m0 == -INFINITY ? 0.f : exp2_approx(m0 - mx), f1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - mx);
+        const int local = tid / p.v.gq;
+        float *dst = n_split > 1 ? p.split + ((size_t)(cta * 2 + (cta == first ? 1 : 0)) * R + tid) * PROW
+                                 : p.whole + ((size_t)(it.s.row + n0 + local) * p.Hq + it.h * p.v.gq + tid - local * p.v.gq) * PROW;
+        // (without a maximum a group's sum is 0, or NaN where its scores are)
+        dst[D] = mx;
+        dst[D + 1] = (m0 == -INFINITY ? l0 : lower_by(l0, m0 - mx)) + (m1 == -INFINITY ? l1 : lower_by(l1, m1 - mx));
+        const uint64_t at = (uint64_t)(uintptr_t)dst;
+        ms.end[tid] = make_float4(f0, f1, __uint_as_float((uint32_t)at), __uint_as_float((uint32_t)(at >> 32)));
       }
+      (void)both_or(false);
+      // group gr writes the columns gr R / 2 .. of both accumulators
+      const bool has0 = tiles > 1 || first_m == (gr == 0 ? 0 : 1), has1 = tiles > 1 || !has0;
 #pragma unroll 1
-      for (int cc = 0; cc < C; cc += CH) {
-        float o[CH];
-        tmem_ld(tO + cc, o);
-        if (PARTS == 2) {
-          float x[CH];
-          tmem_ld(tO + R + cc, x);
+      for (int cc = gr * (R / 2); cc < min((gr + 1) * (R / 2), cols); cc += 16) {
+        float o[2][16];
 #pragma unroll
-          for (int c = 0; c < CH; ++c) o[c] += x[c];
+        for (int g2 = 0; g2 < 2; ++g2) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[g2][e] = 0.f;
+          if (g2 ? has1 : has0) {
+            const uint32_t at = tmem + lane_off + F::TM_O + F::N * g2 + cc;
+            tmem_ld16(at, o[g2]);
+            if (PARTS == 2) {
+              float x[16];
+              tmem_ld16(at + R, x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[g2][e] += x[e];
+            }
+          }
         }
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
-          if (col0 + cc + c < cols) row_of(col0 + cc + c)[32 * wq + lane] = o[c];
+        for (int e = 0; e < 16; ++e) {
+          if (cc + e < cols) {
+            const float4 f = ms.end[cc + e];
+            float *dst = reinterpret_cast<float *>((uintptr_t)(((uint64_t)__float_as_uint(f.w) << 32) | __float_as_uint(f.z)));
+            dst[32 * wq + lane] = (f.x == 0.f ? 0.f : o[0][e] * f.x) + (f.y == 0.f ? 0.f : o[1][e] * f.y);
+          }
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.o_free);
+      if (both_or(false)) break;  // the maxima and sums are read: the next item may write them
     }
   }
   __syncwarp();
@@ -975,7 +1125,7 @@ bool layout(const tq_ctx *k, const PagedView &pv, int Hq, int out_dtype, Layout 
   l->gq = Hq / pv.Hkv;
   l->parts = out_dtype == TQ_DTYPE_BF16 ? 1 : 2;
   const int rows = pv.max_q * l->gq;
-  l->R = rows <= 32 ? 32 : (rows <= 64 || l->parts == 2 ? 64 : 128);
+  l->R = rows <= 32 ? 32 : 64;
   l->npu = l->R / l->gq;  // at least one: 64 heads per KV head at most
   l->n_qt = (pv.max_q + l->npu - 1) / l->npu;
   l->grid = k->num_sms;
@@ -994,7 +1144,7 @@ bool layout(const tq_ctx *k, const PagedView &pv, int Hq, int out_dtype, Layout 
 
 template <int R, int PARTS>
 cudaError_t launch_partial(const PartialParams &p, int grid, cudaStream_t st) {
-  constexpr uint32_t smem = Cfg<R, PARTS>::OFF_MISC + sizeof(Misc) + 1024;  // + slack to align to 1024
+  constexpr uint32_t smem = Cfg<R, PARTS>::OFF_MISC + sizeof(Misc<Cfg<R, PARTS>::NKN>) + 1024;  // + slack to align to 1024
   static_assert(smem <= 227 * 1024, "shared memory budget");
   const cudaError_t e = kernel_smem_attr((const void *)k_tree_partial<R, PARTS>, (int)smem);
   if (e != cudaSuccess) return e;
@@ -1039,6 +1189,7 @@ cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView 
   PartialParams p{};
   p.v = tv, p.kp = kp, p.vp = vp, p.Hq = Hq;
   p.qh = a.qh, p.qsc = a.qsc, p.sees = a.sees;
+  for (int i = 0; i < 8; ++i) p.kc16[i] = k->f16.c16[i];
   for (int i = 0; i < 2; ++i) {
     p.klo[i] = k->f16.lo[i], p.khi[i] = k->f16.hi[i];
     p.vlo[i] = v->f16.lo[i], p.vhi[i] = v->f16.hi[i];
@@ -1047,8 +1198,7 @@ cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView 
   p.whole = reinterpret_cast<float *>(base + l.whole);
   p.unit = reinterpret_cast<int32_t *>(base + l.unit);
   if (l.parts == 1)
-    e = l.R == 32 ? launch_partial<32, 1>(p, l.grid, st)
-                  : (l.R == 64 ? launch_partial<64, 1>(p, l.grid, st) : launch_partial<128, 1>(p, l.grid, st));
+    e = l.R == 32 ? launch_partial<32, 1>(p, l.grid, st) : launch_partial<64, 1>(p, l.grid, st);
   else
     e = l.R == 32 ? launch_partial<32, 2>(p, l.grid, st) : launch_partial<64, 2>(p, l.grid, st);
   if (e != cudaSuccess) return e;

@@ -15,13 +15,10 @@
 //                   empty tiles that stand for its start) and are shared out evenly, as in the paged decode.
 //                   Specialised warps:
 //                     loader      packed tiles, one bulk copy per page and side, on rings; q's images
-//                     K decoders  nibble pairs -> fp16 centroid pairs through a table in shared memory (a column of
-//                                 it per lane: no bank conflicts) into tensor memory, a key per lane: the A
-//                                 operand of S^T
-//                     V decoders  nibbles -> fp16 centroids (byte permutes) into 128-byte swizzled tiles, the
-//                                 MN-major A operand of O^T.  (Tables for both would fill the shared-memory
-//                                 path, permutes for both the ALU, which takes one every other cycle.)
-//                     issuer      one thread
+//                     K decoders  nibbles -> fp16 centroids (byte permutes) into tensor memory, a key per lane:
+//                                 the A operand of S^T, without a trip through shared memory
+//                     V decoders  the same into 128-byte swizzled tiles, the MN-major A operand of O^T
+//                     issuers     one thread for S^T, as far ahead as its buffers go, one for O^T
 //                     softmax     two groups of four warps on alternate key tiles, each with its own O^T: S^T from
 //                                 tensor memory, weights against the columns' running maxima, P as the
 //                                 MN-major B operand in shared memory.  A maximum is raised (and O
@@ -54,21 +51,41 @@ static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REG
 template <int R_, int PARTS_>
 struct Cfg {
   static constexpr int R = R_, PARTS = PARTS_;
-  static constexpr int N = R * PARTS < 64 ? 64 : R * PARTS;  // columns of P and O (whole 128-byte rows)
-  static constexpr int CH = 32;                              // columns a thread takes at a time
-  static constexpr bool LUT = R * PARTS <= 64;               // K by table (32 KB), where shared memory holds it
-  static constexpr int NRAW = 3;
-  static constexpr int NS = R * PARTS == 128 ? 2 : 4;        // buffers of S
+  static constexpr int N = R * PARTS;   // columns of P and O
+  static constexpr int CH = 32;         // columns a thread takes at a time
+  // Stages: packed tiles on their way (more of the values', which the K decoders need for their norms long before
+  // the V decoders come to them), decoded K (tensor memory) and V (shared memory), scores, P.
+  static constexpr int NRAW_K = 3, NRAW_V = N == 128 ? 3 : 4;
+  static constexpr int NK = N == 128 ? 2 : (R == 64 ? 3 : 4), NV = N == 128 ? 2 : 3;
+  static constexpr int NS = N == 128 ? 2 : (R == 64 ? 3 : 4), NP = N == 32 ? 4 : 2;
+  static constexpr int NKN = NS + NK + 2;  // tiles whose norms are kept: see Misc
   static constexpr uint32_t TM_S = 0, TM_O = NS * R, TM_K = TM_O + 2 * N;
-  static_assert(TM_K + 2 * 64 <= 512, "tensor memory");
-  static constexpr int NKN = NS + 4;                         // tiles whose norms are kept (at least NS + 2)
-  static constexpr uint32_t Q_HALF = R * PARTS * 128, Q_BYTES = 2 * Q_HALF, P_BYTES = (N / 64) * SW_HALF_BYTES;
-  static constexpr uint32_t OFF_V = 0, OFF_P = 2 * SW_TILE_BYTES, OFF_Q = OFF_P + 2 * P_BYTES;
-  static constexpr uint32_t OFF_LUT = OFF_Q + Q_BYTES, OFF_RAW = OFF_LUT + (LUT ? 256 * 128 : 0);
-  static constexpr uint32_t OFF_MISC = OFF_RAW + 2 * NRAW * RAW;
+  static_assert(TM_K + NK * 64 <= 512, "tensor memory");
+  // A row of P: 64 bytes where it has 32 columns, else 128 (a second half for more than 64)
+  static constexpr uint32_t P_ROW = N == 32 ? 64 : 128, P_BYTES = N * KT * 2;
+  static constexpr uint32_t Q_HALF = N * 128, Q_BYTES = 2 * Q_HALF;
+  static constexpr uint32_t OFF_V = 0, OFF_P = NV * SW_TILE_BYTES, OFF_Q = OFF_P + NP * P_BYTES;
+  static constexpr uint32_t OFF_RAW = OFF_Q + Q_BYTES;
+  static constexpr uint32_t OFF_RAW_V = OFF_RAW + NRAW_K * RAW, OFF_MISC = OFF_RAW_V + NRAW_V * RAW;
   static constexpr uint32_t IDESC_S = (1u << 4) | (uint32_t(R >> 3) << 17) | ((128u >> 4) << 24);
   static constexpr uint32_t IDESC_PV = (1u << 4) | (1u << 15) | (1u << 16) | (uint32_t(N >> 3) << 17) | ((128u >> 4) << 24);
+  // Byte of P's (key, column): rows of 128 bytes swizzled as the other operands, rows of 64 with 16-byte chunk c of
+  // row r at c ^ (r / 2 % 4), eight rows to 512 bytes.
+  static __device__ __forceinline__ uint32_t p_at(uint32_t key, uint32_t col) {
+    return N == 32 ? key * 64 + (((col >> 3) ^ ((key >> 1) & 3)) << 4) + (col & 7) * 2 : sw128_offset(key, col);
+  }
 };
+// Descriptor of P's 64-byte rows as the MN-major B operand (32 columns): eight rows 512 bytes apart; K-step s of 16 rows
+// starts 1024 s bytes in.
+__device__ __forceinline__ uint64_t sw64_mn_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)1 << 16;                         // leading offset (unused: one atom of columns)
+  d |= (uint64_t)((512u >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;                         // descriptor version
+  d |= (uint64_t)4 << 61;                         // 64-byte swizzle
+  return d;
+}
 
 struct TreeView {
   PagedView pv;
@@ -146,16 +163,20 @@ __device__ __forceinline__ bool next_item(const TreeView &v, Walk &w, Item &it) 
   }
   return false;
 }
-// One warp: all virtual tiles (flagging bad lengths), then where this CTA's share starts.
-__device__ void find_share(const TreeView &v, int lane, Walk &w, int &V, int &G) {
+// Where a CTA's share starts.
+struct Start {
+  int b, u, off, left, v, V, G;
+};
+// One warp: all virtual tiles (flagging bad lengths), then the start of CTA c's share of `grid`.
+__device__ __noinline__ Start find_share(const TreeView &v, int lane, int c, int grid) {
   int sum = 0;
-  for (int b = lane; b < v.pv.B; b += 32) sum += seq_vtiles(v, seq_of(v, b, blockIdx.x == 0));
-  V = __reduce_add_sync(FULL_MASK, sum);
-  G = min((int)gridDim.x, V);
-  w = Walk{};
-  if ((int)blockIdx.x >= G) return;
-  w.v = share_start(blockIdx.x, V, G);
-  w.left = share_start(blockIdx.x + 1, V, G) - w.v;
+  for (int b = lane; b < v.pv.B; b += 32) sum += seq_vtiles(v, seq_of(v, b, c == 0));
+  Start w{};
+  w.V = __reduce_add_sync(FULL_MASK, sum);
+  w.G = min(grid, w.V);
+  if (c >= w.G) return w;
+  w.v = share_start(c, w.V, w.G);
+  w.left = share_start(c + 1, w.V, w.G) - w.v;
   int base = 0;
   for (int b0 = 0; b0 < v.pv.B; b0 += 32) {
     const int t = seq_vtiles(v, seq_of(v, b0 + lane, false));
@@ -174,10 +195,10 @@ __device__ void find_share(const TreeView &v, int lane, Walk &w, int &V, int &G)
     }
     base += __shfl_sync(FULL_MASK, inc, 31);
   }
-  walk_load(v, w);
-  const int vt = w.tiles + ITEM_TILES;
+  const int vt = seq_tiles(seq_of(v, w.b, false)) + ITEM_TILES;
   w.u = w.off / vt;
   w.off -= w.u * vt;
+  return w;
 }
 
 // ------------------------------------------------------------------------------ preparation
@@ -192,6 +213,8 @@ struct PrepParams {
   const uint4 *kfrag;  // R of the keys
   uint8_t *qh;         // [unit] operand images: two halves of 64 dims, rows of 128 bytes (columns' hi parts, then lo)
   float *qsc;          // [unit][R] power-of-two scales, 0 for a column without a node
+  Start *start;        // [CTA of the attention]
+  int grid;            // its CTAs
   uint4 *sees;         // [sequence][tile of nodes][node's key]: the columns that see it
 };
 struct PrepSmem {
@@ -249,10 +272,17 @@ __global__ void __launch_bounds__(PREP_WARPS * 32) k_tree_prep(const PrepParams 
   auto &xs = sm.xs[warp];
   const TreeView &v = p.v;
   const int blocks = p.R / 16;
-  const int64_t q_tasks = (int64_t)v.pv.B * v.pv.Hkv * v.n_qt * blocks, tasks = q_tasks + (int64_t)v.pv.B * v.n_qt * 4;
+  const int64_t q_tasks = (int64_t)v.pv.B * v.pv.Hkv * v.n_qt * blocks, see_tasks = (int64_t)v.pv.B * v.n_qt * 4;
+  const int64_t tasks = q_tasks + see_tasks + p.grid;
   bool have_r = false;
   // tasks over the CTAs first: a few use as many SMs as they can
   for (int64_t task = (int64_t)warp * gridDim.x + blockIdx.x; task < tasks; task += (int64_t)PREP_WARPS * gridDim.x) {
+    if (task >= q_tasks + see_tasks) {
+      const int c = (int)(task - q_tasks - see_tasks);
+      const Start st = find_share(v, lane, c, p.grid);
+      if (lane == 0) p.start[c] = st;
+      continue;
+    }
     if (task >= q_tasks) {
       const int x = (int)(task - q_tasks), bq = x >> 2;
       see_bits(p, bq / v.n_qt, bq % v.n_qt, x & 3, lane);
@@ -388,7 +418,7 @@ struct PartialParams {
   const uint8_t *qh;
   const float *qsc;
   const uint4 *sees;
-  uint32_t kc16[8];  // the keys' fp16 centroids
+  const Start *start;
   uint32_t klo[2], khi[2], vlo[2], vhi[2];
   float *split;   // [CTA][2][R] partials of units that several CTAs share
   float *whole;   // [row][Hq] partials of units one CTA finished
@@ -397,13 +427,14 @@ struct PartialParams {
 
 template <int NKN>
 struct Misc {
-  uint64_t raw_full[2][3], raw_empty[2][3];  // [side][stage]
-  uint64_t k_full[2], k_empty[2], v_full[2];
+  uint64_t raw_full[2][4], raw_empty[2][4];  // [side][stage]
+  uint64_t k_full[4], k_empty[4], v_full[3], v_empty[3];
   uint64_t s_done[4], s_free[4];      // [buffer]
-  uint64_t p_ready[2], pv_done[2];    // [group]: a P buffer and a V stage are free once their product is done
+  uint64_t p_ready[4], pv_done[4];    // [buffer of P]
   uint64_t q_full, q_empty, o_free, drain[2];
-  // Norms of the last tiles, both written by the K decoders, so that the softmax waits for no values: a K stage is
-  // free once its product is done, while the softmax still X
+  // Norms of the last tiles, both written by the K decoders, so that the softmax waits for no values.  Tile j is
+  // decoded once the scores of tile j - NK are done, and those once the softmax has read the scores, and with them the
+  // norms, of tile j - NK - NS.
   float kn[NKN][KT], nv[NKN][KT];
   alignas(16) float nm[2][64], qs[2][64];  // [group] minus the running maxima (less W_SHIFT; none yet: 0), scales of q
   float4 move[2][32];     // and, where maxima are raised: what the scores fall by, the square root of O's factor
@@ -502,7 +533,7 @@ __device__ __forceinline__ void acc2(uint64_t &a, uint64_t b) { asm("add.rn.f32x
 template <int R, int PARTS>
 __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams p) {
   using F = Cfg<R, PARTS>;
-  constexpr int CH = F::CH, NRAW = F::NRAW, NS = F::NS, NKN = F::NKN;
+  constexpr int CH = F::CH, NRAW_K = F::NRAW_K, NRAW_V = F::NRAW_V, NK = F::NK, NV = F::NV, NS = F::NS, NP = F::NP, NKN = F::NKN;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
   Misc<NKN> &ms = *reinterpret_cast<Misc<NKN> *>(smem + F::OFF_MISC);
@@ -510,26 +541,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
   pdl_trigger();
   if (warp == 0) tmem_alloc(smem_addr(&ms.tmem), 512);
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
-      for (int i = 0; i < NRAW; ++i) mbar_init(&ms.raw_full[s][i], 1), mbar_init(&ms.raw_empty[s][i], s ? 8 : 4);
-      mbar_init(&ms.k_full[s], 4), mbar_init(&ms.v_full[s], 4);
-      mbar_init(&ms.k_empty[s], 1), mbar_init(&ms.pv_done[s], 1);
-      mbar_init(&ms.p_ready[s], 4);
-    }
+    for (int s = 0; s < 2; ++s)
+      for (int i = 0; i < (s ? NRAW_V : NRAW_K); ++i) mbar_init(&ms.raw_full[s][i], 1), mbar_init(&ms.raw_empty[s][i], s ? 8 : 4);
+    for (int i = 0; i < NK; ++i) mbar_init(&ms.k_full[i], 4), mbar_init(&ms.k_empty[i], 1);
+    for (int i = 0; i < NV; ++i) mbar_init(&ms.v_full[i], 4), mbar_init(&ms.v_empty[i], 1);
     for (int i = 0; i < NS; ++i) mbar_init(&ms.s_done[i], 1), mbar_init(&ms.s_free[i], 4);
+    for (int i = 0; i < NP; ++i) mbar_init(&ms.p_ready[i], 4), mbar_init(&ms.pv_done[i], 1);
     mbar_init(&ms.q_full, 1), mbar_init(&ms.q_empty, 1), mbar_init(&ms.o_free, 8);
     mbar_init(&ms.drain[0], 1), mbar_init(&ms.drain[1], 1);
     for (int i = 0; i < NITEM; ++i) mbar_init(&ms.item_full[i], 1), mbar_init(&ms.item_empty[i], THREADS / 32 - 1);
     ms.abort_flag = 0;
     fence_mbar_init();
-  }
-  if (F::LUT) {  // entry b: the centroids of nibbles b & 15, b >> 4, once per lane
-    for (int i = tid; i < 256 * 8; i += THREADS) {
-      const int b = i >> 3;
-      const uint32_t lo = (p.kc16[(b & 15) >> 1] >> (16 * (b & 1))) & 0xFFFFu;
-      const uint32_t hi = (p.kc16[b >> 5] >> (16 * ((b >> 4) & 1))) & 0xFFFFu, e = lo | (hi << 16);
-      reinterpret_cast<uint4 *>(smem + F::OFF_LUT)[i] = make_uint4(e, e, e, e);
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -570,9 +592,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
       const uint8_t *pages = side ? p.vp : p.kp;
       Walk w;
       if (!side) {
-        int V, G;
-        find_share(p.v, lane, w, V, G);
-        if (lane == 0) ms.V = V, ms.G = G;
+        const Start st = p.start[blockIdx.x];
+        w.b = st.b, w.u = st.u, w.off = st.off, w.left = st.left, w.v = st.v;
+        if (w.left) walk_load(p.v, w);
+        if (lane == 0) ms.V = st.V, ms.G = st.G;
       }
       auto publish = [&]() -> bool {  // the keys' loader walks its share for all
         const uint32_t i = n_items % NITEM;
@@ -586,7 +609,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
         ++n_items;
         return it.t1 > it.t0;
       };
-      uint32_t n = 0;  // tiles loaded
+      const uint32_t nr = side ? NRAW_V : NRAW_K, raw = side ? F::OFF_RAW_V : F::OFF_RAW;
+      uint32_t n = 0, s = 0, turn = 0;  // tiles loaded; the next one's stage, and rounds of the stages
       while (ok && (side ? next() : publish())) {
         auto page_of = [&](int j) -> int {
           const int pi = ((j * KT) >> psh) + lane;
@@ -595,30 +619,30 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
         };
         int pg = page_of(it.t0);
         for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
-          const int kf = j * KT, nk4 = (min(KT, it.s.len - kf) + 3) & ~3, s = n % NRAW;
+          const int kf = j * KT, nk4 = (min(KT, it.s.len - kf) + 3) & ~3;
           const int pg_next = page_of(j + 1);
-          if (n >= NRAW && !(ok = __all_sync(FULL_MASK, wait(&ms.raw_empty[side][s], ((n / NRAW) - 1) & 1)))) break;
+          if (turn && !(ok = __all_sync(FULL_MASK, wait(&ms.raw_empty[side][s], (turn - 1) & 1)))) break;
           // rows of a tile rounded up to four (16-byte copies; they stay inside the page)
           if (lane == 0) mbar_arrive_expect_tx(&ms.raw_full[side][s], nk4 * PG_ROW);
           __syncwarp();
           if (pg >= 0) {
             const int k0 = max((((kf >> psh) + lane) << psh), kf), k1 = min(((k0 >> psh) + 1) << psh, kf + nk4);
-            bulk_g2s(smem + F::OFF_RAW + (2 * s + side) * RAW + (k0 - kf) * PG_ROW,
+            bulk_g2s(smem + raw + s * RAW + (k0 - kf) * PG_ROW,
                      pages + paged_row(p.v.pv, pg, it.h, k0 & (P - 1)), (uint32_t)(k1 - k0) * PG_ROW, &ms.raw_full[side][s]);
           }
           pg = pg_next;
+          if (++s == nr) s = 0, ++turn;
         }
       }
       // after a failed wait: let the copies in flight land before the CTA ends
       if (*reinterpret_cast<volatile int *>(&ms.abort_flag))
-        for (uint32_t c = n > NRAW ? n - NRAW : 0; c < n; ++c)
-          (void)mbar_wait_bounded(&ms.raw_full[side][c % NRAW], (c / NRAW) & 1, WAIT_LIMIT_NS);
+        for (uint32_t c = n > nr ? n - nr : 0; c < n; ++c)
+          (void)mbar_wait_bounded(&ms.raw_full[side][c % nr], (c / nr) & 1, WAIT_LIMIT_NS);
     } else if (warp < W_PV) {
       // ================ decoders: two groups of four warps for the keys, two for the values, on alternate tiles;
       // thread = key of the tile
       const int row = tid & 127;
       const bool side = warp >= W_VDEC;
-      const int st = (warp >> 2) & 1;  // the group, and its stage
       uint32_t lo2[2], hi2[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) lo2[i] = side ? p.vlo[i] : p.klo[i], hi2[i] = side ? p.vhi[i] : p.khi[i];
@@ -627,12 +651,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
       uint32_t n = 0;
       while (ok && next()) {
         for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
-          if ((n & 1) != (uint32_t)st) continue;
-          const int rs = n % NRAW;
-          if (n >= 2) ok = wait(side ? &ms.pv_done[st] : &ms.k_empty[st], ((n >> 1) - 1) & 1);
-          if (ok) ok = wait(&ms.raw_full[side][rs], (n / NRAW) & 1);
+          if ((n & 1) != (uint32_t)((warp >> 2) & 1)) continue;
+          const uint32_t rv = n % NRAW_V, rs = side ? rv : n % NRAW_K, ns = side ? NV : NK, st = n % ns;
+          if (n >= ns) ok = wait(side ? &ms.v_empty[st] : &ms.k_empty[st], ((n / ns) - 1) & 1);
+          if (ok) ok = wait(&ms.raw_full[side][rs], (n / (side ? NRAW_V : NRAW_K)) & 1);
           if (!(ok = __all_sync(FULL_MASK, ok))) break;
-          const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + F::OFF_RAW + (2 * rs + side) * RAW + row * PG_ROW);
+          const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + (side ? F::OFF_RAW_V : F::OFF_RAW) + rs * RAW + row * PG_ROW);
           // Short loops (the warps of an SM run six different ones), the next words loaded ahead of the stores of these.
           if (side) {
             const uint32_t to = to_v + st * SW_TILE_BYTES;
@@ -656,21 +680,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
             fence_async_smem();
           } else {
             tc_fence_after();  // the product that read the stage
-            const uint32_t lut = smem_addr(smem + F::OFF_LUT) + 4 * lane;
 #pragma unroll 1
             for (int q2 = 0; q2 < 4; ++q2) {
               uint32_t d[16];
 #pragma unroll
               for (int ch = 0; ch < 4; ++ch) {
                 uint32_t x[4];
-                const uint32_t word = src[1 + 4 * q2 + ch];
-                if constexpr (F::LUT) {
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[e]) : "r"(lut + 128u * prmt(word, 0u, 0x4440u + e)));
-                } else {
-                  decode8<0x5140u, 0x7362u>(word, lo2, hi2, x);
-                }
+                decode8<0x5140u, 0x7362u>(src[1 + 4 * q2 + ch], lo2, hi2, x);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) d[4 * ch + e] = x[e];
               }
@@ -679,15 +695,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
             tmem_st_wait();
             const bool live = j * KT + row < it.s.len;
             ms.kn[n % NKN][row] = live ? __uint_as_float(src[0]) : 0.f;
-            ok = __all_sync(FULL_MASK, wait(&ms.raw_full[1][rs], (n / NRAW) & 1));
+            ok = __all_sync(FULL_MASK, wait(&ms.raw_full[1][rv], (n / NRAW_V) & 1));
             if (!ok) break;
-            ms.nv[n % NKN][row] = live ? __uint_as_float(src[RAW / 4]) : 0.f;  // (the values' tile lies behind the keys')
+            ms.nv[n % NKN][row] = live ? *reinterpret_cast<const float *>(smem + F::OFF_RAW_V + rv * RAW + row * PG_ROW) : 0.f;
             tc_fence_before();
           }
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(side ? &ms.v_full[st] : &ms.k_full[st]), mbar_arrive(&ms.raw_empty[side][rs]);
-            if (!side) mbar_arrive(&ms.raw_empty[1][rs]);
+            if (!side) mbar_arrive(&ms.raw_empty[1][rv]);
           }
         }
       }
@@ -708,9 +724,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
         __syncwarp();
         q_ok = ok = __all_sync(FULL_MASK, wait(&ms.q_full, items & 1));
         for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
-          const uint32_t st = n & 1, sb = n % NS;
+          const uint32_t st = n % NK, sb = n % NS;
           if (n >= NS) ok = wait(&ms.s_free[sb], ((n / NS) - 1) & 1);
-          if (ok) ok = wait(&ms.k_full[st], (n >> 1) & 1);
+          if (ok) ok = wait(&ms.k_full[st], (n / NK) & 1);
           if (!(ok = __all_sync(FULL_MASK, ok))) break;
           tc_fence_after();
           if (lead) {
@@ -738,23 +754,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
       // ================ issuer of O^T
       const bool lead = elect_lane();
       const uint32_t tO = __shfl_sync(FULL_MASK, tmem, 0) + F::TM_O;
-      const uint64_t dv = sw128_mn_desc(smem_addr(smem + F::OFF_V)), dp = sw128_mn_desc(smem_addr(smem + F::OFF_P));
+      const uint64_t dv = sw128_mn_desc(smem_addr(smem + F::OFF_V)), dp = F::N == 32 ? sw64_mn_desc(smem_addr(smem + F::OFF_P)) : sw128_mn_desc(smem_addr(smem + F::OFF_P));
       uint32_t n = 0, items = 0;
       bool issued = false;
       while (ok && next()) {
         for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
-          const uint32_t st = n & 1;
-          ok = wait(&ms.p_ready[st], (n >> 1) & 1);
-          if (ok) ok = wait(&ms.v_full[st], (n >> 1) & 1);
+          const uint32_t vs = n % NV, ps = n % NP;
+          ok = wait(&ms.p_ready[ps], (n / NP) & 1);
+          if (ok) ok = wait(&ms.v_full[vs], (n / NV) & 1);
           if (ok && j == it.t0 && items) ok = wait(&ms.o_free, (items - 1) & 1);
           if (!(ok = __all_sync(FULL_MASK, ok))) break;
           tc_fence_after();
           if (lead) {
-            const uint64_t a = desc_step(dv, st * SW_TILE_BYTES), b = desc_step(dp, st * F::P_BYTES);
+            const uint64_t a = desc_step(dv, vs * SW_TILE_BYTES), b = desc_step(dp, ps * F::P_BYTES);
 #pragma unroll
             for (int s = 0; s < 8; ++s)  // (each group's first tile of the item starts its accumulator)
-              umma<F::IDESC_PV>(tO + F::N * st, desc_step(a, 2048 * s), desc_step(b, 2048 * s), (j >= it.t0 + 2 || s) ? 1u : 0u);
-            umma_commit(&ms.pv_done[st]);
+              umma<F::IDESC_PV>(tO + F::N * (n & 1), desc_step(a, 2048 * s), desc_step(b, 16 * F::P_ROW * s), (j >= it.t0 + 2 || s) ? 1u : 0u);
+            umma_commit(&ms.pv_done[ps]);
+            umma_commit(&ms.v_empty[vs]);
           }
           __syncwarp();
           issued = true;
@@ -793,10 +810,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
       const int first_m = (n & 1) == (uint32_t)gr ? 0 : 1;
       bool held = false;  // O^T holds something of the item
       for (int m = first_m; m < tiles; m += 2) {
-        const uint32_t c = n + m, sb = c % NS;
+        const uint32_t c = n + m, sb = c % NS, ps = c % NP;
         const int t = (it.t0 + m) * KT + key, j = t - it.s.base;
         ok = wait(&ms.s_done[sb], (c / NS) & 1);
-        if (ok && c >= 2) ok = wait(&ms.pv_done[gr], ((c >> 1) - 1) & 1);  // the P buffer is free, O^T whole
+        if (ok && c >= NP) ok = wait(&ms.pv_done[ps], ((c / NP) - 1) & 1);  // the P buffer is free
         ok = __all_sync(FULL_MASK, ok);
         tc_fence_after();
         const float kn = ms.kn[c % NKN][key], nv = ms.nv[c % NKN][key], nvf = nv * NORM_FACTOR;
@@ -813,7 +830,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
           for (int i = 0; i < R / 32; ++i) see[i] = t < it.s.len && j < TREE_MAX ? src[i] : 0u;
         }
         bool some = false;
-        uint8_t *const pb = smem + F::OFF_P + gr * F::P_BYTES;
+        uint8_t *const pb = smem + F::OFF_P + ps * F::P_BYTES;
 #pragma unroll
         for (int cc = 0; cc < R; cc += CH) {
           const uint32_t bits = see[cc / 32];
@@ -886,6 +903,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
                 l2[(cc + e) / 2] = mul2(mul2(l2[(cc + e) / 2], f2), f2);
               }
               if (held) {
+                // O^T is whole once the group's last product is done
+                ok = __all_sync(FULL_MASK, wait(&ms.pv_done[(c - 2) % NP], ((c - 2) / NP) & 1));
+                if (group_or(gr, !ok)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
 #pragma unroll
                 for (int at = 0; at < PARTS * CH; at += 16) {
                   float o[16];
@@ -914,8 +938,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
               if (PARTS == 2) split_half2(p0, p1, hi[i / 2], lo[i / 2]);
               else hi[i / 2] = pack_half2(p0, p1);
             }
-            *reinterpret_cast<uint4 *>(pb + sw128_offset(key, cc + e)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (PARTS == 2) *reinterpret_cast<uint4 *>(pb + sw128_offset(key, R + cc + e)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4 *>(pb + F::p_at(key, cc + e)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (PARTS == 2) *reinterpret_cast<uint4 *>(pb + F::p_at(key, R + cc + e)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
         if (!ok) break;
@@ -925,7 +949,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
           for (int c2 = 0; c2 < R * PARTS; ++c2) {
             const int col = c2 % R;
             if (!(((R == 64 && col >= 32 ? see[R / 32 - 1] : see[0]) >> (col & 31)) & 1u))
-              *reinterpret_cast<uint16_t *>(pb + sw128_offset(key, c2)) = 0;
+              *reinterpret_cast<uint16_t *>(pb + F::p_at(key, c2)) = 0;
           }
         }
         fresh = some;
@@ -933,14 +957,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.p_ready[gr]);
+        if (lane == 0) mbar_arrive(&ms.p_ready[ps]);
       }
       n += tiles;
 
       // ---- end of the item: the groups' states merged; O^T: thread = dim
       if (ok && held) {  // the group's last tile
         const uint32_t c = n - 1 - (((n - 1) ^ gr) & 1);
-        ok = __all_sync(FULL_MASK, wait(&ms.pv_done[gr], (c >> 1) & 1));
+        ok = __all_sync(FULL_MASK, wait(&ms.pv_done[c % NP], (c / NP) & 1));
       }
 #pragma unroll
       for (int cc = 0; cc < R; cc += 32) {  // sums over the warp's keys: column cc + l to lane l
@@ -1119,7 +1143,7 @@ __global__ void __launch_bounds__(CB_WARPS * 32) k_tree_combine(const CombinePar
 struct Layout {
   int R, parts, npu, n_qt, gq, grid;
   int64_t units;
-  size_t qsc, sees, unit, split, whole, bytes;
+  size_t qsc, sees, start, unit, split, whole, bytes;
 };
 bool layout(const tq_ctx *k, const PagedView &pv, int Hq, int out_dtype, Layout *l) {
   l->gq = Hq / pv.Hkv;
@@ -1135,7 +1159,8 @@ bool layout(const tq_ctx *k, const PagedView &pv, int Hq, int out_dtype, Layout 
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   l->qsc = up((size_t)l->units * l->R * l->parts * 256);
   l->sees = l->qsc + up((size_t)l->units * l->R * 4);
-  l->unit = l->sees + up((size_t)pv.B * l->n_qt * TREE_MAX * 16);
+  l->start = l->sees + up((size_t)pv.B * l->n_qt * TREE_MAX * 16);
+  l->unit = l->start + up((size_t)l->grid * sizeof(Start));
   l->split = l->unit + up((size_t)l->units * 4);
   l->whole = l->split + up((size_t)l->grid * 2 * l->R * PROW * 4);
   l->bytes = l->whole + up((size_t)pv.n_tokens * Hq * PROW * 4);
@@ -1180,16 +1205,16 @@ cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView 
   a.qh = base;
   a.qsc = reinterpret_cast<float *>(base + l.qsc);
   a.sees = reinterpret_cast<uint4 *>(base + l.sees);
+  a.start = reinterpret_cast<Start *>(base + l.start), a.grid = l.grid;
   cudaError_t e = kernel_smem_attr((const void *)k_tree_prep, (int)sizeof(PrepSmem));
   if (e != cudaSuccess) return e;
-  const int64_t tasks = l.units * (l.R / 16) + (int64_t)pv.B * l.n_qt * 4;
+  const int64_t tasks = l.units * (l.R / 16) + (int64_t)pv.B * l.n_qt * 4 + l.grid;
   e = launch_pdl(k_tree_prep, dim3((unsigned)(tasks < k->num_sms ? tasks : k->num_sms)), dim3(PREP_WARPS * 32),
                  sizeof(PrepSmem), st, a);
   if (e != cudaSuccess) return e;
   PartialParams p{};
   p.v = tv, p.kp = kp, p.vp = vp, p.Hq = Hq;
-  p.qh = a.qh, p.qsc = a.qsc, p.sees = a.sees;
-  for (int i = 0; i < 8; ++i) p.kc16[i] = k->f16.c16[i];
+  p.qh = a.qh, p.qsc = a.qsc, p.sees = a.sees, p.start = a.start;
   for (int i = 0; i < 2; ++i) {
     p.klo[i] = k->f16.lo[i], p.khi[i] = k->f16.hi[i];
     p.vlo[i] = v->f16.lo[i], p.vhi[i] = v->f16.hi[i];

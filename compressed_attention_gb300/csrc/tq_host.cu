@@ -135,6 +135,19 @@ cudaError_t kernel_smem_attr(const void *func, int bytes, bool max_shared) {
   return e;
 }
 
+cudaError_t kernel_wide_clusters(const void *func) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::mutex mu;
+  static std::map<std::pair<const void *, int>, bool> done;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done.count({func, dev})) return cudaSuccess;
+  e = cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done[{func, dev}] = true;
+  return e;
+}
+
 cudaError_t kernel_occupancy(const void *func, int threads, size_t smem, int *blocks) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

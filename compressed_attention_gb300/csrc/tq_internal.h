@@ -123,6 +123,8 @@ tq_status check_current_device(int device, const char *who);
 // the largest shared-memory carveout) once per (kernel, device, setting): the attribute
 // stays with the function on that device, so later launches skip the driver calls.
 cudaError_t kernel_smem_attr(const void *func, int bytes, bool max_shared = false);
+// Allows a kernel clusters of more than the portable eight CTAs, once per (kernel, device).
+cudaError_t kernel_wide_clusters(const void *func);
 // Resident CTAs per SM of a kernel at `threads` threads and `smem` bytes of dynamic shared
 // memory, asked of the runtime once per (kernel, device, launch shape).
 cudaError_t kernel_occupancy(const void *func, int threads, size_t smem, int *blocks);

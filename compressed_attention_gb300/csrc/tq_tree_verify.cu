@@ -13,6 +13,8 @@
 // 10^-7, as much as a rare token has.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "tq_device.cuh"
 #include "tq_internal.h"
 
@@ -26,8 +28,14 @@ constexpr int VT = 512, VW = VT / 32;  // threads, warps of a CTA
 constexpr int MAX_CLUSTER = 16;
 constexpr uint64_t ONE = 1ull << 62;
 
-// A probability in multiples of 2^-62: [0, 1], NaN as 0.
-__device__ __forceinline__ uint64_t fix(float p) { return __float2ull_rz(fminf(fmaxf(p, 0.f), 1.f) * 0x1p62f); }
+// A probability in multiples of 2^-62: [0, 1], NaN as 0.  Its 24 bits in a word's upper end are 2^(e - 128) of 64 bits
+// with biased exponent e: shifts, where the conversion instruction to 64 bits has a fraction of their rate.
+__device__ __forceinline__ uint64_t fix(float p) {
+  const uint32_t b = __float_as_uint(fminf(fmaxf(p, 0.f), 1.f));
+  const uint64_t m = (uint64_t)((b << 8) | 0x80000000u) << 32;
+  const uint32_t e = b >> 23;  // at most 127; below 64 (and for 0) nothing is left
+  return e < 65 ? 0 : m >> (128 - e);
+}
 // floor(a b / 2^62), a < 2^63, b <= 2^62.
 __device__ __forceinline__ uint64_t mul62(uint64_t a, uint64_t b) { return __umul64hi(a << 1, b << 1); }
 // A random number in multiples of 2^-64.
@@ -39,6 +47,37 @@ __device__ __forceinline__ float prob(const void *row, int64_t w) {
   const uint16_t x = static_cast<const uint16_t *>(row)[w];
   return DT == TQ_DTYPE_BF16 ? bf16_bits_to_f32(x) : __half2float(__ushort_as_half(x));
 }
+
+// A row in groups of 16 bytes from the last 16-byte boundary at or before it: group g is elements g E - skip .. , of
+// which the first group and the last may lack some.
+template <int DT>
+struct Groups {
+  static constexpr int E = DT == TQ_DTYPE_F32 ? 4 : 8;
+  static __device__ __forceinline__ int skip(const void *row) {
+    return (int)(((uintptr_t)row & 15) / (DT == TQ_DTYPE_F32 ? 4 : 2));
+  }
+  static __device__ __forceinline__ float at(const uint4 &v, int e) {
+    const uint32_t w = DT == TQ_DTYPE_F32 ? (&v.x)[e] : (&v.x)[e >> 1];
+    if (DT == TQ_DTYPE_F32) return __uint_as_float(w);
+    const uint32_t x = (e & 1) ? w >> 16 : w & 0xFFFFu;
+    return DT == TQ_DTYPE_BF16 ? bf16_bits_to_f32(x) : __half2float(__ushort_as_half((uint16_t)x));
+  }
+  // Group g of a row of V elements with the skip of another row (`with`): one load where the two lie alike and
+  // the group is whole, else element by element; zeros outside the row.
+  static __device__ __forceinline__ uint4 load(const void *row, int g, int with, bool alike, int V) {
+    const int64_t w0 = (int64_t)g * E - with;
+    if (alike && w0 >= 0 && w0 + E <= V)
+      return __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(row) + w0 * (16 / E)));
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (w0 + e < 0 || w0 + e >= V) continue;
+      if (DT == TQ_DTYPE_F32) (&v.x)[e] = static_cast<const uint32_t *>(row)[w0 + e];
+      else (&v.x)[e >> 1] |= (uint32_t)static_cast<const uint16_t *>(row)[w0 + e] << (16 * (e & 1));
+    }
+    return v;
+  }
+};
 
 struct Shared {
   int32_t token[TREE_MAX];
@@ -52,7 +91,7 @@ struct Shared {
 };
 
 template <int DT, bool DRAFT>
-__global__ void __launch_bounds__(VT) k_tree_verify(const VerifyArgs a) {
+__global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
   __shared__ Shared sm;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank(), b = blockIdx.x / C;
@@ -111,18 +150,29 @@ __global__ void __launch_bounds__(VT) k_tree_verify(const VerifyArgs a) {
     return at;
   };
 
-  // this CTA's slice, and a warp's segment of it: whole runs of 32 weights
-  const int64_t s0 = (int64_t)V * rank / C, s1 = (int64_t)V * (rank + 1) / C;
-  const int seg = (((int)(s1 - s0) + VW - 1) / VW + 31) & ~31;
+  // The rows that the walk stands on, this CTA's groups of them, and a warp's: whole runs of 32 groups.
+  using Gr = Groups<DT>;
   int cur = 0, n_path = 1, fails = 0, pass = 0;
-  const void *prow = row_of(a.target, a.target_stride, 0), *qrow = DRAFT ? row_of(a.draft, a.draft_stride, 0) : nullptr;
-  // weight w of r after `fails` failed tests (no draft: without the taken-out tokens)
-  auto weight = [&](int64_t w) -> uint64_t {
-    uint64_t r = fix(prob<DT>(prow, w));
+  const void *prow, *qrow;
+  int skip, lo_g, hi_g, seg;
+  bool alike;
+  auto stand = [&](int node) {
+    prow = row_of(a.target, a.target_stride, node);
+    skip = Gr::skip(prow);
+    alike = true;
+    if (DRAFT) qrow = row_of(a.draft, a.draft_stride, node), alike = Gr::skip(qrow) == skip;
+    const int64_t n = ((int64_t)V + skip + Gr::E - 1) / Gr::E;
+    lo_g = (int)(n * rank / C), hi_g = (int)(n * (rank + 1) / C);
+    seg = ((hi_g - lo_g + VW - 1) / VW + 31) & ~31;
+  };
+  stand(0);
+  // r of one element after `fails` failed tests (no draft: the tokens taken out are the caller's)
+  auto weight = [&](float p, float q) -> uint64_t {
+    uint64_t r = fix(p);
     if (DRAFT && fails) {
-      const uint64_t q = fix(prob<DT>(qrow, w));
+      const uint64_t x = fix(q);
       for (int k = 0; k < fails; ++k) {
-        const uint64_t c = mul62(sm.z[k], q);
+        const uint64_t z = sm.z[k], c = z == ONE ? x : mul62(z, x);
         r = r > c ? r - c : 0;
       }
     }
@@ -135,14 +185,42 @@ __global__ void __launch_bounds__(VT) k_tree_verify(const VerifyArgs a) {
   };
   // sum r over the vocabulary, with the CTAs' sums and the warps' sums left in shared memory
   auto total = [&]() -> uint64_t {
-    const int64_t g0 = s0 + (int64_t)warp * seg, g1 = min(g0 + seg, s1);
+    const int g0 = lo_g + warp * seg, g1 = min(g0 + seg, hi_g);
     uint64_t sum = 0;
-#pragma unroll 8
-    for (int64_t w = g0 + lane; w < g1; w += 32) sum += weight(w);
+    auto add_up = [&](auto fly, auto with_q, auto f) {  // `fly` groups of a thread in flight
+      constexpr int FLY = decltype(fly)::value;
+#pragma unroll 1
+      for (int g = g0 + lane; g < g1; g += 32 * FLY) {
+        uint4 p4[FLY], q4[FLY];
+#pragma unroll
+        for (int i = 0; i < FLY; ++i) {
+          p4[i] = q4[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (g + 32 * i < g1) {
+            p4[i] = Gr::load(prow, g + 32 * i, skip, true, V);
+            if (decltype(with_q)::value) q4[i] = Gr::load(qrow, g + 32 * i, skip, alike, V);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < FLY; ++i)
+#pragma unroll
+          for (int e = 0; e < Gr::E; ++e) sum += f(Gr::at(p4[i], e), Gr::at(q4[i], e));
+      }
+    };
+    using Fly = std::integral_constant<int, DT == TQ_DTYPE_F32 ? 4 : 2>;
+    if (!DRAFT || !fails) {
+      add_up(Fly(), std::false_type(), [](float x, float) { return fix(x); });
+    } else if (fails == 1) {  // (the first test's Z is 1)
+      add_up(std::integral_constant<int, Fly::value / 2>(), std::true_type(), [](float x, float y) {
+        const uint64_t u = fix(x), v = fix(y);
+        return u > v ? u - v : 0;
+      });
+    } else {
+      add_up(std::integral_constant<int, 1>(), std::true_type(), weight);
+    }
     sum = warp_sum(sum);
     if (!DRAFT)  // less the tokens taken out (each once: a token again has failed before)
       for (int k = 0; k < fails; ++k) {
-        const int x = sm.token[sm.gone[k]];
+        const int x = (int)(((int64_t)sm.token[sm.gone[k]] + skip) / Gr::E);
         if (x >= g0 && x < g1) sum -= sm.p[sm.gone[k]];
       }
     if (lane == 0) sm.warp[warp] = sum;
@@ -177,11 +255,11 @@ __global__ void __launch_bounds__(VT) k_tree_verify(const VerifyArgs a) {
       take = __umul64hi(sm.u[c], Z) < r;
     }
     if (take) {
+      __syncthreads();  // (z, gone are read)
       cur = c, fails = 0, Z = ONE, have = false;
       if (rank == 0 && tid == 0) path[n_path] = c;
       ++n_path;
-      prow = row_of(a.target, a.target_stride, cur);
-      if (DRAFT) qrow = row_of(a.draft, a.draft_stride, cur);
+      stand(cur);
     } else if (DRAFT) {
       __syncthreads();  // (z is read)
       if (tid == 0) sm.z[fails] = Z;
@@ -220,14 +298,25 @@ __global__ void __launch_bounds__(VT) k_tree_verify(const VerifyArgs a) {
   if (tid == 0) a.next_token[b] = -1;  // (what the scan below always overwrites, unless sums of 2 and more wrapped around)
   int wseg = 0;
   while (wseg < VW - 1 && t >= sm.warp[wseg]) t -= sm.warp[wseg++];
-  const int64_t g0 = s0 + (int64_t)wseg * seg, g1 = min(g0 + seg, s1);
-  for (int64_t w0 = g0; w0 < g1; w0 += VT) {
-    const int64_t w = w0 + tid;
-    uint64_t r = w < g1 ? weight(w) : 0;
-    if (!DRAFT)
-      for (int k = 0; k < fails; ++k)
-        if (sm.token[sm.gone[k]] == w) r = 0;
-    uint64_t inc = r;
+  const int g0 = lo_g + wseg * seg, g1 = min(g0 + seg, hi_g);
+  for (int gb = g0; gb < g1; gb += VT) {  // a group per thread
+    const int g = gb + tid;
+    uint64_t r[Gr::E], mine = 0;
+    uint4 p4 = make_uint4(0u, 0u, 0u, 0u), q4 = p4;
+    if (g < g1) {
+      p4 = Gr::load(prow, g, skip, true, V);
+      if (DRAFT && fails) q4 = Gr::load(qrow, g, skip, alike, V);
+    }
+    const int64_t w0 = (int64_t)g * Gr::E - skip;
+#pragma unroll
+    for (int e = 0; e < Gr::E; ++e) {
+      r[e] = weight(Gr::at(p4, e), Gr::at(q4, e));
+      if (!DRAFT)
+        for (int k = 0; k < fails; ++k)
+          if (sm.token[sm.gone[k]] == w0 + e) r[e] = 0;
+      mine += r[e];
+    }
+    uint64_t inc = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const uint64_t o = __shfl_up_sync(FULL_MASK, inc, m);
@@ -235,12 +324,22 @@ __global__ void __launch_bounds__(VT) k_tree_verify(const VerifyArgs a) {
     }
     if (lane == 31) sm.scan[warp] = inc;
     __syncthreads();
-    uint64_t before = 0, all = 0;
+    uint64_t before = inc - mine, all = 0;
     for (int i = 0; i < VW; ++i) {
       if (i < warp) before += sm.scan[i];
       all += sm.scan[i];
     }
-    if (t >= before + inc - r && t < before + inc) a.next_token[b] = (int32_t)w;
+    if (t >= before && t - before < mine) {
+      uint64_t left = t - before;
+#pragma unroll
+      for (int e = 0; e < Gr::E; ++e) {
+        if (left < r[e]) {
+          a.next_token[b] = (int32_t)(w0 + e);
+          break;
+        }
+        left -= r[e];
+      }
+    }
     if (t < all) return;
     t -= all;
     __syncthreads();
@@ -251,7 +350,7 @@ template <int DT>
 cudaError_t launch(const VerifyArgs &a, int cluster, cudaStream_t st) {
   auto kern = a.draft ? k_tree_verify<DT, true> : k_tree_verify<DT, false>;
   if (cluster > 8) {
-    const cudaError_t e = cudaFuncSetAttribute((const void *)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = kernel_wide_clusters((const void *)kern);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -272,8 +371,9 @@ cudaError_t launch(const VerifyArgs &a, int cluster, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_tree_verify(const VerifyArgs &a, int num_sms, cudaStream_t st) {
-  (void)num_sms;
-  const int cluster = 8;
+  // As many CTAs per sequence as fill the SMs twice, up to a cluster's sixteen.
+  int cluster = MAX_CLUSTER;
+  while (cluster > 1 && (int64_t)cluster * a.B > 2 * num_sms) cluster >>= 1;
   if (a.dtype == TQ_DTYPE_F32) return launch<TQ_DTYPE_F32>(a, cluster, st);
   if (a.dtype == TQ_DTYPE_BF16) return launch<TQ_DTYPE_BF16>(a, cluster, st);
   return launch<TQ_DTYPE_F16>(a, cluster, st);

@@ -30,12 +30,14 @@ constexpr uint64_t ONE = 1ull << 62;
 
 // A probability in multiples of 2^-62: [0, 1], NaN as 0.  Its 24 bits in a word's upper end are 2^(e - 128) of 64 bits
 // with biased exponent e: shifts, where the conversion instruction to 64 bits has a fraction of their rate.
-__device__ __forceinline__ uint64_t fix(float p) {
-  const uint32_t b = __float_as_uint(fminf(fmaxf(p, 0.f), 1.f));
-  const uint64_t m = (uint64_t)((b << 8) | 0x80000000u) << 32;
-  const uint32_t e = b >> 23;  // at most 127; below 64 (and for 0) nothing is left
-  return e < 65 ? 0 : m >> (128 - e);
+__device__ __forceinline__ float clamp01(float p) { return fminf(fmaxf(p, 0.f), 1.f); }
+__device__ __forceinline__ uint64_t fix01(float p) {  // p in [0, 1]
+  const uint32_t b = __float_as_uint(p);
+  uint64_t r;  // (a shift past 64 leaves 0: exponents below 64, and 0)
+  asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"((uint64_t)((b << 8) | 0x80000000u) << 32), "r"(128u - (b >> 23)));
+  return r;
 }
+__device__ __forceinline__ uint64_t fix(float p) { return fix01(clamp01(p)); }
 // floor(a b / 2^62), a < 2^63, b <= 2^62.
 __device__ __forceinline__ uint64_t mul62(uint64_t a, uint64_t b) { return __umul64hi(a << 1, b << 1); }
 // A random number in multiples of 2^-64.
@@ -201,17 +203,29 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
           }
         }
 #pragma unroll
-        for (int i = 0; i < FLY; ++i)
+        for (int i = 0; i < FLY; ++i) {
+          float x[Gr::E], y[Gr::E];
+          uint32_t most = 0;
 #pragma unroll
-          for (int e = 0; e < Gr::E; ++e) sum += f(Gr::at(p4[i], e), Gr::at(q4[i], e));
+          for (int e = 0; e < Gr::E; ++e) {
+            x[e] = Gr::at(p4[i], e), y[e] = Gr::at(q4[i], e);
+            most = max(most, max(__float_as_uint(x[e]), __float_as_uint(y[e])));
+          }
+          if (most > 0x3F800000u) {  // past 1, negative or NaN
+#pragma unroll
+            for (int e = 0; e < Gr::E; ++e) x[e] = clamp01(x[e]), y[e] = clamp01(y[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < Gr::E; ++e) sum += f(x[e], y[e]);
+        }
       }
     };
     using Fly = std::integral_constant<int, DT == TQ_DTYPE_F32 ? 4 : 2>;
     if (!DRAFT || !fails) {
-      add_up(Fly(), std::false_type(), [](float x, float) { return fix(x); });
+      add_up(Fly(), std::false_type(), [](float x, float) { return fix01(x); });
     } else if (fails == 1) {  // (the first test's Z is 1)
       add_up(std::integral_constant<int, Fly::value / 2>(), std::true_type(), [](float x, float y) {
-        const uint64_t u = fix(x), v = fix(y);
+        const uint64_t u = fix01(x), v = fix01(y);
         return u > v ? u - v : 0;
       });
     } else {

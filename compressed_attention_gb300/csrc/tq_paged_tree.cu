@@ -55,7 +55,10 @@ struct Cfg {
   static constexpr int CH = 32;         // columns a thread takes at a time
   // Stages: packed tiles on their way (more of the values', which the K decoders need for their norms long before
   // the V decoders come to them), decoded K (tensor memory) and V (shared memory), scores, P.
-  static constexpr int NRAW_K = 3, NRAW_V = N == 128 ? 3 : 4;
+  static constexpr int NRAW_K = N == 32 ? 4 : 2, NRAW_V = 4;
+  // A stage of packed tiles always falls to the same group of decoders: copies may land out of order, and a group that
+  // had not waited for a stage's last phase could take its parity for the next one's.
+  static_assert(NRAW_K % 2 == 0 && NRAW_V % 2 == 0, "packed stages");
   static constexpr int NK = N == 128 ? 2 : (R == 64 ? 3 : 4), NV = N == 128 ? 2 : 3;
   static constexpr int NS = N == 128 ? 2 : (R == 64 ? 3 : 4), NP = N == 32 ? 4 : 2;
   static constexpr int NKN = NS + NK + 2;  // tiles whose norms are kept: see Misc
@@ -163,23 +166,22 @@ __device__ __forceinline__ bool next_item(const TreeView &v, Walk &w, Item &it) 
   }
   return false;
 }
-// Where a CTA's share starts.
-struct Start {
-  int b, u, off, left, v, V, G;
-};
-// One warp: all virtual tiles (flagging bad lengths), then the start of CTA c's share of `grid`.
-__device__ __noinline__ Start find_share(const TreeView &v, int lane, int c, int grid) {
-  int sum = 0;
-  for (int b = lane; b < v.pv.B; b += 32) sum += seq_vtiles(v, seq_of(v, b, c == 0));
-  Start w{};
-  w.V = __reduce_add_sync(FULL_MASK, sum);
-  w.G = min(grid, w.V);
-  if (c >= w.G) return w;
-  w.v = share_start(c, w.V, w.G);
-  w.left = share_start(c + 1, w.V, w.G) - w.v;
+// One warp: all virtual tiles (flagging bad lengths), then where this CTA's share of them starts.
+__device__ __forceinline__ void find_share(const TreeView &v, int lane, Walk &w, int &V, int &G) {
+  const bool flag = blockIdx.x == 0;
+  int t = seq_vtiles(v, seq_of(v, lane, flag)), sum = t;
+#pragma unroll 1
+  for (int b = lane + 32; b < v.pv.B; b += 32) sum += seq_vtiles(v, seq_of(v, b, flag));
+  V = __reduce_add_sync(FULL_MASK, sum);
+  G = min((int)gridDim.x, V);
+  w = Walk{};
+  if ((int)blockIdx.x >= G) return;
+  w.v = share_start(blockIdx.x, V, G);
+  w.left = share_start(blockIdx.x + 1, V, G) - w.v;
   int base = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < v.pv.B; b0 += 32) {
-    const int t = seq_vtiles(v, seq_of(v, b0 + lane, false));
+    if (b0) t = seq_vtiles(v, seq_of(v, b0 + lane, false));
     int inc = t;
 #pragma unroll
     for (int h = 1; h < 32; h <<= 1) {
@@ -195,230 +197,21 @@ __device__ __noinline__ Start find_share(const TreeView &v, int lane, int c, int
     }
     base += __shfl_sync(FULL_MASK, inc, 31);
   }
-  const int vt = seq_tiles(seq_of(v, w.b, false)) + ITEM_TILES;
+  walk_load(v, w);
+  const int vt = w.tiles + ITEM_TILES;
   w.u = w.off / vt;
   w.off -= w.u * vt;
-  return w;
-}
-
-// ------------------------------------------------------------------------------ preparation
-constexpr int PREP_WARPS = 16;
-struct PrepParams {
-  TreeView v;
-  RowsView q;
-  RopeView rope;
-  PagedOut o;
-  int Hq, R, parts;
-  float qmul;          // log2(e) * scale / alpha_K
-  const uint4 *kfrag;  // R of the keys
-  uint8_t *qh;         // [unit] operand images: two halves of 64 dims, rows of 128 bytes (columns' hi parts, then lo)
-  float *qsc;          // [unit][R] power-of-two scales, 0 for a column without a node
-  Start *start;        // [CTA of the attention]
-  int grid;            // its CTAs
-  uint4 *sees;         // [sequence][tile of nodes][node's key]: the columns that see it
-};
-struct PrepSmem {
-  uint4 r[2][8][8][32];               // R, bf16 hi and lo
-  uint16_t xs[PREP_WARPS][2][16][D];  // a warp's rows, bf16 hi and lo; 16-byte chunk c of row r at c ^ (r % 8)
-  uint64_t full;
-};
-
-// Which columns of tile qt see key 32 jw + lane of sequence b's nodes.
-__device__ __forceinline__ void see_bits(const PrepParams &p, int b, int qt, int jw, int lane) {
-  const Seq s = seq_of(p.v, b, false);
-  const int n0 = qt * p.v.npu;
-  if (n0 >= s.T) return;
-  uint32_t word[TREE_MAX / 32];  // lane l: ancestors 32 jw .. of nodes n0 + l, n0 + l + 32, ...
-#pragma unroll
-  for (int i = 0; i < TREE_MAX / 32; ++i) {
-    word[i] = 0;
-    const int local = 32 * i + lane;
-    if (local >= p.v.npu || n0 + local >= s.T || s.base + n0 + local < 0) continue;
-    for (int m = n0 + local; m >= 0; m = tree_parent(p.v.parents, s.row, m, p.v.pv.status, jw == 0))
-      if ((m >> 5) == jw) word[i] |= 1u << (m & 31);
-  }
-  uint32_t out[4] = {0, 0, 0, 0};
-  int node = 0, h = 0;
-#pragma unroll
-  for (int o = 0; o < 4; ++o) {
-#pragma unroll 1
-    for (int bit = 0; bit < 32 && 32 * o + bit < p.R; ++bit) {
-      const uint32_t w0 = node < 64 ? (node < 32 ? word[0] : word[1]) : (node < 96 ? word[2] : word[3]);
-      const uint32_t w = __shfl_sync(FULL_MASK, w0, node & 31);  // (node is the same in every lane)
-      if (node < p.v.npu) out[o] |= ((w >> lane) & 1u) << bit;
-      if (++h == p.v.gq) h = 0, ++node;
-    }
-  }
-  p.sees[((size_t)b * p.v.n_qt + qt) * TREE_MAX + 32 * jw + lane] = make_uint4(out[0], out[1], out[2], out[3]);
-}
-
-// R's fragments (64 KB) lie in shared memory once per CTA, from one bulk copy ahead of the wait; each warp takes tasks
-// by itself: 16 columns of a unit (loaded in rows, turned by position, split into bf16 parts in the warp's own
-// shared memory, multiplied by R in three products of parts, stored from the product's fragments), or the
-// bits of 32 keys.
-__global__ void __launch_bounds__(PREP_WARPS * 32) k_tree_prep(const PrepParams p) {
-  extern __shared__ __align__(128) uint8_t smem_prep[];
-  PrepSmem &sm = *reinterpret_cast<PrepSmem *>(smem_prep);
-  pdl_trigger();
-  if (threadIdx.x == 0) {
-    mbar_init(&sm.full, 1);
-    fence_mbar_init();
-    mbar_arrive_expect_tx(&sm.full, sizeof(sm.r));
-    bulk_g2s(&sm.r[0][0][0][0], p.kfrag, sizeof(sm.r), &sm.full);
-  }
-  __syncthreads();
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  auto &xs = sm.xs[warp];
-  const TreeView &v = p.v;
-  const int blocks = p.R / 16;
-  const int64_t q_tasks = (int64_t)v.pv.B * v.pv.Hkv * v.n_qt * blocks, see_tasks = (int64_t)v.pv.B * v.n_qt * 4;
-  const int64_t tasks = q_tasks + see_tasks + p.grid;
-  bool have_r = false;
-  // tasks over the CTAs first: a few use as many SMs as they can
-  for (int64_t task = (int64_t)warp * gridDim.x + blockIdx.x; task < tasks; task += (int64_t)PREP_WARPS * gridDim.x) {
-    if (task >= q_tasks + see_tasks) {
-      const int c = (int)(task - q_tasks - see_tasks);
-      const Start st = find_share(v, lane, c, p.grid);
-      if (lane == 0) p.start[c] = st;
-      continue;
-    }
-    if (task >= q_tasks) {
-      const int x = (int)(task - q_tasks), bq = x >> 2;
-      see_bits(p, bq / v.n_qt, bq % v.n_qt, x & 3, lane);
-      continue;
-    }
-    const int unit = (int)(task / blocks), c0 = 16 * (int)(task - (int64_t)unit * blocks);
-    const int qt = unit % v.n_qt, bh = unit / v.n_qt, b = bh / v.pv.Hkv, h = bh - b * v.pv.Hkv;
-    const Seq s = seq_of(v, b, false);
-    if (qt * v.npu >= s.T) continue;
-    // lane i < 16: column c0 + i
-    int my_turn = 0;
-    uint64_t my_src = 0;
-    if (lane < 16) {
-      const int c = c0 + lane, local = c / v.gq, node = qt * v.npu + local, head = h * v.gq + c - local * v.gq;
-      if (local < v.npu && node < s.T) {
-        const int tok = s.row + node;
-        if (s.base + node >= 0) {
-          my_src = (uint64_t)(uintptr_t)(p.q.data + tok * p.q.token_bytes + head * p.q.head_bytes);
-          if (p.rope.rot_dim)
-            my_turn = rope_pos(p.rope, tree_pos(v.pv, v.parents, b, tok, s.base + node, true), v.pv.status, true);
-        }
-      }
-    }
-    __syncwarp();  // the last task's fragments are read
-    constexpr int NR = 8;
-#pragma unroll 1
-    for (int rb = 0; rb < 16; rb += NR) {  // eight rows' loads in flight
-      float x[NR][4];
-      {
-        uint4 raw[NR];
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const uint8_t *src = reinterpret_cast<const uint8_t *>((uintptr_t)__shfl_sync(FULL_MASK, my_src, rb + i));
-          raw[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (src) raw[i] = load_lane4_raw(src, p.q.dtype, lane);
-        }
-#pragma unroll
-        for (int i = 0; i < NR; ++i) lane4_floats(raw[i], p.q.dtype, x[i]);
-      }
-      if (p.rope.rot_dim) {
-        int turn = -1;
-        LaneAngles an;
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const int mine = __shfl_sync(FULL_MASK, my_turn, rb + i);
-          if (mine != turn) an = rope_angles(lane, p.rope, turn = mine);  // (a node's heads share theirs)
-          rope_turn(x[i], lane, p.rope, an);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        uint32_t hi[2], lo[2];
-        float f[4];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          hi[m] = pack_bf162(x[i][2 * m], x[i][2 * m + 1]);
-          f[2 * m] = __uint_as_float(hi[m] << 16), f[2 * m + 1] = __uint_as_float(hi[m] & 0xFFFF0000u);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = isinf(f[e]) ? x[i][e] = 0.f : f[e];  // an infinite part has no rest
-#pragma unroll
-        for (int m = 0; m < 2; ++m) lo[m] = pack_bf162(x[i][2 * m] - f[2 * m], x[i][2 * m + 1] - f[2 * m + 1]);
-        const int at = 8 * ((lane >> 1) ^ i) + 4 * (lane & 1);  // NR rows: i is the row modulo 8
-        *reinterpret_cast<uint2 *>(&xs[0][rb + i][at]) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2 *>(&xs[1][rb + i][at]) = make_uint2(lo[0], lo[1]);
-      }
-    }
-    __syncwarp();
-    if (!have_r) {
-      if (!mbar_wait_bounded(&sm.full, 0, WAIT_LIMIT_NS)) {
-        if (lane == 0) atomicExch(v.pv.status, (int32_t)DEVERR_TIMEOUT);
-        return;
-      }
-      have_r = true;
-    }
-    // Y = X R^T; R's A fragments hold the B fragments of two column tiles each: registers (0, 2)
-    // and (1, 3)
-    float acc[16][4];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-#pragma unroll 2
-    for (int k = 0; k < 8; ++k) {
-      uint4 a[2];
-#pragma unroll
-      for (int part = 0; part < 2; ++part) a[part] = ldmatrix_x4(&xs[part][lane & 15][8 * ((2 * k + (lane >> 4)) ^ (lane & 7))]);
-#pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        const uint4 rh = sm.r[0][m][k][lane], rl = sm.r[1][m][k][lane];
-        mma_bf16(acc[2 * m], a[0], rh.x, rh.z), mma_bf16(acc[2 * m + 1], a[0], rh.y, rh.w);
-        mma_bf16(acc[2 * m], a[1], rh.x, rh.z), mma_bf16(acc[2 * m + 1], a[1], rh.y, rh.w);
-        mma_bf16(acc[2 * m], a[0], rl.x, rl.z), mma_bf16(acc[2 * m + 1], a[0], rl.y, rl.w);
-      }
-    }
-    // columns g and g + 8 of the task, dims 8 j + 2 t and the next
-    uint8_t *image = p.qh + (size_t)unit * p.R * p.parts * 256;
-    const uint32_t half_bytes = p.R * p.parts * 128;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool live = __shfl_sync(FULL_MASK, my_src, g + 8 * i) != 0;
-      float m = 0.f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        acc[j][2 * i] *= p.qmul, acc[j][2 * i + 1] *= p.qmul;
-        m = fmaxf(m, fmaxf(fabsf(acc[j][2 * i]), fabsf(acc[j][2 * i + 1])));
-      }
-      m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, 2));
-      // The power of two that brings the largest element to [2^13, 2^14); none for rows of ordinary size, of
-      // which fp16 drops what is below 2^-14 of the largest element, and two parts what is below 2^-20 of it.
-      const bool as_is = m >= (p.parts == 2 ? 0x1p-4f : 0x1p-10f) && m < 0x1p14f;
-      const int e = as_is ? 0 : scale_exp(m), row = c0 + g + 8 * i;
-      const float down = pow2i(-e);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        uint32_t hi, lo;
-        split_half2(acc[j][2 * i] * down, acc[j][2 * i + 1] * down, hi, lo);
-        uint8_t *dst = image + (j >> 3) * half_bytes + row * 128 + (((j & 7) ^ (row & 7)) << 4) + 4 * t;
-        *reinterpret_cast<uint32_t *>(dst) = hi;
-        if (p.parts == 2) *reinterpret_cast<uint32_t *>(dst + p.R * 128) = lo;
-      }
-      if (t == 0) p.qsc[(size_t)unit * p.R + row] = live ? pow2i(e) : 0.f;
-    }
-  }
-  // (a CTA without columns: R's copy must land before it ends)
-  if (!have_r && threadIdx.x == 0) (void)mbar_wait_bounded(&sm.full, 0, WAIT_LIMIT_NS);
 }
 
 // ------------------------------------------------------------------------------ attention
 struct PartialParams {
   TreeView v;
   const uint8_t *kp, *vp;
+  RowsView q;
+  RopeView rope;
   int Hq;
-  const uint8_t *qh;
-  const float *qsc;
-  const uint4 *sees;
-  const Start *start;
+  float qmul;          // log2(e) * scale / alpha_K
+  const uint4 *kfrag;  // R of the keys
   uint32_t klo[2], khi[2], vlo[2], vhi[2];
   float *split;   // [CTA][2][R] partials of units that several CTAs share
   float *whole;   // [row][Hq] partials of units one CTA finished
@@ -431,12 +224,14 @@ struct Misc {
   uint64_t k_full[4], k_empty[4], v_full[3], v_empty[3];
   uint64_t s_done[4], s_free[4];      // [buffer]
   uint64_t p_ready[4], pv_done[4];    // [buffer of P]
-  uint64_t q_full, q_empty, o_free, drain[2];
+  uint64_t q_full, o_free, drain[2];
   // Norms of the last tiles, both written by the K decoders, so that the softmax waits for no values.  Tile j is
   // decoded once the scores of tile j - NK are done, and those once the softmax has read the scores, and with them the
   // norms, of tile j - NK - NS.
   float kn[NKN][KT], nv[NKN][KT];
-  alignas(16) float nm[2][64], qs[2][64];  // [group] minus the running maxima (less W_SHIFT; none yet: 0), scales of q
+  alignas(16) float nm[2][64];  // [group] minus the running maxima (less W_SHIFT; none yet: 0)
+  float qs[64], qd[64];   // the columns' powers of two (0 without a node), what R q is held times
+  uint32_t anc[64][TREE_MAX / 32];  // the unit's nodes: ancestors and the node itself
   float4 move[2][32];     // and, where maxima are raised: what the scores fall by, the square root of O's factor
   float mx[2][64];        // the running maxima, -infinity without one
   float red[2][4][64];    // [group][warp][column]
@@ -479,6 +274,7 @@ __device__ __forceinline__ bool group_or(int gr, bool x) {
   return r != 0;
 }
 
+__device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 // Barrier of both softmax groups that ORs a flag across them.
 __device__ __forceinline__ bool both_or(bool x) {
   uint32_t r;
@@ -547,7 +343,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
     for (int i = 0; i < NV; ++i) mbar_init(&ms.v_full[i], 4), mbar_init(&ms.v_empty[i], 1);
     for (int i = 0; i < NS; ++i) mbar_init(&ms.s_done[i], 1), mbar_init(&ms.s_free[i], 4);
     for (int i = 0; i < NP; ++i) mbar_init(&ms.p_ready[i], 4), mbar_init(&ms.pv_done[i], 1);
-    mbar_init(&ms.q_full, 1), mbar_init(&ms.q_empty, 1), mbar_init(&ms.o_free, 8);
+    mbar_init(&ms.q_full, 8), mbar_init(&ms.o_free, 8);
     mbar_init(&ms.drain[0], 1), mbar_init(&ms.drain[1], 1);
     for (int i = 0; i < NITEM; ++i) mbar_init(&ms.item_full[i], 1), mbar_init(&ms.item_empty[i], THREADS / 32 - 1);
     ms.abort_flag = 0;
@@ -592,10 +388,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
       const uint8_t *pages = side ? p.vp : p.kp;
       Walk w;
       if (!side) {
-        const Start st = p.start[blockIdx.x];
-        w.b = st.b, w.u = st.u, w.off = st.off, w.left = st.left, w.v = st.v;
-        if (w.left) walk_load(p.v, w);
-        if (lane == 0) ms.V = st.V, ms.G = st.G;
+        int V, G;
+        find_share(p.v, lane, w, V, G);
+        if (lane == 0) ms.V = V, ms.G = G;
       }
       auto publish = [&]() -> bool {  // the keys' loader walks its share for all
         const uint32_t i = n_items % NITEM;
@@ -708,21 +503,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
         }
       }
     } else if (warp == W_S) {
-      // ================ issuer of the scores, as far ahead as their buffers go; q's image once the last item's are done
+      // ================ issuer of the scores, as far ahead as their buffers go
       const bool lead = elect_lane();
       const uint32_t tb = __shfl_sync(FULL_MASK, tmem, 0), tS = tb + F::TM_S, tK = tb + F::TM_K;
       const uint64_t dq = sw128_desc(smem_addr(smem + F::OFF_Q));
       uint32_t n = 0, items = 0;
-      bool issued = false, q_ok = true;
+      bool issued = false;
       while (ok && next()) {
-        if (items) ok = __all_sync(FULL_MASK, wait(&ms.q_empty, (items - 1) & 1));
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&ms.q_full, F::Q_BYTES);
-          bulk_g2s(smem + F::OFF_Q, p.qh + (size_t)unit_index(p.v, it.b, it.h, it.qt) * F::Q_BYTES, F::Q_BYTES, &ms.q_full);
-        }
-        __syncwarp();
-        q_ok = ok = __all_sync(FULL_MASK, wait(&ms.q_full, items & 1));
+        ok = __all_sync(FULL_MASK, wait(&ms.q_full, items & 1));
         for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
           const uint32_t st = n % NK, sb = n % NS;
           if (n >= NS) ok = wait(&ms.s_free[sb], ((n / NS) - 1) & 1);
@@ -738,18 +526,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
                                     desc_step(dq, (s >> 2) * F::Q_HALF + part * R * 128 + (s & 3) * 32), (part || s) ? 1u : 0u);
             umma_commit(&ms.s_done[sb]);
             umma_commit(&ms.k_empty[st]);
-            if (j == it.t1 - 1) umma_commit(&ms.q_empty);
           }
           __syncwarp();
           issued = true;
         }
         ++items;
       }
-      // after a failed wait: the copy of q and the products in flight end before the CTA does
-      if (*reinterpret_cast<volatile int *>(&ms.abort_flag)) {
-        if (!q_ok) (void)mbar_wait_bounded(&ms.q_full, items & 1, WAIT_LIMIT_NS);
-        if (issued && lead) umma_commit(&ms.drain[0]), (void)mbar_wait_bounded(&ms.drain[0], 0, WAIT_LIMIT_NS);
-      }
+      if (issued && lead && *reinterpret_cast<volatile int *>(&ms.abort_flag))
+        umma_commit(&ms.drain[0]), (void)mbar_wait_bounded(&ms.drain[0], 0, WAIT_LIMIT_NS);
     } else if (warp == W_PV) {
       // ================ issuer of O^T
       const bool lead = elect_lane();
@@ -793,11 +577,117 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
     while (next()) {
       const int unit = unit_index(p.v, it.b, it.h, it.qt), n0 = it.qt * p.v.npu;
       const int cols = min(it.s.T - n0, p.v.npu) * p.v.gq;  // columns with a node
+      // ---- q: rows turned by their nodes' positions, split into bf16 parts in P's buffers (free between items),
+      // times R on the tensor cores (m16n8k16, three products of parts), as fp16 parts in the image of the operand
+      {
+        constexpr int RW = R / 8;  // columns of a warp
+        uint8_t *const xs = smem + F::OFF_P;  // bf16 hi of the columns, then lo; 16-byte chunk c of column r at c ^ (r % 8)
+        int my_turn = 0;
+        uint64_t my_src = 0;
+        const int my_c = warp * RW + lane, my_local = my_c / p.v.gq, my_node = n0 + my_local;
+        if (lane < RW && my_c < cols && it.s.base + my_node >= 0)
+          my_src = (uint64_t)(uintptr_t)(p.q.data + (it.s.row + my_node) * p.q.token_bytes +
+                                         (it.h * p.v.gq + my_c - my_local * p.v.gq) * p.q.head_bytes);
+        // the rows and then their angles are on their way before the first is taken
+        const int row_bytes = p.q.dtype == TQ_DTYPE_F32 ? 512 : 256;
+#pragma unroll 1
+        for (int i = 0; i < RW; ++i) {
+          const uint64_t src = __shfl_sync(FULL_MASK, my_src, i);
+          if (src && 32 * lane < row_bytes) prefetch_l1(reinterpret_cast<const uint8_t *>((uintptr_t)src) + 32 * lane);
+        }
+        if (p.rope.rot_dim) {
+          if (my_src)
+            my_turn = rope_pos(p.rope, tree_pos(p.v.pv, p.v.parents, it.b, it.s.row + my_node, it.s.base + my_node, true), p.v.pv.status, true);
+#pragma unroll 1
+          for (int i = 0; i < RW; ++i) {
+            const size_t at = (size_t)__shfl_sync(FULL_MASK, my_turn, i) * (p.rope.rot_dim >> 1) + 8 * (lane & 7);
+            if (lane < 16 && 8 * (lane & 7) < (p.rope.rot_dim >> 1)) prefetch_l1((lane < 8 ? p.rope.cos_t : p.rope.sin_t) + at);
+          }
+        }
+#pragma unroll 1
+        for (int i = 0; i < RW; ++i) {
+          const uint8_t *src = reinterpret_cast<const uint8_t *>((uintptr_t)__shfl_sync(FULL_MASK, my_src, i));
+          float x[4] = {0.f, 0.f, 0.f, 0.f};
+          if (src) load_lane4(src, p.q.dtype, lane, x);
+          rope_lane4(x, lane, p.rope, __shfl_sync(FULL_MASK, my_turn, i));
+          {
+            const int c = warp * RW + i;
+            float big = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+            big = __uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(big)));  // ordered like the floats
+            // R q is at most sqrt(128) times the largest element: held times a power of two that brings that to
+            // [2^10, 2^11); times none where it lies between, of ordinary size, so that one part drops what is below
+            // 2^-14 of the row's norm, two parts what is below 2^-20 of it.
+            const float m = big * fabsf(p.qmul);
+            const int e = m >= (PARTS == 2 ? 0x1p-4f : 0x1p-8f) && m < 0x1p11f ? 0 : scale_exp(m) + 3;
+            if (lane == 0) ms.qs[c] = src ? pow2i(e) : 0.f, ms.qd[c] = p.qmul * pow2i(-e);
+            uint32_t hi[2], lo[2];
+            float f[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              hi[k] = pack_bf162(x[2 * k], x[2 * k + 1]);
+              f[2 * k] = __uint_as_float(hi[k] << 16), f[2 * k + 1] = __uint_as_float(hi[k] & 0xFFFF0000u);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[k] = isinf(f[k]) ? x[k] = 0.f : f[k];  // an infinite part has no rest
+#pragma unroll
+            for (int k = 0; k < 2; ++k) lo[k] = pack_bf162(x[2 * k] - f[2 * k], x[2 * k + 1] - f[2 * k + 1]);
+            uint8_t *dst = xs + c * 256 + (((lane >> 1) ^ (c & 7)) << 4) + 8 * (lane & 1);
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(dst + R * 256) = make_uint2(lo[0], lo[1]);
+          }
+        }
+        // whom the nodes see of one another: only a share with the last tiles asks
+        if (it.t1 * KT > it.s.base && tid < p.v.npu) {
+          uint32_t word[TREE_MAX / 32] = {};
+          for (int m = n0 + tid < it.s.T ? n0 + tid : -1; m >= 0; m = tree_parent(p.v.parents, it.s.row, m, p.v.pv.status, true)) {
+#pragma unroll
+            for (int i = 0; i < TREE_MAX / 32; ++i) word[i] |= (m >> 5) == i ? 1u << (m & 31) : 0u;
+          }
+          *reinterpret_cast<uint4 *>(ms.anc[tid]) = make_uint4(word[0], word[1], word[2], word[3]);
+        }
+        uint4 rh[8], rl[8];  // this warp's 16 rows of R
+        rot_load(rh, p.kfrag, 0, 0, warp, lane);
+        rot_load(rl, p.kfrag, 0, 1, warp, lane);
+        (void)both_or(false);
+        const int g = lane >> 2, t4 = lane & 3;
+#pragma unroll 1
+        for (int c0 = 0; c0 < R; c0 += 8) {
+          float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint8_t *col = xs + (c0 + g) * 256 + 4 * t4;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t o0 = (uint32_t)((2 * k) ^ g) << 4, o1 = (uint32_t)((2 * k + 1) ^ g) << 4;
+            const uint32_t h0 = *reinterpret_cast<const uint32_t *>(col + o0), h1 = *reinterpret_cast<const uint32_t *>(col + o1);
+            const uint32_t l0 = *reinterpret_cast<const uint32_t *>(col + R * 256 + o0), l1 = *reinterpret_cast<const uint32_t *>(col + R * 256 + o1);
+            mma_bf16(acc, rh[k], h0, h1), mma_bf16(acc2, rh[k], l0, l1), mma_bf16(acc2, rl[k], h0, h1);
+          }
+          // dims 16 warp + g and + 8, columns c0 + 2 t4 and the next
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c = c0 + 2 * t4 + i;
+            const float mul = ms.qd[c];
+            const float a = (acc[i] + acc2[i]) * mul, b = (acc[2 + i] + acc2[2 + i]) * mul;
+            uint32_t hi, lo;
+            split_half2(a, b, hi, lo);
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+              const uint32_t w = part ? lo : hi;
+              uint8_t *dst = smem + F::OFF_Q + (warp >> 2) * F::Q_HALF + (part * R + c) * 128;
+              const int ch = 2 * (warp & 3);
+              *reinterpret_cast<uint16_t *>(dst + ((ch ^ (c & 7)) << 4) + 2 * g) = (uint16_t)w;
+              *reinterpret_cast<uint16_t *>(dst + (((ch + 1) ^ (c & 7)) << 4) + 2 * g) = (uint16_t)(w >> 16);
+            }
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.q_full);
+      }
       // no column has a maximum yet; those without a node keep 0
       bool scale = false;
       if (key < R) {
-        const float sc = p.qsc[(size_t)unit * R + key];
-        ms.qs[gr][key] = sc, nm[key] = 0.f;
+        const float sc = ms.qs[key];
+        nm[key] = 0.f;
         ms.mx[gr][key] = sc == 0.f ? 0.f : -INFINITY;
         scale = sc != 0.f && sc != 1.f;
       }
@@ -824,10 +714,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
         uint32_t see[R / 32];
 #pragma unroll
         for (int i = 0; i < R / 32; ++i) see[i] = ~0u;
-        if (!whole && j >= 0) {
-          const uint32_t *src = reinterpret_cast<const uint32_t *>(p.sees + ((size_t)it.b * p.v.n_qt + it.qt) * TREE_MAX + j);
+        if (!whole && j >= 0) {  // a node's key: the columns of the nodes that have it among their ancestors
+          uint64_t bits = 0;
+          if (t < it.s.len && j < TREE_MAX) {
+            const uint64_t node_cols = p.v.gq < 64 ? (1ull << p.v.gq) - 1 : ~0ull;
+#pragma unroll 1
+            for (int i = 0, c2 = 0; c2 < cols; ++i, c2 += p.v.gq)
+              if ((ms.anc[i][j >> 5] >> (j & 31)) & 1u) bits |= node_cols << c2;
+          }
 #pragma unroll
-          for (int i = 0; i < R / 32; ++i) see[i] = t < it.s.len && j < TREE_MAX ? src[i] : 0u;
+          for (int i = 0; i < R / 32; ++i) see[i] = (uint32_t)(bits >> (32 * i));
         }
         bool some = false;
         uint8_t *const pb = smem + F::OFF_P + ps * F::P_BYTES;
@@ -844,7 +740,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
           }
           if (scaled) {
 #pragma unroll
-            for (int e = 0; e < CH; ++e) d[e] *= ms.qs[gr][cc + e];
+            for (int e = 0; e < CH; ++e) d[e] *= ms.qs[cc + e];
           }
 #pragma unroll
           for (int e = 0; e < CH; e += 2) {
@@ -1143,25 +1039,21 @@ __global__ void __launch_bounds__(CB_WARPS * 32) k_tree_combine(const CombinePar
 struct Layout {
   int R, parts, npu, n_qt, gq, grid;
   int64_t units;
-  size_t qsc, sees, start, unit, split, whole, bytes;
+  size_t unit, split, whole, bytes;
 };
 bool layout(const tq_ctx *k, const PagedView &pv, int Hq, int out_dtype, Layout *l) {
   l->gq = Hq / pv.Hkv;
   l->parts = out_dtype == TQ_DTYPE_BF16 ? 1 : 2;
-  const int rows = pv.max_q * l->gq;
-  l->R = rows <= 32 ? 32 : 64;
+  l->R = pv.max_q * l->gq <= 32 ? 32 : 64;
   l->npu = l->R / l->gq;  // at least one: 64 heads per KV head at most
   l->n_qt = (pv.max_q + l->npu - 1) / l->npu;
   l->grid = k->num_sms;
   l->units = (int64_t)pv.B * pv.Hkv * l->n_qt;
   const int64_t tiles = l->units * (((int64_t)pv.max_len + KT - 1) / KT + ITEM_TILES);
-  if (l->grid > 65535 || tiles > INT32_MAX || (int64_t)pv.n_tokens * Hq > INT32_MAX || l->units > INT32_MAX / 8) return false;
+  if (l->grid > 65535 || tiles > INT32_MAX || (int64_t)pv.n_tokens * Hq > INT32_MAX) return false;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  l->qsc = up((size_t)l->units * l->R * l->parts * 256);
-  l->sees = l->qsc + up((size_t)l->units * l->R * 4);
-  l->start = l->sees + up((size_t)pv.B * l->n_qt * TREE_MAX * 16);
-  l->unit = l->start + up((size_t)l->grid * sizeof(Start));
-  l->split = l->unit + up((size_t)l->units * 4);
+  l->unit = 0;
+  l->split = up((size_t)l->units * 4);
   l->whole = l->split + up((size_t)l->grid * 2 * l->R * PROW * 4);
   l->bytes = l->whole + up((size_t)pv.n_tokens * Hq * PROW * 4);
   return true;
@@ -1197,24 +1089,10 @@ cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView 
   if (!layout(k, pv, Hq, o.dtype, &l)) return cudaErrorInvalidValue;
   uint8_t *base = static_cast<uint8_t *>(ws);
   const TreeView tv{pv, parents, l.npu, l.n_qt, l.gq};
-  PrepParams a{};
-  a.v = tv, a.q = q, a.rope = rope, a.o = o;
-  a.Hq = Hq, a.R = l.R, a.parts = l.parts;
-  a.qmul = LOG2E * scale / k->f16.alpha;
-  a.kfrag = k->d_rfrag;
-  a.qh = base;
-  a.qsc = reinterpret_cast<float *>(base + l.qsc);
-  a.sees = reinterpret_cast<uint4 *>(base + l.sees);
-  a.start = reinterpret_cast<Start *>(base + l.start), a.grid = l.grid;
-  cudaError_t e = kernel_smem_attr((const void *)k_tree_prep, (int)sizeof(PrepSmem));
-  if (e != cudaSuccess) return e;
-  const int64_t tasks = l.units * (l.R / 16) + (int64_t)pv.B * l.n_qt * 4 + l.grid;
-  e = launch_pdl(k_tree_prep, dim3((unsigned)(tasks < k->num_sms ? tasks : k->num_sms)), dim3(PREP_WARPS * 32),
-                 sizeof(PrepSmem), st, a);
-  if (e != cudaSuccess) return e;
   PartialParams p{};
-  p.v = tv, p.kp = kp, p.vp = vp, p.Hq = Hq;
-  p.qh = a.qh, p.qsc = a.qsc, p.sees = a.sees, p.start = a.start;
+  p.v = tv, p.kp = kp, p.vp = vp, p.q = q, p.rope = rope, p.Hq = Hq;
+  p.qmul = LOG2E * scale / k->f16.alpha;
+  p.kfrag = k->d_rfrag;
   for (int i = 0; i < 2; ++i) {
     p.klo[i] = k->f16.lo[i], p.khi[i] = k->f16.hi[i];
     p.vlo[i] = v->f16.lo[i], p.vhi[i] = v->f16.hi[i];
@@ -1222,6 +1100,7 @@ cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView 
   p.split = reinterpret_cast<float *>(base + l.split);
   p.whole = reinterpret_cast<float *>(base + l.whole);
   p.unit = reinterpret_cast<int32_t *>(base + l.unit);
+  cudaError_t e;
   if (l.parts == 1)
     e = l.R == 32 ? launch_partial<32, 1>(p, l.grid, st) : launch_partial<64, 1>(p, l.grid, st);
   else

@@ -39,7 +39,7 @@ namespace tq {
 namespace {
 
 constexpr int KT = 128;          // keys per tile
-constexpr int ITEM_TILES = 3;    // cost of an item ahead of its tiles, in tiles
+constexpr int ITEM_TILES = 6;    // cost of an item ahead of its tiles, in tiles
 constexpr int RAW = KT * PG_ROW; // a packed tile
 constexpr int PROW = D + 4;      // floats of a partial: acc[128], max (less W_SHIFT), sum, 2 spare
 constexpr int W_KDEC = 8, W_VDEC = 16, W_PV = 24, W_LOAD = 25, W_S = 27, THREADS = 896;  // (W_LOAD: keys, then values)
@@ -224,12 +224,14 @@ struct Misc {
   uint64_t k_full[4], k_empty[4], v_full[3], v_empty[3];
   uint64_t s_done[4], s_free[4];      // [buffer]
   uint64_t p_ready[4], pv_done[4];    // [buffer of P]
-  uint64_t q_full, o_free, drain[2];
+  uint64_t q_known, q_full, o_free, drain[2];
   // Norms of the last tiles, both written by the K decoders, so that the softmax waits for no values.  Tile j is
   // decoded once the scores of tile j - NK are done, and those once the softmax has read the scores, and with them the
   // norms, of tile j - NK - NS.
   float kn[NKN][KT], nv[NKN][KT];
   alignas(16) float nm[2][64];  // [group] minus the running maxima (less W_SHIFT; none yet: 0)
+  uint64_t q_src[64];     // the columns' rows of q (0 without a node) and the positions they are turned by
+  int q_turn[64];
   float qs[64], qd[64];   // the columns' powers of two (0 without a node), what R q is held times
   uint32_t anc[64][TREE_MAX / 32];  // the unit's nodes: ancestors and the node itself
   float4 move[2][32];     // and, where maxima are raised: what the scores fall by, the square root of O's factor
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
     for (int i = 0; i < NV; ++i) mbar_init(&ms.v_full[i], 4), mbar_init(&ms.v_empty[i], 1);
     for (int i = 0; i < NS; ++i) mbar_init(&ms.s_done[i], 1), mbar_init(&ms.s_free[i], 4);
     for (int i = 0; i < NP; ++i) mbar_init(&ms.p_ready[i], 4), mbar_init(&ms.pv_done[i], 1);
-    mbar_init(&ms.q_full, 8), mbar_init(&ms.o_free, 8);
+    mbar_init(&ms.q_known, 1), mbar_init(&ms.q_full, 8), mbar_init(&ms.o_free, 8);
     mbar_init(&ms.drain[0], 1), mbar_init(&ms.drain[1], 1);
     for (int i = 0; i < NITEM; ++i) mbar_init(&ms.item_full[i], 1), mbar_init(&ms.item_empty[i], THREADS / 32 - 1);
     ms.abort_flag = 0;
@@ -510,6 +512,30 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
       uint32_t n = 0, items = 0;
       bool issued = false;
       while (ok && next()) {
+        // where the columns' rows of q lie and their positions: found ahead of the softmax warps, which are still on
+        // the last item, with the rows and the angles sent for
+        const int n0 = it.qt * p.v.npu, cols = min(it.s.T - n0, p.v.npu) * p.v.gq;
+#pragma unroll 1
+        for (int c = lane; c < R; c += 32) {
+          const int local = c / p.v.gq, node = n0 + local;
+          uint64_t src = 0;
+          int turn = 0;
+          if (c < cols && it.s.base + node >= 0) {
+            const uint8_t *row = p.q.data + (it.s.row + node) * p.q.token_bytes + (it.h * p.v.gq + c - local * p.v.gq) * p.q.head_bytes;
+            src = (uint64_t)(uintptr_t)row;
+            prefetch_l1(row), prefetch_l1(row + 128);
+            if (p.q.dtype == TQ_DTYPE_F32) prefetch_l1(row + 256), prefetch_l1(row + 384);
+            if (p.rope.rot_dim) {
+              turn = rope_pos(p.rope, tree_pos(p.v.pv, p.v.parents, it.b, it.s.row + node, it.s.base + node, true), p.v.pv.status, true);
+              const size_t at = (size_t)turn * (p.rope.rot_dim >> 1);
+              prefetch_l1(p.rope.cos_t + at), prefetch_l1(p.rope.sin_t + at);
+              if (p.rope.rot_dim == 128) prefetch_l1(p.rope.cos_t + at + 32), prefetch_l1(p.rope.sin_t + at + 32);
+            }
+          }
+          ms.q_src[c] = src, ms.q_turn[c] = turn;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.q_known);
         ok = __all_sync(FULL_MASK, wait(&ms.q_full, items & 1));
         for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
           const uint32_t st = n % NK, sb = n % NS;
@@ -574,7 +600,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
     float *const nm = ms.nm[gr];
     float4 *const mv = ms.move[gr];
     uint32_t n = 0;  // tiles before the item
-    while (next()) {
+    for (uint32_t items = 0;; ++items) {
+      uint4 rh[8], rl[8];  // this warp's 16 rows of R, on their way while the item is waited for
+      rot_load(rh, p.kfrag, 0, 0, warp, lane);
+      rot_load(rl, p.kfrag, 0, 1, warp, lane);
+      if (!next()) break;
       const int unit = unit_index(p.v, it.b, it.h, it.qt), n0 = it.qt * p.v.npu;
       const int cols = min(it.s.T - n0, p.v.npu) * p.v.gq;  // columns with a node
       // ---- q: rows turned by their nodes' positions, split into bf16 parts in P's buffers (free between items),
@@ -582,34 +612,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
       {
         constexpr int RW = R / 8;  // columns of a warp
         uint8_t *const xs = smem + F::OFF_P;  // bf16 hi of the columns, then lo; 16-byte chunk c of column r at c ^ (r % 8)
-        int my_turn = 0;
-        uint64_t my_src = 0;
-        const int my_c = warp * RW + lane, my_local = my_c / p.v.gq, my_node = n0 + my_local;
-        if (lane < RW && my_c < cols && it.s.base + my_node >= 0)
-          my_src = (uint64_t)(uintptr_t)(p.q.data + (it.s.row + my_node) * p.q.token_bytes +
-                                         (it.h * p.v.gq + my_c - my_local * p.v.gq) * p.q.head_bytes);
-        // the rows and then their angles are on their way before the first is taken
-        const int row_bytes = p.q.dtype == TQ_DTYPE_F32 ? 512 : 256;
+        ok = __all_sync(FULL_MASK, wait(&ms.q_known, items & 1));
+        if (both_or(!ok)) break;
 #pragma unroll 1
         for (int i = 0; i < RW; ++i) {
-          const uint64_t src = __shfl_sync(FULL_MASK, my_src, i);
-          if (src && 32 * lane < row_bytes) prefetch_l1(reinterpret_cast<const uint8_t *>((uintptr_t)src) + 32 * lane);
-        }
-        if (p.rope.rot_dim) {
-          if (my_src)
-            my_turn = rope_pos(p.rope, tree_pos(p.v.pv, p.v.parents, it.b, it.s.row + my_node, it.s.base + my_node, true), p.v.pv.status, true);
-#pragma unroll 1
-          for (int i = 0; i < RW; ++i) {
-            const size_t at = (size_t)__shfl_sync(FULL_MASK, my_turn, i) * (p.rope.rot_dim >> 1) + 8 * (lane & 7);
-            if (lane < 16 && 8 * (lane & 7) < (p.rope.rot_dim >> 1)) prefetch_l1((lane < 8 ? p.rope.cos_t : p.rope.sin_t) + at);
-          }
-        }
-#pragma unroll 1
-        for (int i = 0; i < RW; ++i) {
-          const uint8_t *src = reinterpret_cast<const uint8_t *>((uintptr_t)__shfl_sync(FULL_MASK, my_src, i));
+          const uint8_t *src = reinterpret_cast<const uint8_t *>((uintptr_t)ms.q_src[warp * RW + i]);
           float x[4] = {0.f, 0.f, 0.f, 0.f};
           if (src) load_lane4(src, p.q.dtype, lane, x);
-          rope_lane4(x, lane, p.rope, __shfl_sync(FULL_MASK, my_turn, i));
+          rope_lane4(x, lane, p.rope, ms.q_turn[warp * RW + i]);
           {
             const int c = warp * RW + i;
             float big = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
@@ -645,9 +655,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
           }
           *reinterpret_cast<uint4 *>(ms.anc[tid]) = make_uint4(word[0], word[1], word[2], word[3]);
         }
-        uint4 rh[8], rl[8];  // this warp's 16 rows of R
-        rot_load(rh, p.kfrag, 0, 0, warp, lane);
-        rot_load(rl, p.kfrag, 0, 1, warp, lane);
         (void)both_or(false);
         const int g = lane >> 2, t4 = lane & 3;
 #pragma unroll 1
@@ -946,93 +953,134 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
 struct CombineParams {
   TreeView v;
   PagedOut o;
-  int Hq, R, grid;
+  int Hq, R, grid, groups;
   float inv_vscale;    // 2^W_SHIFT / (2^P_SHIFT * alpha_V)
   const uint4 *vfrag;  // R and R^T of the values
   const float *split, *whole;
   const int32_t *unit;
 };
-constexpr int CB_WARPS = 8;
+constexpr int CB_WARPS = 16, CB_COLS = 32;
 
-// Eight columns (a node's q-head each) per CTA and turn: warp w merges column w's partials (m* = max m_s, l* = sum
-// l_s 2^(m_s - m*), o = sum acc_s 2^(m_s - m*) / l*), the eight warps multiply by R^T, then warp w rounds the row.
+// The sequence of row i as paged_seq's, the whole warp looking at 32 offsets at a time.
+__device__ __forceinline__ int warp_seq(const PagedView &v, int i, int lane) {
+  if (!v.cu_q) return i;
+  int lo = 0, n = v.B;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const uint32_t m = __ballot_sync(FULL_MASK, lane == 0 || (lane * step < n && v.cu_q[at] <= i));
+    const int k = __popc(m) - 1;
+    lo += k * step, n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+// 8 `groups` columns (a node's q-head each) per CTA and turn: a warp merges a column's partials, two columns at a time
+// (m* = max m_s, l* = sum l_s 2^(m_s - m*), o = sum acc_s 2^(m_s - m*) / l*), the first eight warps multiply by R^T's hi
+// parts, the others by its lo parts (16 rows of it in a warp's registers), then the rows are summed and rounded.
 __global__ void __launch_bounds__(CB_WARPS * 32) k_tree_combine(const CombineParams p) {
-  __shared__ RotColumns x;
-  __shared__ __align__(16) float y[8][D + 4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ RotColumns x[CB_COLS / 8];
+  __shared__ __align__(16) float y[2][CB_COLS][D + 4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp >> 3, mt = warp & 7;
   pdl_trigger();
-  uint4 ahi[8], alo[8];  // this warp's 16 rows of R^T
-  rot_load(ahi, p.vfrag, 1, 0, warp, lane);
-  rot_load(alo, p.vfrag, 1, 1, warp, lane);
+  uint4 a[8];
+  rot_load(a, p.vfrag, 1, part, mt, lane);
   pdl_wait();
   const TreeView &v = p.v;
   const int64_t n = (int64_t)paged_rows(v.pv) * p.Hq;
-  for (int64_t r0 = (int64_t)blockIdx.x * 8; r0 < n; r0 += (int64_t)gridDim.x * 8) {
-    const int64_t r = r0 + warp;
-    const int tok = (int)(min(r, n - 1) / p.Hq), head = (int)(min(r, n - 1) - (int64_t)tok * p.Hq);
-    const int b = paged_seq(v.pv, tok);
-    const Seq s = seq_of(v, b, false);
-    const int node = tok - s.row;
-    const bool taken = r < n && node >= 0 && node < s.T;  // (rows past max_q are left as they were)
-    float a[4] = {0.f, 0.f, 0.f, 0.f};
-    if (taken && s.base + node >= 0) {
+  const int turn = 8 * p.groups;
+  for (int64_t r0 = (int64_t)blockIdx.x * turn; r0 < n; r0 += (int64_t)gridDim.x * turn) {
+    const float *src[2] = {nullptr, nullptr};  // the column's first partial
+    int more[2] = {0, 0};                      // floats to the next one
+    int ns[2] = {0, 0};
+    bool taken[2] = {false, false};
+    int64_t row[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c0 = warp + CB_WARPS * i;
+      row[i] = r0 + c0;
+      if (c0 >= turn || row[i] >= n) continue;
+      const int tok = (int)(row[i] / p.Hq), head = (int)(row[i] - (int64_t)tok * p.Hq);
+      const int b = warp_seq(v.pv, tok, lane);
+      const Seq s = seq_of(v, b, false);
+      const int node = tok - s.row;
+      taken[i] = node >= 0 && node < s.T;  // (rows past max_q are left as they were)
+      if (!taken[i] || s.base + node < 0) continue;
       const int qt = node / v.npu, h = head / v.gq, c = (node - qt * v.npu) * v.gq + head - h * v.gq;
       const uint32_t info = (uint32_t)p.unit[unit_index(v, b, h, qt)];
-      const int first = min((int)(info & 0xFFFFu), p.grid - 1), ns = min((int)(info >> 16), p.grid - first);
-      float ms = -INFINITY, ls = 0.f;
-      for (int s0 = 0; s0 < ns; s0 += 8) {
-        float m8[8], l8[8];
-        float4 v8[8];
+      const int first = min((int)(info & 0xFFFFu), p.grid - 1);
+      ns[i] = min((int)(info >> 16), p.grid - first);
+      src[i] = ns[i] == 1 ? p.whole + ((size_t)tok * p.Hq + head) * PROW : p.split + ((size_t)first * 2 * p.R + c) * PROW;
+    }
+    // (the first CTA's share is its second partial, the others' their first)
+    auto part_of = [&](int i, int k) { return ns[i] == 1 ? src[i] : src[i] + ((size_t)k * 2 + (k == 0 ? 1 : 0)) * p.R * PROW; };
+    float o[2][4] = {}, ms[2] = {-INFINITY, -INFINITY}, ls[2] = {0.f, 0.f};
+    constexpr int FLY = 4;
+    for (int s0 = 0; s0 < max(ns[0], ns[1]); s0 += FLY) {
+      float m4[2][FLY], l4[2][FLY];
+      float4 v4[2][FLY];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int k = min(s0 + i, ns - 1);
-          const float *src = ns == 1 ? p.whole + ((size_t)tok * p.Hq + head) * PROW
-                                     : p.split + ((size_t)((first + k) * 2 + (k == 0 ? 1 : 0)) * p.R + c) * PROW;
-          m8[i] = __ldcg(src + D), l8[i] = __ldcg(src + D + 1);
-          v8[i] = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
-        }
-        float mc = -INFINITY;
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (s0 + i < ns && l8[i] != 0.f) mc = fmaxf(mc, m8[i]);
-        if (mc > ms) {
-          const float hf = (ms == -INFINITY) ? 0.f : exp2f(0.5f * (ms - mc)), f = hf * hf;
-          ls = lower(ls, hf);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) a[e] *= f;
-          ms = mc;
+        for (int k = 0; k < FLY; ++k) {
+          m4[i][k] = l4[i][k] = 0.f, v4[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (s0 + k < ns[i]) {
+            const float *at = part_of(i, s0 + k);
+            m4[i][k] = __ldcg(at + D), l4[i][k] = __ldcg(at + D + 1);
+            v4[i][k] = __ldcg(reinterpret_cast<const float4 *>(at) + lane);
+          }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (s0 + i < ns && l8[i] != 0.f) {
-            const float hf = exp2f(0.5f * (m8[i] - ms)), f = hf * hf;
-            ls += lower(l8[i], hf);
-            a[0] = fmaf(f, v8[i].x, a[0]), a[1] = fmaf(f, v8[i].y, a[1]);
-            a[2] = fmaf(f, v8[i].z, a[2]), a[3] = fmaf(f, v8[i].w, a[3]);
+      for (int i = 0; i < 2; ++i) {
+        float mc = ms[i];
+#pragma unroll
+        for (int k = 0; k < FLY; ++k)
+          if (l4[i][k] != 0.f) mc = fmaxf(mc, m4[i][k]);
+        if (mc > ms[i]) {
+          const float hf = ms[i] == -INFINITY ? 0.f : exp2f(0.5f * (ms[i] - mc)), f = hf * hf;
+          ls[i] = lower(ls[i], hf);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][e] *= f;
+          ms[i] = mc;
+        }
+#pragma unroll
+        for (int k = 0; k < FLY; ++k) {
+          if (l4[i][k] != 0.f) {
+            const float hf = exp2f(0.5f * (m4[i][k] - ms[i])), f = hf * hf;
+            ls[i] += lower(l4[i][k], hf);
+            o[i][0] = fmaf(f, v4[i][k].x, o[i][0]), o[i][1] = fmaf(f, v4[i][k].y, o[i][1]);
+            o[i][2] = fmaf(f, v4[i][k].z, o[i][2]), o[i][3] = fmaf(f, v4[i][k].w, o[i][3]);
           }
         }
       }
-      const float f = ls == 0.f ? 0.f : p.inv_vscale / ls;  // (NaN stays)
+    }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) a[e] *= f;
-    }
-    rot_put(x, warp, lane, a);
-    __syncthreads();
-    {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
-      rot_mul<true>(acc, ahi, x, lane);
-      rot_mul<false>(acc2, alo, x, lane);
-      float *d = &y[2 * (lane & 3)][16 * warp + (lane >> 2)];
-      d[0] = acc[0] + acc2[0], d[D + 4] = acc[1] + acc2[1];
-      d[8] = acc[2] + acc2[2], d[D + 12] = acc[3] + acc2[3];
+    for (int i = 0; i < 2; ++i) {
+      const int c0 = warp + CB_WARPS * i;
+      if (c0 >= turn) break;
+      const float f = ls[i] == 0.f ? 0.f : p.inv_vscale / ls[i];  // (NaN stays)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] *= f;
+      rot_put(x[c0 >> 3], c0 & 7, lane, o[i]);
     }
     __syncthreads();
-    if (taken) {
-      const float4 z = *reinterpret_cast<const float4 *>(&y[warp][4 * lane]);
-      const float v4[4] = {z.x, z.y, z.z, z.w};
-      store_lane4(p.o.out, p.o.dtype, (size_t)r * D, lane, v4);
+#pragma unroll 1
+    for (int g = 0; g < p.groups; ++g) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      if (part) rot_mul<false>(acc, a, x[g], lane);
+      else rot_mul<true>(acc, a, x[g], lane);
+      float *d = &y[part][8 * g + 2 * (lane & 3)][16 * mt + (lane >> 2)];
+      d[0] = acc[0], d[D + 4] = acc[1], d[8] = acc[2], d[D + 12] = acc[3];
     }
-    __syncthreads();  // x and y are free again
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (!taken[i]) continue;
+      const float4 h4 = *reinterpret_cast<const float4 *>(&y[0][warp + CB_WARPS * i][4 * lane]);
+      const float4 l4 = *reinterpret_cast<const float4 *>(&y[1][warp + CB_WARPS * i][4 * lane]);
+      const float z[4] = {h4.x + l4.x, h4.y + l4.y, h4.z + l4.z, h4.w + l4.w};
+      store_lane4(p.o.out, p.o.dtype, (size_t)row[i] * D, lane, z);
+    }
+    // (the next turn's x is written behind its loads; y behind the next barrier)
   }
 }
 
@@ -1111,10 +1159,12 @@ cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView 
   c.inv_vscale = 1.0f / (exp2f(P_SHIFT - W_SHIFT) * v->f16.alpha);
   c.vfrag = v->d_rfrag;
   c.split = p.split, c.whole = p.whole, c.unit = p.unit;
-  int blocks = 1;
-  if ((e = kernel_occupancy((const void *)k_tree_combine, CB_WARPS * 32, 0, &blocks)) != cudaSuccess) return e;
-  const int64_t want = ((int64_t)pv.n_tokens * Hq + 7) / 8, most = (int64_t)k->num_sms * blocks;
-  return launch_pdl(k_tree_combine, dim3((unsigned)(want < most ? want : most)), dim3(CB_WARPS * 32), 0, st, c);
+  // eight columns a turn while that leaves no SM two turns, up to 32
+  const int64_t cols = (int64_t)pv.n_tokens * Hq;
+  c.groups = 1;
+  while (c.groups < CB_COLS / 8 && cols > (int64_t)8 * c.groups * k->num_sms) c.groups <<= 1;
+  const int64_t want = (cols + 8 * c.groups - 1) / (8 * c.groups);
+  return launch_pdl(k_tree_combine, dim3((unsigned)(want < k->num_sms ? want : k->num_sms)), dim3(CB_WARPS * 32), 0, st, c);
 }
 
 }  // namespace tq

@@ -39,26 +39,31 @@ namespace tq {
 namespace {
 
 constexpr int KT = 128;          // keys per tile
-constexpr int ITEM_TILES = 6;    // cost of an item ahead of its tiles, in tiles
+constexpr int ITEM_TILES = 8;    // cost of an item ahead of its tiles, in tiles
 constexpr int RAW = KT * PG_ROW; // a packed tile
 constexpr int PROW = D + 4;      // floats of a partial: acc[128], max (less W_SHIFT), sum, 2 spare
-constexpr int W_KDEC = 8, W_VDEC = 16, W_PV = 24, W_LOAD = 25, W_S = 27, THREADS = 896;  // (W_LOAD: keys, then values)
 constexpr int NITEM = 4;         // items known ahead
-constexpr int REGS_LAUNCH = 72, REGS_SOFTMAX = 128, REGS_OTHER = 48;
-static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "the launch's registers");
 
 // R columns of a unit, PARTS fp16 parts of q and P.
 template <int R_, int PARTS_>
 struct Cfg {
   static constexpr int R = R_, PARTS = PARTS_;
   static constexpr int N = R * PARTS;   // columns of P and O
+  // Warps: softmax, K and V decoders, the issuer of O^T, the loaders of keys and values, the issuer of S^T.  Two groups of
+  // decoders each, on alternate tiles, where the softmax is quicker than one; with 64 columns it is not, and
+  // takes the registers instead (a sum per column and 32 scores).
+  static constexpr int GROUPS = R == 64 ? 1 : 2;
+  static constexpr int W_KDEC = 8, W_VDEC = 8 + 4 * GROUPS, W_PV = 8 + 8 * GROUPS, W_LOAD = W_PV + 1, W_S = W_PV + 3;
+  static constexpr int THREADS = (W_S + 1) * 32;
+  static constexpr int REGS_LAUNCH = GROUPS == 1 ? 96 : 72, REGS_SOFTMAX = GROUPS == 1 ? 144 : 128, REGS_OTHER = GROUPS == 1 ? 64 : 48;
+  static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "the launch's registers");
   static constexpr int CH = 32;         // columns a thread takes at a time
   // Stages: packed tiles on their way (more of the values', which the K decoders need for their norms long before
   // the V decoders come to them), decoded K (tensor memory) and V (shared memory), scores, P.
   static constexpr int NRAW_K = N == 32 ? 4 : 2, NRAW_V = 4;
   // A stage of packed tiles always falls to the same group of decoders: copies may land out of order, and a group that
   // had not waited for a stage's last phase could take its parity for the next one's.
-  static_assert(NRAW_K % 2 == 0 && NRAW_V % 2 == 0, "packed stages");
+  static_assert(GROUPS == 1 || (NRAW_K % 2 == 0 && NRAW_V % 2 == 0), "packed stages");
   static constexpr int NK = N == 128 ? 2 : (R == 64 ? 3 : 4), NV = N == 128 ? 2 : 3;
   static constexpr int NS = N == 128 ? 2 : (R == 64 ? 3 : 4), NP = N == 32 ? 4 : 2;
   static constexpr int NKN = NS + NK + 2;  // tiles whose norms are kept: see Misc
@@ -130,18 +135,20 @@ struct Item {
   int b, h, qt, t0, t1, tiles, vstart;
   Seq s;
 };
-__device__ __forceinline__ void walk_load(const TreeView &v, Walk &w) {
-  w.s = seq_of(v, w.b, false);
-  w.tiles = seq_tiles(w.s);
-  w.units = seq_qt(v, w.s) * v.pv.Hkv;
-}
 // The next sequence with keys, looked for 32 at a time by the whole warp (idle slots may be many).
 __device__ __forceinline__ bool walk_next(const TreeView &v, Walk &w) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
   for (int b0 = w.b + 1; b0 < v.pv.B; b0 += 32) {
-    const uint32_t m = __ballot_sync(FULL_MASK, seq_tiles(seq_of(v, b0 + (int)(threadIdx.x & 31), false)) > 0);
+    const Seq s = seq_of(v, b0 + lane, false);
+    const uint32_t m = __ballot_sync(FULL_MASK, seq_tiles(s) > 0);
     if (m) {
-      w.b = b0 + __ffs(m) - 1;
-      walk_load(v, w);
+      const int l = __ffs(m) - 1;
+      w.b = b0 + l;
+      w.s = Seq{__shfl_sync(FULL_MASK, s.row, l), __shfl_sync(FULL_MASK, s.T, l), __shfl_sync(FULL_MASK, s.base, l),
+                __shfl_sync(FULL_MASK, s.len, l)};
+      w.tiles = seq_tiles(w.s);
+      w.units = seq_qt(v, w.s) * v.pv.Hkv;
       return true;
     }
   }
@@ -166,22 +173,44 @@ __device__ __forceinline__ bool next_item(const TreeView &v, Walk &w, Item &it) 
   }
   return false;
 }
+// V virtual tiles over G CTAs in equal shares, as share_start and share_of of the other paged kernels, in 32 bits and few
+// instructions (they lie on the way to a CTA's first tile): floor(c V / G) = c (V / G) + floor(c (V % G) / G).
+struct Shares {
+  uint32_t G, q, r;
+  float inv;  // G / V
+  __device__ __forceinline__ void set(int V, int grid) {
+    G = min(grid, V);
+    q = G ? V / G : 0, r = G ? V - q * G : 0;
+    inv = V ? (float)G / (float)V : 0.f;
+  }
+  __device__ __forceinline__ int start(uint32_t c) const { return c * q + (r ? c * r / G : 0); }  // (G < 2^16)
+  __device__ __forceinline__ int of(int v) const {  // the CTA whose share holds virtual tile v; the estimate is near
+    int c = min((int)((float)v * inv), (int)G - 1);
+    while (start(c) > v) --c;
+    while (c + 1 < (int)G && start(c + 1) <= v) ++c;
+    return c;
+  }
+};
 // One warp: all virtual tiles (flagging bad lengths), then where this CTA's share of them starts.
-__device__ __forceinline__ void find_share(const TreeView &v, int lane, Walk &w, int &V, int &G) {
+__device__ __forceinline__ void find_share(const TreeView &v, int lane, Walk &w, Shares &sh) {
   const bool flag = blockIdx.x == 0;
-  int t = seq_vtiles(v, seq_of(v, lane, flag)), sum = t;
+  Seq s;
+  int t = 0, sum = 0, b0 = 0;
 #pragma unroll 1
-  for (int b = lane + 32; b < v.pv.B; b += 32) sum += seq_vtiles(v, seq_of(v, b, flag));
-  V = __reduce_add_sync(FULL_MASK, sum);
-  G = min((int)gridDim.x, V);
+  for (int b = lane; b0 < v.pv.B; b += 32, b0 += 32) {
+    s = seq_of(v, b, flag);
+    t = seq_vtiles(v, s);
+    sum += t;
+  }
+  sh.set(__reduce_add_sync(FULL_MASK, sum), gridDim.x);
   w = Walk{};
-  if ((int)blockIdx.x >= G) return;
-  w.v = share_start(blockIdx.x, V, G);
-  w.left = share_start(blockIdx.x + 1, V, G) - w.v;
+  if (blockIdx.x >= sh.G) return;
+  w.v = sh.start(blockIdx.x);
+  w.left = sh.start(blockIdx.x + 1) - w.v;
   int base = 0;
 #pragma unroll 1
-  for (int b0 = 0; b0 < v.pv.B; b0 += 32) {
-    if (b0) t = seq_vtiles(v, seq_of(v, b0 + lane, false));
+  for (int at = 0;; at += 32) {
+    if (b0 > 32) s = seq_of(v, at + lane, false), t = seq_vtiles(v, s);  // (up to 32 sequences: still here)
     int inc = t;
 #pragma unroll
     for (int h = 1; h < 32; h <<= 1) {
@@ -189,15 +218,18 @@ __device__ __forceinline__ void find_share(const TreeView &v, int lane, Walk &w,
       if (lane >= h) inc += o;
     }
     const uint32_t hit = __ballot_sync(FULL_MASK, base + inc > w.v);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      w.b = b0 + l;
+    if (hit || at + 32 >= v.pv.B) {
+      const int l = hit ? __ffs(hit) - 1 : 31;
+      w.b = at + l;
       w.off = w.v - (base + __shfl_sync(FULL_MASK, inc - t, l));
+      w.s = Seq{__shfl_sync(FULL_MASK, s.row, l), __shfl_sync(FULL_MASK, s.T, l), __shfl_sync(FULL_MASK, s.base, l),
+                __shfl_sync(FULL_MASK, s.len, l)};
       break;
     }
     base += __shfl_sync(FULL_MASK, inc, 31);
   }
-  walk_load(v, w);
+  w.tiles = seq_tiles(w.s);
+  w.units = seq_qt(v, w.s) * v.pv.Hkv;
   const int vt = w.tiles + ITEM_TILES;
   w.u = w.off / vt;
   w.off -= w.u * vt;
@@ -242,7 +274,7 @@ struct Misc {
   int abort_flag;
   uint64_t item_full[NITEM], item_empty[NITEM];
   Item item[NITEM];       // found by the keys' loader, one without tiles at the end
-  int V, G;
+  Shares shares;
 };
 
 __device__ __forceinline__ uint64_t pk2(float a, float b) {
@@ -329,8 +361,9 @@ __device__ __forceinline__ float warp_max(float x) {
 __device__ __forceinline__ void acc2(uint64_t &a, uint64_t b) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b)); }
 
 template <int R, int PARTS>
-__global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams p) {
+__global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(const PartialParams p) {
   using F = Cfg<R, PARTS>;
+  constexpr int W_KDEC = F::W_KDEC, W_VDEC = F::W_VDEC, W_PV = F::W_PV, W_LOAD = F::W_LOAD, W_S = F::W_S, THREADS = F::THREADS;
   constexpr int CH = F::CH, NRAW_K = F::NRAW_K, NRAW_V = F::NRAW_V, NK = F::NK, NV = F::NV, NS = F::NS, NP = F::NP, NKN = F::NKN;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
@@ -383,16 +416,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
     return it.t1 > it.t0;
   };
   if (warp >= W_KDEC) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F::REGS_OTHER));
     if (warp == W_LOAD || warp == W_LOAD + 1) {
       // ================ loaders: a warp for the keys, one for the values; a lane per page of a tile
       const int psh = p.v.pv.page_shift, P = 1 << psh, side = warp - W_LOAD;
       const uint8_t *pages = side ? p.vp : p.kp;
       Walk w;
       if (!side) {
-        int V, G;
-        find_share(p.v, lane, w, V, G);
-        if (lane == 0) ms.V = V, ms.G = G;
+        Shares sh;
+        find_share(p.v, lane, w, sh);
+        if (lane == 0) ms.shares = sh;
       }
       auto publish = [&]() -> bool {  // the keys' loader walks its share for all
         const uint32_t i = n_items % NITEM;
@@ -436,8 +469,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
         for (uint32_t c = n > nr ? n - nr : 0; c < n; ++c)
           (void)mbar_wait_bounded(&ms.raw_full[side][c % nr], (c / nr) & 1, WAIT_LIMIT_NS);
     } else if (warp < W_PV) {
-      // ================ decoders: two groups of four warps for the keys, two for the values, on alternate tiles;
-      // thread = key of the tile
+      // ================ decoders: one or two groups of four warps for the keys, as many for the values, the two on
+      // alternate tiles; thread = key of the tile
       const int row = tid & 127;
       const bool side = warp >= W_VDEC;
       uint32_t lo2[2], hi2[2];
@@ -448,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
       uint32_t n = 0;
       while (ok && next()) {
         for (int j = it.t0; ok && j < it.t1; ++j, ++n) {
-          if ((n & 1) != (uint32_t)((warp >> 2) & 1)) continue;
+          if (F::GROUPS == 2 && (n & 1) != (uint32_t)((warp >> 2) & 1)) continue;
           const uint32_t rv = n % NRAW_V, rs = side ? rv : n % NRAW_K, ns = side ? NV : NK, st = n % ns;
           if (n >= ns) ok = wait(side ? &ms.v_empty[st] : &ms.k_empty[st], ((n / ns) - 1) & 1);
           if (ok) ok = wait(&ms.raw_full[side][rs], (n / (side ? NRAW_V : NRAW_K)) & 1);
@@ -592,7 +625,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
         umma_commit(&ms.drain[1]), (void)mbar_wait_bounded(&ms.drain[1], 0, WAIT_LIMIT_NS);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F::REGS_SOFTMAX));
     // ================ softmax: group gr takes the tiles n with n % 2 == gr, thread = key
     const int gr = warp >> 2, key = tid & 127, wq = warp & 3;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
@@ -601,9 +634,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
     float4 *const mv = ms.move[gr];
     uint32_t n = 0;  // tiles before the item
     for (uint32_t items = 0;; ++items) {
-      uint4 rh[8], rl[8];  // this warp's 16 rows of R, on their way while the item is waited for
-      rot_load(rh, p.kfrag, 0, 0, warp, lane);
-      rot_load(rl, p.kfrag, 0, 1, warp, lane);
+      // This warp's 16 rows of R: on their way while the item is waited for; with 64 columns, where registers are few,
+      // once the rows of q are done (32 trees of mixed sizes 44 -> 41 us, 4 wide trees 178 -> 175; with 32 columns that
+      // order costs one in a hundred).
+      uint4 rh[8], rl[8];
+      auto load_rot = [&]() { rot_load(rh, p.kfrag, 0, 0, warp, lane), rot_load(rl, p.kfrag, 0, 1, warp, lane); };
+      if constexpr (R == 32) load_rot();
       if (!next()) break;
       const int unit = unit_index(p.v, it.b, it.h, it.qt), n0 = it.qt * p.v.npu;
       const int cols = min(it.s.T - n0, p.v.npu) * p.v.gq;  // columns with a node
@@ -614,12 +650,23 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
         uint8_t *const xs = smem + F::OFF_P;  // bf16 hi of the columns, then lo; 16-byte chunk c of column r at c ^ (r % 8)
         ok = __all_sync(FULL_MASK, wait(&ms.q_known, items & 1));
         if (both_or(!ok)) break;
+        uint64_t src, src_next = 0;
+        uint4 raw, raw_next;
+        LaneAngles an, an_next;
+        auto fetch = [&](int i) {  // the next row, while one is worked on
+          src_next = ms.q_src[warp * RW + i];
+          raw_next = make_uint4(0u, 0u, 0u, 0u);
+          if (src_next) raw_next = load_lane4_raw(reinterpret_cast<const uint8_t *>((uintptr_t)src_next), p.q.dtype, lane);
+          if (p.rope.rot_dim) an_next = rope_angles(lane, p.rope, ms.q_turn[warp * RW + i]);
+        };
+        fetch(0);
 #pragma unroll 1
         for (int i = 0; i < RW; ++i) {
-          const uint8_t *src = reinterpret_cast<const uint8_t *>((uintptr_t)ms.q_src[warp * RW + i]);
-          float x[4] = {0.f, 0.f, 0.f, 0.f};
-          if (src) load_lane4(src, p.q.dtype, lane, x);
-          rope_lane4(x, lane, p.rope, ms.q_turn[warp * RW + i]);
+          src = src_next, raw = raw_next, an = an_next;
+          if (i + 1 < RW) fetch(i + 1);
+          float x[4];
+          lane4_floats(raw, p.q.dtype, x);
+          if (p.rope.rot_dim) rope_turn(x, lane, p.rope, an);
           {
             const int c = warp * RW + i;
             float big = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
@@ -655,6 +702,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
           }
           *reinterpret_cast<uint4 *>(ms.anc[tid]) = make_uint4(word[0], word[1], word[2], word[3]);
         }
+        if constexpr (R != 32) load_rot();
         (void)both_or(false);
         const int g = lane >> 2, t4 = lane & 3;
 #pragma unroll 1
@@ -888,8 +936,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tree_partial(const PartialParams
       tc_fence_before();
       if (both_or(!ok)) break;
       tc_fence_after();
-      const int first = share_of(it.vstart, ms.V, ms.G);
-      const int n_split = share_of(it.vstart + it.tiles - 1, ms.V, ms.G) - first + 1, cta = blockIdx.x;
+      const int first = ms.shares.of(it.vstart), n_split = ms.shares.of(it.vstart + it.tiles - 1) - first + 1, cta = blockIdx.x;
       if (tid == 0 && cta == first) p.unit[unit] = first | (n_split << 16);
       if (tid < cols) {
         auto sum = [&](int g2) {
@@ -1113,7 +1160,7 @@ cudaError_t launch_partial(const PartialParams &p, int grid, cudaStream_t st) {
   static_assert(smem <= 227 * 1024, "shared memory budget");
   const cudaError_t e = kernel_smem_attr((const void *)k_tree_partial<R, PARTS>, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_tree_partial<R, PARTS>, dim3(grid), dim3(THREADS), smem, st, p);
+  return launch_pdl(k_tree_partial<R, PARTS>, dim3(grid), dim3(Cfg<R, PARTS>::THREADS), smem, st, p);
 }
 
 }  // namespace

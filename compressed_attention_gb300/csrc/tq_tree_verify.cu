@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
     }
     return;
   }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // begun: waited for ahead of the first sums' exchange
   const size_t esz = DT == TQ_DTYPE_F32 ? 4 : 2;
   auto row_of = [&](const void *base, int64_t stride, int node) {
     return static_cast<const void *>(static_cast<const uint8_t *>(base) + (size_t)(lo + node) * stride * esz);
@@ -239,6 +240,8 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
       }
     if (lane == 0) sm.warp[warp] = sum;
     __syncthreads();
+    // (the others' shared memory is there once they have begun)
+    if (pass == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     const int side = pass++ & 1;
     if (warp == 0) {
       const uint64_t t = warp_sum(lane < VW ? sm.warp[lane] : 0);

@@ -138,6 +138,24 @@ def test_attention_over_long_contexts():
             check_attention(got, ref, dtype, f"p{P} {dtype}")
 
 
+def test_attention_of_few_sequences_among_idle_slots():
+    """Sequences hundreds of slots apart, more than a warp looks at together, and two that share their context's pages."""
+    import torch
+    rng = np.random.default_rng(5)
+    new, lens = [0] * 300, [0] * 300
+    for b in (3, 31, 32, 33, 131, 299):
+        new[b] = int(rng.integers(1, 9))
+        lens[b] = new[b] + int(rng.integers(0, 700))
+    lens[40] = 33  # without rows
+    for od in ("bf16", "f32"):
+        lens[31] = lens[32] = 256 + max(new)
+        s = Trees(lib(), lens, new, 2, 64, 19)
+        s.table[32, :4] = s.table[31, :4]
+        s.kv = s.tq.PagedKV(*s.pages, torch.from_numpy(s.table).cuda(), 64, 2)
+        got, ref = run_tree(s, 8, "bf16", od, 64)
+        check_attention(got, ref, od)
+
+
 @pytest.mark.parametrize("Hq", [2, 8, 24])
 def test_scores_in_the_hundreds(Hq):
     """Sharp softmax: the running maximum rises from tile to tile and between CTAs."""
@@ -333,6 +351,21 @@ def test_verify(case, draft):
     ctx = lib().Ctx("turbo4")
     for seed in range(4):
         Walks(new, V, dtype, seed, draft, wide, pad, stride).check(ctx)
+
+
+def test_verify_many_sequences_and_rows_that_lie_differently():
+    """A CTA per sequence and every smaller cluster on the way; the draft's rows start elsewhere than the target's
+    do within 16 bytes, the vocabulary's last group is short."""
+    import torch
+    ctx = lib().Ctx("turbo4")
+    for B, dtype in ((700, "bf16"), (170, "f32"), (90, "f16"), (45, "bf16")):
+        w = Walks([4, 0, 1, 2] * (B // 4) + [3] * (B % 4), 203, dtype, B, True, 2)
+        held = w.draft.clone()
+        for at in (1, 5):
+            wide = torch.full((w.n, 209), float("nan"), dtype=held.dtype, device="cuda")
+            w.draft = wide[:, at:at + 203]
+            w.draft.copy_(held)
+            w.check(ctx)
 
 
 def test_verify_large_vocabularies():

@@ -718,32 +718,27 @@ def tq_paged_diff_attention(k_ctx, v_ctx, kv, batch, q, diff, out, workspace, ro
 
 # --------------------------------------------------------------------------- drafted trees
 
-def _words(t, n, what):
-    """Address of a packed int32 CUDA tensor of at least n elements."""
-    if t.dtype != _torch()[0].int32 or t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1) or not t.is_cuda:
-        raise ValueError(f"{what} must be a packed int32 CUDA tensor of {n} elements")
-    return t.data_ptr()
-
-
-def _randoms(t, n, what):
-    if t.dtype != _torch()[0].float32 or t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1) or not t.is_cuda:
-        raise ValueError(f"{what} must be a packed float32 CUDA tensor of {n} elements")
+def _packed(t, dtype, n, what):
+    """Address of a packed 1-D CUDA tensor of at least n elements (few attribute reads: a call checks up to six)."""
+    if t.dtype is not dtype or not t.is_cuda or t.dim() != 1 or t.numel() < n or not (n <= 1 or t.is_contiguous()):
+        raise ValueError(f"{what} must be a packed {str(dtype)[6:]} CUDA tensor of {n} elements")
     return t.data_ptr()
 
 
 def _path(t, batch):
     """Address and row stride of a path tensor, int32 [B, max_q] at least."""
-    if t.dtype != _torch()[0].int32 or t.dim() != 2 or t.shape[0] < batch.B or t.shape[1] < batch.c.max_q \
-            or (t.shape[1] > 1 and t.stride(1) != 1) or not t.is_cuda:
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not _torch()[0].int32 or len(shape) != 2 or shape[0] < batch.B or shape[1] < batch.c.max_q \
+            or (shape[1] > 1 and stride[1] != 1) or not t.is_cuda:
         raise ValueError(f"path must be an int32 CUDA tensor [{batch.B}, {batch.c.max_q}] with packed rows")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
 
 
 def _probs(t, n_tokens, what):
-    if t.dim() != 2 or t.shape[0] < n_tokens or (t.shape[1] > 1 and t.stride(1) != 1) or not t.is_cuda:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < n_tokens or (shape[1] > 1 and stride[1] != 1) or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor [n_tokens, vocab] with packed rows")
-    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    return tq_probs(t.data_ptr(), _dtype_code(t), t.shape[1], stride)
+    return tq_probs(t.data_ptr(), _dtype_code(t), shape[1], stride[0] if shape[0] > 1 else shape[1])
 
 
 def tq_paged_tree_append(k_ctx, v_ctx, kv, batch, parents, k, v, rope=None, stream=None):
@@ -752,8 +747,9 @@ def tq_paged_tree_append(k_ctx, v_ctx, kv, batch, parents, k, v, rope=None, stre
     _check_call(kv, batch, rope)
     kr, vr = _rows(k, batch.n_tokens, kv.Hkv, "k"), _rows(v, batch.n_tokens, kv.Hkv, "v")
     _check(lib.tq_paged_tree_append(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref,
-                                    _words(parents, batch.n_tokens, "parents"), ctypes.byref(kr), ctypes.byref(vr),
-                                    rope.ref if rope else None, _stream(stream)), "tq_paged_tree_append")
+                                    _packed(parents, _torch()[0].int32, batch.n_tokens, "parents"),
+                                    ctypes.byref(kr), ctypes.byref(vr), rope.ref if rope else None,
+                                    _stream(stream)), "tq_paged_tree_append")
 
 
 def tq_paged_tree_workspace_size(k_ctx, v_ctx, kv, batch, Hq):
@@ -769,7 +765,7 @@ def tq_paged_tree_attention(k_ctx, v_ctx, kv, batch, parents, q, out, workspace,
     Hq = q.shape[1]
     qr = _rows(q, batch.n_tokens, Hq, "q")
     _check(lib.tq_paged_tree_attention(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref,
-                                       _words(parents, batch.n_tokens, "parents"), ctypes.byref(qr), Hq,
+                                       _packed(parents, _torch()[0].int32, batch.n_tokens, "parents"), ctypes.byref(qr), Hq,
                                        rope.ref if rope else None, scale, _dense_out(out, batch.n_tokens, Hq, "out"),
                                        _dtype_code(out), _ptr(workspace), _wsb(workspace), _stream(stream)),
            "tq_paged_tree_attention")
@@ -782,15 +778,16 @@ def tq_tree_verify(ctx, batch, parents, tokens, target, u_accept, u_next, path, 
     from) or None; fills path [B, max_q] (nodes, then -1), n_path [B] and next_token [B]."""
     if not batch.on_gpu:
         raise ValueError("the batch must be CUDA tensors")
-    n, B = batch.n_tokens, batch.B
+    n, B, torch = batch.n_tokens, batch.B, _torch()[0]
+    i32, f32 = torch.int32, torch.float32
     tp = _probs(target, n, "target")
     dp = None if draft is None else _probs(draft, n, "draft")
     pp, stride = _path(path, batch)
-    _check(lib.tq_tree_verify(ctx.handle, batch.ref, _words(parents, n, "parents"), _words(tokens, n, "tokens"),
-                              ctypes.byref(tp), None if dp is None else ctypes.byref(dp),
-                              _randoms(u_accept, n, "u_accept"), _randoms(u_next, B, "u_next"), pp, stride,
-                              _words(n_path, B, "n_path"), _words(next_token, B, "next_token"), _stream(stream)),
-           "tq_tree_verify")
+    _check(lib.tq_tree_verify(ctx.handle, batch.ref, _packed(parents, i32, n, "parents"),
+                              _packed(tokens, i32, n, "tokens"), ctypes.byref(tp),
+                              None if dp is None else ctypes.byref(dp), _packed(u_accept, f32, n, "u_accept"),
+                              _packed(u_next, f32, B, "u_next"), pp, stride, _packed(n_path, i32, B, "n_path"),
+                              _packed(next_token, i32, B, "next_token"), _stream(stream)), "tq_tree_verify")
 
 
 def tq_paged_tree_keep(k_ctx, v_ctx, kv, batch, path, n_path, new_lens, stream=None):
@@ -798,8 +795,9 @@ def tq_paged_tree_keep(k_ctx, v_ctx, kv, batch, path, n_path, new_lens, stream=N
     batch's own lengths may be given) to context + n_path."""
     _check_call(kv, batch)
     pp, stride = _path(path, batch)
+    i32 = _torch()[0].int32
     _check(lib.tq_paged_tree_keep(k_ctx.handle, v_ctx.handle, kv.ref, batch.ref, pp, stride,
-                                  _words(n_path, batch.B, "n_path"), _words(new_lens, batch.B, "new_lens"),
+                                  _packed(n_path, i32, batch.B, "n_path"), _packed(new_lens, i32, batch.B, "new_lens"),
                                   _stream(stream)), "tq_paged_tree_keep")
 
 

@@ -12,6 +12,7 @@
 // outcome, and a comparison is off by 2^-62 where fp32 sums over 10^5 weights would move the borders between tokens by
 // 10^-7, as much as a rare token has.
 #include <cooperative_groups.h>
+#include <limits.h>
 
 #include <type_traits>
 
@@ -169,13 +170,14 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
     seg = ((hi_g - lo_g + VW - 1) / VW + 31) & ~31;
   };
   stand(0);
-  // r of one element after `fails` failed tests (no draft: the tokens taken out are the caller's)
+  // r of one element after `fails` failed tests (no draft: the tokens taken out are the caller's); p and q in [0, 1]
   auto weight = [&](float p, float q) -> uint64_t {
-    uint64_t r = fix(p);
+    uint64_t r = fix01(p);
     if (DRAFT && fails) {
-      const uint64_t x = fix(q);
-      for (int k = 0; k < fails; ++k) {
-        const uint64_t z = sm.z[k], c = z == ONE ? x : mul62(z, x);
+      const uint64_t x = fix01(q);
+      r -= fix01(fminf(p, q));  // the first test's Z is 1, and of two floats the lesser has the lesser multiple
+      for (int k = 1; k < fails; ++k) {
+        const uint64_t c = mul62(sm.z[k], x);
         r = r > c ? r - c : 0;
       }
     }
@@ -192,45 +194,62 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
     uint64_t sum = 0;
     auto add_up = [&](auto fly, auto with_q, auto f) {  // `fly` groups of a thread in flight
       constexpr int FLY = decltype(fly)::value;
+      constexpr bool Q = decltype(with_q)::value;
+      auto take = [&](const uint4 &p4, const uint4 &q4) {
+        float x[Gr::E], y[Gr::E];
+        uint32_t most = 0;
+#pragma unroll
+        for (int e = 0; e < Gr::E; ++e) {
+          x[e] = Gr::at(p4, e), y[e] = Q ? Gr::at(q4, e) : 0.f;
+          most = max(most, max(__float_as_uint(x[e]), __float_as_uint(y[e])));
+        }
+        if (most > 0x3F800000u) {  // past 1, negative or NaN
+#pragma unroll
+          for (int e = 0; e < Gr::E; ++e) x[e] = clamp01(x[e]), y[e] = clamp01(y[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < Gr::E; ++e) f(x[e], y[e]);
+      };
+      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+      // whole groups first: their loads need no look at the row's ends
+      const bool plain = !Q || alike;
+      const int end = (V + skip) / Gr::E, a = max(g0, skip ? 1 : 0), e = min(g1, end);
+      if (plain) {
+        const uint4 *pg = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(prow) - skip * (16 / Gr::E)) + a + lane;
+        const uint4 *qg = Q ? reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(qrow) - skip * (16 / Gr::E)) + a + lane : nullptr;
 #pragma unroll 1
-      for (int g = g0 + lane; g < g1; g += 32 * FLY) {
-        uint4 p4[FLY], q4[FLY];
+        for (int g = a + lane; g < e; g += 32 * FLY, pg += 32 * FLY, qg += 32 * FLY) {
+          uint4 p4[FLY], q4[FLY];
 #pragma unroll
-        for (int i = 0; i < FLY; ++i) {
-          p4[i] = q4[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (g + 32 * i < g1) {
-            p4[i] = Gr::load(prow, g + 32 * i, skip, true, V);
-            if (decltype(with_q)::value) q4[i] = Gr::load(qrow, g + 32 * i, skip, alike, V);
+          for (int i = 0; i < FLY; ++i) {
+            p4[i] = q4[i] = none;
+            if (g + 32 * i < e) {
+              p4[i] = __ldg(pg + 32 * i);
+              if (Q) q4[i] = __ldg(qg + 32 * i);
+            }
           }
+#pragma unroll
+          for (int i = 0; i < FLY; ++i) take(p4[i], q4[i]);
         }
-#pragma unroll
-        for (int i = 0; i < FLY; ++i) {
-          float x[Gr::E], y[Gr::E];
-          uint32_t most = 0;
-#pragma unroll
-          for (int e = 0; e < Gr::E; ++e) {
-            x[e] = Gr::at(p4[i], e), y[e] = Gr::at(q4[i], e);
-            most = max(most, max(__float_as_uint(x[e]), __float_as_uint(y[e])));
-          }
-          if (most > 0x3F800000u) {  // past 1, negative or NaN
-#pragma unroll
-            for (int e = 0; e < Gr::E; ++e) x[e] = clamp01(x[e]), y[e] = clamp01(y[e]);
-          }
-#pragma unroll
-          for (int e = 0; e < Gr::E; ++e) sum += f(x[e], y[e]);
-        }
+      }
+      // the row's first and last group where they are not whole (a lane each); all of them where p's and q's do not pair
+      int g = g0 + lane;
+      if (plain) g = lane == 0 && skip ? 0 : lane == 1 && !(skip && end == 0) ? end : INT_MAX;
+#pragma unroll 1
+      for (; g < g1; g += 32) {
+        if (g >= g0) take(Gr::load(prow, g, skip, true, V), Q ? Gr::load(qrow, g, skip, alike, V) : none);
+        if (plain) break;
       }
     };
     using Fly = std::integral_constant<int, DT == TQ_DTYPE_F32 ? 4 : 2>;
     if (!DRAFT || !fails) {
-      add_up(Fly(), std::false_type(), [](float x, float) { return fix01(x); });
-    } else if (fails == 1) {  // (the first test's Z is 1)
-      add_up(std::integral_constant<int, Fly::value / 2>(), std::true_type(), [](float x, float y) {
-        const uint64_t u = fix01(x), v = fix01(y);
-        return u > v ? u - v : 0;
+      add_up(Fly(), std::false_type(), [&](float x, float) { sum += fix01(x); });
+    } else if (fails == 1) {
+      add_up(Fly(), std::true_type(), [&](float x, float y) {
+        sum += fix01(x), sum -= fix01(fminf(x, y));
       });
     } else {
-      add_up(std::integral_constant<int, 1>(), std::true_type(), weight);
+      add_up(std::integral_constant<int, 1>(), std::true_type(), [&](float x, float y) { sum += weight(x, y); });
     }
     sum = warp_sum(sum);
     if (!DRAFT)  // less the tokens taken out (each once: a token again has failed before)
@@ -256,45 +275,52 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
   uint64_t Z = ONE, sum = 0;
   bool have = false;  // sum is that of r as it stands
   if (rank == 0 && tid == 0) path[0] = 0;
-  for (int c = next_child(0, 0); c < TREE_MAX;) {
-    uint64_t r = sm.p[c];
-    bool take;
-    if (DRAFT) {
-      for (int k = 0; k < fails; ++k) {
-        const uint64_t d = mul62(sm.z[k], sm.q[c]);
-        r = r > d ? r - d : 0;
+  for (int c = next_child(0, 0);; c = next_child(cur, c)) {
+    const bool done = c == TREE_MAX;  // no child left
+    if (done && have) break;
+    bool refused = false;
+    if (!done) {
+      uint64_t r = sm.p[c];
+      bool take;
+      if (DRAFT) {
+        for (int k = 0; k < fails; ++k) {
+          const uint64_t d = mul62(sm.z[k], sm.q[c]);
+          r = r > d ? r - d : 0;
+        }
+        take = __umul64hi(sm.u[c], mul62(Z, sm.q[c])) < r;
+      } else {
+        bool again = false;
+        for (int k = lane; k < fails; k += 32) again |= sm.token[sm.gone[k]] == sm.token[c];
+        if (__any_sync(FULL_MASK, again)) r = 0;
+        take = __umul64hi(sm.u[c], Z) < r;
       }
-      take = __umul64hi(sm.u[c], mul62(Z, sm.q[c])) < r;
-    } else {
-      bool again = false;
-      for (int k = lane; k < fails; k += 32) again |= sm.token[sm.gone[k]] == sm.token[c];
-      if (__any_sync(FULL_MASK, again)) r = 0;
-      take = __umul64hi(sm.u[c], Z) < r;
-    }
-    if (take) {
       __syncthreads();  // (z, gone are read)
-      cur = c, fails = 0, Z = ONE, have = false;
-      if (rank == 0 && tid == 0) path[n_path] = c;
-      ++n_path;
-      stand(cur);
-    } else if (DRAFT) {
-      __syncthreads();  // (z is read)
-      if (tid == 0) sm.z[fails] = Z;
+      if (take) {
+        cur = c, fails = 0, Z = ONE, have = false;
+        if (rank == 0 && tid == 0) path[n_path] = c;
+        ++n_path;
+        stand(cur);
+      } else if (DRAFT) {
+        if (tid == 0) sm.z[fails] = Z;
+        ++fails;
+        refused = true;
+      } else if (r) {
+        if (tid == 0) sm.gone[fails] = c;
+        ++fails;
+        Z = Z > r ? Z - r : 0;
+      }
       __syncthreads();
-      ++fails;
-      const uint64_t left = total();
-      if (left) Z = left < ONE * 2 ? left : ONE * 2 - 1, sum = left, have = true;
-      else --fails;  // as it was
-    } else if (r) {
-      __syncthreads();
-      if (tid == 0) sm.gone[fails] = c;
-      __syncthreads();
-      ++fails;
-      Z = Z > r ? Z - r : 0;
     }
-    c = next_child(cur, c);
+    if (done || refused) {  // (one place: the passes' code is long)
+      const uint64_t s = total();
+      if (done) {
+        sum = s;
+        break;
+      }
+      if (s) Z = s < ONE * 2 ? s : ONE * 2 - 1, sum = s, have = true;
+      else --fails;  // as it was
+    }
   }
-  if (!have) sum = total();
   if (rank == 0) {
     for (int i = n_path + tid; i < a.max_q; i += VT) path[i] = -1;
     if (tid == 0) a.n_path[b] = n_path;
@@ -327,7 +353,7 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
     const int64_t w0 = (int64_t)g * Gr::E - skip;
 #pragma unroll
     for (int e = 0; e < Gr::E; ++e) {
-      r[e] = weight(Gr::at(p4, e), Gr::at(q4, e));
+      r[e] = weight(clamp01(Gr::at(p4, e)), clamp01(Gr::at(q4, e)));
       if (!DRAFT)
         for (int k = 0; k < fails; ++k)
           if (sm.token[sm.gone[k]] == w0 + e) r[e] = 0;

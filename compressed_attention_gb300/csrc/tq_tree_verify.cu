@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
         break;
       }
       if (s) Z = s < ONE * 2 ? s : ONE * 2 - 1, sum = s, have = true;
-      else --fails;  // as it was
+      else --fails, have = false;  // as it was, its sums to be found again
     }
   }
   if (rank == 0) {

@@ -416,6 +416,28 @@ def test_verify_follows_one_hot_targets_and_rows_without_weight():
     assert lib().tq_ctx_device_status(ctx) == 0
 
 
+@pytest.mark.parametrize("V", [3, 700])
+def test_verify_keeps_a_residual_that_a_test_would_empty(V):
+    """Rows that do not sum to 1: the first refused child leaves r = 1/4 on two tokens, the second one would leave
+    nothing, so r stays and the next token is drawn from it."""
+    import torch
+    ctx = lib().Ctx("turbo4")
+    w = Walks([3, 4], V, "f32", 16, True, 1)
+    w.target.zero_(), w.draft.zero_()
+    for t, rows in ((w.target, (0.75, 0.75, 0.125)), (w.draft, (0.5, 0.5, 0.5))):
+        t[:, [0, V - 2, V - 1]] = torch.tensor(rows, device="cuda")
+    w.host = (w.target.cpu().numpy(), w.draft.cpu().numpy())
+    w.parents[:] = [-1, 0, 0, -1, 0, 0, 0]
+    w.tokens[:] = V - 1
+    w.u[:] = 0.9
+    w.d[0].copy_(torch.from_numpy(w.parents)), w.d[1].copy_(torch.from_numpy(w.tokens)), w.d[3].fill_(0.9)
+    for u in (0.25, 0.75):
+        w.u_next[:] = u
+        w.d[4].fill_(u)
+        w.check(ctx)
+        assert w.run(ctx)[2].tolist() == [0 if u < 0.5 else V - 2] * 2
+
+
 def test_verify_flags_tokens_parents_and_too_many_nodes():
     import torch
     ctx = lib().Ctx("turbo4")

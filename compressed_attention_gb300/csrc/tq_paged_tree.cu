@@ -39,7 +39,9 @@ namespace tq {
 namespace {
 
 constexpr int KT = 128;          // keys per tile
-constexpr int ITEM_TILES = 8;    // cost of an item ahead of its tiles, in tiles
+// Cost of an item ahead of its tiles (q, the first maxima, the partials), in tiles: 8 sequences towards 32K take 118 us
+// with 6 to 8 and 120 with 12, short chains 37.3 with 6, 38.0 with 8 and 40.9 with 12, mixed trees 40.5 with 8 and 41.8 with 12.
+constexpr int ITEM_TILES = 8;
 constexpr int RAW = KT * PG_ROW; // a packed tile
 constexpr int PROW = D + 4;      // floats of a partial: acc[128], max (less W_SHIFT), sum, 2 spare
 constexpr int NITEM = 4;         // items known ahead
@@ -99,7 +101,9 @@ struct TreeView {
   PagedView pv;
   const int32_t *parents;
   int npu, n_qt, gq;  // nodes of a unit, units of a sequence and KV head (for max_q nodes), q-heads per KV head
+  uint32_t by_npu, by_gq;  // floor(2^16 / .) + 1: x / y = x * by_y >> 16 for x < 256, y <= 64
 };
+__device__ __forceinline__ int node_of(const TreeView &v, int col) { return (int)((uint32_t)col * v.by_gq >> 16); }
 
 // A sequence's nodes and keys.
 struct Seq {
@@ -118,7 +122,7 @@ __device__ __forceinline__ Seq seq_of(const TreeView &v, int b, bool flag) {
   return s;
 }
 __device__ __forceinline__ int seq_tiles(const Seq &s) { return s.T ? (s.len + KT - 1) / KT : 0; }
-__device__ __forceinline__ int seq_qt(const TreeView &v, const Seq &s) { return (s.T + v.npu - 1) / v.npu; }
+__device__ __forceinline__ int seq_qt(const TreeView &v, const Seq &s) { return (int)((uint32_t)(s.T + v.npu - 1) * v.by_npu >> 16); }
 // Virtual tiles of the sequence.
 __device__ __forceinline__ int seq_vtiles(const TreeView &v, const Seq &s) {
   const int t = seq_tiles(s);
@@ -369,7 +373,6 @@ __global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(cons
   uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
   Misc<NKN> &ms = *reinterpret_cast<Misc<NKN> *>(smem + F::OFF_MISC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_trigger();
   if (warp == 0) tmem_alloc(smem_addr(&ms.tmem), 512);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s)
@@ -388,6 +391,7 @@ __global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(cons
   __syncthreads();
   tc_fence_after();
   pdl_wait();
+  pdl_trigger();  // (what ran before is done: the combine reads lengths and offsets ahead of its own wait)
   const uint32_t tmem = ms.tmem;
   // Bounded wait, in few instructions (they are on every role's path); fails when another thread has given up.
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(cons
         const int n0 = it.qt * p.v.npu, cols = min(it.s.T - n0, p.v.npu) * p.v.gq;
 #pragma unroll 1
         for (int c = lane; c < R; c += 32) {
-          const int local = c / p.v.gq, node = n0 + local;
+          const int local = node_of(p.v, c), node = n0 + local;
           uint64_t src = 0;
           int turn = 0;
           if (c < cols && it.s.base + node >= 0) {
@@ -634,12 +638,6 @@ __global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(cons
     float4 *const mv = ms.move[gr];
     uint32_t n = 0;  // tiles before the item
     for (uint32_t items = 0;; ++items) {
-      // This warp's 16 rows of R: on their way while the item is waited for; with 64 columns, where registers are few,
-      // once the rows of q are done (32 trees of mixed sizes 44 -> 41 us, 4 wide trees 178 -> 175; with 32 columns that
-      // order costs one in a hundred).
-      uint4 rh[8], rl[8];
-      auto load_rot = [&]() { rot_load(rh, p.kfrag, 0, 0, warp, lane), rot_load(rl, p.kfrag, 0, 1, warp, lane); };
-      if constexpr (R == 32) load_rot();
       if (!next()) break;
       const int unit = unit_index(p.v, it.b, it.h, it.qt), n0 = it.qt * p.v.npu;
       const int cols = min(it.s.T - n0, p.v.npu) * p.v.gq;  // columns with a node
@@ -650,44 +648,57 @@ __global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(cons
         uint8_t *const xs = smem + F::OFF_P;  // bf16 hi of the columns, then lo; 16-byte chunk c of column r at c ^ (r % 8)
         ok = __all_sync(FULL_MASK, wait(&ms.q_known, items & 1));
         if (both_or(!ok)) break;
-        uint64_t src, src_next = 0;
-        uint4 raw, raw_next;
-        LaneAngles an, an_next;
-        auto fetch = [&](int i) {  // the next row, while one is worked on
-          src_next = ms.q_src[warp * RW + i];
-          raw_next = make_uint4(0u, 0u, 0u, 0u);
-          if (src_next) raw_next = load_lane4_raw(reinterpret_cast<const uint8_t *>((uintptr_t)src_next), p.q.dtype, lane);
-          if (p.rope.rot_dim) an_next = rope_angles(lane, p.rope, ms.q_turn[warp * RW + i]);
+        constexpr int W = 2;  // rows at a time
+        uint64_t src[W], src_next[W];
+        uint4 raw[W], raw_next[W];
+        LaneAngles an[W], an_next[W];
+        auto fetch = [&](int i) {  // the next rows, while some are worked on
+#pragma unroll
+          for (int r = 0; r < W; ++r) {
+            src_next[r] = ms.q_src[warp * RW + i + r];
+            raw_next[r] = make_uint4(0u, 0u, 0u, 0u);
+            if (src_next[r]) raw_next[r] = load_lane4_raw(reinterpret_cast<const uint8_t *>((uintptr_t)src_next[r]), p.q.dtype, lane);
+            if (p.rope.rot_dim) an_next[r] = rope_angles(lane, p.rope, ms.q_turn[warp * RW + i + r]);
+          }
         };
         fetch(0);
 #pragma unroll 1
-        for (int i = 0; i < RW; ++i) {
-          src = src_next, raw = raw_next, an = an_next;
-          if (i + 1 < RW) fetch(i + 1);
-          float x[4];
-          lane4_floats(raw, p.q.dtype, x);
-          if (p.rope.rot_dim) rope_turn(x, lane, p.rope, an);
-          {
-            const int c = warp * RW + i;
-            float big = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-            big = __uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(big)));  // ordered like the floats
+        for (int i = 0; i < RW; i += W) {
+          float x[W][4], big[W];
+#pragma unroll
+          for (int r = 0; r < W; ++r) src[r] = src_next[r], raw[r] = raw_next[r], an[r] = an_next[r];
+          if (i + W < RW) fetch(i + W);
+#pragma unroll
+          for (int r = 0; r < W; ++r) lane4_floats(raw[r], p.q.dtype, x[r]);
+          if (p.rope.rot_dim) {
+#pragma unroll
+            for (int r = 0; r < W; ++r) rope_turn(x[r], lane, p.rope, an[r]);
+          }
+#pragma unroll
+          for (int r = 0; r < W; ++r) {
+            big[r] = fmaxf(fmaxf(fabsf(x[r][0]), fabsf(x[r][1])), fmaxf(fabsf(x[r][2]), fabsf(x[r][3])));
+            big[r] = __uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(big[r])));  // ordered like the floats
+          }
+#pragma unroll
+          for (int r = 0; r < W; ++r) {
+            const int c = warp * RW + i + r;
             // R q is at most sqrt(128) times the largest element: held times a power of two that brings that to
             // [2^10, 2^11); times none where it lies between, of ordinary size, so that one part drops what is below
             // 2^-14 of the row's norm, two parts what is below 2^-20 of it.
-            const float m = big * fabsf(p.qmul);
+            const float m = big[r] * fabsf(p.qmul);
             const int e = m >= (PARTS == 2 ? 0x1p-4f : 0x1p-8f) && m < 0x1p11f ? 0 : scale_exp(m) + 3;
-            if (lane == 0) ms.qs[c] = src ? pow2i(e) : 0.f, ms.qd[c] = p.qmul * pow2i(-e);
+            if (lane == 0) ms.qs[c] = src[r] ? pow2i(e) : 0.f, ms.qd[c] = p.qmul * pow2i(-e);
             uint32_t hi[2], lo[2];
             float f[4];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              hi[k] = pack_bf162(x[2 * k], x[2 * k + 1]);
+              hi[k] = pack_bf162(x[r][2 * k], x[r][2 * k + 1]);
               f[2 * k] = __uint_as_float(hi[k] << 16), f[2 * k + 1] = __uint_as_float(hi[k] & 0xFFFF0000u);
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) f[k] = isinf(f[k]) ? x[k] = 0.f : f[k];  // an infinite part has no rest
+            for (int k = 0; k < 4; ++k) f[k] = isinf(f[k]) ? x[r][k] = 0.f : f[k];  // an infinite part has no rest
 #pragma unroll
-            for (int k = 0; k < 2; ++k) lo[k] = pack_bf162(x[2 * k] - f[2 * k], x[2 * k + 1] - f[2 * k + 1]);
+            for (int k = 0; k < 2; ++k) lo[k] = pack_bf162(x[r][2 * k] - f[2 * k], x[r][2 * k + 1] - f[2 * k + 1]);
             uint8_t *dst = xs + c * 256 + (((lane >> 1) ^ (c & 7)) << 4) + 8 * (lane & 1);
             *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2 *>(dst + R * 256) = make_uint2(lo[0], lo[1]);
@@ -702,7 +713,8 @@ __global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(cons
           }
           *reinterpret_cast<uint4 *>(ms.anc[tid]) = make_uint4(word[0], word[1], word[2], word[3]);
         }
-        if constexpr (R != 32) load_rot();
+        uint4 rh[8], rl[8];  // this warp's 16 rows of R (sooner, they would take the registers of the rows of q)
+        rot_load(rh, p.kfrag, 0, 0, warp, lane), rot_load(rl, p.kfrag, 0, 1, warp, lane);
         (void)both_or(false);
         const int g = lane >> 2, t4 = lane & 3;
 #pragma unroll 1
@@ -944,7 +956,7 @@ __global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(cons
         };
         const float m0 = ms.mx[0][tid], m1 = ms.mx[1][tid], mx = fmaxf(m0, m1), l0 = sum(0), l1 = sum(1);
         const float f0 = m0 == -INFINITY ? 0.f : exp2_approx(m0 - mx), f1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - mx);
-        const int local = tid / p.v.gq;
+        const int local = node_of(p.v, tid);
         float *dst = n_split > 1 ? p.split + ((size_t)(cta * 2 + (cta == first ? 1 : 0)) * R + tid) * PROW
                                  : p.whole + ((size_t)(it.s.row + n0 + local) * p.Hq + it.h * p.v.gq + tid - local * p.v.gq) * PROW;
         // (without a maximum a group's sum is 0, or NaN where its scores are)
@@ -1031,32 +1043,41 @@ __global__ void __launch_bounds__(CB_WARPS * 32) k_tree_combine(const CombinePar
   pdl_trigger();
   uint4 a[8];
   rot_load(a, p.vfrag, 1, part, mt, lane);
-  pdl_wait();
   const TreeView &v = p.v;
-  const int64_t n = (int64_t)paged_rows(v.pv) * p.Hq;
-  const int turn = 8 * p.groups;
-  for (int64_t r0 = (int64_t)blockIdx.x * turn; r0 < n; r0 += (int64_t)gridDim.x * turn) {
-    const float *src[2] = {nullptr, nullptr};  // the column's first partial
-    int more[2] = {0, 0};                      // floats to the next one
-    int ns[2] = {0, 0};
-    bool taken[2] = {false, false};
-    int64_t row[2];
+  const uint32_t n = (uint32_t)paged_rows(v.pv) * p.Hq, turn = 8 * p.groups;  // (31 bits)
+  bool taken[2];
+  uint32_t row[2];
+  int unit[2], col[2];  // (-1: zeros)
+  // whose columns c0 = r0 + warp and r0 + warp + 16 are
+  auto locate = [&](uint32_t r0) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int c0 = warp + CB_WARPS * i;
-      row[i] = r0 + c0;
+      const uint32_t c0 = warp + CB_WARPS * i;
+      row[i] = r0 + c0, taken[i] = false, unit[i] = -1;
       if (c0 >= turn || row[i] >= n) continue;
-      const int tok = (int)(row[i] / p.Hq), head = (int)(row[i] - (int64_t)tok * p.Hq);
+      const int tok = (int)(row[i] / (uint32_t)p.Hq), head = (int)row[i] - tok * p.Hq;
       const int b = warp_seq(v.pv, tok, lane);
       const Seq s = seq_of(v, b, false);
       const int node = tok - s.row;
       taken[i] = node >= 0 && node < s.T;  // (rows past max_q are left as they were)
       if (!taken[i] || s.base + node < 0) continue;
-      const int qt = node / v.npu, h = head / v.gq, c = (node - qt * v.npu) * v.gq + head - h * v.gq;
-      const uint32_t info = (uint32_t)p.unit[unit_index(v, b, h, qt)];
+      const int qt = (int)((uint32_t)node * v.by_npu >> 16), h = head / v.gq;
+      unit[i] = unit_index(v, b, h, qt), col[i] = (node - qt * v.npu) * v.gq + head - h * v.gq;
+    }
+  };
+  locate(blockIdx.x * turn);
+  pdl_wait();
+  for (uint32_t r0 = blockIdx.x * turn; r0 < n; r0 += gridDim.x * turn) {
+    if (r0 != blockIdx.x * turn) locate(r0);
+    const float *src[2] = {nullptr, nullptr};  // the column's first partial
+    int ns[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (unit[i] < 0) continue;
+      const uint32_t info = (uint32_t)__ldcg(p.unit + unit[i]);
       const int first = min((int)(info & 0xFFFFu), p.grid - 1);
       ns[i] = min((int)(info >> 16), p.grid - first);
-      src[i] = ns[i] == 1 ? p.whole + ((size_t)tok * p.Hq + head) * PROW : p.split + ((size_t)first * 2 * p.R + c) * PROW;
+      src[i] = ns[i] == 1 ? p.whole + (size_t)row[i] * PROW : p.split + ((size_t)first * 2 * p.R + col[i]) * PROW;
     }
     // (the first CTA's share is its second partial, the others' their first)
     auto part_of = [&](int i, int k) { return ns[i] == 1 ? src[i] : src[i] + ((size_t)k * 2 + (k == 0 ? 1 : 0)) * p.R * PROW; };
@@ -1183,7 +1204,7 @@ cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView 
   Layout l;
   if (!layout(k, pv, Hq, o.dtype, &l)) return cudaErrorInvalidValue;
   uint8_t *base = static_cast<uint8_t *>(ws);
-  const TreeView tv{pv, parents, l.npu, l.n_qt, l.gq};
+  const TreeView tv{pv, parents, l.npu, l.n_qt, l.gq, 65536u / l.npu + 1, 65536u / l.gq + 1};
   PartialParams p{};
   p.v = tv, p.kp = kp, p.vp = vp, p.q = q, p.rope = rope, p.Hq = Hq;
   p.qmul = LOG2E * scale / k->f16.alpha;

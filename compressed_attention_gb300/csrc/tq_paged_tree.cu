@@ -101,6 +101,7 @@ struct TreeView {
   PagedView pv;
   const int32_t *parents;
   int npu, n_qt, gq;  // nodes of a unit, units of a sequence and KV head (for max_q nodes), q-heads per KV head
+  uint32_t by_grid;        // floor((2^32 - 1) / CTAs)
   uint32_t by_npu, by_gq;  // floor(2^16 / .) + 1: x / y = x * by_y >> 16 for x < 256, y <= 64
 };
 __device__ __forceinline__ int node_of(const TreeView &v, int col) { return (int)((uint32_t)col * v.by_gq >> 16); }
@@ -127,6 +128,13 @@ __device__ __forceinline__ int seq_qt(const TreeView &v, const Seq &s) { return 
 __device__ __forceinline__ int seq_vtiles(const TreeView &v, const Seq &s) {
   const int t = seq_tiles(s);
   return t ? seq_qt(v, s) * v.pv.Hkv * (t + ITEM_TILES) : 0;
+}
+// x / y: an estimate in fp32, put right.
+__device__ __forceinline__ int div_near(uint32_t x, uint32_t y) {
+  uint32_t t = (uint32_t)__fdividef((float)x, (float)y);
+  while (t * y > x) --t;
+  while ((t + 1) * y <= x) ++t;
+  return (int)t;
 }
 // Units of a sequence lie KV head by KV head, the tiles of nodes of one next to each other.
 __device__ __forceinline__ int unit_index(const TreeView &v, int b, int h, int qt) { return (b * v.pv.Hkv + h) * v.n_qt + qt; }
@@ -168,7 +176,7 @@ __device__ __forceinline__ bool next_item(const TreeView &v, Walk &w, Item &it) 
       continue;
     }
     const int vt = w.tiles + ITEM_TILES, n = min(vt - w.off, w.left), nq = seq_qt(v, w.s);
-    it.b = w.b, it.h = w.u / nq, it.qt = w.u - it.h * nq, it.s = w.s, it.tiles = w.tiles;
+    it.b = w.b, it.h = div_near(w.u, nq), it.qt = w.u - it.h * nq, it.s = w.s, it.tiles = w.tiles;
     it.t0 = max(w.off - ITEM_TILES, 0), it.t1 = w.off + n - ITEM_TILES;
     it.vstart = w.v - w.off + ITEM_TILES;
     w.v += n, w.left -= n, w.off += n;
@@ -177,17 +185,23 @@ __device__ __forceinline__ bool next_item(const TreeView &v, Walk &w, Item &it) 
   }
   return false;
 }
-// V virtual tiles over G CTAs in equal shares, as share_start and share_of of the other paged kernels, in 32 bits and few
-// instructions (they lie on the way to a CTA's first tile): floor(c V / G) = c (V / G) + floor(c (V % G) / G).
+// V virtual tiles over G CTAs in equal shares, as share_start and share_of of the other paged kernels, in 32 bits and
+// without divisions (they lie on the way to a CTA's first tile): floor(c V / G) = c (V / G) + floor(c (V % G) / G).
 struct Shares {
-  uint32_t G, q, r;
+  uint32_t G, by_grid, q, r;
   float inv;  // G / V
-  __device__ __forceinline__ void set(int V, int grid) {
-    G = min(grid, V);
-    q = G ? V / G : 0, r = G ? V - q * G : 0;
-    inv = V ? (float)G / (float)V : 0.f;
+  // x / grid: the product falls short by one at most
+  __device__ __forceinline__ uint32_t over_grid(uint32_t x) const {
+    const uint32_t t = __umulhi(x, by_grid);
+    return t + (x - t * G >= G ? 1 : 0);
   }
-  __device__ __forceinline__ int start(uint32_t c) const { return c * q + (r ? c * r / G : 0); }  // (G < 2^16)
+  __device__ __forceinline__ void set(int V, const TreeView &v) {
+    G = gridDim.x, by_grid = v.by_grid;
+    if (V < (int)G) G = V, q = 1, r = 0;
+    else q = over_grid(V), r = V - q * G;
+    inv = V ? __fdividef((float)G, (float)V) : 0.f;
+  }
+  __device__ __forceinline__ int start(uint32_t c) const { return c * q + (r ? over_grid(c * r) : 0); }  // (grid < 2^16)
   __device__ __forceinline__ int of(int v) const {  // the CTA whose share holds virtual tile v; the estimate is near
     int c = min((int)((float)v * inv), (int)G - 1);
     while (start(c) > v) --c;
@@ -206,7 +220,7 @@ __device__ __forceinline__ void find_share(const TreeView &v, int lane, Walk &w,
     t = seq_vtiles(v, s);
     sum += t;
   }
-  sh.set(__reduce_add_sync(FULL_MASK, sum), gridDim.x);
+  sh.set(__reduce_add_sync(FULL_MASK, sum), v);
   w = Walk{};
   if (blockIdx.x >= sh.G) return;
   w.v = sh.start(blockIdx.x);
@@ -235,7 +249,7 @@ __device__ __forceinline__ void find_share(const TreeView &v, int lane, Walk &w,
   w.tiles = seq_tiles(w.s);
   w.units = seq_qt(v, w.s) * v.pv.Hkv;
   const int vt = w.tiles + ITEM_TILES;
-  w.u = w.off / vt;
+  w.u = div_near(w.off, vt);
   w.off -= w.u * vt;
 }
 
@@ -1204,7 +1218,7 @@ cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView 
   Layout l;
   if (!layout(k, pv, Hq, o.dtype, &l)) return cudaErrorInvalidValue;
   uint8_t *base = static_cast<uint8_t *>(ws);
-  const TreeView tv{pv, parents, l.npu, l.n_qt, l.gq, 65536u / l.npu + 1, 65536u / l.gq + 1};
+  const TreeView tv{pv, parents, l.npu, l.n_qt, l.gq, UINT32_MAX / (uint32_t)l.grid, 65536u / l.npu + 1, 65536u / l.gq + 1};
   PartialParams p{};
   p.v = tv, p.kp = kp, p.vp = vp, p.q = q, p.rope = rope, p.Hq = Hq;
   p.qmul = LOG2E * scale / k->f16.alpha;

@@ -1171,20 +1171,45 @@ struct Layout {
   int64_t units;
   size_t unit, split, whole, bytes;
 };
+// Columns of a unit, 32 or 64, from what the host knows of the batch: a tile of 64 takes 1.45 times the time of one of 32 and an
+// item 19 tiles' where one of 32 takes 8, so 64 pay where trees fill them over long contexts, 32 where trees are smaller
+// than their bound or contexts short.  Trees are taken to lie evenly about their mean up to max_q.  The time
+// is the CTAs' even share of the items and half an item for the split ends.  Measured, 64 against 32 (4 query heads per KV
+// head, bf16): 4 sequences of 16,000 tokens with 9 nodes 62 / 74 us, 24 nodes 100 / 107, 64 nodes 182 / 265, 1 to 16 nodes
+// 62 / 53; 8 of 1,500 with 9 nodes 32 / 33, 24 nodes 54 / 49, 64 nodes 100 / 112, 1 to 16 nodes 32 / 27; 32 of 16 to
+// 8,000 with up to 20 nodes, 6 query heads, f16: 39 / 31.
+int columns(const PagedView &pv, int gq, int grid) {
+  if (gq > 32) return 64;
+  if (pv.max_q * gq <= 32 || pv.B == 0) return 32;
+  const double hi = pv.max_q, mean = fmin((double)pv.n_tokens / pv.B, hi), lo = fmax(2 * mean - hi, 1.0);
+  const double tiles = (pv.max_len + KT - 1) / KT;
+  auto time = [&](int R, double item, double tile) {
+    const int npu = R / gq;
+    double units = 0;
+    for (int i = 0; i < 16; ++i) {
+      const int T = (int)fmin(lo + (hi - lo + 1) * (i + 0.5) / 16, hi);
+      units += (T + npu - 1) / npu / 16.0;
+    }
+    return pv.B * pv.Hkv * units / grid * (item + tile * tiles) + item / 2;
+  };
+  return time(64, 19, 1.45) < time(32, 8, 1) ? 64 : 32;
+}
 bool layout(const tq_ctx *k, const PagedView &pv, int Hq, int out_dtype, Layout *l) {
   l->gq = Hq / pv.Hkv;
   l->parts = out_dtype == TQ_DTYPE_BF16 ? 1 : 2;
-  l->R = pv.max_q * l->gq <= 32 ? 32 : 64;
+  l->R = columns(pv, l->gq, k->num_sms);
   l->npu = l->R / l->gq;  // at least one: 64 heads per KV head at most
   l->n_qt = (pv.max_q + l->npu - 1) / l->npu;
   l->grid = k->num_sms;
-  l->units = (int64_t)pv.B * pv.Hkv * l->n_qt;
+  // the larger of both widths' needs, so that no smaller batch needs more than a larger one
+  const int least = l->gq <= 32 ? 32 / l->gq : 1;
+  l->units = (int64_t)pv.B * pv.Hkv * ((pv.max_q + least - 1) / least);
   const int64_t tiles = l->units * (((int64_t)pv.max_len + KT - 1) / KT + ITEM_TILES);
   if (l->grid > 65535 || tiles > INT32_MAX || (int64_t)pv.n_tokens * Hq > INT32_MAX) return false;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   l->unit = 0;
   l->split = up((size_t)l->units * 4);
-  l->whole = l->split + up((size_t)l->grid * 2 * l->R * PROW * 4);
+  l->whole = l->split + up((size_t)l->grid * 2 * 64 * PROW * 4);
   l->bytes = l->whole + up((size_t)pv.n_tokens * Hq * PROW * 4);
   return true;
 }

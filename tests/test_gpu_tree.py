@@ -182,10 +182,61 @@ def test_norms_out_of_the_ordinary(out_dtype):
         s.host[i][..., :4] = nat.view(np.uint8)
         s.pages[i].copy_(torch.from_numpy(s.host[i]))
     got, ref = run_tree(s, 8, "f32", out_dtype)
-    got = got.float().cpu().numpy()
+    got, ref = got.float().cpu().numpy()[:s.n], ref[:s.n]
     half = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}[out_dtype]
     big = max(np.abs(ref).max(), 1.0)  # outputs are sums of values of up to 2^8 the ordinary norm: the stated 2e-3 grows with it
     assert np.all(np.isfinite(got)) and np.max(np.abs(got - ref) - half * np.abs(ref)) <= 2e-3 * big
+
+
+class FullTrees(Trees):
+    """A batch whose sizes allow full trees over a million tokens: past 32 columns, units of 64."""
+
+    def __init__(self, tq, lens, new, Hkv, P, seed, wide=4, pad=0, **kw):
+        full = len(lens) * max(max(new), 1) - sum(new)
+        super().__init__(tq, lens, new, Hkv, P, seed, wide, pad=max(pad, full), width=(1 << 20) // P, **kw)
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("case", [c for c in ATTENTION if max(c[1]) * c[2] // c[3] > 32],
+                         ids=lambda c: f"t{max(c[1])}-n{max(c[0])}-h{c[2]}x{c[3]}-p{c[4]}")
+def test_attention_in_units_of_64_columns(case, out_dtype, monkeypatch):
+    monkeypatch.setitem(globals(), "Trees", FullTrees)
+    test_attention(case, out_dtype)
+
+
+@pytest.mark.parametrize("again", [test_attention_over_long_contexts, lambda: test_scores_in_the_hundreds(8),
+                                   lambda: test_scores_in_the_hundreds(24),
+                                   lambda: test_norms_out_of_the_ordinary("bf16"),
+                                   lambda: test_norms_out_of_the_ordinary("f16")],
+                         ids=["long", "sharp-8", "sharp-24", "norms-bf16", "norms-f16"])
+def test_hard_inputs_in_units_of_64_columns(again, monkeypatch):
+    monkeypatch.setitem(globals(), "Trees", FullTrees)
+    again()
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "f16"])
+def test_nan_norms_in_units_of_64_columns(out_dtype):
+    """60 columns in one unit; a node's value (or key) is NaN: its own columns and its descendants', no other."""
+    import torch
+    s = FullTrees(lib(), [231], [20], 2, 32, 29, wide=6)
+    clean, _ = run_tree(s, 6, "bf16", out_dtype)
+    seen = [set() for _ in range(20)]
+    for i, p in enumerate(s.parents[:20].tolist()):
+        seen[i] = {i} | (seen[p] if p >= 0 else set())
+    rows = torch.from_numpy(s.q32).bfloat16().cuda()
+    for side in (0, 1):
+        for node in (0, 3, 11, 19):
+            pages = [p.clone() for p in s.pages]
+            t = 211 + node
+            pages[side][int(s.table[0, t // 32]), 1, t % 32, :4] = torch.tensor([0, 0, 192, 127], dtype=torch.uint8)
+            out = torch.empty_like(clean)
+            s.tq.tq_paged_tree_attention(*s.ctx, s.tq.PagedKV(*pages, s.kv.block_table, 32, 2), s.batch, s.d_parents, rows,
+                                         out, s.tree_workspace(6))
+            hit = [i for i in range(20) if node in seen[i]]
+            keep = [i for i in range(20) if node not in seen[i]]
+            assert not torch.isfinite(out[hit][:, 3:]).any(-1).any() and torch.equal(out[:20, :3], clean[:20, :3])
+            assert torch.equal(out[keep], clean[keep])
+    assert s.status() == 0
 
 
 def test_nan_norms_reach_the_nodes_that_see_them():

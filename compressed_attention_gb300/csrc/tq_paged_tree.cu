@@ -1,32 +1,42 @@
-// Attention of drafted trees over the paged cache on the 5th-generation tensor cores, in three
-// launches.
+// Attention of drafted trees over the paged cache on the 5th-generation tensor cores, in two launches.
 //
+// Node i of a sequence sees the context, its ancestors and itself:
+//   out = R_V^T sum_t p_t n_t c_t / sum_t p_t,  p_t = exp(scale n_t <R_K rope(q, context + depth), c_t>),
+// with n_t the norms and c_t the centroids of the fp16 table of the packed rows.
 // A unit is a sequence's KV head with as many of its nodes as fit R columns (a column is a node's q-head).
 // Few columns against long contexts: so the products are laid with the keys in the rows,
-//   S^T [128 keys x R] = K_hat Q^T,   O^T [128 dims x N] += V_hat^T P^T,
+//   S^T [128 keys x R] = C_K Q^T,   O^T [128 dims x N] += C_V^T P^T,
 // and the time of a tile goes with its 128 keys and its columns, where rows of 128 queries (the chunk kernel's
 // form) would compute 128 exponentials a key whatever the tree holds.  A softmax thread is a key: its norms are two
 // scalars, and the sums of weights stay in its registers until the item's end.
 //
-//   k_tree_prep     each warp turns 16 columns of q by their nodes' positions (fp32), by R (bf16 parts,
-//                   m16n8k16), and rounds them to fp16 parts in images of the units' operand tiles; other
-//                   warps write which columns see each of the nodes' keys.
 //   k_tree_partial  persistent, one CTA per SM; the key tiles of all units lie end to end (each unit after a few
-//                   empty tiles that stand for its start) and are shared out evenly, as in the paged decode.
-//                   Specialised warps:
-//                     loader      packed tiles, one bulk copy per page and side, on rings; q's images
+//                   empty tiles that stand for its start) and are shared out evenly, as in the paged decode.  An
+//                   item is a unit's tiles in one CTA's share.  Specialised warps:
+//                     loaders     keys, values: packed tiles, one bulk copy per page, on rings; the keys' loader
+//                                 walks the share for all
 //                     K decoders  nibbles -> fp16 centroids (byte permutes) into tensor memory, a key per lane:
 //                                 the A operand of S^T, without a trip through shared memory
 //                     V decoders  the same into 128-byte swizzled tiles, the MN-major A operand of O^T
-//                     issuers     one thread for S^T, as far ahead as its buffers go, one for O^T
-//                     softmax     two groups of four warps on alternate key tiles, each with its own O^T: S^T from
-//                                 tensor memory, weights against the columns' running maxima, P as the
-//                                 MN-major B operand in shared memory.  A maximum is raised (and O
-//                                 rescaled) only when a weight would leave the operand's range: one vote a tile.
+//                     issuers     one thread for S^T, as far ahead as its buffers go, one for O^T; the first
+//                                 one's warp finds the next item's positions
+//                     softmax     two groups of four warps on alternate key tiles, each with its own O^T.  An
+//                                 item starts with q: rows turned (fp32), times R in bf16 parts (m16n8k16), as fp16 parts
+//                                 in the operand's image.  Then S^T from tensor memory, weights against the columns'
+//                                 running maxima, P as the MN-major B operand in shared memory.  A maximum is raised
+//                                 (and O rescaled) only when a weight would leave the operand's range: one vote a tile.
 //   k_tree_combine  the log-sum-exp merge of a column's shares, R^T o on the tensor cores, rounding.
 //
-// Parts: for bf16 outputs q and P enter as one fp16 each; for fp16 and fp32 outputs as hi + lo, the lo parts as
-// more columns.  K and V are centroids of the fp16 table with fp32 norms outside the products.
+// Parts: for bf16 outputs q and P enter as one fp16 each (2^-12 of the value at most); for fp16 and fp32 outputs as hi + lo,
+// the lo parts as more columns.  Sums, maxima and O are fp32.
+//
+// Measured: 8 sequences of 24,000 to 32,768 tokens, 8 nodes each, 32 heads on 8, bf16: 117 us for both launches, 2.1 TB/s of
+// packed rows (37 us at the copy rate), 2,150 cycles per 128 keys and SM.  The decoders' byte permutes keep the ALU at 69%
+// of its rate, issue 64%, tensor pipe 12%; with the decoders' arithmetic taken out (scratch build) it would be 99 us, with
+// the copies too 83: what is left is the chain decode -> S -> softmax -> P -> O and its barriers.  Table lookups in place of
+// the permutes, deeper rings and fewer raise barriers change nothing (118 to 124 us).  An item's start and end take 9.5 us
+// wherever they are hidden by nothing: one user's 8 nodes on 733 tokens 16.5 us, where an empty kernel takes 3 and the
+// combine 4; of the 9.5 more than half is q (position, turn, R), a chain of short dependent steps.
 #include <math.h>
 
 #include "tq_decode_common.cuh"
@@ -52,8 +62,9 @@ struct Cfg {
   static constexpr int R = R_, PARTS = PARTS_;
   static constexpr int N = R * PARTS;   // columns of P and O
   // Warps: softmax, K and V decoders, the issuer of O^T, the loaders of keys and values, the issuer of S^T.  Two groups of
-  // decoders each, on alternate tiles, where the softmax is quicker than one; with 64 columns it is not, and
-  // takes the registers instead (a sum per column and 32 scores).
+  // decoders each, on alternate tiles, where the softmax is quicker than one (8 sequences towards 32K 117 us, with one
+  // group 129); with 64 columns it is not, and takes the registers instead, for a sum per column and 32 scores (four
+  // trees of 40 to 64 nodes 172 us, with two groups 206).
   static constexpr int GROUPS = R == 64 ? 1 : 2;
   static constexpr int W_KDEC = 8, W_VDEC = 8 + 4 * GROUPS, W_PV = 8 + 8 * GROUPS, W_LOAD = W_PV + 1, W_S = W_PV + 3;
   static constexpr int THREADS = (W_S + 1) * 32;
@@ -61,7 +72,8 @@ struct Cfg {
   static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "the launch's registers");
   static constexpr int CH = 32;         // columns a thread takes at a time
   // Stages: packed tiles on their way (more of the values', which the K decoders need for their norms long before
-  // the V decoders come to them), decoded K (tensor memory) and V (shared memory), scores, P.
+  // the V decoders come to them), decoded K (tensor memory) and V (shared memory), scores, P: what shared and tensor memory
+  // hold.  For 32 columns six packed stages against one decoded V less, or half the P, were slower (117 -> 121 to 125 us).
   static constexpr int NRAW_K = N == 32 ? 4 : 2, NRAW_V = 4;
   // A stage of packed tiles always falls to the same group of decoders: copies may land out of order, and a group that
   // had not waited for a stage's last phase could take its parity for the next one's.
@@ -662,7 +674,7 @@ __global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(cons
         uint8_t *const xs = smem + F::OFF_P;  // bf16 hi of the columns, then lo; 16-byte chunk c of column r at c ^ (r % 8)
         ok = __all_sync(FULL_MASK, wait(&ms.q_known, items & 1));
         if (both_or(!ok)) break;
-        constexpr int W = 2;  // rows at a time
+        constexpr int W = 2;  // rows at a time (one: short chat 0.5 us more; four spill: four wide trees 30 us more)
         uint64_t src[W], src_next[W];
         uint4 raw[W], raw_next[W];
         LaneAngles an[W], an_next[W];
@@ -1047,6 +1059,8 @@ __device__ __forceinline__ int warp_seq(const PagedView &v, int i, int lane) {
   return lo;
 }
 
+// Ends 4 to 6 us behind the partials of short batches, which is latency: its rows and sequences are found ahead of its wait,
+// then come the unit's entry, the partials, the products.  6,656 columns (four wide trees) take 15 us, two turns of a CTA.
 // 8 `groups` columns (a node's q-head each) per CTA and turn: a warp merges a column's partials, two columns at a time
 // (m* = max m_s, l* = sum l_s 2^(m_s - m*), o = sum acc_s 2^(m_s - m*) / l*), the first eight warps multiply by R^T's hi
 // parts, the others by its lo parts (16 rows of it in a warp's registers), then the rows are summed and rounded.
@@ -1225,7 +1239,8 @@ cudaError_t launch_partial(const PartialParams &p, int grid, cudaStream_t st) {
 
 }  // namespace
 
-// One node per sequence sees all of its sequence's keys: a single row of the paged decode.
+// One node per sequence sees all of its sequence's keys: a single row of the paged decode, which takes 10.1 us for one
+// sequence of 733 tokens and 66 for eight towards 32K, where the kernels above take 15.1 and 126.
 static bool is_decode(const PagedView &pv, int Hq) { return pv.max_q == 1 && Hq / pv.Hkv <= 16; }
 
 bool paged_tree_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes) {
@@ -1266,7 +1281,8 @@ cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView 
   c.inv_vscale = 1.0f / (exp2f(P_SHIFT - W_SHIFT) * v->f16.alpha);
   c.vfrag = v->d_rfrag;
   c.split = p.split, c.whole = p.whole, c.unit = p.unit;
-  // eight columns a turn while that leaves no SM two turns, up to 32
+  // Eight columns a turn while that leaves no SM two turns, up to 32: short chat 16.5 us, with 32 always 18.7; four wide
+  // trees 172, with 8 always 178.
   const int64_t cols = (int64_t)pv.n_tokens * Hq;
   c.groups = 1;
   while (c.groups < CB_COLS / 8 && cols > (int64_t)8 * c.groups * k->num_sms) c.groups <<= 1;

@@ -34,12 +34,13 @@ __global__ void __launch_bounds__(KEEP_T) k_paged_keep(const KeepParams p) {
   if (tid == 0) bad = 0;
   pdl_wait();
   const int len = paged_len(v, b, tid == 0);
-  int T = 1;
+  int T = 1, base = len - 1;
   if (v.cu_q) {
     const int a = v.cu_q[b], e = v.cu_q[b + 1];
     T = a < 0 || a >= v.n_tokens ? 0 : max(min(e, v.n_tokens) - a, 0);
+    base = len - (e - a);  // (slots count rows past n_tokens too, as the append's)
   }
-  const int base = len - T, n = T ? p.n_path[b] : 0;
+  const int n = T ? p.n_path[b] : 0;
   __syncthreads();
   if (T) {
     bool no = n < 0 || n > T || n > p.path_stride || n > TREE_MAX;

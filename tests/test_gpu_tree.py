@@ -566,6 +566,24 @@ def test_keep(case, in_place):
         assert new_lens.tolist() == want_lens
 
 
+def test_keep_of_sequences_cut_by_n_tokens():
+    """Offsets past n_tokens: the slots are those that the append gives the rows."""
+    import torch
+    tq = lib()
+    s = Trees(tq, [50, 40], [6, 5], 2, 16, 73)
+    rows = torch.randn((11, 2, 128), device="cuda")
+    s.batch.c.n_tokens = s.batch.n_tokens = 9
+    tq.tq_paged_tree_append(*s.ctx, s.kv, s.batch, s.d_parents, rows, rows)
+    held = [p.cpu().numpy() for p in s.pages]
+    path = torch.tensor([[0, 5, 0, 0, 0, 0], [1, 2, 0, 0, 0, 0]], dtype=torch.int32, device="cuda")
+    lens = torch.zeros_like(s.d_lens)
+    tq.tq_paged_tree_keep(*s.ctx, s.kv, s.batch, path, torch.tensor([2, 2], dtype=torch.int32).cuda(), lens)
+    assert s.status() == 0 and lens.tolist() == [46, 37]
+    for p, h in zip(s.pages, held):
+        want, _ = tree.keep(h, s.table, [50, 40], s.cu, [[0, 5], [1, 2]])
+        assert np.array_equal(p.cpu().numpy(), want)
+
+
 def test_keep_refuses_paths_out_of_order():
     import torch
     tq = lib()

@@ -745,6 +745,15 @@ __global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(cons
         const int g = lane >> 2, t4 = lane & 3;
 #pragma unroll 1
         for (int c0 = 0; c0 < R; c0 += 8) {
+          // No node: zeros, in this warp's 16 dims of eight columns two 16-byte chunks of each (chains of 5 columns 36.2 ->
+          // 35.3 us; with 64 columns, mostly live, the test costs more than it saves: 171 -> 174).
+          if (R == 32 && c0 >= cols) {
+            const int c = c0 + (lane & 7), ch = 2 * (warp & 3) + ((lane >> 3) & 1), part = lane >> 4;
+            if (part < PARTS)
+              *reinterpret_cast<uint4 *>(smem + F::OFF_Q + (warp >> 2) * F::Q_HALF + (part * R + c) * 128 + ((ch ^ (c & 7)) << 4)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            continue;
+          }
           float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
           const uint8_t *col = xs + (c0 + g) * 256 + 4 * t4;
 #pragma unroll

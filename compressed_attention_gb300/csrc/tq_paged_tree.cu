@@ -1224,7 +1224,7 @@ bool layout(const tq_ctx *k, const PagedView &pv, int Hq, int out_dtype, Layout 
   l->npu = l->R / l->gq;  // at least one: 64 heads per KV head at most
   l->n_qt = (pv.max_q + l->npu - 1) / l->npu;
   l->grid = k->num_sms;
-  // the larger of both widths' needs, so that no smaller batch needs more than a larger one
+  // the larger of both widths' needs, so that no smaller batch of trees needs more than a larger one
   const int least = l->gq <= 32 ? 32 / l->gq : 1;
   l->units = (int64_t)pv.B * pv.Hkv * ((pv.max_q + least - 1) / least);
   const int64_t tiles = l->units * (((int64_t)pv.max_len + KT - 1) / KT + ITEM_TILES);

@@ -212,8 +212,7 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
 #pragma unroll
           for (int e = 0; e < Gr::E; ++e) x[e] = clamp01(x[e]), y[e] = clamp01(y[e]);
         }
-#pragma unroll
-        for (int e = 0; e < Gr::E; ++e) f(x[e], y[e]);
+        f(x, y);
       };
       const uint4 none = make_uint4(0u, 0u, 0u, 0u);
       // whole groups first: their loads need no look at the row's ends
@@ -247,14 +246,39 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
       }
     };
     using Fly = std::integral_constant<int, DT == TQ_DTYPE_F32 ? 4 : 2>;
+    using Row = const float (&)[Gr::E];
     if (!DRAFT || !fails) {
-      add_up(Fly(), std::false_type(), [&](float x, float) { sum += fix01(x); });
+      add_up(Fly(), std::false_type(), [&](Row x, Row) {
+#pragma unroll
+        for (int e = 0; e < Gr::E; ++e) sum += fix01(x[e]);
+      });
     } else if (fails == 1) {
-      add_up(Fly(), std::true_type(), [&](float x, float y) {
-        sum += fix01(x), sum -= fix01(fminf(x, y));
+      add_up(Fly(), std::true_type(), [&](Row x, Row y) {
+#pragma unroll
+        for (int e = 0; e < Gr::E; ++e) sum += fix01(x[e]), sum -= fix01(fminf(x[e], y[e]));
       });
     } else {
-      add_up(std::integral_constant<int, 1>(), std::true_type(), [&](float x, float y) { sum += weight(x, y); });
+      add_up(std::integral_constant<int, 1>(), std::true_type(), [&](Row x, Row y) {
+#pragma unroll
+        for (int h = 0; h < Gr::E; h += 4) {  // `weight` of four elements at once
+          uint64_t r[4], q2[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            r[e] = fix01(x[h + e]) - fix01(fminf(x[h + e], y[h + e]));
+            q2[e] = fix01(y[h + e]) << 1;
+          }
+#pragma unroll 1
+          for (int k = 1; k < fails; ++k) {
+            const uint64_t z2 = sm.z[k] << 1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint64_t c = __umul64hi(z2, q2[e]);
+              r[e] = r[e] > c ? r[e] - c : 0;
+            }
+          }
+          sum += (r[0] + r[1]) + (r[2] + r[3]);
+        }
+      });
     }
     sum = warp_sum(sum);
     if (!DRAFT)  // less the tokens taken out (each once: a token again has failed before)

@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
 
   uint64_t Z = ONE, sum = 0;
   bool have = false;  // sum is that of r as it stands
+  uint32_t out[TREE_MAX / 32] = {};  // no draft: nodes that failed on the current node (every warp keeps its own: no barrier a test)
   if (rank == 0 && tid == 0) path[0] = 0;
   for (int c = next_child(0, 0);; c = next_child(cur, c)) {
     const bool done = c == TREE_MAX;  // no child left
@@ -318,25 +319,40 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
         }
         take = __umul64hi(sm.u[c], mul62(Z, sm.q[c])) < r;
       } else {
-        bool again = false;
-        for (int k = lane; k < fails; k += 32) again |= sm.token[sm.gone[k]] == sm.token[c];
+        bool again = false;  // a token that has failed on this node
+        const int x = sm.token[c];
+#pragma unroll
+        for (int i = 0; i < TREE_MAX / 32; ++i) again |= ((out[i] >> lane) & 1u) && sm.token[32 * i + lane] == x;
         if (__any_sync(FULL_MASK, again)) r = 0;
         take = __umul64hi(sm.u[c], Z) < r;
       }
-      __syncthreads();  // (z, gone are read)
       if (take) {
         cur = c, fails = 0, Z = ONE, have = false;
+#pragma unroll
+        for (int i = 0; i < TREE_MAX / 32; ++i) out[i] = 0;
         if (rank == 0 && tid == 0) path[n_path] = c;
         ++n_path;
         stand(cur);
       } else if (DRAFT) {
+        __syncthreads();  // (z is read)
         if (tid == 0) sm.z[fails] = Z;
+        __syncthreads();
         ++fails;
         refused = true;
       } else if (r) {
-        if (tid == 0) sm.gone[fails] = c;
+#pragma unroll
+        for (int i = 0; i < TREE_MAX / 32; ++i) out[i] |= c >> 5 == i ? 1u << (c & 31) : 0u;
         ++fails;
         Z = Z > r ? Z - r : 0;
+      }
+    } else if (!DRAFT) {  // the list that the sums look at
+      if (warp == 0) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < TREE_MAX / 32; ++i) {
+          if ((out[i] >> lane) & 1u) sm.gone[n + __popc(out[i] & ((1u << lane) - 1))] = 32 * i + lane;
+          n += __popc(out[i]);
+        }
       }
       __syncthreads();
     }
@@ -381,13 +397,17 @@ __global__ void __launch_bounds__(VT, 2) k_tree_verify(const VerifyArgs a) {
     }
     const int64_t w0 = (int64_t)g * Gr::E - skip;
 #pragma unroll
-    for (int e = 0; e < Gr::E; ++e) {
-      r[e] = weight(clamp01(Gr::at(p4, e)), clamp01(Gr::at(q4, e)));
-      if (!DRAFT)
-        for (int k = 0; k < fails; ++k)
-          if (sm.token[sm.gone[k]] == w0 + e) r[e] = 0;
-      mine += r[e];
+    for (int e = 0; e < Gr::E; ++e) r[e] = weight(clamp01(Gr::at(p4, e)), clamp01(Gr::at(q4, e)));
+    if (!DRAFT) {
+#pragma unroll 1
+      for (int k = 0; k < fails; ++k) {
+        const int64_t at = sm.token[sm.gone[k]] - w0;
+#pragma unroll
+        for (int e = 0; e < Gr::E; ++e) r[e] = at == e ? 0 : r[e];
+      }
     }
+#pragma unroll
+    for (int e = 0; e < Gr::E; ++e) mine += r[e];
     uint64_t inc = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {

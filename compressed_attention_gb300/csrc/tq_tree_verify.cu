@@ -12,7 +12,7 @@
 // outcome, and a comparison is off by 2^-62 where fp32 sums over 10^5 weights would move the borders between tokens by
 // 10^-7, as much as a rare token has.
 //
-// Measured: 64 chains over 131,072 tokens (fp32, two rows of each: 67 MB) 22.3 us, 3.0 TB/s; bound by the ALU (47%; whole
+// Measured: 64 chains over 131,072 tokens (fp32, two rows of each: 67 MB) 22.3 us, 3.0 TB/s; bound by the ALU (51%; whole
 // groups loaded without a look at the row's ends and the first residual by comparing floats: 31 -> 23 us) and by SMs with two
 // CTAs beside SMs with one.  One chain 7.5 us: launch, two dependent loads of the nodes, one pass, the token's segment
 // again.  16 trees of several failed tests 20 us: a pass over the rows and a cluster barrier each.  32 trees of 20 to 32

@@ -729,6 +729,30 @@ def test_two_streams_and_repeated_calls_agree():
             assert torch.equal(o, first)
 
 
+def test_lengths_written_just_before_each_call():
+    """Calls back to back, the lengths changed by the kernel ahead of each."""
+    import torch
+    tq = lib()
+    for lens, new in (([900, 300, 77, 1500], [8, 8, 8, 8]), ([700] * 40, [4] * 40)):
+        s = Trees(tq, lens, new, 2, 32, 79)
+        q = torch.randn((s.n_rows, 8, 128), device="cuda").bfloat16()
+        ws, want = s.tree_workspace(8), []
+        turns = [s.d_lens.clone(), s.d_lens - 37]
+        for t in turns:
+            s.d_lens.copy_(t)
+            torch.cuda.synchronize()
+            want.append(torch.empty_like(q))
+            tq.tq_paged_tree_attention(*s.ctx, s.kv, s.batch, s.d_parents, q, want[-1], ws)
+            torch.cuda.synchronize()
+        assert not torch.equal(*want)
+        outs = [torch.empty_like(q) for _ in range(100)]
+        for i, o in enumerate(outs):
+            s.d_lens.copy_(turns[i % 2])
+            tq.tq_paged_tree_attention(*s.ctx, s.kv, s.batch, s.d_parents, q, o, ws)
+        torch.cuda.synchronize()
+        assert s.status() == 0 and all(torch.equal(o, want[i % 2]) for i, o in enumerate(outs))
+
+
 def test_offsets_past_32_bits():
     """Pages of more than 2^32 bytes; the sequence's pages lie at the end."""
     import torch

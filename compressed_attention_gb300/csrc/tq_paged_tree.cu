@@ -30,13 +30,13 @@
 // Parts: for bf16 outputs q and P enter as one fp16 each (2^-12 of the value at most); for fp16 and fp32 outputs as hi + lo,
 // the lo parts as more columns.  Sums, maxima and O are fp32.
 //
-// Measured: 8 sequences of 24,000 to 32,768 tokens, 8 nodes each, 32 heads on 8, bf16: 117 us for both launches, 2.1 TB/s of
-// packed rows (37 us at the copy rate), 2,150 cycles per 128 keys and SM.  The decoders' byte permutes keep the ALU at 69%
-// of its rate, issue 64%, tensor pipe 12%; with the decoders' arithmetic taken out (scratch build) it would be 99 us, with
-// the copies too 83: what is left is the chain decode -> S -> softmax -> P -> O and its barriers.  Table lookups in place of
-// the permutes, deeper rings and fewer raise barriers change nothing (118 to 124 us).  An item's start and end take 9.5 us
-// wherever they are hidden by nothing: one user's 8 nodes on 733 tokens 16.5 us, where an empty kernel takes 3 and the
-// combine 4; of the 9.5 more than half is q (position, turn, R), a chain of short dependent steps.
+// Measured: 8 sequences of 24,000 to 32,768 tokens, 8 nodes each, 32 heads on 8, bf16: 114 us for both launches, 2.2 TB/s of
+// packed rows (37 us at the copy rate), 2,100 cycles per 128 keys and SM.  The decoders' byte permutes keep the ALU at 70%
+// of its rate, issue 65%, tensor pipe 12%; with the decoders' arithmetic taken out (scratch build, when this took 117) it
+// was 99 us, with the copies too 83: what is left is the chain decode -> S -> softmax -> P -> O and its barriers.  Table
+// lookups in place of the permutes, deeper packed rings and fewer raise barriers changed nothing.  An item's start and end
+// take 9.5 us wherever they are hidden by nothing: one user's 8 nodes on 733 tokens 16.4 us, where an empty kernel takes 3
+// and the combine 4; of the 9.5 more than half is q (position, turn, R), a chain of short dependent steps.
 #include <math.h>
 
 #include "tq_decode_common.cuh"
@@ -63,8 +63,8 @@ struct Cfg {
   static constexpr int N = R * PARTS;   // columns of P and O
   // Warps: softmax, K and V decoders, the issuer of O^T, the loaders of keys and values, the issuer of S^T.  Two groups of
   // decoders each, on alternate tiles, where the softmax is quicker than one (8 sequences towards 32K 117 us, with one
-  // group 129); with 64 columns it is not, and takes the registers instead, for a sum per column and 32 scores (four
-  // trees of 40 to 64 nodes 172 us, with two groups 206).
+  // group 129, before K had three stages); with 64 columns it is not, and takes the registers instead, for a sum per
+  // column and 32 scores (four trees of 40 to 64 nodes 172 us, with two groups 206).
   static constexpr int GROUPS = R == 64 ? 1 : 2;
   static constexpr int W_KDEC = 8, W_VDEC = 8 + 4 * GROUPS, W_PV = 8 + 8 * GROUPS, W_LOAD = W_PV + 1, W_S = W_PV + 3;
   static constexpr int THREADS = (W_S + 1) * 32;
@@ -73,13 +73,14 @@ struct Cfg {
   static constexpr int CH = 32;         // columns a thread takes at a time
   // Stages: packed tiles on their way (more of the values', which the K decoders need for their norms long before
   // the V decoders come to them), decoded K (tensor memory) and V (shared memory), scores, P: what shared and tensor memory
-  // hold.  For 32 columns six packed stages against one decoded V less, or half the P, were slower (117 -> 121 to 125 us).
+  // hold.  For 32 columns six packed stages against one decoded V less, or half the P, were slower (117 -> 121 to 125 us), a
+  // fourth decoded K too (114 -> 117: decoders that run further ahead take the issue slots of what is waited for).
   static constexpr int NRAW_K = N == 32 ? 4 : 2, NRAW_V = 4;
   // A stage of packed tiles always falls to the same group of decoders: copies may land out of order, and a group that
   // had not waited for a stage's last phase could take its parity for the next one's.
   static_assert(GROUPS == 1 || (NRAW_K % 2 == 0 && NRAW_V % 2 == 0), "packed stages");
-  static constexpr int NK = N == 128 ? 2 : (R == 64 ? 3 : 4), NV = N == 128 ? 2 : 3;
-  static constexpr int NS = N == 128 ? 2 : (R == 64 ? 3 : 4), NP = N == 32 ? 4 : 2;
+  static constexpr int NK = N == 128 ? 2 : 3, NV = N == 128 ? 2 : 3;
+  static constexpr int NS = N == 128 ? 2 : (R == 64 ? 3 : 5), NP = N == 32 ? 4 : 2;
   static constexpr int NKN = NS + NK + 2;  // tiles whose norms are kept: see Misc
   static constexpr uint32_t TM_S = 0, TM_O = NS * R, TM_K = TM_O + 2 * N;
   static_assert(TM_K + NK * 64 <= 512, "tensor memory");
@@ -283,8 +284,8 @@ struct PartialParams {
 template <int NKN>
 struct Misc {
   uint64_t raw_full[2][4], raw_empty[2][4];  // [side][stage]
-  uint64_t k_full[4], k_empty[4], v_full[3], v_empty[3];
-  uint64_t s_done[4], s_free[4];      // [buffer]
+  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
+  uint64_t s_done[5], s_free[5];      // [buffer]
   uint64_t p_ready[4], pv_done[4];    // [buffer of P]
   uint64_t q_known, q_full, o_free, drain[2];
   // Norms of the last tiles, both written by the K decoders, so that the softmax waits for no values.  Tile j is

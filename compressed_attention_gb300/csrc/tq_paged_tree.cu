@@ -31,7 +31,7 @@
 // the lo parts as more columns.  Sums, maxima and O are fp32.
 //
 // Measured: 8 sequences of 24,000 to 32,768 tokens, 8 nodes each, 32 heads on 8, bf16: 114 us for both launches, 2.2 TB/s of
-// packed rows (37 us at the copy rate), 2,100 cycles per 128 keys and SM.  The decoders' byte permutes keep the ALU at 70%
+// packed rows (37 us at the copy rate), 2,100 cycles per 128 keys and SM.  The decoders' byte permutes keep the ALU at 69%
 // of its rate, issue 65%, tensor pipe 12%; with the decoders' arithmetic taken out (scratch build, when this took 117) it
 // was 99 us, with the copies too 83: what is left is the chain decode -> S -> softmax -> P -> O and its barriers.  Table
 // lookups in place of the permutes, deeper packed rings and fewer raise barriers changed nothing.  An item's start and end

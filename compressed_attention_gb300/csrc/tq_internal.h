@@ -328,7 +328,8 @@ constexpr int TREE_MAX = 128;  // nodes of a sequence
 bool paged_tree_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes);
 cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const int32_t *parents,
                               const uint8_t *kp, const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope,
-                              float scale, const PagedOut &o, void *ws, cudaStream_t st);
+                              float scale, const PagedOut &o, void *ws, cudaStream_t st,
+                              bool late = false);  // failure test: see PartialParams::late
 cudaError_t launch_paged_keep(const PagedView &pv, uint8_t *kp, uint8_t *vp, const int32_t *path, int64_t path_stride,
                               const int32_t *n_path, int32_t *new_lens, cudaStream_t st);
 struct VerifyArgs {

@@ -105,7 +105,7 @@ tq_status check_tree(const tq_paged_batch *bt, const int32_t *parents, bool empt
 tq_status attention(const tq_ctx *k, const tq_ctx *v, const tq_paged_kv *kv, const tq_paged_batch *bt,
                     const tq_rows *q, int Hq, const tq_rope *rope, const DiffView &diff, float scale, void *out,
                     int out_dtype, void *ws, size_t ws_bytes, tq_stream_t stream, const char *who,
-                    bool tree = false, const int32_t *parents = nullptr) {
+                    bool tree = false, const int32_t *parents = nullptr, bool late = false) {
   PagedView pv;
   bool empty;
   tq_status st = check_paged(k, v, kv, bt, who, &pv, &empty);
@@ -132,7 +132,7 @@ tq_status attention(const tq_ctx *k, const tq_ctx *v, const tq_paged_kv *kv, con
   const PagedOut o{out, out_dtype, diff};
   const uint8_t *kp = (const uint8_t *)kv->k_pages, *vp = (const uint8_t *)kv->v_pages;
   const cudaError_t e =
-      tree ? launch_paged_tree(k, v, pv, parents, kp, vp, qv, Hq, rv, scale, o, ws, (cudaStream_t)stream)
+      tree ? launch_paged_tree(k, v, pv, parents, kp, vp, qv, Hq, rv, scale, o, ws, (cudaStream_t)stream, late)
            : launch_paged_attention(k, v, pv, kp, vp, qv, Hq, rv, scale, o, ws, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, who);
   return TQ_OK;
@@ -288,6 +288,17 @@ tq_status tq_paged_tree_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, cons
   return guarded([&] {
     return attention(k_ctx, v_ctx, kv, batch, q, Hq, rope, DiffView{}, scale, out, out_dtype, workspace,
                      workspace_bytes, stream, "tq_paged_tree_attention", true, parents);
+  });
+}
+
+tq_status tq_test_tree_wait_timeout(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                                    const tq_paged_batch *batch, const int32_t *parents, const tq_rows *q, int Hq,
+                                    void *out, int out_dtype, void *workspace, size_t workspace_bytes,
+                                    tq_stream_t stream) {
+  return guarded([&] {
+    if (batch && batch->max_q < 2) return fail(TQ_ERR_UNSUPPORTED, "single nodes take the paged decode");
+    return attention(k_ctx, v_ctx, kv, batch, q, Hq, nullptr, DiffView{}, 0.f, out, out_dtype, workspace,
+                     workspace_bytes, stream, "tq_test_tree_wait_timeout", true, parents, true);
   });
 }
 

@@ -279,6 +279,7 @@ struct PartialParams {
   float *split;   // [CTA][2][R] partials of units that several CTAs share
   float *whole;   // [row][Hq] partials of units one CTA finished
   int32_t *unit;  // per unit: first CTA | CTAs << 16
+  int late;       // failure test: the first item is known once a wait for it has run out
 };
 
 template <int NKN>
@@ -461,6 +462,10 @@ __global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(cons
       auto publish = [&]() -> bool {  // the keys' loader walks its share for all
         const uint32_t i = n_items % NITEM;
         if (!next_item(p.v, w, it)) it.t0 = it.t1 = 0;
+        if (p.late && n_items == 0)
+          for (const uint64_t t0 = global_timer_ns();
+               !*reinterpret_cast<volatile int *>(&ms.abort_flag) && global_timer_ns() - t0 < 2 * WAIT_LIMIT_NS;) {
+          }
         if (n_items >= NITEM && !__all_sync(FULL_MASK, wait(&ms.item_empty[i], ((n_items / NITEM) - 1) & 1))) return ok = false;
         if (lane == 0) {
           ms.item[i] = it;
@@ -665,7 +670,13 @@ __global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(cons
     float4 *const mv = ms.move[gr];
     uint32_t n = 0;  // tiles before the item
     for (uint32_t items = 0;; ++items) {
-      if (!next()) break;
+      // The eight warps meet at named barriers, so they leave together or not at all: a warp that found no item left,
+      // or gave up while another may still have seen one come, says so in the vote that the others take next, below.  (One
+      // vote for both: 80 B more of spills, eight sequences towards 32K 114 -> 119 us, wide trees 172 -> 203.)
+      if (!next()) {
+        (void)both_or(true);
+        break;
+      }
       const int unit = unit_index(p.v, it.b, it.h, it.qt), n0 = it.qt * p.v.npu;
       const int cols = min(it.s.T - n0, p.v.npu) * p.v.gq;  // columns with a node
       // ---- q: rows turned by their nodes' positions, split into bf16 parts in P's buffers (free between items),
@@ -1263,7 +1274,7 @@ bool paged_tree_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *
 
 cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const int32_t *parents,
                               const uint8_t *kp, const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope,
-                              float scale, const PagedOut &o, void *ws, cudaStream_t st) {
+                              float scale, const PagedOut &o, void *ws, cudaStream_t st, bool late) {
   if (is_decode(pv, Hq)) return launch_paged_decode(k, v, pv, kp, vp, q, Hq, rope, scale, o, ws, st);
   Layout l;
   if (!layout(k, pv, Hq, o.dtype, &l)) return cudaErrorInvalidValue;
@@ -1280,6 +1291,7 @@ cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView 
   p.split = reinterpret_cast<float *>(base + l.split);
   p.whole = reinterpret_cast<float *>(base + l.whole);
   p.unit = reinterpret_cast<int32_t *>(base + l.unit);
+  p.late = late;
   cudaError_t e;
   if (l.parts == 1)
     e = l.R == 32 ? launch_partial<32, 1>(p, l.grid, st) : launch_partial<64, 1>(p, l.grid, st);

@@ -704,6 +704,15 @@ tq_status tq_test_decode_wait_timeout(const tq_ctx *k_ctx, const tq_ctx *v_ctx, 
                                       const void *v_cache, int B, int Hq, int Hkv, int L, void *workspace,
                                       size_t workspace_bytes, tq_stream_t stream);
 
+/* The same for the attention of drafted trees (max_q >= 2): the warp that finds the work keeps the first
+ * item back until a wait for it has run out (2 s), and then hands it over, so that some warps have given
+ * up and others may not have.  The kernel records status 3 and returns; what it leaves in out is not
+ * stated.  Arguments as tq_paged_tree_attention (no rotation, scale 0). */
+tq_status tq_test_tree_wait_timeout(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                                    const tq_paged_batch *batch, const int32_t *parents, const tq_rows *q, int Hq,
+                                    void *out, int out_dtype, void *workspace, size_t workspace_bytes,
+                                    tq_stream_t stream);
+
 /* Device-check test (no counterpart on the pages): overwrites the device a context
  * is recorded to belong to, so a test on a one-GPU machine can make the
  * current-device check of every launching call fail (TQ_ERR_INVALID_ARG, nothing

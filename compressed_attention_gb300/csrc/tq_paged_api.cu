@@ -155,8 +155,8 @@ tq_status append(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv
   return e == cudaSuccess ? TQ_OK : cuda_fail(e, who);
 }
 
-tq_status check_probs(const tq_probs *p) {
-  if (!p || !p->data) return fail(TQ_ERR_INVALID_ARG, "null probabilities");
+tq_status check_probs(const tq_probs *p, bool rows) {  // rows: some are read
+  if (!p || (rows && !p->data)) return fail(TQ_ERR_INVALID_ARG, "null probabilities");
   if (!dtype_ok(p->dtype)) return fail(TQ_ERR_INVALID_ARG, "probabilities must be F32, BF16 or F16");
   if (p->vocab < 1) return fail(TQ_ERR_INVALID_ARG, "vocab must be >= 1");
   if (p->row_stride < p->vocab || p->row_stride > INT64_MAX / 8 / INT32_MAX) return fail(TQ_ERR_INVALID_ARG, "bad row stride of the probabilities");
@@ -318,11 +318,12 @@ tq_status tq_tree_verify(const tq_ctx *ctx, const tq_paged_batch *batch, const i
       return fail(TQ_ERR_INVALID_ARG, "without cu_q every sequence has one row: n_tokens == B and max_q == 1");
     if (path_stride < batch->max_q || path_stride > INT64_MAX / 8 / INT32_MAX) return fail(TQ_ERR_INVALID_ARG, "path_stride below max_q");
     if (batch->B > INT32_MAX / 64) return fail(TQ_ERR_UNSUPPORTED, "too many sequences");
-    if ((st = check_probs(target)) != TQ_OK || (draft && (st = check_probs(draft)) != TQ_OK)) return st;
+    const bool rows = batch->n_tokens > 0;  // (sequences without rows: nothing of them is read)
+    if ((st = check_probs(target, rows)) != TQ_OK || (draft && (st = check_probs(draft, rows)) != TQ_OK)) return st;
     if (draft && (draft->dtype != target->dtype || draft->vocab != target->vocab))
       return fail(TQ_ERR_INVALID_ARG, "the draft's rows must have the target's dtype and vocab");
     if (batch->B == 0) return TQ_OK;
-    if (!parents || !tokens || !u_accept || !u_next) return fail(TQ_ERR_INVALID_ARG, "null parents, tokens or random numbers");
+    if (!u_next || (rows && (!parents || !tokens || !u_accept))) return fail(TQ_ERR_INVALID_ARG, "null parents, tokens or random numbers");
     if (!path || !n_path || !next_token) return fail(TQ_ERR_INVALID_ARG, "null output");
     if (!aligned(parents, 4) || !aligned(tokens, 4) || !aligned(u_accept, 4) || !aligned(u_next, 4) || !aligned(path, 4) ||
         !aligned(n_path, 4) || !aligned(next_token, 4) || !aligned(batch->cu_q, 4))

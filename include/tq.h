@@ -591,7 +591,9 @@ typedef struct tq_probs {
  *   path        device int32, the nodes of sequence b's path at path[b * path_stride], ascending, -1
  *               behind them up to max_q; path_stride >= max_q.
  *   n_path      device int32 [B]: nodes of the path, node 0 included; 0 (and next_token -1) for a
- *               sequence without rows.  Nodes past max_q are left out (flagged, status 2). */
+ *               sequence without rows.  Nodes past max_q are left out (flagged, status 2).
+ * Where no sequence has rows (n_tokens = 0) the rows' arrays (parents, tokens, target's and draft's data, u_accept) may
+ * be NULL. */
 tq_status tq_tree_verify(const tq_ctx *ctx, const tq_paged_batch *batch, const int32_t *parents,
                          const int32_t *tokens, const tq_probs *target, const tq_probs *draft,
                          const float *u_accept, const float *u_next, int32_t *path, int64_t path_stride,

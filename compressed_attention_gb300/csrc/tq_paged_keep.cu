@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(KEEP_T) k_paged_keep(const KeepParams p) {
   const int n = T ? p.n_path[b] : 0;
   __syncthreads();
   if (T) {
-    bool no = n < 0 || n > T || n > p.path_stride || n > TREE_MAX;
+    bool no = n < 0 || n > T || n > p.path_stride || n > v.max_q;  // (max_q: what a row of path holds)
     if (!no)
       for (int j = tid; j < n; j += KEEP_T) {
         const int at = p.path[b * p.path_stride + j];

@@ -602,9 +602,9 @@ tq_status tq_tree_verify(const tq_ctx *ctx, const tq_paged_batch *batch, const i
 /* Keep a path of the nodes in the cache: slot c + j takes the record of slot c + path[j], keys and values
  * of every KV head, for j < n_path[b], and new_lens[b] = c + n_path[b] (0 at least; the length itself for a
  * sequence without rows).  Slots behind the path keep their bytes.
- *   path, path_stride, n_path   as tq_tree_verify writes them: ascending nodes.  A path that is not, or
- *               that names a node past the sequence's, is not taken (flagged, status 7): nothing is
- *               moved and new_lens[b] = c.
+ *   path, path_stride, n_path   as tq_tree_verify writes them: ascending nodes.  A path that is not, that
+ *               is longer than max_q or names a node past the sequence's, is not taken (flagged, status 7):
+ *               nothing is moved and new_lens[b] = c.
  *   new_lens    device int32 [B]; may be batch->seq_lens itself.
  * The batch has a row at least (or B = 0: nothing is done).  A row whose page id is out of range is
  * not moved (status 5).  Sequences must not share the pages of their nodes. */

@@ -792,8 +792,9 @@ def tq_tree_verify(ctx, batch, parents, tokens, target, u_accept, u_next, path, 
 
 
 def tq_paged_tree_keep(k_ctx, v_ctx, kv, batch, path, n_path, new_lens, stream=None):
-    """Move the records of each sequence's path to the front of its nodes' slots, and set new_lens [B] (the
-    batch's own lengths may be given) to context + n_path."""
+    """Move the records of each sequence's path to the front of its nodes' slots, and set new_lens [B] to
+    context + n_path.  The batch's own lengths may be given as new_lens in the last layer's call only: the
+    other layers' calls need them as they were, and write new_lens somewhere else."""
     _check_call(kv, batch)
     pp, stride = _path(path, batch)
     i32 = _torch()[0].int32

@@ -530,7 +530,8 @@ tq_status tq_paged_diff_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, cons
 /* Speculative decoding over the paged cache.  A step drafts a tree of tokens per sequence, runs the
  * model on all of them at once, keeps the path that the target's probabilities accept and goes on
  * from the token drawn behind it: tq_paged_tree_append and tq_paged_tree_attention in every layer,
- * then tq_tree_verify, then tq_paged_tree_keep in every layer.
+ * then tq_tree_verify, then tq_paged_tree_keep in every layer (which alone may write the lengths in place, and only
+ * in the last layer's call).
  *   The batch's rows are the nodes: sequence b's rows cu_q[b] .. cu_q[b+1] - 1 are its nodes 0, 1, ... T - 1
  * (T <= 128: max_q above it is TQ_ERR_UNSUPPORTED), and lie in the cache's slots c .. c + T - 1 behind the
  * context of c = seq_lens[b] - T tokens.  parents[i] of row i is the node that node i follows, an
@@ -605,7 +606,10 @@ tq_status tq_tree_verify(const tq_ctx *ctx, const tq_paged_batch *batch, const i
  *   path, path_stride, n_path   as tq_tree_verify writes them: ascending nodes.  A path that is not, that
  *               is longer than max_q or names a node past the sequence's, is not taken (flagged, status 7):
  *               nothing is moved and new_lens[b] = c.
- *   new_lens    device int32 [B]; may be batch->seq_lens itself.
+ *   new_lens    device int32 [B]; may be batch->seq_lens itself IN THE LAST LAYER'S CALL ONLY.  The slots are
+ *               counted from seq_lens, which must still hold the lengths with the nodes in every layer's call:
+ *               a call behind one that wrote in place would move wrong records and cut the lengths again,
+ *               which no call can tell.  The layers before it write somewhere else.
  * The batch has a row at least (or B = 0: nothing is done).  A row whose page id is out of range is
  * not moved (status 5).  Sequences must not share the pages of their nodes. */
 tq_status tq_paged_tree_keep(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,

@@ -37,3 +37,13 @@ def test_pages_in_another_order(tq):
         tq.PagedKV(pages, one, tab, 16, 2)
     with pytest.raises(ValueError):
         tq.PagedKV(pages[:0], pages[:0], tab, 16, 2)
+
+
+def test_the_documentation_says_which_layer_may_write_the_lengths_in_place(tq):
+    """Every layer's call counts its slots from the lengths that the last layer's may overwrite."""
+    import os
+    import re
+    assert "last layer" in " ".join(tq.tq_paged_tree_keep.__doc__.split())
+    header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "tq.h")
+    says = re.search(r"new_lens    device int32(.*?)\*/", open(header).read(), re.S).group(1)
+    assert "last layer's call only" in " ".join(says.replace("*", " ").split()).lower()

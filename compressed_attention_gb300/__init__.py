@@ -114,6 +114,7 @@ _SIGNATURES = {
     "tq_static_workspace_bytes": (_sz, []),
     "tq_test_decode_wait_timeout": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _sz, _vp]),
     "tq_test_ctx_set_device": (_i32, [_vp, _i32]),
+    "tq_test_tree_columns": (_i32, [_vp, _vp, _vp, _vp, _i32, ctypes.POINTER(_i32)]),
     "tq_test_tree_wait_timeout": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _sz, _vp]),
     "tq_store_create": (_i32, [_vp, _vp, _i32, _i32, _i32, _i32, ctypes.POINTER(_vp)]),
     "tq_store_destroy": (_i32, [_vp]),

@@ -326,6 +326,7 @@ cudaError_t launch_paged_attention(const tq_ctx *k, const tq_ctx *v, const Paged
 // ---- drafted trees (tq_paged_tree.cu, tq_tree_verify.cu) ----
 constexpr int TREE_MAX = 128;  // nodes of a sequence
 bool paged_tree_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes);
+int paged_tree_columns(const tq_ctx *k, const PagedView &pv, int Hq);  // of a unit; 0: the paged decode
 cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const int32_t *parents,
                               const uint8_t *kp, const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope,
                               float scale, const PagedOut &o, void *ws, cudaStream_t st,

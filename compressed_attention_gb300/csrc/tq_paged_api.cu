@@ -291,6 +291,19 @@ tq_status tq_paged_tree_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, cons
   });
 }
 
+tq_status tq_test_tree_columns(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                               const tq_paged_batch *batch, int Hq, int32_t *columns) {
+  if (!columns) return fail(TQ_ERR_INVALID_ARG, "null output");
+  return guarded([&] {
+    PagedView pv;
+    bool empty;
+    tq_status st = check_paged(k_ctx, v_ctx, kv, batch, "tq_test_tree_columns", &pv, &empty);
+    if (st != TQ_OK || (st = check_heads(kv, Hq)) != TQ_OK) return st;
+    *columns = empty ? 0 : paged_tree_columns(k_ctx, pv, Hq);
+    return TQ_OK;
+  });
+}
+
 tq_status tq_test_tree_wait_timeout(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
                                     const tq_paged_batch *batch, const int32_t *parents, const tq_rows *q, int Hq,
                                     void *out, int out_dtype, void *workspace, size_t workspace_bytes,

@@ -1272,6 +1272,11 @@ bool paged_tree_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *
   return true;
 }
 
+int paged_tree_columns(const tq_ctx *k, const PagedView &pv, int Hq) {
+  Layout l;
+  return !is_decode(pv, Hq) && layout(k, pv, Hq, TQ_DTYPE_BF16, &l) ? l.R : 0;
+}
+
 cudaError_t launch_paged_tree(const tq_ctx *k, const tq_ctx *v, const PagedView &pv, const int32_t *parents,
                               const uint8_t *kp, const uint8_t *vp, const RowsView &q, int Hq, const RopeView &rope,
                               float scale, const PagedOut &o, void *ws, cudaStream_t st, bool late) {

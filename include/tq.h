@@ -567,7 +567,7 @@ typedef struct tq_probs {
   const void *data;    /* device, aligned to its element */
   int32_t dtype;
   int32_t vocab;       /* >= 1 */
-  int64_t row_stride;  /* >= vocab */
+  int64_t row_stride;  /* >= vocab, at most 2^29 */
 } tq_probs;
 
 /* Verification of drafted tokens from given random numbers.  Sequence b's walk starts on its node
@@ -718,6 +718,11 @@ tq_status tq_test_tree_wait_timeout(const tq_ctx *k_ctx, const tq_ctx *v_ctx, co
                                     const tq_paged_batch *batch, const int32_t *parents, const tq_rows *q, int Hq,
                                     void *out, int out_dtype, void *workspace, size_t workspace_bytes,
                                     tq_stream_t stream);
+
+/* Which form the attention of drafted trees takes for a batch's sizes: units of 32 or 64 columns, 0 for the paged
+ * decode (single nodes) or a batch without rows.  No device work. */
+tq_status tq_test_tree_columns(const tq_ctx *k_ctx, const tq_ctx *v_ctx, const tq_paged_kv *kv,
+                               const tq_paged_batch *batch, int Hq, int32_t *columns);
 
 /* Device-check test (no counterpart on the pages): overwrites the device a context
  * is recorded to belong to, so a test on a one-GPU machine can make the

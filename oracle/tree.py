@@ -88,6 +88,48 @@ def verify(parents, tokens, target, u_accept, u_next, draft=None):
     return path, -1
 
 
+ONE = 1 << 62
+
+
+def fixed(p):
+    """Probabilities in whole multiples of 2^-62, rounded down: Python ints; what is no number in [0, 1] as 0 or 1."""
+    x = np.nan_to_num(np.asarray(p, np.float64), nan=0.0, posinf=1.0, neginf=0.0)
+    return np.floor(np.clip(x, 0.0, 1.0) * 2.0 ** 62).astype(np.uint64).astype(object)
+
+
+def verify_fixed(parents, tokens, target, u_accept, u_next, draft=None):
+    """The walk as the kernel's numbers make it: weights and Z in multiples of 2^-62 (Z q rounded down to one),
+    random numbers in multiples of 2^-64."""
+    def random(u):
+        u = min(max(float(u), 0.0), 1.0 - 2.0 ** -24) if u == u else 0.0
+        return int(u * 2.0 ** 64)
+
+    at, path, T = 0, [0], len(parents)
+    while True:
+        r, Z, taken = fixed(target[at]), ONE, None
+        q = None if draft is None else fixed(draft[at])
+        for c in [i for i in range(at + 1, T) if parents[i] == at]:
+            x = int(tokens[c])
+            if not 0 <= x < len(r):
+                continue
+            if (random(u_accept[c]) * (Z if q is None else Z * q[x] >> 62)) >> 64 < r[x]:
+                taken = c
+                break
+            if q is None:
+                Z, r[x] = max(Z - r[x], 0), 0
+            else:
+                rest = np.maximum(r - (Z * q >> 62), 0)
+                if rest.sum() > 0:
+                    r, Z = rest, min(rest.sum(), 2 * ONE - 1)
+        if taken is None:
+            break
+        at = taken
+        path.append(at)
+    t = (r.sum() * random(u_next)) >> 64
+    over = np.flatnonzero(np.cumsum(r) > t)
+    return path, int(over[0]) if len(over) else -1
+
+
 def keep(pages, table, seq_lens, cu_q, paths):
     """The pages (a copy) with every sequence's path moved to the front of its nodes' slots, and the new
     lengths."""

@@ -90,3 +90,26 @@ def test_keep_moves_what_the_path_names():
     slots = lambda p: [int(p[table[0, t // 16], 0, t % 16, 0]) for t in range(20)]  # noqa: E731
     a, b = slots(pages), slots(out)
     assert b[14:17] == [a[14], a[16], a[19]] and b[:14] == a[:14] and b[17:] == a[17:]
+
+
+@pytest.mark.parametrize("draft", [True, False], ids=["draft", "no-draft"])
+def test_whole_multiples_change_ordinary_walks_nowhere(draft):
+    """2^-62 is far below any border that random rows put next to a random number."""
+    rng = np.random.default_rng(9)
+    for _ in range(60):
+        T, V = int(rng.integers(1, 9)), int(rng.integers(2, 40))
+        p, q = (rng.dirichlet(np.full(V, 0.3), T).astype(np.float32) for _ in range(2))
+        parents = [-1] + [int(rng.integers(max(0, i - 3), i)) for i in range(1, T)]
+        args = (parents, rng.integers(0, V, T), p, rng.random(T).astype(np.float32), np.float32(rng.random()), q if draft else None)
+        assert tree.verify_fixed(*args) == tree.verify(*args)
+
+
+def test_whole_multiples_round_down():
+    """p(1) = 3.99 x 2^-62 holds three of them; 3.5 x 2^-62 of Z = 1 is three as well, so the child is not taken where
+    the exact numbers take it.  A weight below 2^-62 is none."""
+    p = np.array([[1.0, 3.99 * 2.0 ** -62], [2.0 ** -63, 2.0 ** -62]], np.float32)
+    u = np.array([0.0, 3.5 * 2.0 ** -62], np.float32)
+    assert tree.verify([-1, 0], [0, 1], p, u, 0.5) == ([0, 1], 1)
+    assert tree.verify_fixed([-1, 0], [0, 1], p, u, 0.5) == ([0], 0)
+    assert tree.verify_fixed([-1], [0], p[1:], u, 0.0) == ([0], 1) and tree.verify([-1], [0], p[1:], u, 0.0) == ([0], 0)
+    assert list(tree.fixed([np.nan, -1.0, 0.5, 2.0, np.inf])) == [0, 0, 1 << 61, 1 << 62, 1 << 62]

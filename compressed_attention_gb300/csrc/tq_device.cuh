@@ -100,7 +100,9 @@ __device__ __forceinline__ uint32_t bucket_grid(float y, float scale, float offs
 // Every kernel of the library is launched so that it may start while the previous
 // kernel on the stream is still finishing: it runs its prologue (work that reads only
 // the immutable context), then waits here until the previous grid has completed and its
-// memory is visible.  Without such a launch the wait returns at once.
+// memory is visible.  Without such a launch the wait returns at once.  (A kernel that follows one of
+// its own call may also read there what that one only reads, if that one lets it start behind its own wait: the
+// trees' combine reads lengths and offsets so.)
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Allows the next kernel on the stream to be scheduled (it still waits in pdl_wait for
 // this grid to complete before touching its results).

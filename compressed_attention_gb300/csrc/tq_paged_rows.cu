@@ -115,7 +115,8 @@ __device__ __forceinline__ Place place_row(const PagedView &v, const int32_t *pa
 }
 
 // TREE: a row's rotation is by its node's position, not by its slot's.
-// (The walk's dependent loads: 1,792 nodes of 8 heads take 13.0 us where plain rows take 11.2, 8 nodes 3.8 and 3.6.)
+// (The walk's dependent loads, once per head and side of a row: 1,792 nodes of 8 heads take 13.1 us where plain rows take 11.1, 8
+// nodes 3.8 and 3.5, a chain of 128 nodes 12.3; under dense rotations 19.3 and 18.7, 5.8 and 5.2.)
 template <int SRC, bool TREE>
 __global__ void __launch_bounds__(WT_THREADS) k_paged_append_wht(const AppendParams p) {
   __shared__ WhtTables tb;

@@ -7,7 +7,9 @@
 // Few columns against long contexts: so the products are laid with the keys in the rows,
 //   S^T [128 keys x R] = C_K Q^T,   O^T [128 dims x N] += C_V^T P^T,
 // and the time of a tile goes with its 128 keys and its columns, where rows of 128 queries (the chunk kernel's
-// form) would compute 128 exponentials a key whatever the tree holds.  A softmax thread is a key: its norms are two
+// form) would compute 128 exponentials a key whatever the tree holds.  (For trees of some hundred columns a KV head that does
+// not hold: they are cut into units of 64, which decode every tile again, and the chunk kernel spends about as much
+// on a tile of 128 rows as this one on 64 columns; it takes no trees.)  A softmax thread is a key: its norms are two
 // scalars, and the sums of weights stay in its registers until the item's end.
 //
 //   k_tree_partial  persistent, one CTA per SM; the key tiles of all units lie end to end (each unit after a few
@@ -27,7 +29,7 @@
 //                                 (and O rescaled) only when a weight would leave the operand's range: one vote a tile.
 //   k_tree_combine  the log-sum-exp merge of a column's shares, R^T o on the tensor cores, rounding.
 //
-// Parts: for bf16 outputs q and P enter as one fp16 each (2^-12 of the value at most); for fp16 and fp32 outputs as hi + lo,
+// Parts: for bf16 outputs q and P enter as one fp16 each (off by 2^-11 of the value at most); for fp16 and fp32 outputs as hi + lo,
 // the lo parts as more columns.  Sums, maxima and O are fp32.
 //
 // Measured: 8 sequences of 24,000 to 32,768 tokens, 8 nodes each, 32 heads on 8, bf16: 114 us for both launches, 2.2 TB/s of
@@ -36,7 +38,10 @@
 // was 99 us, with the copies too 83: what is left is the chain decode -> S -> softmax -> P -> O and its barriers.  Table
 // lookups in place of the permutes, deeper packed rings and fewer raise barriers changed nothing.  An item's start and end
 // take 9.5 us wherever they are hidden by nothing: one user's 8 nodes on 733 tokens 16.4 us, where an empty kernel takes 3
-// and the combine 4; of the 9.5 more than half is q (position, turn, R), a chain of short dependent steps.
+// and the combine 4; of the 9.5 more than half is q (position, turn, R), a chain of short dependent steps.  R is applied as a
+// product under a WHT too, where the single-row decode turns q by a butterfly in the warp.  Positions and ancestors are walks
+// along the parents, a load a step, at every item's start: on those 733 tokens a chain of 32, 64 and 128 nodes takes 23, 33
+// and 49 us where trees of the same sizes and a few levels take 19, 24 and 31.
 #include <math.h>
 
 #include "tq_decode_common.cuh"
@@ -49,8 +54,8 @@ namespace tq {
 namespace {
 
 constexpr int KT = 128;          // keys per tile
-// Cost of an item ahead of its tiles (q, the first maxima, the partials), in tiles: 8 sequences towards 32K take 118 us
-// with 6 to 8 and 120 with 12, short chains 37.3 with 6, 38.0 with 8 and 40.9 with 12, mixed trees 40.5 with 8 and 41.8 with 12.
+// Cost of an item ahead of its tiles (q, the first maxima, the partials), in tiles.  With 6, 8 and 12: 8 sequences towards 32K
+// take 115, 114 and 116 us, short chains 34.6, 35.5 and 38.2, mixed trees 33.0, 31.9 and 32.9, wide trees 173, 172 and 171.
 constexpr int ITEM_TILES = 8;
 constexpr int RAW = KT * PG_ROW; // a packed tile
 constexpr int PROW = D + 4;      // floats of a partial: acc[128], max (less W_SHIFT), sum, 2 spare
@@ -68,6 +73,8 @@ struct Cfg {
   static constexpr int GROUPS = R == 64 ? 1 : 2;
   static constexpr int W_KDEC = 8, W_VDEC = 8 + 4 * GROUPS, W_PV = 8 + 8 * GROUPS, W_LOAD = W_PV + 1, W_S = W_PV + 3;
   static constexpr int THREADS = (W_S + 1) * 32;
+  // Spilled, for those registers (stores): R = 32 44 B (one part) and 62 (two), R = 64 300 and 352, all where items start
+  // and end and where maxima rise.
   static constexpr int REGS_LAUNCH = GROUPS == 1 ? 96 : 72, REGS_SOFTMAX = GROUPS == 1 ? 144 : 128, REGS_OTHER = GROUPS == 1 ? 64 : 48;
   static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "the launch's registers");
   static constexpr int CH = 32;         // columns a thread takes at a time
@@ -77,7 +84,15 @@ struct Cfg {
   // fourth decoded K too (114 -> 117: decoders that run further ahead take the issue slots of what is waited for).
   static constexpr int NRAW_K = N == 32 ? 4 : 2, NRAW_V = 4;
   // A stage of packed tiles always falls to the same group of decoders: copies may land out of order, and a group that
-  // had not waited for a stage's last phase could take its parity for the next one's.
+  // had not waited for a stage's last phase could take its parity for the next one's.  The decoded stages (three) and the
+  // scores' buffers (five, or three) pass from group to group, so that a waiter meets a buffer's barrier every other phase
+  // only.  They hold because one thread issues their products and commits them in order: a commit arrives when all
+  // products before it are done.  A K decoder that waits for tile n - NK to be scored has waited for tile n - NK - 2 (its
+  // own last tile's wait), so that of the same stage's phase before, tile n - 2 NK, it knows that it has passed: the phase it
+  // waits for is the open one or the one just closed, and parity tells them apart.  The same holds for the values'
+  // stages (O^T's commits), and for a softmax group at the scores of tile n, which has waited for those of tile n - 2, issued
+  // after or with its buffer's last ones, of tile n - NS (NS >= 2).  With another order of commits, or with several issuers, these rings would
+  // have to be even as the packed ones are.
   static_assert(GROUPS == 1 || (NRAW_K % 2 == 0 && NRAW_V % 2 == 0), "packed stages");
   static constexpr int NK = N == 128 ? 2 : 3, NV = N == 128 ? 2 : 3;
   static constexpr int NS = N == 128 ? 2 : (R == 64 ? 3 : 5), NP = N == 32 ? 4 : 2;
@@ -594,7 +609,7 @@ __global__ void __launch_bounds__(Cfg<R, PARTS>::THREADS, 1) k_tree_partial(cons
             src = (uint64_t)(uintptr_t)row;
             prefetch_l1(row), prefetch_l1(row + 128);
             if (p.q.dtype == TQ_DTYPE_F32) prefetch_l1(row + 256), prefetch_l1(row + 384);
-            if (p.rope.rot_dim) {
+            if (p.rope.rot_dim) {  // (a walk per column: see the deep chains in the header)
               turn = rope_pos(p.rope, tree_pos(p.v.pv, p.v.parents, it.b, it.s.row + node, it.s.base + node, true), p.v.pv.status, true);
               const size_t at = (size_t)turn * (p.rope.rot_dim >> 1);
               prefetch_l1(p.rope.cos_t + at), prefetch_l1(p.rope.sin_t + at);
@@ -1212,7 +1227,8 @@ struct Layout {
 // is the CTAs' even share of the items and half an item for the split ends.  Measured, 64 against 32 (4 query heads per KV
 // head, bf16): 4 sequences of 16,000 tokens with 9 nodes 62 / 74 us, 24 nodes 100 / 107, 64 nodes 182 / 265, 1 to 16 nodes
 // 62 / 53; 8 of 1,500 with 9 nodes 32 / 33, 24 nodes 54 / 49, 64 nodes 100 / 112, 1 to 16 nodes 32 / 27; 32 of 16 to
-// 8,000 with up to 20 nodes, 6 query heads, f16: 39 / 31.
+// 8,000 with up to 20 nodes, 6 query heads, f16: 39 / 31.  What the host knows are bounds: a batch padded to full trees, or with
+// the block table's width for max_len, is taken for what it could hold, which can cost it that difference.
 int columns(const PagedView &pv, int gq, int grid) {
   if (gq > 32) return 64;
   if (pv.max_q * gq <= 32 || pv.B == 0) return 32;
@@ -1260,8 +1276,8 @@ cudaError_t launch_partial(const PartialParams &p, int grid, cudaStream_t st) {
 
 }  // namespace
 
-// One node per sequence sees all of its sequence's keys: a single row of the paged decode, which takes 10.1 us for one
-// sequence of 733 tokens and 66 for eight towards 32K, where the kernels above take 15.1 and 126.
+// One node per sequence sees all of its sequence's keys: a single row of the paged decode, which takes 9.5 us for two
+// sequences of 733 tokens and 59 for eight towards 32K, where the kernels above take 15.0 and 110 (captured).
 static bool is_decode(const PagedView &pv, int Hq) { return pv.max_q == 1 && Hq / pv.Hkv <= 16; }
 
 bool paged_tree_workspace(const tq_ctx *k, const PagedView &pv, int Hq, size_t *bytes) {

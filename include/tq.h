@@ -537,6 +537,9 @@ tq_status tq_paged_diff_attention(const tq_ctx *k_ctx, const tq_ctx *v_ctx, cons
  * context of c = seq_lens[b] - T tokens.  parents[i] of row i is the node that node i follows, an
  * earlier node of the same sequence, or -1: the node follows the context.  Node i's position is
  * c + depth(i), the number of its ancestors above the context (siblings share a position, not a slot).
+ *   max_q, n_tokens and max_len choose between the attention's forms (and single nodes with max_q = 1 take the
+ * decode): give them as tight as the batch allows.  A captured step padded to its capacity is right, and up to a
+ * quarter slower.
  *   A parent that is neither -1 nor an earlier node counts as -1 (flagged, status 7, by the calls that
  * read it: without a rotation the append reads none, the attention of single nodes neither).  The calls
  * follow the paged calls' rules on padded batches, idle slots, lengths, pages, streams and capture. */
